@@ -10,16 +10,20 @@ The layer is two hand-written CUDA kernels for sm_103a behind a C ABI
   over all top-k experts' down rows with the routing weight folded in, finished
   by a warp butterfly. No padding, gather, scatter or combine buffers exist.
 
+Around the layer, ``include/warp_decode_block.h`` has the rest of a decoder
+block: projections with MXFP4 weights, a paged KV cache in MXFP4 with its
+attention, and the norms between blocks (``block_ops``).
+
 ``ops`` is the thin Python binding (argument marshalling only); ``workload``
 is the seeded synthetic input generator. Importing this package loads nothing
 native: the CUDA library is built/loaded on first use and any failure raises.
 """
 
-__all__ = ["ops", "workload"]
+__all__ = ["ops", "block_ops", "workload"]
 
 
 def __getattr__(name):
-    if name in ("ops", "workload"):
+    if name in __all__:
         import importlib
 
         return importlib.import_module(f"{__name__}.{name}")

@@ -1,0 +1,294 @@
+"""Thin Python binding of the operators around the MoE layer (``include/warp_decode_block.h``).
+
+Every ``wd_*`` function has the name of the C entry point it calls, checks
+tensor metadata, extracts pointers and raises on a non-OK status, as in
+:mod:`ops`. Outputs are the caller's tensors, work is enqueued on ``stream``
+(default: the current stream), and nothing synchronises. Tensors may have any
+row stride the entry point takes; their last axis is dense.
+
+* ``Fp4Weights``, ``wd_fp4_matvec`` -- projections with MXFP4 weights
+* ``Kv4Cache``, ``wd_kv4_append``, ``wd_kv4_gather``, ``wd_kv4_attend`` -- a paged
+  KV cache held in MXFP4
+* ``wd_block_norm`` -- the norms, gate and residual between two blocks
+"""
+from __future__ import annotations
+
+import ctypes
+
+import torch
+
+from . import ops
+from .ops import WarpDecodeError
+
+__all__ = ["Fp4Weights", "Kv4Cache", "kv4_workspace", "wd_fp4_matvec", "wd_kv4_append", "wd_kv4_gather",
+           "wd_kv4_attend", "wd_block_norm", "exported_symbols"]
+
+_TYPES = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
+
+
+class Fp4Shape(ctypes.Structure):
+    _fields_ = [("N", ctypes.c_int32), ("K", ctypes.c_int32)]
+
+
+class Kv4Struct(ctypes.Structure):
+    _fields_ = [("pages", ctypes.c_int32), ("page_size", ctypes.c_int32), ("heads", ctypes.c_int32),
+                ("dim", ctypes.c_int32), ("k_codes", ctypes.c_void_p), ("k_scales", ctypes.c_void_p),
+                ("v_codes", ctypes.c_void_p), ("v_scales", ctypes.c_void_p)]
+
+
+_lib_cache = None
+
+
+def lib() -> ctypes.CDLL:
+    """The loaded library with these entry points' signatures set."""
+    global _lib_cache
+    if _lib_cache is None:
+        L = ops.lib()
+        vp, i32, i64, f32, sz = (ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_float,
+                                 ctypes.c_size_t)
+        fp, kp = ctypes.POINTER(Fp4Shape), ctypes.POINTER(Kv4Struct)
+        L.wd_fp4_packed_bytes.restype = sz
+        L.wd_fp4_packed_bytes.argtypes = [fp, ctypes.c_int]
+        L.wd_kv4_cache_bytes.restype = sz
+        L.wd_kv4_cache_bytes.argtypes = [kp, ctypes.c_int]
+        L.wd_kv4_attend_workspace.restype = sz
+        L.wd_kv4_attend_workspace.argtypes = [kp, i32, i32]
+        tokens = [kp, vp, vp, i32, i64, i64, i32, vp, i32, vp, vp, i32, vp, vp]
+        for name, args in (
+                ("wd_fp4_pack_codes", [fp, vp, vp, vp, vp, vp]),
+                ("wd_fp4_pack_weights", [fp, vp, i32, i64, vp, vp, vp]),
+                ("wd_fp4_matvec", [fp, vp, vp, vp, i32, i64, i32, vp, i32, i64, vp]),
+                ("wd_kv4_append", tokens), ("wd_kv4_gather", tokens),
+                ("wd_kv4_attend", [kp, vp, i32, i64, i32, i32, vp, i32, vp, f32, i32, vp, i64, vp, vp, sz, vp, vp]),
+                ("wd_block_norm", [i32, i32, vp, i32, i64, vp, i32, i64, vp, vp, vp, i32, i64, i32, f32, f32, vp,
+                                   i64, vp, i32, i64, vp])):
+            fn = getattr(L, name)
+            fn.restype = ctypes.c_int
+            fn.argtypes = args
+        _lib_cache = L
+    return _lib_cache
+
+
+def exported_symbols() -> list[str]:
+    """The entry points include/warp_decode_block.h declares."""
+    return ["wd_fp4_packed_bytes", "wd_fp4_pack_codes", "wd_fp4_pack_weights", "wd_fp4_matvec",
+            "wd_kv4_cache_bytes", "wd_kv4_append", "wd_kv4_gather", "wd_kv4_attend_workspace",
+            "wd_kv4_attend", "wd_block_norm"]
+
+
+def _check(fn: str, status: int) -> None:
+    if status != ops.MOE_OK:
+        raise WarpDecodeError(fn, status, lib().moe_last_error().decode())
+
+
+def _stream(stream) -> int | None:
+    if stream is None:
+        return torch.cuda.current_stream().cuda_stream
+    return stream.cuda_stream if hasattr(stream, "cuda_stream") else stream
+
+
+def _type(t: torch.Tensor, name: str) -> int:
+    code = _TYPES.get(t.dtype)
+    if code is None:
+        raise TypeError(f"{name}: dtype {t.dtype} is not float32, bfloat16 or float16")
+    return code
+
+
+def _rows(t: torch.Tensor, shape: tuple, name: str) -> int:
+    """Row stride of a tensor [rows, ...] whose rows are dense."""
+    if t.shape != shape:
+        raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
+    if t.is_contiguous():
+        return t.numel() // shape[0] if shape[0] else t.stride(0)
+    want = 1
+    for size, stride in zip(reversed(t.shape[1:]), reversed(t.stride()[1:])):
+        if size != 1 and stride != want:
+            raise ValueError(f"{name}: a row must be dense, got strides {t.stride()}")
+        want *= size
+    return t.stride(0) if shape[0] > 1 else max(t.stride(0), want)
+
+
+def _ints(t: torch.Tensor | None, shape: tuple, name: str) -> int | None:
+    if t is None:
+        return None
+    if t.dtype != torch.int32:
+        raise TypeError(f"{name}: dtype {t.dtype} is not int32")
+    if t.shape != shape or not t.is_contiguous():
+        raise ValueError(f"{name}: expected a contiguous tensor of shape {tuple(shape)}, got {tuple(t.shape)}")
+    return t.data_ptr()
+
+
+def _flag(t: torch.Tensor | None) -> int | None:
+    if t is None:
+        return None
+    if t.dtype != torch.int32:
+        raise TypeError(f"err_flag: dtype {t.dtype} is not int32")
+    return t.data_ptr()
+
+
+# ---------------------------------------------------------- 4-bit projections --
+
+class Fp4Weights:
+    """MXFP4 weights [N, K] on the GPU in the packed layout of warp_decode_block.h."""
+
+    def __init__(self, N: int, K: int, device="cuda"):
+        self.shape = Fp4Shape(N, K)
+        self._shape = ctypes.byref(self.shape)
+        sizes = [int(lib().wd_fp4_packed_bytes(self._shape, w)) for w in (0, 1)]
+        if not all(sizes):
+            raise ValueError(f"Fp4Weights: unsupported shape [{N}, {K}] (K % 32 == 0, 32 <= K <= 65536)")
+        self.N, self.K = N, K
+        self.codes, self.scales = (torch.empty(n, dtype=torch.uint8, device=device) for n in sizes)
+        self._ptrs = self.codes.data_ptr(), self.scales.data_ptr()
+
+    @classmethod
+    def from_codes(cls, codes: torch.Tensor, scales: torch.Tensor, stream=None) -> "Fp4Weights":
+        """From an MXFP4 checkpoint: uint8 codes [N, K/2] (even element in the low nibble), scales [N, K/32]."""
+        N, K = codes.shape[0], 2 * codes.shape[1]
+        for t, shape, name in ((codes, (N, K // 2), "codes"), (scales, (N, K // 32), "scales")):
+            if t.dtype != torch.uint8 or t.shape != shape or not t.is_contiguous():
+                raise ValueError(f"{name}: expected contiguous uint8 {shape}, got {t.dtype} {tuple(t.shape)}")
+        w = cls(N, K, codes.device)
+        _check("wd_fp4_pack_codes", lib().wd_fp4_pack_codes(
+            w._shape, codes.data_ptr(), scales.data_ptr(), *w._ptrs, _stream(stream)))
+        return w
+
+    @classmethod
+    def quantize(cls, w: torch.Tensor, stream=None) -> "Fp4Weights":
+        """Quantise w [N, K] (float32, bfloat16 or float16, on the GPU) to MXFP4."""
+        if w.dim() != 2:
+            raise ValueError(f"w: expected [N, K], got {tuple(w.shape)}")
+        out = cls(w.shape[0], w.shape[1], w.device)
+        _check("wd_fp4_pack_weights", lib().wd_fp4_pack_weights(
+            out._shape, w.data_ptr(), _type(w, "w"), _rows(w, w.shape, "w"), *out._ptrs, _stream(stream)))
+        return out
+
+    @property
+    def nbytes(self) -> int:
+        return self.codes.numel() + self.scales.numel()
+
+
+def wd_fp4_matvec(weights: Fp4Weights, x: torch.Tensor, y: torch.Tensor, stream=None) -> torch.Tensor:
+    """y[B, N] = x[B, K] W^T; x bfloat16 or float16, y float32, bfloat16 or float16."""
+    B = x.shape[0]
+    _check("wd_fp4_matvec", lib().wd_fp4_matvec(
+        weights._shape, *weights._ptrs, x.data_ptr(), _type(x, "x"), _rows(x, (B, weights.K), "x"), B,
+        y.data_ptr(), _type(y, "y"), _rows(y, (B, weights.N), "y"), _stream(stream)))
+    return y
+
+
+# ------------------------------------------------------------- 4-bit KV cache --
+
+class Kv4Cache:
+    """One layer's paged KV cache in MXFP4 (four uint8 tensors, layout of warp_decode_block.h)."""
+
+    def __init__(self, pages: int, page_size: int, heads: int, dim: int, device="cuda"):
+        self.pages, self.page_size, self.heads, self.dim = pages, page_size, heads, dim
+        self.struct = Kv4Struct(pages, page_size, heads, dim)
+        self._ref = ctypes.byref(self.struct)
+        codes, scales = (int(lib().wd_kv4_cache_bytes(self._ref, w)) for w in (0, 1))
+        if not codes:
+            raise ValueError(f"Kv4Cache: unsupported sizes: pages {pages}, page_size {page_size} (16 to 256, a power "
+                             f"of two), heads {heads}, dim {dim} (64, 128 or 256)")
+        self.tensors = [torch.zeros(n, dtype=torch.uint8, device=device) for n in (codes, scales, codes, scales)]
+        (self.struct.k_codes, self.struct.k_scales, self.struct.v_codes,
+         self.struct.v_scales) = (t.data_ptr() for t in self.tensors)
+
+    @property
+    def nbytes(self) -> int:
+        return sum(t.numel() for t in self.tensors)
+
+
+def _tokens(fn: str, cache: Kv4Cache, k, v, block_table, seq_lens, cu_new, err_flag, stream) -> None:
+    T, S = k.shape[0], seq_lens.shape[0]
+    if v.dtype != k.dtype:
+        raise TypeError(f"v: dtype {v.dtype} differs from k's {k.dtype}")
+    shape = (T, cache.heads, cache.dim)
+    _check(fn, getattr(lib(), fn)(
+        cache._ref, k.data_ptr(), v.data_ptr(), _type(k, "k"), _rows(k, shape, "k"), _rows(v, shape, "v"), T,
+        _ints(block_table, (S, block_table.shape[-1]), "block_table"), block_table.shape[-1],
+        _ints(seq_lens, (S,), "seq_lens"), _ints(cu_new, (S + 1,), "cu_new"), S, _flag(err_flag), _stream(stream)))
+
+
+def wd_kv4_append(cache: Kv4Cache, k: torch.Tensor, v: torch.Tensor, block_table: torch.Tensor,
+                  seq_lens: torch.Tensor, cu_new: torch.Tensor | None = None,
+                  err_flag: torch.Tensor | None = None, stream=None) -> Kv4Cache:
+    """Quantise the new tokens k, v [T, heads, dim] into the cache behind seq_lens[s] tokens of each
+    sequence; cu_new [S + 1] says which rows are whose (None: one each)."""
+    _tokens("wd_kv4_append", cache, k, v, block_table, seq_lens, cu_new, err_flag, stream)
+    return cache
+
+
+def wd_kv4_gather(cache: Kv4Cache, block_table: torch.Tensor, seq_lens: torch.Tensor, k_out: torch.Tensor,
+                  v_out: torch.Tensor, cu_new: torch.Tensor | None = None,
+                  err_flag: torch.Tensor | None = None, stream=None):
+    """The values of the positions that wd_kv4_append with the same arguments writes."""
+    _tokens("wd_kv4_gather", cache, k_out, v_out, block_table, seq_lens, cu_new, err_flag, stream)
+    return k_out, v_out
+
+
+def kv4_workspace(cache: Kv4Cache, S: int, q_heads: int) -> torch.Tensor:
+    """A workspace for wd_kv4_attend with this cache's sizes: zeroed, reusable, one per overlapping call."""
+    n = int(lib().wd_kv4_attend_workspace(cache._ref, S, q_heads))
+    if not n:
+        raise ValueError(f"kv4_workspace: S {S} or q_heads {q_heads} (a multiple of {cache.heads}) is unsupported")
+    return torch.zeros(n, dtype=torch.uint8, device=cache.tensors[0].device)
+
+
+def wd_kv4_attend(cache: Kv4Cache, q: torch.Tensor, block_table: torch.Tensor, seq_lens: torch.Tensor,
+                  out: torch.Tensor, workspace: torch.Tensor, lse: torch.Tensor | None = None,
+                  scale: float | None = None, window: int = 0, err_flag: torch.Tensor | None = None,
+                  stream=None) -> torch.Tensor:
+    """out[S, q_heads, dim]: attention of one query token per sequence over its seq_lens[s] cached keys
+    (the last `window` of them, 0 for all); lse [S, q_heads] float32. scale: 1 / sqrt(dim) by default."""
+    S, q_heads = q.shape[0], q.shape[1]
+    if out.dtype != q.dtype:
+        raise TypeError(f"out: dtype {out.dtype} differs from q's {q.dtype}")
+    if lse is not None and (lse.dtype != torch.float32 or lse.shape != (S, q_heads) or not lse.is_contiguous()):
+        raise ValueError(f"lse: expected contiguous float32 {(S, q_heads)}, got {lse.dtype} {tuple(lse.shape)}")
+    shape = (S, q_heads, cache.dim)
+    _check("wd_kv4_attend", lib().wd_kv4_attend(
+        cache._ref, q.data_ptr(), _type(q, "q"), _rows(q, shape, "q"), S, q_heads,
+        _ints(block_table, (S, block_table.shape[-1]), "block_table"), block_table.shape[-1],
+        _ints(seq_lens, (S,), "seq_lens"), cache.dim ** -0.5 if scale is None else scale, window,
+        out.data_ptr(), _rows(out, shape, "out"), None if lse is None else lse.data_ptr(), workspace.data_ptr(),
+        workspace.numel() * workspace.element_size(), _flag(err_flag), _stream(stream)))
+    return out
+
+
+# ---------------------------------------------------------------- block norms --
+
+def wd_block_norm(res: torch.Tensor, res_out: torch.Tensor | None = None, out: torch.Tensor | None = None,
+                  y: torch.Tensor | None = None, w_post: torch.Tensor | None = None,
+                  gate: torch.Tensor | None = None, w_pre: torch.Tensor | None = None,
+                  res_scale: float = 1.0, eps: float = 1e-6, stream=None):
+    """r' = res_scale * res + gate * norm(y; w_post) into res_out, norm(r'; w_pre) into out: the step
+    between two blocks. gate broadcasts from [1 or T, 1 or H]. Returns (res_out, out)."""
+    T, H = res.shape
+    w_type = 0
+    params = [p for p in (w_post, w_pre, gate) if p is not None]
+    if params:
+        w_type = _type(params[0], "w_post, w_pre and gate")
+        for p, name in ((w_post, "w_post"), (w_pre, "w_pre")):
+            if p is not None and (p.shape != (H,) or not p.is_contiguous()):
+                raise ValueError(f"{name}: expected contiguous [{H}], got {tuple(p.shape)}")
+        if any(p.dtype != params[0].dtype for p in params):
+            raise TypeError("w_post, w_pre and gate must have one dtype")
+    gate_ld = gate_step = 0
+    if gate is not None:
+        if gate.dim() != 2 or gate.shape[0] not in (1, T) or gate.shape[1] not in (1, H):
+            raise ValueError(f"gate: shape {tuple(gate.shape)} does not broadcast to {(T, H)}")
+        gate_ld = gate.stride(0) if gate.shape[0] > 1 else 0
+        gate_step = gate.stride(1) if gate.shape[1] > 1 else 0
+    if res_out is not None and res_out.dtype != res.dtype:
+        raise TypeError(f"res_out: dtype {res_out.dtype} differs from res's {res.dtype}")
+    none = (None, 0, 0)
+    yp, yt, yl = none if y is None else (y.data_ptr(), _type(y, "y"), _rows(y, (T, H), "y"))
+    rp, _, rl = none if res_out is None else (res_out.data_ptr(), 0, _rows(res_out, (T, H), "res_out"))
+    op, ot, ol = none if out is None else (out.data_ptr(), _type(out, "out"), _rows(out, (T, H), "out"))
+    _check("wd_block_norm", lib().wd_block_norm(
+        T, H, res.data_ptr(), _type(res, "res"), _rows(res, (T, H), "res"), yp, yt, yl,
+        None if w_post is None else w_post.data_ptr(), None if w_pre is None else w_pre.data_ptr(),
+        None if gate is None else gate.data_ptr(), w_type, gate_ld, gate_step, res_scale, eps, rp, rl, op, ot,
+        ol, _stream(stream)))
+    return res_out, out
