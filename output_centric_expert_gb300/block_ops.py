@@ -36,7 +36,7 @@ class Kv4Struct(ctypes.Structure):
                 ("v_codes", ctypes.c_void_p), ("v_scales", ctypes.c_void_p)]
 
 
-_lib_cache = None
+_lib_cache = None  # the entry points read it directly: a call's marshalling is a few us, as long as a small kernel
 
 
 def lib() -> ctypes.CDLL:
@@ -81,9 +81,9 @@ def _check(fn: str, status: int) -> None:
         raise WarpDecodeError(fn, status, lib().moe_last_error().decode())
 
 
-def _stream(stream) -> int | None:
+def _stream(stream, t: torch.Tensor) -> int | None:
     if stream is None:
-        return torch.cuda.current_stream().cuda_stream
+        return torch._C._cuda_getCurrentRawStream(t.get_device()) if t.is_cuda else None
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else stream
 
 
@@ -94,18 +94,18 @@ def _type(t: torch.Tensor, name: str) -> int:
     return code
 
 
-def _rows(t: torch.Tensor, shape: tuple, name: str) -> int:
-    """Row stride of a tensor [rows, ...] whose rows are dense."""
+def _rows(t: torch.Tensor, shape: tuple, row: int, name: str) -> int:
+    """Row stride of a tensor of shape [rows, ...] whose rows are dense, `row` elements each."""
     if t.shape != shape:
         raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
     if t.is_contiguous():
-        return t.numel() // shape[0] if shape[0] else t.stride(0)
+        return row
     want = 1
     for size, stride in zip(reversed(t.shape[1:]), reversed(t.stride()[1:])):
         if size != 1 and stride != want:
             raise ValueError(f"{name}: a row must be dense, got strides {t.stride()}")
         want *= size
-    return t.stride(0) if shape[0] > 1 else max(t.stride(0), want)
+    return t.stride(0)
 
 
 def _ints(t: torch.Tensor | None, shape: tuple, name: str) -> int | None:
@@ -150,7 +150,7 @@ class Fp4Weights:
                 raise ValueError(f"{name}: expected contiguous uint8 {shape}, got {t.dtype} {tuple(t.shape)}")
         w = cls(N, K, codes.device)
         _check("wd_fp4_pack_codes", lib().wd_fp4_pack_codes(
-            w._shape, codes.data_ptr(), scales.data_ptr(), *w._ptrs, _stream(stream)))
+            w._shape, codes.data_ptr(), scales.data_ptr(), *w._ptrs, _stream(stream, codes)))
         return w
 
     @classmethod
@@ -160,7 +160,7 @@ class Fp4Weights:
             raise ValueError(f"w: expected [N, K], got {tuple(w.shape)}")
         out = cls(w.shape[0], w.shape[1], w.device)
         _check("wd_fp4_pack_weights", lib().wd_fp4_pack_weights(
-            out._shape, w.data_ptr(), _type(w, "w"), _rows(w, w.shape, "w"), *out._ptrs, _stream(stream)))
+            out._shape, w.data_ptr(), _type(w, "w"), _rows(w, w.shape, w.shape[1], "w"), *out._ptrs, _stream(stream, w)))
         return out
 
     @property
@@ -170,10 +170,13 @@ class Fp4Weights:
 
 def wd_fp4_matvec(weights: Fp4Weights, x: torch.Tensor, y: torch.Tensor, stream=None) -> torch.Tensor:
     """y[B, N] = x[B, K] W^T; x bfloat16 or float16, y float32, bfloat16 or float16."""
-    B = x.shape[0]
-    _check("wd_fp4_matvec", lib().wd_fp4_matvec(
-        weights._shape, *weights._ptrs, x.data_ptr(), _type(x, "x"), _rows(x, (B, weights.K), "x"), B,
-        y.data_ptr(), _type(y, "y"), _rows(y, (B, weights.N), "y"), _stream(stream)))
+    B, K, N = x.shape[0], weights.K, weights.N
+    codes, scales = weights._ptrs
+    status = _lib_cache.wd_fp4_matvec(
+        weights._shape, codes, scales, x.data_ptr(), _type(x, "x"), _rows(x, (B, K), K, "x"), B,
+        y.data_ptr(), _type(y, "y"), _rows(y, (B, N), N, "y"), _stream(stream, x))
+    if status:
+        _check("wd_fp4_matvec", status)
     return y
 
 
@@ -200,14 +203,17 @@ class Kv4Cache:
 
 
 def _tokens(fn: str, cache: Kv4Cache, k, v, block_table, seq_lens, cu_new, err_flag, stream) -> None:
-    T, S = k.shape[0], seq_lens.shape[0]
+    T, S, blocks = k.shape[0], seq_lens.shape[0], block_table.shape[-1]
     if v.dtype != k.dtype:
         raise TypeError(f"v: dtype {v.dtype} differs from k's {k.dtype}")
+    row = cache.heads * cache.dim
     shape = (T, cache.heads, cache.dim)
-    _check(fn, getattr(lib(), fn)(
-        cache._ref, k.data_ptr(), v.data_ptr(), _type(k, "k"), _rows(k, shape, "k"), _rows(v, shape, "v"), T,
-        _ints(block_table, (S, block_table.shape[-1]), "block_table"), block_table.shape[-1],
-        _ints(seq_lens, (S,), "seq_lens"), _ints(cu_new, (S + 1,), "cu_new"), S, _flag(err_flag), _stream(stream)))
+    status = getattr(_lib_cache, fn)(
+        cache._ref, k.data_ptr(), v.data_ptr(), _type(k, "k"), _rows(k, shape, row, "k"), _rows(v, shape, row, "v"), T,
+        _ints(block_table, (S, blocks), "block_table"), blocks, _ints(seq_lens, (S,), "seq_lens"),
+        _ints(cu_new, (S + 1,), "cu_new"), S, _flag(err_flag), _stream(stream, k))
+    if status:
+        _check(fn, status)
 
 
 def wd_kv4_append(cache: Kv4Cache, k: torch.Tensor, v: torch.Tensor, block_table: torch.Tensor,
@@ -246,17 +252,28 @@ def wd_kv4_attend(cache: Kv4Cache, q: torch.Tensor, block_table: torch.Tensor, s
         raise TypeError(f"out: dtype {out.dtype} differs from q's {q.dtype}")
     if lse is not None and (lse.dtype != torch.float32 or lse.shape != (S, q_heads) or not lse.is_contiguous()):
         raise ValueError(f"lse: expected contiguous float32 {(S, q_heads)}, got {lse.dtype} {tuple(lse.shape)}")
-    shape = (S, q_heads, cache.dim)
-    _check("wd_kv4_attend", lib().wd_kv4_attend(
-        cache._ref, q.data_ptr(), _type(q, "q"), _rows(q, shape, "q"), S, q_heads,
-        _ints(block_table, (S, block_table.shape[-1]), "block_table"), block_table.shape[-1],
-        _ints(seq_lens, (S,), "seq_lens"), cache.dim ** -0.5 if scale is None else scale, window,
-        out.data_ptr(), _rows(out, shape, "out"), None if lse is None else lse.data_ptr(), workspace.data_ptr(),
-        workspace.numel() * workspace.element_size(), _flag(err_flag), _stream(stream)))
+    D, blocks = cache.dim, block_table.shape[-1]
+    shape, row = (S, q_heads, D), q_heads * D
+    status = _lib_cache.wd_kv4_attend(
+        cache._ref, q.data_ptr(), _type(q, "q"), _rows(q, shape, row, "q"), S, q_heads,
+        _ints(block_table, (S, blocks), "block_table"), blocks, _ints(seq_lens, (S,), "seq_lens"),
+        D ** -0.5 if scale is None else scale, window, out.data_ptr(), _rows(out, shape, row, "out"),
+        None if lse is None else lse.data_ptr(), workspace.data_ptr(), workspace.nbytes, _flag(err_flag),
+        _stream(stream, q))
+    if status:
+        _check("wd_kv4_attend", status)
     return out
 
 
 # ---------------------------------------------------------------- block norms --
+
+def _weight(w: torch.Tensor, H: int, first: torch.Tensor, name: str) -> int:
+    if w.shape != (H,) or not w.is_contiguous():
+        raise ValueError(f"{name}: expected contiguous [{H}], got {tuple(w.shape)}")
+    if w.dtype != first.dtype:
+        raise TypeError("w_post, w_pre and gate must have one dtype")
+    return w.data_ptr()
+
 
 def wd_block_norm(res: torch.Tensor, res_out: torch.Tensor | None = None, out: torch.Tensor | None = None,
                   y: torch.Tensor | None = None, w_post: torch.Tensor | None = None,
@@ -264,31 +281,37 @@ def wd_block_norm(res: torch.Tensor, res_out: torch.Tensor | None = None, out: t
                   res_scale: float = 1.0, eps: float = 1e-6, stream=None):
     """r' = res_scale * res + gate * norm(y; w_post) into res_out, norm(r'; w_pre) into out: the step
     between two blocks. gate broadcasts from [1 or T, 1 or H]. Returns (res_out, out)."""
-    T, H = res.shape
+    T, H = shape = res.shape
     w_type = 0
-    params = [p for p in (w_post, w_pre, gate) if p is not None]
-    if params:
-        w_type = _type(params[0], "w_post, w_pre and gate")
-        for p, name in ((w_post, "w_post"), (w_pre, "w_pre")):
-            if p is not None and (p.shape != (H,) or not p.is_contiguous()):
-                raise ValueError(f"{name}: expected contiguous [{H}], got {tuple(p.shape)}")
-        if any(p.dtype != params[0].dtype for p in params):
-            raise TypeError("w_post, w_pre and gate must have one dtype")
-    gate_ld = gate_step = 0
+    first = w_pre if w_pre is not None else w_post if w_post is not None else gate
+    if first is not None:
+        w_type = _type(first, "w_post, w_pre and gate")
+    pp = qp = gp = yp = rp = op = None
+    gate_ld = gate_step = yt = yl = rl = ot = ol = 0
+    if w_post is not None:
+        pp = _weight(w_post, H, first, "w_post")
+    if w_pre is not None:
+        qp = _weight(w_pre, H, first, "w_pre")
     if gate is not None:
-        if gate.dim() != 2 or gate.shape[0] not in (1, T) or gate.shape[1] not in (1, H):
+        if gate.dtype != first.dtype:
+            raise TypeError("w_post, w_pre and gate must have one dtype")
+        rows, cols = gate.shape if gate.dim() == 2 else (0, 0)
+        if rows not in (1, T) or cols not in (1, H):
             raise ValueError(f"gate: shape {tuple(gate.shape)} does not broadcast to {(T, H)}")
-        gate_ld = gate.stride(0) if gate.shape[0] > 1 else 0
-        gate_step = gate.stride(1) if gate.shape[1] > 1 else 0
-    if res_out is not None and res_out.dtype != res.dtype:
-        raise TypeError(f"res_out: dtype {res_out.dtype} differs from res's {res.dtype}")
-    none = (None, 0, 0)
-    yp, yt, yl = none if y is None else (y.data_ptr(), _type(y, "y"), _rows(y, (T, H), "y"))
-    rp, _, rl = none if res_out is None else (res_out.data_ptr(), 0, _rows(res_out, (T, H), "res_out"))
-    op, ot, ol = none if out is None else (out.data_ptr(), _type(out, "out"), _rows(out, (T, H), "out"))
-    _check("wd_block_norm", lib().wd_block_norm(
-        T, H, res.data_ptr(), _type(res, "res"), _rows(res, (T, H), "res"), yp, yt, yl,
-        None if w_post is None else w_post.data_ptr(), None if w_pre is None else w_pre.data_ptr(),
-        None if gate is None else gate.data_ptr(), w_type, gate_ld, gate_step, res_scale, eps, rp, rl, op, ot,
-        ol, _stream(stream)))
+        gp = gate.data_ptr()
+        gate_ld = gate.stride(0) if rows > 1 else 0
+        gate_step = gate.stride(1) if cols > 1 else 0
+    if y is not None:
+        yp, yt, yl = y.data_ptr(), _type(y, "y"), _rows(y, shape, H, "y")
+    if res_out is not None:
+        if res_out.dtype != res.dtype:
+            raise TypeError(f"res_out: dtype {res_out.dtype} differs from res's {res.dtype}")
+        rp, rl = res_out.data_ptr(), _rows(res_out, shape, H, "res_out")
+    if out is not None:
+        op, ot, ol = out.data_ptr(), _type(out, "out"), _rows(out, shape, H, "out")
+    status = (_lib_cache or lib()).wd_block_norm(
+        T, H, res.data_ptr(), _type(res, "res"), _rows(res, shape, H, "res"), yp, yt, yl, pp, qp, gp, w_type, gate_ld,
+        gate_step, res_scale, eps, rp, rl, op, ot, ol, _stream(stream, res))
+    if status:
+        _check("wd_block_norm", status)
     return res_out, out

@@ -135,12 +135,12 @@ def test_norm_refuses_before_launch(change, status):
 
 def test_binding_checks_tensors():
     with pytest.raises(ValueError, match="row must be dense"):
-        block_ops._rows(torch.zeros(4, 6, 2).transpose(1, 2), (4, 2, 6), "x")
+        block_ops._rows(torch.zeros(4, 6, 2).transpose(1, 2), (4, 2, 6), 12, "x")
     with pytest.raises(ValueError, match="expected shape"):
-        block_ops._rows(torch.zeros(4, 6), (4, 5), "x")
+        block_ops._rows(torch.zeros(4, 6), (4, 5), 5, "x")
     wide = torch.zeros(4, 10, 8)
-    assert block_ops._rows(wide[:, 2:5], (4, 3, 8), "x") == 80
-    assert block_ops._rows(wide[:1, 2:5], (1, 3, 8), "x") >= 24  # one row: its stride is not used
+    assert block_ops._rows(wide[:, 2:5], (4, 3, 8), 24, "x") == 80
+    assert block_ops._rows(wide[:1, 2:5], (1, 3, 8), 24, "x") >= 24  # one row: its stride is not used
     with pytest.raises(TypeError, match="int32"):
         block_ops._ints(torch.zeros(3, dtype=torch.int64), (3,), "seq_lens")
     with pytest.raises(TypeError, match="dtype"):
