@@ -30,9 +30,8 @@
 namespace wd {
 namespace {
 
-constexpr int kWarpKeys = 32;                          // keys per warp and iteration
-constexpr int kTileKeys = kWarpsPerCta * kWarpKeys;  // keys per CTA tile
-constexpr int kSub = 16;                               // keys of one MMA tile; a page holds whole ones
+constexpr int kWarpKeys = 32;  // keys per warp and iteration
+constexpr int kSub = 16;       // keys of one MMA tile; a page holds whole ones
 constexpr unsigned kAll = 0xFFFFFFFFu;
 
 struct AttendArgs {
@@ -101,9 +100,9 @@ struct Stage {
 // of head tile n is head n * 8 + c; a lane holds columns 2t and 2t + 1.
 template <int D, int NT>
 struct State {
-  float m[NT][2], l[NT][2];
+  float m[NT][2], l[NT][2];  // maximum of K q (before the scale), sum of 2^6 p
   float acc[NT][D / 16][4];  // rows of MMA tile 2b + h: dims 32b + 4g + 2h (first), + 1
-  uint32_t top[(D + 127) / 128 * 2];  // running maximum of the V scale codes, byte pairs (b, b) like v_scales
+  uint32_t top[D / 64];      // running maximum of the V scale codes, bytes (b, b, b + 1, b + 1) as in v_scales
 };
 
 template <int D, int NT>
@@ -118,226 +117,250 @@ __device__ __forceinline__ void clear(State<D, NT>& s) {
       for (int c = 0; c < 4; ++c) s.acc[n][i][c] = 0.0f;
   }
 #pragma unroll
-  for (int i = 0; i < (D + 127) / 128 * 2; ++i) s.top[i] = 0;
+  for (int i = 0; i < D / 64; ++i) s.top[i] = 0;
 }
 
-// The keys of an iteration: [kb, kb + 32), of which [lo, hi) count.
-struct Keys {
-  int64_t kb, lo, hi;
-  bool page_ok[2];
-};
+// Bytes of shared memory, 4, 8 or 16 at a time.
+template <int WORDS>
+__device__ __forceinline__ void lds(const uint8_t* p, uint32_t (&w)[WORDS]) {
+  if constexpr (WORDS == 1) {
+    w[0] = *reinterpret_cast<const uint32_t*>(p);
+  } else if constexpr (WORDS == 2) {
+    const uint2 v = *reinterpret_cast<const uint2*>(p);
+    w[0] = v.x, w[1] = v.y;
+  } else {
+#pragma unroll
+    for (int i = 0; i < WORDS; i += 4) {
+      const uint4 v = *reinterpret_cast<const uint4*>(p + 4 * i);
+      w[i] = v.x, w[i + 1] = v.y, w[i + 2] = v.z, w[i + 3] = v.w;
+    }
+  }
+}
 
+// The scale codes of one key's blocks -> FP32 scales.
+template <int NB>
+__device__ __forceinline__ void key_scales(const uint8_t* p, float (&f)[NB]) {
+  if constexpr (NB == 2) {
+    const uint32_t w = *reinterpret_cast<const uint16_t*>(p);
+    e8m0x2_to_f32(w & 255u, w >> 8, f[0], f[1]);
+  } else {
+#pragma unroll
+    for (int i = 0; i < NB; i += 4) {
+      float four[4];
+      e8m0x4_to_f32(*reinterpret_cast<const uint32_t*>(p + i), four);
+#pragma unroll
+      for (int k = 0; k < 4; ++k) f[i + k] = four[k];
+    }
+  }
+}
+
+// The V scale codes' maxima with a stage's (rare: kept out of the loop's code).
+template <int NWORD>
+struct Tops {
+  uint32_t w[NWORD];
+  bool poison;  // a NaN block is among the keys
+};
+template <int D>
+__device__ __noinline__ Tops<D / 64> raised_tops(const uint8_t* vs, Tops<D / 64> top) {
+  constexpr int NB = D / 32, NWORD = D / 64, kWords = 16 * NWORD;
+  const int lane = threadIdx.x & 31;
+  bool poison = false;
+  uint32_t best[NB] = {};
+#pragma unroll
+  for (int r = 0; r < (kWords + 31) / 32; ++r) {
+    const int i = lane + 32 * r;
+    if (i >= kWords) break;
+    const uint32_t w = *reinterpret_cast<const uint32_t*>(vs + i * 4);
+    uint32_t both[2] = {0, 0};
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const uint32_t c = (w >> (8 * k)) & 255u;
+      if (c == 255u)
+        poison = true;
+      else
+        both[k >> 1] = max(both[k >> 1], c);
+    }
+#pragma unroll
+    for (int b = 0; b < NB; ++b)
+      if (i % NWORD == b / 2) best[b] = max(best[b], both[b & 1]);
+  }
+#pragma unroll
+  for (int b = 0; b < NB; ++b) {
+    const uint32_t now = max((top.w[b / 2] >> (16 * (b & 1))) & 255u, __reduce_max_sync(kAll, best[b]));
+    const uint32_t two = now | now << 8;
+    top.w[b / 2] = (b & 1) ? (top.w[b / 2] & 0x0000FFFFu) | two << 16 : (top.w[b / 2] & 0xFFFF0000u) | two;
+  }
+  top.poison = __any_sync(kAll, poison);
+  return top;
+}
+
+// One iteration: 32 keys of a ring stage. qf: the queries' B fragments in shared
+// memory, [NT][D / 32][32 lanes][16 bytes]; qs: what turns K q into log 2 units;
+// on: bit (u * 16 + k) tells whether key k of run u counts.
 template <int D, int NT>
-__device__ __forceinline__ void attend_keys(uint8_t* st, const uint32_t (&q)[NT][D / 32][4],
-                                            const float (&qs)[NT][2], const Keys& keys,
-                                            State<D, NT>& s) {
+__device__ __forceinline__ void attend_keys(uint8_t* st, const uint8_t* qf, const float (&qs)[NT][2],
+                                            uint32_t on, State<D, NT>& s) {
   using L = Stage<D>;
-  constexpr int NB = D / 32;          // scale blocks
-  constexpr int NWORD = (NB + 1) / 2;  // 4-byte words of a key's V codes; V scale words of a pair
+  constexpr int NB = D / 32;     // scale blocks
+  constexpr int NWORD = D / 64;  // 4-byte words of a key's V codes in a lane; V scale words of a pair
   const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-  const bool edge = keys.kb < keys.lo || keys.kb + kWarpKeys > keys.hi || !keys.page_ok[0] ||
-                    !keys.page_ok[1];
-  bool off[2][2] = {};  // [16-key run][row g or g + 8]: masked
-  if (edge) {
+  if (on != kAll) {  // what a masked key's V scales hold must not count
+    if (!((on >> lane) & 1u)) {
+      uint8_t* p = st + L::kVs + (lane >> 4) * L::kScales;
 #pragma unroll
-    for (int u = 0; u < 2; ++u)
-#pragma unroll
-      for (int r = 0; r < 2; ++r) {
-        const int64_t j = keys.kb + u * kSub + r * 8 + g;
-        off[u][r] = j < keys.lo || j >= keys.hi || !keys.page_ok[u];
-      }
-    // what a masked key's V scales hold must not count
-    {
-      const int64_t j = keys.kb + lane;
-      if (j < keys.lo || j >= keys.hi || !keys.page_ok[lane >> 4]) {
-        uint8_t* p = st + L::kVs + (lane >> 4) * L::kScales;
-#pragma unroll
-        for (int b = 0; b < NB; ++b) p[v_scale<D>(lane & 15, b)] = 0;
-      }
+      for (int b = 0; b < NB; ++b) p[v_scale<D>(lane & 15, b)] = 0;
     }
     __syncwarp();
   }
 
-  // ---- logits
+  // ---- K q
   float z[2][NT][4];
 #pragma unroll
   for (int u = 0; u < 2; ++u) {
+    const uint8_t* kp = st + L::kK + u * L::kCodes + lane * (D / 8);
+    const uint8_t* sp = st + L::kKs + u * L::kScales + g * NB;
+    uint32_t wl[NB], wh[NB];
+    lds(kp, wl);
+    lds(kp + L::kCodes / 2, wh);
+    float sl[NB], sh[NB];
+    key_scales<NB>(sp, sl);
+    key_scales<NB>(sp + 8 * NB, sh);
 #pragma unroll
-    for (int n = 0; n < NT; ++n) z[u][n][0] = z[u][n][1] = z[u][n][2] = z[u][n][3] = 0.0f;
-    const uint8_t* kp = st + L::kK + u * L::kCodes;
-    const uint8_t* sp = st + L::kKs + u * L::kScales;
+    for (int b = 0; b < NB; ++b) {
+      uint32_t al[4], ah[4];
+      e2m1x8_to_f16(wl[b], al);
+      e2m1x8_to_f16(wh[b], ah);
+      const uint32_t a0[4] = {al[0], ah[0], al[1], ah[1]}, a1[4] = {al[2], ah[2], al[3], ah[3]};
 #pragma unroll
-    for (int b0 = 0; b0 < NB; b0 += 4) {
-      constexpr int W = NB < 4 ? NB : 4;
-      uint32_t wl[4], wh[4], scl = 0, sch = 0;
-      if constexpr (W == 4) {
-        const uint4 a = *reinterpret_cast<const uint4*>(kp + k_word<D>(g, t, b0));
-        const uint4 c = *reinterpret_cast<const uint4*>(kp + k_word<D>(g + 8, t, b0));
-        wl[0] = a.x, wl[1] = a.y, wl[2] = a.z, wl[3] = a.w;
-        wh[0] = c.x, wh[1] = c.y, wh[2] = c.z, wh[3] = c.w;
-        scl = *reinterpret_cast<const uint32_t*>(sp + g * NB + b0);
-        sch = *reinterpret_cast<const uint32_t*>(sp + (g + 8) * NB + b0);
-      } else {
-        const uint2 a = *reinterpret_cast<const uint2*>(kp + k_word<D>(g, t, b0));
-        const uint2 c = *reinterpret_cast<const uint2*>(kp + k_word<D>(g + 8, t, b0));
-        wl[0] = a.x, wl[1] = a.y, wh[0] = c.x, wh[1] = c.y;
-        wl[2] = wl[3] = wh[2] = wh[3] = 0;
-        scl = *reinterpret_cast<const uint16_t*>(sp + g * NB + b0);
-        sch = *reinterpret_cast<const uint16_t*>(sp + (g + 8) * NB + b0);
-      }
-      float sl[4], sh[4];
-      e8m0x4_to_f32(scl, sl);
-      e8m0x4_to_f32(sch, sh);
+      for (int n = 0; n < NT; ++n) {
+        uint32_t q[4];
+        lds(qf + ((n * NB + b) * 32 + lane) * 16, q);
+        const float zero[4] = {};
+        float d[4];
+        mma_16816(d, a0, q[0], q[1], zero);
+        mma_16816(d, a1, q[2], q[3], d);
 #pragma unroll
-      for (int i = 0; i < W; ++i) {
-        uint32_t al[4], ah[4];
-        e2m1x8_to_f16(wl[i], al);
-        e2m1x8_to_f16(wh[i], ah);
-        const uint32_t a0[4] = {al[0], ah[0], al[1], ah[1]}, a1[4] = {al[2], ah[2], al[3], ah[3]};
-#pragma unroll
-        for (int n = 0; n < NT; ++n) {
-          const float zero[4] = {};
-          float d[4];
-          mma_16816(d, a0, q[n][b0 + i][0], q[n][b0 + i][1], zero);
-          mma_16816(d, a1, q[n][b0 + i][2], q[n][b0 + i][3], d);
-          z[u][n][0] = fmaf(sl[i], d[0], z[u][n][0]);
-          z[u][n][1] = fmaf(sl[i], d[1], z[u][n][1]);
-          z[u][n][2] = fmaf(sh[i], d[2], z[u][n][2]);
-          z[u][n][3] = fmaf(sh[i], d[3], z[u][n][3]);
+        for (int c = 0; c < 4; ++c) {
+          const float sc = c < 2 ? sl[b] : sh[b];
+          z[u][n][c] = b == 0 ? sc * d[c] : fmaf(sc, d[c], z[u][n][c]);
         }
       }
     }
+  }
+  if (on != kAll) {
+#pragma unroll
+    for (int u = 0; u < 2; ++u)
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+          if (!((on >> (u * 16 + (c >> 1) * 8 + g)) & 1u)) z[u][n][c] = -INFINITY;
   }
 
   // ---- running maximum, probabilities (times 2^6)
   uint32_t p[2][NT][2];  // f16x2 as the B fragment of out = V^T p
 #pragma unroll
   for (int n = 0; n < NT; ++n) {
-    float mx[2] = {s.m[n][0], s.m[n][1]};
+    float mx[2];
 #pragma unroll
-    for (int u = 0; u < 2; ++u)
-#pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        float v = z[u][n][c] * qs[n][c & 1];
-        if (edge && off[u][c >> 1]) v = -INFINITY;
-        z[u][n][c] = v;
-        mx[c & 1] = fmaxf(mx[c & 1], v);
-      }
-    mx[0] = over_g_max(mx[0]);
-    mx[1] = over_g_max(mx[1]);
-    const float b0 = mx[0] == -INFINITY ? 0.0f : mx[0], b1 = mx[1] == -INFINITY ? 0.0f : mx[1];
+    for (int c = 0; c < 2; ++c)
+      mx[c] = over_g_max(fmaxf(fmaxf(fmaxf(z[0][n][c], z[0][n][c + 2]), fmaxf(z[1][n][c], z[1][n][c + 2])), s.m[n][c]));
     if (__any_sync(kAll, mx[0] > s.m[n][0] || mx[1] > s.m[n][1])) {
-      const float f0 = exp2_fast(s.m[n][0] - b0), f1 = exp2_fast(s.m[n][1] - b1);
-      s.l[n][0] *= f0;
-      s.l[n][1] *= f1;
 #pragma unroll
-      for (int i = 0; i < D / 16; ++i) {
-        s.acc[n][i][0] *= f0;
-        s.acc[n][i][1] *= f1;
-        s.acc[n][i][2] *= f0;
-        s.acc[n][i][3] *= f1;
+      for (int c = 0; c < 2; ++c) {
+        // from -inf the sums are 0: any finite factor will do
+        const float f = s.m[n][c] == -INFINITY ? 0.0f : exp2_fast((s.m[n][c] - mx[c]) * qs[n][c]);
+        s.m[n][c] = mx[c];
+        s.l[n][c] *= f;
+#pragma unroll
+        for (int i = 0; i < D / 16; ++i) {
+          s.acc[n][i][c] *= f;
+          s.acc[n][i][c + 2] *= f;
+        }
       }
-      s.m[n][0] = mx[0];
-      s.m[n][1] = mx[1];
     }
+    // the maximum is taken off before the scale: exact at the maximum however large the logits are
+    const float base[2] = {mx[0] == -INFINITY ? 0.0f : mx[0], mx[1] == -INFINITY ? 0.0f : mx[1]};
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
-      const float e0 = exp2_fast(z[u][n][0] - b0 + 6.0f), e1 = exp2_fast(z[u][n][1] - b1 + 6.0f);
-      const float e2 = exp2_fast(z[u][n][2] - b0 + 6.0f), e3 = exp2_fast(z[u][n][3] - b1 + 6.0f);
-      s.l[n][0] += e0 + e2;
-      s.l[n][1] += e1 + e3;
-      p[u][n][0] = transpose8x8(pack2<false>(e0, e1));
-      p[u][n][1] = transpose8x8(pack2<false>(e2, e3));
+      float e[4];
+#pragma unroll
+      for (int c = 0; c < 4; ++c) e[c] = exp2_fast(fmaf(z[u][n][c] - base[c & 1], qs[n][c & 1], 6.0f));
+      s.l[n][0] += e[0] + e[2];
+      s.l[n][1] += e[1] + e[3];
+      p[u][n][0] = transpose8x8(pack2<false>(e[0], e[1]));
+      p[u][n][1] = transpose8x8(pack2<false>(e[2], e[3]));
     }
   }
 
-  // ---- running maximum of the V scales: a warp's 16 pairs x NWORD words
-  bool poison = false;  // a NaN block among the keys
+  // ---- V scales above the running maximum? (the 16 pairs' words lie together)
+  bool poison = false;
   {
-    constexpr int kWords = 16 * NWORD;  // of both runs, contiguous
+    constexpr int kWords = 16 * NWORD;
     bool above = false;
 #pragma unroll
-    for (int i = lane, r = 0; r < (kWords + 31) / 32; i += 32, ++r) {
-      if (i < kWords) {
+    for (int r = 0; r < (kWords + 31) / 32; ++r) {
+      const int i = lane + 32 * r;
+      if (kWords >= 32 || i < kWords) {
         const uint32_t w = *reinterpret_cast<const uint32_t*>(st + L::kVs + i * 4);
-        const uint32_t have = NWORD == 1 ? s.top[0]
-                              : NWORD == 2 ? ((i & 1) ? s.top[1] : s.top[0])
-                                           : ((i & 3) == 0   ? s.top[0]
-                                              : (i & 3) == 1 ? s.top[1]
-                                              : (i & 3) == 2 ? s.top[2]
-                                                             : s.top[3]);
+        uint32_t have = s.top[0];
+#pragma unroll
+        for (int k = 1; k < NWORD; ++k)
+          if (lane % NWORD == k) have = s.top[k];
         above |= __vmaxu4(w, have) != have;
       }
     }
     if (__any_sync(kAll, above)) {
-      uint32_t best[NB] = {};
+      Tops<NWORD> top;
 #pragma unroll
-      for (int i = lane, r = 0; r < (kWords + 31) / 32; i += 32, ++r) {
-        if (i < kWords) {
-          const uint32_t w = *reinterpret_cast<const uint32_t*>(st + L::kVs + i * 4);
-          const uint32_t c[4] = {w & 255u, (w >> 8) & 255u, (w >> 16) & 255u, w >> 24};
-          uint32_t lo = 0, hi = 0;
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            if (c[k] == 255u)
-              poison = true;
-            else if (k < 2)
-              lo = max(lo, c[k]);
-            else
-              hi = max(hi, c[k]);
-          }
-#pragma unroll
-          for (int b = 0; b < NB; b += 2)
-            if (i % NWORD == b / 2) {
-              best[b] = max(best[b], lo);
-              best[b + 1] = max(best[b + 1], hi);
-            }
-        }
-      }
-      poison = __any_sync(kAll, poison);
+      for (int k = 0; k < NWORD; ++k) top.w[k] = s.top[k];
+      top = raised_tops<D>(st + L::kVs, top);
+      poison = top.poison;
 #pragma unroll
       for (int b = 0; b < NB; ++b) {
-        const uint32_t have = (s.top[b / 2] >> (16 * (b & 1))) & 255u;
-        const uint32_t now = max(have, __reduce_max_sync(kAll, best[b]));
-        if (now > have) {
-          const float f = exp2i(max(-126, (int)have - (int)now));
+        const int have = (s.top[b / 2] >> (16 * (b & 1))) & 255u, now = (top.w[b / 2] >> (16 * (b & 1))) & 255u;
+        const float f = exp2i(max(-126, have - now));
 #pragma unroll
-          for (int n = 0; n < NT; ++n)
+        for (int n = 0; n < NT; ++n)
 #pragma unroll
-            for (int c = 0; c < 4; ++c) {
-              s.acc[n][2 * b][c] *= f;
-              s.acc[n][2 * b + 1][c] *= f;
-            }
-          const uint32_t two = now | now << 8;
-          s.top[b / 2] = (b & 1) ? (s.top[b / 2] & 0x0000FFFFu) | two << 16
-                                 : (s.top[b / 2] & 0xFFFF0000u) | two;
-        }
+          for (int c = 0; c < 4; ++c) {
+            s.acc[n][2 * b][c] *= f;
+            s.acc[n][2 * b + 1][c] *= f;
+          }
       }
+#pragma unroll
+      for (int k = 0; k < NWORD; ++k) s.top[k] = top.w[k];
     }
   }
 
   // ---- out += V^T p
+  uint32_t up[NB];  // 24 - top in both halves
+#pragma unroll
+  for (int b = 0; b < NB; ++b) {
+    const uint32_t d = 24u - ((s.top[b / 2] >> (16 * (b & 1))) & 255u);
+    up[b] = __byte_perm(d, d, 0x1010);
+  }
 #pragma unroll
   for (int u = 0; u < 2; ++u) {
-    const uint8_t* vp = st + L::kV + u * L::kCodes;
-    const uint8_t* sp = st + L::kVs + u * L::kScales;
+    uint32_t v[2][2 * NWORD], sc[2][NWORD];  // pairs t and t + 4: k rows 2t, 2t + 1 and 8 more
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      lds(st + L::kV + u * L::kCodes + (t + 4 * h) * D + g * (D / 8), v[h]);
+      lds(st + L::kVs + u * L::kScales + (t + 4 * h) * (D / 16), sc[h]);
+    }
 #pragma unroll
     for (int j = 0; j < NWORD; ++j) {
       uint32_t even[2][4], odd[2][4], mult[2][2];
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {  // pairs t and t + 4: k rows 2t, 2t + 1 and 8 more
-        const uint8_t* row = vp + (t + 4 * h) * D + g * (D / 8) + j * 4;
-        const uint32_t w0 = *reinterpret_cast<const uint32_t*>(row);
-        const uint32_t w1 = *reinterpret_cast<const uint32_t*>(row + D / 16);
+      for (int h = 0; h < 2; ++h) {
+        const uint32_t w0 = v[h][j], w1 = v[h][NWORD + j];
         e2m1x8_to_f16((w0 & 0x0F0F0F0Fu) | ((w1 << 4) & 0xF0F0F0F0u), even[h]);
         e2m1x8_to_f16(((w0 >> 4) & 0x0F0F0F0Fu) | (w1 & 0xF0F0F0F0u), odd[h]);
-        const uint32_t sc = *reinterpret_cast<const uint32_t*>(sp + (t + 4 * h) * (D / 16) + j * 4);
 #pragma unroll
         for (int k = 0; k < 2; ++k) {  // block 2j + k
-          const uint32_t two = __byte_perm(sc, 0, k ? 0x4342 : 0x4140);  // codes of the two keys
-          const int bias = 24 - (int)((s.top[j] >> (16 * k)) & 255u);
-          const uint32_t add = ((uint32_t)bias & 0xFFFFu) | (uint32_t)bias << 16;
-          uint32_t e = __viaddmax_s16x2_relu(two, add, 0u) << 10;
+          const uint32_t two = __byte_perm(sc[h][j], 0, k ? 0x4342 : 0x4140);  // codes of the two keys
+          // 2^(s - top + 9) as f16: exponent field s - top + 24, 0 where that is negative
+          uint32_t e = __viaddmax_s16x2_relu(two, up[2 * j + k], 0u) << 10;
           if (poison) {
             if ((two & 0xFFFFu) == 255u) e = (e & 0xFFFF0000u) | 0x7E00u;
             if ((two >> 16) == 255u) e = (e & 0x0000FFFFu) | 0x7E000000u;
@@ -361,112 +384,92 @@ __device__ __forceinline__ void attend_keys(uint8_t* st, const uint32_t (&q)[NT]
   }
 }
 
-// Start copying the 32 keys from kb of (sequence, head) into a ring stage.
+// Start copying the 32 keys from kb of (sequence, head) into a ring stage; page[u]
+// -1: zeros.
 template <int D>
-__device__ __forceinline__ void fetch(uint8_t* st, const AttendArgs& a, int head, int64_t kb,
+__device__ __forceinline__ void fetch(uint8_t* st, const AttendArgs& a, int head, uint32_t kb,
                                       const int (&page)[2]) {
   using L = Stage<D>;
   const int lane = threadIdx.x & 31;
 #pragma unroll
   for (int u = 0; u < 2; ++u) {
     const bool real = page[u] >= 0;
-    const int64_t key = kb + u * kSub;
-    const size_t at = ((((size_t)(real ? page[u] : 0) * a.heads) + head) << a.page_shift) +
-                      (size_t)(real ? (key & ((1 << a.page_shift) - 1)) : 0);
+    const uint32_t slot = (kb + u * kSub) & ((1u << a.page_shift) - 1u);
+    const size_t at = real ? (((size_t)page[u] * a.heads + head) << a.page_shift) + slot : 0;
+    const uint8_t *kc = a.kc + at * (D / 2) + lane * 16, *vc = a.vc + at * (D / 2) + lane * 16;
 #pragma unroll
     for (int i = 0; i < L::kCodes / 512; ++i) {
-      const int o = (lane + 32 * i) * 16;
-      cp_async16(st + L::kK + u * L::kCodes + o, a.kc + at * (D / 2) + o, real);
-      cp_async16(st + L::kV + u * L::kCodes + o, a.vc + at * (D / 2) + o, real);
+      cp_async16(st + L::kK + u * L::kCodes + lane * 16 + 512 * i, kc + 512 * i, real);
+      cp_async16(st + L::kV + u * L::kCodes + lane * 16 + 512 * i, vc + 512 * i, real);
     }
-    if (lane < L::kScales / 16)
-      cp_async16(st + L::kKs + u * L::kScales + lane * 16, a.ks + at * (D / 32) + lane * 16, real);
-    else if (lane >= 16 && lane < 16 + L::kScales / 16)
-      cp_async16(st + L::kVs + u * L::kScales + (lane - 16) * 16,
-                 a.vs + at * (D / 32) + (lane - 16) * 16, real);
-  }
-}
-
-// The pages of the two 16-key runs from kb (-1: outside the counted keys or invalid).
-__device__ __forceinline__ void pages_of(const AttendArgs& a, int seq, int64_t kb, int64_t lo,
-                                         int64_t hi, int (&page)[2]) {
-#pragma unroll
-  for (int u = 0; u < 2; ++u) {
-    const int64_t key = kb + u * kSub;
-    page[u] = -1;
-    if (key < hi && key + kSub > lo) {
-      const int id = __ldg(a.table + (int64_t)seq * a.max_blocks + (key >> a.page_shift));
-      if (id >= 0 && id < a.pages)
-        page[u] = id;
-      else
-        flag_invalid(a.err);
+    constexpr int n = L::kScales / 16;  // lanes 0 .. n - 1 copy K's scales, n .. 2n - 1 V's
+    if (lane < 2 * n) {
+      const uint8_t* sc = (lane < n ? a.ks : a.vs - n * 16) + at * (D / 32) + lane * 16;
+      cp_async16(st + (lane < n ? L::kKs : L::kVs - n * 16) + u * L::kScales + lane * 16, sc, real);
     }
   }
 }
 
-// The keys that count for sequence s and its number of tiles.
-__device__ __forceinline__ int tiles_of(const AttendArgs& a, int s, int64_t& lo, int64_t& hi) {
+// The keys that count for sequence s, and its number of tiles of TILE keys.
+template <int TILE>
+__device__ __forceinline__ int tiles_of(const AttendArgs& a, int s, uint32_t& lo, uint32_t& hi) {
   const int64_t len = __ldg(a.lens + s), most = (int64_t)a.max_blocks << a.page_shift;
-  hi = len < 0 ? 0 : len > most ? most : len;
-  lo = a.window > 0 && hi > a.window ? hi - a.window : 0;
-  return (int)((hi - (lo & ~(int64_t)(kSub - 1)) + kTileKeys - 1) / kTileKeys);
+  hi = (uint32_t)(len < 0 ? 0 : len > most ? most : len);
+  lo = a.window > 0 && hi > (uint32_t)a.window ? hi - a.window : 0u;
+  return (int)((hi - (lo & ~(uint32_t)(kWarpKeys - 1)) + TILE - 1) / TILE);
 }
 
-template <int D, int NT, int STAGES, bool BF16>
-__global__ void __launch_bounds__(kThreads)
-    kv4_attend_kernel(const AttendArgs a) {
+template <int D, int NT, int W, int STAGES, int CTAS, bool BF16>
+__global__ void __launch_bounds__(W * 32, CTAS) kv4_attend_kernel(const AttendArgs a) {
   using L = Stage<D>;
-  constexpr int NH = NT * 8;              // heads of a tile
-  constexpr int kPart = NH * (D + 2);     // floats of a partial result: acc [NH][D], m [NH], l [NH]
+  constexpr int TILE = W * kWarpKeys, THREADS = W * 32;
+  constexpr int NB = D / 32;
+  constexpr int NH = NT * 8;           // heads of a tile
+  constexpr int kPart = NH * (D + 2);  // floats of a partial result: acc [NH][D], m [NH], l [NH]
   extern __shared__ uint4 dyn4[];
   uint8_t* smem = reinterpret_cast<uint8_t*>(dyn4);
-  __shared__ int64_t s_scan[kWarpsPerCta];
-  __shared__ int64_t s_total, s_base;
+  __shared__ uint4 s_q[NT * NB * 32];
+  __shared__ float s_qs[NH];
+  __shared__ int64_t s_scan[W];
+  __shared__ int64_t s_base;
   __shared__ int s_seq;
-  __shared__ float s_m[kWarpsPerCta][NH], s_l[kWarpsPerCta][NH], s_w[kWarpsPerCta][NH];
+  __shared__ float s_m[W][NH], s_l[W][NH], s_w[W][NH];
   __shared__ float s_sum[NH], s_max[NH];
   __shared__ bool s_last;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
   const int rows = a.heads * a.head_tiles;  // of a sequence
-  int64_t lo, hi;
+  uint32_t lo, hi;
 
   // ---- this CTA's share of all tiles
+  int64_t total = 0;
   {
     int64_t sum = 0;
-    for (int s = tid; s < a.S; s += kThreads) {
-      const int n = tiles_of(a, s, lo, hi);
-      if (blockIdx.x == 0 && (__ldg(a.lens + s) < 0 ||
-                              __ldg(a.lens + s) > ((int64_t)a.max_blocks << a.page_shift)))
-        flag_invalid(a.err);
-      sum += (int64_t)n * rows;
+    for (int s = tid; s < a.S; s += THREADS) {
+      sum += (int64_t)tiles_of<TILE>(a, s, lo, hi) * rows;
+      if (blockIdx.x == 0 && (uint32_t)__ldg(a.lens + s) != hi) flag_invalid(a.err);
     }
 #pragma unroll
     for (int m = 16; m >= 1; m >>= 1) sum += __shfl_xor_sync(kAll, sum, m);
     if (lane == 0) s_scan[warp] = sum;
     __syncthreads();
-    if (tid == 0) {
-      int64_t all = 0;
-      for (int w = 0; w < kWarpsPerCta; ++w) all += s_scan[w];
-      s_total = all;
-    }
-    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < W; ++w) total += s_scan[w];
   }
-  const int64_t total = s_total;
   const int64_t G = total < gridDim.x ? total : gridDim.x;
   // sequences without keys: their outputs are zeros
   for (int s = blockIdx.x; s < a.S; s += gridDim.x) {
-    if (tiles_of(a, s, lo, hi) != 0) continue;
+    if (tiles_of<TILE>(a, s, lo, hi) != 0) continue;
     const int heads = a.heads * a.group;
-    for (int i = tid; i < heads * D; i += kThreads) a.out[(int64_t)s * a.ldo + i] = 0;
-    for (int i = tid; a.lse && i < heads; i += kThreads) a.lse[(int64_t)s * heads + i] = -INFINITY;
+    for (int i = tid; i < heads * D; i += THREADS) a.out[(int64_t)s * a.ldo + i] = 0;
+    for (int i = tid; a.lse && i < heads; i += THREADS) a.lse[(int64_t)s * heads + i] = -INFINITY;
   }
   if ((int64_t)blockIdx.x >= G) return;
   const int64_t begin = total * blockIdx.x / G, end = total * (blockIdx.x + 1) / G;
   {
     int64_t base = 0;
-    for (int s0 = 0; s0 < a.S; s0 += kThreads) {
+    for (int s0 = 0; s0 < a.S; s0 += THREADS) {
       const int s = s0 + tid;
-      const int64_t mine = s < a.S ? (int64_t)tiles_of(a, s, lo, hi) * rows : 0;
+      const int64_t mine = s < a.S ? (int64_t)tiles_of<TILE>(a, s, lo, hi) * rows : 0;
       int64_t inc = mine;
 #pragma unroll
       for (int d = 1; d < 32; d <<= 1) {
@@ -477,7 +480,8 @@ __global__ void __launch_bounds__(kThreads)
       if (lane == 31) s_scan[warp] = inc;
       __syncthreads();
       int64_t before = base, chunk = 0;
-      for (int w = 0; w < kWarpsPerCta; ++w) {
+#pragma unroll
+      for (int w = 0; w < W; ++w) {
         if (w < warp) before += s_scan[w];
         chunk += s_scan[w];
       }
@@ -493,90 +497,108 @@ __global__ void __launch_bounds__(kThreads)
   }
   int seq = s_seq;
   int64_t base = s_base;
-  int n_tiles = tiles_of(a, seq, lo, hi);
+  int n_tiles = tiles_of<TILE>(a, seq, lo, hi);
   uint8_t* ring = smem + (size_t)warp * STAGES * L::kBytes;
 
   for (int64_t pos = begin; pos < end;) {
     while (pos >= base + (int64_t)n_tiles * rows) {
       base += (int64_t)n_tiles * rows;
-      n_tiles = tiles_of(a, ++seq, lo, hi);
+      n_tiles = tiles_of<TILE>(a, ++seq, lo, hi);
     }
     const int row = (int)((pos - base) / n_tiles), first = (int)((pos - base) - (int64_t)row * n_tiles);
     const int last = (int)min((int64_t)n_tiles, first + (end - pos));  // tiles [first, last) of the row
     const int head = row / a.head_tiles, h0 = (row % a.head_tiles) * NH;
     const int nh = min(NH, a.group - h0);  // real heads of the tile
-    const int64_t k0 = lo & ~(int64_t)(kSub - 1);
 
-    // ---- queries: f16 times a power of two per head
-    uint32_t q[NT][D / 32][4];
-    float qs[NT][2];
-#pragma unroll
-    for (int n = 0; n < NT; ++n) {
+    // ---- the warp's keys: 32 of each tile, from kw on, TILE apart
+    const int iters = last - first;
+    const uint32_t kw = (lo & ~(uint32_t)(kWarpKeys - 1)) + (uint32_t)first * TILE + warp * kWarpKeys;
+    const int32_t* trow = a.table + (int64_t)seq * a.max_blocks;
+    // pages of the 16-key runs: lane l holds run (l & 1) of iteration i0 + (l >> 1);
+    // -1: no key of the run counts, or its page is invalid
+    int held = -1;
+    auto hold = [&](int i0) {
+      const uint32_t key = kw + (uint32_t)(i0 + (lane >> 1)) * TILE + (lane & 1) * kSub;
+      held = -1;
+      if (i0 + (lane >> 1) < iters && key < hi && key + kSub > lo) {
+        held = __ldg(trow + (key >> a.page_shift));
+        if (held < 0 || held >= a.pages) {
+          held = -1;
+          flag_invalid(a.err);
+        }
+      }
+    };
+    uint32_t ok = 0;  // two bits per iteration in flight, the oldest lowest: pages that hold keys
+    auto start = [&](int i, int stage) {
+      if ((i & 15) == 0) hold(i);
+      int page[2];
+      page[0] = __shfl_sync(kAll, held, (i & 15) * 2);
+      page[1] = __shfl_sync(kAll, held, (i & 15) * 2 + 1);
+      if (i < iters) fetch<D>(ring + stage * L::kBytes, a, head, kw + (uint32_t)i * TILE, page);
+      ok |= ((page[0] >= 0 ? 1u : 0u) | (page[1] >= 0 ? 2u : 0u)) << (2 * (STAGES - 1));
+      cp_async_commit();
+    };
+#pragma unroll 1
+    for (int i = 0; i < STAGES - 1; ++i) {
+      start(i, i);
+      ok >>= 2;
+    }
+
+    // ---- queries: f16 times a power of two per head, the scale's sign among it
+    for (int n = warp; n < NT; n += W) {
       const bool real = n * 8 + g < nh;
       const uint16_t* qp = a.q + (int64_t)seq * a.ldq + ((int64_t)head * a.group + h0 + (real ? n * 8 + g : 0)) * D;
       float m = 0.0f;
-      uint4 raw[D / 32];
+      uint4 raw[NB];
 #pragma unroll
-      for (int b = 0; b < D / 32; ++b) {
-        raw[b] = real ? ld_cached16(qp + 32 * b + 8 * t) : make_uint4(0, 0, 0, 0);
+      for (int b = 0; b < NB; ++b) raw[b] = real ? ld_cached16(qp + 32 * b + 8 * t) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+      for (int b = 0; b < NB; ++b) {
         float f[8];
         unpack8<BF16>(raw[b], f);
 #pragma unroll
-        for (int j = 0; j < 8; ++j)
-          if (fabsf(f[j]) < INFINITY) m = fmaxf(m, fabsf(f[j]));
+        for (int k = 0; k < 8; ++k)
+          if (fabsf(f[k]) < INFINITY) m = fmaxf(m, fabsf(f[k]));
       }
       m = fmaxf(m, __shfl_xor_sync(kAll, m, 1));
       m = fmaxf(m, __shfl_xor_sync(kAll, m, 2));
       const int sigma = pow2_shift_for(m);
-      const float up = exp2i(sigma), back = exp2i(-sigma) * a.scale_log2;
+      const float up = copysignf(exp2i(sigma), a.scale_log2);
 #pragma unroll
-      for (int b = 0; b < D / 32; ++b) {
+      for (int b = 0; b < NB; ++b) {
         float f[8];
         unpack8<BF16>(raw[b], f);
-#pragma unroll
-        for (int j = 0; j < 4; ++j) q[n][b][j] = pack2<false>(f[2 * j] * up, f[2 * j + 1] * up);
+        s_q[(n * NB + b) * 32 + lane] =
+            make_uint4(pack2<false>(f[0] * up, f[1] * up), pack2<false>(f[2] * up, f[3] * up),
+                       pack2<false>(f[4] * up, f[5] * up), pack2<false>(f[6] * up, f[7] * up));
       }
-      qs[n][0] = __shfl_sync(kAll, back, 8 * t);  // head 2t: lane g = 2t
-      qs[n][1] = __shfl_sync(kAll, back, 8 * t + 4);
+      const float back = exp2i(-sigma) * fabsf(a.scale_log2);
+      if (t == 0) s_qs[n * 8 + g] = back == 0.0f ? 1.17549435e-38f : back;  // masked: -inf times it stays -inf
+    }
+    __syncthreads();
+    float qs[NT][2];
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+      qs[n][0] = s_qs[n * 8 + 2 * t];
+      qs[n][1] = s_qs[n * 8 + 2 * t + 1];
     }
 
-    // ---- the warp's keys of tiles [first, last)
     State<D, NT> st;
     clear(st);
-    const int iters = last - first;
-    const int64_t kw = k0 + (int64_t)first * kTileKeys + warp * kWarpKeys;  // of iteration 0
-    int page[STAGES][2];  // pages of the stages in flight
-#pragma unroll
-    for (int i = 0; i < STAGES - 1; ++i) {
-      page[i][0] = page[i][1] = -1;
-      if (i < iters) {
-        pages_of(a, seq, kw + (int64_t)i * kTileKeys, lo, hi, page[i]);
-        fetch<D>(ring + i * L::kBytes, a, head, kw + (int64_t)i * kTileKeys, page[i]);
+#pragma unroll 1
+    for (int i = 0, stage = 0; i < iters; ++i, stage = stage + 1 == STAGES ? 0 : stage + 1) {
+      cp_async_wait<STAGES - 2>();
+      __syncwarp();
+      start(i + STAGES - 1, stage == 0 ? STAGES - 1 : stage - 1);
+      const uint32_t kb = kw + (uint32_t)i * TILE;
+      uint32_t on = ((ok & 1u) ? 0x0000FFFFu : 0u) | ((ok & 2u) ? 0xFFFF0000u : 0u);
+      ok >>= 2;
+      if (on) {
+        if (kb < lo) on &= kAll << (lo - kb);       // lo - kb < 32: the run counts
+        if (kb + kWarpKeys > hi) on &= kAll >> (kb + kWarpKeys - hi);
+        attend_keys<D, NT>(ring + stage * L::kBytes, reinterpret_cast<const uint8_t*>(s_q), qs, on, st);
       }
-      cp_async_commit();
-    }
-    int next[2] = {-1, -1};  // pages of the next stage to fetch
-    if (STAGES - 1 < iters) pages_of(a, seq, kw + (int64_t)(STAGES - 1) * kTileKeys, lo, hi, next);
-    for (int i0 = 0; i0 < iters; i0 += STAGES) {
-#pragma unroll
-      for (int k = 0; k < STAGES; ++k) {
-        const int i = i0 + k;
-        if (i >= iters) break;
-        cp_async_wait<STAGES - 2>();
-        __syncwarp();
-        constexpr int kAhead = STAGES - 1;
-        const int into = (k + kAhead) % STAGES;
-        page[into][0] = next[0];
-        page[into][1] = next[1];
-        if (i + kAhead < iters)
-          fetch<D>(ring + into * L::kBytes, a, head, kw + (int64_t)(i + kAhead) * kTileKeys, next);
-        cp_async_commit();
-        next[0] = next[1] = -1;
-        if (i + STAGES < iters) pages_of(a, seq, kw + (int64_t)(i + STAGES) * kTileKeys, lo, hi, next);
-        const Keys keys = {kw + (int64_t)i * kTileKeys, lo, hi, {page[k][0] >= 0, page[k][1] >= 0}};
-        if (keys.kb < hi && keys.kb + kWarpKeys > lo) attend_keys<D, NT>(ring + k * L::kBytes, q, qs, keys, st);
-        __syncwarp();
-      }
+      __syncwarp();
     }
     cp_async_wait<0>();
 
@@ -587,13 +609,14 @@ __global__ void __launch_bounds__(kThreads)
     for (int n = 0; n < NT; ++n) {
       const float l0 = over_g_sum(st.l[n][0]), l1 = over_g_sum(st.l[n][1]);
       if (g == 0) {
-        s_m[warp][n * 8 + 2 * t] = st.m[n][0];
-        s_m[warp][n * 8 + 2 * t + 1] = st.m[n][1];
+#pragma unroll
+        for (int c = 0; c < 2; ++c)
+          s_m[warp][n * 8 + 2 * t + c] = st.m[n][c] == -INFINITY ? -INFINITY : st.m[n][c] * qs[n][c];
         s_l[warp][n * 8 + 2 * t] = l0;
         s_l[warp][n * 8 + 2 * t + 1] = l1;
       }
 #pragma unroll
-      for (int b = 0; b < D / 32; ++b) {
+      for (int b = 0; b < NB; ++b) {
         // the accumulators hold 2^6 p times 2^(9 - top) of the scale
         const float f = e8m0_to_f32((st.top[b / 2] >> (16 * (b & 1))) & 255u) * 0.001953125f;
 #pragma unroll
@@ -607,11 +630,11 @@ __global__ void __launch_bounds__(kThreads)
     if (tid < NH) {
       float m = s_m[0][tid];
 #pragma unroll
-      for (int w = 1; w < kWarpsPerCta; ++w) m = fmaxf(m, s_m[w][tid]);
+      for (int w = 1; w < W; ++w) m = fmaxf(m, s_m[w][tid]);
       const float b = m == -INFINITY ? 0.0f : m;
       float l = 0.0f;
 #pragma unroll
-      for (int w = 0; w < kWarpsPerCta; ++w) {
+      for (int w = 0; w < W; ++w) {
         const float f = exp2_fast(s_m[w][tid] - b);
         s_w[w][tid] = f;
         l = fmaf(s_l[w][tid], f, l);
@@ -622,24 +645,29 @@ __global__ void __launch_bounds__(kThreads)
     __syncthreads();
     const bool whole = first == 0 && last == n_tiles;
     const int64_t row0 = base + (int64_t)row * n_tiles;
-    const int64_t c0 = whole ? 0 : ((row0 + 1) * G - 1) / total;
+    const int64_t c0 = whole ? 0 : ((row0 + 1) * G - 1) / total;  // the row's first CTA
     float* part = a.parts + ((size_t)blockIdx.x * 2 + ((int64_t)blockIdx.x == c0 ? 1 : 0)) * kPart;
     const int heads = a.heads * a.group;
     uint16_t* orow = a.out + (int64_t)seq * a.ldo + ((int64_t)head * a.group + h0) * D;
     float* lrow = a.lse ? a.lse + (int64_t)seq * heads + head * a.group + h0 : nullptr;
-    for (int i = tid * 2; i < nh * D; i += kThreads * 2) {
+    for (int i = tid * 4; i < nh * D; i += THREADS * 4) {
       const int h = i / D;
-      float v0 = 0.0f, v1 = 0.0f;
+      float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll
-      for (int w = 0; w < kWarpsPerCta; ++w) {
-        const float2 v = *reinterpret_cast<const float2*>(sums + (size_t)w * NH * D + i);
-        v0 = fmaf(v.x, s_w[w][h], v0);
-        v1 = fmaf(v.y, s_w[w][h], v1);
+      for (int w = 0; w < W; ++w) {
+        const float4 o = *reinterpret_cast<const float4*>(sums + (size_t)w * NH * D + i);
+        const float f = s_w[w][h];
+        v.x = fmaf(o.x, f, v.x);
+        v.y = fmaf(o.y, f, v.y);
+        v.z = fmaf(o.z, f, v.z);
+        v.w = fmaf(o.w, f, v.w);
       }
-      if (whole)
-        *reinterpret_cast<uint32_t*>(orow + i) = pack2<BF16>(v0 / s_sum[h], v1 / s_sum[h]);
-      else
-        *reinterpret_cast<float2*>(part + i) = make_float2(v0, v1);
+      if (whole) {
+        const float inv = 1.0f / s_sum[h];
+        *reinterpret_cast<uint2*>(orow + i) = make_uint2(pack2<BF16>(v.x * inv, v.y * inv), pack2<BF16>(v.z * inv, v.w * inv));
+      } else {
+        *reinterpret_cast<float4*>(part + i) = v;
+      }
     }
     if (tid < nh) {
       if (whole) {
@@ -660,37 +688,53 @@ __global__ void __launch_bounds__(kThreads)
       if (s_last) {
         __threadfence();
         if (tid == 0) a.arrived[c0] = 0;
-        const float* p0 = a.parts + ((size_t)c0 * 2 + 1) * kPart;        // of the first CTA
-        const float* p1 = a.parts + (size_t)(c0 + 1) * 2 * kPart;        // of the others, 2 * kPart apart
+        const float* p0 = a.parts + ((size_t)c0 * 2 + 1) * kPart;  // of the first CTA
+        const float* p1 = a.parts + (size_t)(c0 + 1) * 2 * kPart;  // of the others, 2 * kPart apart
         auto at = [&](int i) { return i == 0 ? p0 : p1 + (size_t)(i - 1) * 2 * kPart; };
-        if (tid < nh) {
-          float m = -INFINITY, l = 0.0f;
-          for (int i = 0; i < parts; ++i) m = fmaxf(m, __ldcg(at(i) + NH * D + tid));
+        float* wts = reinterpret_cast<float*>(smem);  // [parts][NH]: maxima, then weights
+        for (int h = warp; h < nh; h += W) {  // a warp per head
+          float m = -INFINITY;
+          for (int i = lane; i < parts; i += 32) {
+            const float v = __ldcg(at(i) + NH * D + h);
+            wts[i * NH + h] = v;
+            m = fmaxf(m, v);
+          }
+          m = warp_max(m);
           const float b = m == -INFINITY ? 0.0f : m;
-          for (int i = 0; i < parts; ++i)
-            l = fmaf(__ldcg(at(i) + NH * D + NH + tid), exp2_fast(__ldcg(at(i) + NH * D + tid) - b), l);
-          s_max[tid] = b;
-          s_sum[tid] = l;
-          if (lrow) lrow[tid] = (b + log2f(l) - 6.0f) * 0.6931471805599453f;
+          float l = 0.0f;
+          for (int i = lane; i < parts; i += 32) {
+            const float f = exp2_fast(wts[i * NH + h] - b);
+            wts[i * NH + h] = f;
+            l = fmaf(__ldcg(at(i) + NH * D + NH + h), f, l);
+          }
+#pragma unroll
+          for (int k = 16; k >= 1; k >>= 1) l += __shfl_xor_sync(kAll, l, k);
+          if (lane == 0) {
+            s_sum[h] = l;
+            if (lrow) lrow[h] = (b + log2f(l) - 6.0f) * 0.6931471805599453f;
+          }
         }
         __syncthreads();
-        for (int i = tid * 4; i < nh * D; i += kThreads * 4) {
+        for (int i = tid * 4; i < nh * D; i += THREADS * 4) {
           const int h = i / D;
           float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll 4
-          for (int k = 0; k < parts; ++k) {
-            const float f = exp2_fast(__ldcg(at(k) + NH * D + h) - s_max[h]);
-            const float4 o = __ldcg(reinterpret_cast<const float4*>(at(k) + i));
-            v.x = fmaf(o.x, f, v.x);
-            v.y = fmaf(o.y, f, v.y);
-            v.z = fmaf(o.z, f, v.z);
-            v.w = fmaf(o.w, f, v.w);
+          for (int k0 = 0; k0 < parts; k0 += 8) {
+            float4 o[8];
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+              if (k0 + k < parts) o[k] = __ldcg(reinterpret_cast<const float4*>(at(k0 + k) + i));
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+              if (k0 + k < parts) {
+                const float f = wts[(k0 + k) * NH + h];
+                v.x = fmaf(o[k].x, f, v.x);
+                v.y = fmaf(o[k].y, f, v.y);
+                v.z = fmaf(o[k].z, f, v.z);
+                v.w = fmaf(o[k].w, f, v.w);
+              }
           }
           const float inv = 1.0f / s_sum[h];
-          uint2 o;
-          o.x = pack2<BF16>(v.x * inv, v.y * inv);
-          o.y = pack2<BF16>(v.z * inv, v.w * inv);
-          *reinterpret_cast<uint2*>(orow + i) = o;
+          *reinterpret_cast<uint2*>(orow + i) = make_uint2(pack2<BF16>(v.x * inv, v.y * inv), pack2<BF16>(v.z * inv, v.w * inv));
         }
       }
     }
@@ -706,19 +750,26 @@ int head_tiles(const wd_kv4_cache* c, int group) {
   return (group + n - 1) / n;
 }
 
-template <int D, int NT, int STAGES, bool BF16>
-moe_status launch(const AttendArgs& a, unsigned grid, cudaStream_t st) {
-  auto k = kv4_attend_kernel<D, NT, STAGES, BF16>;
-  const size_t ring = (size_t)kWarpsPerCta * STAGES * Stage<D>::kBytes;
-  const size_t sums = (size_t)kWarpsPerCta * NT * 8 * D * 4;
-  const size_t smem = ring > sums ? ring : sums;
+constexpr int kMaxCtasPerSm = 2;
+
+template <int D, int NT, int W, int STAGES, int CTAS>
+moe_status launch(const AttendArgs& a, bool bf16, cudaStream_t st) {
+  static_assert(CTAS <= kMaxCtasPerSm, "the workspace has room for 2 CTAs per SM");
+  auto k = bf16 ? kv4_attend_kernel<D, NT, W, STAGES, CTAS, true> : kv4_attend_kernel<D, NT, W, STAGES, CTAS, false>;
+  const size_t ring = (size_t)W * STAGES * Stage<D>::kBytes;
+  const size_t sums = (size_t)W * NT * 8 * D * 4;
+  const size_t wts = (size_t)sm_count() * CTAS * NT * 8 * 4;
+  const size_t smem = ring > sums ? (ring > wts ? ring : wts) : (sums > wts ? sums : wts);
   moe_status rc = allow_smem(k, smem);
   if (rc != MOE_OK) return rc;
-  k<<<grid, kThreads, smem, st>>>(a);
+  // no more CTAs than tiles that the rows' capacity allows
+  const int64_t keys = (int64_t)a.max_blocks << a.page_shift;
+  const int64_t most = a.window > 0 && a.window + 2 * kWarpKeys < keys ? a.window + 2 * kWarpKeys : keys;
+  const int64_t tiles = (most + W * kWarpKeys - 1) / (W * kWarpKeys) * a.S * a.heads * a.head_tiles;
+  const int64_t grid = (int64_t)sm_count() * CTAS;
+  k<<<(unsigned)(tiles < grid ? tiles : grid), W * 32, smem, st>>>(a);
   return launched("wd_kv4_attend launch");
 }
-
-constexpr int kCtasPerSm = 1;
 
 size_t part_floats(const wd_kv4_cache* c, int group) {
   return (size_t)tile_heads(c, group) * (c->dim + 2);
@@ -731,7 +782,7 @@ extern "C" size_t wd_kv4_attend_workspace(const wd_kv4_cache* c, int32_t S, int3
   using namespace wd;
   if (!c || wd_kv4_cache_bytes(c, WD_KV4_CODES) == 0 || S < 0 || q_heads < 1 || q_heads % c->heads)
     return 0;
-  const size_t grid = (size_t)sm_count() * kCtasPerSm;
+  const size_t grid = (size_t)sm_count() * kMaxCtasPerSm;
   return (grid * 4 + 15) / 16 * 16 + grid * 2 * part_floats(c, q_heads / c->heads) * 4;
 }
 
@@ -758,7 +809,7 @@ extern "C" moe_status wd_kv4_attend(const wd_kv4_cache* c, const void* q, int32_
   if (workspace_bytes < wd_kv4_attend_workspace(c, S, q_heads))
     return refuse(MOE_ERR_SHAPE, "wd_kv4_attend: workspace is smaller than wd_kv4_attend_workspace");
   const int group = q_heads / c->heads;
-  const unsigned grid = (unsigned)(sm_count() * kCtasPerSm);
+  const unsigned grid = (unsigned)(sm_count() * kMaxCtasPerSm);
   AttendArgs a = {};
   a.kc = c->k_codes, a.ks = c->k_scales, a.vc = c->v_codes, a.vs = c->v_scales;
   a.q = static_cast<const uint16_t*>(q);
@@ -771,13 +822,7 @@ extern "C" moe_status wd_kv4_attend(const wd_kv4_cache* c, const void* q, int32_
   a.scale_log2 = scale * 1.4426950408889634f;
   cudaStream_t st = (cudaStream_t)stream;
   const bool bf16 = type == WD_BF16, wide = tile_heads(c, group) == 16;
-  if (c->dim == 64) {
-    if (wide) return bf16 ? launch<64, 2, 4, true>(a, grid, st) : launch<64, 2, 4, false>(a, grid, st);
-    return bf16 ? launch<64, 1, 4, true>(a, grid, st) : launch<64, 1, 4, false>(a, grid, st);
-  }
-  if (c->dim == 128) {
-    if (wide) return bf16 ? launch<128, 2, 4, true>(a, grid, st) : launch<128, 2, 4, false>(a, grid, st);
-    return bf16 ? launch<128, 1, 4, true>(a, grid, st) : launch<128, 1, 4, false>(a, grid, st);
-  }
-  return bf16 ? launch<256, 1, 3, true>(a, grid, st) : launch<256, 1, 3, false>(a, grid, st);
+  if (c->dim == 64) return wide ? launch<64, 2, 8, 4, 2>(a, bf16, st) : launch<64, 1, 8, 4, 2>(a, bf16, st);
+  if (c->dim == 128) return wide ? launch<128, 2, 12, 4, 1>(a, bf16, st) : launch<128, 1, 8, 3, 2>(a, bf16, st);
+  return launch<256, 1, 8, 3, 1>(a, bf16, st);
 }
