@@ -138,9 +138,8 @@ moe_status wd_kv4_gather(const wd_kv4_cache* cache, void* k_out, void* v_out, in
  * multiple of 8, 16-byte aligned); lse [S][q_heads] F32 or NULL. A sequence
  * without keys gets out = 0 and lse = -inf. Results are the same on every call
  * with the same inputs.
- * workspace: wd_kv4_attend_workspace bytes, 16-byte aligned, zeroed once when
- * it is allocated; a call leaves it ready for the next. Calls that may overlap
- * need one each.
+ * workspace: wd_kv4_attend_workspace bytes, 16-byte aligned; its contents do not
+ * matter before or after a call. Calls that may overlap need one each.
  */
 size_t wd_kv4_attend_workspace(const wd_kv4_cache* cache, int32_t S, int32_t q_heads);
 moe_status wd_kv4_attend(const wd_kv4_cache* cache, const void* q, int32_t type, int64_t ldq,

@@ -234,11 +234,11 @@ def wd_kv4_gather(cache: Kv4Cache, block_table: torch.Tensor, seq_lens: torch.Te
 
 
 def kv4_workspace(cache: Kv4Cache, S: int, q_heads: int) -> torch.Tensor:
-    """A workspace for wd_kv4_attend with this cache's sizes: zeroed, reusable, one per overlapping call."""
+    """A workspace for wd_kv4_attend with this cache's sizes: reusable, one per overlapping call."""
     n = int(lib().wd_kv4_attend_workspace(cache._ref, S, q_heads))
     if not n:
         raise ValueError(f"kv4_workspace: S {S} or q_heads {q_heads} (a multiple of {cache.heads}) is unsupported")
-    return torch.zeros(n, dtype=torch.uint8, device=cache.tensors[0].device)
+    return torch.empty(n, dtype=torch.uint8, device=cache.tensors[0].device)
 
 
 def wd_kv4_attend(cache: Kv4Cache, q: torch.Tensor, block_table: torch.Tensor, seq_lens: torch.Tensor,

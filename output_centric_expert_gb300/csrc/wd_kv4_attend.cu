@@ -10,7 +10,7 @@
 //   values down to 2^-32 of it). A block's 32 products are summed by two MMAs
 //   and added to the FP32 logit times the key's E8M0 scale.
 //   out = V^T p: rows are dims, k is the keys. A V scale belongs to (key, block):
-//   it multiplies the probabilities, which are f16 here (11 bits, 2^6 p): the
+//   it multiplies the probabilities, which are f16 here (11 bits, 2^2 p): the
 //   power of two 2^(s - M + 9), with M the running maximum of the block's scale
 //   codes, is exact in f16. A key whose scale is below 2^-23 of the block's
 //   largest adds nothing (its part is below FP32's own rounding of the sum's
@@ -21,9 +21,10 @@
 // lengths on the device, so ragged batches and single long sequences load the
 // SMs evenly and the host needs no lengths. In a tile each of the 8 warps takes
 // 32 keys by itself, streamed through its own cp.async ring. The warps' sums join
-// in shared memory. A row that several CTAs share is joined by the last of them
-// to finish (a counter per first CTA; the sums are taken in CTA order, so the
-// result does not depend on which one it is), without waiting.
+// in shared memory. A row that several CTAs share leaves their parts in the
+// workspace; a second, dependent launch joins them in CTA order. (Joining in the
+// last CTA to finish, by a counter, took 11 us of 42 for 76 parts of one row: one
+// SM reads them all.)
 #include "wd_block.cuh"
 #include "wd_kv4.cuh"
 
@@ -34,6 +35,16 @@ constexpr int kWarpKeys = 32;  // keys per warp and iteration
 constexpr int kSub = 16;       // keys of one MMA tile; a page holds whole ones
 constexpr unsigned kAll = 0xFFFFFFFFu;
 
+constexpr float kLift = 2.0f;   // probabilities are held times 2^2
+constexpr float kSlack = 4.0f;  // and may be 2^4 above their reference: 2^6, times 2^9 at most, fits f16
+
+constexpr int kMinTiles = 2;    // tiles of a CTA of a split row, on average
+
+// A row that begins in CTA c and goes on in the next: [c], parts 0 where there is none.
+struct __align__(16) Split {
+  int32_t parts, seq, head, nh;  // head: the first query head of the row
+};
+
 struct AttendArgs {
   const uint8_t *kc, *ks, *vc, *vs;
   const uint16_t* q;
@@ -41,7 +52,7 @@ struct AttendArgs {
   uint16_t* out;
   float* lse;
   float* parts;       // [2 * grid][heads of a tile * (D + 2)]
-  uint32_t* arrived;  // [grid]
+  Split* split;       // [grid]
   int32_t* err;
   int64_t ldq, ldo;
   int32_t S, max_blocks, pages, page_shift, heads, group, head_tiles, window;
@@ -76,6 +87,18 @@ __device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
   return *reinterpret_cast<const uint32_t*>(&r);
 }
 
+// d += a * b, and d = a * b: operands in place, so no register is copied around the MMA.
+__device__ __forceinline__ void mma_add(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void mma_new(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.0f));
+}
+
 __device__ __forceinline__ float over_g_max(float v) {
 #pragma unroll
   for (int m = 4; m <= 16; m <<= 1) v = fmaxf(v, __shfl_xor_sync(kAll, v, m));
@@ -100,7 +123,7 @@ struct Stage {
 // of head tile n is head n * 8 + c; a lane holds columns 2t and 2t + 1.
 template <int D, int NT>
 struct State {
-  float m[NT][2], l[NT][2];  // maximum of K q (before the scale), sum of 2^6 p
+  float m[NT][2], l[NT][2];  // reference of K q (before the scale), sum of 2^2 p
   float acc[NT][D / 16][4];  // rows of MMA tile 2b + h: dims 32b + 4g + 2h (first), + 1
   uint32_t top[D / 64];      // running maximum of the V scale codes, bytes (b, b, b + 1, b + 1) as in v_scales
 };
@@ -158,14 +181,13 @@ __device__ __forceinline__ void key_scales(const uint8_t* p, float (&f)[NB]) {
 template <int NWORD>
 struct Tops {
   uint32_t w[NWORD];
-  bool poison;  // a NaN block is among the keys
+  uint32_t nan;  // bit b: a NaN block b is among the keys
 };
 template <int D>
 __device__ __noinline__ Tops<D / 64> raised_tops(const uint8_t* vs, Tops<D / 64> top) {
   constexpr int NB = D / 32, NWORD = D / 64, kWords = 16 * NWORD;
   const int lane = threadIdx.x & 31;
-  bool poison = false;
-  uint32_t best[NB] = {};
+  uint32_t best[NB] = {}, nan = 0;
 #pragma unroll
   for (int r = 0; r < (kWords + 31) / 32; ++r) {
     const int i = lane + 32 * r;
@@ -176,7 +198,7 @@ __device__ __noinline__ Tops<D / 64> raised_tops(const uint8_t* vs, Tops<D / 64>
     for (int k = 0; k < 4; ++k) {
       const uint32_t c = (w >> (8 * k)) & 255u;
       if (c == 255u)
-        poison = true;
+        nan |= 1u << (2 * (i % NWORD) + (k >> 1));
       else
         both[k >> 1] = max(both[k >> 1], c);
     }
@@ -190,7 +212,7 @@ __device__ __noinline__ Tops<D / 64> raised_tops(const uint8_t* vs, Tops<D / 64>
     const uint32_t two = now | now << 8;
     top.w[b / 2] = (b & 1) ? (top.w[b / 2] & 0x0000FFFFu) | two << 16 : (top.w[b / 2] & 0xFFFF0000u) | two;
   }
-  top.poison = __any_sync(kAll, poison);
+  top.nan = __reduce_or_sync(kAll, nan);
   return top;
 }
 
@@ -235,10 +257,9 @@ __device__ __forceinline__ void attend_keys(uint8_t* st, const uint8_t* qf, cons
       for (int n = 0; n < NT; ++n) {
         uint32_t q[4];
         lds(qf + ((n * NB + b) * 32 + lane) * 16, q);
-        const float zero[4] = {};
         float d[4];
-        mma_16816(d, a0, q[0], q[1], zero);
-        mma_16816(d, a1, q[2], q[3], d);
+        mma_new(d, a0, q[0], q[1]);
+        mma_add(d, a1, q[2], q[3]);
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
           const float sc = c < 2 ? sl[b] : sh[b];
@@ -257,20 +278,24 @@ __device__ __forceinline__ void attend_keys(uint8_t* st, const uint8_t* qf, cons
           if (!((on >> (u * 16 + (c >> 1) * 8 + g)) & 1u)) z[u][n][c] = -INFINITY;
   }
 
-  // ---- running maximum, probabilities (times 2^6)
+  // ---- reference maximum, probabilities (times 2^2)
+  // The reference follows the maximum only when that is kSlack above it (in log 2
+  // units), so the sums are seldom rescaled; 2^2 p then stays below 2^6.
   uint32_t p[2][NT][2];  // f16x2 as the B fragment of out = V^T p
 #pragma unroll
   for (int n = 0; n < NT; ++n) {
     float mx[2];
 #pragma unroll
     for (int c = 0; c < 2; ++c)
-      mx[c] = over_g_max(fmaxf(fmaxf(fmaxf(z[0][n][c], z[0][n][c + 2]), fmaxf(z[1][n][c], z[1][n][c + 2])), s.m[n][c]));
-    if (__any_sync(kAll, mx[0] > s.m[n][0] || mx[1] > s.m[n][1])) {
+      mx[c] = fmaxf(fmaxf(z[0][n][c], z[0][n][c + 2]), fmaxf(z[1][n][c], z[1][n][c + 2]));
+    // (from -inf to -inf the difference is NaN, which is not above)
+    if (__any_sync(kAll, (mx[0] - s.m[n][0]) * qs[n][0] > kSlack || (mx[1] - s.m[n][1]) * qs[n][1] > kSlack)) {
 #pragma unroll
       for (int c = 0; c < 2; ++c) {
+        const float to = fmaxf(s.m[n][c], over_g_max(mx[c]));
         // from -inf the sums are 0: any finite factor will do
-        const float f = s.m[n][c] == -INFINITY ? 0.0f : exp2_fast((s.m[n][c] - mx[c]) * qs[n][c]);
-        s.m[n][c] = mx[c];
+        const float f = s.m[n][c] == -INFINITY ? 0.0f : exp2_fast((s.m[n][c] - to) * qs[n][c]);
+        s.m[n][c] = to;
         s.l[n][c] *= f;
 #pragma unroll
         for (int i = 0; i < D / 16; ++i) {
@@ -279,13 +304,13 @@ __device__ __forceinline__ void attend_keys(uint8_t* st, const uint8_t* qf, cons
         }
       }
     }
-    // the maximum is taken off before the scale: exact at the maximum however large the logits are
-    const float base[2] = {mx[0] == -INFINITY ? 0.0f : mx[0], mx[1] == -INFINITY ? 0.0f : mx[1]};
+    // the reference is taken off before the scale: exact near the maximum however large the logits are
+    const float base[2] = {s.m[n][0] == -INFINITY ? 0.0f : s.m[n][0], s.m[n][1] == -INFINITY ? 0.0f : s.m[n][1]};
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
       float e[4];
 #pragma unroll
-      for (int c = 0; c < 4; ++c) e[c] = exp2_fast(fmaf(z[u][n][c] - base[c & 1], qs[n][c & 1], 6.0f));
+      for (int c = 0; c < 4; ++c) e[c] = exp2_fast(fmaf(z[u][n][c] - base[c & 1], qs[n][c & 1], kLift));
       s.l[n][0] += e[0] + e[2];
       s.l[n][1] += e[1] + e[3];
       p[u][n][0] = transpose8x8(pack2<false>(e[0], e[1]));
@@ -294,7 +319,6 @@ __device__ __forceinline__ void attend_keys(uint8_t* st, const uint8_t* qf, cons
   }
 
   // ---- V scales above the running maximum? (the 16 pairs' words lie together)
-  bool poison = false;
   {
     constexpr int kWords = 16 * NWORD;
     bool above = false;
@@ -315,11 +339,11 @@ __device__ __forceinline__ void attend_keys(uint8_t* st, const uint8_t* qf, cons
 #pragma unroll
       for (int k = 0; k < NWORD; ++k) top.w[k] = s.top[k];
       top = raised_tops<D>(st + L::kVs, top);
-      poison = top.poison;
 #pragma unroll
       for (int b = 0; b < NB; ++b) {
         const int have = (s.top[b / 2] >> (16 * (b & 1))) & 255u, now = (top.w[b / 2] >> (16 * (b & 1))) & 255u;
-        const float f = exp2i(max(-126, have - now));
+        // a key with a NaN block makes that block's sums NaN, whatever its probability
+        const float f = (top.nan >> b) & 1u ? NAN : exp2i(max(-126, have - now));
 #pragma unroll
         for (int n = 0; n < NT; ++n)
 #pragma unroll
@@ -360,12 +384,7 @@ __device__ __forceinline__ void attend_keys(uint8_t* st, const uint8_t* qf, cons
         for (int k = 0; k < 2; ++k) {  // block 2j + k
           const uint32_t two = __byte_perm(sc[h][j], 0, k ? 0x4342 : 0x4140);  // codes of the two keys
           // 2^(s - top + 9) as f16: exponent field s - top + 24, 0 where that is negative
-          uint32_t e = __viaddmax_s16x2_relu(two, up[2 * j + k], 0u) << 10;
-          if (poison) {
-            if ((two & 0xFFFFu) == 255u) e = (e & 0xFFFF0000u) | 0x7E00u;
-            if ((two >> 16) == 255u) e = (e & 0x0000FFFFu) | 0x7E000000u;
-          }
-          mult[h][k] = e;
+          mult[h][k] = __viaddmax_s16x2_relu(two, up[2 * j + k], 0u) << 10;
         }
       }
 #pragma unroll
@@ -376,8 +395,8 @@ __device__ __forceinline__ void attend_keys(uint8_t* st, const uint8_t* qf, cons
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
           const uint32_t p0 = hmul2(p[u][n][0], mult[0][k]), p1 = hmul2(p[u][n][1], mult[1][k]);
-          mma_16816(s.acc[n][2 * (2 * j + k)], a0, p0, p1, s.acc[n][2 * (2 * j + k)]);
-          mma_16816(s.acc[n][2 * (2 * j + k) + 1], a1, p0, p1, s.acc[n][2 * (2 * j + k) + 1]);
+          mma_add(s.acc[n][2 * (2 * j + k)], a0, p0, p1);
+          mma_add(s.acc[n][2 * (2 * j + k) + 1], a1, p0, p1);
         }
       }
     }
@@ -430,32 +449,45 @@ __global__ void __launch_bounds__(W * 32, CTAS) kv4_attend_kernel(const AttendAr
   uint8_t* smem = reinterpret_cast<uint8_t*>(dyn4);
   __shared__ uint4 s_q[NT * NB * 32];
   __shared__ float s_qs[NH];
-  __shared__ int64_t s_scan[W];
-  __shared__ int64_t s_base;
-  __shared__ int s_seq;
+  __shared__ int s_scan[W];
+  __shared__ int s_base, s_seq;
   __shared__ float s_m[W][NH], s_l[W][NH], s_w[W][NH];
   __shared__ float s_sum[NH], s_max[NH];
-  __shared__ bool s_last;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
   const int rows = a.heads * a.head_tiles;  // of a sequence
   uint32_t lo, hi;
 
-  // ---- this CTA's share of all tiles
-  int64_t total = 0;
-  {
-    int64_t sum = 0;
-    for (int s = tid; s < a.S; s += THREADS) {
-      sum += (int64_t)tiles_of<TILE>(a, s, lo, hi) * rows;
+  if (tid == 0) a.split[blockIdx.x].parts = 0;  // until this CTA turns out to begin a split row
+  launch_dependents();
+  // ---- this CTA's share of all tiles: an inclusive scan over the sequences
+  const int chunks = (a.S + THREADS - 1) / THREADS;
+  int with_keys = 0;  // sequences
+  auto scan = [&](int chunk, int before, int& inc, int& mine) {  // returns the tiles up to the chunk's end
+    const int s = chunk * THREADS + tid;
+    mine = 0;
+    if (s < a.S) {
+      mine = tiles_of<TILE>(a, s, lo, hi) * rows;
       if (blockIdx.x == 0 && (uint32_t)__ldg(a.lens + s) != hi) flag_invalid(a.err);
     }
+    inc = mine;
 #pragma unroll
-    for (int m = 16; m >= 1; m >>= 1) sum += __shfl_xor_sync(kAll, sum, m);
-    if (lane == 0) s_scan[warp] = sum;
-    __syncthreads();
+    for (int d = 1; d < 32; d <<= 1) {
+      const int o = __shfl_up_sync(kAll, inc, d);
+      if (lane >= d) inc += o;
+    }
+    if (chunks > 1) __syncthreads();  // s_scan may still be read
+    if (lane == 31) s_scan[warp] = inc;
+    with_keys += __syncthreads_count(mine > 0);
+    int end = before;
 #pragma unroll
-    for (int w = 0; w < W; ++w) total += s_scan[w];
-  }
-  const int64_t G = total < gridDim.x ? total : gridDim.x;
+    for (int w = 0; w < W; ++w) {
+      if (w == warp) inc += end;
+      end += s_scan[w];
+    }
+    return end;
+  };
+  int inc, mine, total = 0;
+  for (int k = 0; k < chunks; ++k) total = scan(k, total, inc, mine);
   // sequences without keys: their outputs are zeros
   for (int s = blockIdx.x; s < a.S; s += gridDim.x) {
     if (tiles_of<TILE>(a, s, lo, hi) != 0) continue;
@@ -463,50 +495,32 @@ __global__ void __launch_bounds__(W * 32, CTAS) kv4_attend_kernel(const AttendAr
     for (int i = tid; i < heads * D; i += THREADS) a.out[(int64_t)s * a.ldo + i] = 0;
     for (int i = tid; a.lse && i < heads; i += THREADS) a.lse[(int64_t)s * heads + i] = -INFINITY;
   }
-  if ((int64_t)blockIdx.x >= G) return;
-  const int64_t begin = total * blockIdx.x / G, end = total * (blockIdx.x + 1) / G;
-  {
-    int64_t base = 0;
-    for (int s0 = 0; s0 < a.S; s0 += THREADS) {
-      const int s = s0 + tid;
-      const int64_t mine = s < a.S ? (int64_t)tiles_of<TILE>(a, s, lo, hi) * rows : 0;
-      int64_t inc = mine;
-#pragma unroll
-      for (int d = 1; d < 32; d <<= 1) {
-        const int64_t o = __shfl_up_sync(kAll, inc, d);
-        if (lane >= d) inc += o;
-      }
-      __syncthreads();
-      if (lane == 31) s_scan[warp] = inc;
-      __syncthreads();
-      int64_t before = base, chunk = 0;
-#pragma unroll
-      for (int w = 0; w < W; ++w) {
-        if (w < warp) before += s_scan[w];
-        chunk += s_scan[w];
-      }
-      const int64_t start = before + inc - mine;
-      if (begin >= start && begin < start + mine) {
-        s_seq = s;
-        s_base = start;
-      }
-      base += chunk;
-      if (base > begin) break;
+  // CTA c of G has tiles [c q + min(c, r), ...) with total = G q + r. Rows are not cut
+  // finer than kMinTiles tiles on average: joining parts costs more than a tile
+  const int G = min((int)gridDim.x, max(with_keys * rows, (total + kMinTiles - 1) / kMinTiles));
+  if ((int)blockIdx.x >= G) return;
+  const int gq = total / G, gr = total - G * gq;
+  const int begin = (int)blockIdx.x * gq + min((int)blockIdx.x, gr);
+  const int end = begin + gq + ((int)blockIdx.x < gr ? 1 : 0);
+  for (int k = 0, before = 0; k < chunks; ++k) {
+    if (chunks > 1) before = scan(k, before, inc, mine);
+    if (begin >= inc - mine && begin < inc) {
+      s_seq = k * THREADS + tid;
+      s_base = inc - mine;
     }
-    __syncthreads();
   }
-  int seq = s_seq;
-  int64_t base = s_base;
+  __syncthreads();
+  int seq = s_seq, base = s_base;
   int n_tiles = tiles_of<TILE>(a, seq, lo, hi);
   uint8_t* ring = smem + (size_t)warp * STAGES * L::kBytes;
 
-  for (int64_t pos = begin; pos < end;) {
-    while (pos >= base + (int64_t)n_tiles * rows) {
-      base += (int64_t)n_tiles * rows;
+  for (int pos = begin; pos < end;) {
+    while (pos >= base + n_tiles * rows) {
+      base += n_tiles * rows;
       n_tiles = tiles_of<TILE>(a, ++seq, lo, hi);
     }
-    const int row = (int)((pos - base) / n_tiles), first = (int)((pos - base) - (int64_t)row * n_tiles);
-    const int last = (int)min((int64_t)n_tiles, first + (end - pos));  // tiles [first, last) of the row
+    const int row = (pos - base) / n_tiles, first = pos - base - row * n_tiles;
+    const int last = min(n_tiles, first + end - pos);  // tiles [first, last) of the row
     const int head = row / a.head_tiles, h0 = (row % a.head_tiles) * NH;
     const int nh = min(NH, a.group - h0);  // real heads of the tile
 
@@ -617,7 +631,7 @@ __global__ void __launch_bounds__(W * 32, CTAS) kv4_attend_kernel(const AttendAr
       }
 #pragma unroll
       for (int b = 0; b < NB; ++b) {
-        // the accumulators hold 2^6 p times 2^(9 - top) of the scale
+        // the accumulators hold 2^2 p times 2^(9 - top) of the scale
         const float f = e8m0_to_f32((st.top[b / 2] >> (16 * (b & 1))) & 255u) * 0.001953125f;
 #pragma unroll
         for (int c = 0; c < 2; ++c)
@@ -644,9 +658,13 @@ __global__ void __launch_bounds__(W * 32, CTAS) kv4_attend_kernel(const AttendAr
     }
     __syncthreads();
     const bool whole = first == 0 && last == n_tiles;
-    const int64_t row0 = base + (int64_t)row * n_tiles;
-    const int64_t c0 = whole ? 0 : ((row0 + 1) * G - 1) / total;  // the row's first CTA
-    float* part = a.parts + ((size_t)blockIdx.x * 2 + ((int64_t)blockIdx.x == c0 ? 1 : 0)) * kPart;
+    // a row that ends in another CTA's share: its first part goes to slot 1, the others to slot 0
+    float* part = a.parts + ((size_t)blockIdx.x * 2 + (first == 0 ? 1 : 0)) * kPart;
+    if (first == 0 && !whole && tid == 0) {
+      const int t1 = base + row * n_tiles + n_tiles - 1;  // the row's last tile, and the CTA that has it
+      const int c1 = t1 < gr * (gq + 1) ? t1 / (gq + 1) : gr + (t1 - gr * (gq + 1)) / gq;
+      a.split[blockIdx.x] = {c1 - (int)blockIdx.x + 1, seq, head * a.group + h0, nh};
+    }
     const int heads = a.heads * a.group;
     uint16_t* orow = a.out + (int64_t)seq * a.ldo + ((int64_t)head * a.group + h0) * D;
     float* lrow = a.lse ? a.lse + (int64_t)seq * heads + head * a.group + h0 : nullptr;
@@ -671,76 +689,81 @@ __global__ void __launch_bounds__(W * 32, CTAS) kv4_attend_kernel(const AttendAr
     }
     if (tid < nh) {
       if (whole) {
-        if (lrow) lrow[tid] = (s_max[tid] + log2f(s_sum[tid]) - 6.0f) * 0.6931471805599453f;
+        if (lrow) lrow[tid] = (s_max[tid] + log2f(s_sum[tid]) - kLift) * 0.6931471805599453f;
       } else {
         part[NH * D + tid] = s_max[tid];
         part[NH * D + NH + tid] = s_sum[tid];
       }
     }
-    if (!whole) {
-      // ---- the last CTA of the row joins its parts, in CTA order
-      const int64_t c1 = ((row0 + n_tiles) * G - 1) / total;
-      const int parts = (int)(c1 - c0) + 1;
-      __threadfence();
-      __syncthreads();
-      if (tid == 0) s_last = atomicAdd(a.arrived + c0, 1u) == (uint32_t)parts - 1;
-      __syncthreads();
-      if (s_last) {
-        __threadfence();
-        if (tid == 0) a.arrived[c0] = 0;
-        const float* p0 = a.parts + ((size_t)c0 * 2 + 1) * kPart;  // of the first CTA
-        const float* p1 = a.parts + (size_t)(c0 + 1) * 2 * kPart;  // of the others, 2 * kPart apart
-        auto at = [&](int i) { return i == 0 ? p0 : p1 + (size_t)(i - 1) * 2 * kPart; };
-        float* wts = reinterpret_cast<float*>(smem);  // [parts][NH]: maxima, then weights
-        for (int h = warp; h < nh; h += W) {  // a warp per head
-          float m = -INFINITY;
-          for (int i = lane; i < parts; i += 32) {
-            const float v = __ldcg(at(i) + NH * D + h);
-            wts[i * NH + h] = v;
-            m = fmaxf(m, v);
-          }
-          m = warp_max(m);
-          const float b = m == -INFINITY ? 0.0f : m;
-          float l = 0.0f;
-          for (int i = lane; i < parts; i += 32) {
-            const float f = exp2_fast(wts[i * NH + h] - b);
-            wts[i * NH + h] = f;
-            l = fmaf(__ldcg(at(i) + NH * D + NH + h), f, l);
-          }
-#pragma unroll
-          for (int k = 16; k >= 1; k >>= 1) l += __shfl_xor_sync(kAll, l, k);
-          if (lane == 0) {
-            s_sum[h] = l;
-            if (lrow) lrow[h] = (b + log2f(l) - 6.0f) * 0.6931471805599453f;
-          }
-        }
-        __syncthreads();
-        for (int i = tid * 4; i < nh * D; i += THREADS * 4) {
-          const int h = i / D;
-          float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-          for (int k0 = 0; k0 < parts; k0 += 8) {
-            float4 o[8];
-#pragma unroll
-            for (int k = 0; k < 8; ++k)
-              if (k0 + k < parts) o[k] = __ldcg(reinterpret_cast<const float4*>(at(k0 + k) + i));
-#pragma unroll
-            for (int k = 0; k < 8; ++k)
-              if (k0 + k < parts) {
-                const float f = wts[(k0 + k) * NH + h];
-                v.x = fmaf(o[k].x, f, v.x);
-                v.y = fmaf(o[k].y, f, v.y);
-                v.z = fmaf(o[k].z, f, v.z);
-                v.w = fmaf(o[k].w, f, v.w);
-              }
-          }
-          const float inv = 1.0f / s_sum[h];
-          *reinterpret_cast<uint2*>(orow + i) = make_uint2(pack2<BF16>(v.x * inv, v.y * inv), pack2<BF16>(v.z * inv, v.w * inv));
-        }
-      }
-    }
     __syncthreads();  // the sums and the ring share their memory
     pos += last - first;
   }
+}
+
+// Joins the parts of the rows that several CTAs share: a CTA per (first CTA of a
+// row, 256 sums of it); a quarter of the threads each takes every fourth part. A
+// dependent launch: its CTAs are resident when the parts are ready.
+constexpr int kJoin = 256;
+template <int D, int NT, bool BF16>
+__global__ void __launch_bounds__(kJoin) kv4_join_kernel(const AttendArgs a) {
+  constexpr int NH = NT * 8, kPart = NH * (D + 2), kHeads = kJoin / D < 1 ? 1 : kJoin / D;  // heads of a CTA's sums
+  __shared__ float s_max[4][kHeads], s_l[4][kHeads];
+  __shared__ float4 s_acc[4][kJoin / 4];
+  const int tid = threadIdx.x, quarter = tid >> 6, i = blockIdx.y * kJoin + (tid & 63) * 4;
+  wait_prerequisite();
+  const Split sp = a.split[blockIdx.x];
+  if (sp.parts == 0 || blockIdx.y * kJoin >= sp.nh * D) return;
+  const float* p0 = a.parts + ((size_t)blockIdx.x * 2 + 1) * kPart;  // of the first CTA
+  const float* p1 = a.parts + (size_t)(blockIdx.x + 1) * 2 * kPart;  // of the others, 2 * kPart apart
+  auto at = [&](int k) { return k == 0 ? p0 : p1 + (size_t)(k - 1) * 2 * kPart; };
+  const bool real = i < sp.nh * D;
+  const int h = real ? i / D : 0;
+  float m = -INFINITY;
+  for (int k = quarter; k < sp.parts; k += 4) m = fmaxf(m, __ldcg(at(k) + NH * D + h));
+  const int hl = (tid & 63) * 4 / D;  // the head among the CTA's
+  if ((tid & 63) * 4 % D == 0) s_max[quarter][hl] = m;
+  __syncthreads();
+  m = fmaxf(fmaxf(s_max[0][hl], s_max[1][hl]), fmaxf(s_max[2][hl], s_max[3][hl]));
+  const float b = m == -INFINITY ? 0.0f : m;
+  float l = 0.0f;
+  float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+  constexpr int kFlight = 8;  // parts in flight
+  for (int k0 = quarter; k0 < sp.parts; k0 += 4 * kFlight) {
+    float4 o[kFlight];
+    float om[kFlight], ol[kFlight];
+#pragma unroll
+    for (int k = 0; k < kFlight; ++k)
+      if (real && k0 + 4 * k < sp.parts) {
+        o[k] = __ldcg(reinterpret_cast<const float4*>(at(k0 + 4 * k) + i));
+        om[k] = __ldcg(at(k0 + 4 * k) + NH * D + h);
+        ol[k] = __ldcg(at(k0 + 4 * k) + NH * D + NH + h);
+      }
+#pragma unroll
+    for (int k = 0; k < kFlight; ++k)
+      if (real && k0 + 4 * k < sp.parts) {
+        const float f = exp2_fast(om[k] - b);
+        l = fmaf(ol[k], f, l);
+        v.x = fmaf(o[k].x, f, v.x);
+        v.y = fmaf(o[k].y, f, v.y);
+        v.z = fmaf(o[k].z, f, v.z);
+        v.w = fmaf(o[k].w, f, v.w);
+      }
+  }
+  s_acc[quarter][tid & 63] = v;
+  if ((tid & 63) * 4 % D == 0) s_l[quarter][hl] = l;
+  __syncthreads();
+  if (quarter != 0 || !real) return;
+  l = (s_l[0][hl] + s_l[1][hl]) + (s_l[2][hl] + s_l[3][hl]);
+#pragma unroll
+  for (int k = 1; k < 4; ++k) {
+    const float4 o = s_acc[k][tid & 63];
+    v.x += o.x, v.y += o.y, v.z += o.z, v.w += o.w;
+  }
+  const float inv = 1.0f / l;
+  uint16_t* orow = a.out + (int64_t)sp.seq * a.ldo + (int64_t)sp.head * D;
+  *reinterpret_cast<uint2*>(orow + i) = make_uint2(pack2<BF16>(v.x * inv, v.y * inv), pack2<BF16>(v.z * inv, v.w * inv));
+  if (a.lse && i % D == 0)
+    a.lse[(int64_t)sp.seq * a.heads * a.group + sp.head + h] = (b + log2f(l) - kLift) * 0.6931471805599453f;
 }
 
 // Heads of a tile: 8, or 16 where the group has more and the accumulators fit.
@@ -758,17 +781,36 @@ moe_status launch(const AttendArgs& a, bool bf16, cudaStream_t st) {
   auto k = bf16 ? kv4_attend_kernel<D, NT, W, STAGES, CTAS, true> : kv4_attend_kernel<D, NT, W, STAGES, CTAS, false>;
   const size_t ring = (size_t)W * STAGES * Stage<D>::kBytes;
   const size_t sums = (size_t)W * NT * 8 * D * 4;
-  const size_t wts = (size_t)sm_count() * CTAS * NT * 8 * 4;
-  const size_t smem = ring > sums ? (ring > wts ? ring : wts) : (sums > wts ? sums : wts);
+  const size_t smem = ring > sums ? ring : sums;
   moe_status rc = allow_smem(k, smem);
   if (rc != MOE_OK) return rc;
   // no more CTAs than tiles that the rows' capacity allows
   const int64_t keys = (int64_t)a.max_blocks << a.page_shift;
   const int64_t most = a.window > 0 && a.window + 2 * kWarpKeys < keys ? a.window + 2 * kWarpKeys : keys;
-  const int64_t tiles = (most + W * kWarpKeys - 1) / (W * kWarpKeys) * a.S * a.heads * a.head_tiles;
-  const int64_t grid = (int64_t)sm_count() * CTAS;
-  k<<<(unsigned)(tiles < grid ? tiles : grid), W * 32, smem, st>>>(a);
-  return launched("wd_kv4_attend launch");
+  const int64_t row_tiles = (most + W * kWarpKeys - 1) / (W * kWarpKeys);
+  const int64_t tiles = row_tiles * a.S * a.heads * a.head_tiles;
+  if (tiles > 0x7FFFFFFF) return refuse(MOE_ERR_SHAPE, "wd_kv4_attend: block_table's capacity is too large");
+  const int64_t fill = (int64_t)sm_count() * CTAS;
+  const unsigned grid = (unsigned)(tiles < fill ? tiles : fill);
+  k<<<grid, W * 32, smem, st>>>(a);
+  rc = launched("wd_kv4_attend launch");
+  if (rc != MOE_OK || row_tiles == 1) return rc;  // a row of one tile is never split
+  cudaLaunchAttribute dependent = {};
+  dependent.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  dependent.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid, NT * 8 * D / kJoin);
+  cfg.blockDim = dim3(kJoin);
+  cfg.stream = st;
+  cfg.attrs = &dependent;
+  cfg.numAttrs = 1;
+  const cudaError_t e =
+      bf16 ? cudaLaunchKernelEx(&cfg, kv4_join_kernel<D, NT, true>, a) : cudaLaunchKernelEx(&cfg, kv4_join_kernel<D, NT, false>, a);
+  if (e != cudaSuccess) {
+    set_error("wd_kv4_attend join launch", e);
+    return MOE_ERR_CUDA;
+  }
+  return MOE_OK;
 }
 
 size_t part_floats(const wd_kv4_cache* c, int group) {
@@ -783,7 +825,7 @@ extern "C" size_t wd_kv4_attend_workspace(const wd_kv4_cache* c, int32_t S, int3
   if (!c || wd_kv4_cache_bytes(c, WD_KV4_CODES) == 0 || S < 0 || q_heads < 1 || q_heads % c->heads)
     return 0;
   const size_t grid = (size_t)sm_count() * kMaxCtasPerSm;
-  return (grid * 4 + 15) / 16 * 16 + grid * 2 * part_floats(c, q_heads / c->heads) * 4;
+  return grid * sizeof(Split) + grid * 2 * part_floats(c, q_heads / c->heads) * 4;
 }
 
 extern "C" moe_status wd_kv4_attend(const wd_kv4_cache* c, const void* q, int32_t type,
@@ -814,8 +856,8 @@ extern "C" moe_status wd_kv4_attend(const wd_kv4_cache* c, const void* q, int32_
   a.kc = c->k_codes, a.ks = c->k_scales, a.vc = c->v_codes, a.vs = c->v_scales;
   a.q = static_cast<const uint16_t*>(q);
   a.table = table, a.lens = lens, a.out = static_cast<uint16_t*>(out), a.lse = lse;
-  a.arrived = static_cast<uint32_t*>(workspace);
-  a.parts = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + ((size_t)grid * 4 + 15) / 16 * 16);
+  a.split = static_cast<Split*>(workspace);
+  a.parts = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + (size_t)grid * sizeof(Split));
   a.err = err, a.ldq = ldq, a.ldo = ldo, a.S = S, a.max_blocks = max_blocks, a.pages = c->pages;
   a.page_shift = kv4_page_shift(c->page_size), a.heads = c->heads, a.group = group;
   a.head_tiles = head_tiles(c, group), a.window = window;
