@@ -16,12 +16,12 @@
 //   largest adds nothing (its part is below FP32's own rounding of the sum's
 //   largest term).
 //
-// Work. All (sequence, KV head, head tile) rows are cut into tiles of 256 keys;
-// CTA c of G takes the c-th contiguous share of all tiles, found from the
+// Work. All (sequence, KV head, head tile) rows are cut into tiles of 32 keys per
+// warp; CTA c of G takes the c-th contiguous share of all tiles, found from the
 // lengths on the device, so ragged batches and single long sequences load the
-// SMs evenly and the host needs no lengths. In a tile each of the 8 warps takes
-// 32 keys by itself, streamed through its own cp.async ring. The warps' sums join
-// in shared memory. A row that several CTAs share leaves their parts in the
+// SMs evenly and the host needs no lengths. In a tile each warp takes 32 keys by
+// itself, streamed through its own cp.async ring, which runs ahead into the CTA's
+// next row. The warps' sums join in shared memory. A row that several CTAs share leaves their parts in the
 // workspace; a second, dependent launch joins them in CTA order. (Joining in the
 // last CTA to finish, by a counter, took 11 us of 42 for 76 parts of one row: one
 // SM reads them all.)
@@ -39,6 +39,7 @@ constexpr float kLift = 2.0f;   // probabilities are held times 2^2
 constexpr float kSlack = 4.0f;  // and may be 2^4 above their reference: 2^6, times 2^9 at most, fits f16
 
 constexpr int kMinTiles = 2;    // tiles of a CTA of a split row, on average
+constexpr int kRowUnits = 1;    // what a row costs beside its tiles, in tiles: CTAs share both out
 
 // A row that begins in CTA c and goes on in the next: [c], parts 0 where there is none.
 struct __align__(16) Split {
@@ -438,6 +439,13 @@ __device__ __forceinline__ int tiles_of(const AttendArgs& a, int s, uint32_t& lo
   return (int)((hi - (lo & ~(uint32_t)(kWarpKeys - 1)) + TILE - 1) / TILE);
 }
 
+// A segment: the tiles of one row that fall to a CTA.
+struct Segment {
+  int seq, head, nh, iters;  // head: its first query head
+  uint32_t kw, lo, hi;       // the first tile's first key, the keys that count
+  int begins, ends, last_unit;  // whether it has the row's first and last tile; the latter's unit
+};
+
 template <int D, int NT, int W, int STAGES, int CTAS, bool BF16>
 __global__ void __launch_bounds__(W * 32, CTAS) kv4_attend_kernel(const AttendArgs a) {
   using L = Stage<D>;
@@ -445,28 +453,35 @@ __global__ void __launch_bounds__(W * 32, CTAS) kv4_attend_kernel(const AttendAr
   constexpr int NB = D / 32;
   constexpr int NH = NT * 8;           // heads of a tile
   constexpr int kPart = NH * (D + 2);  // floats of a partial result: acc [NH][D], m [NH], l [NH]
+  static_assert(8 * D * 4 <= L::kBytes && NH * D / 8 <= THREADS, "sums and query pieces");
   extern __shared__ uint4 dyn4[];
   uint8_t* smem = reinterpret_cast<uint8_t*>(dyn4);
+  __shared__ uint4 s_raw[2][NH * D / 8];  // two segments' queries as they are in memory
   __shared__ uint4 s_q[NT * NB * 32];
   __shared__ float s_qs[NH];
+  __shared__ Segment s_seg[W][2];  // every warp keeps its own
   __shared__ int s_scan[W];
   __shared__ int s_base, s_seq;
-  __shared__ float s_m[W][NH], s_l[W][NH], s_w[W][NH];
-  __shared__ float s_sum[NH], s_max[NH];
+  __shared__ float s_m[W][NH], s_l[W][NH];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
   const int rows = a.heads * a.head_tiles;  // of a sequence
-  uint32_t lo, hi;
 
   if (tid == 0) a.split[blockIdx.x].parts = 0;  // until this CTA turns out to begin a split row
   launch_dependents();
-  // ---- this CTA's share of all tiles: an inclusive scan over the sequences
+  // ---- this CTA's share of all units: an inclusive scan over the sequences
+  uint32_t lo, hi;
   const int chunks = (a.S + THREADS - 1) / THREADS;
   int with_keys = 0;  // sequences
-  auto scan = [&](int chunk, int before, int& inc, int& mine) {  // returns the tiles up to the chunk's end
+  auto units_of = [&](int s, int& tiles, uint32_t& first, uint32_t& end) {
+    tiles = tiles_of<TILE>(a, s, first, end);
+    return tiles ? (tiles + kRowUnits) * rows : 0;
+  };
+  auto scan = [&](int chunk, int before, int& inc, int& mine) {  // returns the units up to the chunk's end
     const int s = chunk * THREADS + tid;
     mine = 0;
     if (s < a.S) {
-      mine = tiles_of<TILE>(a, s, lo, hi) * rows;
+      int tiles;
+      mine = units_of(s, tiles, lo, hi);
       if (blockIdx.x == 0 && (uint32_t)__ldg(a.lens + s) != hi) flag_invalid(a.err);
     }
     inc = mine;
@@ -495,9 +510,9 @@ __global__ void __launch_bounds__(W * 32, CTAS) kv4_attend_kernel(const AttendAr
     for (int i = tid; i < heads * D; i += THREADS) a.out[(int64_t)s * a.ldo + i] = 0;
     for (int i = tid; a.lse && i < heads; i += THREADS) a.lse[(int64_t)s * heads + i] = -INFINITY;
   }
-  // CTA c of G has tiles [c q + min(c, r), ...) with total = G q + r. Rows are not cut
+  // CTA c of G has units [c q + min(c, r), ...) with total = G q + r. Rows are not cut
   // finer than kMinTiles tiles on average: joining parts costs more than a tile
-  const int G = min((int)gridDim.x, max(with_keys * rows, (total + kMinTiles - 1) / kMinTiles));
+  const int G = min((int)gridDim.x, max(with_keys * rows, total / (kMinTiles + kRowUnits)));
   if ((int)blockIdx.x >= G) return;
   const int gq = total / G, gr = total - G * gq;
   const int begin = (int)blockIdx.x * gq + min((int)blockIdx.x, gr);
@@ -510,66 +525,96 @@ __global__ void __launch_bounds__(W * 32, CTAS) kv4_attend_kernel(const AttendAr
     }
   }
   __syncthreads();
-  int seq = s_seq, base = s_base;
-  int n_tiles = tiles_of<TILE>(a, seq, lo, hi);
+
+  // ---- the fetching side: runs up to STAGES - 1 iterations ahead, also into the
+  // next segment. All warps go through the same segments and iterations.
   uint8_t* ring = smem + (size_t)warp * STAGES * L::kBytes;
-
-  for (int pos = begin; pos < end;) {
-    while (pos >= base + n_tiles * rows) {
-      base += n_tiles * rows;
-      n_tiles = tiles_of<TILE>(a, ++seq, lo, hi);
+  int f_seq = s_seq, f_base = s_base, f_tiles, f_unit = begin;
+  int f_units = units_of(f_seq, f_tiles, lo, hi);  // lo, hi: of f_seq from here on
+  int f_segs = 0, f_i = 0, f_iters = 0, f_head = 0, f_stage = 0;
+  uint32_t f_key = 0;  // the warp's first key of the segment
+  int held = -1;       // pages of 16-key runs: lane l has run (l & 1) of iteration (l >> 1) of 16
+  uint32_t ok = 0;     // two bits per iteration in flight, the oldest lowest: runs with a page
+  int lead = 0;        // iterations in flight
+  auto next_segment = [&]() {
+    while (f_unit < end) {
+      while (f_unit >= f_base + f_units) {
+        f_base += f_units;
+        f_units = units_of(++f_seq, f_tiles, lo, hi);
+      }
+      const int per = f_tiles + kRowUnits, row = (f_unit - f_base) / per, row0 = f_base + row * per;
+      const int first = max(0, f_unit - row0 - kRowUnits), stop = min(per, end - row0);
+      const int last = max(0, stop - kRowUnits);
+      f_unit = row0 + stop;
+      if (last == first) continue;  // only the row's own units
+      const int kv = row / a.head_tiles, h0 = (row - kv * a.head_tiles) * NH, nh = min(NH, a.group - h0);
+      f_i = 0, f_iters = last - first, f_head = kv;
+      const uint32_t kw = (lo & ~(uint32_t)(kWarpKeys - 1)) + (uint32_t)first * TILE;
+      f_key = kw + warp * kWarpKeys;
+      const int slot = f_segs & 1;
+      if (lane == 0)
+        s_seg[warp][slot] = {f_seq, kv * a.group + h0, nh, f_iters, kw, lo, hi, first == 0, last == f_tiles,
+                             row0 + per - 1};
+      if (tid < NH * D / 8) {
+        const bool real = tid / (D / 8) < nh;
+        cp_async16(&s_raw[slot][tid],
+                   a.q + (int64_t)f_seq * a.ldq + (int64_t)(kv * a.group + h0) * D + (real ? tid * 8 : 0), real);
+      }
+      ++f_segs;
+      return true;
     }
-    const int row = (pos - base) / n_tiles, first = pos - base - row * n_tiles;
-    const int last = min(n_tiles, first + end - pos);  // tiles [first, last) of the row
-    const int head = row / a.head_tiles, h0 = (row % a.head_tiles) * NH;
-    const int nh = min(NH, a.group - h0);  // real heads of the tile
-
-    // ---- the warp's keys: 32 of each tile, from kw on, TILE apart
-    const int iters = last - first;
-    const uint32_t kw = (lo & ~(uint32_t)(kWarpKeys - 1)) + (uint32_t)first * TILE + warp * kWarpKeys;
-    const int32_t* trow = a.table + (int64_t)seq * a.max_blocks;
-    // pages of the 16-key runs: lane l holds run (l & 1) of iteration i0 + (l >> 1);
-    // -1: no key of the run counts, or its page is invalid
-    int held = -1;
-    auto hold = [&](int i0) {
-      const uint32_t key = kw + (uint32_t)(i0 + (lane >> 1)) * TILE + (lane & 1) * kSub;
-      held = -1;
-      if (i0 + (lane >> 1) < iters && key < hi && key + kSub > lo) {
-        held = __ldg(trow + (key >> a.page_shift));
-        if (held < 0 || held >= a.pages) {
-          held = -1;
-          flag_invalid(a.err);
+    return false;
+  };
+  auto fill = [&](int segs) {  // segs: segments that the computing side has finished
+#pragma unroll 1
+    while (lead < STAGES - 1) {
+      if (f_i == f_iters && (f_segs - segs >= 2 || !next_segment())) break;
+      if ((f_i & 15) == 0) {
+        const uint32_t key = f_key + (uint32_t)(f_i + (lane >> 1)) * TILE + (lane & 1) * kSub;
+        held = -1;
+        if (f_i + (lane >> 1) < f_iters && key < hi && key + kSub > lo) {
+          held = __ldg(a.table + (int64_t)f_seq * a.max_blocks + (key >> a.page_shift));
+          if (held < 0 || held >= a.pages) {
+            held = -1;
+            flag_invalid(a.err);
+          }
         }
       }
-    };
-    uint32_t ok = 0;  // two bits per iteration in flight, the oldest lowest: pages that hold keys
-    auto start = [&](int i, int stage) {
-      if ((i & 15) == 0) hold(i);
       int page[2];
-      page[0] = __shfl_sync(kAll, held, (i & 15) * 2);
-      page[1] = __shfl_sync(kAll, held, (i & 15) * 2 + 1);
-      if (i < iters) fetch<D>(ring + stage * L::kBytes, a, head, kw + (uint32_t)i * TILE, page);
-      ok |= ((page[0] >= 0 ? 1u : 0u) | (page[1] >= 0 ? 2u : 0u)) << (2 * (STAGES - 1));
+      page[0] = __shfl_sync(kAll, held, (f_i & 15) * 2);
+      page[1] = __shfl_sync(kAll, held, (f_i & 15) * 2 + 1);
+      fetch<D>(ring + f_stage * L::kBytes, a, f_head, f_key + (uint32_t)f_i * TILE, page);
       cp_async_commit();
-    };
-#pragma unroll 1
-    for (int i = 0; i < STAGES - 1; ++i) {
-      start(i, i);
-      ok >>= 2;
+      ok |= ((page[0] >= 0 ? 1u : 0u) | (page[1] >= 0 ? 2u : 0u)) << (2 * lead);
+      f_stage = f_stage + 1 == STAGES ? 0 : f_stage + 1;
+      ++lead;
+      ++f_i;
     }
+  };
+  auto await = [&]() {  // the oldest iteration in flight
+    if (lead == STAGES - 1)
+      cp_async_wait<STAGES - 2>();
+    else
+      cp_async_wait<0>();
+    __syncwarp();
+  };
 
+  int stage = 0;
+#pragma unroll 1
+  for (int seg = 0;; ++seg) {
+    fill(seg);
+    if (lead == 0) break;
+    await();
+    const Segment& sg = s_seg[warp][seg & 1];
     // ---- queries: f16 times a power of two per head, the scale's sign among it
+    __syncthreads();  // every thread's piece of the queries is here, and s_q is free
     for (int n = warp; n < NT; n += W) {
-      const bool real = n * 8 + g < nh;
-      const uint16_t* qp = a.q + (int64_t)seq * a.ldq + ((int64_t)head * a.group + h0 + (real ? n * 8 + g : 0)) * D;
       float m = 0.0f;
-      uint4 raw[NB];
-#pragma unroll
-      for (int b = 0; b < NB; ++b) raw[b] = real ? ld_cached16(qp + 32 * b + 8 * t) : make_uint4(0, 0, 0, 0);
+      const uint4* raw = s_raw[seg & 1] + (n * 8 + g) * (D / 8) + t;
 #pragma unroll
       for (int b = 0; b < NB; ++b) {
         float f[8];
-        unpack8<BF16>(raw[b], f);
+        unpack8<BF16>(raw[4 * b], f);
 #pragma unroll
         for (int k = 0; k < 8; ++k)
           if (fabsf(f[k]) < INFINITY) m = fmaxf(m, fabsf(f[k]));
@@ -581,7 +626,7 @@ __global__ void __launch_bounds__(W * 32, CTAS) kv4_attend_kernel(const AttendAr
 #pragma unroll
       for (int b = 0; b < NB; ++b) {
         float f[8];
-        unpack8<BF16>(raw[b], f);
+        unpack8<BF16>(raw[4 * b], f);
         s_q[(n * NB + b) * 32 + lane] =
             make_uint4(pack2<false>(f[0] * up, f[1] * up), pack2<false>(f[2] * up, f[3] * up),
                        pack2<false>(f[4] * up, f[5] * up), pack2<false>(f[6] * up, f[7] * up));
@@ -596,31 +641,43 @@ __global__ void __launch_bounds__(W * 32, CTAS) kv4_attend_kernel(const AttendAr
       qs[n][0] = s_qs[n * 8 + 2 * t];
       qs[n][1] = s_qs[n * 8 + 2 * t + 1];
     }
-
     State<D, NT> st;
     clear(st);
+
+    const int iters = sg.iters;
 #pragma unroll 1
-    for (int i = 0, stage = 0; i < iters; ++i, stage = stage + 1 == STAGES ? 0 : stage + 1) {
-      cp_async_wait<STAGES - 2>();
-      __syncwarp();
-      start(i + STAGES - 1, stage == 0 ? STAGES - 1 : stage - 1);
-      const uint32_t kb = kw + (uint32_t)i * TILE;
+    for (int i = 0; i < iters; ++i) {
+      if (i > 0) {
+        stage = stage + 1 == STAGES ? 0 : stage + 1;
+        fill(seg);
+        await();
+      }
+      const uint32_t kb = sg.kw + (uint32_t)i * TILE + warp * kWarpKeys;
       uint32_t on = ((ok & 1u) ? 0x0000FFFFu : 0u) | ((ok & 2u) ? 0xFFFF0000u : 0u);
       ok >>= 2;
+      --lead;
       if (on) {
-        if (kb < lo) on &= kAll << (lo - kb);       // lo - kb < 32: the run counts
-        if (kb + kWarpKeys > hi) on &= kAll >> (kb + kWarpKeys - hi);
+        if (kb < sg.lo) on &= kAll << (sg.lo - kb);  // less than 32: a run counts
+        if (kb + kWarpKeys > sg.hi) on &= kAll >> (kb + kWarpKeys - sg.hi);
         attend_keys<D, NT>(ring + stage * L::kBytes, reinterpret_cast<const uint8_t*>(s_q), qs, on, st);
       }
       __syncwarp();
     }
-    cp_async_wait<0>();
 
-    // ---- join the warps
-    __syncthreads();  // every ring is idle: its memory holds the sums now
-    float* sums = reinterpret_cast<float*>(smem);  // [warp][NH][D]
+    // ---- join the warps: 8 heads at a time through the stages just used
+    const bool whole = sg.begins && sg.ends;
+    // a row that goes on in another CTA's share: its first part goes to slot 1, the others to slot 0
+    float* part = a.parts + ((size_t)blockIdx.x * 2 + (sg.begins ? 1 : 0)) * kPart;
+    if (sg.begins && !whole && tid == 0) {
+      const int u = sg.last_unit;  // the CTA that has it
+      const int c1 = u < gr * (gq + 1) ? u / (gq + 1) : gr + (u - gr * (gq + 1)) / gq;
+      a.split[blockIdx.x] = {c1 - (int)blockIdx.x + 1, sg.seq, sg.head, sg.nh};
+    }
+    uint16_t* orow = a.out + (int64_t)sg.seq * a.ldo + (int64_t)sg.head * D;
+    float* lrow = a.lse ? a.lse + (int64_t)sg.seq * a.heads * a.group + sg.head : nullptr;
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
+      float* mine_sums = reinterpret_cast<float*>(ring + stage * L::kBytes);  // [8][D]
       const float l0 = over_g_sum(st.l[n][0]), l1 = over_g_sum(st.l[n][1]);
       if (g == 0) {
 #pragma unroll
@@ -635,69 +692,48 @@ __global__ void __launch_bounds__(W * 32, CTAS) kv4_attend_kernel(const AttendAr
         const float f = e8m0_to_f32((st.top[b / 2] >> (16 * (b & 1))) & 255u) * 0.001953125f;
 #pragma unroll
         for (int c = 0; c < 2; ++c)
-          *reinterpret_cast<float4*>(sums + (size_t)(warp * NH + n * 8 + 2 * t + c) * D + 32 * b + 4 * g) =
+          *reinterpret_cast<float4*>(mine_sums + (2 * t + c) * D + 32 * b + 4 * g) =
               make_float4(st.acc[n][2 * b][c] * f, st.acc[n][2 * b][2 + c] * f,
                           st.acc[n][2 * b + 1][c] * f, st.acc[n][2 * b + 1][2 + c] * f);
       }
-    }
-    __syncthreads();
-    if (tid < NH) {
-      float m = s_m[0][tid];
+      __syncthreads();
+      for (int i = tid * 4; i < 8 * D; i += THREADS * 4) {
+        const int h = n * 8 + i / D;
+        if (h >= sg.nh) break;
+        float m = s_m[0][h];
 #pragma unroll
-      for (int w = 1; w < W; ++w) m = fmaxf(m, s_m[w][tid]);
-      const float b = m == -INFINITY ? 0.0f : m;
-      float l = 0.0f;
+        for (int w = 1; w < W; ++w) m = fmaxf(m, s_m[w][h]);
+        const float b = m == -INFINITY ? 0.0f : m;
+        float l = 0.0f;
+        float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll
-      for (int w = 0; w < W; ++w) {
-        const float f = exp2_fast(s_m[w][tid] - b);
-        s_w[w][tid] = f;
-        l = fmaf(s_l[w][tid], f, l);
+        for (int w = 0; w < W; ++w) {
+          const float4 o = *reinterpret_cast<const float4*>(smem + (size_t)(w * STAGES + stage) * L::kBytes + i * 4);
+          const float f = exp2_fast(s_m[w][h] - b);
+          l = fmaf(s_l[w][h], f, l);
+          v.x = fmaf(o.x, f, v.x);
+          v.y = fmaf(o.y, f, v.y);
+          v.z = fmaf(o.z, f, v.z);
+          v.w = fmaf(o.w, f, v.w);
+        }
+        if (whole) {
+          const float inv = 1.0f / l;
+          *reinterpret_cast<uint2*>(orow + n * 8 * D + i) =
+              make_uint2(pack2<BF16>(v.x * inv, v.y * inv), pack2<BF16>(v.z * inv, v.w * inv));
+          if (lrow && i % D == 0) lrow[h] = (b + log2f(l) - kLift) * 0.6931471805599453f;
+        } else {
+          *reinterpret_cast<float4*>(part + n * 8 * D + i) = v;
+          if (i % D == 0) {
+            part[NH * D + h] = m;
+            part[NH * D + NH + h] = l;
+          }
+        }
       }
-      s_max[tid] = m;
-      s_sum[tid] = l;
+      __syncthreads();  // the stages are free again
     }
-    __syncthreads();
-    const bool whole = first == 0 && last == n_tiles;
-    // a row that ends in another CTA's share: its first part goes to slot 1, the others to slot 0
-    float* part = a.parts + ((size_t)blockIdx.x * 2 + (first == 0 ? 1 : 0)) * kPart;
-    if (first == 0 && !whole && tid == 0) {
-      const int t1 = base + row * n_tiles + n_tiles - 1;  // the row's last tile, and the CTA that has it
-      const int c1 = t1 < gr * (gq + 1) ? t1 / (gq + 1) : gr + (t1 - gr * (gq + 1)) / gq;
-      a.split[blockIdx.x] = {c1 - (int)blockIdx.x + 1, seq, head * a.group + h0, nh};
-    }
-    const int heads = a.heads * a.group;
-    uint16_t* orow = a.out + (int64_t)seq * a.ldo + ((int64_t)head * a.group + h0) * D;
-    float* lrow = a.lse ? a.lse + (int64_t)seq * heads + head * a.group + h0 : nullptr;
-    for (int i = tid * 4; i < nh * D; i += THREADS * 4) {
-      const int h = i / D;
-      float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll
-      for (int w = 0; w < W; ++w) {
-        const float4 o = *reinterpret_cast<const float4*>(sums + (size_t)w * NH * D + i);
-        const float f = s_w[w][h];
-        v.x = fmaf(o.x, f, v.x);
-        v.y = fmaf(o.y, f, v.y);
-        v.z = fmaf(o.z, f, v.z);
-        v.w = fmaf(o.w, f, v.w);
-      }
-      if (whole) {
-        const float inv = 1.0f / s_sum[h];
-        *reinterpret_cast<uint2*>(orow + i) = make_uint2(pack2<BF16>(v.x * inv, v.y * inv), pack2<BF16>(v.z * inv, v.w * inv));
-      } else {
-        *reinterpret_cast<float4*>(part + i) = v;
-      }
-    }
-    if (tid < nh) {
-      if (whole) {
-        if (lrow) lrow[tid] = (s_max[tid] + log2f(s_sum[tid]) - kLift) * 0.6931471805599453f;
-      } else {
-        part[NH * D + tid] = s_max[tid];
-        part[NH * D + NH + tid] = s_sum[tid];
-      }
-    }
-    __syncthreads();  // the sums and the ring share their memory
-    pos += last - first;
+    stage = stage + 1 == STAGES ? 0 : stage + 1;
   }
+  cp_async_wait<0>();
 }
 
 // Joins the parts of the rows that several CTAs share: a CTA per (first CTA of a
@@ -780,19 +816,17 @@ moe_status launch(const AttendArgs& a, bool bf16, cudaStream_t st) {
   static_assert(CTAS <= kMaxCtasPerSm, "the workspace has room for 2 CTAs per SM");
   auto k = bf16 ? kv4_attend_kernel<D, NT, W, STAGES, CTAS, true> : kv4_attend_kernel<D, NT, W, STAGES, CTAS, false>;
   const size_t ring = (size_t)W * STAGES * Stage<D>::kBytes;
-  const size_t sums = (size_t)W * NT * 8 * D * 4;
-  const size_t smem = ring > sums ? ring : sums;
-  moe_status rc = allow_smem(k, smem);
+  moe_status rc = allow_smem(k, ring);
   if (rc != MOE_OK) return rc;
   // no more CTAs than tiles that the rows' capacity allows
   const int64_t keys = (int64_t)a.max_blocks << a.page_shift;
   const int64_t most = a.window > 0 && a.window + 2 * kWarpKeys < keys ? a.window + 2 * kWarpKeys : keys;
   const int64_t row_tiles = (most + W * kWarpKeys - 1) / (W * kWarpKeys);
   const int64_t tiles = row_tiles * a.S * a.heads * a.head_tiles;
-  if (tiles > 0x7FFFFFFF) return refuse(MOE_ERR_SHAPE, "wd_kv4_attend: block_table's capacity is too large");
+  if ((row_tiles + kRowUnits) * a.S * a.heads * a.head_tiles > 0x7FFFFFFF) return refuse(MOE_ERR_SHAPE, "wd_kv4_attend: block_table's capacity is too large");
   const int64_t fill = (int64_t)sm_count() * CTAS;
   const unsigned grid = (unsigned)(tiles < fill ? tiles : fill);
-  k<<<grid, W * 32, smem, st>>>(a);
+  k<<<grid, W * 32, ring, st>>>(a);
   rc = launched("wd_kv4_attend launch");
   if (rc != MOE_OK || row_tiles == 1) return rc;  // a row of one tile is never split
   cudaLaunchAttribute dependent = {};
