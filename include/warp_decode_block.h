@@ -43,7 +43,7 @@ typedef struct {
  *   codes  [N/16][K/128][16 rows][4 t][4 blocks][4 bytes]: byte j of (t, b) holds
  *          elements 32b + 8t + 2j (low nibble) and 32b + 8t + 2j + 1 (high) of
  *          the column tile;
- *   scales [N/16][K/128][16 rows][4 blocks].
+ *   scales [N/16][K/128][8 g][2 h][4 blocks]: of row g + 8h of the tile.
  * Both 32-byte aligned. */
 enum { WD_FP4_CODES = 0, WD_FP4_SCALES = 1 };
 

@@ -33,7 +33,7 @@ __device__ __forceinline__ WordAt word_at(int64_t i, int N, int K) {
   const size_t tile = (size_t)(w.row / kTileRows) * col_tiles(K) + w.k / kTileCols;
   const int r = (int)(w.row % kTileRows), b = (w.k % kTileCols) / 32, t = (w.k % 32) / 8;
   w.code = tile * kTileCodes + r * 64 + t * 16 + b * 4;
-  w.scale = tile * kTileScales + r * 4 + b;
+  w.scale = tile * kTileScales + (r % 8) * 8 + (r / 8) * 4 + b;
   return w;
 }
 
@@ -79,118 +79,227 @@ __global__ void __launch_bounds__(kThreads)
 }
 
 // ----------------------------------------------------------------- matvec --
-// One CTA per row tile of 16 and per NT * 8 tokens; its 8 warps share the
-// columns out tile by tile and add their sums through shared memory.
+// A CTA of 16 warps per SM takes a contiguous run of row tiles; their (row tile,
+// column tile) pairs, which lie one after another in memory, are shared out evenly
+// among its warps, so each warp streams one dense run of codes through registers.
 //   mma.sync m16n8k16, f16 x f16 -> FP32: rows are output rows, columns are
 //   tokens. A block's 32 products are summed by two MMAs, times its scale
 //   added to the FP32 accumulator.
-// x is staged in shared memory as f16 times a power of two per token (the
-// largest finite magnitude of the staged columns in [2^14, 2^15)).
+// x is staged once per CTA in shared memory, as f16 times a power of two per
+// token (the largest finite magnitude in [2^14, 2^15)) and in the order of the B
+// fragment: [column tile][block][lane][16 bytes]. Row tiles that warps share are
+// joined in shared memory in column order, so results do not depend on timing.
 
-constexpr int kStageCols = 4096;  // columns of x staged at a time
-constexpr int kStageRow = 2 * kStageCols + 64;  // bytes; 16 banks apart: conflict-free reads
+constexpr int kMvWarps = 16, kMvThreads = kMvWarps * 32;
+constexpr int kAhead = 4;  // column tiles in flight per warp
+// Static and dynamic shared memory count together against the default limit: this
+// much is asked for beside the dynamic part.
+constexpr size_t kStaticSmem = 512;
 
+struct MvArgs {
+  const uint8_t *codes, *scales;
+  const uint16_t* x;
+  void* y;
+  int64_t ldx, ldy;
+  int32_t B, y_type, N, K;
+  int32_t tok0;   // first token of this launch
+  int32_t chunk;  // column tiles of x staged at a time; all of them where that fits
+  int32_t batch;  // row tiles of a CTA whose sums wait in shared memory for the other chunks
+};
+
+// The power of two that brings magnitude bits m into [2^14, 2^15), as pow2_shift_for
+// for finite m (a subnormal m counts as the smallest normal).
+__device__ __forceinline__ int shift_of_bits(uint32_t m) {
+  return m == 0 ? 0 : min(126, max(-126, 141 - (int)(m >> 23)));
+}
+
+// Stage `toks` tokens' columns [128 c0, 128 c1) (zero from K on) as f16 fragments;
+// s_max[n] becomes the bits of the token's largest finite magnitude. All threads of
+// the CTA; ends behind a barrier.
 template <int NT, bool BF16>
-__global__ void __launch_bounds__(kThreads)
-    fp4_matvec_kernel(const uint8_t* __restrict__ codes, const uint8_t* __restrict__ scales,
-                      const uint16_t* __restrict__ x, int64_t ldx, int B, void* __restrict__ y,
-                      int32_t y_type, int64_t ldy, int N, int K) {
-  extern __shared__ uint4 dyn4[];
-  uint8_t* xs = reinterpret_cast<uint8_t*>(dyn4);
-  __shared__ float s_back[NT * 8];
-  __shared__ float s_sum[kWarpsPerCta][kTileRows][NT * 8];
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
-  const int64_t tile_row = blockIdx.x;
-  const int tok0 = blockIdx.y * NT * 8;
-  const int ct = col_tiles(K);
-  const uint8_t* crow = codes + (size_t)tile_row * ct * kTileCodes;
-  const uint8_t* srow = scales + (size_t)tile_row * ct * kTileScales;
-
-  float total[NT][4] = {};
-  for (int c0 = 0; c0 < ct; c0 += kStageCols / kTileCols) {
-    const int c1 = min(ct, c0 + kStageCols / kTileCols);
-    __syncthreads();
-    for (int r = warp; r < NT * 8; r += kWarpsPerCta) {  // a warp stages whole tokens
-      const int k0 = c0 * kTileCols, k1 = min(K, c1 * kTileCols), kp = c1 * kTileCols;
-      const bool real = tok0 + r < B;
-      const uint16_t* row = x + (real ? (int64_t)(tok0 + r) * ldx : 0);
-      float m = 0.0f;
-      for (int k = k0 + lane * 8; real && k < k1; k += 256) {
-        float f[8];
-        unpack8<BF16>(ld_cached16(row + k), f);
+__device__ __forceinline__ void stage_x(const MvArgs& a, int c0, int c1, int toks, uint4* xs,
+                                        uint32_t* s_max) {
+  const int k0 = c0 * kTileCols, per = (c1 - c0) * (kTileCols / 8);  // pieces of 8 elements per token
+  const int pieces = toks * per, real = (min(a.K, c1 * kTileCols) - k0) / 8;
+  const uint16_t* x = a.x + (int64_t)a.tok0 * a.ldx + k0;
+  auto load = [&](int tok, int piece) {
+    return piece < real ? ld_cached16(x + (int64_t)tok * a.ldx + piece * 8) : make_uint4(0, 0, 0, 0);
+  };
+  if (threadIdx.x < NT * 8) s_max[threadIdx.x] = 0;
+  constexpr int kHold = 4;  // pieces per thread that stay in registers between the two passes
+  uint4 held[kHold];
 #pragma unroll
-        for (int j = 0; j < 8; ++j)
-          if (fabsf(f[j]) < INFINITY) m = fmaxf(m, fabsf(f[j]));
-      }
-      m = warp_max(m);
-      const int sigma = pow2_shift_for(m);
-      const float up = exp2i(sigma);
-      for (int k = k0 + lane * 8; k < kp; k += 256) {
-        float f[8] = {};
-        if (real && k < k1) unpack8<BF16>(ld_cached16(row + k), f);
-        uint4 o;
-        o.x = pack2<false>(f[0] * up, f[1] * up);
-        o.y = pack2<false>(f[2] * up, f[3] * up);
-        o.z = pack2<false>(f[4] * up, f[5] * up);
-        o.w = pack2<false>(f[6] * up, f[7] * up);
-        *reinterpret_cast<uint4*>(xs + (size_t)r * kStageRow + (k - k0) * 2) = o;
-      }
-      if (lane == 0) s_back[r] = exp2i(-sigma);
-    }
-    __syncthreads();
-    float acc[NT][4] = {};
-    for (int c = c0 + warp; c < c1; c += kWarpsPerCta) {
-      const uint4 lo = ld_cached16(crow + (size_t)c * kTileCodes + g * 64 + t * 16);
-      const uint4 hi = ld_cached16(crow + (size_t)c * kTileCodes + (g + 8) * 64 + t * 16);
-      const uint32_t wl[4] = {lo.x, lo.y, lo.z, lo.w}, wh[4] = {hi.x, hi.y, hi.z, hi.w};
-      float sl[4], sh[4];
-      e8m0x4_to_f32(__ldg(reinterpret_cast<const uint32_t*>(srow + (size_t)c * kTileScales) + g), sl);
-      e8m0x4_to_f32(__ldg(reinterpret_cast<const uint32_t*>(srow + (size_t)c * kTileScales) + g + 8), sh);
-#pragma unroll
-      for (int b = 0; b < 4; ++b) {
-        uint32_t al[4], ah[4];
-        e2m1x8_to_f16(wl[b], al);
-        e2m1x8_to_f16(wh[b], ah);
-        const uint32_t a0[4] = {al[0], ah[0], al[1], ah[1]}, a1[4] = {al[2], ah[2], al[3], ah[3]};
-#pragma unroll
-        for (int n = 0; n < NT; ++n) {
-          const uint4 v = *reinterpret_cast<const uint4*>(
-              xs + (size_t)(n * 8 + g) * kStageRow + ((c - c0) * kTileCols + 32 * b + 8 * t) * 2);
-          const float zero[4] = {};
-          float d[4];
-          mma_16816(d, a0, v.x, v.y, zero);
-          mma_16816(d, a1, v.z, v.w, d);
-          acc[n][0] = fmaf(sl[b], d[0], acc[n][0]);
-          acc[n][1] = fmaf(sl[b], d[1], acc[n][1]);
-          acc[n][2] = fmaf(sh[b], d[2], acc[n][2]);
-          acc[n][3] = fmaf(sh[b], d[3], acc[n][3]);
-        }
-      }
-    }
-#pragma unroll
-    for (int n = 0; n < NT; ++n) {
-      const float b0 = s_back[n * 8 + 2 * t], b1 = s_back[n * 8 + 2 * t + 1];
-      total[n][0] = fmaf(acc[n][0], b0, total[n][0]);
-      total[n][1] = fmaf(acc[n][1], b1, total[n][1]);
-      total[n][2] = fmaf(acc[n][2], b0, total[n][2]);
-      total[n][3] = fmaf(acc[n][3], b1, total[n][3]);
-    }
-  }
-#pragma unroll
-  for (int n = 0; n < NT; ++n) {
-    s_sum[warp][g][n * 8 + 2 * t] = total[n][0];
-    s_sum[warp][g][n * 8 + 2 * t + 1] = total[n][1];
-    s_sum[warp][g + 8][n * 8 + 2 * t] = total[n][2];
-    s_sum[warp][g + 8][n * 8 + 2 * t + 1] = total[n][3];
+  for (int i = 0; i < kHold; ++i) {
+    const int p = threadIdx.x + i * kMvThreads;
+    if (p < pieces) held[i] = load(p / per, p % per);
   }
   __syncthreads();
-  for (int i = tid; i < kTileRows * NT * 8; i += kThreads) {
-    const int r = i % kTileRows, n = i / kTileRows;
-    float s = s_sum[0][r][n];
+  auto largest = [&](int p, const uint4& v) {  // called by whole warps
+    int tok = -1;
+    uint32_t m = 0;
+    if (p < pieces) {
+      tok = p / per;
+      float f[8];
+      unpack8<BF16>(v, f);
 #pragma unroll
-    for (int w = 1; w < kWarpsPerCta; ++w) s += s_sum[w][r][n];
-    const int64_t row = tile_row * kTileRows + r;
-    if (row < N && tok0 + n < B) store_elem(y, y_type, (int64_t)(tok0 + n) * ldy + row, s);
+      for (int j = 0; j < 8; ++j) {
+        const uint32_t b = __float_as_uint(fabsf(f[j]));
+        if (b < 0x7F800000u) m = max(m, b);
+      }
+    }
+    // magnitudes are ordered as integers; one atomic per warp where it holds one token
+    if (__all_sync(0xFFFFFFFFu, tok == __shfl_sync(0xFFFFFFFFu, tok, 0))) {
+      m = __reduce_max_sync(0xFFFFFFFFu, m);
+      if ((threadIdx.x & 31) == 0 && tok >= 0) atomicMax(s_max + tok, m);
+    } else if (tok >= 0) {
+      atomicMax(s_max + tok, m);
+    }
+  };
+  auto store = [&](int p, const uint4& v) {
+    const int tok = p / per, piece = p - tok * per;
+    const float up = exp2i(shift_of_bits(s_max[tok]));
+    float f[8];
+    unpack8<BF16>(v, f);
+    xs[((piece / 4) * NT + (tok >> 3)) * 32 + (tok & 7) * 4 + piece % 4] =
+        make_uint4(pack2<false>(f[0] * up, f[1] * up), pack2<false>(f[2] * up, f[3] * up),
+                   pack2<false>(f[4] * up, f[5] * up), pack2<false>(f[6] * up, f[7] * up));
+  };
+#pragma unroll
+  for (int i = 0; i < kHold; ++i)
+    if (i * kMvThreads < pieces) largest(threadIdx.x + i * kMvThreads, held[i]);
+  for (int p0 = kHold * kMvThreads; p0 < pieces; p0 += kMvThreads) {
+    const int p = p0 + threadIdx.x;
+    largest(p, p < pieces ? load(p / per, p % per) : make_uint4(0, 0, 0, 0));
+  }
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < kHold; ++i)
+    if (threadIdx.x + i * kMvThreads < pieces) store(threadIdx.x + i * kMvThreads, held[i]);
+  for (int p = threadIdx.x + kHold * kMvThreads; p < pieces; p += kMvThreads) store(p, load(p / per, p % per));
+  __syncthreads();
+}
+
+template <int NT, bool BF16>
+__global__ void __launch_bounds__(kMvThreads, 1) fp4_matvec_kernel(const MvArgs a) {
+  extern __shared__ uint4 dyn4[];
+  __shared__ uint32_t s_max[NT * 8];
+  constexpr int kSums = kTileRows * NT * 8;  // of a row tile: [token][row]
+  // parts of row tiles that warps share: [warp][0: begun before, 1: begun here]
+  float(*s_part)[2][kSums] = reinterpret_cast<float(*)[2][kSums]>(dyn4);
+  float(*s_sum)[kSums] = reinterpret_cast<float(*)[kSums]>(dyn4 + kMvWarps * 2 * kSums / 4);  // [batch]
+  const int ct = col_tiles(a.K);
+  const bool chunked = a.chunk < ct;
+  float(*s_held)[kSums] = s_sum + a.batch;  // sums of the chunks before, where there are any
+  uint4* xs = dyn4 + (kMvWarps * 2 + a.batch * (chunked ? 2 : 1)) * (kSums / 4);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
+  const int toks = min(NT * 8, a.B - a.tok0);
+  const int64_t tiles = row_tiles(a.N);
+  const int64_t r0 = tiles * blockIdx.x / gridDim.x, r1 = tiles * (blockIdx.x + 1) / gridDim.x;
+
+  struct Tile {
+    uint4 lo, hi;
+    uint2 sc;
+  };
+  bool staged = false;
+  for (int64_t q0 = r0; q0 < r1; q0 += a.batch) {
+    const int nq = (int)min((int64_t)a.batch, r1 - q0);
+    for (int c0 = 0; c0 < ct; c0 += a.chunk) {
+      const int kt = min(a.chunk, ct - c0), units = nq * kt;
+      const int u0 = units * warp / kMvWarps, u1 = units * (warp + 1) / kMvWarps;
+      Tile buf[kAhead];
+      int lr = u0 / kt, lk = u0 - lr * kt;  // of the next tile to load
+      auto load = [&](Tile& b) {
+        const size_t at = (size_t)(q0 + lr) * ct + c0 + lk;
+        const uint8_t* p = a.codes + at * kTileCodes + lane * 16;
+        b.lo = ld_codes16(p);
+        b.hi = ld_codes16(p + 512);
+        b.sc = ld_scales8(a.scales + at * kTileScales + g * 8);
+        if (++lk == kt) {
+          lk = 0;
+          ++lr;
+        }
+      };
+#pragma unroll
+      for (int i = 0; i < kAhead; ++i)
+        if (u0 + i < u1) load(buf[i]);
+      if (!staged) stage_x<NT, BF16>(a, c0, c0 + kt, toks, xs, s_max);
+      staged = !chunked;
+
+      float acc[NT][4] = {};
+      int r = u0 / kt, k = u0 - r * kt, begun = k;  // the tile at hand; its first column tile here
+      auto finish = [&](float* to) {
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            to[(n * 8 + 2 * t + (c & 1)) * kTileRows + g + 8 * (c >> 1)] = acc[n][c];
+            acc[n][c] = 0.0f;
+          }
+      };
+      for (int u = u0; u < u1; u += kAhead) {
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i) {
+          if (u + i >= u1) break;
+          const Tile b = buf[i];
+          if (u + i + kAhead < u1) load(buf[i]);
+          const uint32_t wl[4] = {b.lo.x, b.lo.y, b.lo.z, b.lo.w}, wh[4] = {b.hi.x, b.hi.y, b.hi.z, b.hi.w};
+          float sl[4], sh[4];
+          e8m0x4_to_f32(b.sc.x, sl);
+          e8m0x4_to_f32(b.sc.y, sh);
+          const uint4* xk = xs + (size_t)k * 4 * NT * 32 + lane;
+#pragma unroll
+          for (int blk = 0; blk < 4; ++blk) {
+            uint32_t al[4], ah[4];
+            e2m1x8_to_f16(wl[blk], al);
+            e2m1x8_to_f16(wh[blk], ah);
+            const uint32_t a0[4] = {al[0], ah[0], al[1], ah[1]}, a1[4] = {al[2], ah[2], al[3], ah[3]};
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+              // columns without a token hold whatever is there: they reach no other column
+              const uint4 v = xk[(blk * NT + n) * 32];
+              float d[4];
+              mma_new(d, a0, v.x, v.y);
+              mma_add(d, a1, v.z, v.w);
+              acc[n][0] = fmaf(sl[blk], d[0], acc[n][0]);
+              acc[n][1] = fmaf(sl[blk], d[1], acc[n][1]);
+              acc[n][2] = fmaf(sh[blk], d[2], acc[n][2]);
+              acc[n][3] = fmaf(sh[blk], d[3], acc[n][3]);
+            }
+          }
+          if (++k == kt) {
+            finish(begun == 0 ? s_sum[r] : s_part[warp][0]);
+            k = begun = 0;
+            ++r;
+          }
+        }
+      }
+      if (u0 < u1 && k > 0) finish(s_part[warp][begun == 0 ? 1 : 0]);
+      __syncthreads();
+      const bool last = c0 + kt >= ct;
+      for (int i = tid; i < nq * kSums; i += kMvThreads) {
+        const int q = i / kSums, o = i % kSums, tok = o / kTileRows;
+        const float back = exp2i(-shift_of_bits(s_max[tok]));
+        // the warps that have the tile's first and last column tile
+        const int w0 = ((q * kt + 1) * kMvWarps - 1) / units, w1 = ((q + 1) * kt * kMvWarps - 1) / units;
+        float v = 0.0f;
+        if (w0 == w1) {
+          v = s_sum[q][o];
+        } else {
+          v = s_part[w0][1][o];
+          for (int w = w0 + 1; w <= w1; ++w)
+            if (units * w / kMvWarps < units * (w + 1) / kMvWarps) v += s_part[w][0][o];
+        }
+        v *= back;
+        if (c0 > 0) v += s_held[q][o];
+        if (!last) {
+          s_held[q][o] = v;
+        } else {
+          const int64_t n = (q0 + q) * kTileRows + o % kTileRows;
+          if (n < a.N && tok < toks) store_elem(a.y, a.y_type, (int64_t)(a.tok0 + tok) * a.ldy + n, v);
+        }
+      }
+      __syncthreads();  // the sums, and x where it comes in chunks, are written again
+    }
   }
 }
 
@@ -208,16 +317,35 @@ int64_t padded_words(const wd_fp4_shape* s) {
 }
 
 template <int NT, bool BF16>
-moe_status launch_matvec(const wd_fp4_shape* s, const uint8_t* pc, const uint8_t* ps,
-                         const uint16_t* x, int64_t ldx, int B, void* y, int32_t y_type,
-                         int64_t ldy, cudaStream_t st) {
+moe_status launch_matvec(MvArgs a, cudaStream_t st) {
   auto k = fp4_matvec_kernel<NT, BF16>;
-  const size_t smem = (size_t)NT * 8 * kStageRow;
-  moe_status rc = allow_smem(k, smem);
+  constexpr size_t kTileX = (size_t)4 * NT * 32 * 16;  // x of a column tile
+  constexpr size_t kTileSum = (size_t)kTileRows * NT * 8 * 4;
+  constexpr size_t kRoom = kMaxDynSmem - kStaticSmem - kMvWarps * 2 * kTileSum;
+  const int ct = col_tiles(a.K);
+  const int64_t tiles = row_tiles(a.N);
+  const int sms = sm_count();
+  const unsigned grid = (unsigned)(tiles < sms ? tiles : sms);
+  const int64_t per = (tiles + grid - 1) / grid;
+  size_t smem;
+  if (ct * kTileX + 8 * kTileSum <= kRoom) {  // all of x, and the sums of as many row tiles as fit
+    const int64_t fit = (int64_t)((kRoom - ct * kTileX) / kTileSum);
+    a.chunk = ct;
+    a.batch = (int)(per < fit ? per : fit);
+    smem = ct * kTileX + a.batch * kTileSum;
+  } else {  // columns in chunks of 128 KB of x
+    a.chunk = 64 / NT;
+    a.batch = (int)(per < 32 ? per : 32);
+    smem = a.chunk * kTileX + 2 * a.batch * kTileSum;
+  }
+  smem += kMvWarps * 2 * kTileSum;
+  moe_status rc = allow_smem(k, smem + kStaticSmem);
   if (rc != MOE_OK) return rc;
-  const dim3 grid((unsigned)row_tiles(s->N), (unsigned)((B + NT * 8 - 1) / (NT * 8)));
-  k<<<grid, kThreads, smem, st>>>(pc, ps, x, ldx, B, y, y_type, ldy, s->N, s->K);
-  return launched("wd_fp4_matvec launch");
+  for (a.tok0 = 0; a.tok0 < a.B; a.tok0 += NT * 8) {
+    k<<<grid, kMvThreads, smem, st>>>(a);
+    if ((rc = launched("wd_fp4_matvec launch")) != MOE_OK) return rc;
+  }
+  return MOE_OK;
 }
 
 }  // namespace
@@ -269,16 +397,12 @@ extern "C" moe_status wd_fp4_matvec(const wd_fp4_shape* s, const uint8_t* pc, co
   if (!x || !y) return refuse(MOE_ERR_NULL, "wd_fp4_matvec: x and y are required");
   if (!half_type(x_type) || !valid_type(y_type))
     return refuse(MOE_ERR_UNSUPPORTED, "wd_fp4_matvec: x is BF16 or F16, y is F32, BF16 or F16");
-  if (ldx < s->K || ldy < s->N || (B + 7) / 8 > 65535)
-    return refuse(MOE_ERR_SHAPE, "wd_fp4_matvec: ldx or ldy is shorter than a row, or B is too large");
+  if (ldx < s->K || ldy < s->N)
+    return refuse(MOE_ERR_SHAPE, "wd_fp4_matvec: ldx or ldy is shorter than a row");
   if (!aligned(x, 16) || ldx % 8 || !aligned(y, type_bytes(y_type)))
     return refuse(MOE_ERR_ALIGN, "wd_fp4_matvec: x needs 16 bytes and ldx % 8 == 0, y its type's size");
-  const uint16_t* x16 = static_cast<const uint16_t*>(x);
+  const MvArgs a = {pc, ps, static_cast<const uint16_t*>(x), y, ldx, ldy, B, y_type, s->N, s->K, 0, 0, 0};
   cudaStream_t st = (cudaStream_t)stream;
-  const bool bf16 = x_type == WD_BF16;
-  if (B <= 8)
-    return bf16 ? launch_matvec<1, true>(s, pc, ps, x16, ldx, B, y, y_type, ldy, st)
-                : launch_matvec<1, false>(s, pc, ps, x16, ldx, B, y, y_type, ldy, st);
-  return bf16 ? launch_matvec<2, true>(s, pc, ps, x16, ldx, B, y, y_type, ldy, st)
-              : launch_matvec<2, false>(s, pc, ps, x16, ldx, B, y, y_type, ldy, st);
+  if (x_type == WD_BF16) return B <= 8 ? launch_matvec<1, true>(a, st) : launch_matvec<2, true>(a, st);
+  return B <= 8 ? launch_matvec<1, false>(a, st) : launch_matvec<2, false>(a, st);
 }

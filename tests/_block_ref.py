@@ -44,12 +44,12 @@ def pack_rows(codes, scales):
     N, K = codes.shape
     rt, ct = -(-N // 16), -(-K // 128)
     pc = np.zeros((rt, ct, 16, 4, 4, 4), np.uint8)
-    ps = np.zeros((rt, ct, 16, 4), np.uint8)
+    ps = np.zeros((rt, ct, 8, 2, 4), np.uint8)
     n, k = np.meshgrid(np.arange(N), np.arange(K), indexing="ij")
     at = (n // 16, k // 128, n % 16, k % 32 // 8, k % 128 // 32, k % 8 // 2)
     np.add.at(pc, at, codes << (4 * (k % 2)).astype(np.uint8))
     n, b = np.meshgrid(np.arange(N), np.arange(K // 32), indexing="ij")
-    ps[n // 16, b // 4, n % 16, b % 4] = scales
+    ps[n // 16, b // 4, n % 8, n % 16 // 8, b % 4] = scales
     return pc.reshape(-1), ps.reshape(-1)
 
 

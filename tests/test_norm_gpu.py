@@ -59,7 +59,8 @@ def test_widths_and_gates(T, H, gate_kind):
 @pytest.mark.parametrize("yk", ["f32", "bf16", "f16"])
 @pytest.mark.parametrize("rk", ["f32", "bf16", "f16"])
 @pytest.mark.parametrize("wk,ok", [("f32", "bf16"), ("bf16", "f16"), ("f16", "f32")])
-@pytest.mark.parametrize("H", [96, 2056])
+# 2048 and 3000: the ring of rows takes exactly the 48 KB that need no opt-in, beside the static memory
+@pytest.mark.parametrize("H", [96, 2048, 2056, 3000])
 def test_types(H, yk, rk, wk, ok):
     rng = np.random.default_rng(H)
     T = 5
