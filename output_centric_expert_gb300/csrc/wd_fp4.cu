@@ -179,7 +179,10 @@ __device__ __forceinline__ void stage_x(const MvArgs& a, int c0, int c1, int tok
   __syncthreads();
 }
 
-template <int NT, bool BF16>
+// CHUNKED: x is staged a.chunk column tiles at a time, the sums of a batch of row
+// tiles wait in shared memory; else all of x is staged once and a warp's run is one
+// dense stretch of memory.
+template <int NT, bool BF16, bool CHUNKED>
 __global__ void __launch_bounds__(kMvThreads, 1) fp4_matvec_kernel(const MvArgs a) {
   extern __shared__ uint4 dyn4[];
   __shared__ uint32_t s_max[NT * 8];
@@ -187,14 +190,13 @@ __global__ void __launch_bounds__(kMvThreads, 1) fp4_matvec_kernel(const MvArgs 
   // parts of row tiles that warps share: [warp][0: begun before, 1: begun here]
   float(*s_part)[2][kSums] = reinterpret_cast<float(*)[2][kSums]>(dyn4);
   float(*s_sum)[kSums] = reinterpret_cast<float(*)[kSums]>(dyn4 + kMvWarps * 2 * kSums / 4);  // [batch]
-  const int ct = col_tiles(a.K);
-  const bool chunked = a.chunk < ct;
-  float(*s_held)[kSums] = s_sum + a.batch;  // sums of the chunks before, where there are any
-  uint4* xs = dyn4 + (kMvWarps * 2 + a.batch * (chunked ? 2 : 1)) * (kSums / 4);
+  float(*s_held)[kSums] = s_sum + a.batch;  // CHUNKED: sums of the chunks before
+  uint4* xs = dyn4 + (kMvWarps * 2 + a.batch * (CHUNKED ? 2 : 1)) * (kSums / 4);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
   const int toks = min(NT * 8, a.B - a.tok0);
   const int64_t tiles = row_tiles(a.N);
   const int64_t r0 = tiles * blockIdx.x / gridDim.x, r1 = tiles * (blockIdx.x + 1) / gridDim.x;
+  const int ct = col_tiles(a.K);
 
   struct Tile {
     uint4 lo, hi;
@@ -203,99 +205,117 @@ __global__ void __launch_bounds__(kMvThreads, 1) fp4_matvec_kernel(const MvArgs 
   bool staged = false;
   for (int64_t q0 = r0; q0 < r1; q0 += a.batch) {
     const int nq = (int)min((int64_t)a.batch, r1 - q0);
-    for (int c0 = 0; c0 < ct; c0 += a.chunk) {
-      const int kt = min(a.chunk, ct - c0), units = nq * kt;
+    for (int c0 = 0; c0 < ct; c0 += CHUNKED ? a.chunk : ct) {
+      const int kt = CHUNKED ? min(a.chunk, ct - c0) : ct, units = nq * kt;
       const int u0 = units * warp / kMvWarps, u1 = units * (warp + 1) / kMvWarps;
+      int k = u0 % kt;  // column tile at hand
+      const size_t at = (size_t)(q0 + u0 / kt) * ct + c0 + k;
+      const uint8_t* lc = a.codes + at * kTileCodes + lane * 16;  // of the next tile to load
+      const uint8_t* ls = a.scales + at * kTileScales + g * 8;
+      int left = CHUNKED ? kt - k : 0;  // column tiles up to the chunk's end
       Tile buf[kAhead];
-      int lr = u0 / kt, lk = u0 - lr * kt;  // of the next tile to load
       auto load = [&](Tile& b) {
-        const size_t at = (size_t)(q0 + lr) * ct + c0 + lk;
-        const uint8_t* p = a.codes + at * kTileCodes + lane * 16;
-        b.lo = ld_codes16(p);
-        b.hi = ld_codes16(p + 512);
-        b.sc = ld_scales8(a.scales + at * kTileScales + g * 8);
-        if (++lk == kt) {
-          lk = 0;
-          ++lr;
+        b.lo = ld_codes16(lc);
+        b.hi = ld_codes16(lc + 512);
+        b.sc = ld_scales8(ls);
+        lc += kTileCodes;
+        ls += kTileScales;
+        if (CHUNKED && --left == 0) {
+          left = kt;
+          lc += (size_t)(ct - kt) * kTileCodes;
+          ls += (size_t)(ct - kt) * kTileScales;
         }
       };
 #pragma unroll
       for (int i = 0; i < kAhead; ++i)
         if (u0 + i < u1) load(buf[i]);
       if (!staged) stage_x<NT, BF16>(a, c0, c0 + kt, toks, xs, s_max);
-      staged = !chunked;
+      staged = !CHUNKED;
 
       float acc[NT][4] = {};
-      int r = u0 / kt, k = u0 - r * kt, begun = k;  // the tile at hand; its first column tile here
-      auto finish = [&](float* to) {
+      const uint4* xk = xs + (size_t)k * 4 * NT * 32 + lane;
+      // where the sums of the tile at hand go: a slot if it began in another warp's run
+      const int sum_at = 2 * t * kTileRows + g;
+      float* whole = s_sum[u0 / kt] + sum_at;
+      float* to = k == 0 ? whole : s_part[warp][0] + sum_at;
+      auto finish = [&](float* p) {
 #pragma unroll
         for (int n = 0; n < NT; ++n)
 #pragma unroll
           for (int c = 0; c < 4; ++c) {
-            to[(n * 8 + 2 * t + (c & 1)) * kTileRows + g + 8 * (c >> 1)] = acc[n][c];
+            p[(n * 8 + (c & 1)) * kTileRows + 8 * (c >> 1)] = acc[n][c];
             acc[n][c] = 0.0f;
           }
       };
-      for (int u = u0; u < u1; u += kAhead) {
+      auto use = [&](const Tile& b) {
+        const uint32_t wl[4] = {b.lo.x, b.lo.y, b.lo.z, b.lo.w}, wh[4] = {b.hi.x, b.hi.y, b.hi.z, b.hi.w};
+        float sl[4], sh[4];
+        e8m0x4_to_f32(b.sc.x, sl);
+        e8m0x4_to_f32(b.sc.y, sh);
+#pragma unroll
+        for (int blk = 0; blk < 4; ++blk) {
+          uint32_t al[4], ah[4];
+          e2m1x8_to_f16(wl[blk], al);
+          e2m1x8_to_f16(wh[blk], ah);
+          const uint32_t a0[4] = {al[0], ah[0], al[1], ah[1]}, a1[4] = {al[2], ah[2], al[3], ah[3]};
+#pragma unroll
+          for (int n = 0; n < NT; ++n) {
+            // columns without a token hold whatever is there: they reach no other column
+            const uint4 v = xk[(blk * NT + n) * 32];
+            float d[4];
+            mma_new(d, a0, v.x, v.y);
+            mma_add(d, a1, v.z, v.w);
+            acc[n][0] = fmaf(sl[blk], d[0], acc[n][0]);
+            acc[n][1] = fmaf(sl[blk], d[1], acc[n][1]);
+            acc[n][2] = fmaf(sh[blk], d[2], acc[n][2]);
+            acc[n][3] = fmaf(sh[blk], d[3], acc[n][3]);
+          }
+        }
+        xk += 4 * NT * 32;
+        if (++k == kt) {
+          finish(to);
+          k = 0;
+          xk = xs + lane;
+          whole += kSums;
+          to = whole;
+        }
+      };
+      int u = u0;
+      for (; u + 2 * kAhead <= u1; u += kAhead) {
 #pragma unroll
         for (int i = 0; i < kAhead; ++i) {
-          if (u + i >= u1) break;
-          const Tile b = buf[i];
-          if (u + i + kAhead < u1) load(buf[i]);
-          const uint32_t wl[4] = {b.lo.x, b.lo.y, b.lo.z, b.lo.w}, wh[4] = {b.hi.x, b.hi.y, b.hi.z, b.hi.w};
-          float sl[4], sh[4];
-          e8m0x4_to_f32(b.sc.x, sl);
-          e8m0x4_to_f32(b.sc.y, sh);
-          const uint4* xk = xs + (size_t)k * 4 * NT * 32 + lane;
-#pragma unroll
-          for (int blk = 0; blk < 4; ++blk) {
-            uint32_t al[4], ah[4];
-            e2m1x8_to_f16(wl[blk], al);
-            e2m1x8_to_f16(wh[blk], ah);
-            const uint32_t a0[4] = {al[0], ah[0], al[1], ah[1]}, a1[4] = {al[2], ah[2], al[3], ah[3]};
-#pragma unroll
-            for (int n = 0; n < NT; ++n) {
-              // columns without a token hold whatever is there: they reach no other column
-              const uint4 v = xk[(blk * NT + n) * 32];
-              float d[4];
-              mma_new(d, a0, v.x, v.y);
-              mma_add(d, a1, v.z, v.w);
-              acc[n][0] = fmaf(sl[blk], d[0], acc[n][0]);
-              acc[n][1] = fmaf(sl[blk], d[1], acc[n][1]);
-              acc[n][2] = fmaf(sh[blk], d[2], acc[n][2]);
-              acc[n][3] = fmaf(sh[blk], d[3], acc[n][3]);
-            }
-          }
-          if (++k == kt) {
-            finish(begun == 0 ? s_sum[r] : s_part[warp][0]);
-            k = begun = 0;
-            ++r;
-          }
+          use(buf[i]);
+          load(buf[i]);
         }
       }
-      if (u0 < u1 && k > 0) finish(s_part[warp][begun == 0 ? 1 : 0]);
+#pragma unroll 1
+      for (; u < u1; u += kAhead) {
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i) {
+          if (u + i < u1) use(buf[i]);
+          if (u + i + kAhead < u1) load(buf[i]);
+        }
+      }
+      if (k > 0 && u0 < u1) finish(to == whole ? s_part[warp][1] + sum_at : to);
       __syncthreads();
-      const bool last = c0 + kt >= ct;
-      for (int i = tid; i < nq * kSums; i += kMvThreads) {
-        const int q = i / kSums, o = i % kSums, tok = o / kTileRows;
-        const float back = exp2i(-shift_of_bits(s_max[tok]));
-        // the warps that have the tile's first and last column tile
+      const bool last = !CHUNKED || c0 + kt >= ct;
+      for (int q = warp; q < nq; q += kMvWarps) {  // a warp per row tile
+        // the warps that have its first and last column tile
         const int w0 = ((q * kt + 1) * kMvWarps - 1) / units, w1 = ((q + 1) * kt * kMvWarps - 1) / units;
-        float v = 0.0f;
-        if (w0 == w1) {
-          v = s_sum[q][o];
-        } else {
-          v = s_part[w0][1][o];
+#pragma unroll
+        for (int o = lane; o < kSums; o += 32) {
+          float v = w0 == w1 ? s_sum[q][o] : s_part[w0][1][o];
           for (int w = w0 + 1; w <= w1; ++w)
             if (units * w / kMvWarps < units * (w + 1) / kMvWarps) v += s_part[w][0][o];
-        }
-        v *= back;
-        if (c0 > 0) v += s_held[q][o];
-        if (!last) {
-          s_held[q][o] = v;
-        } else {
+          const int tok = o / kTileRows;
+          v *= exp2i(-shift_of_bits(s_max[tok]));
+          if (CHUNKED) {
+            if (c0 > 0) v += s_held[q][o];
+            if (!last) s_held[q][o] = v;
+          }
           const int64_t n = (q0 + q) * kTileRows + o % kTileRows;
-          if (n < a.N && tok < toks) store_elem(a.y, a.y_type, (int64_t)(a.tok0 + tok) * a.ldy + n, v);
+          if (last && n < a.N && tok < toks)
+            store_elem(a.y, a.y_type, (int64_t)(a.tok0 + tok) * a.ldy + n, v);
         }
       }
       __syncthreads();  // the sums, and x where it comes in chunks, are written again
@@ -318,7 +338,7 @@ int64_t padded_words(const wd_fp4_shape* s) {
 
 template <int NT, bool BF16>
 moe_status launch_matvec(MvArgs a, cudaStream_t st) {
-  auto k = fp4_matvec_kernel<NT, BF16>;
+  auto k = fp4_matvec_kernel<NT, BF16, false>;
   constexpr size_t kTileX = (size_t)4 * NT * 32 * 16;  // x of a column tile
   constexpr size_t kTileSum = (size_t)kTileRows * NT * 8 * 4;
   constexpr size_t kRoom = kMaxDynSmem - kStaticSmem - kMvWarps * 2 * kTileSum;
@@ -334,6 +354,7 @@ moe_status launch_matvec(MvArgs a, cudaStream_t st) {
     a.batch = (int)(per < fit ? per : fit);
     smem = ct * kTileX + a.batch * kTileSum;
   } else {  // columns in chunks of 128 KB of x
+    k = fp4_matvec_kernel<NT, BF16, true>;
     a.chunk = 64 / NT;
     a.batch = (int)(per < 32 ? per : 32);
     smem = a.chunk * kTileX + 2 * a.batch * kTileSum;
