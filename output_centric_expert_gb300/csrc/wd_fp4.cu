@@ -1,14 +1,11 @@
 // Projections with 4-bit weights (MXFP4): the packers and the matrix-vector
 // product.
+#include "wd_fp4.h"
+
 #include "wd_block.cuh"
 
 namespace wd {
 namespace {
-
-constexpr int kTileRows = 16;   // rows of a packed tile: one MMA row tile
-constexpr int kTileCols = 128;  // columns of a packed tile: 4 scale blocks
-constexpr int kTileCodes = kTileRows * kTileCols / 2;    // 1024 bytes
-constexpr int kTileScales = kTileRows * kTileCols / 32;  // 64 bytes
 
 __host__ __device__ inline int64_t row_tiles(int N) { return (N + kTileRows - 1) / kTileRows; }
 __host__ __device__ inline int col_tiles(int K) { return (K + kTileCols - 1) / kTileCols; }
@@ -96,17 +93,6 @@ constexpr int kAhead = 4;  // column tiles in flight per warp
 // much is asked for beside the dynamic part.
 constexpr size_t kStaticSmem = 512;
 
-struct MvArgs {
-  const uint8_t *codes, *scales;
-  const uint16_t* x;
-  void* y;
-  int64_t ldx, ldy;
-  int32_t B, y_type, N, K;
-  int32_t tok0;   // first token of this launch
-  int32_t chunk;  // column tiles of x staged at a time; all of them where that fits
-  int32_t batch;  // row tiles of a CTA whose sums wait in shared memory for the other chunks
-};
-
 // The power of two that brings magnitude bits m into [2^14, 2^15), as pow2_shift_for
 // for finite m (a subnormal m counts as the smallest normal).
 __device__ __forceinline__ int shift_of_bits(uint32_t m) {
@@ -114,68 +100,75 @@ __device__ __forceinline__ int shift_of_bits(uint32_t m) {
 }
 
 // Stage `toks` tokens' columns [128 c0, 128 c1) (zero from K on) as f16 fragments;
-// s_max[n] becomes the bits of the token's largest finite magnitude. All threads of
-// the CTA; ends behind a barrier.
+// s_max[n] becomes the bits of the token's largest finite magnitude. A warp takes
+// whole tokens (n = warp, warp + 16, ...), or with 8 tokens and fewer 2, 4, 8 or 16
+// warps share one. All of a warp's loads are in flight at once: 16 pieces of 8
+// elements per lane, which is all of the columns up to 8192 for 8 tokens and the most
+// that the wide kernel stages. All threads of the CTA; ends behind a barrier.
 template <int NT, bool BF16>
 __device__ __forceinline__ void stage_x(const MvArgs& a, int c0, int c1, int toks, uint4* xs,
                                         uint32_t* s_max) {
-  const int k0 = c0 * kTileCols, per = (c1 - c0) * (kTileCols / 8);  // pieces of 8 elements per token
-  const int pieces = toks * per, real = (min(a.K, c1 * kTileCols) - k0) / 8;
+  constexpr int TPW = NT < 2 ? 1 : NT / 2;  // tokens per warp
+  constexpr int PPL = 16 / TPW;             // pieces per lane and token in flight
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int k0 = c0 * kTileCols, pieces = (c1 - c0) * (kTileCols / 8);
+  const int real = (min(a.K, c1 * kTileCols) - k0) / 8;
   const uint16_t* x = a.x + (int64_t)a.tok0 * a.ldx + k0;
+  // lanes that share a token: 32 << share
+  const int share = NT > 1 || toks > 4 ? (NT > 1 ? 0 : 1) : toks > 2 ? 2 : toks > 1 ? 3 : 4;
+  const int first = (warp & ((1 << share) - 1)) * 32 + lane, step = 32 << share;
   auto load = [&](int tok, int piece) {
-    return piece < real ? ld_cached16(x + (int64_t)tok * a.ldx + piece * 8) : make_uint4(0, 0, 0, 0);
+    return piece < real && tok < toks ? ld_cached16(x + (int64_t)tok * a.ldx + piece * 8) : make_uint4(0, 0, 0, 0);
   };
-  if (threadIdx.x < NT * 8) s_max[threadIdx.x] = 0;
-  constexpr int kHold = 4;  // pieces per thread that stay in registers between the two passes
-  uint4 held[kHold];
+  auto largest = [&](const uint4& v, uint32_t m) {
+    float f[8];
+    unpack8<BF16>(v, f);
 #pragma unroll
-  for (int i = 0; i < kHold; ++i) {
-    const int p = threadIdx.x + i * kMvThreads;
-    if (p < pieces) held[i] = load(p / per, p % per);
-  }
-  __syncthreads();
-  auto largest = [&](int p, const uint4& v) {  // called by whole warps
-    int tok = -1;
-    uint32_t m = 0;
-    if (p < pieces) {
-      tok = p / per;
-      float f[8];
-      unpack8<BF16>(v, f);
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const uint32_t b = __float_as_uint(fabsf(f[j]));
-        if (b < 0x7F800000u) m = max(m, b);
-      }
+    for (int k = 0; k < 8; ++k) {
+      const uint32_t b = __float_as_uint(fabsf(f[k]));  // ordered as integers
+      if (b < 0x7F800000u) m = max(m, b);
     }
-    // magnitudes are ordered as integers; one atomic per warp where it holds one token
-    if (__all_sync(0xFFFFFFFFu, tok == __shfl_sync(0xFFFFFFFFu, tok, 0))) {
-      m = __reduce_max_sync(0xFFFFFFFFu, m);
-      if ((threadIdx.x & 31) == 0 && tok >= 0) atomicMax(s_max + tok, m);
-    } else if (tok >= 0) {
-      atomicMax(s_max + tok, m);
-    }
+    return m;
   };
-  auto store = [&](int p, const uint4& v) {
-    const int tok = p / per, piece = p - tok * per;
-    const float up = exp2i(shift_of_bits(s_max[tok]));
+  auto store = [&](int tok, int piece, const uint4& v, float up) {
     float f[8];
     unpack8<BF16>(v, f);
     xs[((piece / 4) * NT + (tok >> 3)) * 32 + (tok & 7) * 4 + piece % 4] =
         make_uint4(pack2<false>(f[0] * up, f[1] * up), pack2<false>(f[2] * up, f[3] * up),
                    pack2<false>(f[4] * up, f[5] * up), pack2<false>(f[6] * up, f[7] * up));
   };
-#pragma unroll
-  for (int i = 0; i < kHold; ++i)
-    if (i * kMvThreads < pieces) largest(threadIdx.x + i * kMvThreads, held[i]);
-  for (int p0 = kHold * kMvThreads; p0 < pieces; p0 += kMvThreads) {
-    const int p = p0 + threadIdx.x;
-    largest(p, p < pieces ? load(p / per, p % per) : make_uint4(0, 0, 0, 0));
+  if (NT == 1) {
+    if (threadIdx.x < 8) s_max[threadIdx.x] = 0;
+    __syncthreads();
   }
-  __syncthreads();
+  uint4 v[TPW][PPL];
 #pragma unroll
-  for (int i = 0; i < kHold; ++i)
-    if (threadIdx.x + i * kMvThreads < pieces) store(threadIdx.x + i * kMvThreads, held[i]);
-  for (int p = threadIdx.x + kHold * kMvThreads; p < pieces; p += kMvThreads) store(p, load(p / per, p % per));
+  for (int j = 0; j < TPW; ++j)
+#pragma unroll
+    for (int i = 0; i < PPL; ++i) v[j][i] = load((warp >> share) + 16 * j, first + step * i);
+#pragma unroll
+  for (int j = 0; j < TPW; ++j) {
+    const int tok = (warp >> share) + 16 * j;
+    uint32_t m = 0;
+#pragma unroll
+    for (int i = 0; i < PPL; ++i) m = largest(v[j][i], m);
+    for (int p = first + step * PPL; p < pieces; p += step) m = largest(load(tok, p), m);
+    m = __reduce_max_sync(0xFFFFFFFFu, m);
+    if (NT == 1) {
+      if (lane == 0 && tok < toks) atomicMax(s_max + tok, m);
+      __syncthreads();
+      m = s_max[tok & 7];
+    } else if (lane == 0) {
+      s_max[tok] = m;
+    }
+    if (tok < toks) {
+      const float up = exp2i(shift_of_bits(m));
+#pragma unroll
+      for (int i = 0; i < PPL; ++i)
+        if (first + step * i < pieces) store(tok, first + step * i, v[j][i], up);
+      for (int p = first + step * PPL; p < pieces; p += step) store(tok, p, load(tok, p), up);
+    }
+  }
   __syncthreads();
 }
 
@@ -424,6 +417,7 @@ extern "C" moe_status wd_fp4_matvec(const wd_fp4_shape* s, const uint8_t* pc, co
     return refuse(MOE_ERR_ALIGN, "wd_fp4_matvec: x needs 16 bytes and ldx % 8 == 0, y its type's size");
   const MvArgs a = {pc, ps, static_cast<const uint16_t*>(x), y, ldx, ldy, B, y_type, s->N, s->K, 0, 0, 0};
   cudaStream_t st = (cudaStream_t)stream;
-  if (x_type == WD_BF16) return B <= 8 ? launch_matvec<1, true>(a, st) : launch_matvec<2, true>(a, st);
-  return B <= 8 ? launch_matvec<1, false>(a, st) : launch_matvec<2, false>(a, st);
+  // up to 8 tokens, and rows too long for the other kernel's shared memory: the stream kernel
+  if (B > 8 && s->K <= tc_most_columns(B)) return launch_tc(a, x_type == WD_BF16, st);
+  return x_type == WD_BF16 ? launch_matvec<1, true>(a, st) : launch_matvec<1, false>(a, st);
 }
