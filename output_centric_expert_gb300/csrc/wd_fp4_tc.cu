@@ -14,10 +14,12 @@
 //
 // Work. A cluster of CTAs shares a run of 128-row tiles, each CTA with its share of the
 // columns, so that it stages and converts only that share of x (64 tokens of 1024
-// columns are 128 KB). In a CTA each of two warpgroups takes a row tile: a thread
-// decodes a row, 128 columns at a time, stores them to tensor memory, and one thread
-// issues the eight MMAs while all decode the next columns. The CTAs add their sums
-// in column order through distributed shared memory.
+// columns are 128 KB). In a CTA two warpgroups take a row tile, every other column tile
+// each: a thread decodes 128 columns of a row, stores them to tensor memory, and one
+// thread issues the eight MMAs while all decode the next columns. (One warpgroup per
+// row tile left the decode waiting on its own latency: two warps per scheduler.) The
+// pair's sums and then the CTAs' are added in a fixed order, the latter through
+// distributed shared memory.
 #include <cooperative_groups.h>
 
 #include <mutex>
@@ -30,34 +32,33 @@ namespace {
 
 namespace cg = cooperative_groups;
 
-constexpr int kTcThreads = 256, kGroups = 2;  // warpgroups
+constexpr int kTcThreads = 512, kGroups = 4;  // warpgroups
+constexpr int kRowTiles = 2;        // row tiles of a CTA at a time, two warpgroups on each
 constexpr int kTcRows = 128;
-constexpr int kTcAhead = 3;         // column tiles of codes in flight per row
-constexpr int kTmemCols = 256;      // per warpgroup: 64 for A, up to 64 for D
+constexpr int kTcAhead = 2;         // column tiles of codes in flight per thread
+constexpr int kTmemCols = 512;      // per warpgroup: 64 for A, up to 64 for D
 constexpr int kStageX = 128 * 1024; // bytes of x per CTA at most
 constexpr uint32_t kWaitLimit = 1u << 22;
 
 __device__ __forceinline__ uint32_t smem_addr(const void* p) { return (uint32_t)__cvta_generic_to_shared(p); }
 
-__device__ __forceinline__ void tmem_store32(uint32_t at, const uint32_t (&r)[64], int o) {
+__device__ __forceinline__ void tmem_store32(uint32_t at, const uint32_t (&r)[32]) {
   asm volatile(
       "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,"
       "%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(at),
-      "r"(r[o]), "r"(r[o + 1]), "r"(r[o + 2]), "r"(r[o + 3]), "r"(r[o + 4]), "r"(r[o + 5]), "r"(r[o + 6]),
-      "r"(r[o + 7]), "r"(r[o + 8]), "r"(r[o + 9]), "r"(r[o + 10]), "r"(r[o + 11]), "r"(r[o + 12]),
-      "r"(r[o + 13]), "r"(r[o + 14]), "r"(r[o + 15]), "r"(r[o + 16]), "r"(r[o + 17]), "r"(r[o + 18]),
-      "r"(r[o + 19]), "r"(r[o + 20]), "r"(r[o + 21]), "r"(r[o + 22]), "r"(r[o + 23]), "r"(r[o + 24]),
-      "r"(r[o + 25]), "r"(r[o + 26]), "r"(r[o + 27]), "r"(r[o + 28]), "r"(r[o + 29]), "r"(r[o + 30]),
-      "r"(r[o + 31])
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]),
+      "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]),
+      "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]),
+      "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]),
+      "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]), "r"(r[30]),
+      "r"(r[31])
       : "memory");
 }
 
-__device__ __forceinline__ void tmem_load16(uint32_t at, uint32_t (&r)[16]) {
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
-        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
-      : "r"(at));
+__device__ __forceinline__ void tmem_load8(uint32_t at, uint32_t (&r)[8]) {
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+               : "r"(at));
   asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
 }
 
@@ -89,18 +90,16 @@ __device__ __forceinline__ void group_sync(int group) {
   asm volatile("bar.sync %0, 128;" ::"r"(group + 1) : "memory");
 }
 
-// Magnitude bits of eight 16-bit elements' largest finite one (BF16 or F16).
+// The two warpgroups of a row tile.
+__device__ __forceinline__ void pair_sync(int side) {
+  asm volatile("bar.sync %0, 256;" ::"r"(side + 1 + kGroups) : "memory");
+}
+
+// The largest finite magnitude's bits of both halves of 16-bit pairs.
 template <bool BF16>
-__device__ __forceinline__ uint32_t largest16(const uint4& v, uint32_t m) {
+__device__ __forceinline__ uint32_t finite_or_0(uint32_t m) {
   constexpr uint32_t kInf = BF16 ? 0x7F80u : 0x7C00u;
-  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const uint32_t lo = w[i] & 0x7FFFu, hi = (w[i] >> 16) & 0x7FFFu;
-    m = max(m, lo < kInf ? lo : 0u);
-    m = max(m, hi < kInf ? hi : 0u);
-  }
-  return m;
+  return (m & 0xFFFFu) < kInf ? m & 0xFFFFu : 0u;
 }
 
 // The exponent of a token's power of two: its magnitude bits m come into [2^14, 2^15).
@@ -111,39 +110,71 @@ __device__ __forceinline__ int token_shift(uint32_t m) {
 }
 
 // x of `toks` tokens (zero up to n), columns [128 c0, 128 c1) (zero from K on), as f16
-// times a power of two per token, K-major without a swizzle: 16-byte unit (k / 8) n +
-// token. Copied as it is, then converted in place. s_max: magnitude bits per token.
+// times a power of two per token, K-major in the 128-byte swizzle: [64 columns][token]
+// [128 bytes], 16-byte unit u of a row at u ^ (token & 7). Copied as it is, then
+// converted in place: 8 lanes have a token's 128 bytes (whole lines, no bank
+// conflicts), and a thread converts what it has copied. s_max: magnitude bits per token.
 template <bool BF16>
 __device__ __forceinline__ void stage(const MvArgs& a, int c0, int c1, int toks, int n, uint4* xs, uint32_t* s_max) {
-  const int k0 = c0 * kTileCols, k8 = (c1 - c0) * (kTileCols / 8), real = (min(a.K, c1 * kTileCols) - k0) / 8;
+  const int k0 = c0 * kTileCols, real = (min(a.K, c1 * kTileCols) - k0) / 8;
   const uint16_t* x = a.x + (int64_t)a.tok0 * a.ldx + k0;
-  // 2 units of 16 tokens per warp and step: whole sectors, two-way bank conflicts
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, blocks = n >> 4;
-  for (int i = warp; i < blocks * (k8 / 2); i += kTcThreads / 32) {
-    const int tok = (i % blocks) * 16 + (lane >> 1), u = (i / blocks) * 2 + (lane & 1);
-    const bool ok = tok < toks && u < real;
-    const uint16_t* p = x + (ok ? (int64_t)tok * a.ldx + u * 8 : 0);
+  const int u = threadIdx.x & 7, rows = (c1 - c0) * 2 * n;  // 128-byte rows, row = 64-column run * n + token
+  constexpr int kStep = kTcThreads / 8;
+  for (int r = threadIdx.x >> 3; r < rows; r += kStep) {
+    const int tok = r & (n - 1), unit = r / n * 8 + u;
+    const bool ok = tok < toks && unit < real;
+    const uint16_t* p = x + (ok ? (int64_t)tok * a.ldx + unit * 8 : 0);
     const int bytes = ok ? 16 : 0;  // 0: zeros, the source is not read
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_addr(xs + u * n + tok)), "l"(p), "r"(bytes)
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_addr(xs + r * 8 + (u ^ (tok & 7)))),
+                 "l"(p), "r"(bytes)
                  : "memory");
   }
   asm volatile("cp.async.commit_group;" ::: "memory");
   if (threadIdx.x < n) s_max[threadIdx.x] = 0;
+  __syncthreads();
   asm volatile("cp.async.wait_group 0;" ::: "memory");
-  __syncthreads();
-  const int tok = threadIdx.x & (n - 1);  // of every unit that this thread converts
-  uint32_t m = 0;
+  // with 64 rows a step, every row of this thread is of one token
+  const int tok = (threadIdx.x >> 3) & (n - 1);
+  uint4* own = xs + (threadIdx.x >> 3) * 8 + (u ^ (tok & 7));  // and 512 units on
+  const int mine = (rows - (int)(threadIdx.x >> 3) + kStep - 1) / kStep;
+  // magnitudes are ordered as integers, two to a word; infinities and NaN (rare) are
+  // seen in the maximum and left out one by one
+  uint32_t pair = 0, m = 0;
 #pragma unroll 4
-  for (int i = threadIdx.x; i < k8 * n; i += kTcThreads) m = largest16<BF16>(xs[i], m);
-  if (m) atomicMax(s_max + tok, m);
+  for (int i = 0; i < mine; ++i) {
+    const uint4 v = own[i * kStep * 8];
+    pair = __vmaxu2(__vmaxu2(pair, v.x & 0x7FFF7FFFu), __vmaxu2(v.y & 0x7FFF7FFFu, __vmaxu2(v.z & 0x7FFF7FFFu, v.w & 0x7FFF7FFFu)));
+  }
+  m = max(pair & 0xFFFFu, pair >> 16);
+  if (finite_or_0<BF16>(m) != m) {
+    m = 0;
+#pragma unroll 1
+    for (int i = 0; i < mine * 4; ++i) {
+      const uint32_t w = reinterpret_cast<const uint32_t*>(own + (i >> 2) * kStep * 8)[i & 3] & 0x7FFF7FFFu;
+      m = max(m, max(finite_or_0<BF16>(w), finite_or_0<BF16>(w >> 16)));
+    }
+  }
+#pragma unroll
+  for (int o = 1; o < 8; o <<= 1) m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
+  if (u == 0) atomicMax(s_max + tok, m);
   __syncthreads();
-  float f[8];
   const float up = exp2i(token_shift<BF16>(s_max[tok]));
-#pragma unroll 4
-  for (int i = threadIdx.x; i < k8 * n; i += kTcThreads) {
-    unpack8<BF16>(xs[i], f);
-    xs[i] = make_uint4(pack2<false>(f[0] * up, f[1] * up), pack2<false>(f[2] * up, f[3] * up),
+  constexpr int kAtOnce = 4;  // read before the first is written back: a store may hide no load
+#pragma unroll 1
+  for (int i = 0; i < mine; i += kAtOnce) {
+    uint4 v[kAtOnce];
+#pragma unroll
+    for (int j = 0; j < kAtOnce; ++j)
+      if (i + j < mine) v[j] = own[(i + j) * kStep * 8];
+#pragma unroll
+    for (int j = 0; j < kAtOnce; ++j) {
+      float f[8];
+      unpack8<BF16>(v[j], f);
+      if (i + j < mine)
+        own[(i + j) * kStep * 8] =
+            make_uint4(pack2<false>(f[0] * up, f[1] * up), pack2<false>(f[2] * up, f[3] * up),
                        pack2<false>(f[4] * up, f[5] * up), pack2<false>(f[6] * up, f[7] * up));
+    }
   }
   // the tensor core reads through the asynchronous proxy
   asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
@@ -153,18 +184,20 @@ template <bool BF16>
 __global__ void __launch_bounds__(kTcThreads, 1) fp4_tc_kernel(const MvArgs a, int n) {
   extern __shared__ uint4 dyn4[];
   __shared__ uint32_t s_max[64], s_tmem;
+  __shared__ __align__(16) float s_back[64];  // 1 / the tokens' powers of two
   __shared__ __align__(8) uint64_t s_bar[kGroups];
   cg::cluster_group cluster = cg::this_cluster();
   const int rank = cluster.block_rank(), size = cluster.num_blocks();
   const int tid = threadIdx.x, warp = tid >> 5, group = tid >> 7, gt = tid & 127;
+  const int side = group >> 1, half = group & 1;  // row tile of the CTA, and which column tiles of it
   const int toks = min(n, a.B - a.tok0);
   const int ct = (a.K + kTileCols - 1) / kTileCols, c0 = ct * rank / size, kt = ct * (rank + 1) / size - c0;
   const int mt = (a.N + kTcRows - 1) / kTcRows, tiles = (a.N + kTileRows - 1) / kTileRows;
   const int set = blockIdx.x / size, sets = gridDim.x / size;
   const int per = mt / sets, more = mt - per * sets;
   const int q0 = set * per + min(set, more), q1 = q0 + per + (set < more ? 1 : 0);
-  float* sums = reinterpret_cast<float*>(dyn4);  // [group][token][128 rows]
-  uint4* xs = dyn4 + kGroups * n * kTcRows / 4;
+  uint4* xs = dyn4 + (1024 - (smem_addr(dyn4) & 1023)) % 1024 / 16;  // the swizzle counts from 1024-byte boundaries
+  float* sums = reinterpret_cast<float*>(xs + ((ct + size - 1) / size) * 16 * n);  // [row tile][token][128 rows]
 
   if (warp == 0)
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_addr(&s_tmem)),
@@ -184,30 +217,47 @@ __global__ void __launch_bounds__(kTcThreads, 1) fp4_tc_kernel(const MvArgs a, i
   Tile buf[kTcAhead];
   const uint8_t *lc, *ls;
   bool inside;
+  const int my_kt = (kt - half + 1) / 2;  // column tiles half, half + 2, ...
   auto point = [&](int q) {  // at this thread's row of tile q
     const int row = q * kTcRows + gt, rt = row / kTileRows;
     inside = q < q1 && rt < tiles;
-    const size_t at = inside ? (size_t)rt * ct + c0 : 0;
+    const size_t at = inside ? (size_t)rt * ct + c0 + half : 0;
     lc = a.codes + at * kTileCodes + (row % kTileRows) * 64;
     ls = a.scales + at * kTileScales + (row % 8) * 8 + (row % kTileRows) / 8 * 4;
   };
   auto load = [&](Tile& t, int k) {
     if (inside) {
-      t.a = ld_codes32(lc + (size_t)k * kTileCodes);
-      t.b = ld_codes32(lc + (size_t)k * kTileCodes + 32);
-      t.sc = __ldg(reinterpret_cast<const uint32_t*>(ls + (size_t)k * kTileScales));
+      t.a = ld_codes32(lc + (size_t)k * 2 * kTileCodes);
+      t.b = ld_codes32(lc + (size_t)k * 2 * kTileCodes + 32);
+      t.sc = __ldg(reinterpret_cast<const uint32_t*>(ls + (size_t)k * 2 * kTileScales));
     } else {
 #pragma unroll
       for (int i = 0; i < 8; ++i) t.a.w[i] = t.b.w[i] = 0;
       t.sc = 0;
     }
   };
-  point(q0 + group);
+  auto largest_scale = [&]() {  // of the row's blocks here, NaN blocks apart
+    uint32_t top = 0;
+    if (inside) {
+#pragma unroll 8
+      for (int k = 0; k < my_kt; ++k) {
+        const uint32_t w = __ldg(reinterpret_cast<const uint32_t*>(ls + (size_t)k * 2 * kTileScales));
+#pragma unroll
+        for (int b = 0; b < 4; ++b) {
+          const uint32_t s = (w >> (8 * b)) & 255u;
+          top = max(top, s == 255u ? 0u : s);
+        }
+      }
+    }
+    return top;
+  };
+  point(q0 + side);
 #pragma unroll
   for (int i = 0; i < kTcAhead; ++i)
-    if (i < kt) load(buf[i], i);
+    if (i < my_kt) load(buf[i], i);
 
   stage<BF16>(a, c0, c0 + kt, toks, n, xs, s_max);
+  if (tid < n) s_back[tid] = exp2i(-token_shift<BF16>(s_max[tid]));
   asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
   __syncthreads();
   asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
@@ -216,100 +266,130 @@ __global__ void __launch_bounds__(kTcThreads, 1) fp4_tc_kernel(const MvArgs a, i
   const uint32_t bar = smem_addr(&s_bar[group]);
   // kind::f16: D FP32, A and B f16, both K-major, N / 8 at bit 17, M / 16 at bit 24
   const uint32_t idesc = (1u << 4) | ((uint32_t)(n / 8) << 17) | ((uint32_t)(kTcRows / 16) << 24);
-  // B: core matrices of 8 tokens x 16 bytes; 16 n bytes to the next 8 columns, 128 to the next 8 tokens
-  const uint64_t bdesc = ((uint64_t)(smem_addr(xs) >> 4) & 0x3FFFu) | ((uint64_t)n << 16) | ((uint64_t)8 << 32) |
-                         ((uint64_t)1 << 46);
-  uint32_t phase = 0;
+  // B: K-major, 128-byte swizzle; 1024 bytes from 8 tokens to the next 8
+  const uint64_t bdesc = ((uint64_t)(smem_addr(xs) >> 4) & 0x3FFFu) | ((uint64_t)1 << 16) | ((uint64_t)64 << 32) |
+                         ((uint64_t)1 << 46) | ((uint64_t)2 << 61);
+  uint32_t phase = 0, next_top = largest_scale();
   bool ok = true;
 
-  for (int q = q0; q < q1; q += kGroups) {
-    if (q + group < q1) {
-      // the row's largest scale code (NaN blocks apart)
-      uint32_t top = 0;
-      if (inside) {
-#pragma unroll 8
-        for (int k = 0; k < kt; ++k) {
-          const uint32_t w = __ldg(reinterpret_cast<const uint32_t*>(ls + (size_t)k * kTileScales));
-#pragma unroll
-          for (int b = 0; b < 4; ++b) {
-            const uint32_t s = (w >> (8 * b)) & 255u;
-            top = max(top, s == 255u ? 0u : s);
-          }
-        }
-      }
-      for (int k0 = 0; k0 < kt; k0 += kTcAhead) {
+  for (int q = q0; q < q1; q += kRowTiles) {
+    if (q + side < q1) {
+      const uint32_t top = next_top;
+      for (int k0 = 0; k0 < my_kt; k0 += kTcAhead) {
 #pragma unroll
         for (int i = 0; i < kTcAhead; ++i) {
           const int k = k0 + i;
-          if (k >= kt) break;
-          // ---- decode: MMA step j covers columns 16j ..: block j / 2, quarters 2 (j & 1) and + 1
-          uint32_t v[64], mul[4];
+          if (k >= my_kt) break;
+          uint32_t mul[4];
 #pragma unroll
           for (int b = 0; b < 4; ++b) {
             const uint32_t s = (buf[i].sc >> (8 * b)) & 255u;
             const int e = max(0, (int)s - (int)top + 27);
             mul[b] = s == 255u ? 0x7E007E00u : (uint32_t)e * 0x04000400u;
           }
+          // ---- decode and store two blocks at a time; column k / 2 of A holds the elements k, k + 1
 #pragma unroll
-          for (int t = 0; t < 4; ++t)
+          for (int o = 0; o < 2; ++o) {
+            uint32_t v[32];
 #pragma unroll
-            for (int b = 0; b < 4; ++b) {
-              uint32_t h[4];
-              e2m1x8_to_f16(t < 2 ? buf[i].a.w[t * 4 + b] : buf[i].b.w[(t - 2) * 4 + b], h);
+            for (int t = 0; t < 4; ++t)
 #pragma unroll
-              for (int c = 0; c < 4; ++c) {
-                const __half2 p = __hmul2(*reinterpret_cast<const __half2*>(&h[c]),
-                                          *reinterpret_cast<const __half2*>(&mul[b]));
-                v[b * 16 + t * 4 + c] = *reinterpret_cast<const uint32_t*>(&p);
+              for (int b = 0; b < 2; ++b) {
+                uint32_t h[4];
+                e2m1x8_to_f16(t < 2 ? buf[i].a.w[t * 4 + 2 * o + b] : buf[i].b.w[(t - 2) * 4 + 2 * o + b], h);
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                  const __half2 p = __hmul2(*reinterpret_cast<const __half2*>(&h[c]),
+                                            *reinterpret_cast<const __half2*>(&mul[2 * o + b]));
+                  v[b * 16 + t * 4 + c] = *reinterpret_cast<const uint32_t*>(&p);
+                }
               }
+            if (o == 0 && k > 0) {  // the MMAs of the column tile before have read A
+              ok = ok && wait_phase(bar, phase);
+              phase ^= 1;
+              asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
             }
-          if (k + kTcAhead < kt) load(buf[i], k + kTcAhead);
-          if (k > 0) {  // the MMAs of the column tile before have read A
-            ok = ok && wait_phase(bar, phase);
-            phase ^= 1;
-            asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+            tmem_store32(mine + 32 * o, v);
           }
-          tmem_store32(mine, v, 0);
-          tmem_store32(mine + 32, v, 32);
+          if (k + kTcAhead < my_kt) load(buf[i], k + kTcAhead);
           asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
           asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
           group_sync(group);
           if (gt == 0) {
             asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-            const uint64_t b = bdesc + (uint64_t)(k * 16 * n);  // 16 units of 8 columns, n * 16 bytes each
+            const uint64_t b = bdesc + (uint64_t)((2 * k + half) * 16 * n);  // two runs of 64 columns, 8 n units each
 #pragma unroll
-            for (int j = 0; j < 8; ++j) tc_mma(tmem + 64, tmem + j * 8, b + (uint64_t)(j * 2 * n), idesc, k + j > 0);
+            for (int j = 0; j < 8; ++j)  // 32 bytes on in a row, or in the second run
+              tc_mma(tmem + 64, tmem + j * 8, b + (uint64_t)(j / 4 * 8 * n + j % 4 * 2), idesc, k + j > 0);
             asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar)
                          : "memory");
           }
         }
       }
       // the next row tile's first codes, while this one's sums are taken
-      point(q + kGroups + group);
+      point(q + kRowTiles + side);
 #pragma unroll
       for (int i = 0; i < kTcAhead; ++i)
-        if (i < kt) load(buf[i], i);
-      ok = ok && wait_phase(bar, phase);
-      phase ^= 1;
+        if (i < my_kt) load(buf[i], i);
+      next_top = largest_scale();
+      if (my_kt > 0) {
+        ok = ok && wait_phase(bar, phase);
+        phase ^= 1;
+      }
       asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-      float* to = sums + group * n * kTcRows + gt;
-#pragma unroll 1
-      for (int c = 0; c < n; c += 16) {
-        uint32_t d[16];
-        tmem_load16(mine + 64 + c, d);
+      float* to = sums + side * n * kTcRows + gt;
+      // D holds the sum times 2^(12 - (top - 127)) and the token's power of two. Taken off
+      // one after the other where neither step can leave FP32's range, else in one.
+      // Each half first leaves the tokens that the other half adds to its own.
+      const bool plain = __all_sync(0xFFFFFFFFu, top >= 64u && top <= 190u);
+      const float back = ok ? exp2i(plain ? (int)top - 139 : 0) : NAN;  // a wait that ran out: no sum to trust
+      auto take = [&](int c, float (&o)[8]) {  // tokens c .. c + 7 of this half's sum
+        if (my_kt == 0) {
 #pragma unroll
-        for (int j = 0; j < 16; ++j)
-          // D holds 2^(12 - (top - 127)) times the token's power of two (one step: either
-          // factor alone may leave FP32's range); a wait that ran out: no sum to trust
-          to[(c + j) * kTcRows] =
-              ok ? ldexpf(__uint_as_float(d[j]), (int)top - 139 - token_shift<BF16>(s_max[c + j])) : NAN;
+          for (int j = 0; j < 8; ++j) o[j] = 0.0f;
+          return;
+        }
+        uint32_t d[8];
+        tmem_load8(mine + 64 + c, d);
+        const float4 b0 = *reinterpret_cast<const float4*>(s_back + c), b1 = *reinterpret_cast<const float4*>(s_back + c + 4);
+        const float b[8] = {b0.x, b0.y, b0.z, b0.w, b1.x, b1.y, b1.z, b1.w};
+#pragma unroll
+        for (int j = 0; j < 8; ++j) o[j] = __uint_as_float(d[j]) * back * b[j];
+        if (!plain) {
+#pragma unroll 1
+          for (int j = 0; j < 8; ++j) {
+            float v = 0.0f;
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+              if (j == k) v = __uint_as_float(d[k]) * back;
+            v = ldexpf(v, (int)top - 139 - token_shift<BF16>(s_max[c + j]));
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+              if (j == k) o[k] = v;
+          }
+        }
+      };
+      const int own0 = half * (n / 2), other0 = n / 2 - own0;  // first token of either share
+      float o[8];
+#pragma unroll 1
+      for (int c = 0; c < n / 2; c += 8) {
+        take(other0 + c, o);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) to[(other0 + c + j) * kTcRows] = o[j];
+      }
+      pair_sync(side);
+#pragma unroll 1
+      for (int c = 0; c < n / 2; c += 8) {
+        take(own0 + c, o);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) to[(own0 + c + j) * kTcRows] += o[j];
       }
       asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
     }
     cluster.sync();
     // ---- add the CTAs' sums: this CTA's share of the tokens, 4 rows a thread
     const int t0 = toks * rank / size, t1 = toks * (rank + 1) / size;
-    const int here = min(kGroups, q1 - q) * (t1 - t0) * (kTcRows / 4);
+    const int here = min(kRowTiles, q1 - q) * (t1 - t0) * (kTcRows / 4);
     for (int i = tid; i < here; i += kTcThreads) {
       const int r = i % (kTcRows / 4) * 4, tt = i / (kTcRows / 4), tok = t0 + tt % (t1 - t0), g = tt / (t1 - t0);
       float* src = sums + (g * n + tok) * kTcRows + r;
@@ -383,16 +463,18 @@ moe_status launch(MvArgs a, cudaStream_t st) {
   const int ct = (a.K + kTileCols - 1) / kTileCols, mt = (a.N + kTcRows - 1) / kTcRows;
   int n = tokens_up(a.B - a.tok0);
   while (n > 16 && ct > kMaxCluster * stage_tiles(n)) n /= 2;
-  // CTAs per cluster: as many as x needs, and more while there are fewer row tiles than
-  // warpgroups and every CTA keeps 4 column tiles
-  int size = 1;
-  while (size < kMaxCluster && ((ct + size - 1) / size > stage_tiles(n) ||
-                                (mt * size < sm_count() * kGroups && ct >= 8 * size)))
-    size *= 2;
-  const size_t room = kStageX + (size_t)kGroups * 64 * kTcRows * 4;
+  const size_t room = kStageX + (size_t)kRowTiles * 64 * kTcRows * 4 + 1024;
   moe_status rc = allow_smem(k, room);
   if (rc != MOE_OK) return rc;
-  const int most = resident_clusters(k, size, room), want = (mt + kGroups - 1) / kGroups;
+  // CTAs per cluster: as many as x needs, and more while all row tiles still have a
+  // place at once and every CTA keeps 2 column tiles. 16 tokens of 9216 x 4096 (36 pairs
+  // of row tiles): 26.8 us alone, 16.7, 12.4 and, where only 15 clusters fit, 18.7 us
+  // for 2, 4 and 8 CTAs; 65536 x 4096: 50.4, 54.9, 77.8, 114.
+  const int want = (mt + kRowTiles - 1) / kRowTiles;
+  int size = 1;
+  while (size < kMaxCluster && (ct + size - 1) / size > stage_tiles(n)) size *= 2;
+  while (size < kMaxCluster && ct >= 4 * size && want <= resident_clusters(k, 2 * size, room)) size *= 2;
+  const int most = resident_clusters(k, size, room);
   cudaLaunchAttribute attr = {};
   attr.id = cudaLaunchAttributeClusterDimension;
   attr.val.clusterDim.x = size;
@@ -400,7 +482,7 @@ moe_status launch(MvArgs a, cudaStream_t st) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)((want < most ? want : most) * size));
   cfg.blockDim = dim3(kTcThreads);
-  cfg.dynamicSmemBytes = (size_t)((ct + size - 1) / size) * n * 2 * kTileCols + (size_t)kGroups * n * kTcRows * 4;
+  cfg.dynamicSmemBytes = (size_t)((ct + size - 1) / size) * n * 2 * kTileCols + (size_t)kRowTiles * n * kTcRows * 4 + 1024;
   cfg.stream = st;
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
