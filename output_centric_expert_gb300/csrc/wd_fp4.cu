@@ -88,107 +88,66 @@ __global__ void __launch_bounds__(kThreads)
 // joined in shared memory in column order, so results do not depend on timing.
 
 constexpr int kMvWarps = 16, kMvThreads = kMvWarps * 32;
+constexpr int kMvTokens = 8;  // of a launch: the columns of an MMA
 constexpr int kAhead = 4;  // column tiles in flight per warp
 // Static and dynamic shared memory count together against the default limit: this
 // much is asked for beside the dynamic part.
 constexpr size_t kStaticSmem = 512;
 
-// The power of two that brings magnitude bits m into [2^14, 2^15), as pow2_shift_for
-// for finite m (a subnormal m counts as the smallest normal).
-__device__ __forceinline__ int shift_of_bits(uint32_t m) {
-  return m == 0 ? 0 : min(126, max(-126, 141 - (int)(m >> 23)));
-}
-
 // Stage `toks` tokens' columns [128 c0, 128 c1) (zero from K on) as f16 fragments;
-// s_max[n] becomes the bits of the token's largest finite magnitude. A warp takes
-// whole tokens (n = warp, warp + 16, ...), or with 8 tokens and fewer 2, 4, 8 or 16
-// warps share one. All of a warp's loads are in flight at once: 16 pieces of 8
-// elements per lane, which is all of the columns up to 8192 for 8 tokens and the most
-// that the wide kernel stages. All threads of the CTA; ends behind a barrier.
-template <int NT, bool BF16>
-__device__ __forceinline__ void stage_x(const MvArgs& a, int c0, int c1, int toks, uint4* xs,
-                                        uint32_t* s_max) {
-  constexpr int TPW = NT < 2 ? 1 : NT / 2;  // tokens per warp
-  constexpr int PPL = 16 / TPW;             // pieces per lane and token in flight
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int k0 = c0 * kTileCols, pieces = (c1 - c0) * (kTileCols / 8);
+// s_max[n] becomes the bits of the token's largest finite magnitude (16 bits). Copied
+// as they are to their places, then converted there by the thread that copied them;
+// its pieces are all of one token. Short loops instead of unrolled registers: a
+// small product spends its time fetching code. All threads of the CTA; ends behind a
+// barrier.
+template <bool BF16>
+__device__ __forceinline__ void stage_x(const MvArgs& a, int c0, int c1, int toks, uint4* xs, uint32_t* s_max) {
+  const int k0 = c0 * kTileCols, quads = (c1 - c0) * 4;  // blocks of 32 columns: 4 pieces of 8
   const int real = (min(a.K, c1 * kTileCols) - k0) / 8;
-  const uint16_t* x = a.x + (int64_t)a.tok0 * a.ldx + k0;
-  // lanes that share a token: 32 << share
-  const int share = NT > 1 || toks > 4 ? (NT > 1 ? 0 : 1) : toks > 2 ? 2 : toks > 1 ? 3 : 4;
-  const int first = (warp & ((1 << share) - 1)) * 32 + lane, step = 32 << share;
-  auto load = [&](int tok, int piece) {
-    return piece < real && tok < toks ? ld_cached16(x + (int64_t)tok * a.ldx + piece * 8) : make_uint4(0, 0, 0, 0);
-  };
-  auto largest = [&](const uint4& v, uint32_t m) {
-    float f[8];
-    unpack8<BF16>(v, f);
-#pragma unroll
-    for (int k = 0; k < 8; ++k) {
-      const uint32_t b = __float_as_uint(fabsf(f[k]));  // ordered as integers
-      if (b < 0x7F800000u) m = max(m, b);
-    }
-    return m;
-  };
-  auto store = [&](int tok, int piece, const uint4& v, float up) {
-    float f[8];
-    unpack8<BF16>(v, f);
-    xs[((piece / 4) * NT + (tok >> 3)) * 32 + (tok & 7) * 4 + piece % 4] =
-        make_uint4(pack2<false>(f[0] * up, f[1] * up), pack2<false>(f[2] * up, f[3] * up),
-                   pack2<false>(f[4] * up, f[5] * up), pack2<false>(f[6] * up, f[7] * up));
-  };
-  if (NT == 1) {
-    if (threadIdx.x < 8) s_max[threadIdx.x] = 0;
-    __syncthreads();
+  const int share = toks > 4 ? 3 : toks > 2 ? 2 : toks > 1 ? 1 : 0;  // 1 << share tokens, the last may be zero
+  const int q = threadIdx.x & 3, tok = (threadIdx.x >> 2) & ((1 << share) - 1);
+  const int first = threadIdx.x >> (2 + share), step = kMvThreads >> (2 + share);
+  const uint16_t* x = a.x + (int64_t)(a.tok0 + (tok < toks ? tok : 0)) * a.ldx + k0 + q * 8;
+  uint4* own = xs + first * 32 + tok * 4 + q;  // and 32 * step units on
+  for (int b = first; b < quads; b += step) {
+    const int bytes = tok < toks && b * 4 + q < real ? 16 : 0;  // 0: zeros, the source is not read
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(
+                     (uint32_t)__cvta_generic_to_shared(xs + b * 32 + tok * 4 + q)),
+                 "l"(x + (bytes ? b * 32 : 0)), "r"(bytes)
+                 : "memory");
   }
-  uint4 v[TPW][PPL];
-#pragma unroll
-  for (int j = 0; j < TPW; ++j)
-#pragma unroll
-    for (int i = 0; i < PPL; ++i) v[j][i] = load((warp >> share) + 16 * j, first + step * i);
-#pragma unroll
-  for (int j = 0; j < TPW; ++j) {
-    const int tok = (warp >> share) + 16 * j;
-    uint32_t m = 0;
-#pragma unroll
-    for (int i = 0; i < PPL; ++i) m = largest(v[j][i], m);
-    for (int p = first + step * PPL; p < pieces; p += step) m = largest(load(tok, p), m);
-    m = __reduce_max_sync(0xFFFFFFFFu, m);
-    if (NT == 1) {
-      if (lane == 0 && tok < toks) atomicMax(s_max + tok, m);
-      __syncthreads();
-      m = s_max[tok & 7];
-    } else if (lane == 0) {
-      s_max[tok] = m;
-    }
-    if (tok < toks) {
-      const float up = exp2i(shift_of_bits(m));
-#pragma unroll
-      for (int i = 0; i < PPL; ++i)
-        if (first + step * i < pieces) store(tok, first + step * i, v[j][i], up);
-      for (int p = first + step * PPL; p < pieces; p += step) store(tok, p, load(tok, p), up);
-    }
-  }
+  asm volatile("cp.async.commit_group;" ::: "memory");
+  if (threadIdx.x < 8) s_max[threadIdx.x] = 0;
+  __syncthreads();
+  asm volatile("cp.async.wait_group 0;" ::: "memory");
+  const int mine = (quads - first + step - 1) / step;
+  uint32_t m = largest_finite16<BF16>(own, mine, 32 * step);
+  m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 1));
+  m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 2));
+  for (int o = 16; o >= 4 << share; o >>= 1) m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
+  if ((threadIdx.x & 31) < 4u << share && q == 0) atomicMax(s_max + tok, m);
+  __syncthreads();
+  scale_to_f16<BF16>(own, mine, 32 * step, exp2i(shift_of_16<BF16>(s_max[tok])));
   __syncthreads();
 }
 
 // CHUNKED: x is staged a.chunk column tiles at a time, the sums of a batch of row
 // tiles wait in shared memory; else all of x is staged once and a warp's run is one
 // dense stretch of memory.
-template <int NT, bool BF16, bool CHUNKED>
+template <bool BF16, bool CHUNKED>
 __global__ void __launch_bounds__(kMvThreads, 1) fp4_matvec_kernel(const MvArgs a) {
   extern __shared__ uint4 dyn4[];
-  __shared__ uint32_t s_max[NT * 8];
-  constexpr int kSums = kTileRows * NT * 8;  // of a row tile: [token][row]
+  __shared__ uint32_t s_max[kMvTokens];
+  constexpr int kSums = kTileRows * kMvTokens;  // of a row tile: [token][row]
   // parts of row tiles that warps share: [warp][0: begun before, 1: begun here]
   float(*s_part)[2][kSums] = reinterpret_cast<float(*)[2][kSums]>(dyn4);
   float(*s_sum)[kSums] = reinterpret_cast<float(*)[kSums]>(dyn4 + kMvWarps * 2 * kSums / 4);  // [batch]
   float(*s_held)[kSums] = s_sum + a.batch;  // CHUNKED: sums of the chunks before
   uint4* xs = dyn4 + (kMvWarps * 2 + a.batch * (CHUNKED ? 2 : 1)) * (kSums / 4);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
-  const int toks = min(NT * 8, a.B - a.tok0);
-  const int64_t tiles = row_tiles(a.N);
-  const int64_t r0 = tiles * blockIdx.x / gridDim.x, r1 = tiles * (blockIdx.x + 1) / gridDim.x;
+  const int toks = min(kMvTokens, a.B - a.tok0);
+  const int b0 = blockIdx.x;  // row tiles [r0, r1)
+  const int r0 = b0 * a.per + min(b0, a.more), r1 = r0 + a.per + (b0 < a.more ? 1 : 0);
   const int ct = col_tiles(a.K);
 
   struct Tile {
@@ -196,13 +155,14 @@ __global__ void __launch_bounds__(kMvThreads, 1) fp4_matvec_kernel(const MvArgs 
     uint2 sc;
   };
   bool staged = false;
-  for (int64_t q0 = r0; q0 < r1; q0 += a.batch) {
-    const int nq = (int)min((int64_t)a.batch, r1 - q0);
+  for (int q0 = r0; q0 < r1; q0 += a.batch) {
+    const int nq = min(a.batch, r1 - q0);
     for (int c0 = 0; c0 < ct; c0 += CHUNKED ? a.chunk : ct) {
       const int kt = CHUNKED ? min(a.chunk, ct - c0) : ct, units = nq * kt;
       const int u0 = units * warp / kMvWarps, u1 = units * (warp + 1) / kMvWarps;
-      int k = u0 % kt;  // column tile at hand
-      const size_t at = (size_t)(q0 + u0 / kt) * ct + c0 + k;
+      const int t0 = u0 / kt;
+      int k = u0 - t0 * kt;  // column tile at hand
+      const size_t at = (size_t)(q0 + t0) * ct + c0 + k;
       const uint8_t* lc = a.codes + at * kTileCodes + lane * 16;  // of the next tile to load
       const uint8_t* ls = a.scales + at * kTileScales + g * 8;
       int left = CHUNKED ? kt - k : 0;  // column tiles up to the chunk's end
@@ -222,23 +182,21 @@ __global__ void __launch_bounds__(kMvThreads, 1) fp4_matvec_kernel(const MvArgs 
 #pragma unroll
       for (int i = 0; i < kAhead; ++i)
         if (u0 + i < u1) load(buf[i]);
-      if (!staged) stage_x<NT, BF16>(a, c0, c0 + kt, toks, xs, s_max);
+      if (!staged) stage_x<BF16>(a, c0, c0 + kt, toks, xs, s_max);
       staged = !CHUNKED;
 
-      float acc[NT][4] = {};
-      const uint4* xk = xs + (size_t)k * 4 * NT * 32 + lane;
+      float acc[4] = {};
+      const uint4* xk = xs + (size_t)k * 4 * 32 + lane;
       // where the sums of the tile at hand go: a slot if it began in another warp's run
       const int sum_at = 2 * t * kTileRows + g;
-      float* whole = s_sum[u0 / kt] + sum_at;
+      float* whole = s_sum[t0] + sum_at;
       float* to = k == 0 ? whole : s_part[warp][0] + sum_at;
       auto finish = [&](float* p) {
 #pragma unroll
-        for (int n = 0; n < NT; ++n)
-#pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            p[(n * 8 + (c & 1)) * kTileRows + 8 * (c >> 1)] = acc[n][c];
-            acc[n][c] = 0.0f;
-          }
+        for (int c = 0; c < 4; ++c) {
+          p[(c & 1) * kTileRows + 8 * (c >> 1)] = acc[c];
+          acc[c] = 0.0f;
+        }
       };
       auto use = [&](const Tile& b) {
         const uint32_t wl[4] = {b.lo.x, b.lo.y, b.lo.z, b.lo.w}, wh[4] = {b.hi.x, b.hi.y, b.hi.z, b.hi.w};
@@ -251,20 +209,17 @@ __global__ void __launch_bounds__(kMvThreads, 1) fp4_matvec_kernel(const MvArgs 
           e2m1x8_to_f16(wl[blk], al);
           e2m1x8_to_f16(wh[blk], ah);
           const uint32_t a0[4] = {al[0], ah[0], al[1], ah[1]}, a1[4] = {al[2], ah[2], al[3], ah[3]};
-#pragma unroll
-          for (int n = 0; n < NT; ++n) {
-            // columns without a token hold whatever is there: they reach no other column
-            const uint4 v = xk[(blk * NT + n) * 32];
-            float d[4];
-            mma_new(d, a0, v.x, v.y);
-            mma_add(d, a1, v.z, v.w);
-            acc[n][0] = fmaf(sl[blk], d[0], acc[n][0]);
-            acc[n][1] = fmaf(sl[blk], d[1], acc[n][1]);
-            acc[n][2] = fmaf(sh[blk], d[2], acc[n][2]);
-            acc[n][3] = fmaf(sh[blk], d[3], acc[n][3]);
-          }
+          // columns without a token hold whatever is there: they reach no other column
+          const uint4 v = xk[blk * 32];
+          float d[4];
+          mma_new(d, a0, v.x, v.y);
+          mma_add(d, a1, v.z, v.w);
+          acc[0] = fmaf(sl[blk], d[0], acc[0]);
+          acc[1] = fmaf(sl[blk], d[1], acc[1]);
+          acc[2] = fmaf(sh[blk], d[2], acc[2]);
+          acc[3] = fmaf(sh[blk], d[3], acc[3]);
         }
-        xk += 4 * NT * 32;
+        xk += 4 * 32;
         if (++k == kt) {
           finish(to);
           k = 0;
@@ -293,23 +248,23 @@ __global__ void __launch_bounds__(kMvThreads, 1) fp4_matvec_kernel(const MvArgs 
       __syncthreads();
       const bool last = !CHUNKED || c0 + kt >= ct;
       for (int q = warp; q < nq; q += kMvWarps) {  // a warp per row tile
-        // the warps that have its first and last column tile
+        // the warps that have its first and last column tile; a lane has 4 rows of a token
         const int w0 = ((q * kt + 1) * kMvWarps - 1) / units, w1 = ((q + 1) * kt * kMvWarps - 1) / units;
-#pragma unroll
-        for (int o = lane; o < kSums; o += 32) {
-          float v = w0 == w1 ? s_sum[q][o] : s_part[w0][1][o];
-          for (int w = w0 + 1; w <= w1; ++w)
-            if (units * w / kMvWarps < units * (w + 1) / kMvWarps) v += s_part[w][0][o];
-          const int tok = o / kTileRows;
-          v *= exp2i(-shift_of_bits(s_max[tok]));
-          if (CHUNKED) {
-            if (c0 > 0) v += s_held[q][o];
-            if (!last) s_held[q][o] = v;
-          }
-          const int64_t n = (q0 + q) * kTileRows + o % kTileRows;
-          if (last && n < a.N && tok < toks)
-            store_elem(a.y, a.y_type, (int64_t)(a.tok0 + tok) * a.ldy + n, v);
+        const int o = lane * 4, tok = o / kTileRows;
+        float4 v = *reinterpret_cast<const float4*>(w0 == w1 ? s_sum[q] + o : s_part[w0][1] + o);
+        for (int w = w0 + 1; w <= w1; ++w) {
+          if (units * w / kMvWarps == units * (w + 1) / kMvWarps) continue;  // an empty run
+          const float4 p = *reinterpret_cast<const float4*>(s_part[w][0] + o);
+          v.x += p.x, v.y += p.y, v.z += p.z, v.w += p.w;
         }
+        const float back = exp2i(-shift_of_16<BF16>(s_max[tok]));
+        v.x *= back, v.y *= back, v.z *= back, v.w *= back;
+        if (CHUNKED) {
+          float4* held = reinterpret_cast<float4*>(s_held[q] + o);
+          if (c0 > 0) v.x += held->x, v.y += held->y, v.z += held->z, v.w += held->w;
+          if (!last) *held = v;
+        }
+        if (last && tok < toks) store_rows(a, a.tok0 + tok, (int64_t)(q0 + q) * kTileRows + o % kTileRows, v);
       }
       __syncthreads();  // the sums, and x where it comes in chunks, are written again
     }
@@ -329,16 +284,18 @@ int64_t padded_words(const wd_fp4_shape* s) {
   return row_tiles(s->N) * kTileRows * col_tiles(s->K) * (kTileCols / 8);
 }
 
-template <int NT, bool BF16>
+template <bool BF16>
 moe_status launch_matvec(MvArgs a, cudaStream_t st) {
-  auto k = fp4_matvec_kernel<NT, BF16, false>;
-  constexpr size_t kTileX = (size_t)4 * NT * 32 * 16;  // x of a column tile
-  constexpr size_t kTileSum = (size_t)kTileRows * NT * 8 * 4;
+  auto k = fp4_matvec_kernel<BF16, false>;
+  constexpr size_t kTileX = (size_t)4 * 32 * 16;  // x of a column tile
+  constexpr size_t kTileSum = (size_t)kTileRows * kMvTokens * 4;
   constexpr size_t kRoom = kMaxDynSmem - kStaticSmem - kMvWarps * 2 * kTileSum;
   const int ct = col_tiles(a.K);
   const int64_t tiles = row_tiles(a.N);
   const int sms = sm_count();
   const unsigned grid = (unsigned)(tiles < sms ? tiles : sms);
+  a.per = (int)(tiles / grid);
+  a.more = (int)(tiles - (int64_t)a.per * grid);
   const int64_t per = (tiles + grid - 1) / grid;
   size_t smem;
   if (ct * kTileX + 8 * kTileSum <= kRoom) {  // all of x, and the sums of as many row tiles as fit
@@ -347,15 +304,15 @@ moe_status launch_matvec(MvArgs a, cudaStream_t st) {
     a.batch = (int)(per < fit ? per : fit);
     smem = ct * kTileX + a.batch * kTileSum;
   } else {  // columns in chunks of 128 KB of x
-    k = fp4_matvec_kernel<NT, BF16, true>;
-    a.chunk = 64 / NT;
+    k = fp4_matvec_kernel<BF16, true>;
+    a.chunk = 64;
     a.batch = (int)(per < 32 ? per : 32);
     smem = a.chunk * kTileX + 2 * a.batch * kTileSum;
   }
   smem += kMvWarps * 2 * kTileSum;
   moe_status rc = allow_smem(k, smem + kStaticSmem);
   if (rc != MOE_OK) return rc;
-  for (a.tok0 = 0; a.tok0 < a.B; a.tok0 += NT * 8) {
+  for (a.tok0 = 0; a.tok0 < a.B; a.tok0 += kMvTokens) {
     k<<<grid, kMvThreads, smem, st>>>(a);
     if ((rc = launched("wd_fp4_matvec launch")) != MOE_OK) return rc;
   }
@@ -419,5 +376,5 @@ extern "C" moe_status wd_fp4_matvec(const wd_fp4_shape* s, const uint8_t* pc, co
   cudaStream_t st = (cudaStream_t)stream;
   // up to 8 tokens, and rows too long for the other kernel's shared memory: the stream kernel
   if (B > 8 && s->K <= tc_most_columns(B)) return launch_tc(a, x_type == WD_BF16, st);
-  return x_type == WD_BF16 ? launch_matvec<1, true>(a, st) : launch_matvec<1, false>(a, st);
+  return x_type == WD_BF16 ? launch_matvec<true>(a, st) : launch_matvec<false>(a, st);
 }

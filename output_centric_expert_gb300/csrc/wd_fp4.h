@@ -1,7 +1,8 @@
-// What the two matvec kernels share: the packed tile sizes and the arguments.
+// What the two matvec kernels share: the packed tile sizes, the arguments and the
+// conversion of x.
 #pragma once
 
-#include "warp_decode_block.h"
+#include "wd_block.cuh"
 
 namespace wd {
 
@@ -19,11 +20,94 @@ struct MvArgs {
   int32_t tok0;   // first token of this launch
   int32_t chunk;  // stream kernel: column tiles of x staged at a time; all of them where that fits
   int32_t batch;  // stream kernel: row tiles of a CTA whose sums wait in shared memory
+  int32_t per, more;  // stream kernel: row tiles of a CTA, and how many CTAs have one more
 };
 
 // Columns that the tensor-memory kernel takes for `tokens` tokens (wd_fp4_tc.cu), and
 // its launch: tokens tok0 .. B-1, in runs of 64 or fewer.
 int tc_most_columns(int tokens);
 moe_status launch_tc(MvArgs a, bool bf16, cudaStream_t st);
+
+namespace {  // device code: one copy per translation unit
+
+// Four rows of a token's y, rounded to its type.
+__device__ __forceinline__ void store_rows(const MvArgs& a, int tok, int64_t row, const float4& v) {
+  const int64_t at = (int64_t)tok * a.ldy + row;
+  if (row + 4 <= a.N && a.y_type != WD_F32 && at % 4 == 0 && (reinterpret_cast<uintptr_t>(a.y) & 7) == 0) {
+    *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.y) + at) =
+        a.y_type == WD_BF16 ? make_uint2(pack2<true>(v.x, v.y), pack2<true>(v.z, v.w))
+                            : make_uint2(pack2<false>(v.x, v.y), pack2<false>(v.z, v.w));
+    return;
+  }
+  const float f[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+  for (int j = 0; j < 4; ++j)
+    if (row + j < a.N) store_elem(a.y, a.y_type, at + j, f[j]);
+}
+
+// ---- x as f16 times a power of two per token: its largest finite magnitude comes
+// into [2^14, 2^15), so BF16 and F16 values are exact down to 2^-32 of it.
+
+// The lower of a word's two 16-bit magnitudes, 0 for infinities and NaN.
+template <bool BF16>
+__device__ __forceinline__ uint32_t finite_or_0(uint32_t m) {
+  constexpr uint32_t kInf = BF16 ? 0x7F80u : 0x7C00u;
+  return (m & 0xFFFFu) < kInf ? m & 0xFFFFu : 0u;
+}
+
+// The bits of the largest finite magnitude in `count` pieces of 8 elements, `step`
+// pieces apart. Magnitudes are ordered as integers, two to a word; infinities and NaN
+// (rare) show in the maximum and are then left out one by one.
+template <bool BF16>
+__device__ __forceinline__ uint32_t largest_finite16(const uint4* p, int count, int step) {
+  uint32_t pair = 0;
+#pragma unroll 4
+  for (int i = 0; i < count; ++i) {
+    const uint4 v = p[i * step];
+    pair = __vmaxu2(__vmaxu2(pair, v.x & 0x7FFF7FFFu),
+                    __vmaxu2(v.y & 0x7FFF7FFFu, __vmaxu2(v.z & 0x7FFF7FFFu, v.w & 0x7FFF7FFFu)));
+  }
+  uint32_t m = max(pair & 0xFFFFu, pair >> 16);
+  if (finite_or_0<BF16>(m) != m) {
+    m = 0;
+#pragma unroll 1
+    for (int i = 0; i < count * 4; ++i) {
+      const uint32_t w = reinterpret_cast<const uint32_t*>(p + (i >> 2) * step)[i & 3] & 0x7FFF7FFFu;
+      m = max(m, max(finite_or_0<BF16>(w), finite_or_0<BF16>(w >> 16)));
+    }
+  }
+  return m;
+}
+
+// The exponent of the power of two for largest magnitude bits m.
+template <bool BF16>
+__device__ __forceinline__ int shift_of_16(uint32_t m) {
+  const uint32_t mag = BF16 ? m << 16 : __float_as_uint(half_lo(m));
+  return mag == 0 ? 0 : min(126, max(-126, 141 - (int)(mag >> 23)));
+}
+
+// Pieces of 8 elements times `up`, as f16, in place. Four are read before the first is
+// written back: the compiler cannot know that a store hides no later load.
+template <bool BF16>
+__device__ __forceinline__ void scale_to_f16(uint4* p, int count, int step, float up) {
+  constexpr int kAtOnce = 4;
+#pragma unroll 1
+  for (int i = 0; i < count; i += kAtOnce) {
+    uint4 v[kAtOnce];
+#pragma unroll
+    for (int j = 0; j < kAtOnce; ++j)
+      if (i + j < count) v[j] = p[(i + j) * step];
+#pragma unroll
+    for (int j = 0; j < kAtOnce; ++j) {
+      float f[8];
+      unpack8<BF16>(v[j], f);
+      if (i + j < count)
+        p[(i + j) * step] = make_uint4(pack2<false>(f[0] * up, f[1] * up), pack2<false>(f[2] * up, f[3] * up),
+                                       pack2<false>(f[4] * up, f[5] * up), pack2<false>(f[6] * up, f[7] * up));
+    }
+  }
+}
+
+}  // namespace
 
 }  // namespace wd

@@ -95,20 +95,6 @@ __device__ __forceinline__ void pair_sync(int side) {
   asm volatile("bar.sync %0, 256;" ::"r"(side + 1 + kGroups) : "memory");
 }
 
-// The largest finite magnitude's bits of both halves of 16-bit pairs.
-template <bool BF16>
-__device__ __forceinline__ uint32_t finite_or_0(uint32_t m) {
-  constexpr uint32_t kInf = BF16 ? 0x7F80u : 0x7C00u;
-  return (m & 0xFFFFu) < kInf ? m & 0xFFFFu : 0u;
-}
-
-// The exponent of a token's power of two: its magnitude bits m come into [2^14, 2^15).
-template <bool BF16>
-__device__ __forceinline__ int token_shift(uint32_t m) {
-  const uint32_t mag = BF16 ? m << 16 : __float_as_uint(half_lo(m));
-  return mag == 0 ? 0 : min(126, max(-126, 141 - (int)(mag >> 23)));
-}
-
 // x of `toks` tokens (zero up to n), columns [128 c0, 128 c1) (zero from K on), as f16
 // times a power of two per token, K-major in the 128-byte swizzle: [64 columns][token]
 // [128 bytes], 16-byte unit u of a row at u ^ (token & 7). Copied as it is, then
@@ -137,45 +123,12 @@ __device__ __forceinline__ void stage(const MvArgs& a, int c0, int c1, int toks,
   const int tok = (threadIdx.x >> 3) & (n - 1);
   uint4* own = xs + (threadIdx.x >> 3) * 8 + (u ^ (tok & 7));  // and 512 units on
   const int mine = (rows - (int)(threadIdx.x >> 3) + kStep - 1) / kStep;
-  // magnitudes are ordered as integers, two to a word; infinities and NaN (rare) are
-  // seen in the maximum and left out one by one
-  uint32_t pair = 0, m = 0;
-#pragma unroll 4
-  for (int i = 0; i < mine; ++i) {
-    const uint4 v = own[i * kStep * 8];
-    pair = __vmaxu2(__vmaxu2(pair, v.x & 0x7FFF7FFFu), __vmaxu2(v.y & 0x7FFF7FFFu, __vmaxu2(v.z & 0x7FFF7FFFu, v.w & 0x7FFF7FFFu)));
-  }
-  m = max(pair & 0xFFFFu, pair >> 16);
-  if (finite_or_0<BF16>(m) != m) {
-    m = 0;
-#pragma unroll 1
-    for (int i = 0; i < mine * 4; ++i) {
-      const uint32_t w = reinterpret_cast<const uint32_t*>(own + (i >> 2) * kStep * 8)[i & 3] & 0x7FFF7FFFu;
-      m = max(m, max(finite_or_0<BF16>(w), finite_or_0<BF16>(w >> 16)));
-    }
-  }
+  uint32_t m = largest_finite16<BF16>(own, mine, kStep * 8);
 #pragma unroll
   for (int o = 1; o < 8; o <<= 1) m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
   if (u == 0) atomicMax(s_max + tok, m);
   __syncthreads();
-  const float up = exp2i(token_shift<BF16>(s_max[tok]));
-  constexpr int kAtOnce = 4;  // read before the first is written back: a store may hide no load
-#pragma unroll 1
-  for (int i = 0; i < mine; i += kAtOnce) {
-    uint4 v[kAtOnce];
-#pragma unroll
-    for (int j = 0; j < kAtOnce; ++j)
-      if (i + j < mine) v[j] = own[(i + j) * kStep * 8];
-#pragma unroll
-    for (int j = 0; j < kAtOnce; ++j) {
-      float f[8];
-      unpack8<BF16>(v[j], f);
-      if (i + j < mine)
-        own[(i + j) * kStep * 8] =
-            make_uint4(pack2<false>(f[0] * up, f[1] * up), pack2<false>(f[2] * up, f[3] * up),
-                       pack2<false>(f[4] * up, f[5] * up), pack2<false>(f[6] * up, f[7] * up));
-    }
-  }
+  scale_to_f16<BF16>(own, mine, kStep * 8, exp2i(shift_of_16<BF16>(s_max[tok])));
   // the tensor core reads through the asynchronous proxy
   asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
 }
@@ -257,7 +210,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) fp4_tc_kernel(const MvArgs a, i
     if (i < my_kt) load(buf[i], i);
 
   stage<BF16>(a, c0, c0 + kt, toks, n, xs, s_max);
-  if (tid < n) s_back[tid] = exp2i(-token_shift<BF16>(s_max[tid]));
+  if (tid < n) s_back[tid] = exp2i(-shift_of_16<BF16>(s_max[tid]));
   asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
   __syncthreads();
   asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
@@ -362,7 +315,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) fp4_tc_kernel(const MvArgs a, i
 #pragma unroll
             for (int k = 0; k < 8; ++k)
               if (j == k) v = __uint_as_float(d[k]) * back;
-            v = ldexpf(v, (int)top - 139 - token_shift<BF16>(s_max[c + j]));
+            v = ldexpf(v, (int)top - 139 - shift_of_16<BF16>(s_max[c + j]));
 #pragma unroll
             for (int k = 0; k < 8; ++k)
               if (j == k) o[k] = v;
@@ -398,17 +351,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) fp4_tc_kernel(const MvArgs a, i
         const float4 w = *reinterpret_cast<const float4*>(cluster.map_shared_rank(src, o));
         v.x += w.x, v.y += w.y, v.z += w.z, v.w += w.w;
       }
-      const int64_t row = (int64_t)(q + g) * kTcRows + r, at = (int64_t)(a.tok0 + tok) * a.ldy + row;
-      const float f[4] = {v.x, v.y, v.z, v.w};
-      if (row + 4 <= a.N && a.y_type != WD_F32 && at % 4 == 0 && (reinterpret_cast<uintptr_t>(a.y) & 7) == 0) {
-        const uint2 o = a.y_type == WD_BF16 ? make_uint2(pack2<true>(v.x, v.y), pack2<true>(v.z, v.w))
-                                            : make_uint2(pack2<false>(v.x, v.y), pack2<false>(v.z, v.w));
-        *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.y) + at) = o;
-      } else {
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-          if (row + j < a.N) store_elem(a.y, a.y_type, at + j, f[j]);
-      }
+      store_rows(a, a.tok0 + tok, (int64_t)(q + g) * kTcRows + r, v);
     }
     cluster.sync();  // the sums are written again, or their CTA leaves
   }
