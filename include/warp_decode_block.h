@@ -81,8 +81,8 @@ moe_status wd_fp4_matvec(const wd_fp4_shape* shape, const uint8_t* packed_codes,
  *   k_codes  [page_size][4 t][dim/32 blocks][4 bytes]: byte j of (t, b) holds
  *            elements 32b + 8t + 2j (low nibble), + 1 (high)
  *   k_scales [page_size][dim/32]
- *   v_codes  [page_size/2 pairs][8 g][2 keys][dim/32 blocks][2 bytes]: byte j of
- *            (g, key, b) holds elements 32b + 4g + 2j (low nibble), + 1 (high)
+ *   v_codes  [page_size/2 pairs][8 g][dim/32 blocks][4 bytes]: byte j of (g, b)
+ *            holds element 32b + 4g + j of key 2 pair (low nibble), 2 pair + 1 (high)
  *   v_scales [page_size/2 pairs][dim/32][2 keys]
  * Arrays [pages][heads][...], each 16-byte aligned. */
 typedef struct {

@@ -18,10 +18,15 @@ struct TokenArgs {
   int32_t pages, page_shift, heads;
 };
 
-// The place of new token `tok`: page and slot in the page. False for a token
-// that is ignored (behind cu[S]) or left out (flagged).
-__device__ __forceinline__ bool place_of(const TokenArgs& a, int tok, int& page, int& slot) {
-  int s = tok, first = tok;
+// The place of new token `tok`: page and slot in the page, and whether the tokens
+// before and behind it are new ones of its sequence too. False for a token that is
+// ignored (behind cu[S]) or left out (flagged).
+struct Place {
+  int page, slot;
+  bool before, behind;
+};
+__device__ __forceinline__ bool place_of(const TokenArgs& a, int tok, Place& p) {
+  int s = tok, first = tok, end = tok + 1;
   if (a.cu) {
     if (tok >= __ldg(a.cu + a.S) || tok < __ldg(a.cu)) return false;
     int lo = 0, hi = a.S - 1;  // the last s with cu[s] <= tok
@@ -34,14 +39,17 @@ __device__ __forceinline__ bool place_of(const TokenArgs& a, int tok, int& page,
     }
     s = lo;
     first = __ldg(a.cu + s);
+    end = min(__ldg(a.cu + s + 1), a.T);
   }
+  p.before = tok > first;
+  p.behind = tok + 1 < end;
   const int len = __ldg(a.lens + s);
   const int64_t pos = (int64_t)len + (tok - first);
   const int64_t block = pos >> a.page_shift;
-  page = -1;
-  if (len >= 0 && block < a.max_blocks) page = __ldg(a.table + (int64_t)s * a.max_blocks + block);
-  slot = (int)(pos & ((1 << a.page_shift) - 1));
-  if (page < 0 || page >= a.pages) {
+  p.page = -1;
+  if (len >= 0 && block < a.max_blocks) p.page = __ldg(a.table + (int64_t)s * a.max_blocks + block);
+  p.slot = (int)(pos & ((1 << a.page_shift) - 1));
+  if (p.page < 0 || p.page >= a.pages) {
     flag_invalid(a.err);
     return false;
   }
@@ -68,34 +76,56 @@ __global__ void __launch_bounds__(kThreads)
   int tok, head, b, t;
   item_of<D>(i, a.heads, tok, head, b, t);
   const unsigned quad = 0xFu << (threadIdx.x & 28);
-  int page, slot;
-  if (!place_of(a, tok, page, slot)) return;  // the same answer for the whole block
+  Place p;
+  if (!place_of(a, tok, p)) return;  // the same answer for the whole block
   const int e = head * D + 32 * b + 8 * t;
-  float f[2][8];
-  unpack8<BF16>(ld_cached16(k + tok * a.ldk + e), f[0]);
-  unpack8<BF16>(ld_cached16(v + tok * a.ldv + e), f[1]);
-  uint32_t code[2], scale[2];
-#pragma unroll
-  for (int p = 0; p < 2; ++p) {
+  const size_t at = ((size_t)p.page * a.heads + head) << a.page_shift;  // in tokens
+  // scale code of a block, and its elements times 2^-scale (0 in a NaN block)
+  auto scaled = [&](const uint16_t* src, float (&f)[8]) {
+    unpack8<BF16>(ld_cached16(src + e), f);
     uint32_t m = 0;
 #pragma unroll
-    for (int j = 0; j < 8; ++j) m = max(m, magnitude(f[p][j]));
+    for (int j = 0; j < 8; ++j) m = max(m, magnitude(f[j]));
     m = max(m, __shfl_xor_sync(quad, m, 1));
     m = max(m, __shfl_xor_sync(quad, m, 2));
-    scale[p] = fp4_scale_code(__uint_as_float(m));
-    const float u = fp4_unscale(scale[p]);
+    const uint32_t s = fp4_scale_code(__uint_as_float(m));
+    const float u = fp4_unscale(s);
 #pragma unroll
-    for (int j = 0; j < 8; ++j) f[p][j] = scale[p] == 255u ? 0.0f : f[p][j] * u;
-    code[p] = e2m1x8(f[p]);
+    for (int j = 0; j < 8; ++j) f[j] = s == 255u ? 0.0f : f[j] * u;
+    return s;
+  };
+  float f[8];
+  const uint32_t sk = scaled(k + tok * a.ldk, f);
+  *reinterpret_cast<uint32_t*>(kc + at * (D / 2) + k_word<D>(p.slot, t, b)) = e2m1x8(f);
+  if (t == 0) ks[at * (D / 32) + p.slot * (D / 32) + b] = (uint8_t)sk;
+
+  // V: a byte holds an element of an even key and the next, so one thread writes both:
+  // the even key's where both are new
+  const bool odd = p.slot & 1;
+  if (odd && p.before) return;
+  float pair[2][8];
+  const uint32_t sv = scaled(v + tok * a.ldv, f);
+  uint32_t next = 0;
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    pair[0][j] = odd ? 0.0f : f[j];
+    pair[1][j] = odd ? f[j] : 0.0f;
   }
-  const size_t at = ((size_t)page * a.heads + head) << a.page_shift;  // in tokens
-  *reinterpret_cast<uint32_t*>(kc + at * (D / 2) + k_word<D>(slot, t, b)) = code[0];
-  uint8_t* vp = vc + at * (D / 2) + v_half<D>(slot, 2 * t, b);
-  *reinterpret_cast<uint16_t*>(vp) = (uint16_t)code[1];
-  *reinterpret_cast<uint16_t*>(vp + D / 8) = (uint16_t)(code[1] >> 16);
+  if (!odd && p.behind) next = scaled(v + (int64_t)(tok + 1) * a.ldv, pair[1]);
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {  // elements 4h .. 4h + 3: g = 2t + h
+    const float both[8] = {pair[0][4 * h],     pair[1][4 * h],     pair[0][4 * h + 1], pair[1][4 * h + 1],
+                           pair[0][4 * h + 2], pair[1][4 * h + 2], pair[0][4 * h + 3], pair[1][4 * h + 3]};
+    uint32_t* to = reinterpret_cast<uint32_t*>(vc + at * (D / 2) + v_word<D>(p.slot >> 1, 2 * t + h, b));
+    const uint32_t w = e2m1x8(both);
+    *to = odd ? (*to & 0x0F0F0F0Fu) | (w & 0xF0F0F0F0u) : w;  // an odd key alone joins the key before
+  }
   if (t == 0) {
-    ks[at * (D / 32) + slot * (D / 32) + b] = (uint8_t)scale[0];
-    vs[at * (D / 32) + v_scale<D>(slot, b)] = (uint8_t)scale[1];
+    uint8_t* to = vs + at * (D / 32) + v_scale<D>(p.slot, b);
+    if (!odd && p.behind)
+      *reinterpret_cast<uint16_t*>(to) = (uint16_t)(sv | next << 8);
+    else
+      *to = (uint8_t)sv;
   }
 }
 
@@ -130,17 +160,21 @@ __global__ void __launch_bounds__(kThreads)
   if (i >= total) return;
   int tok, head, b, t;
   item_of<D>(i, a.heads, tok, head, b, t);
-  int page, slot;
-  if (!place_of(a, tok, page, slot)) return;
-  const size_t at = ((size_t)page * a.heads + head) << a.page_shift;
+  Place p;
+  if (!place_of(a, tok, p)) return;
+  const int slot = p.slot;
+  const size_t at = ((size_t)p.page * a.heads + head) << a.page_shift;
   const int e = head * D + 32 * b + 8 * t;
   uint32_t h[4];
   e2m1x8_to_f16(*reinterpret_cast<const uint32_t*>(kc + at * (D / 2) + k_word<D>(slot, t, b)), h);
   store8<TYPE>(k, tok * a.ldk + e, h, e8m0_to_f32(ks[at * (D / 32) + slot * (D / 32) + b]));
-  const uint8_t* vp = vc + at * (D / 2) + v_half<D>(slot, 2 * t, b);
-  const uint32_t w = *reinterpret_cast<const uint16_t*>(vp) |
-                     (uint32_t)*reinterpret_cast<const uint16_t*>(vp + D / 8) << 16;
-  e2m1x8_to_f16(w, h);
+  uint32_t pair[2][4];
+#pragma unroll
+  for (int i = 0; i < 2; ++i)
+    e2m1x8_to_f16(*reinterpret_cast<const uint32_t*>(vc + at * (D / 2) + v_word<D>(slot >> 1, 2 * t + i, b)), pair[i]);
+  const uint32_t pick = slot & 1 ? 0x7632 : 0x5410;  // the halves of an odd or an even key
+#pragma unroll
+  for (int i = 0; i < 4; ++i) h[i] = __byte_perm(pair[i >> 1][2 * (i & 1)], pair[i >> 1][2 * (i & 1) + 1], pick);
   store8<TYPE>(v, tok * a.ldv + e, h, e8m0_to_f32(vs[at * (D / 32) + v_scale<D>(slot, b)]));
 }
 

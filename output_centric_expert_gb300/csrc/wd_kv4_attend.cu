@@ -213,7 +213,7 @@ __device__ __forceinline__ void attend_keys(uint8_t* st, const uint8_t* qf, cons
                                             uint32_t on, State<D, NT>& s) {
   using L = Stage<D>;
   constexpr int NB = D / 32;     // scale blocks
-  constexpr int NWORD = D / 64;  // 4-byte words of a key's V codes in a lane; V scale words of a pair
+  constexpr int NWORD = D / 64;  // 4-byte words of a pair's V scales
   const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
   if (on != kAll) {  // what a masked key's V scales hold must not count
     if (!((on >> lane) & 1u)) {
@@ -355,38 +355,28 @@ __device__ __forceinline__ void attend_keys(uint8_t* st, const uint8_t* qf, cons
   }
 #pragma unroll
   for (int u = 0; u < 2; ++u) {
-    uint32_t v[2][2 * NWORD], sc[2][NWORD];  // pairs t and t + 4: k rows 2t, 2t + 1 and 8 more
+    uint32_t v[2][NB], sc[2][NWORD];  // pairs t and t + 4: k rows 2t, 2t + 1 and 8 more
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       lds(st + L::kV + u * L::kCodes + (t + 4 * h) * D + g * (D / 8), v[h]);
       lds(st + L::kVs + u * L::kScales + (t + 4 * h) * (D / 16), sc[h]);
     }
 #pragma unroll
-    for (int j = 0; j < NWORD; ++j) {
-      uint32_t even[2][4], odd[2][4], mult[2][2];
+    for (int b = 0; b < NB; ++b) {
+      uint32_t e[2][4], mult[2];
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        const uint32_t w0 = v[h][j], w1 = v[h][NWORD + j];
-        e2m1x8_to_f16((w0 & 0x0F0F0F0Fu) | ((w1 << 4) & 0xF0F0F0F0u), even[h]);
-        e2m1x8_to_f16(((w0 >> 4) & 0x0F0F0F0Fu) | (w1 & 0xF0F0F0F0u), odd[h]);
-#pragma unroll
-        for (int k = 0; k < 2; ++k) {  // block 2j + k
-          const uint32_t two = __byte_perm(sc[h][j], 0, k ? 0x4342 : 0x4140);  // codes of the two keys
-          // 2^(s - top + 9) as f16: exponent field s - top + 24, 0 where that is negative
-          mult[h][k] = __viaddmax_s16x2_relu(two, up[2 * j + k], 0u) << 10;
-        }
+        e2m1x8_to_f16(v[h][b], e[h]);  // e[h][i]: element i of both keys
+        const uint32_t two = __byte_perm(sc[h][b / 2], 0, b & 1 ? 0x4342 : 0x4140);  // codes of the two keys
+        // 2^(s - top + 9) as f16: exponent field s - top + 24, 0 where that is negative
+        mult[h] = __viaddmax_s16x2_relu(two, up[b], 0u) << 10;
       }
+      const uint32_t a0[4] = {e[0][0], e[0][1], e[1][0], e[1][1]}, a1[4] = {e[0][2], e[0][3], e[1][2], e[1][3]};
 #pragma unroll
-      for (int k = 0; k < 2; ++k) {
-        const uint32_t a0[4] = {even[0][2 * k], odd[0][2 * k], even[1][2 * k], odd[1][2 * k]};
-        const uint32_t a1[4] = {even[0][2 * k + 1], odd[0][2 * k + 1], even[1][2 * k + 1],
-                                odd[1][2 * k + 1]};
-#pragma unroll
-        for (int n = 0; n < NT; ++n) {
-          const uint32_t p0 = hmul2(p[u][n][0], mult[0][k]), p1 = hmul2(p[u][n][1], mult[1][k]);
-          mma_add(s.acc[n][2 * (2 * j + k)], a0, p0, p1);
-          mma_add(s.acc[n][2 * (2 * j + k) + 1], a1, p0, p1);
-        }
+      for (int n = 0; n < NT; ++n) {
+        const uint32_t p0 = hmul2(p[u][n][0], mult[0]), p1 = hmul2(p[u][n][1], mult[1]);
+        mma_add(s.acc[n][2 * b], a0, p0, p1);
+        mma_add(s.acc[n][2 * b + 1], a1, p0, p1);
       }
     }
   }

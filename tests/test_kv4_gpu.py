@@ -58,12 +58,12 @@ def _raw(cache):
     P, H, D, N = cache.page_size, cache.heads, cache.dim, cache.pages
     kc, ks, vc, vs = (t.cpu().numpy() for t in cache.tensors)
     kc = kc.reshape(N, H, P, 4, D // 32, 4)
-    vc = vc.reshape(N, H, P // 2, 8, 2, D // 32, 2)
+    vc = vc.reshape(N, H, P // 2, 8, D // 32, 4)
     slot, d = np.meshgrid(np.arange(P), np.arange(D), indexing="ij")
     kb = kc[:, :, slot, d % 32 // 8, d // 32, d % 8 // 2]
-    vb = vc[:, :, slot // 2, d % 32 // 4, slot % 2, d // 32, d % 4 // 2]
+    vb = vc[:, :, slot // 2, d % 32 // 4, d // 32, d % 4]
     vs = vs.reshape(N, H, P // 2, D // 32, 2).swapaxes(3, 4).reshape(N, H, P, D // 32)
-    return [ref.values((b >> (4 * (d % 2))) & 15, s) for b, s in ((kb, ks.reshape(N, H, P, D // 32)), (vb, vs))]
+    return [ref.values((b >> (4 * (n % 2))) & 15, s) for b, n, s in ((kb, d, ks.reshape(N, H, P, D // 32)), (vb, slot, vs))]
 
 
 @pytest.mark.parametrize("kind", ["bf16", "f16"])
@@ -112,6 +112,27 @@ def test_gather_reads_back_and_steps_extend(dim, page, out):
             want = np.concatenate([old, one[s:s + 1]])
             want = torch.from_numpy(want).to(TYPES[out]).double().numpy()
             assert np.array_equal(got[a:b].double().cpu().numpy(), want)
+
+
+@pytest.mark.parametrize("steps", [[1] * 9, [3, 1, 4, 1], [1, 2, 2, 4], [2, 7]])
+def test_steps_join_keys_that_share_bytes(steps):
+    """Two neighbouring keys' V share bytes: appended together or one by one, they are the same."""
+    rng = np.random.default_rng(len(steps))
+    cache = block_ops.Kv4Cache(4, 16, 2, 128)
+    for t in cache.tensors:
+        t.fill_(255)
+    k, v = (torch.from_numpy(rng.standard_normal((2, 9, 2, 128)).astype(np.float32)).cuda().to(torch.bfloat16) for _ in range(2))
+    table = torch.tensor([[2], [1]], dtype=torch.int32, device="cuda")
+    at = 0
+    for n in steps:
+        cu = torch.tensor([0, n, 2 * n], dtype=torch.int32, device="cuda")
+        lens = torch.full((2,), at, dtype=torch.int32, device="cuda")
+        block_ops.wd_kv4_append(cache, k[:, at:at + n].reshape(2 * n, 2, 128), v[:, at:at + n].reshape(2 * n, 2, 128), table, lens, cu)
+        at += n
+    got_k, got_v = _raw(cache)
+    for s, page in enumerate((2, 1)):
+        assert np.array_equal(got_k[page].swapaxes(0, 1)[:9], ref.rounded(k[s].double().cpu().numpy()))
+        assert np.array_equal(got_v[page].swapaxes(0, 1)[:9], ref.rounded(v[s].double().cpu().numpy()))
 
 
 def test_special_blocks():
