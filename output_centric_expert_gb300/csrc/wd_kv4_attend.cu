@@ -39,7 +39,8 @@ constexpr float kLift = 2.0f;   // probabilities are held times 2^2
 constexpr float kSlack = 4.0f;  // and may be 2^4 above their reference: 2^6, times 2^9 at most, fits f16
 
 constexpr int kMinTiles = 2;    // tiles of a CTA of a split row, on average
-constexpr int kRowUnits = 1;    // what a row costs beside its tiles, in tiles: CTAs share both out
+// What a row costs beside its tiles, in tiles: CTAs share both out.
+__host__ __device__ constexpr int row_units(int NT) { return NT == 2 ? 2 : 1; }
 
 // A row that begins in CTA c and goes on in the next: [c], parts 0 where there is none.
 struct __align__(16) Split {
@@ -427,11 +428,11 @@ struct Segment {
 template <int D, int NT, int W, int STAGES, int CTAS, bool BF16>
 __global__ void __launch_bounds__(W * 32, CTAS) kv4_attend_kernel(const AttendArgs a) {
   using L = Stage<D>;
-  constexpr int TILE = W * kWarpKeys, THREADS = W * 32;
+  constexpr int TILE = W * kWarpKeys, THREADS = W * 32, kRowUnits = row_units(NT);
   constexpr int NB = D / 32;
   constexpr int NH = NT * 8;           // heads of a tile
   constexpr int kPart = NH * (D + 2);  // floats of a partial result: acc [NH][D], m [NH], l [NH]
-  static_assert(8 * D * 4 <= L::kBytes && NH * D / 8 <= THREADS, "sums and query pieces");
+  static_assert(8 * D * 4 <= L::kBytes, "a warp's sums of 8 heads fit the stage they came from");
   extern __shared__ uint4 dyn4[];
   uint8_t* smem = reinterpret_cast<uint8_t*>(dyn4);
   __shared__ uint4 s_raw[2][NH * D / 8];  // two segments' queries as they are in memory
@@ -533,10 +534,10 @@ __global__ void __launch_bounds__(W * 32, CTAS) kv4_attend_kernel(const AttendAr
       if (lane == 0)
         s_seg[warp][slot] = {f_seq, kv * a.group + h0, nh, f_iters, kw, lo, hi, first == 0, last == f_tiles,
                              row0 + per - 1};
-      if (tid < NH * D / 8) {
-        const bool real = tid / (D / 8) < nh;
-        cp_async16(&s_raw[slot][tid],
-                   a.q + (int64_t)f_seq * a.ldq + (int64_t)(kv * a.group + h0) * D + (real ? tid * 8 : 0), real);
+      for (int i = tid; i < NH * D / 8; i += THREADS) {
+        const bool real = i / (D / 8) < nh;
+        cp_async16(&s_raw[slot][i],
+                   a.q + (int64_t)f_seq * a.ldq + (int64_t)(kv * a.group + h0) * D + (real ? i * 8 : 0), real);
       }
       ++f_segs;
       return true;
@@ -675,25 +676,31 @@ __global__ void __launch_bounds__(W * 32, CTAS) kv4_attend_kernel(const AttendAr
                           st.acc[n][2 * b + 1][c] * f, st.acc[n][2 * b + 1][2 + c] * f);
       }
       __syncthreads();
-      for (int i = tid * 4; i < 8 * D; i += THREADS * 4) {
-        const int h = n * 8 + i / D;
-        if (h >= sg.nh) break;
-        float m = s_m[0][h];
+      // 4 sums a thread; LW lanes have a head, and its warps' weights in their first W
+      constexpr int LW = D >= 128 ? 32 : 16;
+      static_assert(W <= LW, "a lane per warp's part");
+      for (int i0 = warp * 128; i0 < 8 * D; i0 += THREADS * 4) {
+        __syncwarp();
+        const int i = i0 + lane * 4, h = n * 8 + i / D, part_of = lane % LW;
+        const float pm = part_of < W ? s_m[part_of][h] : -INFINITY;
+        float m = pm;
 #pragma unroll
-        for (int w = 1; w < W; ++w) m = fmaxf(m, s_m[w][h]);
-        const float b = m == -INFINITY ? 0.0f : m;
-        float l = 0.0f;
+        for (int o = LW / 2; o >= 1; o >>= 1) m = fmaxf(m, __shfl_xor_sync(kAll, m, o));
+        const float b = m == -INFINITY ? 0.0f : m, f = exp2_fast(pm - b);
+        float l = part_of < W ? s_l[part_of][h] * f : 0.0f;
+#pragma unroll
+        for (int o = LW / 2; o >= 1; o >>= 1) l += __shfl_xor_sync(kAll, l, o);
         float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll
         for (int w = 0; w < W; ++w) {
           const float4 o = *reinterpret_cast<const float4*>(smem + (size_t)(w * STAGES + stage) * L::kBytes + i * 4);
-          const float f = exp2_fast(s_m[w][h] - b);
-          l = fmaf(s_l[w][h], f, l);
-          v.x = fmaf(o.x, f, v.x);
-          v.y = fmaf(o.y, f, v.y);
-          v.z = fmaf(o.z, f, v.z);
-          v.w = fmaf(o.w, f, v.w);
+          const float fw = __shfl_sync(kAll, f, w, LW);
+          v.x = fmaf(o.x, fw, v.x);
+          v.y = fmaf(o.y, fw, v.y);
+          v.z = fmaf(o.z, fw, v.z);
+          v.w = fmaf(o.w, fw, v.w);
         }
+        if (h >= sg.nh) continue;
         if (whole) {
           const float inv = 1.0f / l;
           *reinterpret_cast<uint2*>(orow + n * 8 * D + i) =
@@ -721,8 +728,10 @@ constexpr int kJoin = 256;
 template <int D, int NT, bool BF16>
 __global__ void __launch_bounds__(kJoin) kv4_join_kernel(const AttendArgs a) {
   constexpr int NH = NT * 8, kPart = NH * (D + 2), kHeads = kJoin / D < 1 ? 1 : kJoin / D;  // heads of a CTA's sums
-  __shared__ float s_max[4][kHeads], s_l[4][kHeads];
+  __shared__ float s_max[kHeads], s_l[kHeads];
   __shared__ float4 s_acc[4][kJoin / 4];
+  extern __shared__ float s_pm[];  // [parts][head]: maxima, then weights; behind them the sums
+  float* s_pl = s_pm + gridDim.x * kHeads;
   const int tid = threadIdx.x, quarter = tid >> 6, i = blockIdx.y * kJoin + (tid & 63) * 4;
   wait_prerequisite();
   const Split sp = a.split[blockIdx.x];
@@ -731,32 +740,47 @@ __global__ void __launch_bounds__(kJoin) kv4_join_kernel(const AttendArgs a) {
   const float* p1 = a.parts + (size_t)(blockIdx.x + 1) * 2 * kPart;  // of the others, 2 * kPart apart
   auto at = [&](int k) { return k == 0 ? p0 : p1 + (size_t)(k - 1) * 2 * kPart; };
   const bool real = i < sp.nh * D;
-  const int h = real ? i / D : 0;
+  const int hl = (tid & 63) * 4 / D, h0 = blockIdx.y * kJoin / D;  // the head among the CTA's, and their first
+  // the parts' maxima and sums, all of them in flight at once
   float m = -INFINITY;
-  for (int k = quarter; k < sp.parts; k += 4) m = fmaxf(m, __ldcg(at(k) + NH * D + h));
-  const int hl = (tid & 63) * 4 / D;  // the head among the CTA's
-  if ((tid & 63) * 4 % D == 0) s_max[quarter][hl] = m;
+  for (int k = tid; k < sp.parts * kHeads; k += kJoin) {
+    const int h = h0 + k % kHeads;
+    const float* src = at(k / kHeads) + NH * D + h;
+    const float pm = h < sp.nh ? __ldcg(src) : -INFINITY, pl = h < sp.nh ? __ldcg(src + NH) : 0.0f;
+    s_pm[k] = pm;
+    s_pl[k] = pl;
+  }
   __syncthreads();
-  m = fmaxf(fmaxf(s_max[0][hl], s_max[1][hl]), fmaxf(s_max[2][hl], s_max[3][hl]));
-  const float b = m == -INFINITY ? 0.0f : m;
-  float l = 0.0f;
+  if (tid < 32 * kHeads) {  // a warp per head: weights instead of maxima
+    const int hh = tid >> 5, lane = tid & 31;
+    for (int k = lane; k < sp.parts; k += 32) m = fmaxf(m, s_pm[k * kHeads + hh]);
+    m = warp_max(m);
+    const float b = m == -INFINITY ? 0.0f : m;
+    float l = 0.0f;
+    for (int k = lane; k < sp.parts; k += 32) {
+      const float f = exp2_fast(s_pm[k * kHeads + hh] - b);
+      s_pm[k * kHeads + hh] = f;
+      l = fmaf(s_pl[k * kHeads + hh], f, l);
+    }
+#pragma unroll
+    for (int o = 16; o >= 1; o >>= 1) l += __shfl_xor_sync(kAll, l, o);
+    if (lane == 0) {
+      s_max[hh] = b;
+      s_l[hh] = l;
+    }
+  }
+  __syncthreads();
   float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-  constexpr int kFlight = 8;  // parts in flight
+  constexpr int kFlight = 20;  // parts in flight per thread
   for (int k0 = quarter; k0 < sp.parts; k0 += 4 * kFlight) {
     float4 o[kFlight];
-    float om[kFlight], ol[kFlight];
+#pragma unroll
+    for (int k = 0; k < kFlight; ++k)
+      if (real && k0 + 4 * k < sp.parts) o[k] = __ldcg(reinterpret_cast<const float4*>(at(k0 + 4 * k) + i));
 #pragma unroll
     for (int k = 0; k < kFlight; ++k)
       if (real && k0 + 4 * k < sp.parts) {
-        o[k] = __ldcg(reinterpret_cast<const float4*>(at(k0 + 4 * k) + i));
-        om[k] = __ldcg(at(k0 + 4 * k) + NH * D + h);
-        ol[k] = __ldcg(at(k0 + 4 * k) + NH * D + NH + h);
-      }
-#pragma unroll
-    for (int k = 0; k < kFlight; ++k)
-      if (real && k0 + 4 * k < sp.parts) {
-        const float f = exp2_fast(om[k] - b);
-        l = fmaf(ol[k], f, l);
+        const float f = s_pm[(k0 + 4 * k) * kHeads + hl];
         v.x = fmaf(o[k].x, f, v.x);
         v.y = fmaf(o[k].y, f, v.y);
         v.z = fmaf(o[k].z, f, v.z);
@@ -764,10 +788,9 @@ __global__ void __launch_bounds__(kJoin) kv4_join_kernel(const AttendArgs a) {
       }
   }
   s_acc[quarter][tid & 63] = v;
-  if ((tid & 63) * 4 % D == 0) s_l[quarter][hl] = l;
   __syncthreads();
   if (quarter != 0 || !real) return;
-  l = (s_l[0][hl] + s_l[1][hl]) + (s_l[2][hl] + s_l[3][hl]);
+  const float l = s_l[hl], b = s_max[hl];
 #pragma unroll
   for (int k = 1; k < 4; ++k) {
     const float4 o = s_acc[k][tid & 63];
@@ -777,7 +800,7 @@ __global__ void __launch_bounds__(kJoin) kv4_join_kernel(const AttendArgs a) {
   uint16_t* orow = a.out + (int64_t)sp.seq * a.ldo + (int64_t)sp.head * D;
   *reinterpret_cast<uint2*>(orow + i) = make_uint2(pack2<BF16>(v.x * inv, v.y * inv), pack2<BF16>(v.z * inv, v.w * inv));
   if (a.lse && i % D == 0)
-    a.lse[(int64_t)sp.seq * a.heads * a.group + sp.head + h] = (b + log2f(l) - kLift) * 0.6931471805599453f;
+    a.lse[(int64_t)sp.seq * a.heads * a.group + sp.head + h0 + hl] = (b + log2f(l) - kLift) * 0.6931471805599453f;
 }
 
 // Heads of a tile: 8, or 16 where the group has more and the accumulators fit.
@@ -801,7 +824,7 @@ moe_status launch(const AttendArgs& a, bool bf16, cudaStream_t st) {
   const int64_t most = a.window > 0 && a.window + 2 * kWarpKeys < keys ? a.window + 2 * kWarpKeys : keys;
   const int64_t row_tiles = (most + W * kWarpKeys - 1) / (W * kWarpKeys);
   const int64_t tiles = row_tiles * a.S * a.heads * a.head_tiles;
-  if ((row_tiles + kRowUnits) * a.S * a.heads * a.head_tiles > 0x7FFFFFFF) return refuse(MOE_ERR_SHAPE, "wd_kv4_attend: block_table's capacity is too large");
+  if ((row_tiles + row_units(NT)) * a.S * a.heads * a.head_tiles > 0x7FFFFFFF) return refuse(MOE_ERR_SHAPE, "wd_kv4_attend: block_table's capacity is too large");
   const int64_t fill = (int64_t)sm_count() * CTAS;
   const unsigned grid = (unsigned)(tiles < fill ? tiles : fill);
   k<<<grid, W * 32, ring, st>>>(a);
@@ -813,6 +836,7 @@ moe_status launch(const AttendArgs& a, bool bf16, cudaStream_t st) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(grid, NT * 8 * D / kJoin);
   cfg.blockDim = dim3(kJoin);
+  cfg.dynamicSmemBytes = (size_t)grid * (kJoin / D < 1 ? 1 : kJoin / D) * 8;  // a maximum and a sum per part and head
   cfg.stream = st;
   cfg.attrs = &dependent;
   cfg.numAttrs = 1;
@@ -877,6 +901,6 @@ extern "C" moe_status wd_kv4_attend(const wd_kv4_cache* c, const void* q, int32_
   cudaStream_t st = (cudaStream_t)stream;
   const bool bf16 = type == WD_BF16, wide = tile_heads(c, group) == 16;
   if (c->dim == 64) return wide ? launch<64, 2, 8, 4, 2>(a, bf16, st) : launch<64, 1, 8, 4, 2>(a, bf16, st);
-  if (c->dim == 128) return wide ? launch<128, 2, 12, 4, 1>(a, bf16, st) : launch<128, 1, 8, 3, 2>(a, bf16, st);
-  return launch<256, 1, 8, 3, 1>(a, bf16, st);
+  if (c->dim == 128) return wide ? launch<128, 2, 6, 3, 2>(a, bf16, st) : launch<128, 1, 8, 3, 2>(a, bf16, st);
+  return launch<256, 1, 4, 2, 2>(a, bf16, st);
 }
