@@ -80,7 +80,7 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t v) {
 
 __device__ __forceinline__ float exp2_fast(float v) {
   float r;
-  asm("ex2.approx.f32 %0, %1;" : "=f"(r) : "f"(v));
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));  // below 2^-126: 0
   return r;
 }
 
