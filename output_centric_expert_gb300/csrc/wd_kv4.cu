@@ -6,9 +6,12 @@ namespace wd {
 namespace {
 
 // ------------------------------------------------------- append and gather --
-// One thread per 8 elements of one (token, head) of K and of V; the four
-// threads of a 32-element block are neighbours, so a block's largest magnitude
-// takes two shuffles. The sequence of a token is found by bisection in cu_new.
+// A CTA takes `per` tokens in a row and up to 128 of their 8-element pieces. Its first
+// threads find the tokens' places (sequence by bisection in cu_new, page, slot) once
+// for all. The four threads of a 32-element block are neighbours: its largest magnitude
+// takes two shuffles. Both kernels are bound by integer instructions (conversions,
+// packing, addresses), so magnitudes are compared as 16-bit pairs and a thread steps
+// through its pieces without divisions.
 
 struct TokenArgs {
   const int32_t *table, *lens, *cu;
@@ -16,19 +19,23 @@ struct TokenArgs {
   int64_t ldk, ldv;
   int32_t T, S, max_blocks;
   int32_t pages, page_shift, heads;
+  int32_t per, chunk;  // tokens of a CTA, pieces of a token in a CTA
 };
 
-// The place of new token `tok`: page and slot in the page, and whether the tokens
-// before and behind it are new ones of its sequence too. False for a token that is
-// ignored (behind cu[S]) or left out (flagged).
+// The place of a new token; `before`, `behind`: the tokens next to it are new ones of
+// its sequence too. page -1: ignored (behind cu[S]) or left out (flagged).
 struct Place {
-  int page, slot;
+  int32_t page, slot;
   bool before, behind;
 };
-__device__ __forceinline__ bool place_of(const TokenArgs& a, int tok, Place& p) {
+constexpr int kMostPer = 64;
+
+__device__ __forceinline__ Place place_of(const TokenArgs& a, int tok, bool flag) {
+  Place p = {-1, 0, false, false};
   int s = tok, first = tok, end = tok + 1;
+  if (tok >= a.T) return p;
   if (a.cu) {
-    if (tok >= __ldg(a.cu + a.S) || tok < __ldg(a.cu)) return false;
+    if (tok >= __ldg(a.cu + a.S) || tok < __ldg(a.cu)) return p;
     int lo = 0, hi = a.S - 1;  // the last s with cu[s] <= tok
     while (lo < hi) {
       const int mid = (lo + hi + 1) >> 1;
@@ -46,86 +53,110 @@ __device__ __forceinline__ bool place_of(const TokenArgs& a, int tok, Place& p) 
   const int len = __ldg(a.lens + s);
   const int64_t pos = (int64_t)len + (tok - first);
   const int64_t block = pos >> a.page_shift;
-  p.page = -1;
   if (len >= 0 && block < a.max_blocks) p.page = __ldg(a.table + (int64_t)s * a.max_blocks + block);
   p.slot = (int)(pos & ((1 << a.page_shift) - 1));
   if (p.page < 0 || p.page >= a.pages) {
-    flag_invalid(a.err);
-    return false;
+    p.page = -1;
+    if (flag) flag_invalid(a.err);
   }
-  return true;
+  return p;
 }
 
-template <int D>
-__device__ __forceinline__ void item_of(int64_t i, int heads, int& tok, int& head, int& b, int& t) {
-  const int w = (int)(i % (D / 8));
-  const int64_t th = i / (D / 8);
-  head = (int)(th % heads);
-  tok = (int)(th / heads);
-  b = w >> 2;
-  t = w & 3;
+// The (token, piece) of a thread's i-th item, i = threadIdx.x, + kThreads, ...
+struct Walk {
+  int i, j, w;
+  const int chunk, dj, dw;
+  __device__ explicit Walk(int c)
+      : i(threadIdx.x), j(threadIdx.x / c), w(threadIdx.x - threadIdx.x / c * c), chunk(c), dj(kThreads / c),
+        dw(kThreads - kThreads / c * c) {}
+  __device__ void next() {
+    i += kThreads;
+    j += dj;
+    w += dw;
+    if (w >= chunk) {
+      w -= chunk;
+      ++j;
+    }
+  }
+};
+
+// Four E2M1 codes (the low 16 bits) to the low nibbles of four bytes.
+__device__ __forceinline__ uint32_t spread4(uint32_t x) {
+  const uint32_t t = __byte_perm(x, 0, 0x4140);  // byte 0 and byte 1 to the halves
+  return (t & 0x000F000Fu) | ((t << 4) & 0x0F000F00u);
 }
 
 template <int D, bool BF16>
 __global__ void __launch_bounds__(kThreads)
     kv4_append_kernel(const uint16_t* __restrict__ k, const uint16_t* __restrict__ v,
                       uint8_t* __restrict__ kc, uint8_t* __restrict__ ks, uint8_t* __restrict__ vc,
-                      uint8_t* __restrict__ vs, const TokenArgs a, int64_t total) {
-  const int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x;
-  if (i >= total) return;  // total % (D / 8) == 0: the four threads of a block leave together
-  int tok, head, b, t;
-  item_of<D>(i, a.heads, tok, head, b, t);
-  const unsigned quad = 0xFu << (threadIdx.x & 28);
-  Place p;
-  if (!place_of(a, tok, p)) return;  // the same answer for the whole block
-  const int e = head * D + 32 * b + 8 * t;
-  const size_t at = ((size_t)p.page * a.heads + head) << a.page_shift;  // in tokens
-  // scale code of a block, and its elements times 2^-scale (0 in a NaN block)
-  auto scaled = [&](const uint16_t* src, float (&f)[8]) {
-    unpack8<BF16>(ld_cached16(src + e), f);
-    uint32_t m = 0;
-#pragma unroll
-    for (int j = 0; j < 8; ++j) m = max(m, magnitude(f[j]));
+                      uint8_t* __restrict__ vs, const TokenArgs a) {
+  __shared__ Place s_place[kMostPer + 1];
+  extern __shared__ uint32_t s_code[];  // V's codes: [per + 1 tokens][chunk]; scale codes behind
+  uint8_t* s_scale = reinterpret_cast<uint8_t*>(s_code + (a.per + 1) * a.chunk);
+  const int tok0 = blockIdx.x * a.per, w0 = blockIdx.y * a.chunk, tid = threadIdx.x;
+  if (tid <= a.per) s_place[tid] = place_of(a, tok0 + tid, tid < a.per);
+  __syncthreads();
+  // the scale code of a piece's block, and its codes
+  auto quantise = [&](const uint16_t* src, unsigned quad, uint32_t& scale) {
+    const uint4 raw = ld_cached16(src);
+    // magnitudes as 16-bit integers, two to a word (NaN above infinity above the rest)
+    const uint32_t two = __vmaxu2(__vmaxu2(raw.x & 0x7FFF7FFFu, raw.y & 0x7FFF7FFFu),
+                                  __vmaxu2(raw.z & 0x7FFF7FFFu, raw.w & 0x7FFF7FFFu));
+    uint32_t m = max(two & 0xFFFFu, two >> 16);
     m = max(m, __shfl_xor_sync(quad, m, 1));
     m = max(m, __shfl_xor_sync(quad, m, 2));
-    const uint32_t s = fp4_scale_code(__uint_as_float(m));
-    const float u = fp4_unscale(s);
+    float f[8];
+    unpack8<BF16>(raw, f);
+    scale = fp4_scale_code(BF16 ? __uint_as_float(m << 16) : half_lo(m));
+    const float u = fp4_unscale(scale);  // (the codes of a NaN block, whose u is 0, do not matter)
 #pragma unroll
-    for (int j = 0; j < 8; ++j) f[j] = s == 255u ? 0.0f : f[j] * u;
-    return s;
+    for (int j = 0; j < 8; ++j) f[j] *= u;
+    return e2m1x8(f);
   };
-  float f[8];
-  const uint32_t sk = scaled(k + tok * a.ldk, f);
-  *reinterpret_cast<uint32_t*>(kc + at * (D / 2) + k_word<D>(p.slot, t, b)) = e2m1x8(f);
-  if (t == 0) ks[at * (D / 32) + p.slot * (D / 32) + b] = (uint8_t)sk;
-
+  const unsigned quad = 0xFu << (tid & 28);
+  // the token behind the last may share bytes with it
+  for (Walk walk(a.chunk); walk.j <= a.per; walk.next()) {
+    const int i = walk.i, j = walk.j, w = w0 + walk.w;
+    const Place p = s_place[j];
+    if (p.page < 0) continue;  // the four threads of a block alike
+    const int head = w / (D / 8), b = w % (D / 8) >> 2, t = w & 3;
+    const int64_t tok = tok0 + j;
+    uint32_t sv;
+    s_code[i] = quantise(v + tok * a.ldv + w * 8, quad, sv);
+    if (t == 0) s_scale[i >> 2] = (uint8_t)sv;
+    if (j == a.per) continue;
+    uint32_t sk;
+    const uint32_t code = quantise(k + tok * a.ldk + w * 8, quad, sk);
+    const size_t at = ((size_t)p.page * a.heads + head) << a.page_shift;  // in tokens
+    *reinterpret_cast<uint32_t*>(kc + at * (D / 2) + k_word<D>(p.slot, t, b)) = code;
+    if (t == 0) ks[at * (D / 32) + p.slot * (D / 32) + b] = (uint8_t)sk;
+  }
+  __syncthreads();
   // V: a byte holds an element of an even key and the next, so one thread writes both:
   // the even key's where both are new
-  const bool odd = p.slot & 1;
-  if (odd && p.before) return;
-  float pair[2][8];
-  const uint32_t sv = scaled(v + tok * a.ldv, f);
-  uint32_t next = 0;
+  for (Walk walk(a.chunk); walk.j < a.per; walk.next()) {
+    const int i = walk.i, j = walk.j, w = w0 + walk.w;
+    const Place p = s_place[j];
+    const bool odd = p.slot & 1;
+    if (p.page < 0 || (odd && p.before)) continue;
+    const int head = w / (D / 8), b = w % (D / 8) >> 2, t = w & 3;
+    const size_t at = ((size_t)p.page * a.heads + head) << a.page_shift;
+    const bool both = !odd && p.behind;
+    const uint32_t even = odd ? 0u : s_code[i], next = odd ? s_code[i] : both ? s_code[i + a.chunk] : 0u;
 #pragma unroll
-  for (int j = 0; j < 8; ++j) {
-    pair[0][j] = odd ? 0.0f : f[j];
-    pair[1][j] = odd ? f[j] : 0.0f;
-  }
-  if (!odd && p.behind) next = scaled(v + (int64_t)(tok + 1) * a.ldv, pair[1]);
-#pragma unroll
-  for (int h = 0; h < 2; ++h) {  // elements 4h .. 4h + 3: g = 2t + h
-    const float both[8] = {pair[0][4 * h],     pair[1][4 * h],     pair[0][4 * h + 1], pair[1][4 * h + 1],
-                           pair[0][4 * h + 2], pair[1][4 * h + 2], pair[0][4 * h + 3], pair[1][4 * h + 3]};
-    uint32_t* to = reinterpret_cast<uint32_t*>(vc + at * (D / 2) + v_word<D>(p.slot >> 1, 2 * t + h, b));
-    const uint32_t w = e2m1x8(both);
-    *to = odd ? (*to & 0x0F0F0F0Fu) | (w & 0xF0F0F0F0u) : w;  // an odd key alone joins the key before
-  }
-  if (t == 0) {
-    uint8_t* to = vs + at * (D / 32) + v_scale<D>(p.slot, b);
-    if (!odd && p.behind)
-      *reinterpret_cast<uint16_t*>(to) = (uint16_t)(sv | next << 8);
-    else
-      *to = (uint8_t)sv;
+    for (int h = 0; h < 2; ++h) {  // elements 4h .. 4h + 3: g = 2t + h
+      uint32_t* to = reinterpret_cast<uint32_t*>(vc + at * (D / 2) + v_word<D>(p.slot >> 1, 2 * t + h, b));
+      const uint32_t x = spread4(even >> (16 * h)) | spread4(next >> (16 * h)) << 4;
+      *to = odd ? (*to & 0x0F0F0F0Fu) | x : x;  // an odd key alone joins the key before
+    }
+    if (t == 0) {
+      uint8_t* to = vs + at * (D / 32) + v_scale<D>(p.slot, b);
+      if (both)
+        *reinterpret_cast<uint16_t*>(to) = (uint16_t)(s_scale[i >> 2] | s_scale[(i + a.chunk) >> 2] << 8);
+      else
+        *to = s_scale[i >> 2];
+    }
   }
 }
 
@@ -155,27 +186,34 @@ template <int D, int TYPE>
 __global__ void __launch_bounds__(kThreads)
     kv4_gather_kernel(void* __restrict__ k, void* __restrict__ v, const uint8_t* __restrict__ kc,
                       const uint8_t* __restrict__ ks, const uint8_t* __restrict__ vc,
-                      const uint8_t* __restrict__ vs, const TokenArgs a, int64_t total) {
-  const int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x;
-  if (i >= total) return;
-  int tok, head, b, t;
-  item_of<D>(i, a.heads, tok, head, b, t);
-  Place p;
-  if (!place_of(a, tok, p)) return;
-  const int slot = p.slot;
-  const size_t at = ((size_t)p.page * a.heads + head) << a.page_shift;
-  const int e = head * D + 32 * b + 8 * t;
-  uint32_t h[4];
-  e2m1x8_to_f16(*reinterpret_cast<const uint32_t*>(kc + at * (D / 2) + k_word<D>(slot, t, b)), h);
-  store8<TYPE>(k, tok * a.ldk + e, h, e8m0_to_f32(ks[at * (D / 32) + slot * (D / 32) + b]));
-  uint32_t pair[2][4];
+                      const uint8_t* __restrict__ vs, const TokenArgs a) {
+  __shared__ Place s_place[kMostPer];
+  const int tok0 = blockIdx.x * a.per, w0 = blockIdx.y * a.chunk, tid = threadIdx.x;
+  if (tid < a.per) s_place[tid] = place_of(a, tok0 + tid, true);
+  __syncthreads();
+  for (Walk walk(a.chunk); walk.j < a.per; walk.next()) {
+    const int j = walk.j, w = w0 + walk.w;
+    const Place p = s_place[j];
+    if (p.page < 0) continue;
+    const int head = w / (D / 8), b = w % (D / 8) >> 2, t = w & 3, slot = p.slot;
+    const int64_t tok = tok0 + j;
+    const size_t at = ((size_t)p.page * a.heads + head) << a.page_shift;
+    uint32_t h[4], pair[2][4];
+    const uint32_t kw = *reinterpret_cast<const uint32_t*>(kc + at * (D / 2) + k_word<D>(slot, t, b));
+    uint32_t vw[2];
 #pragma unroll
-  for (int i = 0; i < 2; ++i)
-    e2m1x8_to_f16(*reinterpret_cast<const uint32_t*>(vc + at * (D / 2) + v_word<D>(slot >> 1, 2 * t + i, b)), pair[i]);
-  const uint32_t pick = slot & 1 ? 0x7632 : 0x5410;  // the halves of an odd or an even key
+    for (int n = 0; n < 2; ++n)
+      vw[n] = *reinterpret_cast<const uint32_t*>(vc + at * (D / 2) + v_word<D>(slot >> 1, 2 * t + n, b));
+    const uint32_t sk = ks[at * (D / 32) + slot * (D / 32) + b], sv = vs[at * (D / 32) + v_scale<D>(slot, b)];
+    e2m1x8_to_f16(kw, h);
+    store8<TYPE>(k, tok * a.ldk + w * 8, h, e8m0_to_f32(sk));
+    const uint32_t pick = slot & 1 ? 0x7632 : 0x5410;  // the halves of an odd or an even key
 #pragma unroll
-  for (int i = 0; i < 4; ++i) h[i] = __byte_perm(pair[i >> 1][2 * (i & 1)], pair[i >> 1][2 * (i & 1) + 1], pick);
-  store8<TYPE>(v, tok * a.ldv + e, h, e8m0_to_f32(vs[at * (D / 32) + v_scale<D>(slot, b)]));
+    for (int n = 0; n < 2; ++n) e2m1x8_to_f16(vw[n], pair[n]);
+#pragma unroll
+    for (int n = 0; n < 4; ++n) h[n] = __byte_perm(pair[n >> 1][2 * (n & 1)], pair[n >> 1][2 * (n & 1) + 1], pick);
+    store8<TYPE>(v, tok * a.ldv + w * 8, h, e8m0_to_f32(sv));
+  }
 }
 
 moe_status check_tokens(const wd_kv4_cache* c, const void* k, const void* v, int32_t type,
@@ -204,33 +242,45 @@ moe_status check_tokens(const wd_kv4_cache* c, const void* k, const void* v, int
 TokenArgs token_args(const wd_kv4_cache* c, int64_t ldk, int64_t ldv, int32_t T,
                      const int32_t* table, int32_t max_blocks, const int32_t* lens,
                      const int32_t* cu, int32_t S, int32_t* err) {
+  const int piece = c->dim / 8, words = c->heads * piece;  // 8-element pieces of a head, of a token
+  int h = 128 / piece < c->heads ? 128 / piece : c->heads;  // heads of a CTA
+  while (c->heads % h) --h;
+  const int chunk = h * piece;
+  // as many tokens per CTA as leave two CTAs per SM, up to 4 pieces a thread
+  int per = 2;
+  while (per < kMostPer && 2 * per * chunk <= 4 * kThreads &&
+         (int64_t)T * words >= 2ll * sm_count() * 2 * per * chunk)
+    per *= 2;
   return {table, lens, cu, err, ldk, ldv, T, S, max_blocks, c->pages, kv4_page_shift(c->page_size),
-          c->heads};
+          c->heads, per, chunk};
+}
+
+// The grid: runs of tokens, and pieces of a token in chunks of whole heads.
+dim3 token_grid(const TokenArgs& a, int words) {
+  return dim3((unsigned)((a.T + a.per - 1) / a.per), (unsigned)(words / a.chunk));
 }
 
 template <int D>
 moe_status append(const wd_kv4_cache* c, const void* k, const void* v, int32_t type,
                   const TokenArgs& a, cudaStream_t st) {
-  const int64_t total = (int64_t)a.T * a.heads * (D / 8);
-  const unsigned grid = (unsigned)((total + kThreads - 1) / kThreads);
+  const dim3 grid = token_grid(a, a.heads * (D / 8));
+  const size_t smem = (size_t)(a.per + 1) * a.chunk * 4 + (size_t)(a.per + 1) * a.chunk / 4;
   const uint16_t *k16 = static_cast<const uint16_t*>(k), *v16 = static_cast<const uint16_t*>(v);
   if (type == WD_BF16)
-    kv4_append_kernel<D, true><<<grid, kThreads, 0, st>>>(k16, v16, c->k_codes, c->k_scales,
-                                                          c->v_codes, c->v_scales, a, total);
+    kv4_append_kernel<D, true><<<grid, kThreads, smem, st>>>(k16, v16, c->k_codes, c->k_scales,
+                                                             c->v_codes, c->v_scales, a);
   else
-    kv4_append_kernel<D, false><<<grid, kThreads, 0, st>>>(k16, v16, c->k_codes, c->k_scales,
-                                                           c->v_codes, c->v_scales, a, total);
+    kv4_append_kernel<D, false><<<grid, kThreads, smem, st>>>(k16, v16, c->k_codes, c->k_scales,
+                                                              c->v_codes, c->v_scales, a);
   return launched("wd_kv4_append launch");
 }
 
 template <int D>
 moe_status gather(const wd_kv4_cache* c, void* k, void* v, int32_t type, const TokenArgs& a,
                   cudaStream_t st) {
-  const int64_t total = (int64_t)a.T * a.heads * (D / 8);
-  const unsigned grid = (unsigned)((total + kThreads - 1) / kThreads);
+  const dim3 grid = token_grid(a, a.heads * (D / 8));
   auto run = [&](auto kernel) {
-    kernel<<<grid, kThreads, 0, st>>>(k, v, c->k_codes, c->k_scales, c->v_codes, c->v_scales, a,
-                                      total);
+    kernel<<<grid, kThreads, 0, st>>>(k, v, c->k_codes, c->k_scales, c->v_codes, c->v_scales, a);
   };
   if (type == WD_F32)
     run(kv4_gather_kernel<D, WD_F32>);

@@ -69,7 +69,7 @@ def _raw(cache):
 @pytest.mark.parametrize("kind", ["bf16", "f16"])
 @pytest.mark.parametrize("lens,heads,dim,page", [
     ([1], 1, 64, 16), ([5, 0, 33, 16], 2, 128, 16), ([70, 1, 64], 3, 256, 32), ([300, 129], 1, 128, 128),
-    ([257], 5, 64, 256), ([63, 65], 2, 128, 64)])
+    ([257], 5, 64, 256), ([63, 65], 2, 128, 64), ([31, 18], 17, 64, 16), ([9, 40], 9, 256, 32)])
 def test_append_writes_the_documented_layout(lens, heads, dim, page, kind):
     f = Filled(lens, heads, dim, page, kind)
     k, v = _raw(f.cache)
