@@ -19,7 +19,7 @@ is the seeded synthetic input generator. Importing this package loads nothing
 native: the CUDA library is built/loaded on first use and any failure raises.
 """
 
-__all__ = ["ops", "block_ops", "workload"]
+__all__ = ["ops", "block_ops", "decoder_layer", "workload"]
 
 
 def __getattr__(name):
