@@ -24,6 +24,7 @@ __all__ = ["Fp4Weights", "Kv4Cache", "kv4_workspace", "wd_fp4_matvec", "wd_kv4_a
            "wd_kv4_attend", "wd_block_norm", "exported_symbols"]
 
 _TYPES = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
+_raw_stream = torch._C._cuda_getCurrentRawStream  # torch.cuda.current_stream() without its Python object
 
 
 class Fp4Shape(ctypes.Structure):
@@ -83,7 +84,7 @@ def _check(fn: str, status: int) -> None:
 
 def _stream(stream, t: torch.Tensor) -> int | None:
     if stream is None:
-        return torch._C._cuda_getCurrentRawStream(t.get_device()) if t.is_cuda else None
+        return _raw_stream(t.get_device()) if t.is_cuda else None
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else stream
 
 
@@ -108,20 +109,16 @@ def _rows(t: torch.Tensor, shape: tuple, row: int, name: str) -> int:
     return t.stride(0)
 
 
-def _ints(t: torch.Tensor | None, shape: tuple, name: str) -> int | None:
-    if t is None:
-        return None
-    if t.dtype != torch.int32:
+def _ints(t: torch.Tensor, shape: tuple, name: str) -> int:
+    if t.dtype is not torch.int32:
         raise TypeError(f"{name}: dtype {t.dtype} is not int32")
     if t.shape != shape or not t.is_contiguous():
         raise ValueError(f"{name}: expected a contiguous tensor of shape {tuple(shape)}, got {tuple(t.shape)}")
     return t.data_ptr()
 
 
-def _flag(t: torch.Tensor | None) -> int | None:
-    if t is None:
-        return None
-    if t.dtype != torch.int32:
+def _flag(t: torch.Tensor) -> int:
+    if t.dtype is not torch.int32:
         raise TypeError(f"err_flag: dtype {t.dtype} is not int32")
     return t.data_ptr()
 
@@ -202,16 +199,17 @@ class Kv4Cache:
         return sum(t.numel() for t in self.tensors)
 
 
-def _tokens(fn: str, cache: Kv4Cache, k, v, block_table, seq_lens, cu_new, err_flag, stream) -> None:
+def _tokens(fn: str, call, cache: Kv4Cache, k, v, block_table, seq_lens, cu_new, err_flag, stream) -> None:
     T, S, blocks = k.shape[0], seq_lens.shape[0], block_table.shape[-1]
     if v.dtype != k.dtype:
         raise TypeError(f"v: dtype {v.dtype} differs from k's {k.dtype}")
     row = cache.heads * cache.dim
     shape = (T, cache.heads, cache.dim)
-    status = getattr(_lib_cache, fn)(
+    status = call(
         cache._ref, k.data_ptr(), v.data_ptr(), _type(k, "k"), _rows(k, shape, row, "k"), _rows(v, shape, row, "v"), T,
         _ints(block_table, (S, blocks), "block_table"), blocks, _ints(seq_lens, (S,), "seq_lens"),
-        _ints(cu_new, (S + 1,), "cu_new"), S, _flag(err_flag), _stream(stream, k))
+        None if cu_new is None else _ints(cu_new, (S + 1,), "cu_new"), S,
+        None if err_flag is None else _flag(err_flag), _stream(stream, k))
     if status:
         _check(fn, status)
 
@@ -221,7 +219,7 @@ def wd_kv4_append(cache: Kv4Cache, k: torch.Tensor, v: torch.Tensor, block_table
                   err_flag: torch.Tensor | None = None, stream=None) -> Kv4Cache:
     """Quantise the new tokens k, v [T, heads, dim] into the cache behind seq_lens[s] tokens of each
     sequence; cu_new [S + 1] says which rows are whose (None: one each)."""
-    _tokens("wd_kv4_append", cache, k, v, block_table, seq_lens, cu_new, err_flag, stream)
+    _tokens("wd_kv4_append", _lib_cache.wd_kv4_append, cache, k, v, block_table, seq_lens, cu_new, err_flag, stream)
     return cache
 
 
@@ -229,7 +227,7 @@ def wd_kv4_gather(cache: Kv4Cache, block_table: torch.Tensor, seq_lens: torch.Te
                   v_out: torch.Tensor, cu_new: torch.Tensor | None = None,
                   err_flag: torch.Tensor | None = None, stream=None):
     """The values of the positions that wd_kv4_append with the same arguments writes."""
-    _tokens("wd_kv4_gather", cache, k_out, v_out, block_table, seq_lens, cu_new, err_flag, stream)
+    _tokens("wd_kv4_gather", _lib_cache.wd_kv4_gather, cache, k_out, v_out, block_table, seq_lens, cu_new, err_flag, stream)
     return k_out, v_out
 
 
@@ -258,8 +256,8 @@ def wd_kv4_attend(cache: Kv4Cache, q: torch.Tensor, block_table: torch.Tensor, s
         cache._ref, q.data_ptr(), _type(q, "q"), _rows(q, shape, row, "q"), S, q_heads,
         _ints(block_table, (S, blocks), "block_table"), blocks, _ints(seq_lens, (S,), "seq_lens"),
         D ** -0.5 if scale is None else scale, window, out.data_ptr(), _rows(out, shape, row, "out"),
-        None if lse is None else lse.data_ptr(), workspace.data_ptr(), workspace.nbytes, _flag(err_flag),
-        _stream(stream, q))
+        None if lse is None else lse.data_ptr(), workspace.data_ptr(), workspace.nbytes,
+        None if err_flag is None else _flag(err_flag), _stream(stream, q))
     if status:
         _check("wd_kv4_attend", status)
     return out
@@ -267,11 +265,11 @@ def wd_kv4_attend(cache: Kv4Cache, q: torch.Tensor, block_table: torch.Tensor, s
 
 # ---------------------------------------------------------------- block norms --
 
-def _weight(w: torch.Tensor, H: int, first: torch.Tensor, name: str) -> int:
-    if w.shape != (H,) or not w.is_contiguous():
-        raise ValueError(f"{name}: expected contiguous [{H}], got {tuple(w.shape)}")
-    if w.dtype != first.dtype:
+def _weight(w: torch.Tensor, H: int, kind: torch.dtype, name: str) -> int:
+    if w.dtype is not kind:
         raise TypeError("w_post, w_pre and gate must have one dtype")
+    if w.dim() != 1 or w.shape[0] != H or not w.is_contiguous():
+        raise ValueError(f"{name}: expected contiguous [{H}], got {tuple(w.shape)}")
     return w.data_ptr()
 
 
@@ -282,18 +280,17 @@ def wd_block_norm(res: torch.Tensor, res_out: torch.Tensor | None = None, out: t
     """r' = res_scale * res + gate * norm(y; w_post) into res_out, norm(r'; w_pre) into out: the step
     between two blocks. gate broadcasts from [1 or T, 1 or H]. Returns (res_out, out)."""
     T, H = shape = res.shape
-    w_type = 0
-    first = w_pre if w_pre is not None else w_post if w_post is not None else gate
-    if first is not None:
-        w_type = _type(first, "w_post, w_pre and gate")
-    pp = qp = gp = yp = rp = op = None
+    pp = qp = gp = yp = rp = op = kind = None
     gate_ld = gate_step = yt = yl = rl = ot = ol = 0
-    if w_post is not None:
-        pp = _weight(w_post, H, first, "w_post")
     if w_pre is not None:
-        qp = _weight(w_pre, H, first, "w_pre")
+        kind = w_pre.dtype
+        qp = _weight(w_pre, H, kind, "w_pre")
+    if w_post is not None:
+        kind = kind or w_post.dtype
+        pp = _weight(w_post, H, kind, "w_post")
     if gate is not None:
-        if gate.dtype != first.dtype:
+        kind = kind or gate.dtype
+        if gate.dtype is not kind:
             raise TypeError("w_post, w_pre and gate must have one dtype")
         rows, cols = gate.shape if gate.dim() == 2 else (0, 0)
         if rows not in (1, T) or cols not in (1, H):
@@ -309,6 +306,9 @@ def wd_block_norm(res: torch.Tensor, res_out: torch.Tensor | None = None, out: t
         rp, rl = res_out.data_ptr(), _rows(res_out, shape, H, "res_out")
     if out is not None:
         op, ot, ol = out.data_ptr(), _type(out, "out"), _rows(out, shape, H, "out")
+    w_type = _TYPES.get(kind, 0)
+    if w_type == 0 and kind is not None and kind is not torch.float32:
+        raise TypeError(f"w_post, w_pre and gate: dtype {kind} is not float32, bfloat16 or float16")
     status = (_lib_cache or lib()).wd_block_norm(
         T, H, res.data_ptr(), _type(res, "res"), _rows(res, shape, H, "res"), yp, yt, yl, pp, qp, gp, w_type, gate_ld,
         gate_step, res_scale, eps, rp, rl, op, ot, ol, _stream(stream, res))

@@ -3,6 +3,8 @@
 // the E2M1 decode.
 #pragma once
 
+#include <atomic>
+
 #include "warp_decode_block.h"
 #include "wd_device.cuh"
 
@@ -23,6 +25,22 @@ inline moe_status launched(const char* what) {
   set_error(what, e);
   return MOE_ERR_CUDA;
 }
+
+// allow_smem once per device for a kernel's largest size (a call of the runtime takes as
+// long as a small kernel): one of these per kernel, static beside its launch.
+struct SmemOnce {
+  std::atomic<uint64_t> done{0};  // a bit per device
+  template <typename K>
+  moe_status allow(K kernel, size_t most) {
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return allow_smem(kernel, most);
+    const uint64_t bit = 1ull << dev;
+    if (done.load(std::memory_order_acquire) & bit) return MOE_OK;
+    const moe_status rc = allow_smem(kernel, most);
+    if (rc == MOE_OK) done.fetch_or(bit, std::memory_order_release);
+    return rc;
+  }
+};
 
 namespace {  // device code: one copy per translation unit
 

@@ -90,9 +90,7 @@ __global__ void __launch_bounds__(kThreads)
 constexpr int kMvWarps = 16, kMvThreads = kMvWarps * 32;
 constexpr int kMvTokens = 8;  // of a launch: the columns of an MMA
 constexpr int kAhead = 4;  // column tiles in flight per warp
-// Static and dynamic shared memory count together against the default limit: this
-// much is asked for beside the dynamic part.
-constexpr size_t kStaticSmem = 512;
+constexpr size_t kStaticSmem = 512;  // more than the kernel's static shared memory
 
 // Stage `toks` tokens' columns [128 c0, 128 c1) (zero from K on) as f16 fragments;
 // s_max[n] becomes the bits of the token's largest finite magnitude (16 bits). Copied
@@ -286,6 +284,7 @@ int64_t padded_words(const wd_fp4_shape* s) {
 
 template <bool BF16>
 moe_status launch_matvec(MvArgs a, cudaStream_t st) {
+  static SmemOnce once[2];
   auto k = fp4_matvec_kernel<BF16, false>;
   constexpr size_t kTileX = (size_t)4 * 32 * 16;  // x of a column tile
   constexpr size_t kTileSum = (size_t)kTileRows * kMvTokens * 4;
@@ -310,7 +309,7 @@ moe_status launch_matvec(MvArgs a, cudaStream_t st) {
     smem = a.chunk * kTileX + 2 * a.batch * kTileSum;
   }
   smem += kMvWarps * 2 * kTileSum;
-  moe_status rc = allow_smem(k, smem + kStaticSmem);
+  moe_status rc = once[a.chunk < ct].allow(k, kMaxDynSmem - kStaticSmem);
   if (rc != MOE_OK) return rc;
   for (a.tok0 = 0; a.tok0 < a.B; a.tok0 += kMvTokens) {
     k<<<grid, kMvThreads, smem, st>>>(a);

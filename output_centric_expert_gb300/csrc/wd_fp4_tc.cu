@@ -407,7 +407,8 @@ moe_status launch(MvArgs a, cudaStream_t st) {
   int n = tokens_up(a.B - a.tok0);
   while (n > 16 && ct > kMaxCluster * stage_tiles(n)) n /= 2;
   const size_t room = kStageX + (size_t)kRowTiles * 64 * kTcRows * 4 + 1024;
-  moe_status rc = allow_smem(k, room);
+  static SmemOnce once;
+  const moe_status rc = once.allow(k, room);
   if (rc != MOE_OK) return rc;
   // CTAs per cluster: as many as x needs, and more while all row tiles still have a
   // place at once and every CTA keeps 2 column tiles. 16 tokens of 9216 x 4096 (36 pairs

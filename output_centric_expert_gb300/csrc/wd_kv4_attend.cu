@@ -817,7 +817,8 @@ moe_status launch(const AttendArgs& a, bool bf16, cudaStream_t st) {
   static_assert(CTAS <= kMaxCtasPerSm, "the workspace has room for 2 CTAs per SM");
   auto k = bf16 ? kv4_attend_kernel<D, NT, W, STAGES, CTAS, true> : kv4_attend_kernel<D, NT, W, STAGES, CTAS, false>;
   const size_t ring = (size_t)W * STAGES * Stage<D>::kBytes;
-  moe_status rc = allow_smem(k, ring);
+  static SmemOnce once[2];
+  moe_status rc = once[bf16].allow(k, ring);
   if (rc != MOE_OK) return rc;
   // no more CTAs than tiles that the rows' capacity allows
   const int64_t keys = (int64_t)a.max_blocks << a.page_shift;

@@ -18,9 +18,7 @@ namespace {
 
 constexpr int kNormMaxH = 8192;
 constexpr int kNormPer = 8;  // channels per thread
-// Static and dynamic shared memory count together against the default limit: this
-// much is asked for beside the dynamic part.
-constexpr size_t kStaticSmem = 512;
+constexpr size_t kStaticSmem = 512;  // more than the kernels' static shared memory
 
 struct NormArgs {
   const void *res, *y, *w_post, *w_pre, *gate;
@@ -279,7 +277,8 @@ moe_status launch_norm(const NormArgs& a, cudaStream_t st) {
   const int rows = N == 32 ? kWarpsPerCta : 1;
   const int threads = N == 32 ? kThreads : VEC ? ((a.H + 7) / 8 + 31) / 32 * 32 : N;
   const size_t smem = VEC ? (size_t)threads * row_depth(RT, YT) * 8 * (elem_bytes(RT) + elem_bytes(YT)) : 0;
-  const moe_status rc = allow_smem(k, smem + kStaticSmem);
+  static SmemOnce once[2];
+  const moe_status rc = VEC ? once[rows_gate].allow(k, kMaxDynSmem - kStaticSmem) : MOE_OK;
   if (rc != MOE_OK) return rc;
   // resident CTAs: 64 registers a thread at most, so 1024 threads fill an SM
   const int64_t most = (int64_t)sm_count() * (1024 / threads);
