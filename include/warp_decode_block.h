@@ -64,9 +64,15 @@ moe_status wd_fp4_pack_weights(const wd_fp4_shape* shape, const void* w, int32_t
 /*
  * wd_fp4_matvec -- y[b,n] = sum_k x[b,k] W[n,k] for the B tokens of a decode
  * batch. x [B][K] BF16 or F16, 16-byte aligned with ldx % 8 == 0; y [B][N] F32,
- * BF16 or F16. Products are exact, sums FP32, y is rounded once. A value of x
- * is used exactly down to 2^-32 of the largest finite one in its token's
- * staged part of the row, and rounded to 2^-40 of that below.
+ * BF16 or F16. Products are exact, sums FP32, y is rounded once. Values of x are
+ * used exactly down to 2^-32 of their token's largest finite one and rounded to
+ * 2^-40 of it below. With more than 8 tokens a block of weights whose scale is
+ * below 2^-26 of the largest of its row (within a run of columns) counts as 0:
+ * less than FP32 rounding of the row's largest products. Up to 8 tokens one
+ * kernel streams the weights through mma.sync; more go through tcgen05 (K up
+ * to 32768), 64 at a time. The results are the same on every call; a token's do
+ * not depend on the other tokens' values, but their order of summation does on
+ * the batch's size.
  */
 moe_status wd_fp4_matvec(const wd_fp4_shape* shape, const uint8_t* packed_codes,
                          const uint8_t* packed_scales, const void* x, int32_t x_type,

@@ -20,7 +20,7 @@ struct MvArgs {
   int32_t tok0;   // first token of this launch
   int32_t chunk;  // stream kernel: column tiles of x staged at a time; all of them where that fits
   int32_t batch;  // stream kernel: row tiles of a CTA whose sums wait in shared memory
-  int32_t per, more;  // stream kernel: row tiles of a CTA, and how many CTAs have one more
+  int32_t per, more;  // row tiles of a CTA (or cluster), and how many have one more
 };
 
 // Columns that the tensor-memory kernel takes for `tokens` tokens (wd_fp4_tc.cu), and

@@ -37,6 +37,7 @@ constexpr int kRowTiles = 2;        // row tiles of a CTA at a time, two warpgro
 constexpr int kTcRows = 128;
 constexpr int kTcAhead = 2;         // column tiles of codes in flight per thread
 constexpr int kTmemCols = 512;      // per warpgroup: 64 for A, up to 64 for D
+constexpr int kMaxCluster = 8;      // CTAs, a power of two as every size here
 constexpr int kStageX = 128 * 1024; // bytes of x per CTA at most
 constexpr uint32_t kWaitLimit = 1u << 22;
 
@@ -144,13 +145,13 @@ __global__ void __launch_bounds__(kTcThreads, 1) fp4_tc_kernel(const MvArgs a, i
   const int tid = threadIdx.x, warp = tid >> 5, group = tid >> 7, gt = tid & 127;
   const int side = group >> 1, half = group & 1;  // row tile of the CTA, and which column tiles of it
   const int toks = min(n, a.B - a.tok0);
-  const int ct = (a.K + kTileCols - 1) / kTileCols, c0 = ct * rank / size, kt = ct * (rank + 1) / size - c0;
-  const int mt = (a.N + kTcRows - 1) / kTcRows, tiles = (a.N + kTileRows - 1) / kTileRows;
-  const int set = blockIdx.x / size, sets = gridDim.x / size;
-  const int per = mt / sets, more = mt - per * sets;
-  const int q0 = set * per + min(set, more), q1 = q0 + per + (set < more ? 1 : 0);
+  const int log = 31 - __clz(size);
+  const int ct = (a.K + kTileCols - 1) / kTileCols, c0 = (ct * rank) >> log, kt = ((ct * (rank + 1)) >> log) - c0;
+  const int tiles = (a.N + kTileRows - 1) / kTileRows;
+  const int set = blockIdx.x >> log;  // a cluster's row tiles [q0, q1)
+  const int q0 = set * a.per + min(set, a.more), q1 = q0 + a.per + (set < a.more ? 1 : 0);
   uint4* xs = dyn4 + (1024 - (smem_addr(dyn4) & 1023)) % 1024 / 16;  // the swizzle counts from 1024-byte boundaries
-  float* sums = reinterpret_cast<float*>(xs + ((ct + size - 1) / size) * 16 * n);  // [row tile][token][128 rows]
+  float* sums = reinterpret_cast<float*>(xs + ((ct + size - 1) >> log) * 16 * n);  // [row tile][token][128 rows]
 
   if (warp == 0)
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_addr(&s_tmem)),
@@ -233,13 +234,13 @@ __global__ void __launch_bounds__(kTcThreads, 1) fp4_tc_kernel(const MvArgs a, i
         for (int i = 0; i < kTcAhead; ++i) {
           const int k = k0 + i;
           if (k >= my_kt) break;
-          uint32_t mul[4];
+          uint32_t mul[4];  // 2^(s - top + 12) in both halves, 0 below 2^-14
 #pragma unroll
-          for (int b = 0; b < 4; ++b) {
-            const uint32_t s = (buf[i].sc >> (8 * b)) & 255u;
-            const int e = max(0, (int)s - (int)top + 27);
-            mul[b] = s == 255u ? 0x7E007E00u : (uint32_t)e * 0x04000400u;
-          }
+          for (int b = 0; b < 4; ++b)
+            mul[b] = (uint32_t)max(0, (int)((buf[i].sc >> (8 * b)) & 255u) - (int)top + 27) * 0x04000400u;
+#pragma unroll
+          for (int b = 0; b < 4; ++b)
+            if (((buf[i].sc >> (8 * b)) & 255u) == 255u) mul[b] = 0x7E007E00u;
           // ---- decode and store two blocks at a time; column k / 2 of A holds the elements k, k + 1
 #pragma unroll
           for (int o = 0; o < 2; ++o) {
@@ -341,7 +342,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) fp4_tc_kernel(const MvArgs a, i
     }
     cluster.sync();
     // ---- add the CTAs' sums: this CTA's share of the tokens, 4 rows a thread
-    const int t0 = toks * rank / size, t1 = toks * (rank + 1) / size;
+    const int t0 = (toks * rank) >> log, t1 = (toks * (rank + 1)) >> log;
     const int here = min(kRowTiles, q1 - q) * (t1 - t0) * (kTcRows / 4);
     for (int i = tid; i < here; i += kTcThreads) {
       const int r = i % (kTcRows / 4) * 4, tt = i / (kTcRows / 4), tok = t0 + tt % (t1 - t0), g = tt / (t1 - t0);
@@ -396,7 +397,6 @@ int resident_clusters(K k, int size, size_t smem) {
   return cached[dev][l];
 }
 
-constexpr int kMaxCluster = 8;
 int tokens_up(int tokens) { return tokens > 32 ? 64 : tokens > 16 ? 32 : 16; }
 int stage_tiles(int n) { return kStageX / (n * 2 * kTileCols); }  // column tiles of x in a CTA
 
@@ -424,7 +424,10 @@ moe_status launch(MvArgs a, cudaStream_t st) {
   attr.val.clusterDim.x = size;
   attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)((want < most ? want : most) * size));
+  const int sets = want < most ? want : most;
+  a.per = mt / sets;
+  a.more = mt - a.per * sets;
+  cfg.gridDim = dim3((unsigned)(sets * size));
   cfg.blockDim = dim3(kTcThreads);
   cfg.dynamicSmemBytes = (size_t)((ct + size - 1) / size) * n * 2 * kTileCols + (size_t)kRowTiles * n * kTcRows * 4 + 1024;
   cfg.stream = st;
