@@ -137,27 +137,31 @@ __device__ __forceinline__ void stage(const MvArgs& a, int c0, int c1, int toks,
 template <bool BF16>
 __global__ void __launch_bounds__(kTcThreads, 1) fp4_tc_kernel(const MvArgs a, int n) {
   extern __shared__ uint4 dyn4[];
-  __shared__ uint32_t s_max[64], s_tmem;
+  __shared__ uint32_t s_max[64], s_tmem, s_failed;
   __shared__ __align__(16) float s_back[64];  // 1 / the tokens' powers of two
   __shared__ __align__(8) uint64_t s_bar[kGroups];
+  __shared__ uint8_t s_top[kGroups][kTcRows];
   cg::cluster_group cluster = cg::this_cluster();
   const int rank = cluster.block_rank(), size = cluster.num_blocks();
   const int tid = threadIdx.x, warp = tid >> 5, group = tid >> 7, gt = tid & 127;
   const int side = group >> 1, half = group & 1;  // row tile of the CTA, and which column tiles of it
   const int toks = min(n, a.B - a.tok0);
-  const int log = 31 - __clz(size);
+  const int log = 31 - __clz(size), nlog = 31 - __clz(n);
   const int ct = (a.K + kTileCols - 1) / kTileCols, c0 = (ct * rank) >> log, kt = ((ct * (rank + 1)) >> log) - c0;
   const int tiles = (a.N + kTileRows - 1) / kTileRows;
   const int set = blockIdx.x >> log;  // a cluster's row tiles [q0, q1)
   const int q0 = set * a.per + min(set, a.more), q1 = q0 + a.per + (set < a.more ? 1 : 0);
   uint4* xs = dyn4 + (1024 - (smem_addr(dyn4) & 1023)) % 1024 / 16;  // the swizzle counts from 1024-byte boundaries
-  float* sums = reinterpret_cast<float*>(xs + ((ct + size - 1) >> log) * 16 * n);  // [row tile][token][128 rows]
+  const int own = n >> log;  // tokens whose sums this CTA writes, rank * own on
+  float* sums = reinterpret_cast<float*>(xs + ((ct + size - 1) >> log) * 16 * n);  // [row tile][CTA][token][128 rows]
 
+  if (size > 1) cluster.barrier_arrive();  // waited for before the first sums go to another CTA
   if (warp == 0)
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_addr(&s_tmem)),
                  "n"(kTmemCols)
                  : "memory");
   if (tid == 0) {
+    s_failed = 0;
 #pragma unroll
     for (int i = 0; i < kGroups; ++i)
       asm volatile("mbarrier.init.shared::cta.b64 [%0], 1;" ::"r"(smem_addr(&s_bar[i])) : "memory");
@@ -191,7 +195,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) fp4_tc_kernel(const MvArgs a, i
     }
   };
   auto largest_scale = [&]() {  // of the row's blocks here, NaN blocks apart
-    uint32_t top = 0;
+    uint32_t top = inside ? 0 : 127;
     if (inside) {
 #pragma unroll 8
       for (int k = 0; k < my_kt; ++k) {
@@ -229,6 +233,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) fp4_tc_kernel(const MvArgs a, i
   for (int q = q0; q < q1; q += kRowTiles) {
     if (q + side < q1) {
       const uint32_t top = next_top;
+      s_top[group][gt] = (uint8_t)top;
       for (int k0 = 0; k0 < my_kt; k0 += kTcAhead) {
 #pragma unroll
         for (int i = 0; i < kTcAhead; ++i) {
@@ -269,7 +274,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) fp4_tc_kernel(const MvArgs a, i
           asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
           asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
           group_sync(group);
-          if (gt == 0) {
+          if (gt == 32 * group) {  // a different scheduler's warp in each group
             asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
             const uint64_t b = bdesc + (uint64_t)((2 * k + half) * 16 * n);  // two runs of 64 columns, 8 n units each
 #pragma unroll
@@ -291,70 +296,78 @@ __global__ void __launch_bounds__(kTcThreads, 1) fp4_tc_kernel(const MvArgs a, i
         phase ^= 1;
       }
       asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-      float* to = sums + side * n * kTcRows + gt;
+      asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+      if (!ok) s_failed = 1;
+      pair_sync(side);  // both halves' sums are there
+      asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+    }
+    if (size > 1) cluster.barrier_wait();  // the owners have read the sums before
+    if (q + side < q1) {
       // D holds the sum times 2^(12 - (top - 127)) and the token's power of two. Taken off
       // one after the other where neither step can leave FP32's range, else in one.
-      // Each half first leaves the tokens that the other half adds to its own.
-      const bool plain = __all_sync(0xFFFFFFFFu, top >= 64u && top <= 190u);
-      const float back = ok ? exp2i(plain ? (int)top - 139 : 0) : NAN;  // a wait that ran out: no sum to trust
-      auto take = [&](int c, float (&o)[8]) {  // tokens c .. c + 7 of this half's sum
-        if (my_kt == 0) {
-#pragma unroll
-          for (int j = 0; j < 8; ++j) o[j] = 0.0f;
-          return;
-        }
-        uint32_t d[8];
-        tmem_load8(mine + 64 + c, d);
+      // Either half adds both halves' sums of its half of the tokens.
+      const uint32_t t0 = s_top[side * 2][gt], t1 = kt > 1 ? s_top[side * 2 + 1][gt] : t0;
+      const bool plain = __all_sync(0xFFFFFFFFu, min(t0, t1) >= 64u && max(t0, t1) <= 190u);
+      const float fail = s_failed ? NAN : 1.0f;  // a wait that ran out: no sum to trust
+      const float back0 = plain ? exp2i((int)t0 - 139) * fail : fail, back1 = plain ? exp2i((int)t1 - 139) * fail : fail;
+      const uint32_t d0 = s_tmem + side * 2 * (kTmemCols / kGroups) + ((uint32_t)(warp & 3) << 21) + 64;
+      const int64_t row = (int64_t)(q + side) * kTcRows + gt;
+#pragma unroll 1
+      for (int c = half * (n / 2); c < (half + 1) * (n / 2); c += 8) {
+        uint32_t d[8], e[8] = {};
+        tmem_load8(d0 + c, d);
+        if (kt > 1) tmem_load8(d0 + kTmemCols / kGroups + c, e);
         const float4 b0 = *reinterpret_cast<const float4*>(s_back + c), b1 = *reinterpret_cast<const float4*>(s_back + c + 4);
         const float b[8] = {b0.x, b0.y, b0.z, b0.w, b1.x, b1.y, b1.z, b1.w};
+        float o[8];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) o[j] = __uint_as_float(d[j]) * back * b[j];
+        for (int j = 0; j < 8; ++j)
+          o[j] = (__uint_as_float(d[j]) * back0 + __uint_as_float(e[j]) * back1) * b[j];
         if (!plain) {
 #pragma unroll 1
           for (int j = 0; j < 8; ++j) {
-            float v = 0.0f;
+            float v = 0.0f, w = 0.0f;
 #pragma unroll
             for (int k = 0; k < 8; ++k)
-              if (j == k) v = __uint_as_float(d[k]) * back;
-            v = ldexpf(v, (int)top - 139 - shift_of_16<BF16>(s_max[c + j]));
+              if (j == k) v = __uint_as_float(d[k]) * back0, w = __uint_as_float(e[k]) * back1;
+            const int shift = shift_of_16<BF16>(s_max[c + j]);
+            v = ldexpf(v, (int)t0 - 139 - shift) + ldexpf(w, (int)t1 - 139 - shift);
 #pragma unroll
             for (int k = 0; k < 8; ++k)
               if (j == k) o[k] = v;
           }
         }
-      };
-      const int own0 = half * (n / 2), other0 = n / 2 - own0;  // first token of either share
-      float o[8];
-#pragma unroll 1
-      for (int c = 0; c < n / 2; c += 8) {
-        take(other0 + c, o);
+        if (size == 1) {
 #pragma unroll
-        for (int j = 0; j < 8; ++j) to[(other0 + c + j) * kTcRows] = o[j];
-      }
-      pair_sync(side);
-#pragma unroll 1
-      for (int c = 0; c < n / 2; c += 8) {
-        take(own0 + c, o);
+          for (int j = 0; j < 8; ++j)
+            if (c + j < toks && row < a.N) store_elem(a.y, a.y_type, (int64_t)(a.tok0 + c + j) * a.ldy + row, o[j]);
+        } else {
 #pragma unroll
-        for (int j = 0; j < 8; ++j) to[(own0 + c + j) * kTcRows] += o[j];
+          for (int j = 0; j < 8; ++j) {
+            const int to = (c + j) >> (nlog - log), at = ((side << log) + rank) * own + ((c + j) & (own - 1));
+            *cluster.map_shared_rank(sums + at * kTcRows + gt, to) = o[j];
+          }
+        }
       }
       asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+      if (size == 1) pair_sync(side);  // the next row tile's MMAs write D again
     }
-    cluster.sync();
-    // ---- add the CTAs' sums: this CTA's share of the tokens, 4 rows a thread
-    const int t0 = (toks * rank) >> log, t1 = (toks * (rank + 1)) >> log;
-    const int here = min(kRowTiles, q1 - q) * (t1 - t0) * (kTcRows / 4);
-    for (int i = tid; i < here; i += kTcThreads) {
-      const int r = i % (kTcRows / 4) * 4, tt = i / (kTcRows / 4), tok = t0 + tt % (t1 - t0), g = tt / (t1 - t0);
-      float* src = sums + (g * n + tok) * kTcRows + r;
-      float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-      for (int o = 0; o < size; ++o) {
-        const float4 w = *reinterpret_cast<const float4*>(cluster.map_shared_rank(src, o));
-        v.x += w.x, v.y += w.y, v.z += w.z, v.w += w.w;
+    if (size > 1) {
+      cluster.sync();
+      // ---- add the CTAs' sums of this one's tokens, 4 rows a thread
+      const int here = q + side < q1 ? min(own, toks - rank * own) * (kTcRows / 4) : 0;
+      for (int i = tid & (kTcThreads / kRowTiles - 1); i < here; i += kTcThreads / kRowTiles) {
+        const int r = i % (kTcRows / 4) * 4, tok = i / (kTcRows / 4);
+        const float* src = sums + ((side << log) * own + tok) * kTcRows + r;
+        float4 v = *reinterpret_cast<const float4*>(src);
+        for (int o = 1; o < size; ++o) {
+          const float4 w = *reinterpret_cast<const float4*>(src + o * own * kTcRows);
+          v.x += w.x, v.y += w.y, v.z += w.z, v.w += w.w;
+        }
+        store_rows(a, a.tok0 + rank * own + tok, (int64_t)(q + side) * kTcRows + r, v);
       }
-      store_rows(a, a.tok0 + tok, (int64_t)(q + g) * kTcRows + r, v);
+      if (q + kRowTiles < q1) cluster.barrier_arrive();
     }
-    cluster.sync();  // the sums are written again, or their CTA leaves
   }
   asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
   __syncthreads();
