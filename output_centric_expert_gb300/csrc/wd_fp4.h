@@ -48,35 +48,31 @@ __device__ __forceinline__ void store_rows(const MvArgs& a, int tok, int64_t row
 // ---- x as f16 times a power of two per token: its largest finite magnitude comes
 // into [2^14, 2^15), so BF16 and F16 values are exact down to 2^-32 of it.
 
-// The lower of a word's two 16-bit magnitudes, 0 for infinities and NaN.
+// The largest finite magnitude, as an integer: 16-bit pairs, plus what takes infinities
+// and NaN past the largest signed value, so that they lose against anything.
 template <bool BF16>
-__device__ __forceinline__ uint32_t finite_or_0(uint32_t m) {
-  constexpr uint32_t kInf = BF16 ? 0x7F80u : 0x7C00u;
-  return (m & 0xFFFFu) < kInf ? m & 0xFFFFu : 0u;
+constexpr uint32_t kPairs0 = BF16 ? 0x00800080u : 0x04000400u;
+
+template <bool BF16>
+__device__ __forceinline__ uint32_t largest_pairs(const uint4& v, uint32_t pair) {
+  pair = __viaddmax_s16x2(v.x & 0x7FFF7FFFu, kPairs0<BF16>, pair);
+  pair = __viaddmax_s16x2(v.y & 0x7FFF7FFFu, kPairs0<BF16>, pair);
+  pair = __viaddmax_s16x2(v.z & 0x7FFF7FFFu, kPairs0<BF16>, pair);
+  return __viaddmax_s16x2(v.w & 0x7FFF7FFFu, kPairs0<BF16>, pair);
 }
 
-// The bits of the largest finite magnitude in `count` pieces of 8 elements, `step`
-// pieces apart. Magnitudes are ordered as integers, two to a word; infinities and NaN
-// (rare) show in the maximum and are then left out one by one.
+template <bool BF16>
+__device__ __forceinline__ uint32_t largest_of(uint32_t pair) {
+  return max(pair & 0xFFFFu, pair >> 16) - (kPairs0<BF16> & 0xFFFFu);
+}
+
+// Of `count` pieces of 8 elements, `step` pieces apart.
 template <bool BF16>
 __device__ __forceinline__ uint32_t largest_finite16(const uint4* p, int count, int step) {
-  uint32_t pair = 0;
+  uint32_t pair = kPairs0<BF16>;
 #pragma unroll 4
-  for (int i = 0; i < count; ++i) {
-    const uint4 v = p[i * step];
-    pair = __vmaxu2(__vmaxu2(pair, v.x & 0x7FFF7FFFu),
-                    __vmaxu2(v.y & 0x7FFF7FFFu, __vmaxu2(v.z & 0x7FFF7FFFu, v.w & 0x7FFF7FFFu)));
-  }
-  uint32_t m = max(pair & 0xFFFFu, pair >> 16);
-  if (finite_or_0<BF16>(m) != m) {
-    m = 0;
-#pragma unroll 1
-    for (int i = 0; i < count * 4; ++i) {
-      const uint32_t w = reinterpret_cast<const uint32_t*>(p + (i >> 2) * step)[i & 3] & 0x7FFF7FFFu;
-      m = max(m, max(finite_or_0<BF16>(w), finite_or_0<BF16>(w >> 16)));
-    }
-  }
-  return m;
+  for (int i = 0; i < count; ++i) pair = largest_pairs<BF16>(p[i * step], pair);
+  return largest_of<BF16>(pair);
 }
 
 // The exponent of the power of two for largest magnitude bits m.
@@ -84,6 +80,14 @@ template <bool BF16>
 __device__ __forceinline__ int shift_of_16(uint32_t m) {
   const uint32_t mag = BF16 ? m << 16 : __float_as_uint(half_lo(m));
   return mag == 0 ? 0 : min(126, max(-126, 141 - (int)(mag >> 23)));
+}
+
+template <bool BF16>
+__device__ __forceinline__ uint4 scaled_f16(const uint4& v, float up) {
+  float f[8];
+  unpack8<BF16>(v, f);
+  return make_uint4(pack2<false>(f[0] * up, f[1] * up), pack2<false>(f[2] * up, f[3] * up),
+                    pack2<false>(f[4] * up, f[5] * up), pack2<false>(f[6] * up, f[7] * up));
 }
 
 // Pieces of 8 elements times `up`, as f16, in place. Four are read before the first is
@@ -98,13 +102,8 @@ __device__ __forceinline__ void scale_to_f16(uint4* p, int count, int step, floa
     for (int j = 0; j < kAtOnce; ++j)
       if (i + j < count) v[j] = p[(i + j) * step];
 #pragma unroll
-    for (int j = 0; j < kAtOnce; ++j) {
-      float f[8];
-      unpack8<BF16>(v[j], f);
-      if (i + j < count)
-        p[(i + j) * step] = make_uint4(pack2<false>(f[0] * up, f[1] * up), pack2<false>(f[2] * up, f[3] * up),
-                                       pack2<false>(f[4] * up, f[5] * up), pack2<false>(f[6] * up, f[7] * up));
-    }
+    for (int j = 0; j < kAtOnce; ++j)
+      if (i + j < count) p[(i + j) * step] = scaled_f16<BF16>(v[j], up);
   }
 }
 

@@ -98,38 +98,48 @@ __device__ __forceinline__ void pair_sync(int side) {
 
 // x of `toks` tokens (zero up to n), columns [128 c0, 128 c1) (zero from K on), as f16
 // times a power of two per token, K-major in the 128-byte swizzle: [64 columns][token]
-// [128 bytes], 16-byte unit u of a row at u ^ (token & 7). Copied as it is, then
-// converted in place: 8 lanes have a token's 128 bytes (whole lines, no bank
-// conflicts), and a thread converts what it has copied. s_max: magnitude bits per token.
+// [128 bytes], 16-byte unit u of a row at u ^ (token & 7). 8 lanes have a token's 128
+// bytes (whole lines, no bank conflicts) and keep them in registers from the load to the
+// converted store. s_max: magnitude bits per token. 1 << nlog = n.
 template <bool BF16>
-__device__ __forceinline__ void stage(const MvArgs& a, int c0, int c1, int toks, int n, uint4* xs, uint32_t* s_max) {
-  const int k0 = c0 * kTileCols, real = (min(a.K, c1 * kTileCols) - k0) / 8;
-  const uint16_t* x = a.x + (int64_t)a.tok0 * a.ldx + k0;
-  const int u = threadIdx.x & 7, rows = (c1 - c0) * 2 * n;  // 128-byte rows, row = 64-column run * n + token
-  constexpr int kStep = kTcThreads / 8;
-  for (int r = threadIdx.x >> 3; r < rows; r += kStep) {
-    const int tok = r & (n - 1), unit = r / n * 8 + u;
-    const bool ok = tok < toks && unit < real;
-    const uint16_t* p = x + (ok ? (int64_t)tok * a.ldx + unit * 8 : 0);
-    const int bytes = ok ? 16 : 0;  // 0: zeros, the source is not read
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_addr(xs + r * 8 + (u ^ (tok & 7)))),
-                 "l"(p), "r"(bytes)
-                 : "memory");
-  }
-  asm volatile("cp.async.commit_group;" ::: "memory");
-  if (threadIdx.x < n) s_max[threadIdx.x] = 0;
+__device__ __forceinline__ void stage(const MvArgs& a, int c0, int c1, int toks, int nlog, uint4* xs, uint32_t* s_max) {
+  constexpr int kStep = kTcThreads / 8, kMost = kStageX / 16 / kTcThreads;
+  const int u = threadIdx.x & 7, first = threadIdx.x >> 3;
+  const int rows = (c1 - c0) * 2 << nlog;  // 128-byte rows, row = 64-column run * n + token
+  const int tok = first & ((1 << nlog) - 1);  // with 64 rows a step, every row of this thread is of one token
+  const int k0 = c0 * kTileCols + (first >> nlog) * 64 + u * 8, dk = kStep >> nlog << 6;
+  const uint16_t* x = a.x + (int64_t)(a.tok0 + tok) * a.ldx + k0;
+  const int mine = tok < toks ? (min(a.K, c1 * kTileCols) - k0 + dk - 1) / dk : 0;  // pieces that are there
+  // in fours that small products skip: they spend their time fetching code
+  constexpr int kFour = 4;
+  uint4 v[kMost];
+#pragma unroll
+  for (int f = 0; f < kMost; f += kFour)
+    if (f * kStep < rows)
+#pragma unroll
+      for (int i = f; i < f + kFour; ++i)
+        v[i] = i < mine ? __ldg(reinterpret_cast<const uint4*>(x + i * dk)) : make_uint4(0, 0, 0, 0);
+  if (threadIdx.x < 1 << nlog) s_max[threadIdx.x] = 0;
   __syncthreads();
-  asm volatile("cp.async.wait_group 0;" ::: "memory");
-  // with 64 rows a step, every row of this thread is of one token
-  const int tok = (threadIdx.x >> 3) & (n - 1);
-  uint4* own = xs + (threadIdx.x >> 3) * 8 + (u ^ (tok & 7));  // and 512 units on
-  const int mine = (rows - (int)(threadIdx.x >> 3) + kStep - 1) / kStep;
-  uint32_t m = largest_finite16<BF16>(own, mine, kStep * 8);
+  uint32_t pair = kPairs0<BF16>;
+#pragma unroll
+  for (int f = 0; f < kMost; f += kFour)
+    if (f * kStep < rows)
+#pragma unroll
+      for (int i = f; i < f + kFour; ++i) pair = largest_pairs<BF16>(v[i], pair);
+  uint32_t m = largest_of<BF16>(pair);
 #pragma unroll
   for (int o = 1; o < 8; o <<= 1) m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
   if (u == 0) atomicMax(s_max + tok, m);
   __syncthreads();
-  scale_to_f16<BF16>(own, mine, kStep * 8, exp2i(shift_of_16<BF16>(s_max[tok])));
+  const float up = exp2i(shift_of_16<BF16>(s_max[tok]));
+  uint4* to = xs + first * 8 + (u ^ (tok & 7));
+#pragma unroll
+  for (int f = 0; f < kMost; f += kFour)
+    if (f * kStep < rows)
+#pragma unroll
+      for (int i = f; i < f + kFour; ++i)
+        if (first + i * kStep < rows) to[i * kStep * 8] = scaled_f16<BF16>(v[i], up);
   // the tensor core reads through the asynchronous proxy
   asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
 }
@@ -213,8 +223,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) fp4_tc_kernel(const MvArgs a, i
 #pragma unroll
   for (int i = 0; i < kTcAhead; ++i)
     if (i < my_kt) load(buf[i], i);
-
-  stage<BF16>(a, c0, c0 + kt, toks, n, xs, s_max);
+  stage<BF16>(a, c0, c0 + kt, toks, nlog, xs, s_max);
   if (tid < n) s_back[tid] = exp2i(-shift_of_16<BF16>(s_max[tid]));
   asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
   __syncthreads();
