@@ -56,11 +56,19 @@ __device__ __forceinline__ void tmem_store32(uint32_t at, const uint32_t (&r)[32
       : "memory");
 }
 
-__device__ __forceinline__ void tmem_load8(uint32_t at, uint32_t (&r)[8]) {
+// Eight columns from `at` and, where `both`, from `at2`.
+__device__ __forceinline__ void tmem_load8(uint32_t at, uint32_t at2, bool both, uint32_t (&r)[8], uint32_t (&q)[8]) {
   asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
                : "r"(at));
-  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+  if (both)
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+                 : "=r"(q[0]), "=r"(q[1]), "=r"(q[2]), "=r"(q[3]), "=r"(q[4]), "=r"(q[5]), "=r"(q[6]), "=r"(q[7])
+                 : "r"(at2));
+  // the registers are operands, so that no use of them moves above
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
+                 "+r"(q[0]), "+r"(q[1]), "+r"(q[2]), "+r"(q[3]), "+r"(q[4]), "+r"(q[5]), "+r"(q[6]), "+r"(q[7])::"memory");
 }
 
 // D (+)= A B: A in tensor memory, B by its shared-memory descriptor.
@@ -184,40 +192,28 @@ __global__ void __launch_bounds__(kTcThreads, 1) fp4_tc_kernel(const MvArgs a, i
   };
   Tile buf[kTcAhead];
   const uint8_t *lc, *ls;
-  bool inside;
   const int my_kt = (kt - half + 1) / 2;  // column tiles half, half + 2, ...
-  auto point = [&](int q) {  // at this thread's row of tile q
+  auto point = [&](int q) {  // at this thread's row of tile q; behind the last row: any row, y has none
     const int row = q * kTcRows + gt, rt = row / kTileRows;
-    inside = q < q1 && rt < tiles;
-    const size_t at = inside ? (size_t)rt * ct + c0 + half : 0;
+    const size_t at = (size_t)(rt < tiles ? rt : 0) * ct + c0 + half;
     lc = a.codes + at * kTileCodes + (row % kTileRows) * 64;
     ls = a.scales + at * kTileScales + (row % 8) * 8 + (row % kTileRows) / 8 * 4;
   };
   auto load = [&](Tile& t, int k) {
-    if (inside) {
-      t.a = ld_codes32(lc + (size_t)k * 2 * kTileCodes);
-      t.b = ld_codes32(lc + (size_t)k * 2 * kTileCodes + 32);
-      t.sc = __ldg(reinterpret_cast<const uint32_t*>(ls + (size_t)k * 2 * kTileScales));
-    } else {
-#pragma unroll
-      for (int i = 0; i < 8; ++i) t.a.w[i] = t.b.w[i] = 0;
-      t.sc = 0;
-    }
+    t.a = ld_codes32(lc + (size_t)k * 2 * kTileCodes);
+    t.b = ld_codes32(lc + (size_t)k * 2 * kTileCodes + 32);
+    t.sc = __ldg(reinterpret_cast<const uint32_t*>(ls + (size_t)k * 2 * kTileScales));
   };
-  auto largest_scale = [&]() {  // of the row's blocks here, NaN blocks apart
-    uint32_t top = inside ? 0 : 127;
-    if (inside) {
+  // The row's largest scale here, NaN blocks apart: their 255 + 0x7F01 is negative in 16 bits.
+  auto largest_scale = [&]() {
+    uint32_t top = 0x7F017F01u;
 #pragma unroll 8
-      for (int k = 0; k < my_kt; ++k) {
-        const uint32_t w = __ldg(reinterpret_cast<const uint32_t*>(ls + (size_t)k * 2 * kTileScales));
-#pragma unroll
-        for (int b = 0; b < 4; ++b) {
-          const uint32_t s = (w >> (8 * b)) & 255u;
-          top = max(top, s == 255u ? 0u : s);
-        }
-      }
+    for (int k = 0; k < my_kt; ++k) {
+      const uint32_t w = __ldg(reinterpret_cast<const uint32_t*>(ls + (size_t)k * 2 * kTileScales));
+      top = __viaddmax_s16x2(w & 0x00FF00FFu, 0x7F017F01u, top);
+      top = __viaddmax_s16x2((w >> 8) & 0x00FF00FFu, 0x7F017F01u, top);
     }
-    return top;
+    return max(top & 0xFFFFu, top >> 16) - 0x7F01u;
   };
   point(q0 + side);
 #pragma unroll
@@ -248,13 +244,17 @@ __global__ void __launch_bounds__(kTcThreads, 1) fp4_tc_kernel(const MvArgs a, i
         for (int i = 0; i < kTcAhead; ++i) {
           const int k = k0 + i;
           if (k >= my_kt) break;
-          uint32_t mul[4];  // 2^(s - top + 12) in both halves, 0 below 2^-14
-#pragma unroll
-          for (int b = 0; b < 4; ++b)
-            mul[b] = (uint32_t)max(0, (int)((buf[i].sc >> (8 * b)) & 255u) - (int)top + 27) * 0x04000400u;
-#pragma unroll
-          for (int b = 0; b < 4; ++b)
-            if (((buf[i].sc >> (8 * b)) & 255u) == 255u) mul[b] = 0x7E007E00u;
+          // 2^(s - top + 12) in both halves of mul[b], 0 below 2^-14; a NaN block's is above 2^12
+          uint32_t mul[4];
+          {
+            const uint32_t less = ((27u - top) & 0xFFFFu) * 0x10001u;
+            const uint32_t e02 = __viaddmax_s16x2(buf[i].sc & 0x00FF00FFu, less, 0u);
+            const uint32_t e13 = __viaddmax_s16x2((buf[i].sc >> 8) & 0x00FF00FFu, less, 0u);
+            mul[0] = __byte_perm(e02 << 10, 0, 0x1010), mul[2] = __byte_perm(e02 << 10, 0, 0x3232);
+            mul[1] = __byte_perm(e13 << 10, 0, 0x1010), mul[3] = __byte_perm(e13 << 10, 0, 0x3232);
+            if ((__vmaxs2(e02, e13) + 0x7FE47FE4u) & 0x80008000u)  // the row's sum is NaN
+              mul[0] = mul[1] = mul[2] = mul[3] = 0x7E007E00u;
+          }
           // ---- decode and store two blocks at a time; column k / 2 of A holds the elements k, k + 1
 #pragma unroll
           for (int o = 0; o < 2; ++o) {
@@ -295,11 +295,13 @@ __global__ void __launch_bounds__(kTcThreads, 1) fp4_tc_kernel(const MvArgs a, i
         }
       }
       // the next row tile's first codes, while this one's sums are taken
-      point(q + kRowTiles + side);
+      if (q + kRowTiles + side < q1) {
+        point(q + kRowTiles + side);
 #pragma unroll
-      for (int i = 0; i < kTcAhead; ++i)
-        if (i < my_kt) load(buf[i], i);
-      next_top = largest_scale();
+        for (int i = 0; i < kTcAhead; ++i)
+          if (i < my_kt) load(buf[i], i);
+        next_top = largest_scale();
+      }
       if (my_kt > 0) {
         ok = ok && wait_phase(bar, phase);
         phase ^= 1;
@@ -321,11 +323,12 @@ __global__ void __launch_bounds__(kTcThreads, 1) fp4_tc_kernel(const MvArgs a, i
       const float back0 = plain ? exp2i((int)t0 - 139) * fail : fail, back1 = plain ? exp2i((int)t1 - 139) * fail : fail;
       const uint32_t d0 = s_tmem + side * 2 * (kTmemCols / kGroups) + ((uint32_t)(warp & 3) << 21) + 64;
       const int64_t row = (int64_t)(q + side) * kTcRows + gt;
+      const uint32_t slot = smem_addr(sums + ((side << log) + rank) * own * kTcRows + gt);
+      uint32_t place = 0;
 #pragma unroll 1
       for (int c = half * (n / 2); c < (half + 1) * (n / 2); c += 8) {
         uint32_t d[8], e[8] = {};
-        tmem_load8(d0 + c, d);
-        if (kt > 1) tmem_load8(d0 + kTmemCols / kGroups + c, e);
+        tmem_load8(d0 + c, d0 + kTmemCols / kGroups + c, kt > 1, d, e);
         const float4 b0 = *reinterpret_cast<const float4*>(s_back + c), b1 = *reinterpret_cast<const float4*>(s_back + c + 4);
         const float b[8] = {b0.x, b0.y, b0.z, b0.w, b1.x, b1.y, b1.z, b1.w};
         float o[8];
@@ -352,9 +355,14 @@ __global__ void __launch_bounds__(kTcThreads, 1) fp4_tc_kernel(const MvArgs a, i
             if (c + j < toks && row < a.N) store_elem(a.y, a.y_type, (int64_t)(a.tok0 + c + j) * a.ldy + row, o[j]);
         } else {
 #pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            const int to = (c + j) >> (nlog - log), at = ((side << log) + rank) * own + ((c + j) & (own - 1));
-            *cluster.map_shared_rank(sums + at * kTcRows + gt, to) = o[j];
+          for (int j = 0; j < 8; j += 2) {  // own >= 2
+            if (j == 0 || own < 8)  // the owner's place for token c + j
+              asm("mapa.shared::cluster.u32 %0, %1, %2;"
+                  : "=r"(place)
+                  : "r"(slot + ((c + j) & (own - 1)) * (kTcRows * 4)), "r"((c + j) >> (nlog - log)));
+            const uint32_t to = own < 8 ? place : place + j * kTcRows * 4;
+            asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(to), "f"(o[j]) : "memory");
+            asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(to + kTcRows * 4), "f"(o[j + 1]) : "memory");
           }
         }
       }
