@@ -109,8 +109,10 @@ __device__ __forceinline__ void pair_sync(int side) {
 // [128 bytes], 16-byte unit u of a row at u ^ (token & 7). 8 lanes have a token's 128
 // bytes (whole lines, no bank conflicts) and keep them in registers from the load to the
 // converted store. s_max: magnitude bits per token. 1 << nlog = n.
-template <bool BF16>
-__device__ __forceinline__ void stage(const MvArgs& a, int c0, int c1, int toks, int nlog, uint4* xs, uint32_t* s_max) {
+// `meanwhile` runs while they are loaded.
+template <bool BF16, typename F>
+__device__ __forceinline__ void stage(const MvArgs& a, int c0, int c1, int toks, int nlog, uint4* xs, uint32_t* s_max,
+                                      F meanwhile) {
   constexpr int kStep = kTcThreads / 8, kMost = kStageX / 16 / kTcThreads;
   const int u = threadIdx.x & 7, first = threadIdx.x >> 3;
   const int rows = (c1 - c0) * 2 << nlog;  // 128-byte rows, row = 64-column run * n + token
@@ -128,6 +130,7 @@ __device__ __forceinline__ void stage(const MvArgs& a, int c0, int c1, int toks,
       for (int i = f; i < f + kFour; ++i)
         v[i] = i < mine ? __ldg(reinterpret_cast<const uint4*>(x + i * dk)) : make_uint4(0, 0, 0, 0);
   if (threadIdx.x < 1 << nlog) s_max[threadIdx.x] = 0;
+  meanwhile();
   __syncthreads();
   uint32_t pair = kPairs0<BF16>;
 #pragma unroll
@@ -174,18 +177,6 @@ __global__ void __launch_bounds__(kTcThreads, 1) fp4_tc_kernel(const MvArgs a, i
   float* sums = reinterpret_cast<float*>(xs + ((ct + size - 1) >> log) * 16 * n);  // [row tile][CTA][token][128 rows]
 
   if (size > 1) cluster.barrier_arrive();  // waited for before the first sums go to another CTA
-  if (warp == 0)
-    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_addr(&s_tmem)),
-                 "n"(kTmemCols)
-                 : "memory");
-  if (tid == 0) {
-    s_failed = 0;
-#pragma unroll
-    for (int i = 0; i < kGroups; ++i)
-      asm volatile("mbarrier.init.shared::cta.b64 [%0], 1;" ::"r"(smem_addr(&s_bar[i])) : "memory");
-    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
-  }
-
   struct Tile {
     Codes32 a, b;  // a row's 64 bytes of a column tile
     uint32_t sc;
@@ -215,11 +206,36 @@ __global__ void __launch_bounds__(kTcThreads, 1) fp4_tc_kernel(const MvArgs a, i
     }
     return max(top & 0xFFFFu, top >> 16) - 0x7F01u;
   };
+  // The next round's weights to L2, 16 rows a lane. Clusters wait for one another between rounds:
+  // 64 tokens of 65536 x 4096 83.4 -> 77.8 us. (A CTA alone has its row tiles out of step, and so
+  // much ahead only disturbs the loads at hand: 16 tokens 42.8 -> 49 us.)
+  auto prefetch = [&](int q) {
+    const int rt = q * (kTcRows / kTileRows) + (tid & 31);
+    if (warp == 1 && (tid & 31) < kRowTiles * kTcRows / kTileRows && rt < tiles && rt < q1 * (kTcRows / kTileRows)) {
+      const size_t at = (size_t)rt * ct + c0;
+      asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(a.codes + at * kTileCodes), "r"(kt * kTileCodes)
+                   : "memory");
+      asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(a.scales + at * kTileScales), "r"(kt * kTileScales)
+                   : "memory");
+    }
+  };
   point(q0 + side);
 #pragma unroll
   for (int i = 0; i < kTcAhead; ++i)
     if (i < my_kt) load(buf[i], i);
-  stage<BF16>(a, c0, c0 + kt, toks, nlog, xs, s_max);
+  stage<BF16>(a, c0, c0 + kt, toks, nlog, xs, s_max, [&]() {
+    if (warp == 0)
+      asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_addr(&s_tmem)),
+                   "n"(kTmemCols)
+                   : "memory");
+    if (tid == 0) {
+      s_failed = 0;
+#pragma unroll
+      for (int i = 0; i < kGroups; ++i)
+        asm volatile("mbarrier.init.shared::cta.b64 [%0], 1;" ::"r"(smem_addr(&s_bar[i])) : "memory");
+      asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+  });
   if (tid < n) s_back[tid] = exp2i(-shift_of_16<BF16>(s_max[tid]));
   asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
   __syncthreads();
@@ -236,6 +252,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) fp4_tc_kernel(const MvArgs a, i
   bool ok = true;
 
   for (int q = q0; q < q1; q += kRowTiles) {
+    if (size > 1 && q + kRowTiles < q1) prefetch(q + kRowTiles);
     if (q + side < q1) {
       const uint32_t top = next_top;
       s_top[group][gt] = (uint8_t)top;
