@@ -42,9 +42,10 @@ constexpr int kMinTiles = 2;    // tiles of a CTA of a split row, on average
 // What a row costs beside its tiles, in tiles: CTAs share both out.
 __host__ __device__ constexpr int row_units(int NT) { return NT == 2 ? 2 : 1; }
 
-// A row that begins in CTA c and goes on in the next: [c], parts 0 where there is none.
+// The split row that goes on from this CTA into the next, parts 0 where there is none:
+// a row with parts in the CTAs c .. c + parts - 1 is in all their entries but the last.
 struct __align__(16) Split {
-  int32_t parts, seq, head, nh;  // head: the first query head of the row
+  int32_t parts, index, seq, head;  // index: this CTA's among them; head: the row's first query head
 };
 
 struct AttendArgs {
@@ -422,7 +423,7 @@ __device__ __forceinline__ int tiles_of(const AttendArgs& a, int s, uint32_t& lo
 struct Segment {
   int seq, head, nh, iters;  // head: its first query head
   uint32_t kw, lo, hi;       // the first tile's first key, the keys that count
-  int begins, ends, last_unit;  // whether it has the row's first and last tile; the latter's unit
+  int begins, ends;          // whether it has the row's first and last tile
 };
 
 template <int D, int NT, int W, int STAGES, int CTAS, bool BF16>
@@ -445,7 +446,7 @@ __global__ void __launch_bounds__(W * 32, CTAS) kv4_attend_kernel(const AttendAr
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
   const int rows = a.heads * a.head_tiles;  // of a sequence
 
-  if (tid == 0) a.split[blockIdx.x].parts = 0;  // until this CTA turns out to begin a split row
+  if (tid == 0) a.split[blockIdx.x].parts = 0;  // until a split row turns out to go on from here
   launch_dependents();
   // ---- this CTA's share of all units: an inclusive scan over the sequences
   uint32_t lo, hi;
@@ -532,8 +533,12 @@ __global__ void __launch_bounds__(W * 32, CTAS) kv4_attend_kernel(const AttendAr
       f_key = kw + warp * kWarpKeys;
       const int slot = f_segs & 1;
       if (lane == 0)
-        s_seg[warp][slot] = {f_seq, kv * a.group + h0, nh, f_iters, kw, lo, hi, first == 0, last == f_tiles,
-                             row0 + per - 1};
+        s_seg[warp][slot] = {f_seq, kv * a.group + h0, nh, f_iters, kw, lo, hi, first == 0, last == f_tiles};
+      if (tid == 0 && last != f_tiles) {
+        auto cta_of = [&](int u) { return u < gr * (gq + 1) ? u / (gq + 1) : gr + (u - gr * (gq + 1)) / gq; };
+        const int c0 = first == 0 ? (int)blockIdx.x : cta_of(row0 + kRowUnits), c1 = cta_of(row0 + per - 1);
+        a.split[blockIdx.x] = {c1 - c0 + 1, (int)blockIdx.x - c0, f_seq, kv * a.group + h0};
+      }
       for (int i = tid; i < NH * D / 8; i += THREADS) {
         const bool real = i / (D / 8) < nh;
         cp_async16(&s_raw[slot][i],
@@ -647,11 +652,6 @@ __global__ void __launch_bounds__(W * 32, CTAS) kv4_attend_kernel(const AttendAr
     const bool whole = sg.begins && sg.ends;
     // a row that goes on in another CTA's share: its first part goes to slot 1, the others to slot 0
     float* part = a.parts + ((size_t)blockIdx.x * 2 + (sg.begins ? 1 : 0)) * kPart;
-    if (sg.begins && !whole && tid == 0) {
-      const int u = sg.last_unit;  // the CTA that has it
-      const int c1 = u < gr * (gq + 1) ? u / (gq + 1) : gr + (u - gr * (gq + 1)) / gq;
-      a.split[blockIdx.x] = {c1 - (int)blockIdx.x + 1, sg.seq, sg.head, sg.nh};
-    }
     uint16_t* orow = a.out + (int64_t)sg.seq * a.ldo + (int64_t)sg.head * D;
     float* lrow = a.lse ? a.lse + (int64_t)sg.seq * a.heads * a.group + sg.head : nullptr;
 #pragma unroll
@@ -721,86 +721,78 @@ __global__ void __launch_bounds__(W * 32, CTAS) kv4_attend_kernel(const AttendAr
   cp_async_wait<0>();
 }
 
-// Joins the parts of the rows that several CTAs share: a CTA per (first CTA of a
-// row, 256 sums of it); a quarter of the threads each takes every fourth part. A
-// dependent launch: its CTAs are resident when the parts are ready.
+// Joins the parts of the rows that several CTAs share. A row with P parts has P - 1
+// CTAs here (each attending CTA's entry names at most one row), which share out its
+// sums, so a CTA reads about one part's size whatever P is: many rows of two parts and
+// one row of many take one wave. A sum of P parts is taken by as many threads as there
+// are: 1 for two parts of 2048 sums, 64 for 76 parts of 1024. (A CTA per 256 sums of
+// each row, threads sized for many parts: 2432 CTAs in 8 waves for 64 sequences.)
+// A dependent launch.
 constexpr int kJoin = 256;
 template <int D, int NT, bool BF16>
 __global__ void __launch_bounds__(kJoin) kv4_join_kernel(const AttendArgs a) {
-  constexpr int NH = NT * 8, kPart = NH * (D + 2), kHeads = kJoin / D < 1 ? 1 : kJoin / D;  // heads of a CTA's sums
-  __shared__ float s_max[kHeads], s_l[kHeads];
-  __shared__ float4 s_acc[4][kJoin / 4];
-  extern __shared__ float s_pm[];  // [parts][head]: maxima, then weights; behind them the sums
-  float* s_pl = s_pm + gridDim.x * kHeads;
-  const int tid = threadIdx.x, quarter = tid >> 6, i = blockIdx.y * kJoin + (tid & 63) * 4;
+  constexpr int NH = NT * 8, kPart = NH * (D + 2);
+  __shared__ float4 s_v[kJoin];
+  __shared__ float s_m[kJoin], s_l[kJoin];
+  const int tid = threadIdx.x;
   wait_prerequisite();
   const Split sp = a.split[blockIdx.x];
-  if (sp.parts == 0 || blockIdx.y * kJoin >= sp.nh * D) return;
-  const float* p0 = a.parts + ((size_t)blockIdx.x * 2 + 1) * kPart;  // of the first CTA
-  const float* p1 = a.parts + (size_t)(blockIdx.x + 1) * 2 * kPart;  // of the others, 2 * kPart apart
+  if (sp.parts == 0) return;
+  const int c0 = (int)blockIdx.x - sp.index, shares = sp.parts - 1;
+  const int all = min(NH, a.group - sp.head % a.group) * (D / 4);  // groups of 4 sums of the row
+  const int i0 = all * sp.index / shares, i1 = all * (sp.index + 1) / shares;
+  if (i0 == i1) return;
+  const int log = i1 - i0 >= kJoin ? 8 : 32 - __clz(i1 - i0 - 1);  // threads side by side: 1 << log
+  const int side = tid >> log, sides = kJoin >> log;                 // and at one group of sums
+  const float* p0 = a.parts + ((size_t)c0 * 2 + 1) * kPart;  // of the first CTA
+  const float* p1 = a.parts + (size_t)(c0 + 1) * 2 * kPart;  // of the others, 2 * kPart apart
   auto at = [&](int k) { return k == 0 ? p0 : p1 + (size_t)(k - 1) * 2 * kPart; };
-  const bool real = i < sp.nh * D;
-  const int hl = (tid & 63) * 4 / D, h0 = blockIdx.y * kJoin / D;  // the head among the CTA's, and their first
-  // the parts' maxima and sums, all of them in flight at once
-  float m = -INFINITY;
-  for (int k = tid; k < sp.parts * kHeads; k += kJoin) {
-    const int h = h0 + k % kHeads;
-    const float* src = at(k / kHeads) + NH * D + h;
-    const float pm = h < sp.nh ? __ldcg(src) : -INFINITY, pl = h < sp.nh ? __ldcg(src + NH) : 0.0f;
-    s_pm[k] = pm;
-    s_pl[k] = pl;
-  }
-  __syncthreads();
-  if (tid < 32 * kHeads) {  // a warp per head: weights instead of maxima
-    const int hh = tid >> 5, lane = tid & 31;
-    for (int k = lane; k < sp.parts; k += 32) m = fmaxf(m, s_pm[k * kHeads + hh]);
-    m = warp_max(m);
-    const float b = m == -INFINITY ? 0.0f : m;
-    float l = 0.0f;
-    for (int k = lane; k < sp.parts; k += 32) {
-      const float f = exp2_fast(s_pm[k * kHeads + hh] - b);
-      s_pm[k * kHeads + hh] = f;
-      l = fmaf(s_pl[k * kHeads + hh], f, l);
-    }
+  for (int first = i0; first < i1; first += kJoin) {
+    const int i = first + (tid & ((1 << log) - 1)), h = i * 4 / D;
+    float m = -INFINITY, l = 0.0f;
+    float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    auto add = [&](float pm, float pl, const float4& o) {
+      const float to = fmaxf(m, pm), b = to == -INFINITY ? 0.0f : to;
+      const float f = exp2_fast(m - b), g = exp2_fast(pm - b);
+      m = to;
+      l = fmaf(pl, g, l * f);
+      v.x = fmaf(o.x, g, v.x * f);
+      v.y = fmaf(o.y, g, v.y * f);
+      v.z = fmaf(o.z, g, v.z * f);
+      v.w = fmaf(o.w, g, v.w * f);
+    };
+    if (i < i1) {
+      constexpr int kFlight = 4;  // parts in flight per thread
+      for (int k0 = side; k0 < sp.parts; k0 += kFlight * sides) {
+        float4 o[kFlight];
+        float pm[kFlight], pl[kFlight];
 #pragma unroll
-    for (int o = 16; o >= 1; o >>= 1) l += __shfl_xor_sync(kAll, l, o);
-    if (lane == 0) {
-      s_max[hh] = b;
-      s_l[hh] = l;
-    }
-  }
-  __syncthreads();
-  float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-  constexpr int kFlight = 20;  // parts in flight per thread
-  for (int k0 = quarter; k0 < sp.parts; k0 += 4 * kFlight) {
-    float4 o[kFlight];
+        for (int k = 0; k < kFlight; ++k)
+          if (k0 + k * sides < sp.parts) {
+            const float* part = at(k0 + k * sides);
+            o[k] = __ldcg(reinterpret_cast<const float4*>(part) + i);
+            pm[k] = __ldcg(part + NH * D + h);
+            pl[k] = __ldcg(part + NH * D + NH + h);
+          }
 #pragma unroll
-    for (int k = 0; k < kFlight; ++k)
-      if (real && k0 + 4 * k < sp.parts) o[k] = __ldcg(reinterpret_cast<const float4*>(at(k0 + 4 * k) + i));
-#pragma unroll
-    for (int k = 0; k < kFlight; ++k)
-      if (real && k0 + 4 * k < sp.parts) {
-        const float f = s_pm[(k0 + 4 * k) * kHeads + hl];
-        v.x = fmaf(o[k].x, f, v.x);
-        v.y = fmaf(o[k].y, f, v.y);
-        v.z = fmaf(o[k].z, f, v.z);
-        v.w = fmaf(o[k].w, f, v.w);
+        for (int k = 0; k < kFlight; ++k)
+          if (k0 + k * sides < sp.parts) add(pm[k], pl[k], o[k]);
       }
+    }
+    for (int n = kJoin / 2; n >= 1 << log; n >>= 1) {  // halves: the upper threads' sums to the lower
+      if (tid >= n && tid < 2 * n) s_v[tid] = v, s_m[tid] = m, s_l[tid] = l;
+      __syncthreads();
+      if (tid < n) add(s_m[tid + n], s_l[tid + n], s_v[tid + n]);
+    }
+    if (side != 0 || i >= i1) continue;
+    const float inv = 1.0f / l;
+    uint16_t* orow = a.out + (int64_t)sp.seq * a.ldo + (int64_t)sp.head * D;
+    *reinterpret_cast<uint2*>(orow + i * 4) =
+        make_uint2(pack2<BF16>(v.x * inv, v.y * inv), pack2<BF16>(v.z * inv, v.w * inv));
+    if (a.lse && i * 4 % D == 0)
+      a.lse[(int64_t)sp.seq * a.heads * a.group + sp.head + h] =
+          ((m == -INFINITY ? 0.0f : m) + log2f(l) - kLift) * 0.6931471805599453f;
   }
-  s_acc[quarter][tid & 63] = v;
-  __syncthreads();
-  if (quarter != 0 || !real) return;
-  const float l = s_l[hl], b = s_max[hl];
-#pragma unroll
-  for (int k = 1; k < 4; ++k) {
-    const float4 o = s_acc[k][tid & 63];
-    v.x += o.x, v.y += o.y, v.z += o.z, v.w += o.w;
-  }
-  const float inv = 1.0f / l;
-  uint16_t* orow = a.out + (int64_t)sp.seq * a.ldo + (int64_t)sp.head * D;
-  *reinterpret_cast<uint2*>(orow + i) = make_uint2(pack2<BF16>(v.x * inv, v.y * inv), pack2<BF16>(v.z * inv, v.w * inv));
-  if (a.lse && i % D == 0)
-    a.lse[(int64_t)sp.seq * a.heads * a.group + sp.head + h0 + hl] = (b + log2f(l) - kLift) * 0.6931471805599453f;
 }
 
 // Heads of a tile: 8, or 16 where the group has more and the accumulators fit.
@@ -835,9 +827,8 @@ moe_status launch(const AttendArgs& a, bool bf16, cudaStream_t st) {
   dependent.id = cudaLaunchAttributeProgrammaticStreamSerialization;
   dependent.val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(grid, NT * 8 * D / kJoin);
+  cfg.gridDim = dim3(grid);
   cfg.blockDim = dim3(kJoin);
-  cfg.dynamicSmemBytes = (size_t)grid * (kJoin / D < 1 ? 1 : kJoin / D) * 8;  // a maximum and a sum per part and head
   cfg.stream = st;
   cfg.attrs = &dependent;
   cfg.numAttrs = 1;
