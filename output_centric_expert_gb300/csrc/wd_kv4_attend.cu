@@ -654,63 +654,74 @@ __global__ void __launch_bounds__(W * 32, CTAS) kv4_attend_kernel(const AttendAr
     float* part = a.parts + ((size_t)blockIdx.x * 2 + (sg.begins ? 1 : 0)) * kPart;
     uint16_t* orow = a.out + (int64_t)sg.seq * a.ldo + (int64_t)sg.head * D;
     float* lrow = a.lse ? a.lse + (int64_t)sg.seq * a.heads * a.group + sg.head : nullptr;
+    // every warp's weights against the CTA's maximum first: then its sums only add
+    if (g == 0)
 #pragma unroll
-    for (int n = 0; n < NT; ++n) {
-      float* mine_sums = reinterpret_cast<float*>(ring + stage * L::kBytes);  // [8][D]
-      const float l0 = over_g_sum(st.l[n][0]), l1 = over_g_sum(st.l[n][1]);
-      if (g == 0) {
+      for (int n = 0; n < NT; ++n)
 #pragma unroll
         for (int c = 0; c < 2; ++c)
           s_m[warp][n * 8 + 2 * t + c] = st.m[n][c] == -INFINITY ? -INFINITY : st.m[n][c] * qs[n][c];
-        s_l[warp][n * 8 + 2 * t] = l0;
-        s_l[warp][n * 8 + 2 * t + 1] = l1;
+    __syncthreads();
+    auto top_of = [&](int h) {
+      float m = s_m[0][h];
+#pragma unroll
+      for (int w = 1; w < W; ++w) m = fmaxf(m, s_m[w][h]);
+      return m;
+    };
+    auto sum_of = [&](int h) {
+      float l = s_l[0][h];
+#pragma unroll
+      for (int w = 1; w < W; ++w) l += s_l[w][h];
+      return l;
+    };
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+      float* mine_sums = reinterpret_cast<float*>(ring + stage * L::kBytes);  // [8][D]
+      float f[2];
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        const int h = n * 8 + 2 * t + c;
+        const float m = top_of(h);
+        f[c] = exp2_fast(s_m[warp][h] - (m == -INFINITY ? 0.0f : m));
+        const float l = over_g_sum(st.l[n][c]) * f[c];
+        if (g == 0) s_l[warp][h] = l;
+        f[c] *= 0.001953125f;
       }
 #pragma unroll
       for (int b = 0; b < NB; ++b) {
         // the accumulators hold 2^2 p times 2^(9 - top) of the scale
-        const float f = e8m0_to_f32((st.top[b / 2] >> (16 * (b & 1))) & 255u) * 0.001953125f;
+        const float scale = e8m0_to_f32((st.top[b / 2] >> (16 * (b & 1))) & 255u);
 #pragma unroll
-        for (int c = 0; c < 2; ++c)
+        for (int c = 0; c < 2; ++c) {
+          const float up = scale * f[c];
           *reinterpret_cast<float4*>(mine_sums + (2 * t + c) * D + 32 * b + 4 * g) =
-              make_float4(st.acc[n][2 * b][c] * f, st.acc[n][2 * b][2 + c] * f,
-                          st.acc[n][2 * b + 1][c] * f, st.acc[n][2 * b + 1][2 + c] * f);
+              make_float4(st.acc[n][2 * b][c] * up, st.acc[n][2 * b][2 + c] * up,
+                          st.acc[n][2 * b + 1][c] * up, st.acc[n][2 * b + 1][2 + c] * up);
+        }
       }
       __syncthreads();
-      // 4 sums a thread; LW lanes have a head, and its warps' weights in their first W
-      constexpr int LW = D >= 128 ? 32 : 16;
-      static_assert(W <= LW, "a lane per warp's part");
-      for (int i0 = warp * 128; i0 < 8 * D; i0 += THREADS * 4) {
-        __syncwarp();
-        const int i = i0 + lane * 4, h = n * 8 + i / D, part_of = lane % LW;
-        const float pm = part_of < W ? s_m[part_of][h] : -INFINITY;
-        float m = pm;
-#pragma unroll
-        for (int o = LW / 2; o >= 1; o >>= 1) m = fmaxf(m, __shfl_xor_sync(kAll, m, o));
-        const float b = m == -INFINITY ? 0.0f : m, f = exp2_fast(pm - b);
-        float l = part_of < W ? s_l[part_of][h] * f : 0.0f;
-#pragma unroll
-        for (int o = LW / 2; o >= 1; o >>= 1) l += __shfl_xor_sync(kAll, l, o);
+      for (int i = tid * 4; i < 8 * D; i += THREADS * 4) {
+        const int h = n * 8 + i / D;
+        if (h >= sg.nh) break;
         float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll
         for (int w = 0; w < W; ++w) {
           const float4 o = *reinterpret_cast<const float4*>(smem + (size_t)(w * STAGES + stage) * L::kBytes + i * 4);
-          const float fw = __shfl_sync(kAll, f, w, LW);
-          v.x = fmaf(o.x, fw, v.x);
-          v.y = fmaf(o.y, fw, v.y);
-          v.z = fmaf(o.z, fw, v.z);
-          v.w = fmaf(o.w, fw, v.w);
+          v.x += o.x, v.y += o.y, v.z += o.z, v.w += o.w;
         }
-        if (h >= sg.nh) continue;
         if (whole) {
-          const float inv = 1.0f / l;
+          const float l = sum_of(h), inv = 1.0f / l;
           *reinterpret_cast<uint2*>(orow + n * 8 * D + i) =
               make_uint2(pack2<BF16>(v.x * inv, v.y * inv), pack2<BF16>(v.z * inv, v.w * inv));
-          if (lrow && i % D == 0) lrow[h] = (b + log2f(l) - kLift) * 0.6931471805599453f;
+          if (lrow && i % D == 0) {
+            const float m = top_of(h);
+            lrow[h] = ((m == -INFINITY ? 0.0f : m) + log2f(l) - kLift) * 0.6931471805599453f;
+          }
         } else {
           *reinterpret_cast<float4*>(part + n * 8 * D + i) = v;
           if (i % D == 0) {
-            part[NH * D + h] = m;
-            part[NH * D + NH + h] = l;
+            part[NH * D + h] = top_of(h);
+            part[NH * D + NH + h] = sum_of(h);
           }
         }
       }
