@@ -38,9 +38,13 @@ constexpr unsigned kAll = 0xFFFFFFFFu;
 constexpr float kLift = 2.0f;   // probabilities are held times 2^2
 constexpr float kSlack = 4.0f;  // and may be 2^4 above their reference: 2^6, times 2^9 at most, fits f16
 
-constexpr int kMinTiles = 2;    // tiles of a CTA of a split row, on average
-// What a row costs beside its tiles, in tiles: CTAs share both out.
-__host__ __device__ constexpr int row_units(int NT) { return NT == 2 ? 2 : 1; }
+// What a row costs beside its tiles (queries staged, sums joined), in tiles: CTAs share
+// both out. 1, 2, 3: 45.0, 43.6, 44.9 us for 64 sequences up to 4096 with 8 heads, 17.1,
+// 16.1, 16.1 for 16 up to 16384 of dim 64; 53.3, 52.0, 52.1 for 64 up to 8192 with 16 heads.
+constexpr int kRowUnits = 2;
+// Units of a CTA at least, on average, unless it has a row to itself: joining is cheap
+// (one sequence of 8192: 13.1 us with 4, 12.4 with 2).
+constexpr int kMinUnits = 2;
 
 // The split row that goes on from this CTA into the next, parts 0 where there is none:
 // a row with parts in the CTAs c .. c + parts - 1 is in all their entries but the last.
@@ -429,7 +433,7 @@ struct Segment {
 template <int D, int NT, int W, int STAGES, int CTAS, bool BF16>
 __global__ void __launch_bounds__(W * 32, CTAS) kv4_attend_kernel(const AttendArgs a) {
   using L = Stage<D>;
-  constexpr int TILE = W * kWarpKeys, THREADS = W * 32, kRowUnits = row_units(NT);
+  constexpr int TILE = W * kWarpKeys, THREADS = W * 32;
   constexpr int NB = D / 32;
   constexpr int NH = NT * 8;           // heads of a tile
   constexpr int kPart = NH * (D + 2);  // floats of a partial result: acc [NH][D], m [NH], l [NH]
@@ -490,9 +494,8 @@ __global__ void __launch_bounds__(W * 32, CTAS) kv4_attend_kernel(const AttendAr
     for (int i = tid; i < heads * D; i += THREADS) a.out[(int64_t)s * a.ldo + i] = 0;
     for (int i = tid; a.lse && i < heads; i += THREADS) a.lse[(int64_t)s * heads + i] = -INFINITY;
   }
-  // CTA c of G has units [c q + min(c, r), ...) with total = G q + r. Rows are not cut
-  // finer than kMinTiles tiles on average: joining parts costs more than a tile
-  const int G = min((int)gridDim.x, max(with_keys * rows, total / (kMinTiles + kRowUnits)));
+  // CTA c of G has units [c q + min(c, r), ...) with total = G q + r
+  const int G = min((int)gridDim.x, max(with_keys * rows, total / kMinUnits));
   if ((int)blockIdx.x >= G) return;
   const int gq = total / G, gr = total - G * gq;
   const int begin = (int)blockIdx.x * gq + min((int)blockIdx.x, gr);
@@ -828,7 +831,7 @@ moe_status launch(const AttendArgs& a, bool bf16, cudaStream_t st) {
   const int64_t most = a.window > 0 && a.window + 2 * kWarpKeys < keys ? a.window + 2 * kWarpKeys : keys;
   const int64_t row_tiles = (most + W * kWarpKeys - 1) / (W * kWarpKeys);
   const int64_t tiles = row_tiles * a.S * a.heads * a.head_tiles;
-  if ((row_tiles + row_units(NT)) * a.S * a.heads * a.head_tiles > 0x7FFFFFFF) return refuse(MOE_ERR_SHAPE, "wd_kv4_attend: block_table's capacity is too large");
+  if ((row_tiles + kRowUnits) * a.S * a.heads * a.head_tiles > 0x7FFFFFFF) return refuse(MOE_ERR_SHAPE, "wd_kv4_attend: block_table's capacity is too large");
   const int64_t fill = (int64_t)sm_count() * CTAS;
   const unsigned grid = (unsigned)(tiles < fill ? tiles : fill);
   k<<<grid, W * 32, ring, st>>>(a);
