@@ -11,7 +11,9 @@ namespace {
 // for all. The four threads of a 32-element block are neighbours: its largest magnitude
 // takes two shuffles. Both kernels are bound by integer instructions (conversions,
 // packing, addresses), so magnitudes are compared as 16-bit pairs and a thread steps
-// through its pieces without divisions.
+// through its pieces without divisions. Prompts of 9.7k tokens, 8 heads of dim 128, into
+// the cache and back (100 MB): 27.2 us, 3.7 TB/s; ALU 55 % busy, DRAM 27 %, 70 % of the
+// issue slots in larger batches. One token each of 64 sequences: 3.8 us a launch.
 
 struct TokenArgs {
   const int32_t *table, *lens, *cu;
@@ -246,7 +248,8 @@ TokenArgs token_args(const wd_kv4_cache* c, int64_t ldk, int64_t ldv, int32_t T,
   int h = 128 / piece < c->heads ? 128 / piece : c->heads;  // heads of a CTA
   while (c->heads % h) --h;
   const int chunk = h * piece;
-  // as many tokens per CTA as leave two CTAs per SM, up to 4 pieces a thread
+  // as many tokens per CTA as leave two CTAs per SM, up to 4 pieces a thread (the prompts above: 30.5 us
+  // with up to 2, 27.2 with 4, 31.3 with 8)
   int per = 2;
   while (per < kMostPer && 2 * per * chunk <= 4 * kThreads &&
          (int64_t)T * words >= 2ll * sm_count() * 2 * per * chunk)

@@ -21,10 +21,17 @@
 // lengths on the device, so ragged batches and single long sequences load the
 // SMs evenly and the host needs no lengths. In a tile each warp takes 32 keys by
 // itself, streamed through its own cp.async ring, which runs ahead into the CTA's
-// next row. The warps' sums join in shared memory. A row that several CTAs share leaves their parts in the
-// workspace; a second, dependent launch joins them in CTA order. (Joining in the
-// last CTA to finish, by a counter, took 11 us of 42 for 76 parts of one row: one
-// SM reads them all.)
+// next row. The warps' sums join in shared memory. A row that several CTAs share
+// leaves their parts in the workspace; a second, dependent launch joins them in CTA
+// order. (Joining in the last CTA to finish, by a counter, took 11 us of 42 for 76
+// parts of one row: one SM reads them all.)
+//
+// Bound. 64 sequences of up to 8192 keys with 16 heads per KV head (119 MB): 52 us,
+// 2.3 TB/s; one of 131071 with 8 heads (71 MB): 28 us, 2.5 TB/s. Decoding, scaling and
+// the softmax are about 780 instructions per warp and 32 keys for 16 heads (60 of them
+// MMAs, 128 conversions at half rate), issued in 44 % of the cycles: registers leave 12
+// to 16 warps per SM, too few to hide every dependency. The first 6 us are a chain of
+// trips to memory: lengths, block table, keys.
 #include "wd_block.cuh"
 #include "wd_kv4.cuh"
 
@@ -906,6 +913,9 @@ extern "C" moe_status wd_kv4_attend(const wd_kv4_cache* c, const void* q, int32_
   a.scale_log2 = scale * 1.4426950408889634f;
   cudaStream_t st = (cudaStream_t)stream;
   const bool bf16 = type == WD_BF16, wide = tile_heads(c, group) == 16;
+  // <dim, head tiles, warps, ring stages, CTAs per SM>. 16 heads of dim 128 take 168 registers: 2 x 6
+  // warps 63.8 us, 1 x 12 warps 67.3 (their barriers hold each other up); a fourth ring stage leaves room
+  // for one CTA only, 74 us against 52. Dim 256: 2 x 4 warps 52.8 us, 1 x 8 warps 54.0.
   if (c->dim == 64) return wide ? launch<64, 2, 8, 4, 2>(a, bf16, st) : launch<64, 1, 8, 4, 2>(a, bf16, st);
   if (c->dim == 128) return wide ? launch<128, 2, 6, 3, 2>(a, bf16, st) : launch<128, 1, 8, 3, 2>(a, bf16, st);
   return launch<256, 1, 4, 2, 2>(a, bf16, st);

