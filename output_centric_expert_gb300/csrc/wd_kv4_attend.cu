@@ -78,6 +78,24 @@ __device__ __forceinline__ void cp_async16(void* dst, const void* src, bool real
   const int n = real ? 16 : 0;  // 0: zeros, the source is not read
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(d), "l"(src), "r"(n) : "memory");
 }
+// 16 bytes, and 16 more elsewhere, where `here`; without a branch.
+__device__ __forceinline__ void copy16_if(bool here, uint32_t to, const uint8_t* from) {
+  asm volatile(
+      "{.reg .pred p;\n\t"
+      "setp.ne.u32 p, %2, 0;\n\t"
+      "@p cp.async.cg.shared.global [%0], [%1], 16;\n\t}" ::"r"(to),
+      "l"(from), "r"((uint32_t)here)
+      : "memory");
+}
+__device__ __forceinline__ void copy16_if(bool here, uint32_t to, const uint8_t* from, uint32_t to2, const uint8_t* from2) {
+  asm volatile(
+      "{.reg .pred p;\n\t"
+      "setp.ne.u32 p, %4, 0;\n\t"
+      "@p cp.async.cg.shared.global [%0], [%1], 16;\n\t"
+      "@p cp.async.cg.shared.global [%2], [%3], 16;\n\t}" ::"r"(to),
+      "l"(from), "r"(to2), "l"(from2), "r"((uint32_t)here)
+      : "memory");
+}
 __device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
 __device__ __forceinline__ void cp_async_wait() {
@@ -395,29 +413,24 @@ __device__ __forceinline__ void attend_keys(uint8_t* st, const uint8_t* qf, cons
   }
 }
 
-// Start copying the 32 keys from kb of (sequence, head) into a ring stage; page[u]
-// -1: zeros.
+// Start copying the 16-key runs run[0], run[1] of the cache (-1: none) into a ring stage. sc: this
+// lane's scales of run 0 (lanes below n K's, the next n V's), sc_to their place in a stage.
 template <int D>
-__device__ __forceinline__ void fetch(uint8_t* st, const AttendArgs& a, int head, uint32_t kb,
-                                      const int (&page)[2]) {
+__device__ __forceinline__ void fetch(uint8_t* st, const AttendArgs& a, const int (&run)[2], const uint8_t* sc,
+                                      uint32_t sc_to) {
   using L = Stage<D>;
+  constexpr int n = L::kScales / 16;
   const int lane = threadIdx.x & 31;
+  const uint32_t to = (uint32_t)__cvta_generic_to_shared(st);
 #pragma unroll
   for (int u = 0; u < 2; ++u) {
-    const bool real = page[u] >= 0;
-    const uint32_t slot = (kb + u * kSub) & ((1u << a.page_shift) - 1u);
-    const size_t at = real ? (((size_t)page[u] * a.heads + head) << a.page_shift) + slot : 0;
-    const uint8_t *kc = a.kc + at * (D / 2) + lane * 16, *vc = a.vc + at * (D / 2) + lane * 16;
+    const uint64_t at = (uint64_t)(uint32_t)run[u] * L::kCodes + lane * 16;
 #pragma unroll
     for (int i = 0; i < L::kCodes / 512; ++i) {
-      cp_async16(st + L::kK + u * L::kCodes + lane * 16 + 512 * i, kc + 512 * i, real);
-      cp_async16(st + L::kV + u * L::kCodes + lane * 16 + 512 * i, vc + 512 * i, real);
+      const uint32_t piece = to + u * L::kCodes + 512 * i + lane * 16;
+      copy16_if(run[u] >= 0, piece + L::kK, a.kc + at + 512 * i, piece + L::kV, a.vc + at + 512 * i);
     }
-    constexpr int n = L::kScales / 16;  // lanes 0 .. n - 1 copy K's scales, n .. 2n - 1 V's
-    if (lane < 2 * n) {
-      const uint8_t* sc = (lane < n ? a.ks : a.vs - n * 16) + at * (D / 32) + lane * 16;
-      cp_async16(st + (lane < n ? L::kKs : L::kVs - n * 16) + u * L::kScales + lane * 16, sc, real);
-    }
+    copy16_if(run[u] >= 0 && lane < 2 * n, to + sc_to + u * L::kScales, sc + (uint64_t)(uint32_t)run[u] * L::kScales);
   }
 }
 
@@ -523,9 +536,15 @@ __global__ void __launch_bounds__(W * 32, CTAS) kv4_attend_kernel(const AttendAr
   int f_units = units_of(f_seq, f_tiles, lo, hi);  // lo, hi: of f_seq from here on
   int f_segs = 0, f_i = 0, f_iters = 0, f_head = 0, f_stage = 0;
   uint32_t f_key = 0;  // the warp's first key of the segment
-  int held = -1;       // pages of 16-key runs: lane l has run (l & 1) of iteration (l >> 1) of 16
+  // 16-key runs, counted through the cache ([page][head][run of the page]), -1 without a page:
+  // lane l has run (l & 1) of iteration (l >> 1) of 16
+  int held = -1;
   uint32_t ok = 0;     // two bits per iteration in flight, the oldest lowest: runs with a page
   int lead = 0;        // iterations in flight
+  const int run_shift = a.page_shift - 4;
+  constexpr int kScaleLanes = L::kScales / 16;
+  const uint8_t* sc_from = lane < kScaleLanes ? a.ks + lane * 16 : a.vs + (lane - kScaleLanes) * 16;
+  const uint32_t sc_to = lane < kScaleLanes ? L::kKs + lane * 16 : L::kVs + (lane - kScaleLanes) * 16;
   auto next_segment = [&]() {
     while (f_unit < end) {
       while (f_unit >= f_base + f_units) {
@@ -567,19 +586,19 @@ __global__ void __launch_bounds__(W * 32, CTAS) kv4_attend_kernel(const AttendAr
         const uint32_t key = f_key + (uint32_t)(f_i + (lane >> 1)) * TILE + (lane & 1) * kSub;
         held = -1;
         if (f_i + (lane >> 1) < f_iters && key < hi && key + kSub > lo) {
-          held = __ldg(a.table + (int64_t)f_seq * a.max_blocks + (key >> a.page_shift));
-          if (held < 0 || held >= a.pages) {
-            held = -1;
+          const int page = __ldg(a.table + (int64_t)f_seq * a.max_blocks + (key >> a.page_shift));
+          if (page < 0 || page >= a.pages)
             flag_invalid(a.err);
-          }
+          else
+            held = ((page * a.heads + f_head) << run_shift) + (int)((key >> 4) & ((1u << run_shift) - 1u));
         }
       }
-      int page[2];
-      page[0] = __shfl_sync(kAll, held, (f_i & 15) * 2);
-      page[1] = __shfl_sync(kAll, held, (f_i & 15) * 2 + 1);
-      fetch<D>(ring + f_stage * L::kBytes, a, f_head, f_key + (uint32_t)f_i * TILE, page);
+      int run[2];
+      run[0] = __shfl_sync(kAll, held, (f_i & 15) * 2);
+      run[1] = __shfl_sync(kAll, held, (f_i & 15) * 2 + 1);
+      ok |= ((run[0] >= 0 ? 1u : 0u) | (run[1] >= 0 ? 2u : 0u)) << (2 * lead);
+      fetch<D>(ring + f_stage * L::kBytes, a, run, sc_from, sc_to);
       cp_async_commit();
-      ok |= ((page[0] >= 0 ? 1u : 0u) | (page[1] >= 0 ? 2u : 0u)) << (2 * lead);
       f_stage = f_stage + 1 == STAGES ? 0 : f_stage + 1;
       ++lead;
       ++f_i;
@@ -899,6 +918,8 @@ extern "C" moe_status wd_kv4_attend(const wd_kv4_cache* c, const void* q, int32_
     return refuse(MOE_ERR_ALIGN, "wd_kv4_attend: q, out and workspace need 16 bytes, strides % 8 == 0, the others 4");
   if (workspace_bytes < wd_kv4_attend_workspace(c, S, q_heads))
     return refuse(MOE_ERR_SHAPE, "wd_kv4_attend: workspace is smaller than wd_kv4_attend_workspace");
+  if ((int64_t)c->pages * c->heads * (c->page_size / kSub) > 0x7FFFFFFF)  // 1 TB of codes
+    return refuse(MOE_ERR_SHAPE, "wd_kv4_attend: the cache has too many pages");
   const int group = q_heads / c->heads;
   const unsigned grid = (unsigned)(sm_count() * kMaxCtasPerSm);
   AttendArgs a = {};
