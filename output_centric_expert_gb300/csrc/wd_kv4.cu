@@ -12,8 +12,8 @@ namespace {
 // takes two shuffles. Both kernels are bound by integer instructions (conversions,
 // packing, addresses), so magnitudes are compared as 16-bit pairs and a thread steps
 // through its pieces without divisions. Prompts of 9.7k tokens, 8 heads of dim 128, into
-// the cache and back (100 MB): 27.2 us, 3.7 TB/s; ALU 55 % busy, DRAM 27 %, 70 % of the
-// issue slots in larger batches. One token each of 64 sequences: 3.8 us a launch.
+// the cache and back (100 MB): 27.5 us, 3.6 TB/s; ALU 55 % busy, DRAM 27 %, 70 % of the
+// issue slots in larger batches. One token each of 64 sequences: 3.7 us a launch.
 
 struct TokenArgs {
   const int32_t *table, *lens, *cu;
@@ -31,6 +31,7 @@ struct Place {
   bool before, behind;
 };
 constexpr int kMostPer = 64;
+constexpr int kResident = 6;  // CTAs of an SM: both loads of a thread in flight take 39 registers
 
 __device__ __forceinline__ Place place_of(const TokenArgs& a, int tok, bool flag) {
   Place p = {-1, 0, false, false};
@@ -89,7 +90,7 @@ __device__ __forceinline__ uint32_t spread4(uint32_t x) {
 }
 
 template <int D, bool BF16>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreads, kResident)
     kv4_append_kernel(const uint16_t* __restrict__ k, const uint16_t* __restrict__ v,
                       uint8_t* __restrict__ kc, uint8_t* __restrict__ ks, uint8_t* __restrict__ vc,
                       uint8_t* __restrict__ vs, const TokenArgs a) {
@@ -100,8 +101,7 @@ __global__ void __launch_bounds__(kThreads)
   if (tid <= a.per) s_place[tid] = place_of(a, tok0 + tid, tid < a.per);
   __syncthreads();
   // the scale code of a piece's block, and its codes
-  auto quantise = [&](const uint16_t* src, unsigned quad, uint32_t& scale) {
-    const uint4 raw = ld_cached16(src);
+  auto quantise = [&](const uint4& raw, unsigned quad, uint32_t& scale) {
     // magnitudes as 16-bit integers, two to a word (NaN above infinity above the rest)
     const uint32_t two = __vmaxu2(__vmaxu2(raw.x & 0x7FFF7FFFu, raw.y & 0x7FFF7FFFu),
                                   __vmaxu2(raw.z & 0x7FFF7FFFu, raw.w & 0x7FFF7FFFu));
@@ -124,12 +124,15 @@ __global__ void __launch_bounds__(kThreads)
     if (p.page < 0) continue;  // the four threads of a block alike
     const int head = w / (D / 8), b = w % (D / 8) >> 2, t = w & 3;
     const int64_t tok = tok0 + j;
+    const uint4 raw_v = ld_cached16(v + tok * a.ldv + w * 8);
+    uint4 raw_k;
+    if (j < a.per) raw_k = ld_cached16(k + tok * a.ldk + w * 8);
     uint32_t sv;
-    s_code[i] = quantise(v + tok * a.ldv + w * 8, quad, sv);
+    s_code[i] = quantise(raw_v, quad, sv);
     if (t == 0) s_scale[i >> 2] = (uint8_t)sv;
     if (j == a.per) continue;
     uint32_t sk;
-    const uint32_t code = quantise(k + tok * a.ldk + w * 8, quad, sk);
+    const uint32_t code = quantise(raw_k, quad, sk);
     const size_t at = ((size_t)p.page * a.heads + head) << a.page_shift;  // in tokens
     *reinterpret_cast<uint32_t*>(kc + at * (D / 2) + k_word<D>(p.slot, t, b)) = code;
     if (t == 0) ks[at * (D / 32) + p.slot * (D / 32) + b] = (uint8_t)sk;
@@ -248,12 +251,13 @@ TokenArgs token_args(const wd_kv4_cache* c, int64_t ldk, int64_t ldv, int32_t T,
   int h = 128 / piece < c->heads ? 128 / piece : c->heads;  // heads of a CTA
   while (c->heads % h) --h;
   const int chunk = h * piece;
-  // as many tokens per CTA as leave two CTAs per SM, up to 4 pieces a thread (the prompts above: 30.5 us
-  // with up to 2, 27.2 with 4, 31.3 with 8)
-  int per = 2;
-  while (per < kMostPer && 2 * per * chunk <= 4 * kThreads &&
-         (int64_t)T * words >= 2ll * sm_count() * 2 * per * chunk)
-    per *= 2;
+  // tokens of a CTA: up to 8 pieces a thread, in whole waves of resident CTAs. (Powers of two up to 4
+  // pieces: 15.6 us instead of 13.1 for 16 prompts of up to 2000, 8 heads of dim 64.)
+  const int64_t runs = (int64_t)T * (words / chunk), slots = (int64_t)sm_count() * kResident;
+  const int most = 8 * kThreads / chunk < kMostPer ? 8 * kThreads / chunk : kMostPer;
+  const int64_t waves = (runs + slots * most - 1) / (slots * most);
+  const int64_t even = (runs + slots * waves - 1) / (slots * waves);
+  const int per = even < 2 ? 2 : (int)even;
   return {table, lens, cu, err, ldk, ldv, T, S, max_blocks, c->pages, kv4_page_shift(c->page_size),
           c->heads, per, chunk};
 }
