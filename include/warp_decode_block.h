@@ -146,6 +146,7 @@ moe_status wd_kv4_gather(const wd_kv4_cache* cache, void* k_out, void* v_out, in
  * with the same inputs.
  * workspace: wd_kv4_attend_workspace bytes, 16-byte aligned; its contents do not
  * matter before or after a call. Calls that may overlap need one each.
+ * pages * heads * (page_size / 16) < 2^31, 1 TB of codes.
  */
 size_t wd_kv4_attend_workspace(const wd_kv4_cache* cache, int32_t S, int32_t q_heads);
 moe_status wd_kv4_attend(const wd_kv4_cache* cache, const void* q, int32_t type, int64_t ldq,

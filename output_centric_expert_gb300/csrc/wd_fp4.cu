@@ -87,9 +87,10 @@ __global__ void __launch_bounds__(kThreads)
 // fragment: [column tile][block][lane][16 bytes]. Row tiles that warps share are
 // joined in shared memory in column order, so results do not depend on timing.
 //   Bound by the codes' bytes where the matrix is large: 8 tokens of 129283 x 2048
-// (145 MB) take 30.4 us, 4.8 TB/s, 70 % of a copy. 12, 20 and 24 warps: 32.2, 31.7, 34.4
-// us; 3 and 5 column tiles ahead: 30.8 and 31.2. Small products are latency: one token of
-// 4096 x 2048 4.9 us, of which 2.5 are the launch and 1 is the trip for x.
+// (145 MB) take 29.2 us, 5.0 TB/s, 73 % of a copy. 16 warps and 4 column tiles ahead of
+// each: 12, 20 and 24 warps took 6, 4 and 13 % longer, 3 and 5 column tiles 1 and 2 %.
+// Small products are latency: one token of 4096 x 2048 4.9 us, of which 2.5 are the
+// launch and 1 is the trip for x.
 
 constexpr int kMvWarps = 16, kMvThreads = kMvWarps * 32;
 constexpr int kMvTokens = 8;  // of a launch: the columns of an MMA
@@ -133,11 +134,15 @@ __device__ __forceinline__ void stage_x(const MvArgs& a, int c0, int c1, int tok
   __syncthreads();
 }
 
-// CHUNKED: x is staged a.chunk column tiles at a time, the sums of a batch of row
-// tiles wait in shared memory; else all of x is staged once and a warp's run is one
-// dense stretch of memory.
-template <bool BF16, bool CHUNKED>
+// kChunked: x is staged a.chunk column tiles at a time, the sums of a batch of row tiles
+// wait in shared memory. Else all of x is staged once and a warp's run is one dense
+// stretch of memory; its row tiles' sums wait too (kWait), or a row tile that the run has
+// all of is written as it ends (kDirect: more code for each, and no burst of writes behind
+// the loads).
+enum Mode { kWait, kDirect, kChunked };
+template <bool BF16, Mode MODE>
 __global__ void __launch_bounds__(kMvThreads, 1) fp4_matvec_kernel(const MvArgs a) {
+  constexpr bool CHUNKED = MODE == kChunked;
   extern __shared__ uint4 dyn4[];
   __shared__ uint32_t s_max[kMvTokens];
   constexpr int kSums = kTileRows * kMvTokens;  // of a row tile: [token][row]
@@ -200,6 +205,21 @@ __global__ void __launch_bounds__(kMvThreads, 1) fp4_matvec_kernel(const MvArgs 
           acc[c] = 0.0f;
         }
       };
+      int q = q0 + t0;  // kDirect: the row tile at hand, and what tokens 2t and 2t + 1 are multiplied by
+      float back[2];
+      if (MODE == kDirect)
+#pragma unroll
+        for (int c = 0; c < 2; ++c) back[c] = exp2i(-shift_of_16<BF16>(s_max[2 * t + c]));
+      auto write = [&]() {  // 32 bytes of a token and more from 8 lanes
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          const int64_t row = (int64_t)q * kTileRows + g + 8 * (c >> 1);
+          const int tok = 2 * t + (c & 1);
+          if (tok < toks && row < a.N)
+            store_elem(a.y, a.y_type, (int64_t)(a.tok0 + tok) * a.ldy + row, acc[c] * back[c & 1]);
+          acc[c] = 0.0f;
+        }
+      };
       auto use = [&](const Tile& b) {
         const uint32_t wl[4] = {b.lo.x, b.lo.y, b.lo.z, b.lo.w}, wh[4] = {b.hi.x, b.hi.y, b.hi.z, b.hi.w};
         float sl[4], sh[4];
@@ -223,7 +243,11 @@ __global__ void __launch_bounds__(kMvThreads, 1) fp4_matvec_kernel(const MvArgs 
         }
         xk += 4 * 32;
         if (++k == kt) {
-          finish(to);
+          if (MODE == kDirect && to == whole)
+            write();
+          else
+            finish(to);
+          ++q;
           k = 0;
           xk = xs + lane;
           whole += kSums;
@@ -252,6 +276,7 @@ __global__ void __launch_bounds__(kMvThreads, 1) fp4_matvec_kernel(const MvArgs 
       for (int q = warp; q < nq; q += kMvWarps) {  // a warp per row tile
         // the warps that have its first and last column tile; a lane has 4 rows of a token
         const int w0 = ((q * kt + 1) * kMvWarps - 1) / units, w1 = ((q + 1) * kt * kMvWarps - 1) / units;
+        if (MODE == kDirect && w0 == w1) continue;
         const int o = lane * 4, tok = o / kTileRows;
         float4 v = *reinterpret_cast<const float4*>(w0 == w1 ? s_sum[q] + o : s_part[w0][1] + o);
         for (int w = w0 + 1; w <= w1; ++w) {
@@ -288,8 +313,8 @@ int64_t padded_words(const wd_fp4_shape* s) {
 
 template <bool BF16>
 moe_status launch_matvec(MvArgs a, cudaStream_t st) {
-  static SmemOnce once[2];
-  auto k = fp4_matvec_kernel<BF16, false>;
+  static SmemOnce once[3];
+  Mode mode = kWait;
   constexpr size_t kTileX = (size_t)4 * 32 * 16;  // x of a column tile
   constexpr size_t kTileSum = (size_t)kTileRows * kMvTokens * 4;
   constexpr size_t kRoom = kMaxDynSmem - kStaticSmem - kMvWarps * 2 * kTileSum;
@@ -305,15 +330,20 @@ moe_status launch_matvec(MvArgs a, cudaStream_t st) {
     const int64_t fit = (int64_t)((kRoom - ct * kTileX) / kTileSum);
     a.chunk = ct;
     a.batch = (int)(per < fit ? per : fit);
+    // us for 8 tokens: 129283 x 2048 (54 row tiles a CTA) 28.9 written as they end, 30.5 waiting;
+    // 65536 x 4096 (27) 30.0 and 30.7; 9216 x 4096 (4) 10.5 and 10.4; 2048 x 2048 (1) 5.9 and 5.6
+    if (per >= kMvWarps) mode = kDirect;
     smem = ct * kTileX + a.batch * kTileSum;
   } else {  // columns in chunks of 128 KB of x
-    k = fp4_matvec_kernel<BF16, true>;
+    mode = kChunked;
     a.chunk = 64;
     a.batch = (int)(per < 32 ? per : 32);
     smem = a.chunk * kTileX + 2 * a.batch * kTileSum;
   }
   smem += kMvWarps * 2 * kTileSum;
-  moe_status rc = once[a.chunk < ct].allow(k, kMaxDynSmem - kStaticSmem);
+  auto k = mode == kWait ? fp4_matvec_kernel<BF16, kWait> : mode == kDirect ? fp4_matvec_kernel<BF16, kDirect>
+                                                                            : fp4_matvec_kernel<BF16, kChunked>;
+  moe_status rc = once[mode].allow(k, kMaxDynSmem - kStaticSmem);
   if (rc != MOE_OK) return rc;
   for (a.tok0 = 0; a.tok0 < a.B; a.tok0 += kMvTokens) {
     k<<<grid, kMvThreads, smem, st>>>(a);
@@ -378,8 +408,8 @@ extern "C" moe_status wd_fp4_matvec(const wd_fp4_shape* s, const uint8_t* pc, co
   const MvArgs a = {pc, ps, static_cast<const uint16_t*>(x), y, ldx, ldy, B, y_type, s->N, s->K, 0, 0, 0};
   cudaStream_t st = (cudaStream_t)stream;
   // Up to 8 tokens (and where rows are too long for the other kernel's shared memory) the stream kernel:
-  // it reads the weights once per 8 tokens. us for 8 and 9 tokens: 10.3 and 18.0 against 11.9 and 11.5 for
-  // 9216 x 4096, 5.7 and 9.7 against 7.3 and 6.9 for 2048 x 2048, 31 and 60 against 50 and 42 for 65536 x 4096.
+  // it reads the weights once per 8 tokens. us for 8 and 9 tokens: 10.3 and 18.0 against 11.9 and 10.8 for
+  // 9216 x 4096, 5.7 and 9.7 against 7.3 and 6.9 for 2048 x 2048, 30 and 59 against 50 and 42 for 65536 x 4096.
   if (B > 8 && s->K <= tc_most_columns(B)) return launch_tc(a, x_type == WD_BF16, st);
   return x_type == WD_BF16 ? launch_matvec<true>(a, st) : launch_matvec<false>(a, st);
 }

@@ -116,6 +116,12 @@ def test_attend_refuses_before_launch(change, status):
                                          a["bytes"], None, None) == status
 
 
+def test_attend_refuses_a_cache_of_too_many_runs():
+    c = ctypes.byref(block_ops.Kv4Struct(1 << 27, 256, 2, 128, P, P, P, P))
+    assert block_ops.lib().wd_kv4_attend(c, P, 1, 512, 2, 4, P, 4, P, 1.0, 0, P, 512, P, P, 1 << 30, None, None) == SHAPE
+    assert b"too many pages" in block_ops.lib().moe_last_error()
+
+
 @pytest.mark.parametrize("change,status", [
     (dict(T=0, res=None), 0),
     (dict(res=None), NULL), (dict(w_pre=None), NULL), (dict(out=None), NULL), (dict(y=None), NULL),

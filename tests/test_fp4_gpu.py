@@ -109,6 +109,19 @@ def test_shapes_types_and_strides(N, K, B, xk, yk):
     assert (wide[:, N:] == 7.0).all()  # nothing beside the rows is written
 
 
+@pytest.mark.parametrize("yk", ["f32", "bf16"])
+@pytest.mark.parametrize("N,K,B", [(40003, 160, 8), (40003, 96, 16), (24001, 1152, 40)])
+def test_many_rows(N, K, B, yk):
+    """More rows than the CTAs take at a time: written as they end, in rounds, in rounds of clusters."""
+    rng = np.random.default_rng(N + B)
+    w, w64, *_ = _weights(rng, N, K)
+    x = _x(rng, B, K, "bf16")
+    wide = torch.full((B, N + 3), 7.0, dtype=TYPES[yk], device="cuda")
+    block_ops.wd_fp4_matvec(w, x, wide[:, :N])
+    _close(wide[:, :N], x, w64, yk)
+    assert (wide[:, N:] == 7.0).all()
+
+
 @pytest.mark.parametrize("B", [1, 12, 40])
 def test_extremes(B):
     """Zero tokens, loud channels, infinities and NaN stay where they belong; scale codes 0, 254 and 255."""
