@@ -178,6 +178,20 @@ moe_status wd_block_norm(int32_t T, int32_t H, const void* res, int32_t res_type
                          int32_t gate_step, float res_scale, float eps, void* res_out,
                          int64_t ldro, void* out, int32_t out_type, int64_t ldo, void* stream);
 
+/* ------------------------------------------------- arguments as a block -- */
+
+/* wd_call -- the entry point `which` with its arguments, 8 bytes each, in their
+ * order: integers and pointers as int64, floats as double. For bindings that pay
+ * per argument; the result and the errors are the entry point's. */
+enum {
+  WD_CALL_FP4_MATVEC = 0,
+  WD_CALL_KV4_APPEND = 1,
+  WD_CALL_KV4_GATHER = 2,
+  WD_CALL_KV4_ATTEND = 3,
+  WD_CALL_BLOCK_NORM = 4
+};
+moe_status wd_call(int32_t which, const void* args);
+
 #ifdef __cplusplus
 }
 #endif

@@ -1,6 +1,7 @@
 """Thin Python binding of the operators around the MoE layer (``include/warp_decode_block.h``).
 
-Every ``wd_*`` function has the name of the C entry point it calls, checks
+Every ``wd_*`` function has the name of the C entry point it calls (through
+``wd_call``, its arguments as one block), checks
 tensor metadata, extracts pointers and raises on a non-OK status, as in
 :mod:`ops`. Outputs are the caller's tensors, work is enqueued on ``stream``
 (default: the current stream), and nothing synchronises. Tensors may have any
@@ -14,6 +15,7 @@ row stride the entry point takes; their last axis is dense.
 from __future__ import annotations
 
 import ctypes
+from struct import Struct
 
 import torch
 
@@ -38,6 +40,13 @@ class Kv4Struct(ctypes.Structure):
 
 
 _lib_cache = None  # the entry points read it directly: a call's marshalling is a few us, as long as a small kernel
+
+# wd_call: number and arguments of the entry points of a decode step (q: integers and pointers, d: floats)
+_MATVEC, _APPEND, _GATHER, _ATTEND, _NORM = range(5)
+_matvec_args = Struct("11q").pack
+_token_args = Struct("14q").pack
+_attend_args = Struct("9qd8q").pack
+_norm_args = Struct("14q2d6q").pack
 
 
 def lib() -> ctypes.CDLL:
@@ -66,6 +75,8 @@ def lib() -> ctypes.CDLL:
             fn = getattr(L, name)
             fn.restype = ctypes.c_int
             fn.argtypes = args
+        L.wd_call.restype = ctypes.c_int
+        L.wd_call.argtypes = [i32, ctypes.c_char_p]
         _lib_cache = L
     return _lib_cache
 
@@ -74,7 +85,7 @@ def exported_symbols() -> list[str]:
     """The entry points include/warp_decode_block.h declares."""
     return ["wd_fp4_packed_bytes", "wd_fp4_pack_codes", "wd_fp4_pack_weights", "wd_fp4_matvec",
             "wd_kv4_cache_bytes", "wd_kv4_append", "wd_kv4_gather", "wd_kv4_attend_workspace",
-            "wd_kv4_attend", "wd_block_norm"]
+            "wd_kv4_attend", "wd_block_norm", "wd_call"]
 
 
 def _check(fn: str, status: int) -> None:
@@ -82,9 +93,9 @@ def _check(fn: str, status: int) -> None:
         raise WarpDecodeError(fn, status, lib().moe_last_error().decode())
 
 
-def _stream(stream, t: torch.Tensor) -> int | None:
+def _stream(stream, t: torch.Tensor) -> int:
     if stream is None:
-        return _raw_stream(t.get_device()) if t.is_cuda else None
+        return _raw_stream(t.get_device()) if t.is_cuda else 0
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else stream
 
 
@@ -130,7 +141,7 @@ class Fp4Weights:
 
     def __init__(self, N: int, K: int, device="cuda"):
         self.shape = Fp4Shape(N, K)
-        self._shape = ctypes.byref(self.shape)
+        self._shape, self._at = ctypes.byref(self.shape), ctypes.addressof(self.shape)
         sizes = [int(lib().wd_fp4_packed_bytes(self._shape, w)) for w in (0, 1)]
         if not all(sizes):
             raise ValueError(f"Fp4Weights: unsupported shape [{N}, {K}] (K % 32 == 0, 32 <= K <= 65536)")
@@ -169,9 +180,9 @@ def wd_fp4_matvec(weights: Fp4Weights, x: torch.Tensor, y: torch.Tensor, stream=
     """y[B, N] = x[B, K] W^T; x bfloat16 or float16, y float32, bfloat16 or float16."""
     B, K, N = x.shape[0], weights.K, weights.N
     codes, scales = weights._ptrs
-    status = _lib_cache.wd_fp4_matvec(
-        weights._shape, codes, scales, x.data_ptr(), _type(x, "x"), _rows(x, (B, K), K, "x"), B,
-        y.data_ptr(), _type(y, "y"), _rows(y, (B, N), N, "y"), _stream(stream, x))
+    status = _lib_cache.wd_call(_MATVEC, _matvec_args(
+        weights._at, codes, scales, x.data_ptr(), _type(x, "x"), _rows(x, (B, K), K, "x"), B,
+        y.data_ptr(), _type(y, "y"), _rows(y, (B, N), N, "y"), _stream(stream, x)))
     if status:
         _check("wd_fp4_matvec", status)
     return y
@@ -185,7 +196,7 @@ class Kv4Cache:
     def __init__(self, pages: int, page_size: int, heads: int, dim: int, device="cuda"):
         self.pages, self.page_size, self.heads, self.dim = pages, page_size, heads, dim
         self.struct = Kv4Struct(pages, page_size, heads, dim)
-        self._ref = ctypes.byref(self.struct)
+        self._ref, self._at = ctypes.byref(self.struct), ctypes.addressof(self.struct)
         codes, scales = (int(lib().wd_kv4_cache_bytes(self._ref, w)) for w in (0, 1))
         if not codes:
             raise ValueError(f"Kv4Cache: unsupported sizes: pages {pages}, page_size {page_size} (16 to 256, a power "
@@ -199,17 +210,17 @@ class Kv4Cache:
         return sum(t.numel() for t in self.tensors)
 
 
-def _tokens(fn: str, call, cache: Kv4Cache, k, v, block_table, seq_lens, cu_new, err_flag, stream) -> None:
+def _tokens(fn: str, which: int, cache: Kv4Cache, k, v, block_table, seq_lens, cu_new, err_flag, stream) -> None:
     T, S, blocks = k.shape[0], seq_lens.shape[0], block_table.shape[-1]
     if v.dtype != k.dtype:
         raise TypeError(f"v: dtype {v.dtype} differs from k's {k.dtype}")
     row = cache.heads * cache.dim
     shape = (T, cache.heads, cache.dim)
-    status = call(
-        cache._ref, k.data_ptr(), v.data_ptr(), _type(k, "k"), _rows(k, shape, row, "k"), _rows(v, shape, row, "v"), T,
+    status = _lib_cache.wd_call(which, _token_args(
+        cache._at, k.data_ptr(), v.data_ptr(), _type(k, "k"), _rows(k, shape, row, "k"), _rows(v, shape, row, "v"), T,
         _ints(block_table, (S, blocks), "block_table"), blocks, _ints(seq_lens, (S,), "seq_lens"),
-        None if cu_new is None else _ints(cu_new, (S + 1,), "cu_new"), S,
-        None if err_flag is None else _flag(err_flag), _stream(stream, k))
+        0 if cu_new is None else _ints(cu_new, (S + 1,), "cu_new"), S,
+        0 if err_flag is None else _flag(err_flag), _stream(stream, k)))
     if status:
         _check(fn, status)
 
@@ -219,7 +230,7 @@ def wd_kv4_append(cache: Kv4Cache, k: torch.Tensor, v: torch.Tensor, block_table
                   err_flag: torch.Tensor | None = None, stream=None) -> Kv4Cache:
     """Quantise the new tokens k, v [T, heads, dim] into the cache behind seq_lens[s] tokens of each
     sequence; cu_new [S + 1] says which rows are whose (None: one each)."""
-    _tokens("wd_kv4_append", _lib_cache.wd_kv4_append, cache, k, v, block_table, seq_lens, cu_new, err_flag, stream)
+    _tokens("wd_kv4_append", _APPEND, cache, k, v, block_table, seq_lens, cu_new, err_flag, stream)
     return cache
 
 
@@ -227,7 +238,7 @@ def wd_kv4_gather(cache: Kv4Cache, block_table: torch.Tensor, seq_lens: torch.Te
                   v_out: torch.Tensor, cu_new: torch.Tensor | None = None,
                   err_flag: torch.Tensor | None = None, stream=None):
     """The values of the positions that wd_kv4_append with the same arguments writes."""
-    _tokens("wd_kv4_gather", _lib_cache.wd_kv4_gather, cache, k_out, v_out, block_table, seq_lens, cu_new, err_flag, stream)
+    _tokens("wd_kv4_gather", _GATHER, cache, k_out, v_out, block_table, seq_lens, cu_new, err_flag, stream)
     return k_out, v_out
 
 
@@ -252,12 +263,12 @@ def wd_kv4_attend(cache: Kv4Cache, q: torch.Tensor, block_table: torch.Tensor, s
         raise ValueError(f"lse: expected contiguous float32 {(S, q_heads)}, got {lse.dtype} {tuple(lse.shape)}")
     D, blocks = cache.dim, block_table.shape[-1]
     shape, row = (S, q_heads, D), q_heads * D
-    status = _lib_cache.wd_kv4_attend(
-        cache._ref, q.data_ptr(), _type(q, "q"), _rows(q, shape, row, "q"), S, q_heads,
+    status = _lib_cache.wd_call(_ATTEND, _attend_args(
+        cache._at, q.data_ptr(), _type(q, "q"), _rows(q, shape, row, "q"), S, q_heads,
         _ints(block_table, (S, blocks), "block_table"), blocks, _ints(seq_lens, (S,), "seq_lens"),
         D ** -0.5 if scale is None else scale, window, out.data_ptr(), _rows(out, shape, row, "out"),
-        None if lse is None else lse.data_ptr(), workspace.data_ptr(), workspace.nbytes,
-        None if err_flag is None else _flag(err_flag), _stream(stream, q))
+        0 if lse is None else lse.data_ptr(), workspace.data_ptr(), workspace.nbytes,
+        0 if err_flag is None else _flag(err_flag), _stream(stream, q)))
     if status:
         _check("wd_kv4_attend", status)
     return out
@@ -268,7 +279,7 @@ def wd_kv4_attend(cache: Kv4Cache, q: torch.Tensor, block_table: torch.Tensor, s
 def _weight(w: torch.Tensor, H: int, kind: torch.dtype, name: str) -> int:
     if w.dtype is not kind:
         raise TypeError("w_post, w_pre and gate must have one dtype")
-    if w.dim() != 1 or w.shape[0] != H or not w.is_contiguous():
+    if w.shape != (H,) or not w.is_contiguous():
         raise ValueError(f"{name}: expected contiguous [{H}], got {tuple(w.shape)}")
     return w.data_ptr()
 
@@ -280,8 +291,8 @@ def wd_block_norm(res: torch.Tensor, res_out: torch.Tensor | None = None, out: t
     """r' = res_scale * res + gate * norm(y; w_post) into res_out, norm(r'; w_pre) into out: the step
     between two blocks. gate broadcasts from [1 or T, 1 or H]. Returns (res_out, out)."""
     T, H = shape = res.shape
-    pp = qp = gp = yp = rp = op = kind = None
-    gate_ld = gate_step = yt = yl = rl = ot = ol = 0
+    kind = None
+    pp = qp = gp = yp = rp = op = gate_ld = gate_step = yt = yl = rl = ot = ol = 0
     if w_pre is not None:
         kind = w_pre.dtype
         qp = _weight(w_pre, H, kind, "w_pre")
@@ -309,9 +320,9 @@ def wd_block_norm(res: torch.Tensor, res_out: torch.Tensor | None = None, out: t
     w_type = _TYPES.get(kind, 0)
     if w_type == 0 and kind is not None and kind is not torch.float32:
         raise TypeError(f"w_post, w_pre and gate: dtype {kind} is not float32, bfloat16 or float16")
-    status = (_lib_cache or lib()).wd_block_norm(
-        T, H, res.data_ptr(), _type(res, "res"), _rows(res, shape, H, "res"), yp, yt, yl, pp, qp, gp, w_type, gate_ld,
-        gate_step, res_scale, eps, rp, rl, op, ot, ol, _stream(stream, res))
+    status = (_lib_cache or lib()).wd_call(_NORM, _norm_args(
+        T, H, res.data_ptr(), _type(res, "res"), H if res.is_contiguous() else _rows(res, shape, H, "res"), yp, yt, yl,
+        pp, qp, gp, w_type, gate_ld, gate_step, res_scale, eps, rp, rl, op, ot, ol, _stream(stream, res)))
     if status:
         _check("wd_block_norm", status)
     return res_out, out

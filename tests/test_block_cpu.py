@@ -116,6 +116,25 @@ def test_attend_refuses_before_launch(change, status):
                                          a["bytes"], None, None) == status
 
 
+def test_call_refuses_what_it_does_not_know():
+    L = block_ops.lib()
+    assert L.wd_call(5, bytes(8)) == UNSUPPORTED and L.wd_call(-1, bytes(8)) == UNSUPPORTED
+    assert L.wd_call(0, None) == NULL
+
+
+@pytest.mark.parametrize("change,status", [
+    ({}, 0), (dict(T=-1), SHAPE), (dict(H=0), SHAPE), (dict(res=None), NULL), (dict(ldr=63), SHAPE), (dict(y_type=3), UNSUPPORTED),
+    (dict(y=P + 2), ALIGN), (dict(gate=P + 2), ALIGN), (dict(step=2), SHAPE), (dict(ldo=63), SHAPE), (dict(out=None), NULL)])
+def test_call_passes_every_argument_on(change, status):
+    """The refusals of wd_block_norm, its arguments as a block (T = 0 launches nothing)."""
+    a = dict(T=0 if not change else 2, H=64, res=P, ldr=64, y=P, y_type=0, ldy=64, w_post=P, w_pre=P, gate=P, step=1,
+             res_out=P, out=P, ldo=64) | change
+    args = block_ops._norm_args(a["T"], a["H"], a["res"] or 0, 1, a["ldr"], a["y"], a["y_type"], a["ldy"], a["w_post"],
+                                a["w_pre"], a["gate"], 0, 0, a["step"], 1.0, 1e-6, a["res_out"], 64, a["out"] or 0, 1,
+                                a["ldo"], 0)
+    assert block_ops.lib().wd_call(block_ops._NORM, args) == status
+
+
 def test_attend_refuses_a_cache_of_too_many_runs():
     c = ctypes.byref(block_ops.Kv4Struct(1 << 27, 256, 2, 128, P, P, P, P))
     assert block_ops.lib().wd_kv4_attend(c, P, 1, 512, 2, 4, P, 4, P, 1.0, 0, P, 512, P, P, 1 << 30, None, None) == SHAPE
