@@ -11,7 +11,10 @@
 // the type, and converted after.
 //   Bound by DRAM for many rows: 8192 tokens of 4096 BF16 channels (268 MB) 47.6 us,
 // 5.6 TB/s, 83 % of a copy; one token 2.8 us, a launch and one trip to memory. A width
-// of 7167 goes channel by channel: 33 tokens 5.3 us, most of it that trip and two sums.
+// of 7167 goes channel by channel: 33 tokens 5.1 us, most of it that trip and two sums;
+// 4000 tokens 96 us, 2.4 TB/s: a row per SM at a time, so its trip shows again. (Rows
+// copied ahead through shared memory at their own alignment: 94 us, and narrower ones
+// lost, 25.3 instead of 21.3 us for 4000 of 2047.)
 #include <type_traits>
 
 #include "wd_block.cuh"
@@ -148,7 +151,8 @@ __host__ __device__ constexpr int elem_bytes(int type) { return type == WD_F32 ?
 // The vector path copies its rows ahead with cp.async; a thread reads only what it
 // has copied itself, so the copies need no barrier.
 template <int RT, int YT, bool VEC, bool ROWS, int N>
-__global__ void __launch_bounds__(N == 32 ? kThreads : 1024) block_norm_kernel(const NormArgs a) {
+__global__ void __launch_bounds__(N == 32 ? kThreads : VEC ? 1024 : N, N == 32 ? 1024 / kThreads : VEC ? 1 : 1024 / N)
+    block_norm_kernel(const NormArgs a) {
   constexpr bool WARP = N == 32;
   constexpr int DEPTH = VEC ? row_depth(RT, YT) : 1;
   constexpr int RB = VEC ? elem_bytes(RT) / 2 : 0, YB = VEC ? elem_bytes(YT) / 2 : 0;  // 16-byte words
@@ -338,7 +342,13 @@ extern "C" moe_status wd_block_norm(int32_t T, int32_t H, const void* res, int32
                    (gate_step == 0 || vector_rows(gate, w_type, gate_ld));
   cudaStream_t st = (cudaStream_t)stream;
   if (vec) return H <= 32 * kNormPer ? launch_vector<32>(a, st) : launch_vector<1024>(a, st);
+  // As few threads as hold the row: more rows of an SM overlap, each waiting for its loads and sums. 8000
+  // rows of 511, 1001, 4095 channels: 11.4, 21.2, 79.4 us; with 256 threads for up to 2048 and 1024 above
+  // 32.7, 35.9, 156.
   return H <= 32 * kNormPer    ? launch_norm<-1, -1, false, 32>(a, st)
+         : H <= 64 * kNormPer  ? launch_norm<-1, -1, false, 64>(a, st)
+         : H <= 128 * kNormPer ? launch_norm<-1, -1, false, 128>(a, st)
          : H <= 256 * kNormPer ? launch_norm<-1, -1, false, 256>(a, st)
+         : H <= 512 * kNormPer ? launch_norm<-1, -1, false, 512>(a, st)
                                : launch_norm<-1, -1, false, 1024>(a, st);
 }
