@@ -56,6 +56,20 @@ def test_widths_and_gates(T, H, gate_kind):
     _check(H, res, y, w_post, gate, w_pre, float(np.float32(0.7)), float(np.float32(1e-6)), r, o, "bf16", "bf16")
 
 
+@pytest.mark.parametrize("T,H", [(3000, 255), (3000, 257), (5200, 511), (2600, 513), (2600, 1023), (1300, 1025), (700, 2049),
+                                 (400, 4095), (200, 4097)])
+@pytest.mark.parametrize("gate_kind", ["channel", "both"])
+def test_odd_widths_of_many_rows(T, H, gate_kind):
+    """Every number of threads that a row takes, and more rows than an SM has at a time."""
+    rng = np.random.default_rng(T + H)
+    y, res = _t(rng.standard_normal((T, H)) * 3, "f16"), _t(rng.standard_normal((T, H)), "f32")
+    w_post, w_pre = _t(1 + rng.standard_normal(H) / 8, "bf16"), _t(1 + rng.standard_normal(H) / 8, "bf16")
+    gate = _t(rng.standard_normal((1 if gate_kind == "channel" else T, H)), "bf16")
+    r, o = torch.empty_like(res), torch.empty(T, H, dtype=torch.bfloat16, device="cuda")
+    block_ops.wd_block_norm(res, r, o, y=y, w_post=w_post, gate=gate, w_pre=w_pre, res_scale=0.7)
+    _check(H, res, y, w_post, gate, w_pre, float(np.float32(0.7)), float(np.float32(1e-6)), r, o, "f32", "bf16")
+
+
 @pytest.mark.parametrize("yk", ["f32", "bf16", "f16"])
 @pytest.mark.parametrize("rk", ["f32", "bf16", "f16"])
 @pytest.mark.parametrize("wk,ok", [("f32", "bf16"), ("bf16", "f16"), ("f16", "f32")])
