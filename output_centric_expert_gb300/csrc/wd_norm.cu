@@ -9,12 +9,12 @@
 // Loads of different arrays must not wait for one another (a token's latency is
 // one trip to memory, not four): they are issued as raw words under a branch on
 // the type, and converted after.
-//   Bound by DRAM for many rows: 8192 tokens of 4096 BF16 channels (268 MB) 47.6 us,
-// 5.6 TB/s, 83 % of a copy; one token 2.8 us, a launch and one trip to memory. A width
-// of 7167 goes channel by channel: 33 tokens 5.1 us, most of it that trip and two sums;
-// 4000 tokens 96 us, 2.4 TB/s: a row per SM at a time, so its trip shows again. (Rows
-// copied ahead through shared memory at their own alignment: 94 us, and narrower ones
-// lost, 25.3 instead of 21.3 us for 4000 of 2047.)
+//   Bound by DRAM for many rows: 8192 tokens of 4096 BF16 channels (268 MB) 43.1 us,
+// 6.2 TB/s, 92 % of a copy (47.4 with a division in each sum's use); one token 2.8 us, a
+// launch and one trip to memory. A width of 7167 goes channel by channel: 33 tokens 4.9
+// us, most of it that trip and two sums; 4000 tokens 88 us, 2.6 TB/s: instructions, of
+// one row per SM at a time. (Rows ahead through shared memory at their own alignment, or
+// in registers: 2 to 5 % less for it, 8 to 20 % more for narrower ones.)
 #include <type_traits>
 
 #include "wd_block.cuh"
@@ -40,6 +40,13 @@ struct Raw {
   uint32_t w[8];
 };
 
+// Whether a thread's k-th channel on the element path is inside the row, which has more
+// than 4 N channels where N is the least that holds it.
+template <int N>
+__device__ __forceinline__ bool has(int i, int k, int H) {
+  return (N >= 64 && k < 4) || i + k * N < H;
+}
+
 // N: threads of the row, a constant on the element path so that strides are immediates.
 template <bool VEC, int N>
 __device__ __forceinline__ void load_raw(const void* p, int32_t type, int64_t row, int i, int H,
@@ -61,11 +68,11 @@ __device__ __forceinline__ void load_raw(const void* p, int32_t type, int64_t ro
   } else if (type == WD_F32) {
     const uint32_t* a = static_cast<const uint32_t*>(p) + row + i;
 #pragma unroll
-    for (int k = 0; k < 8; ++k) r.w[k] = i + k * N < H ? a[k * N] : 0u;
+    for (int k = 0; k < 8; ++k) r.w[k] = has<N>(i, k, H) ? a[k * N] : 0u;
   } else {
     const uint16_t* a = static_cast<const uint16_t*>(p) + row + i;
 #pragma unroll
-    for (int k = 0; k < 8; ++k) r.w[k] = i + k * N < H ? a[k * N] : 0u;
+    for (int k = 0; k < 8; ++k) r.w[k] = has<N>(i, k, H) ? a[k * N] : 0u;
   }
 }
 
@@ -105,12 +112,12 @@ __device__ __forceinline__ void store_row(void* p, int32_t type, int64_t row, in
     float* a = static_cast<float*>(p) + row + i;
 #pragma unroll
     for (int k = 0; k < 8; ++k)
-      if (i + k * N < H) a[k * N] = f[k];
+      if (has<N>(i, k, H)) a[k * N] = f[k];
   } else {
     uint16_t* a = static_cast<uint16_t*>(p) + row + i;
 #pragma unroll
     for (int k = 0; k < 8; ++k)
-      if (i + k * N < H)
+      if (has<N>(i, k, H))
         a[k * N] = (uint16_t)(type == WD_BF16 ? pack2<true>(f[k], 0.0f) : pack2<false>(f[k], 0.0f));
   }
 }
@@ -211,6 +218,7 @@ __global__ void __launch_bounds__(N == 32 ? kThreads : VEC ? 1024 : N, N == 32 ?
     }
   }
 
+  const float per_channel = 1.0f / (float)a.H;
   for (int stage = 0; tok < a.T; tok += step, stage = stage + 1 == DEPTH ? 0 : stage + 1) {
     float y[8], r[8];
     Raw rg;
@@ -246,7 +254,7 @@ __global__ void __launch_bounds__(N == 32 ? kThreads : VEC ? 1024 : N, N == 32 ?
     }
     if (a.y) {
       float inv = g1;
-      if (a.w_post) inv *= rsqrtf(row_sum<WARP>(y, red, slot) / (float)a.H + a.eps);
+      if (a.w_post) inv *= rsqrtf(row_sum<WARP>(y, red, slot) * per_channel + a.eps);
 #pragma unroll
       for (int k = 0; k < 8; ++k) y[k] *= post[k];
       if (ROWS) {
@@ -263,7 +271,7 @@ __global__ void __launch_bounds__(N == 32 ? kThreads : VEC ? 1024 : N, N == 32 ?
     }
     if (a.res_out) store_row<VEC, N>(a.res_out, rt, tok * a.ldro, i, a.H, r);
     if (a.out) {
-      const float inv = rsqrtf(row_sum<WARP>(r, red, slot) / (float)a.H + a.eps);
+      const float inv = rsqrtf(row_sum<WARP>(r, red, slot) * per_channel + a.eps);
 #pragma unroll
       for (int k = 0; k < 8; ++k) r[k] = r[k] * inv * pre[k];
       store_row<VEC, N>(a.out, a.out_type, tok * a.ldo, i, a.H, r);
@@ -343,8 +351,8 @@ extern "C" moe_status wd_block_norm(int32_t T, int32_t H, const void* res, int32
   cudaStream_t st = (cudaStream_t)stream;
   if (vec) return H <= 32 * kNormPer ? launch_vector<32>(a, st) : launch_vector<1024>(a, st);
   // As few threads as hold the row: more rows of an SM overlap, each waiting for its loads and sums. 8000
-  // rows of 511, 1001, 4095 channels: 11.4, 21.2, 79.4 us; with 256 threads for up to 2048 and 1024 above
-  // 32.7, 35.9, 156.
+  // rows of 511, 1001, 4095 channels: 10.5, 19.9, 70.8 us; with 256 threads for up to 2048 and 1024 above
+  // three times, 1.7 times and twice that.
   return H <= 32 * kNormPer    ? launch_norm<-1, -1, false, 32>(a, st)
          : H <= 64 * kNormPer  ? launch_norm<-1, -1, false, 64>(a, st)
          : H <= 128 * kNormPer ? launch_norm<-1, -1, false, 128>(a, st)
