@@ -12,7 +12,7 @@ namespace {
 // takes two shuffles. Both kernels are bound by integer instructions (conversions,
 // packing, addresses), so magnitudes are compared as 16-bit pairs and a thread steps
 // through its pieces without divisions. Prompts of 9.7k tokens, 8 heads of dim 128, into
-// the cache and back (100 MB): 27.5 us, 3.6 TB/s; ALU 55 % busy, DRAM 27 %, 70 % of the
+// the cache and back (100 MB): 27.4 us, 3.7 TB/s; ALU 55 % busy, DRAM 27 %, 68 % of the
 // issue slots in larger batches. One token each of 64 sequences: 3.7 us a launch.
 
 struct TokenArgs {

@@ -26,10 +26,10 @@
 // order. (Joining in the last CTA to finish, by a counter, took 11 us of 42 for 76
 // parts of one row: one SM reads them all.)
 //
-// Bound. 64 sequences of up to 8192 keys with 16 heads per KV head (119 MB): 52 us,
-// 2.3 TB/s; one of 131071 with 8 heads (71 MB): 28 us, 2.5 TB/s. Decoding, scaling and
-// the softmax are about 780 instructions per warp and 32 keys for 16 heads (60 of them
-// MMAs, 128 conversions at half rate), issued in 44 % of the cycles: registers leave 12
+// Bound. 64 sequences of up to 8192 keys with 16 heads per KV head (119 MB): 50.2 us,
+// 2.4 TB/s; one of 131071 with 8 heads (71 MB): 27.9 us, 2.6 TB/s. Decoding, scaling and
+// the softmax are about 880 instructions per warp and 32 keys for 16 heads (64 of them
+// MMAs, 145 conversions at half rate), issued in 41 % of the cycles: registers leave 12
 // to 16 warps per SM, too few to hide every dependency. The first 6 us are a chain of
 // trips to memory: lengths, block table, keys.
 #include "wd_block.cuh"
