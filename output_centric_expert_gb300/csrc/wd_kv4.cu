@@ -8,12 +8,15 @@ namespace {
 // ------------------------------------------------------- append and gather --
 // A CTA takes `per` tokens in a row and up to 128 of their 8-element pieces. Its first
 // threads find the tokens' places (sequence by bisection in cu_new, page, slot) once
-// for all. The four threads of a 32-element block are neighbours: its largest magnitude
-// takes two shuffles. Both kernels are bound by integer instructions (conversions,
+// for all, and a thread takes a piece of two tokens that share bytes of V: no exchange
+// between threads (through shared memory and a barrier: 27.4 us for the prompts below).
+// The four threads of a 32-element block are neighbours: its largest magnitude takes
+// two shuffles. Both kernels are bound by integer instructions (conversions,
 // packing, addresses), so magnitudes are compared as 16-bit pairs and a thread steps
 // through its pieces without divisions. Prompts of 9.7k tokens, 8 heads of dim 128, into
-// the cache and back (100 MB): 27.4 us, 3.7 TB/s; ALU 55 % busy, DRAM 27 %, 68 % of the
-// issue slots in larger batches. One token each of 64 sequences: 3.7 us a launch.
+// the cache and back (100 MB): 23.6 us, 4.2 TB/s, half of it places, first loads and the
+// two launches; 262k tokens of 4 heads into it 98 us, DRAM 69 %, ALU 64 %. One token each
+// of 64 sequences: 3.7 us a launch.
 
 struct TokenArgs {
   const int32_t *table, *lens, *cu;
@@ -30,13 +33,19 @@ struct Place {
   int32_t page, slot;
   bool before, behind;
 };
+// A new token with an even slot and the next one where that is new too (`both`), or one
+// with an odd slot whose neighbour was there before: what shares bytes of V. j: the first's.
+struct Pair {
+  int32_t page, slot, j;
+  bool both;
+};
 constexpr int kMostPer = 64;
-constexpr int kResident = 6;  // CTAs of an SM: both loads of a thread in flight take 39 registers
+constexpr int kResident = 5;  // CTAs of an SM: a pair's four loads in flight take 48 registers
 
-__device__ __forceinline__ Place place_of(const TokenArgs& a, int tok, bool flag) {
+__device__ __forceinline__ Place place_of(const TokenArgs& a, int tok, bool here) {
   Place p = {-1, 0, false, false};
   int s = tok, first = tok, end = tok + 1;
-  if (tok >= a.T) return p;
+  if (!here || tok >= a.T) return p;
   if (a.cu) {
     if (tok >= __ldg(a.cu + a.S) || tok < __ldg(a.cu)) return p;
     int lo = 0, hi = a.S - 1;  // the last s with cu[s] <= tok
@@ -60,12 +69,37 @@ __device__ __forceinline__ Place place_of(const TokenArgs& a, int tok, bool flag
   p.slot = (int)(pos & ((1 << a.page_shift) - 1));
   if (p.page < 0 || p.page >= a.pages) {
     p.page = -1;
-    if (flag) flag_invalid(a.err);
+    flag_invalid(a.err);
   }
   return p;
 }
 
-// The (token, piece) of a thread's i-th item, i = threadIdx.x, + kThreads, ...
+// The pairs that begin in a CTA's tokens, in order; returns their number. All threads.
+__device__ __forceinline__ int find_pairs(const TokenArgs& a, int tok0, Pair* s_pair) {
+  __shared__ uint32_t s_first[kMostPer / 32];
+  const int tid = threadIdx.x;
+  Place p;
+  uint32_t first = 0;
+  if (tid < kMostPer) {  // whole warps
+    p = place_of(a, tok0 + tid, tid < a.per);
+    first = __ballot_sync(0xFFFFFFFFu, p.page >= 0 && !((p.slot & 1) && p.before));
+    if ((tid & 31) == 0) s_first[tid >> 5] = first;
+  }
+  __syncthreads();
+  int pairs = 0;
+#pragma unroll
+  for (int n = 0; n < kMostPer / 32; ++n) pairs += __popc(s_first[n]);
+  if (tid < kMostPer && (first >> (tid & 31)) & 1u) {
+    int at = __popc(first & ((1u << (tid & 31)) - 1u));
+#pragma unroll
+    for (int n = 0; n < kMostPer / 32; ++n) at += n < tid >> 5 ? __popc(s_first[n]) : 0;
+    s_pair[at] = {p.page, p.slot, tid, !(p.slot & 1) && p.behind};
+  }
+  __syncthreads();
+  return pairs;
+}
+
+// The (pair, piece) of a thread's i-th item, i = threadIdx.x, + kThreads, ...
 struct Walk {
   int i, j, w;
   const int chunk, dj, dw;
@@ -94,14 +128,12 @@ __global__ void __launch_bounds__(kThreads, kResident)
     kv4_append_kernel(const uint16_t* __restrict__ k, const uint16_t* __restrict__ v,
                       uint8_t* __restrict__ kc, uint8_t* __restrict__ ks, uint8_t* __restrict__ vc,
                       uint8_t* __restrict__ vs, const TokenArgs a) {
-  __shared__ Place s_place[kMostPer + 1];
-  extern __shared__ uint32_t s_code[];  // V's codes: [per + 1 tokens][chunk]; scale codes behind
-  uint8_t* s_scale = reinterpret_cast<uint8_t*>(s_code + (a.per + 1) * a.chunk);
+  __shared__ Pair s_pair[kMostPer];
   const int tok0 = blockIdx.x * a.per, w0 = blockIdx.y * a.chunk, tid = threadIdx.x;
-  if (tid <= a.per) s_place[tid] = place_of(a, tok0 + tid, tid < a.per);
-  __syncthreads();
+  const int pairs = find_pairs(a, tok0, s_pair);
   // the scale code of a piece's block, and its codes
-  auto quantise = [&](const uint4& raw, unsigned quad, uint32_t& scale) {
+  const unsigned quad = 0xFu << (tid & 28);
+  auto quantise = [&](const uint4& raw, uint32_t& scale) {
     // magnitudes as 16-bit integers, two to a word (NaN above infinity above the rest)
     const uint32_t two = __vmaxu2(__vmaxu2(raw.x & 0x7FFF7FFFu, raw.y & 0x7FFF7FFFu),
                                   __vmaxu2(raw.z & 0x7FFF7FFFu, raw.w & 0x7FFF7FFFu));
@@ -116,39 +148,29 @@ __global__ void __launch_bounds__(kThreads, kResident)
     for (int j = 0; j < 8; ++j) f[j] *= u;
     return e2m1x8(f);
   };
-  const unsigned quad = 0xFu << (tid & 28);
-  // the token behind the last may share bytes with it
-  for (Walk walk(a.chunk); walk.j <= a.per; walk.next()) {
-    const int i = walk.i, j = walk.j, w = w0 + walk.w;
-    const Place p = s_place[j];
-    if (p.page < 0) continue;  // the four threads of a block alike
+  for (Walk walk(a.chunk); walk.j < pairs; walk.next()) {
+    const int w = w0 + walk.w;
+    const Pair p = s_pair[walk.j];  // the four threads of a block have the same
     const int head = w / (D / 8), b = w % (D / 8) >> 2, t = w & 3;
-    const int64_t tok = tok0 + j;
-    const uint4 raw_v = ld_cached16(v + tok * a.ldv + w * 8);
-    uint4 raw_k;
-    if (j < a.per) raw_k = ld_cached16(k + tok * a.ldk + w * 8);
-    uint32_t sv;
-    s_code[i] = quantise(raw_v, quad, sv);
-    if (t == 0) s_scale[i >> 2] = (uint8_t)sv;
-    if (j == a.per) continue;
-    uint32_t sk;
-    const uint32_t code = quantise(raw_k, quad, sk);
+    const int64_t tok = tok0 + p.j;
+    const uint16_t *kp = k + tok * a.ldk + w * 8, *vp = v + tok * a.ldv + w * 8;
+    const uint4 raw_v = ld_cached16(vp), raw_k = ld_cached16(kp);
+    uint4 next_v, next_k;
+    if (p.both) next_v = ld_cached16(vp + a.ldv), next_k = ld_cached16(kp + a.ldk);
     const size_t at = ((size_t)p.page * a.heads + head) << a.page_shift;  // in tokens
-    *reinterpret_cast<uint32_t*>(kc + at * (D / 2) + k_word<D>(p.slot, t, b)) = code;
-    if (t == 0) ks[at * (D / 32) + p.slot * (D / 32) + b] = (uint8_t)sk;
-  }
-  __syncthreads();
-  // V: a byte holds an element of an even key and the next, so one thread writes both:
-  // the even key's where both are new
-  for (Walk walk(a.chunk); walk.j < a.per; walk.next()) {
-    const int i = walk.i, j = walk.j, w = w0 + walk.w;
-    const Place p = s_place[j];
+    uint32_t sv, sk, v0 = quantise(raw_v, sv), v1 = 0, sv1 = 0;
+    uint8_t* kto = kc + at * (D / 2) + k_word<D>(p.slot, t, b);
+    uint8_t* ksto = ks + at * (D / 32) + p.slot * (D / 32) + b;
+    *reinterpret_cast<uint32_t*>(kto) = quantise(raw_k, sk);
+    if (t == 0) *ksto = (uint8_t)sk;
+    if (p.both) {
+      v1 = quantise(next_v, sv1);
+      *reinterpret_cast<uint32_t*>(kto + D / 2) = quantise(next_k, sk);
+      if (t == 0) ksto[D / 32] = (uint8_t)sk;
+    }
+    // V: a byte holds an element of an even key and the next
     const bool odd = p.slot & 1;
-    if (p.page < 0 || (odd && p.before)) continue;
-    const int head = w / (D / 8), b = w % (D / 8) >> 2, t = w & 3;
-    const size_t at = ((size_t)p.page * a.heads + head) << a.page_shift;
-    const bool both = !odd && p.behind;
-    const uint32_t even = odd ? 0u : s_code[i], next = odd ? s_code[i] : both ? s_code[i + a.chunk] : 0u;
+    const uint32_t even = odd ? 0u : v0, next = odd ? v0 : v1;
 #pragma unroll
     for (int h = 0; h < 2; ++h) {  // elements 4h .. 4h + 3: g = 2t + h
       uint32_t* to = reinterpret_cast<uint32_t*>(vc + at * (D / 2) + v_word<D>(p.slot >> 1, 2 * t + h, b));
@@ -157,10 +179,10 @@ __global__ void __launch_bounds__(kThreads, kResident)
     }
     if (t == 0) {
       uint8_t* to = vs + at * (D / 32) + v_scale<D>(p.slot, b);
-      if (both)
-        *reinterpret_cast<uint16_t*>(to) = (uint16_t)(s_scale[i >> 2] | s_scale[(i + a.chunk) >> 2] << 8);
+      if (p.both)
+        *reinterpret_cast<uint16_t*>(to) = (uint16_t)(sv | sv1 << 8);
       else
-        *to = s_scale[i >> 2];
+        *to = (uint8_t)sv;
     }
   }
 }
@@ -192,32 +214,43 @@ __global__ void __launch_bounds__(kThreads)
     kv4_gather_kernel(void* __restrict__ k, void* __restrict__ v, const uint8_t* __restrict__ kc,
                       const uint8_t* __restrict__ ks, const uint8_t* __restrict__ vc,
                       const uint8_t* __restrict__ vs, const TokenArgs a) {
-  __shared__ Place s_place[kMostPer];
-  const int tok0 = blockIdx.x * a.per, w0 = blockIdx.y * a.chunk, tid = threadIdx.x;
-  if (tid < a.per) s_place[tid] = place_of(a, tok0 + tid, true);
-  __syncthreads();
-  for (Walk walk(a.chunk); walk.j < a.per; walk.next()) {
-    const int j = walk.j, w = w0 + walk.w;
-    const Place p = s_place[j];
-    if (p.page < 0) continue;
-    const int head = w / (D / 8), b = w % (D / 8) >> 2, t = w & 3, slot = p.slot;
-    const int64_t tok = tok0 + j;
+  __shared__ Pair s_pair[kMostPer];
+  const int tok0 = blockIdx.x * a.per, w0 = blockIdx.y * a.chunk;
+  const int pairs = find_pairs(a, tok0, s_pair);
+  for (Walk walk(a.chunk); walk.j < pairs; walk.next()) {
+    const int w = w0 + walk.w;
+    const Pair p = s_pair[walk.j];
+    const int head = w / (D / 8), b = w % (D / 8) >> 2, t = w & 3, odd = p.slot & 1;
+    const int64_t tok = tok0 + p.j;
     const size_t at = ((size_t)p.page * a.heads + head) << a.page_shift;
-    uint32_t h[4], pair[2][4];
-    const uint32_t kw = *reinterpret_cast<const uint32_t*>(kc + at * (D / 2) + k_word<D>(slot, t, b));
-    uint32_t vw[2];
+    const uint8_t* kfrom = kc + at * (D / 2) + k_word<D>(p.slot, t, b);
+    const uint8_t* ksfrom = ks + at * (D / 32) + p.slot * (D / 32) + b;
+    const uint8_t* vsfrom = vs + at * (D / 32) + v_scale<D>(p.slot, b);
+    const uint32_t kw = *reinterpret_cast<const uint32_t*>(kfrom), sk = *ksfrom, sv = *vsfrom;
+    uint32_t vw[2], kw1 = 0, sk1 = 0, sv1 = 0;
 #pragma unroll
     for (int n = 0; n < 2; ++n)
-      vw[n] = *reinterpret_cast<const uint32_t*>(vc + at * (D / 2) + v_word<D>(slot >> 1, 2 * t + n, b));
-    const uint32_t sk = ks[at * (D / 32) + slot * (D / 32) + b], sv = vs[at * (D / 32) + v_scale<D>(slot, b)];
+      vw[n] = *reinterpret_cast<const uint32_t*>(vc + at * (D / 2) + v_word<D>(p.slot >> 1, 2 * t + n, b));
+    if (p.both) kw1 = *reinterpret_cast<const uint32_t*>(kfrom + D / 2), sk1 = ksfrom[D / 32], sv1 = vsfrom[1];
+    uint32_t h[4], pair[2][4];  // pair: the even key's element and the odd key's
+    const int64_t k_to = tok * a.ldk + w * 8, v_to = tok * a.ldv + w * 8;
     e2m1x8_to_f16(kw, h);
-    store8<TYPE>(k, tok * a.ldk + w * 8, h, e8m0_to_f32(sk));
-    const uint32_t pick = slot & 1 ? 0x7632 : 0x5410;  // the halves of an odd or an even key
+    store8<TYPE>(k, k_to, h, e8m0_to_f32(sk));
 #pragma unroll
     for (int n = 0; n < 2; ++n) e2m1x8_to_f16(vw[n], pair[n]);
+    auto pick = [&](int key) {
 #pragma unroll
-    for (int n = 0; n < 4; ++n) h[n] = __byte_perm(pair[n >> 1][2 * (n & 1)], pair[n >> 1][2 * (n & 1) + 1], pick);
-    store8<TYPE>(v, tok * a.ldv + w * 8, h, e8m0_to_f32(sv));
+      for (int n = 0; n < 4; ++n)
+        h[n] = __byte_perm(pair[n >> 1][2 * (n & 1)], pair[n >> 1][2 * (n & 1) + 1], key ? 0x7632 : 0x5410);
+    };
+    pick(odd);
+    store8<TYPE>(v, v_to, h, e8m0_to_f32(sv));
+    if (p.both) {
+      pick(1);
+      store8<TYPE>(v, v_to + a.ldv, h, e8m0_to_f32(sv1));
+      e2m1x8_to_f16(kw1, h);
+      store8<TYPE>(k, k_to + a.ldk, h, e8m0_to_f32(sk1));
+    }
   }
 }
 
@@ -252,7 +285,8 @@ TokenArgs token_args(const wd_kv4_cache* c, int64_t ldk, int64_t ldv, int32_t T,
   while (c->heads % h) --h;
   const int chunk = h * piece;
   // tokens of a CTA: up to 8 pieces a thread, in whole waves of resident CTAs. (Powers of two up to 4
-  // pieces: 15.6 us instead of 13.1 for 16 prompts of up to 2000, 8 heads of dim 64.)
+  // pieces: 15.6 us instead of 13.1 for 16 prompts of up to 2000, 8 heads of dim 64, with one token
+  // a thread; 12.1 now.)
   const int64_t runs = (int64_t)T * (words / chunk), slots = (int64_t)sm_count() * kResident;
   const int most = 8 * kThreads / chunk < kMostPer ? 8 * kThreads / chunk : kMostPer;
   const int64_t waves = (runs + slots * most - 1) / (slots * most);
@@ -271,13 +305,12 @@ template <int D>
 moe_status append(const wd_kv4_cache* c, const void* k, const void* v, int32_t type,
                   const TokenArgs& a, cudaStream_t st) {
   const dim3 grid = token_grid(a, a.heads * (D / 8));
-  const size_t smem = (size_t)(a.per + 1) * a.chunk * 4 + (size_t)(a.per + 1) * a.chunk / 4;
   const uint16_t *k16 = static_cast<const uint16_t*>(k), *v16 = static_cast<const uint16_t*>(v);
   if (type == WD_BF16)
-    kv4_append_kernel<D, true><<<grid, kThreads, smem, st>>>(k16, v16, c->k_codes, c->k_scales,
+    kv4_append_kernel<D, true><<<grid, kThreads, 0, st>>>(k16, v16, c->k_codes, c->k_scales,
                                                              c->v_codes, c->v_scales, a);
   else
-    kv4_append_kernel<D, false><<<grid, kThreads, smem, st>>>(k16, v16, c->k_codes, c->k_scales,
+    kv4_append_kernel<D, false><<<grid, kThreads, 0, st>>>(k16, v16, c->k_codes, c->k_scales,
                                                               c->v_codes, c->v_scales, a);
   return launched("wd_kv4_append launch");
 }
