@@ -122,6 +122,20 @@ def test_many_rows(N, K, B, yk):
     assert (wide[:, N:] == 7.0).all()
 
 
+@pytest.mark.parametrize("N,K,B", [(12001, 4096, 40), (6001, 8192, 64)])
+def test_rounds_of_wide_clusters(N, K, B):
+    """More row tiles than clusters of 4 and of 8 CTAs take at a time."""
+    rng = np.random.default_rng(N)
+    w, w64, *_ = _weights(rng, N, K)
+    x = _x(rng, B, K, "bf16")
+    y = torch.full((B, N), float("nan"), device="cuda")
+    block_ops.wd_fp4_matvec(w, x, y)
+    _close(y, x, w64, "f32")
+    again = torch.empty_like(y)
+    block_ops.wd_fp4_matvec(w, x, again)
+    assert torch.equal(y, again)
+
+
 @pytest.mark.parametrize("B", [1, 12, 40])
 def test_extremes(B):
     """Zero tokens, loud channels, infinities and NaN stay where they belong; scale codes 0, 254 and 255."""
