@@ -350,6 +350,18 @@ def test_what_has_no_page_is_flagged_and_left_out():
     assert (out[1] == 0).all() and (lse[1] == -float("inf")).all()
 
 
+@pytest.mark.parametrize("dim,group", [(64, 1), (64, 3), (64, 16), (128, 1), (128, 12), (256, 1), (256, 9)])
+@pytest.mark.parametrize("lens", [[40001], [20000, 5, 7777, 0, 300]])
+def test_rows_of_many_parts(lens, dim, group):
+    """Rows that many CTAs share, more of them than there are groups of sums to join for few heads."""
+    f = Filled(lens, 1, dim, 32, seed=group)
+    q = _q(f.rng, len(lens), group, dim)
+    out, lse = _attend(f, q)
+    _check(f, q, out, lse)
+    again, lse2 = _attend(f, q)
+    assert torch.equal(out, again) and torch.equal(lse, lse2)
+
+
 def test_long_sequence_and_another_stream():
     f = Filled([40001], 1, 128, 64)
     q = _q(f.rng, 1, 8, 128)
