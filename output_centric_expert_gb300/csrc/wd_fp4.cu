@@ -89,7 +89,7 @@ __global__ void __launch_bounds__(kThreads)
 //   Bound by the codes' bytes where the matrix is large: 8 tokens of 129283 x 2048
 // (145 MB) take 29.2 us, 5.0 TB/s, 73 % of a copy. 16 warps and 4 column tiles ahead of
 // each: 12, 20 and 24 warps took 6, 4 and 13 % longer, 3 and 5 column tiles 1 and 2 %.
-// Small products are latency: one token of 4096 x 2048 4.9 us, of which 2.5 are the
+// Small products are latency: one token of 4096 x 2048 4.7 us, of which 2.5 are the
 // launch and 1 is the trip for x.
 
 constexpr int kMvWarps = 16, kMvThreads = kMvWarps * 32;
@@ -273,9 +273,11 @@ __global__ void __launch_bounds__(kMvThreads, 1) fp4_matvec_kernel(const MvArgs 
       if (k > 0 && u0 < u1) finish(to == whole ? s_part[warp][1] + sum_at : to);
       __syncthreads();
       const bool last = !CHUNKED || c0 + kt >= ct;
+      const int starts = lane < kMvWarps ? units * lane / kMvWarps : 0x7FFFFFFF;  // of the warps' runs
       for (int q = warp; q < nq; q += kMvWarps) {  // a warp per row tile
         // the warps that have its first and last column tile; a lane has 4 rows of a token
-        const int w0 = ((q * kt + 1) * kMvWarps - 1) / units, w1 = ((q + 1) * kt * kMvWarps - 1) / units;
+        const int w0 = __popc(__ballot_sync(0xFFFFFFFFu, starts <= q * kt)) - 1;
+        const int w1 = __popc(__ballot_sync(0xFFFFFFFFu, starts < (q + 1) * kt)) - 1;
         if (MODE == kDirect && w0 == w1) continue;
         const int o = lane * 4, tok = o / kTileRows;
         float4 v = *reinterpret_cast<const float4*>(w0 == w1 ? s_sum[q] + o : s_part[w0][1] + o);
@@ -331,7 +333,7 @@ moe_status launch_matvec(MvArgs a, cudaStream_t st) {
     a.chunk = ct;
     a.batch = (int)(per < fit ? per : fit);
     // us for 8 tokens: 129283 x 2048 (54 row tiles a CTA) 28.9 written as they end, 30.5 waiting;
-    // 65536 x 4096 (27) 30.0 and 30.7; 9216 x 4096 (4) 10.5 and 10.4; 2048 x 2048 (1) 5.9 and 5.6
+    // 65536 x 4096 (27) 30.0 and 30.7; 9216 x 4096 (4) 10.5 and 10.4; 2048 x 2048 (1) 5.9 and 5.6 (when both were measured)
     if (per >= kMvWarps) mode = kDirect;
     smem = ct * kTileX + a.batch * kTileSum;
   } else {  // columns in chunks of 128 KB of x
@@ -409,7 +411,7 @@ extern "C" moe_status wd_fp4_matvec(const wd_fp4_shape* s, const uint8_t* pc, co
   cudaStream_t st = (cudaStream_t)stream;
   // Up to 8 tokens (and where rows are too long for the other kernel's shared memory) the stream kernel:
   // it reads the weights once per 8 tokens. us for 8 and 9 tokens: 10.3 and 18.0 against 11.9 and 10.8 for
-  // 9216 x 4096, 5.7 and 9.7 against 7.3 and 6.9 for 2048 x 2048, 30 and 59 against 50 and 42 for 65536 x 4096.
+  // 9216 x 4096, 5.4 and 9.7 against 7.3 and 6.9 for 2048 x 2048, 30 and 59 against 50 and 42 for 65536 x 4096.
   if (B > 8 && s->K <= tc_most_columns(B)) return launch_tc(a, x_type == WD_BF16, st);
   return x_type == WD_BF16 ? launch_matvec<true>(a, st) : launch_matvec<false>(a, st);
 }
