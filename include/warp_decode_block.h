@@ -144,6 +144,10 @@ moe_status wd_kv4_gather(const wd_kv4_cache* cache, void* k_out, void* v_out, in
  * multiple of 8, 16-byte aligned); lse [S][q_heads] F32 or NULL. A sequence
  * without keys gets out = 0 and lse = -inf. Results are the same on every call
  * with the same inputs.
+ * Logits, softmax statistics and sums are FP32. The weight of a value's block, its
+ * probability times its E8M0 scale, has 16 bits and FP32's range of exponents: a
+ * probability below 2^-126 of the row's largest counts as 0, and a weight below 2^-140
+ * of the largest probability times the block's largest scale among the keys.
  * workspace: wd_kv4_attend_workspace bytes, 16-byte aligned; its contents do not
  * matter before or after a call. Calls that may overlap need one each.
  * pages * heads * (page_size / 16) < 2^31, 1 TB of codes.

@@ -10,11 +10,14 @@
 //   values down to 2^-32 of it). A block's 32 products are summed by two MMAs
 //   and added to the FP32 logit times the key's E8M0 scale.
 //   out = V^T p: rows are dims, k is the keys. A V scale belongs to (key, block):
-//   it multiplies the probabilities, which are f16 here (11 bits, 2^2 p): the
-//   power of two 2^(s - M + 9), with M the running maximum of the block's scale
-//   codes, is exact in f16. A key whose scale is below 2^-23 of the block's
-//   largest adds nothing (its part is below FP32's own rounding of the sum's
-//   largest term).
+//   it multiplies the probabilities, as the power of two 2^(s - M + kLift) with M the
+//   running maximum of the block's scale codes. A weight p 2^(s - M) is two BF16 terms,
+//   the second what the rounding of the first left: 16 bits, and FP32's range of
+//   exponents. So it is off by 2^-17 of itself whatever the other keys hold, and the row
+//   sum l (of the unrounded p) matches the weights. (f16 weights, one term of 11 bits with
+//   5 of exponent, took 27.9 and 50.3 us where these take 32.0 and 62.5, but outputs were
+//   off by 2^-12 of their terms, and keys with small p or small scales beside a large one
+//   were lost.)
 //
 // Work. All (sequence, KV head, head tile) rows are cut into tiles of 32 keys per
 // warp; CTA c of G takes the c-th contiguous share of all tiles, found from the
@@ -26,10 +29,9 @@
 // order. (Joining in the last CTA to finish, by a counter, took 11 us of 42 for 76
 // parts of one row: one SM reads them all.)
 //
-// Bound. 64 sequences of up to 8192 keys with 16 heads per KV head (119 MB): 50.2 us,
-// 2.4 TB/s; one of 131071 with 8 heads (71 MB): 27.9 us, 2.6 TB/s. Decoding, scaling and
-// the softmax are about 880 instructions per warp and 32 keys for 16 heads (64 of them
-// MMAs, 145 conversions at half rate), issued in 41 % of the cycles: registers leave 12
+// Bound. 64 sequences of up to 8192 keys with 16 heads per KV head (119 MB): 62.5 us,
+// 1.9 TB/s; one of 131071 with 8 heads (71 MB): 32.0 us, 2.2 TB/s. Decoding, scaling, the
+// softmax and 96 MMAs per warp and 32 keys of 16 heads: registers leave 12
 // to 16 warps per SM, too few to hide every dependency. The first 6 us are a chain of
 // trips to memory: lengths, block table, keys.
 #include "wd_block.cuh"
@@ -42,8 +44,8 @@ constexpr int kWarpKeys = 32;  // keys per warp and iteration
 constexpr int kSub = 16;       // keys of one MMA tile; a page holds whole ones
 constexpr unsigned kAll = 0xFFFFFFFFu;
 
-constexpr float kLift = 2.0f;   // probabilities are held times 2^2
-constexpr float kSlack = 4.0f;  // and may be 2^4 above their reference: 2^6, times 2^9 at most, fits f16
+constexpr float kSlack = 4.0f;  // how far (in log 2) a probability may be above its reference
+constexpr int kLift = 122;      // a weight is p 2^(s - M + 122): up to 2^126, which BF16 holds
 
 // What a row costs beside its tiles (queries staged, sums joined), in tiles: CTAs share
 // both out. 1, 2, 3: 45.0, 43.6, 44.9 us for 64 sequences up to 4096 with 8 heads, 17.1,
@@ -114,9 +116,30 @@ __device__ __forceinline__ float exp2_fast(float v) {
   return r;
 }
 
-__device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
-  const __half2 r = __hmul2(*reinterpret_cast<const __half2*>(&a), *reinterpret_cast<const __half2*>(&b));
+__device__ __forceinline__ uint32_t mul2_bf16(uint32_t a, uint32_t b) {
+  const __nv_bfloat162 r =
+      __hmul2(*reinterpret_cast<const __nv_bfloat162*>(&a), *reinterpret_cast<const __nv_bfloat162*>(&b));
   return *reinterpret_cast<const uint32_t*>(&r);
+}
+
+// d += a * b with BF16 operands.
+__device__ __forceinline__ void mma_add_bf16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+// Eight E2M1 codes -> BF16 pairs times 2^-126, e[j] the codes of byte j (low nibble in the low half): E2M1's
+// exponent and mantissa are the lowest bits of BF16's exponent and the highest of its mantissa, and its 0.5
+// becomes the subnormal 2^-127, which the MMA takes as it is.
+__device__ __forceinline__ void e2m1x8_to_bf16(uint32_t w, uint32_t (&e)[4]) {
+  const uint32_t lo = w & 0x0F0F0F0Fu, hi = (w >> 4) & 0x0F0F0F0Fu;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    uint32_t two;  // the codes of byte j in the halves: a selector from 8 on repeats a byte's top bit, 0 here
+    asm("prmt.b32 %0, %1, %2, %3;" : "=r"(two) : "r"(lo), "r"(hi), "r"(0xC480 + 0x1111 * j));
+    e[j] = two * 0x1040u & 0x81C081C0u;
+  }
 }
 
 __device__ __forceinline__ float over_g_max(float v) {
@@ -143,7 +166,7 @@ struct Stage {
 // of head tile n is head n * 8 + c; a lane holds columns 2t and 2t + 1.
 template <int D, int NT>
 struct State {
-  float m[NT][2], l[NT][2];  // reference of K q (before the scale), sum of 2^2 p
+  float m[NT][2], l[NT][2];  // reference of K q (before the scale), sum of p
   float acc[NT][D / 16][4];  // rows of MMA tile 2b + h: dims 32b + 4g + 2h (first), + 1
   uint32_t top[D / 64];      // running maximum of the V scale codes, bytes (b, b, b + 1, b + 1) as in v_scales
 };
@@ -298,10 +321,10 @@ __device__ __forceinline__ void attend_keys(uint8_t* st, const uint8_t* qf, cons
           if (!((on >> (u * 16 + (c >> 1) * 8 + g)) & 1u)) z[u][n][c] = -INFINITY;
   }
 
-  // ---- reference maximum, probabilities (times 2^2)
+  // ---- reference maximum, probabilities
   // The reference follows the maximum only when that is kSlack above it (in log 2
-  // units), so the sums are seldom rescaled; 2^2 p then stays below 2^6.
-  uint32_t p[2][NT][2];  // f16x2 as the B fragment of out = V^T p
+  // units), so the sums are seldom rescaled; p then stays below 2^4.
+  uint32_t p[2][NT][2][2];  // BF16 pairs as the B fragment of out = V^T p; and what their rounding left
 #pragma unroll
   for (int n = 0; n < NT; ++n) {
     float mx[2];
@@ -330,11 +353,15 @@ __device__ __forceinline__ void attend_keys(uint8_t* st, const uint8_t* qf, cons
     for (int u = 0; u < 2; ++u) {
       float e[4];
 #pragma unroll
-      for (int c = 0; c < 4; ++c) e[c] = exp2_fast(fmaf(z[u][n][c] - base[c & 1], qs[n][c & 1], kLift));
+      for (int c = 0; c < 4; ++c) e[c] = exp2_fast((z[u][n][c] - base[c & 1]) * qs[n][c & 1]);
       s.l[n][0] += e[0] + e[2];
       s.l[n][1] += e[1] + e[3];
-      p[u][n][0] = transpose8x8(pack2<false>(e[0], e[1]));
-      p[u][n][1] = transpose8x8(pack2<false>(e[2], e[3]));
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const uint32_t first = pack2<true>(e[2 * h], e[2 * h + 1]);
+        p[u][n][h][0] = transpose8x8(first);
+        p[u][n][h][1] = transpose8x8(pack2<true>(e[2 * h] - bf16_lo(first), e[2 * h + 1] - bf16_hi(first)));
+      }
     }
   }
 
@@ -363,7 +390,7 @@ __device__ __forceinline__ void attend_keys(uint8_t* st, const uint8_t* qf, cons
       for (int b = 0; b < NB; ++b) {
         const int have = (s.top[b / 2] >> (16 * (b & 1))) & 255u, now = (top.w[b / 2] >> (16 * (b & 1))) & 255u;
         // a key with a NaN block makes that block's sums NaN, whatever its probability
-        const float f = (top.nan >> b) & 1u ? NAN : exp2i(max(-126, have - now));
+        const float f = (top.nan >> b) & 1u ? NAN : exp2i(max(-126, have - now)) * exp2i(max(-126, min(0, have - now + 126)));
 #pragma unroll
         for (int n = 0; n < NT; ++n)
 #pragma unroll
@@ -378,10 +405,10 @@ __device__ __forceinline__ void attend_keys(uint8_t* st, const uint8_t* qf, cons
   }
 
   // ---- out += V^T p
-  uint32_t up[NB];  // 24 - top in both halves
+  uint32_t up[NB];  // the exponent field of 2^(kLift - top) in both halves
 #pragma unroll
   for (int b = 0; b < NB; ++b) {
-    const uint32_t d = 24u - ((s.top[b / 2] >> (16 * (b & 1))) & 255u);
+    const uint32_t d = kLift + 127u - ((s.top[b / 2] >> (16 * (b & 1))) & 255u);
     up[b] = __byte_perm(d, d, 0x1010);
   }
 #pragma unroll
@@ -397,18 +424,20 @@ __device__ __forceinline__ void attend_keys(uint8_t* st, const uint8_t* qf, cons
       uint32_t e[2][4], mult[2];
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        e2m1x8_to_f16(v[h][b], e[h]);  // e[h][i]: element i of both keys
+        e2m1x8_to_bf16(v[h][b], e[h]);  // e[h][i]: element i of both keys
         const uint32_t two = __byte_perm(sc[h][b / 2], 0, b & 1 ? 0x4342 : 0x4140);  // codes of the two keys
-        // 2^(s - top + 9) as f16: exponent field s - top + 24, 0 where that is negative
-        mult[h] = __viaddmax_s16x2_relu(two, up[b], 0u) << 10;
+        // 2^(s - top + kLift) as BF16, 0 where that is below its range
+        mult[h] = __viaddmax_s16x2_relu(two, up[b], 0u) << 7;
       }
       const uint32_t a0[4] = {e[0][0], e[0][1], e[1][0], e[1][1]}, a1[4] = {e[0][2], e[0][3], e[1][2], e[1][3]};
 #pragma unroll
-      for (int n = 0; n < NT; ++n) {
-        const uint32_t p0 = hmul2(p[u][n][0], mult[0]), p1 = hmul2(p[u][n][1], mult[1]);
-        mma_add(s.acc[n][2 * b], a0, p0, p1);
-        mma_add(s.acc[n][2 * b + 1], a1, p0, p1);
-      }
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          const uint32_t p0 = mul2_bf16(p[u][n][0][k], mult[0]), p1 = mul2_bf16(p[u][n][1][k], mult[1]);
+          mma_add_bf16(s.acc[n][2 * b], a0, p0, p1);
+          mma_add_bf16(s.acc[n][2 * b + 1], a1, p0, p1);
+        }
     }
   }
 }
@@ -714,11 +743,11 @@ __global__ void __launch_bounds__(W * 32, CTAS) kv4_attend_kernel(const AttendAr
         f[c] = exp2_fast(s_m[warp][h] - (m == -INFINITY ? 0.0f : m));
         const float l = over_g_sum(st.l[n][c]) * f[c];
         if (g == 0) s_l[warp][h] = l;
-        f[c] *= 0.001953125f;
+        f[c] *= exp2i(126 - kLift);
       }
 #pragma unroll
       for (int b = 0; b < NB; ++b) {
-        // the accumulators hold 2^2 p times 2^(9 - top) of the scale
+        // the accumulators hold E2M1 times 2^-126 and p times 2^(kLift - top) of the scale
         const float scale = e8m0_to_f32((st.top[b / 2] >> (16 * (b & 1))) & 255u);
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
@@ -744,7 +773,7 @@ __global__ void __launch_bounds__(W * 32, CTAS) kv4_attend_kernel(const AttendAr
               make_uint2(pack2<BF16>(v.x * inv, v.y * inv), pack2<BF16>(v.z * inv, v.w * inv));
           if (lrow && i % D == 0) {
             const float m = top_of(h);
-            lrow[h] = ((m == -INFINITY ? 0.0f : m) + log2f(l) - kLift) * 0.6931471805599453f;
+            lrow[h] = ((m == -INFINITY ? 0.0f : m) + log2f(l)) * 0.6931471805599453f;
           }
         } else {
           *reinterpret_cast<float4*>(part + n * 8 * D + i) = v;
@@ -831,7 +860,7 @@ __global__ void __launch_bounds__(kJoin) kv4_join_kernel(const AttendArgs a) {
         make_uint2(pack2<BF16>(v.x * inv, v.y * inv), pack2<BF16>(v.z * inv, v.w * inv));
     if (a.lse && i * 4 % D == 0)
       a.lse[(int64_t)sp.seq * a.heads * a.group + sp.head + h] =
-          ((m == -INFINITY ? 0.0f : m) + log2f(l) - kLift) * 0.6931471805599453f;
+          ((m == -INFINITY ? 0.0f : m) + log2f(l)) * 0.6931471805599453f;
   }
 }
 
