@@ -153,6 +153,10 @@ moe_status wd_kv4_gather(const wd_kv4_cache* cache, void* k_out, void* v_out, in
  * pages * heads * (page_size / 16) < 2^31, 1 TB of codes.
  */
 size_t wd_kv4_attend_workspace(const wd_kv4_cache* cache, int32_t S, int32_t q_heads);
+/* The CTAs that a call with these sizes launches, at most 2 per SM; 0 where it launches
+ * none: nothing to do, or refused. The pointers are not looked at. */
+int32_t wd_kv4_attend_ctas(const wd_kv4_cache* cache, int32_t S, int32_t q_heads,
+                           int32_t max_blocks, int32_t window);
 moe_status wd_kv4_attend(const wd_kv4_cache* cache, const void* q, int32_t type, int64_t ldq,
                          int32_t S, int32_t q_heads, const int32_t* block_table,
                          int32_t max_blocks, const int32_t* seq_lens, float scale,

@@ -63,6 +63,8 @@ def lib() -> ctypes.CDLL:
         L.wd_kv4_cache_bytes.argtypes = [kp, ctypes.c_int]
         L.wd_kv4_attend_workspace.restype = sz
         L.wd_kv4_attend_workspace.argtypes = [kp, i32, i32]
+        L.wd_kv4_attend_ctas.restype = i32
+        L.wd_kv4_attend_ctas.argtypes = [kp, i32, i32, i32, i32]
         tokens = [kp, vp, vp, i32, i64, i64, i32, vp, i32, vp, vp, i32, vp, vp]
         for name, args in (
                 ("wd_fp4_pack_codes", [fp, vp, vp, vp, vp, vp]),
@@ -85,7 +87,7 @@ def exported_symbols() -> list[str]:
     """The entry points include/warp_decode_block.h declares."""
     return ["wd_fp4_packed_bytes", "wd_fp4_pack_codes", "wd_fp4_pack_weights", "wd_fp4_matvec",
             "wd_kv4_cache_bytes", "wd_kv4_append", "wd_kv4_gather", "wd_kv4_attend_workspace",
-            "wd_kv4_attend", "wd_block_norm", "wd_call"]
+            "wd_kv4_attend_ctas", "wd_kv4_attend", "wd_block_norm", "wd_call"]
 
 
 def _check(fn: str, status: int) -> None:

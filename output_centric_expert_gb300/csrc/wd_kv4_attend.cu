@@ -871,32 +871,44 @@ int head_tiles(const wd_kv4_cache* c, int group) {
   return (group + n - 1) / n;
 }
 
-constexpr int kMaxCtasPerSm = 2;
+constexpr int kCtasPerSm = 2;  // the workspace has room for as many
+
+// Warps of a CTA.
+constexpr int warps_of(int dim, bool wide) { return dim == 256 ? 4 : dim == 128 && wide ? 6 : 8; }
+
+// The launch for the capacity of the sequences' rows, which the host knows, whatever their lengths are.
+struct Plan {
+  int64_t row_tiles;  // tiles of a row at most
+  unsigned grid;      // CTAs, no more than tiles; 0: more tiles than the kernel counts
+};
+Plan plan_of(const wd_kv4_cache* c, int32_t S, int group, int32_t max_blocks, int32_t window) {
+  const int64_t keys = (int64_t)max_blocks * c->page_size;
+  const int64_t seen = (int64_t)window + 2 * kWarpKeys;  // (in 64 bits: a window may be INT32_MAX)
+  const int64_t most = window > 0 && seen < keys ? seen : keys;
+  const int tile = warps_of(c->dim, tile_heads(c, group) == 16) * kWarpKeys;
+  const int64_t row_tiles = (most + tile - 1) / tile;
+  const int64_t rows = (int64_t)S * c->heads * head_tiles(c, group);
+  if (rows > 0x7FFFFFFF / (row_tiles + kRowUnits)) return {row_tiles, 0};
+  const int64_t tiles = row_tiles * rows, fill = (int64_t)sm_count() * kCtasPerSm;
+  return {row_tiles, (unsigned)(tiles < fill ? tiles : fill)};
+}
 
 template <int D, int NT, int W, int STAGES, int CTAS>
-moe_status launch(const AttendArgs& a, bool bf16, cudaStream_t st) {
-  static_assert(CTAS <= kMaxCtasPerSm, "the workspace has room for 2 CTAs per SM");
+moe_status launch(const AttendArgs& a, const Plan& plan, bool bf16, cudaStream_t st) {
+  static_assert(CTAS == kCtasPerSm && W == warps_of(D, NT == 2), "the plan's");
   auto k = bf16 ? kv4_attend_kernel<D, NT, W, STAGES, CTAS, true> : kv4_attend_kernel<D, NT, W, STAGES, CTAS, false>;
   const size_t ring = (size_t)W * STAGES * Stage<D>::kBytes;
   static SmemOnce once[2];
   moe_status rc = once[bf16].allow(k, ring);
   if (rc != MOE_OK) return rc;
-  // no more CTAs than tiles that the rows' capacity allows
-  const int64_t keys = (int64_t)a.max_blocks << a.page_shift;
-  const int64_t most = a.window > 0 && a.window + 2 * kWarpKeys < keys ? a.window + 2 * kWarpKeys : keys;
-  const int64_t row_tiles = (most + W * kWarpKeys - 1) / (W * kWarpKeys);
-  const int64_t tiles = row_tiles * a.S * a.heads * a.head_tiles;
-  if ((row_tiles + kRowUnits) * a.S * a.heads * a.head_tiles > 0x7FFFFFFF) return refuse(MOE_ERR_SHAPE, "wd_kv4_attend: block_table's capacity is too large");
-  const int64_t fill = (int64_t)sm_count() * CTAS;
-  const unsigned grid = (unsigned)(tiles < fill ? tiles : fill);
-  k<<<grid, W * 32, ring, st>>>(a);
+  k<<<plan.grid, W * 32, ring, st>>>(a);
   rc = launched("wd_kv4_attend launch");
-  if (rc != MOE_OK || row_tiles == 1) return rc;  // a row of one tile is never split
+  if (rc != MOE_OK || plan.row_tiles == 1) return rc;  // a row of one tile is never split
   cudaLaunchAttribute dependent = {};
   dependent.id = cudaLaunchAttributeProgrammaticStreamSerialization;
   dependent.val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(grid);
+  cfg.gridDim = dim3(plan.grid);
   cfg.blockDim = dim3(kJoin);
   cfg.stream = st;
   cfg.attrs = &dependent;
@@ -921,8 +933,15 @@ extern "C" size_t wd_kv4_attend_workspace(const wd_kv4_cache* c, int32_t S, int3
   using namespace wd;
   if (!c || wd_kv4_cache_bytes(c, WD_KV4_CODES) == 0 || S < 0 || q_heads < 1 || q_heads % c->heads)
     return 0;
-  const size_t grid = (size_t)sm_count() * kMaxCtasPerSm;
+  const size_t grid = (size_t)sm_count() * kCtasPerSm;
   return grid * sizeof(Split) + grid * 2 * part_floats(c, q_heads / c->heads) * 4;
+}
+
+extern "C" int32_t wd_kv4_attend_ctas(const wd_kv4_cache* c, int32_t S, int32_t q_heads, int32_t max_blocks,
+                                      int32_t window) {
+  using namespace wd;
+  if (wd_kv4_attend_workspace(c, S, q_heads) == 0 || max_blocks < 1 || window < 0) return 0;
+  return (int32_t)plan_of(c, S, q_heads / c->heads, max_blocks, window).grid;
 }
 
 extern "C" moe_status wd_kv4_attend(const wd_kv4_cache* c, const void* q, int32_t type,
@@ -950,7 +969,9 @@ extern "C" moe_status wd_kv4_attend(const wd_kv4_cache* c, const void* q, int32_
   if ((int64_t)c->pages * c->heads * (c->page_size / kSub) > 0x7FFFFFFF)  // 1 TB of codes
     return refuse(MOE_ERR_SHAPE, "wd_kv4_attend: the cache has too many pages");
   const int group = q_heads / c->heads;
-  const unsigned grid = (unsigned)(sm_count() * kMaxCtasPerSm);
+  const Plan plan = plan_of(c, S, group, max_blocks, window);
+  if (plan.grid == 0) return refuse(MOE_ERR_SHAPE, "wd_kv4_attend: block_table's capacity is too large");
+  const unsigned grid = (unsigned)(sm_count() * kCtasPerSm);
   AttendArgs a = {};
   a.kc = c->k_codes, a.ks = c->k_scales, a.vc = c->v_codes, a.vs = c->v_scales;
   a.q = static_cast<const uint16_t*>(q);
@@ -966,7 +987,7 @@ extern "C" moe_status wd_kv4_attend(const wd_kv4_cache* c, const void* q, int32_
   // <dim, head tiles, warps, ring stages, CTAs per SM>. 16 heads of dim 128 take 168 registers: 2 x 6
   // warps 63.8 us, 1 x 12 warps 67.3 (their barriers hold each other up); a fourth ring stage leaves room
   // for one CTA only, 74 us against 52. Dim 256: 2 x 4 warps 52.8 us, 1 x 8 warps 54.0.
-  if (c->dim == 64) return wide ? launch<64, 2, 8, 4, 2>(a, bf16, st) : launch<64, 1, 8, 4, 2>(a, bf16, st);
-  if (c->dim == 128) return wide ? launch<128, 2, 6, 3, 2>(a, bf16, st) : launch<128, 1, 8, 3, 2>(a, bf16, st);
-  return launch<256, 1, 4, 2, 2>(a, bf16, st);
+  if (c->dim == 64) return wide ? launch<64, 2, 8, 4, 2>(a, plan, bf16, st) : launch<64, 1, 8, 4, 2>(a, plan, bf16, st);
+  if (c->dim == 128) return wide ? launch<128, 2, 6, 3, 2>(a, plan, bf16, st) : launch<128, 1, 8, 3, 2>(a, plan, bf16, st);
+  return launch<256, 1, 4, 2, 2>(a, plan, bf16, st);
 }
