@@ -142,6 +142,9 @@ __device__ __forceinline__ void e2m1x8_to_bf16(uint32_t w, uint32_t (&e)[4]) {
   }
 }
 
+// 1 / l; 0 where no key of the row has a page, whose sums are 0 then.
+__device__ __forceinline__ float over(float l) { return l == 0.0f ? 0.0f : 1.0f / l; }
+
 __device__ __forceinline__ float over_g_max(float v) {
 #pragma unroll
   for (int m = 4; m <= 16; m <<= 1) v = fmaxf(v, __shfl_xor_sync(kAll, v, m));
@@ -768,7 +771,7 @@ __global__ void __launch_bounds__(W * 32, CTAS) kv4_attend_kernel(const AttendAr
           v.x += o.x, v.y += o.y, v.z += o.z, v.w += o.w;
         }
         if (whole) {
-          const float l = sum_of(h), inv = 1.0f / l;
+          const float l = sum_of(h), inv = over(l);
           *reinterpret_cast<uint2*>(orow + n * 8 * D + i) =
               make_uint2(pack2<BF16>(v.x * inv, v.y * inv), pack2<BF16>(v.z * inv, v.w * inv));
           if (lrow && i % D == 0) {
@@ -854,7 +857,7 @@ __global__ void __launch_bounds__(kJoin) kv4_join_kernel(const AttendArgs a) {
       if (tid < n) add(s_m[tid + n], s_l[tid + n], s_v[tid + n]);
     }
     if (side != 0 || i >= i1) continue;
-    const float inv = 1.0f / l;
+    const float inv = over(l);
     uint16_t* orow = a.out + (int64_t)sp.seq * a.ldo + (int64_t)sp.head * D;
     *reinterpret_cast<uint2*>(orow + i * 4) =
         make_uint2(pack2<BF16>(v.x * inv, v.y * inv), pack2<BF16>(v.z * inv, v.w * inv));
