@@ -117,7 +117,8 @@ size_t wd_kv4_cache_bytes(const wd_kv4_cache* cache, int which);
  * Sequence s holds seq_lens[s] tokens before the call; its new ones are rows
  * cu_new[s] ... cu_new[s+1]-1 of k and v (cu_new [S+1] int32, not decreasing).
  * Rows from cu_new[S] on are ignored. cu_new NULL: one new token each (T == S).
- * Two sequences must not append to the same slot.
+ * Two sequences must not append to the same slot; neighbouring slots of a page
+ * are independent, although their V shares bytes.
  *
  * wd_kv4_gather -- the reverse with the same arguments: the values of positions
  * seq_lens[s] ... of each sequence as k_out and v_out. Every MXFP4 value is

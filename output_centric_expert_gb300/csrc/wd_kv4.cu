@@ -34,7 +34,7 @@ struct Place {
   bool before, behind;
 };
 // A new token with an even slot and the next one where that is new too (`both`), or one
-// with an odd slot whose neighbour was there before: what shares bytes of V. j: the first's.
+// with an odd slot whose neighbour is none of its sequence's new ones: what shares bytes of V. j: the first's.
 struct Pair {
   int32_t page, slot, j;
   bool both;
@@ -168,14 +168,20 @@ __global__ void __launch_bounds__(kThreads, kResident)
       *reinterpret_cast<uint32_t*>(kto + D / 2) = quantise(next_k, sk);
       if (t == 0) ksto[D / 32] = (uint8_t)sk;
     }
-    // V: a byte holds an element of an even key and the next
-    const bool odd = p.slot & 1;
-    const uint32_t even = odd ? 0u : v0, next = odd ? v0 : v1;
+    // V: a byte holds an element of an even key and the next. A key alone replaces its own nibbles, and the
+    // neighbour's stay as they are: another entry of the call may write those meanwhile, so each of the two
+    // steps is one operation of memory. (They touch different bits, so their order does not matter.)
 #pragma unroll
     for (int h = 0; h < 2; ++h) {  // elements 4h .. 4h + 3: g = 2t + h
       uint32_t* to = reinterpret_cast<uint32_t*>(vc + at * (D / 2) + v_word<D>(p.slot >> 1, 2 * t + h, b));
-      const uint32_t x = spread4(even >> (16 * h)) | spread4(next >> (16 * h)) << 4;
-      *to = odd ? (*to & 0x0F0F0F0Fu) | x : x;  // an odd key alone joins the key before
+      const uint32_t x = spread4(v0 >> (16 * h));
+      if (p.both) {
+        *to = x | spread4(v1 >> (16 * h)) << 4;
+      } else {
+        const int up = (p.slot & 1) * 4;
+        atomicAnd(to, ~(0x0F0F0F0Fu << up));
+        atomicOr(to, x << up);
+      }
     }
     if (t == 0) {
       uint8_t* to = vs + at * (D / 32) + v_scale<D>(p.slot, b);

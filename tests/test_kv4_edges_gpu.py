@@ -1,8 +1,12 @@
 """The 4-bit KV cache at the ends of its arguments' ranges."""
+import numpy as np
 import pytest
 import torch
 
-from .test_kv4_gpu import Filled, _attend, _q
+from output_centric_expert_gb300 import block_ops
+
+from . import _block_ref as ref
+from .test_kv4_gpu import Filled, _attend, _q, _raw
 
 pytestmark = pytest.mark.gpu
 
@@ -43,3 +47,40 @@ def test_a_window_that_reaches_no_page_has_no_keys(window):
     assert (out == 0).all() and (lse == -float("inf")).all()
     out, _ = _attend(f, q, table=table)  # the keys before it count without a window
     assert torch.isfinite(out).all() and (out != 0).any()
+
+
+def _fresh(pages=4, page=16, heads=2, dim=128):
+    cache = block_ops.Kv4Cache(pages, page, heads, dim)
+    for t in cache.tensors:
+        t.fill_(255)
+    return cache
+
+
+@pytest.mark.parametrize("dim", [64, 128, 256])
+@pytest.mark.parametrize("cuts", [[1], [3], [1, 2, 3, 4, 5], [5, 6, 11], [9, 23, 41, 57]])
+def test_a_prompt_given_as_several_entries_on_one_row(cuts, dim):
+    """Entries that end on an even slot and begin on the odd one behind it write halves of the same bytes in one call."""
+    T, heads = 64, 2
+    rng = np.random.default_rng(dim)
+    k, v = (torch.from_numpy(rng.standard_normal((T, heads, dim)).astype(np.float32)).cuda().to(torch.bfloat16) for _ in range(2))
+    ends = [0] + cuts + [T]
+    cache = _fresh(dim=dim)
+    table = torch.tensor([[2, 0, 3, 1]] * (len(ends) - 1), dtype=torch.int32, device="cuda")
+    lens = torch.tensor(ends[:-1], dtype=torch.int32, device="cuda")
+    cu = torch.tensor(ends, dtype=torch.int32, device="cuda")
+    block_ops.wd_kv4_append(cache, k, v, table, lens, cu)
+    got_k, got_v = _raw(cache)
+    for got, want in ((got_k, k), (got_v, v)):
+        rows = np.concatenate([got[p].swapaxes(0, 1) for p in (2, 0, 3, 1)])
+        assert np.array_equal(rows, ref.rounded(want.double().cpu().numpy()))
+
+
+@pytest.mark.parametrize("at", [0, 1, 6, 7, 14, 15])
+def test_writing_one_slot_again_leaves_the_others(at):
+    f = Filled([16], 2, 128, 16)
+    new = torch.randn(2, 1, 2, 128, device="cuda").to(torch.bfloat16)
+    block_ops.wd_kv4_append(f.cache, new[0], new[1], f.table_d, torch.tensor([at], dtype=torch.int32, device="cuda"))
+    page = int(f.table_d[0, 0])
+    for got, held, one in zip(_raw(f.cache), (f.k64, f.v64), new):
+        held[at] = ref.rounded(one[0].double().cpu().numpy())
+        assert np.array_equal(got[page].swapaxes(0, 1), held)
