@@ -66,9 +66,9 @@ moe_status wd_fp4_pack_weights(const wd_fp4_shape* shape, const void* w, int32_t
  * batch. x [B][K] BF16 or F16, 16-byte aligned with ldx % 8 == 0; y [B][N] F32,
  * BF16 or F16. Products are exact, sums FP32, y is rounded once. Values of x are
  * used exactly down to 2^-32 of their token's largest finite one and rounded to
- * 2^-40 of it below. With more than 8 tokens a block of weights whose scale is
- * below 2^-26 of the largest of its row (within a run of columns) counts as 0:
- * less than FP32 rounding of the row's largest products. Up to 8 tokens one
+ * 2^-40 of it below. Any scales may stand beside one another in a row (with more
+ * than 8 tokens, blocks below 2^-26 of their row's largest scale are slower, where
+ * they are not zeros). Up to 8 tokens one
  * kernel streams the weights through mma.sync; more go through tcgen05 (K up
  * to 32768), 64 at a time. The results are the same on every call; a token's do
  * not depend on the other tokens' values, but their order of summation does on

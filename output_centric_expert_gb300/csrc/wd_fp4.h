@@ -45,6 +45,52 @@ __device__ __forceinline__ void store_rows(const MvArgs& a, int tok, int64_t row
     if (row + j < a.N) store_elem(a.y, a.y_type, at + j, f[j]);
 }
 
+// ---- sums from the packed weights and x themselves, for the few that the kernels' own cannot hold
+
+// The products of one row's block (codes word t of 4 at codes + 16 t) with 32 values of x, times 2^-8 so that
+// none overflows.
+template <bool BF16>
+__device__ __forceinline__ float plain_block(const uint8_t* codes, const uint16_t* x) {
+  float d = 0.0f;
+#pragma unroll 1
+  for (int t = 0; t < 4; ++t) {
+    uint32_t h[4];
+    e2m1x8_to_f16(__ldg(reinterpret_cast<const uint32_t*>(codes + 16 * t)), h);
+    float f[8];
+    unpack8<BF16>(ld_cached16(x + 8 * t), f);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      d = fmaf(half_lo(h[j]), f[2 * j] * 0.00390625f, d);
+      d = fmaf(half_hi(h[j]), f[2 * j + 1] * 0.00390625f, d);
+    }
+  }
+  return d;
+}
+
+// The sum of one row and token over the blocks of the column tiles [c0, c1), every `step`-th of them, whose
+// scale code is at most `top` (NaN blocks are none such; 255: all). In 64 bits between blocks, so only the result
+// can leave FP32's range.
+template <bool BF16>
+__device__ __forceinline__ float plain_sum(const MvArgs& a, int64_t row, int tok, int c0, int c1, int step, int top) {
+  const int ct = (a.K + kTileCols - 1) / kTileCols, r = (int)(row % kTileRows);
+  const uint16_t* x = a.x + (int64_t)tok * a.ldx;
+  double sum = 0.0;
+#pragma unroll 1
+  for (int c = c0; c < c1; c += step) {
+    const size_t tile = (size_t)(row / kTileRows) * ct + c;
+    const uint32_t scales = __ldg(reinterpret_cast<const uint32_t*>(a.scales + tile * kTileScales + (r % 8) * 8 + r / 8 * 4));
+#pragma unroll 1
+    for (int b = 0; b < 4; ++b) {
+      const int s = (scales >> (8 * b)) & 255, k = c * kTileCols + 32 * b;
+      if (s > top || k >= a.K) continue;
+      if (s == 255) return NAN;
+      const float d = plain_block<BF16>(a.codes + tile * kTileCodes + r * 64 + b * 4, x + k);
+      sum += (double)d * __longlong_as_double((long long)(s - 127 + 8 + 1023) << 52);
+    }
+  }
+  return (float)sum;
+}
+
 // ---- x as f16 times a power of two per token: its largest finite magnitude comes
 // into [2^14, 2^15), so BF16 and F16 values are exact down to 2^-32 of it.
 

@@ -9,8 +9,9 @@
 // Scales. The sums run over all of a CTA's columns inside the tensor core, so a
 // block's scale has to be in A: the decoded value times 2^(s - top + 12), with top the
 // largest scale code of the row among the CTA's columns. Exact in f16 for blocks
-// down to 2^-26 of the row's largest scale; smaller ones add nothing (less than FP32
-// rounding of the row's largest products). The row's 2^top comes back at the end.
+// down to 2^-26 of the row's largest scale. Smaller ones are 0 there; where one has a
+// code other than 0, which no ordinary matrix has, its products are added at the end,
+// block by block. The row's 2^top comes back at the end.
 //
 // Work. A cluster of CTAs shares a run of 128-row tiles, each CTA with its share of the
 // columns, so that it stages and converts only that share of x (64 tokens of 1024
@@ -169,6 +170,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) fp4_tc_kernel(const MvArgs a, i
   __shared__ __align__(16) float s_back[64];  // 1 / the tokens' powers of two
   __shared__ __align__(8) uint64_t s_bar[kGroups];
   __shared__ uint8_t s_top[kGroups][kTcRows];
+  __shared__ uint8_t s_low[kGroups][kTcRows];  // whether the row has blocks that A has as 0 although they are not
   cg::cluster_group cluster = cg::this_cluster();
   const int rank = cluster.block_rank(), size = cluster.num_blocks();
   const int tid = threadIdx.x, warp = tid >> 5, group = tid >> 7, gt = tid & 127;
@@ -262,6 +264,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) fp4_tc_kernel(const MvArgs a, i
     if (size > 1 && q + kRowTiles < q1) prefetch(q + kRowTiles);
     if (q + side < q1) {
       const uint32_t top = next_top;
+      uint32_t low = 0;
       s_top[group][gt] = (uint8_t)top;
       for (int k0 = 0; k0 < my_kt; k0 += kTcAhead) {
 #pragma unroll
@@ -278,6 +281,11 @@ __global__ void __launch_bounds__(kTcThreads, 1) fp4_tc_kernel(const MvArgs a, i
             mul[1] = __byte_perm(e13 << 10, 0, 0x1010), mul[3] = __byte_perm(e13 << 10, 0, 0x3232);
             if ((__vmaxs2(e02, e13) + 0x7FE47FE4u) & 0x80008000u)  // the row's sum is NaN
               mul[0] = mul[1] = mul[2] = mul[3] = 0x7E007E00u;
+            if (((e02 + 0x7FFF7FFFu) & (e13 + 0x7FFF7FFFu) & 0x80008000u) != 0x80008000u) {  // a multiplier is 0
+#pragma unroll
+              for (int b = 0; b < 4; ++b)
+                if (mul[b] == 0) low |= buf[i].a.w[b] | buf[i].a.w[4 + b] | buf[i].b.w[b] | buf[i].b.w[4 + b];
+            }
           }
           // ---- decode and store two blocks at a time; column k / 2 of A holds the elements k, k + 1
 #pragma unroll
@@ -332,6 +340,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) fp4_tc_kernel(const MvArgs a, i
       }
       asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
       asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+      s_low[group][gt] = (low & 0x77777777u) != 0;
       if (!ok) s_failed = 1;
       pair_sync(side);  // both halves' sums are there
       asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
@@ -347,6 +356,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) fp4_tc_kernel(const MvArgs a, i
       const float back0 = plain ? exp2i((int)t0 - 139) * fail : fail, back1 = plain ? exp2i((int)t1 - 139) * fail : fail;
       const uint32_t d0 = s_tmem + side * 2 * (kTmemCols / kGroups) + ((uint32_t)(warp & 3) << 21) + 64;
       const int64_t row = (int64_t)(q + side) * kTcRows + gt;
+      const bool low = row < a.N && (s_low[side * 2][gt] | s_low[side * 2 + 1][gt]);
       const uint32_t slot = smem_addr(sums + ((side << log) + rank) * own * kTcRows + gt);
       uint32_t place = 0;
 #pragma unroll 1
@@ -372,6 +382,26 @@ __global__ void __launch_bounds__(kTcThreads, 1) fp4_tc_kernel(const MvArgs a, i
             for (int k = 0; k < 8; ++k)
               if (j == k) o[k] = v;
           }
+        }
+        if (__any_sync(0xFFFFFFFFu, low)) {
+#pragma unroll 1
+          for (int j = 0; low && j < 8 && c + j < toks; ++j) {
+            float v = 0.0f;
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+              if (j == k) v = o[k];
+#pragma unroll 1
+            for (int part = 0; part < 3; ++part) {  // either half's column tiles; all, where an infinity met a 0 of A
+              if (part == 2 && fabsf(v) < INFINITY) break;
+              const float more = plain_sum<BF16>(a, row, a.tok0 + c + j, c0 + (part & 1), c0 + kt, part < 2 ? 2 : 1,
+                                                 part == 2 ? 255 : (int)(part ? t1 : t0) - 27);
+              v = part < 2 ? v + more : more;
+            }
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+              if (j == k) o[k] = v;
+          }
+          __syncwarp();
         }
         if (size == 1) {
 #pragma unroll
