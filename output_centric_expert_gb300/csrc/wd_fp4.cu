@@ -81,7 +81,9 @@ __global__ void __launch_bounds__(kThreads)
 // among its warps, so each warp streams one dense run of codes through registers.
 //   mma.sync m16n8k16, f16 x f16 -> FP32: rows are output rows, columns are
 //   tokens. A block's 32 products are summed by two MMAs, times its scale
-//   added to the FP32 accumulator.
+//   added to the FP32 accumulator. x times 2^14 and more beside weights past 2^96 can
+//   overflow it where the result does not: a sum that is not finite is taken again
+//   from x itself.
 // x is staged once per CTA in shared memory, as f16 times a power of two per
 // token (the largest finite magnitude in [2^14, 2^15)) and in the order of the B
 // fragment: [column tile][block][lane][16 bytes]. Row tiles that warps share are
@@ -161,7 +163,7 @@ __global__ void __launch_bounds__(kMvThreads, 1) fp4_matvec_kernel(const MvArgs 
     uint4 lo, hi;
     uint2 sc;
   };
-  bool staged = false;
+  bool staged = false, again = false;  // again: an output is not finite
   for (int q0 = r0; q0 < r1; q0 += a.batch) {
     const int nq = min(a.batch, r1 - q0);
     for (int c0 = 0; c0 < ct; c0 += CHUNKED ? a.chunk : ct) {
@@ -215,8 +217,11 @@ __global__ void __launch_bounds__(kMvThreads, 1) fp4_matvec_kernel(const MvArgs 
         for (int c = 0; c < 4; ++c) {
           const int64_t row = (int64_t)q * kTileRows + g + 8 * (c >> 1);
           const int tok = 2 * t + (c & 1);
-          if (tok < toks && row < a.N)
-            store_elem(a.y, a.y_type, (int64_t)(a.tok0 + tok) * a.ldy + row, acc[c] * back[c & 1]);
+          const float v = acc[c] * back[c & 1];
+          if (tok < toks && row < a.N) {
+            store_elem(a.y, a.y_type, (int64_t)(a.tok0 + tok) * a.ldy + row, v);
+            again |= !(fabsf(v) < INFINITY);
+          }
           acc[c] = 0.0f;
         }
       };
@@ -293,11 +298,16 @@ __global__ void __launch_bounds__(kMvThreads, 1) fp4_matvec_kernel(const MvArgs 
           if (c0 > 0) v.x += held->x, v.y += held->y, v.z += held->z, v.w += held->w;
           if (!last) *held = v;
         }
-        if (last && tok < toks) store_rows(a, a.tok0 + tok, (int64_t)(q0 + q) * kTileRows + o % kTileRows, v);
+        if (last && tok < toks) {
+          store_rows(a, a.tok0 + tok, (int64_t)(q0 + q) * kTileRows + o % kTileRows, v);
+          again |= not_finite(v);
+        }
       }
       __syncthreads();  // the sums, and x where it comes in chunks, are written again
     }
   }
+  if (__syncthreads_or(again))
+    take_again<BF16>(a, (int64_t)r0 * kTileRows, (int64_t)r1 * kTileRows, a.tok0, a.tok0 + toks);
 }
 
 moe_status check_fp4(const wd_fp4_shape* s, const uint8_t* pc, const uint8_t* ps) {

@@ -91,6 +91,34 @@ __device__ __forceinline__ float plain_sum(const MvArgs& a, int64_t row, int tok
   return (float)sum;
 }
 
+__device__ __forceinline__ bool not_finite(const float4& v) {  // (or so large that their sum is not)
+  return !(fabsf(v.x) + fabsf(v.y) + fabsf(v.z) + fabsf(v.w) < INFINITY);
+}
+
+// Takes the outputs of rows [row0, row1) and tokens [tok0, tok1) again that are not finite: FP32 may have
+// overflowed on the way to a result that fits, or an infinity of x have met a 0 that stands for a small weight.
+// All threads of the CTA, whose own outputs they are.
+template <bool BF16>
+__device__ __forceinline__ void take_again(const MvArgs& a, int64_t row0, int64_t row1, int tok0, int tok1) {
+  constexpr uint32_t kInf = BF16 ? 0x7F80u : 0x7C00u;
+  for (int tok = tok0; tok < tok1; ++tok) {
+    bool nan = false;  // in x: then all of the token's outputs are NaN
+    for (int k = threadIdx.x * 2; k < a.K; k += blockDim.x * 2) {
+      const uint32_t two = __ldg(reinterpret_cast<const uint32_t*>(a.x + (int64_t)tok * a.ldx + k));
+      nan |= (two & 0x7FFFu) > kInf || (two >> 16 & 0x7FFFu) > kInf;
+    }
+    if (__syncthreads_or(nan)) continue;
+#pragma unroll 1
+    for (int64_t row = row0 + threadIdx.x; row < row1 && row < a.N; row += blockDim.x) {
+      const int64_t at = (int64_t)tok * a.ldy + row;
+      const bool fine = a.y_type == WD_F32    ? (__ldcg(static_cast<const uint32_t*>(a.y) + at) & 0x7F800000u) != 0x7F800000u
+                        : a.y_type == WD_BF16 ? (__ldcg(static_cast<const uint16_t*>(a.y) + at) & 0x7F80u) != 0x7F80u
+                                              : (__ldcg(static_cast<const uint16_t*>(a.y) + at) & 0x7C00u) != 0x7C00u;
+      if (!fine) store_elem(a.y, a.y_type, at, plain_sum<BF16>(a, row, tok, 0, (a.K + kTileCols - 1) / kTileCols, 1, 255));
+    }
+  }
+}
+
 // ---- x as f16 times a power of two per token: its largest finite magnitude comes
 // into [2^14, 2^15), so BF16 and F16 values are exact down to 2^-32 of it.
 

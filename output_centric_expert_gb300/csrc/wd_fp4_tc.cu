@@ -166,7 +166,7 @@ __device__ __forceinline__ void stage(const MvArgs& a, int c0, int c1, int toks,
 template <bool BF16>
 __global__ void __launch_bounds__(kTcThreads, 1) fp4_tc_kernel(const MvArgs a, int n) {
   extern __shared__ uint4 dyn4[];
-  __shared__ uint32_t s_max[64], s_tmem, s_failed;
+  __shared__ uint32_t s_max[64], s_tmem, s_failed, s_again;  // s_again: an output is not finite
   __shared__ __align__(16) float s_back[64];  // 1 / the tokens' powers of two
   __shared__ __align__(8) uint64_t s_bar[kGroups];
   __shared__ uint8_t s_top[kGroups][kTcRows];
@@ -238,7 +238,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) fp4_tc_kernel(const MvArgs a, i
                    "n"(kTmemCols)
                    : "memory");
     if (tid == 0) {
-      s_failed = 0;
+      s_failed = s_again = 0;
 #pragma unroll
       for (int i = 0; i < kGroups; ++i)
         asm volatile("mbarrier.init.shared::cta.b64 [%0], 1;" ::"r"(smem_addr(&s_bar[i])) : "memory");
@@ -391,12 +391,8 @@ __global__ void __launch_bounds__(kTcThreads, 1) fp4_tc_kernel(const MvArgs a, i
             for (int k = 0; k < 8; ++k)
               if (j == k) v = o[k];
 #pragma unroll 1
-            for (int part = 0; part < 3; ++part) {  // either half's column tiles; all, where an infinity met a 0 of A
-              if (part == 2 && fabsf(v) < INFINITY) break;
-              const float more = plain_sum<BF16>(a, row, a.tok0 + c + j, c0 + (part & 1), c0 + kt, part < 2 ? 2 : 1,
-                                                 part == 2 ? 255 : (int)(part ? t1 : t0) - 27);
-              v = part < 2 ? v + more : more;
-            }
+            for (int part = 0; part < 2; ++part)  // either half's column tiles
+              v += plain_sum<BF16>(a, row, a.tok0 + c + j, c0 + part, c0 + kt, 2, (int)(part ? t1 : t0) - 27);
 #pragma unroll
             for (int k = 0; k < 8; ++k)
               if (j == k) o[k] = v;
@@ -406,7 +402,10 @@ __global__ void __launch_bounds__(kTcThreads, 1) fp4_tc_kernel(const MvArgs a, i
         if (size == 1) {
 #pragma unroll
           for (int j = 0; j < 8; ++j)
-            if (c + j < toks && row < a.N) store_elem(a.y, a.y_type, (int64_t)(a.tok0 + c + j) * a.ldy + row, o[j]);
+            if (c + j < toks && row < a.N) {
+              store_elem(a.y, a.y_type, (int64_t)(a.tok0 + c + j) * a.ldy + row, o[j]);
+              if (!(fabsf(o[j]) < INFINITY)) s_again = 1;
+            }
         } else {
 #pragma unroll
           for (int j = 0; j < 8; j += 2) {  // own >= 2
@@ -436,6 +435,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) fp4_tc_kernel(const MvArgs a, i
           v.x += w.x, v.y += w.y, v.z += w.z, v.w += w.w;
         }
         store_rows(a, a.tok0 + rank * own + tok, (int64_t)(q + side) * kTcRows + r, v);
+        if (not_finite(v)) s_again = 1;
       }
       if (q + kRowTiles < q1) cluster.barrier_arrive();
     }
@@ -446,6 +446,10 @@ __global__ void __launch_bounds__(kTcThreads, 1) fp4_tc_kernel(const MvArgs a, i
     asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(s_tmem), "n"(kTmemCols));
+  }
+  if (s_again) {
+    const int first = size == 1 ? 0 : rank * own, end = size == 1 ? toks : min(toks, first + own);
+    take_again<BF16>(a, (int64_t)q0 * kTcRows, (int64_t)q1 * kTcRows, a.tok0 + first, a.tok0 + end);
   }
 }
 
