@@ -64,9 +64,9 @@ moe_status wd_fp4_pack_weights(const wd_fp4_shape* shape, const void* w, int32_t
 /*
  * wd_fp4_matvec -- y[b,n] = sum_k x[b,k] W[n,k] for the B tokens of a decode
  * batch. x [B][K] BF16 or F16, 16-byte aligned with ldx % 8 == 0; y [B][N] F32,
- * BF16 or F16. Products are exact, sums FP32, y is rounded once. Values of x are
- * used exactly down to 2^-32 of their token's largest finite one and rounded to
- * 2^-40 of it below. Any scales may stand beside one another in a row (with more
+ * BF16 or F16. Products are exact, sums FP32, y is rounded once. F16 values of x are
+ * used exactly, BF16 ones down to 2^-31 of their token's largest finite one; below that
+ * they are off by at most 2^-39 of it. Any scales may stand beside one another in a row (with more
  * than 8 tokens, blocks below 2^-26 of their row's largest scale are slower, where
  * they are not zeros). Up to 8 tokens one
  * kernel streams the weights through mma.sync; more go through tcgen05 (K up
@@ -145,7 +145,7 @@ moe_status wd_kv4_gather(const wd_kv4_cache* cache, void* k_out, void* v_out, in
  * multiple of 8, 16-byte aligned); lse [S][q_heads] F32 or NULL. A sequence
  * without keys gets out = 0 and lse = -inf. Results are the same on every call
  * with the same inputs.
- * Logits, softmax statistics and sums are FP32. The weight of a value's block, its
+ * Logits, softmax statistics and sums are FP32; q is used as exactly as x above (per head). The weight of a value's block, its
  * probability times its E8M0 scale, has 16 bits and FP32's range of exponents: a
  * probability below 2^-126 of the row's largest counts as 0, and a weight below 2^-140
  * of the largest probability times the block's largest scale among the keys.

@@ -85,7 +85,7 @@ __global__ void __launch_bounds__(kThreads)
 //   overflow it where the result does not: a sum that is not finite is taken again
 //   from x itself.
 // x is staged once per CTA in shared memory, as f16 times a power of two per
-// token (the largest finite magnitude in [2^14, 2^15)) and in the order of the B
+// token and in the order of the B
 // fragment: [column tile][block][lane][16 bytes]. Row tiles that warps share are
 // joined in shared memory in column order, so results do not depend on timing.
 //   Bound by the codes' bytes where the matrix is large: 8 tokens of 129283 x 2048

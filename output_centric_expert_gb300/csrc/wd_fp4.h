@@ -119,8 +119,9 @@ __device__ __forceinline__ void take_again(const MvArgs& a, int64_t row0, int64_
   }
 }
 
-// ---- x as f16 times a power of two per token: its largest finite magnitude comes
-// into [2^14, 2^15), so BF16 and F16 values are exact down to 2^-32 of it.
+// ---- x as f16 times a power of two per token. BF16: the largest finite magnitude
+// comes into [2^14, 2^15), so values are exact down to 2^-31 of it and off by at most
+// 2^-39 of it below. F16: the same where that scales up, else as it is: always exact.
 
 // The largest finite magnitude, as an integer: 16-bit pairs, plus what takes infinities
 // and NaN past the largest signed value, so that they lose against anything.
@@ -153,7 +154,7 @@ __device__ __forceinline__ uint32_t largest_finite16(const uint4* p, int count, 
 template <bool BF16>
 __device__ __forceinline__ int shift_of_16(uint32_t m) {
   const uint32_t mag = BF16 ? m << 16 : __float_as_uint(half_lo(m));
-  return mag == 0 ? 0 : min(126, max(-126, 141 - (int)(mag >> 23)));
+  return mag == 0 ? 0 : min(126, max(BF16 ? -126 : 0, 141 - (int)(mag >> 23)));
 }
 
 template <bool BF16>

@@ -6,8 +6,8 @@
 // results join as l = sum l_i 2^(m_i - m), acc likewise, out = acc / l.
 //   S = K q: mma.sync m16n8k16, rows are 16 keys, columns 8 query heads that
 //   share the KV head. E2M1 codes decode exactly to f16; q is f16 times a power of
-//   two per head (largest magnitude in [2^14, 2^15), exact for BF16 and F16
-//   values down to 2^-32 of it). A block's 32 products are summed by two MMAs
+//   two per head: the largest magnitude in [2^14, 2^15) is exact for BF16 values down
+//   to 2^-31 of it; F16 is never scaled down and always exact. A block's 32 products are summed by two MMAs
 //   and added to the FP32 logit times the key's E8M0 scale.
 //   out = V^T p: rows are dims, k is the keys. A V scale belongs to (key, block):
 //   it multiplies the probabilities, as the power of two 2^(s - M + kLift) with M the
@@ -666,7 +666,7 @@ __global__ void __launch_bounds__(W * 32, CTAS) kv4_attend_kernel(const AttendAr
       }
       m = fmaxf(m, __shfl_xor_sync(kAll, m, 1));
       m = fmaxf(m, __shfl_xor_sync(kAll, m, 2));
-      const int sigma = pow2_shift_for(m);
+      const int sigma = BF16 ? pow2_shift_for(m) : max(0, pow2_shift_for(m));
       const float up = copysignf(exp2i(sigma), a.scale_log2);
 #pragma unroll
       for (int b = 0; b < NB; ++b) {

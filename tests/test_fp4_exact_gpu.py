@@ -144,3 +144,17 @@ def test_infinities_and_nan_in_x(N, K, B):
     x[2, 41] = float("nan")
     got, w64 = _run(codes, scales, x)
     _check(got, x, w64)
+
+
+@pytest.mark.parametrize("N,K,B", BATCHES)
+def test_f16_values_are_exact_beside_the_largest(N, K, B):
+    """The largest F16 values under zeros, the smallest subnormals under the rest."""
+    rng = np.random.default_rng(N + B)
+    codes = rng.integers(0, 16, (N, K), dtype=np.uint8)
+    codes[:, :8] = 0
+    scales = rng.integers(120, 124, (N, K // 32), dtype=np.uint8)
+    x = torch.from_numpy(rng.integers(-7, 8, (B, K)).astype(np.float32) * 2.0 ** -24).half().cuda()
+    x[:, 3] = 65504.0
+    x[1:, 5] = -32768.0
+    got, w64 = _run(codes, scales, x)
+    _check(got, x, w64)

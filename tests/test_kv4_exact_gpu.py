@@ -63,3 +63,21 @@ def test_outputs_that_only_improbable_keys_make(n, dim, group):
     q[:, :, 0] = 30.0
     out, _ = _attend(f, q)
     _check_elements(f, q, out, "bf16")
+
+
+@pytest.mark.parametrize("dim,group", [(64, 3), (128, 8), (128, 16), (256, 8)])
+def test_f16_queries_are_exact_beside_the_largest(dim, group):
+    """The largest F16 query under zeros of K, the smallest subnormals under large keys."""
+    def edit(k, v):
+        k *= 2.0 ** 10
+        k[:, :, :32] = 0
+    f = Filled([40, 3000], 1, dim, 16, "f16", edit=edit)
+    q = torch.from_numpy(f.rng.integers(-7, 8, (2, group, dim)).astype(np.float32) * 2.0 ** -24).half().cuda()
+    q[:, :, 5] = 65504.0
+    scale = 2.0 ** 14
+    out, _ = _attend(f, q, scale=scale)
+    for s in range(2):
+        want, _, mag, reach = ref.attend(q[s].double().cpu().numpy(), *f.of(s), scale)
+        d = ((dim / 32 + 32) * 2.0 ** -23 + 2.0 ** -22) * reach[:, None]
+        tol = (2 * d + 2.0 ** -17 + 2.0 ** -19) * mag + 2.0 ** -11 * 1.01 * np.abs(want) + 2.0 ** -25
+        assert (np.abs(out[s].double().cpu().numpy() - want) <= tol).all()
