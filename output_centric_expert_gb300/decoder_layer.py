@@ -41,7 +41,8 @@ class LayerWeights:
 
 
 class DecoderLayer:
-    """A layer with its step's buffers. `cache` is the layer's own KV cache."""
+    """A layer with its step's buffers. `cache` is the layer's own KV cache. A token's position is its
+    sequence's length before the step, below `max_positions`, for which the rotations are tabled."""
 
     def __init__(self, weights: LayerWeights, cache: block_ops.Kv4Cache, q_heads: int, max_batch: int,
                  max_positions: int, rope_base: float = 10000.0, eps: float = 1e-6):
@@ -68,6 +69,14 @@ class DecoderLayer:
         angle = torch.arange(max_positions, device=device, dtype=torch.float32)[:, None] * freq
         self.cos, self.sin = angle.cos(), angle.sin()
 
+    def _positions(self, seq_lens: torch.Tensor, err_flag: torch.Tensor | None) -> torch.Tensor:
+        """The tokens' rows in the rotations' tables. A length outside them takes the nearest and sets bit 0 of
+        err_flag, as the operators do with one outside the cache: nothing indexes a table with it."""
+        pos = seq_lens.clamp(0, self.cos.shape[0] - 1)
+        if err_flag is not None:
+            err_flag.bitwise_or_((pos != seq_lens).any())
+        return pos
+
     def _rotate(self, x: torch.Tensor, pos: torch.Tensor) -> None:
         """Rotate the halves of x [B, heads, dim] by its tokens' positions, in place."""
         cos, sin = self.cos[pos][:, None], self.sin[pos][:, None]
@@ -77,13 +86,14 @@ class DecoderLayer:
     def step(self, res: torch.Tensor, block_table: torch.Tensor, seq_lens: torch.Tensor,
              err_flag: torch.Tensor | None = None) -> torch.Tensor:
         """One token of each sequence through the layer: res [B, H] (bfloat16 or float32) is updated in
-        place and returned. seq_lens [B]: tokens that the cache holds before the step."""
+        place and returned. seq_lens [B]: tokens that the cache holds before the step. What has no place in the
+        cache or no rotation sets bit 0 of err_flag, and its output does not count."""
         w, B, D, n = self.w, res.shape[0], self.cache.dim, self.q_heads
         a, m, o, y = self.a[:B], self.m[:B], self.o[:B], self.y[:B]
         block_ops.wd_block_norm(res, None, a, w_pre=w.attn_pre, eps=self.eps)
         heads = block_ops.wd_fp4_matvec(w.qkv, a, self.qkv[:B]).view(B, -1, D)
         q, k, v = heads[:, :n], heads[:, n:n + self.cache.heads], heads[:, n + self.cache.heads:]
-        self._rotate(heads[:, :n + self.cache.heads], seq_lens.long())
+        self._rotate(heads[:, :n + self.cache.heads], self._positions(seq_lens, err_flag))
         block_ops.wd_kv4_append(self.cache, k, v, block_table, seq_lens, err_flag=err_flag)
         lens = torch.add(seq_lens, 1, out=self.lens[:B])
         block_ops.wd_kv4_attend(self.cache, q, block_table, lens, self.attn[:B], self.workspace, err_flag=err_flag)
