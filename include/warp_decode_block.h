@@ -191,7 +191,8 @@ moe_status wd_block_norm(int32_t T, int32_t H, const void* res, int32_t res_type
 
 /* wd_call -- the entry point `which` with its arguments, 8 bytes each, in their
  * order: integers and pointers as int64, floats as double. For bindings that pay
- * per argument; the result and the errors are the entry point's. */
+ * per argument; the result and the errors are the entry point's. An int32 argument
+ * whose word holds more is refused (MOE_ERR_SHAPE). */
 enum {
   WD_CALL_FP4_MATVEC = 0,
   WD_CALL_KV4_APPEND = 1,

@@ -12,13 +12,19 @@ namespace {
 // The next argument.
 struct Args {
   const char* at;
+  explicit Args(const void* args) : at(static_cast<const char*>(args)) {}
   int64_t word() {
     int64_t v;
     std::memcpy(&v, at, 8);
     at += 8;
     return v;
   }
-  int32_t i32() { return (int32_t)word(); }
+  bool wide = false;  // an argument of 32 bits does not fit them
+  int32_t i32() {
+    const int64_t v = word();
+    wide |= v != (int32_t)v;
+    return (int32_t)v;
+  }
   float f32() {
     double v;
     std::memcpy(&v, at, 8);
@@ -35,7 +41,8 @@ struct Args {
 
 extern "C" moe_status wd_call(int32_t which, const void* args) {
   if (!args) return wd::refuse(MOE_ERR_NULL, "wd_call: arguments are required");
-  Args a = {static_cast<const char*>(args)};
+  Args a(args);
+  auto refused = [] { return wd::refuse(MOE_ERR_SHAPE, "wd_call: an argument does not fit its 32 bits"); };
   // (each read on its own: the order in which a call's operands are evaluated is open)
   switch (which) {
     case WD_CALL_FP4_MATVEC: {
@@ -48,6 +55,7 @@ extern "C" moe_status wd_call(int32_t which, const void* args) {
       auto* y = a.ptr<void>();
       const int32_t yt = a.i32();
       const int64_t ldy = a.word();
+      if (a.wide) return refused();
       return wd_fp4_matvec(s, pc, ps, x, xt, ldx, B, y, yt, ldy, a.ptr<void>());
     }
     case WD_CALL_KV4_APPEND:
@@ -63,6 +71,7 @@ extern "C" moe_status wd_call(int32_t which, const void* args) {
       const int32_t S = a.i32();
       auto* err = a.ptr<int32_t>();
       auto* st = a.ptr<void>();
+      if (a.wide) return refused();
       return which == WD_CALL_KV4_APPEND ? wd_kv4_append(c, k, v, type, ldk, ldv, T, table, blocks, lens, cu, S, err, st)
                                          : wd_kv4_gather(c, k, v, type, ldk, ldv, T, table, blocks, lens, cu, S, err, st);
     }
@@ -83,6 +92,7 @@ extern "C" moe_status wd_call(int32_t which, const void* args) {
       auto* work = a.ptr<void>();
       const size_t bytes = (size_t)a.word();
       auto* err = a.ptr<int32_t>();
+      if (a.wide) return refused();
       return wd_kv4_attend(c, q, type, ldq, S, heads, table, blocks, lens, scale, window, out, ldo, lse, work, bytes,
                            err, a.ptr<void>());
     }
@@ -104,6 +114,7 @@ extern "C" moe_status wd_call(int32_t which, const void* args) {
       auto* out = a.ptr<void>();
       const int32_t ot = a.i32();
       const int64_t ldo = a.word();
+      if (a.wide) return refused();
       return wd_block_norm(T, H, res, rt, ldr, y, yt, ldy, post, pre, gate, wt, gate_ld, gate_step, res_scale, eps,
                            res_out, ldro, out, ot, ldo, a.ptr<void>());
     }

@@ -43,3 +43,29 @@ def test_attend_refuses_more_tiles_than_it_counts():
     c = ctypes.byref(block_ops.Kv4Struct(2, 16, 8, 128, P, P, P, P))
     assert block_ops.lib().wd_kv4_attend(c, P, 1, 1024, 1 << 20, 8, P, 1 << 20, P, 1.0, 0, P, 1024, P, P, 1 << 40, None, None) == 2
     assert b"capacity" in block_ops.lib().moe_last_error()
+
+
+P = 0x20000  # a fake device address, never dereferenced
+SHAPE = block_ops.Fp4Shape(16, 128)
+CACHE = block_ops.Kv4Struct(2, 16, 2, 128, P, P, P, P)
+CALLS = {  # arguments that launch nothing, and which of them have 32 bits
+    "matvec": (block_ops._MATVEC, block_ops._matvec_args, [ctypes.addressof(SHAPE), P, P, P, 1, 128, 0, P, 0, 16, 0], [4, 6, 8]),
+    "append": (block_ops._APPEND, block_ops._token_args, [ctypes.addressof(CACHE), P, P, 1, 256, 256, 0, P, 4, P, P, 0, 0, 0], [3, 6, 8, 11]),
+    "gather": (block_ops._GATHER, block_ops._token_args, [ctypes.addressof(CACHE), P, P, 1, 256, 256, 0, P, 4, P, P, 0, 0, 0], [3, 6, 8, 11]),
+    "attend": (block_ops._ATTEND, block_ops._attend_args,
+               [ctypes.addressof(CACHE), P, 1, 512, 0, 4, P, 4, P, 1.0, 7, P, 512, P, P, 1 << 30, 0, 0], [2, 4, 5, 7, 10]),
+    "norm": (block_ops._NORM, block_ops._norm_args, [0, 64, P, 1, 64, P, 0, 64, P, P, P, 0, 0, 1, 1.0, 1e-6, P, 64, P, 1, 64, 0],
+             [0, 1, 3, 6, 11, 13, 19])}
+
+
+@pytest.mark.parametrize("name,at", [(n, None) for n in CALLS] + [(n, at) for n, c in CALLS.items() for at in c[3]])
+def test_a_word_past_32_bits_is_refused_and_not_cut(name, at):
+    which, pack, args, _ = CALLS[name]
+    if at is None:
+        assert block_ops.lib().wd_call(which, pack(*args)) == 0
+        return
+    for past in (1 << 32, -(1 << 32), 1 << 62):  # what is left of it in 32 bits would be taken
+        wide = list(args)
+        wide[at] += past
+        assert block_ops.lib().wd_call(which, pack(*wide)) == 2
+        assert b"32 bits" in block_ops.lib().moe_last_error()
