@@ -148,8 +148,17 @@ class Fp4Weights:
         if not all(sizes):
             raise ValueError(f"Fp4Weights: unsupported shape [{N}, {K}] (K % 32 == 0, 32 <= K <= 65536)")
         self.N, self.K = N, K
-        self.codes, self.scales = (torch.empty(n, dtype=torch.uint8, device=device) for n in sizes)
-        self._ptrs = self.codes.data_ptr(), self.scales.data_ptr()
+        self._tensors = tuple(torch.empty(n, dtype=torch.uint8, device=device) for n in sizes)
+        self._ptrs = tuple(t.data_ptr() for t in self._tensors)
+
+    # read-only: the kernels are given the addresses taken above
+    @property
+    def codes(self) -> torch.Tensor:
+        return self._tensors[0]
+
+    @property
+    def scales(self) -> torch.Tensor:
+        return self._tensors[1]
 
     @classmethod
     def from_codes(cls, codes: torch.Tensor, scales: torch.Tensor, stream=None) -> "Fp4Weights":
@@ -203,9 +212,14 @@ class Kv4Cache:
         if not codes:
             raise ValueError(f"Kv4Cache: unsupported sizes: pages {pages}, page_size {page_size} (16 to 256, a power "
                              f"of two), heads {heads}, dim {dim} (64, 128 or 256)")
-        self.tensors = [torch.zeros(n, dtype=torch.uint8, device=device) for n in (codes, scales, codes, scales)]
+        self._tensors = tuple(torch.zeros(n, dtype=torch.uint8, device=device) for n in (codes, scales, codes, scales))
         (self.struct.k_codes, self.struct.k_scales, self.struct.v_codes,
-         self.struct.v_scales) = (t.data_ptr() for t in self.tensors)
+         self.struct.v_scales) = (t.data_ptr() for t in self._tensors)
+
+    @property
+    def tensors(self) -> tuple:
+        """K's codes and scales, V's codes and scales. Read-only: the kernels are given their addresses."""
+        return self._tensors
 
     @property
     def nbytes(self) -> int:

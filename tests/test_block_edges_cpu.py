@@ -2,6 +2,7 @@
 import ctypes
 
 import pytest
+import torch
 
 from output_centric_expert_gb300 import block_ops
 
@@ -69,3 +70,18 @@ def test_a_word_past_32_bits_is_refused_and_not_cut(name, at):
         wide[at] += past
         assert block_ops.lib().wd_call(which, pack(*wide)) == 2
         assert b"32 bits" in block_ops.lib().moe_last_error()
+
+
+def test_tensors_whose_addresses_are_held_cannot_be_replaced():
+    """Replaced tensors would leave the kernels on the old memory."""
+    w = block_ops.Fp4Weights(16, 128, device="cpu")
+    for name in ("codes", "scales"):
+        with pytest.raises(AttributeError):
+            setattr(w, name, torch.zeros_like(getattr(w, name)))
+    assert w._ptrs == (w.codes.data_ptr(), w.scales.data_ptr())
+    c = block_ops.Kv4Cache(2, 16, 1, 64, device="cpu")
+    with pytest.raises(AttributeError):
+        c.tensors = [t.clone() for t in c.tensors]
+    with pytest.raises(TypeError):
+        c.tensors[2] = c.tensors[2].clone()
+    assert (c.struct.k_codes, c.struct.k_scales, c.struct.v_codes, c.struct.v_scales) == tuple(t.data_ptr() for t in c.tensors)
