@@ -101,6 +101,22 @@ def _stream(stream, t: torch.Tensor) -> int:
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else stream
 
 
+def _hand_over(stream, *tensors: torch.Tensor) -> None:
+    """Let `stream` use tensors of the current stream: it waits for what that one has queued (their memory may still
+    be in use there), and their memory is kept until its own work is done."""
+    device = tensors[0].device
+    if stream is None or device.type != "cuda":
+        return
+    current = torch.cuda.current_stream(device)
+    if not hasattr(stream, "cuda_stream"):
+        stream = torch.cuda.ExternalStream(stream, device) if stream else torch.cuda.default_stream(device)
+    if stream.cuda_stream == current.cuda_stream:
+        return
+    stream.wait_stream(current)
+    for t in tensors:
+        t.record_stream(stream)
+
+
 def _type(t: torch.Tensor, name: str) -> int:
     code = _TYPES.get(t.dtype)
     if code is None:
@@ -139,7 +155,12 @@ def _flag(t: torch.Tensor) -> int:
 # ---------------------------------------------------------- 4-bit projections --
 
 class Fp4Weights:
-    """MXFP4 weights [N, K] on the GPU in the packed layout of warp_decode_block.h."""
+    """MXFP4 weights [N, K] on the GPU in the packed layout of warp_decode_block.h.
+
+    `stream` of the two constructors: where they are packed, behind what the current stream has queued (it needs no
+    waiting for the inputs, and they may be freed at once). Another stream, the current one too, has to wait for it
+    before it uses the weights.
+    """
 
     def __init__(self, N: int, K: int, device="cuda"):
         self.shape = Fp4Shape(N, K)
@@ -168,6 +189,7 @@ class Fp4Weights:
             if t.dtype != torch.uint8 or t.shape != shape or not t.is_contiguous():
                 raise ValueError(f"{name}: expected contiguous uint8 {shape}, got {t.dtype} {tuple(t.shape)}")
         w = cls(N, K, codes.device)
+        _hand_over(stream, codes, scales, *w._tensors)
         _check("wd_fp4_pack_codes", lib().wd_fp4_pack_codes(
             w._shape, codes.data_ptr(), scales.data_ptr(), *w._ptrs, _stream(stream, codes)))
         return w
@@ -178,6 +200,7 @@ class Fp4Weights:
         if w.dim() != 2:
             raise ValueError(f"w: expected [N, K], got {tuple(w.shape)}")
         out = cls(w.shape[0], w.shape[1], w.device)
+        _hand_over(stream, w, *out._tensors)
         _check("wd_fp4_pack_weights", lib().wd_fp4_pack_weights(
             out._shape, w.data_ptr(), _type(w, "w"), _rows(w, w.shape, w.shape[1], "w"), *out._ptrs, _stream(stream, w)))
         return out
