@@ -97,7 +97,7 @@ def _check(fn: str, status: int) -> None:
 
 def _stream(stream, t: torch.Tensor) -> int:
     if stream is None:
-        return _raw_stream(t.get_device()) if t.is_cuda else 0
+        return _raw_stream(t.get_device())
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else stream
 
 
@@ -117,10 +117,16 @@ def _hand_over(stream, *tensors: torch.Tensor) -> None:
         t.record_stream(stream)
 
 
+def _elsewhere(name: str):
+    raise ValueError(f"{name}: not on a GPU")
+
+
 def _type(t: torch.Tensor, name: str) -> int:
     code = _TYPES.get(t.dtype)
     if code is None:
         raise TypeError(f"{name}: dtype {t.dtype} is not float32, bfloat16 or float16")
+    if not t.is_cuda:
+        _elsewhere(name)
     return code
 
 
@@ -143,12 +149,16 @@ def _ints(t: torch.Tensor, shape: tuple, name: str) -> int:
         raise TypeError(f"{name}: dtype {t.dtype} is not int32")
     if t.shape != shape or not t.is_contiguous():
         raise ValueError(f"{name}: expected a contiguous tensor of shape {tuple(shape)}, got {tuple(t.shape)}")
+    if not t.is_cuda:
+        _elsewhere(name)
     return t.data_ptr()
 
 
 def _flag(t: torch.Tensor) -> int:
     if t.dtype is not torch.int32:
         raise TypeError(f"err_flag: dtype {t.dtype} is not int32")
+    if not t.is_cuda or t.numel() == 0:
+        raise ValueError("err_flag: expected an element on a GPU")
     return t.data_ptr()
 
 
@@ -171,6 +181,7 @@ class Fp4Weights:
         self.N, self.K = N, K
         self._tensors = tuple(torch.empty(n, dtype=torch.uint8, device=device) for n in sizes)
         self._ptrs = tuple(t.data_ptr() for t in self._tensors)
+        self._on_gpu = self._tensors[0].is_cuda
 
     # read-only: the kernels are given the addresses taken above
     @property
@@ -188,6 +199,8 @@ class Fp4Weights:
         for t, shape, name in ((codes, (N, K // 2), "codes"), (scales, (N, K // 32), "scales")):
             if t.dtype != torch.uint8 or t.shape != shape or not t.is_contiguous():
                 raise ValueError(f"{name}: expected contiguous uint8 {shape}, got {t.dtype} {tuple(t.shape)}")
+            if not t.is_cuda:
+                _elsewhere(name)
         w = cls(N, K, codes.device)
         _hand_over(stream, codes, scales, *w._tensors)
         _check("wd_fp4_pack_codes", lib().wd_fp4_pack_codes(
@@ -199,10 +212,11 @@ class Fp4Weights:
         """Quantise w [N, K] (float32, bfloat16 or float16, on the GPU) to MXFP4."""
         if w.dim() != 2:
             raise ValueError(f"w: expected [N, K], got {tuple(w.shape)}")
+        kind = _type(w, "w")
         out = cls(w.shape[0], w.shape[1], w.device)
         _hand_over(stream, w, *out._tensors)
         _check("wd_fp4_pack_weights", lib().wd_fp4_pack_weights(
-            out._shape, w.data_ptr(), _type(w, "w"), _rows(w, w.shape, w.shape[1], "w"), *out._ptrs, _stream(stream, w)))
+            out._shape, w.data_ptr(), kind, _rows(w, w.shape, w.shape[1], "w"), *out._ptrs, _stream(stream, w)))
         return out
 
     @property
@@ -213,6 +227,8 @@ class Fp4Weights:
 def wd_fp4_matvec(weights: Fp4Weights, x: torch.Tensor, y: torch.Tensor, stream=None) -> torch.Tensor:
     """y[B, N] = x[B, K] W^T; x bfloat16 or float16, y float32, bfloat16 or float16."""
     B, K, N = x.shape[0], weights.K, weights.N
+    if not weights._on_gpu:
+        _elsewhere("weights")
     codes, scales = weights._ptrs
     status = _lib_cache.wd_call(_MATVEC, _matvec_args(
         weights._at, codes, scales, x.data_ptr(), _type(x, "x"), _rows(x, (B, K), K, "x"), B,
@@ -238,6 +254,7 @@ class Kv4Cache:
         self._tensors = tuple(torch.zeros(n, dtype=torch.uint8, device=device) for n in (codes, scales, codes, scales))
         (self.struct.k_codes, self.struct.k_scales, self.struct.v_codes,
          self.struct.v_scales) = (t.data_ptr() for t in self._tensors)
+        self._on_gpu = self._tensors[0].is_cuda
 
     @property
     def tensors(self) -> tuple:
@@ -253,6 +270,8 @@ def _tokens(fn: str, which: int, cache: Kv4Cache, k, v, block_table, seq_lens, c
     T, S, blocks = k.shape[0], seq_lens.shape[0], block_table.shape[-1]
     if v.dtype != k.dtype:
         raise TypeError(f"v: dtype {v.dtype} differs from k's {k.dtype}")
+    if not (cache._on_gpu and v.is_cuda):
+        _elsewhere("cache or v")
     row = cache.heads * cache.dim
     shape = (T, cache.heads, cache.dim)
     status = _lib_cache.wd_call(which, _token_args(
@@ -300,6 +319,10 @@ def wd_kv4_attend(cache: Kv4Cache, q: torch.Tensor, block_table: torch.Tensor, s
         raise TypeError(f"out: dtype {out.dtype} differs from q's {q.dtype}")
     if lse is not None and (lse.dtype != torch.float32 or lse.shape != (S, q_heads) or not lse.is_contiguous()):
         raise ValueError(f"lse: expected contiguous float32 {(S, q_heads)}, got {lse.dtype} {tuple(lse.shape)}")
+    if not (cache._on_gpu and out.is_cuda and workspace.is_cuda and (lse is None or lse.is_cuda)):
+        _elsewhere("cache, out, workspace or lse")
+    if not workspace.is_contiguous():
+        raise ValueError("workspace: must be contiguous")
     D, blocks = cache.dim, block_table.shape[-1]
     shape, row = (S, q_heads, D), q_heads * D
     status = _lib_cache.wd_call(_ATTEND, _attend_args(
@@ -320,6 +343,8 @@ def _weight(w: torch.Tensor, H: int, kind: torch.dtype, name: str) -> int:
         raise TypeError("w_post, w_pre and gate must have one dtype")
     if w.shape != (H,) or not w.is_contiguous():
         raise ValueError(f"{name}: expected contiguous [{H}], got {tuple(w.shape)}")
+    if not w.is_cuda:
+        _elsewhere(name)
     return w.data_ptr()
 
 
@@ -345,6 +370,8 @@ def wd_block_norm(res: torch.Tensor, res_out: torch.Tensor | None = None, out: t
         rows, cols = gate.shape if gate.dim() == 2 else (0, 0)
         if rows not in (1, T) or cols not in (1, H):
             raise ValueError(f"gate: shape {tuple(gate.shape)} does not broadcast to {(T, H)}")
+        if not gate.is_cuda:
+            _elsewhere("gate")
         gp = gate.data_ptr()
         gate_ld = gate.stride(0) if rows > 1 else 0
         gate_step = gate.stride(1) if cols > 1 else 0
@@ -353,6 +380,8 @@ def wd_block_norm(res: torch.Tensor, res_out: torch.Tensor | None = None, out: t
     if res_out is not None:
         if res_out.dtype != res.dtype:
             raise TypeError(f"res_out: dtype {res_out.dtype} differs from res's {res.dtype}")
+        if not res_out.is_cuda:
+            _elsewhere("res_out")
         rp, rl = res_out.data_ptr(), _rows(res_out, shape, H, "res_out")
     if out is not None:
         op, ot, ol = out.data_ptr(), _type(out, "out"), _rows(out, shape, H, "out")
