@@ -7,7 +7,7 @@
 namespace wd {
 namespace {
 
-__host__ __device__ inline int64_t row_tiles(int N) { return (N + kTileRows - 1) / kTileRows; }
+__host__ __device__ inline int64_t row_tiles(int N) { return (N - 1) / kTileRows + 1; }  // (N + 15 may pass 2^31)
 __host__ __device__ inline int col_tiles(int K) { return (K + kTileCols - 1) / kTileCols; }
 
 // ---------------------------------------------------------------- packers --
@@ -357,7 +357,8 @@ moe_status launch_matvec(MvArgs a, cudaStream_t st) {
                                                                             : fp4_matvec_kernel<BF16, kChunked>;
   moe_status rc = once[mode].allow(k, kMaxDynSmem - kStaticSmem);
   if (rc != MOE_OK) return rc;
-  for (a.tok0 = 0; a.tok0 < a.B; a.tok0 += kMvTokens) {
+  for (int64_t tok = 0; tok < a.B; tok += kMvTokens) {
+    a.tok0 = (int)tok;
     k<<<grid, kMvThreads, smem, st>>>(a);
     if ((rc = launched("wd_fp4_matvec launch")) != MOE_OK) return rc;
   }

@@ -178,7 +178,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) fp4_tc_kernel(const MvArgs a, i
   const int toks = min(n, a.B - a.tok0);
   const int log = 31 - __clz(size), nlog = 31 - __clz(n);
   const int ct = (a.K + kTileCols - 1) / kTileCols, c0 = (ct * rank) >> log, kt = ((ct * (rank + 1)) >> log) - c0;
-  const int tiles = (a.N + kTileRows - 1) / kTileRows;
+  const int tiles = (a.N - 1) / kTileRows + 1;
   const int set = blockIdx.x >> log;  // a cluster's row tiles [q0, q1)
   const int q0 = set * a.per + min(set, a.more), q1 = q0 + a.per + (set < a.more ? 1 : 0);
   uint4* xs = dyn4 + (1024 - (smem_addr(dyn4) & 1023)) % 1024 / 16;  // the swizzle counts from 1024-byte boundaries
@@ -491,7 +491,7 @@ int stage_tiles(int n) { return kStageX / (n * 2 * kTileCols); }  // column tile
 template <bool BF16>
 moe_status launch(MvArgs a, cudaStream_t st) {
   auto k = fp4_tc_kernel<BF16>;
-  const int ct = (a.K + kTileCols - 1) / kTileCols, mt = (a.N + kTcRows - 1) / kTcRows;
+  const int ct = (a.K + kTileCols - 1) / kTileCols, mt = (a.N - 1) / kTcRows + 1;
   int n = tokens_up(a.B - a.tok0);
   while (n > 16 && ct > kMaxCluster * stage_tiles(n)) n /= 2;
   const size_t room = kStageX + (size_t)kRowTiles * 64 * kTcRows * 4 + 1024;
@@ -521,7 +521,8 @@ moe_status launch(MvArgs a, cudaStream_t st) {
   cfg.stream = st;
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
-  for (; a.tok0 < a.B; a.tok0 += n) {
+  for (int64_t tok = a.tok0; tok < a.B; tok += n) {
+    a.tok0 = (int)tok;
     const cudaError_t e = cudaLaunchKernelEx(&cfg, k, a, n);
     if (e != cudaSuccess) {
       set_error("wd_fp4_matvec launch", e);

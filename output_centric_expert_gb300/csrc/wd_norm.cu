@@ -167,8 +167,8 @@ __global__ void __launch_bounds__(N == 32 ? kThreads : VEC ? 1024 : N, N == 32 ?
   __shared__ float red[2][32];
   const int i = WARP ? (threadIdx.x & 31) : threadIdx.x;
   const int per = WARP ? blockDim.x >> 5 : 1;       // rows of a CTA at a time
-  const int step = gridDim.x * per;
-  int tok = blockIdx.x * per + (WARP ? threadIdx.x >> 5 : 0);
+  const uint32_t step = gridDim.x * per, T = a.T;  // (unsigned: the last row and a step may pass 2^31)
+  uint32_t tok = blockIdx.x * per + (WARP ? threadIdx.x >> 5 : 0);
   int slot = 0;
   const int rt = RT >= 0 ? RT : a.res_type, yt = YT >= 0 ? YT : a.y_type;
   const bool own_gate = a.gate && a.gate_ld != 0;  // a gate row or value per token
@@ -219,7 +219,7 @@ __global__ void __launch_bounds__(N == 32 ? kThreads : VEC ? 1024 : N, N == 32 ?
   }
 
   const float per_channel = 1.0f / (float)a.H;
-  for (int stage = 0; tok < a.T; tok += step, stage = stage + 1 == DEPTH ? 0 : stage + 1) {
+  for (int stage = 0; tok < T; tok += step, stage = stage + 1 == DEPTH ? 0 : stage + 1) {
     float y[8], r[8];
     Raw rg;
     float g1 = 1.0f;

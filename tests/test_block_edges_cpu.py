@@ -85,3 +85,10 @@ def test_tensors_whose_addresses_are_held_cannot_be_replaced():
     with pytest.raises(TypeError):
         c.tensors[2] = c.tensors[2].clone()
     assert (c.struct.k_codes, c.struct.k_scales, c.struct.v_codes, c.struct.v_scales) == tuple(t.data_ptr() for t in c.tensors)
+
+
+@pytest.mark.parametrize("N", [INT_MAX - 15, INT_MAX - 14, INT_MAX])
+def test_the_most_rows(N):
+    sh = ctypes.byref(block_ops.Fp4Shape(N, 32))
+    assert block_ops.lib().wd_fp4_packed_bytes(sh, 0) == -(-N // 16) * 1024
+    assert block_ops.lib().wd_fp4_packed_bytes(sh, 1) == -(-N // 16) * 64
