@@ -169,8 +169,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) fp4_tc_kernel(const MvArgs a, i
   __shared__ uint32_t s_max[64], s_tmem, s_failed, s_again;  // s_again: an output is not finite
   __shared__ __align__(16) float s_back[64];  // 1 / the tokens' powers of two
   __shared__ __align__(8) uint64_t s_bar[kGroups];
-  __shared__ uint8_t s_top[kGroups][kTcRows];
-  __shared__ uint8_t s_low[kGroups][kTcRows];  // whether the row has blocks that A has as 0 although they are not
+  __shared__ uint16_t s_top[kGroups][kTcRows];  // and bit 8: the row has blocks that A has as 0 although they are not
   cg::cluster_group cluster = cg::this_cluster();
   const int rank = cluster.block_rank(), size = cluster.num_blocks();
   const int tid = threadIdx.x, warp = tid >> 5, group = tid >> 7, gt = tid & 127;
@@ -265,7 +264,6 @@ __global__ void __launch_bounds__(kTcThreads, 1) fp4_tc_kernel(const MvArgs a, i
     if (q + side < q1) {
       const uint32_t top = next_top;
       uint32_t low = 0;
-      s_top[group][gt] = (uint8_t)top;
       for (int k0 = 0; k0 < my_kt; k0 += kTcAhead) {
 #pragma unroll
         for (int i = 0; i < kTcAhead; ++i) {
@@ -281,7 +279,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) fp4_tc_kernel(const MvArgs a, i
             mul[1] = __byte_perm(e13 << 10, 0, 0x1010), mul[3] = __byte_perm(e13 << 10, 0, 0x3232);
             if ((__vmaxs2(e02, e13) + 0x7FE47FE4u) & 0x80008000u)  // the row's sum is NaN
               mul[0] = mul[1] = mul[2] = mul[3] = 0x7E007E00u;
-            if (((e02 + 0x7FFF7FFFu) & (e13 + 0x7FFF7FFFu) & 0x80008000u) != 0x80008000u) {  // a multiplier is 0
+            if (((__vminu2(e02, e13) + 0x7FFF7FFFu) & 0x80008000u) != 0x80008000u) {  // a multiplier is 0
 #pragma unroll
               for (int b = 0; b < 4; ++b)
                 if (mul[b] == 0) low |= buf[i].a.w[b] | buf[i].a.w[4 + b] | buf[i].b.w[b] | buf[i].b.w[4 + b];
@@ -340,7 +338,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) fp4_tc_kernel(const MvArgs a, i
       }
       asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
       asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
-      s_low[group][gt] = (low & 0x77777777u) != 0;
+      s_top[group][gt] = (uint16_t)(top | ((low & 0x77777777u) != 0 ? 256 : 0));
       if (!ok) s_failed = 1;
       pair_sync(side);  // both halves' sums are there
       asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
@@ -350,13 +348,15 @@ __global__ void __launch_bounds__(kTcThreads, 1) fp4_tc_kernel(const MvArgs a, i
       // D holds the sum times 2^(12 - (top - 127)) and the token's power of two. Taken off
       // one after the other where neither step can leave FP32's range, else in one.
       // Either half adds both halves' sums of its half of the tokens.
-      const uint32_t t0 = s_top[side * 2][gt], t1 = kt > 1 ? s_top[side * 2 + 1][gt] : t0;
+      const uint32_t half0 = s_top[side * 2][gt], half1 = s_top[side * 2 + 1][gt];
+      const uint32_t t0 = half0 & 255u, t1 = kt > 1 ? half1 & 255u : t0;
       const bool plain = __all_sync(0xFFFFFFFFu, min(t0, t1) >= 64u && max(t0, t1) <= 190u);
       const float fail = s_failed ? NAN : 1.0f;  // a wait that ran out: no sum to trust
       const float back0 = plain ? exp2i((int)t0 - 139) * fail : fail, back1 = plain ? exp2i((int)t1 - 139) * fail : fail;
       const uint32_t d0 = s_tmem + side * 2 * (kTmemCols / kGroups) + ((uint32_t)(warp & 3) << 21) + 64;
       const int64_t row = (int64_t)(q + side) * kTcRows + gt;
-      const bool low = row < a.N && (s_low[side * 2][gt] | s_low[side * 2 + 1][gt]);
+      const bool low = row < a.N && ((half0 | half1) & 256u);
+      const bool any_low = __any_sync(0xFFFFFFFFu, low);
       const uint32_t slot = smem_addr(sums + ((side << log) + rank) * own * kTcRows + gt);
       uint32_t place = 0;
 #pragma unroll 1
@@ -383,7 +383,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) fp4_tc_kernel(const MvArgs a, i
               if (j == k) o[k] = v;
           }
         }
-        if (__any_sync(0xFFFFFFFFu, low)) {
+        if (any_low) {
 #pragma unroll 1
           for (int j = 0; low && j < 8 && c + j < toks; ++j) {
             float v = 0.0f;
@@ -402,10 +402,11 @@ __global__ void __launch_bounds__(kTcThreads, 1) fp4_tc_kernel(const MvArgs a, i
         if (size == 1) {
 #pragma unroll
           for (int j = 0; j < 8; ++j)
-            if (c + j < toks && row < a.N) {
-              store_elem(a.y, a.y_type, (int64_t)(a.tok0 + c + j) * a.ldy + row, o[j]);
-              if (!(fabsf(o[j]) < INFINITY)) s_again = 1;
-            }
+            if (c + j < toks && row < a.N) store_elem(a.y, a.y_type, (int64_t)(a.tok0 + c + j) * a.ldy + row, o[j]);
+          float all = 0.0f;
+#pragma unroll
+          for (int j = 0; j < 8; ++j) all += fabsf(o[j]);
+          if (!(all < INFINITY)) s_again = 1;
         } else {
 #pragma unroll
           for (int j = 0; j < 8; j += 2) {  // own >= 2
