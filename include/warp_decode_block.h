@@ -68,11 +68,12 @@ moe_status wd_fp4_pack_weights(const wd_fp4_shape* shape, const void* w, int32_t
  * used exactly, BF16 ones down to 2^-31 of their token's largest finite one; below that
  * they are off by at most 2^-39 of it. Any scales may stand beside one another in a row (with more
  * than 8 tokens, blocks below 2^-26 of their row's largest scale are slower, where
- * they are not zeros). Up to 8 tokens one
- * kernel streams the weights through mma.sync; more go through tcgen05 (K up
- * to 32768), 64 at a time. The results are the same on every call; a token's do
- * not depend on the other tokens' values, but their order of summation does on
- * the batch's size.
+ * they are not zeros; so are calls with results that are not finite). Up to 8
+ * tokens one kernel streams the weights through mma.sync; more go through tcgen05,
+ * 64 at a time, 32 above K = 8192, 16 above K = 16384, or 8 at a time through the
+ * first above K = 32768. The results are the same on every call; a token's do not
+ * depend on the other tokens' values, but their order of summation does on the
+ * batch's size.
  */
 moe_status wd_fp4_matvec(const wd_fp4_shape* shape, const uint8_t* packed_codes,
                          const uint8_t* packed_scales, const void* x, int32_t x_type,
@@ -148,7 +149,8 @@ moe_status wd_kv4_gather(const wd_kv4_cache* cache, void* k_out, void* v_out, in
  * Logits, softmax statistics and sums are FP32; q is used as exactly as x above (per head). The weight of a value's block, its
  * probability times its E8M0 scale, has 16 bits and FP32's range of exponents: a
  * probability below 2^-126 of the row's largest counts as 0, and a weight below 2^-140
- * of the largest probability times the block's largest scale among the keys.
+ * of the largest probability times the block's largest scale among the keys. Keys and
+ * values of up to 2^100 in magnitude do not overflow a sum on the way.
  * workspace: wd_kv4_attend_workspace bytes, 16-byte aligned; its contents do not
  * matter before or after a call. Calls that may overlap need one each.
  * pages * heads * (page_size / 16) < 2^31, 1 TB of codes.

@@ -422,7 +422,8 @@ extern "C" moe_status wd_fp4_matvec(const wd_fp4_shape* s, const uint8_t* pc, co
   cudaStream_t st = (cudaStream_t)stream;
   // Up to 8 tokens (and where rows are too long for the other kernel's shared memory) the stream kernel:
   // it reads the weights once per 8 tokens. us for 8 and 9 tokens: 10.3 and 18.0 against 11.9 and 10.8 for
-  // 9216 x 4096, 5.4 and 9.7 against 7.3 and 6.9 for 2048 x 2048, 30 and 59 against 50 and 42 for 65536 x 4096.
+  // 9216 x 4096, 5.4 and 9.7 against 7.3 and 6.9 for 2048 x 2048, 30 and 59 against 50 and 42 for 65536 x 4096
+  // (when the other kernel had no test for quiet blocks, 1 to 5 % of it).
   if (B > 8 && s->K <= tc_most_columns(B)) return launch_tc(a, x_type == WD_BF16, st);
   return x_type == WD_BF16 ? launch_matvec<true>(a, st) : launch_matvec<false>(a, st);
 }

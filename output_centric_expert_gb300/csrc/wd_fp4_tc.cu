@@ -22,12 +22,12 @@
 // pair's sums are added on their way out of tensor memory; the CTAs' go to the one that
 // writes their tokens, through distributed shared memory, and are added there in order.
 //
-// Bound. 64 tokens of 9216 x 4096 (20 MB, 4.8 GFLOP): 14.9 us, of which 2.5 are the
+// Bound. 64 tokens of 9216 x 4096 (20 MB, 4.8 GFLOP): 15.3 us, of which 2.5 are the
 // launch, 4.7 x (1.7 for its trip from L2 to all SMs, the rest largest magnitudes and
 // conversion), 4.1 the loop (about 330 instructions per warp and column tile of 128,
 // 64 of them conversions at half rate), 3.4 the sums. Tensor cores are busy 14 % of it,
-// DRAM 20 %. Large matrices are held by the loop: 16 tokens of 65536 x 4096 42.4 us,
-// 3.4 TB/s; 64 tokens 77 us.
+// DRAM 20 %. Large matrices are held by the loop: 16 tokens of 65536 x 4096 43.3 us,
+// 3.3 TB/s; 64 tokens 79 us (42.1 and 77 without the test for blocks that A has as 0).
 #include <cooperative_groups.h>
 
 #include <mutex>

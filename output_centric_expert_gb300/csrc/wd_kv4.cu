@@ -14,9 +14,9 @@ namespace {
 // two shuffles. Both kernels are bound by integer instructions (conversions,
 // packing, addresses), so magnitudes are compared as 16-bit pairs and a thread steps
 // through its pieces without divisions. Prompts of 9.7k tokens, 8 heads of dim 128, into
-// the cache and back (100 MB): 23.6 us, 4.2 TB/s, half of it places, first loads and the
-// two launches; 262k tokens of 4 heads into it 98 us, DRAM 69 %, ALU 64 %. One token each
-// of 64 sequences: 3.7 us a launch.
+// the cache and back (100 MB): 23.5 us, 4.3 TB/s, half of it places, first loads and the
+// two launches; 262k tokens of 4 heads into it 98 us, DRAM 70 %, ALU 64 %. One token each
+// of 64 sequences: 3.6 us a launch.
 
 struct TokenArgs {
   const int32_t *table, *lens, *cu;

@@ -30,10 +30,11 @@
 // parts of one row: one SM reads them all.)
 //
 // Bound. 64 sequences of up to 8192 keys with 16 heads per KV head (119 MB): 62.5 us,
-// 1.9 TB/s; one of 131071 with 8 heads (71 MB): 32.0 us, 2.2 TB/s. Decoding, scaling, the
-// softmax and 96 MMAs per warp and 32 keys of 16 heads: registers leave 12
-// to 16 warps per SM, too few to hide every dependency. The first 6 us are a chain of
-// trips to memory: lengths, block table, keys.
+// 1.9 TB/s; one of 131071 with 8 heads (71 MB): 32.0 us, 2.2 TB/s. Decoding, scaling and
+// the softmax are about 1170 instructions per warp and 32 keys for 16 heads (96 of them
+// MMAs), issued in 45 % of the cycles: registers leave 12 to 16 warps per SM, too few to
+// hide every dependency. The first 6 us are a chain of trips to memory: lengths, block
+// table, keys.
 #include "wd_block.cuh"
 #include "wd_kv4.cuh"
 
@@ -49,7 +50,8 @@ constexpr int kLift = 122;      // a weight is p 2^(s - M + 122): up to 2^126, w
 
 // What a row costs beside its tiles (queries staged, sums joined), in tiles: CTAs share
 // both out. 1, 2, 3: 45.0, 43.6, 44.9 us for 64 sequences up to 4096 with 8 heads, 17.1,
-// 16.1, 16.1 for 16 up to 16384 of dim 64; 53.3, 52.0, 52.1 for 64 up to 8192 with 16 heads.
+// 16.1, 16.1 for 16 up to 16384 of dim 64; 53.3, 52.0, 52.1 for 64 up to 8192 with 16 heads
+// (with weights of one term).
 constexpr int kRowUnits = 2;
 // Units of a CTA at least, on average, unless it has a row to itself: joining is cheap
 // (one sequence of 8192: 13.1 us with 4, 12.4 with 2).
@@ -989,7 +991,8 @@ extern "C" moe_status wd_kv4_attend(const wd_kv4_cache* c, const void* q, int32_
   const bool bf16 = type == WD_BF16, wide = tile_heads(c, group) == 16;
   // <dim, head tiles, warps, ring stages, CTAs per SM>. 16 heads of dim 128 take 168 registers: 2 x 6
   // warps 63.8 us, 1 x 12 warps 67.3 (their barriers hold each other up); a fourth ring stage leaves room
-  // for one CTA only, 74 us against 52. Dim 256: 2 x 4 warps 52.8 us, 1 x 8 warps 54.0.
+  // for one CTA only, 74 us against 52. Dim 256: 2 x 4 warps 52.8 us, 1 x 8 warps 54.0. (All with
+  // weights of one term.)
   if (c->dim == 64) return wide ? launch<64, 2, 8, 4, 2>(a, plan, bf16, st) : launch<64, 1, 8, 4, 2>(a, plan, bf16, st);
   if (c->dim == 128) return wide ? launch<128, 2, 6, 3, 2>(a, plan, bf16, st) : launch<128, 1, 8, 3, 2>(a, plan, bf16, st);
   return launch<256, 1, 4, 2, 2>(a, plan, bf16, st);

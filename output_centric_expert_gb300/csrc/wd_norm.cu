@@ -9,9 +9,9 @@
 // Loads of different arrays must not wait for one another (a token's latency is
 // one trip to memory, not four): they are issued as raw words under a branch on
 // the type, and converted after.
-//   Bound by DRAM for many rows: 8192 tokens of 4096 BF16 channels (268 MB) 43.1 us,
-// 6.2 TB/s, 92 % of a copy (47.4 with a division in each sum's use); one token 2.8 us, a
-// launch and one trip to memory. A width of 7167 goes channel by channel: 33 tokens 4.9
+//   Bound by DRAM for many rows: 8192 tokens of 4096 BF16 channels (268 MB) 42.9 us,
+// 6.3 TB/s, 92 % of a copy (47.4 with a division in each sum's use); one token 2.7 us, a
+// launch and one trip to memory. A width of 7167 goes channel by channel: 33 tokens 4.8
 // us, most of it that trip and two sums; 4000 tokens 88 us, 2.6 TB/s: instructions, of
 // one row per SM at a time. (Rows ahead through shared memory at their own alignment, or
 // in registers: 2 to 5 % less for it, 8 to 20 % more for narrower ones.)
