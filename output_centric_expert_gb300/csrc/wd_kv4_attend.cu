@@ -15,7 +15,7 @@
 //   the second what the rounding of the first left: 16 bits, and FP32's range of
 //   exponents. So it is off by 2^-17 of itself whatever the other keys hold, and the row
 //   sum l (of the unrounded p) matches the weights. (f16 weights, one term of 11 bits with
-//   5 of exponent, took 27.9 and 50.3 us where these take 32.0 and 62.5, but outputs were
+//   5 of exponent, took 27.9 and 50.3 us where these take 31.5 and 61.0, but outputs were
 //   off by 2^-12 of their terms, and keys with small p or small scales beside a large one
 //   were lost.)
 //
@@ -29,9 +29,9 @@
 // order. (Joining in the last CTA to finish, by a counter, took 11 us of 42 for 76
 // parts of one row: one SM reads them all.)
 //
-// Bound. 64 sequences of up to 8192 keys with 16 heads per KV head (119 MB): 62.5 us,
-// 1.9 TB/s; one of 131071 with 8 heads (71 MB): 32.0 us, 2.2 TB/s. Decoding, scaling and
-// the softmax are about 1170 instructions per warp and 32 keys for 16 heads (96 of them
+// Bound. 64 sequences of up to 8192 keys with 16 heads per KV head (119 MB): 61.0 us,
+// 2.0 TB/s; one of 131071 with 8 heads (71 MB): 31.5 us, 2.3 TB/s. Decoding, scaling and
+// the softmax are about 1140 instructions per warp and 32 keys for 16 heads (96 of them
 // MMAs), issued in 45 % of the cycles: registers leave 12 to 16 warps per SM, too few to
 // hide every dependency. The first 6 us are a chain of trips to memory: lengths, block
 // table, keys.
@@ -133,14 +133,15 @@ __device__ __forceinline__ void mma_add_bf16(float (&d)[4], const uint32_t (&a)[
 
 // Eight E2M1 codes -> BF16 pairs times 2^-126, e[j] the codes of byte j (low nibble in the low half): E2M1's
 // exponent and mantissa are the lowest bits of BF16's exponent and the highest of its mantissa, and its 0.5
-// becomes the subnormal 2^-127, which the MMA takes as it is.
+// becomes the subnormal 2^-127, which the MMA takes as it is. A selector from 8 on repeats a byte's top bit,
+// here the code's sign, which so comes to the half's top.
 __device__ __forceinline__ void e2m1x8_to_bf16(uint32_t w, uint32_t (&e)[4]) {
-  const uint32_t lo = w & 0x0F0F0F0Fu, hi = (w >> 4) & 0x0F0F0F0Fu;
+  const uint32_t up = w << 4;
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
-    uint32_t two;  // the codes of byte j in the halves: a selector from 8 on repeats a byte's top bit, 0 here
-    asm("prmt.b32 %0, %1, %2, %3;" : "=r"(two) : "r"(lo), "r"(hi), "r"(0xC480 + 0x1111 * j));
-    e[j] = two * 0x1040u & 0x81C081C0u;
+    uint32_t two;  // the codes in bits 7 .. 4 of the halves, their signs in 15 .. 8
+    asm("prmt.b32 %0, %1, %2, %3;" : "=r"(two) : "r"(up), "r"(w), "r"(0xC480 + 0x1111 * j));
+    e[j] = two << 2 & 0x81C081C0u;
   }
 }
 
