@@ -370,7 +370,7 @@ def exact(case, seed):
     for held, new in zip(s["held"], s["news"]):
         k, v = (_nearest(s[x][key : key + held]) for x in "kv")
         key += held
-        step = max(1, (1 << 27) // (heads * group * held))
+        step = max(1, (1 << 27) // (heads * group * max(1, held)))
         for first in range(0, new, step):
             n = min(step, new - first)
             pos = torch.arange(held - new + first, held - new + first + n, device="cuda")
