@@ -1,8 +1,8 @@
 /*
  * warp_decode_block.h -- C ABI of the operators around the MoE layer in a
  * decoder block: dense projections with 4-bit weights, a paged KV cache held
- * in 4 bits with the attention that reads it, and the norms that join a block
- * to the residual stream. Same library, statuses and conventions as
+ * in 4 bits with the attentions that read it, rotary positions, and the norms
+ * that join a block to the residual stream. Same library, statuses and conventions as
  * warp_decode.h: the caller owns every device buffer, nothing is allocated or
  * synchronised, work is enqueued on `stream`, what the host can see wrong
  * launches nothing, and moe_last_error() says why.
@@ -166,6 +166,88 @@ moe_status wd_kv4_attend(const wd_kv4_cache* cache, const void* q, int32_t type,
                          int32_t window, void* out, int64_t ldo, float* lse, void* workspace,
                          size_t workspace_bytes, int32_t* err_flag, void* stream);
 
+/*
+ * wd_kv4_attend_chunk -- attention of several new tokens per sequence over the
+ * cache, which holds them already: prompts, chunks of prompts, drafts to verify.
+ * T, block_table, seq_lens, cu_new and S are wd_kv4_append's: row cu_new[s] + i of q
+ * is at position p = seq_lens[s] + i (seq_lens without the new tokens) and attends to
+ *   z_j = scale * q . k_j  for the keys j in [max(0, p + 1 - window), p]
+ *   out = sum_j softmax(z)_j v_j,  lse = log sum_j exp(z_j)
+ * with window 0 for all keys up to p. q [T][q_heads][dim] BF16 or F16 (token stride
+ * ldq, a multiple of 8, 16-byte aligned), q_heads a multiple of the cache's heads:
+ * query head h reads KV head h / (q_heads / heads). out [T][q_heads][dim] of q's type
+ * (token stride ldo, a multiple of 8, 16-byte aligned); lse [T][q_heads] F32 or NULL.
+ * Rows of q that belong to no sequence (in front of cu_new[0], from cu_new[S] on) are
+ * ignored: their out and lse are not written. A row that sees no key (a negative
+ * length, none of its pages valid) gets out = 0 and lse = -inf. A key that a row does
+ * not see has no influence on it, NaN and infinities included. Results are the same on
+ * every call with the same inputs.
+ * Logits, softmax statistics and sums are FP32, q is used exactly; a probability has
+ * 16 bits and FP32's range of exponents. Keys and values of up to 2^100 in magnitude
+ * do not overflow a sum on the way.
+ * workspace: wd_kv4_attend_chunk_workspace bytes for T tokens or more, 16-byte aligned;
+ * its contents do not matter before or after a call. Calls that may overlap need one
+ * each. max_blocks * page_size < 2^31 - 2^16, T * q_heads < 2^31 - 2^16.
+ */
+size_t wd_kv4_attend_chunk_workspace(const wd_kv4_cache* cache, int32_t T, int32_t q_heads);
+moe_status wd_kv4_attend_chunk(const wd_kv4_cache* cache, const void* q, int32_t type,
+                               int64_t ldq, int32_t T, int32_t q_heads,
+                               const int32_t* block_table, int32_t max_blocks,
+                               const int32_t* seq_lens, const int32_t* cu_new, int32_t S,
+                               float scale, int32_t window, void* out, int64_t ldo, float* lse,
+                               void* workspace, size_t workspace_bytes, int32_t* err_flag,
+                               void* stream);
+
+/* ---------------------------------------------------- rotary positions -- */
+
+/* How heads turn with their tokens' positions. rot_dim elements of a head (its
+ * first; a multiple of 16) form rot_dim / 2 pairs: pair i is elements i and
+ * i + rot_dim / 2, or, where neighbours is not 0, 2i and 2i + 1. At position p it
+ * turns by the angle p * f_i and is multiplied by magnitude (at most 65536):
+ *   a' = magnitude (a cos - b sin),   b' = magnitude (b cos + a sin)
+ * turns [rot_dim/2] (device memory, 8 bytes aligned): f_i as turns per position
+ * times 2^64, modulo whole turns, written on the host by wd_rope_turns. */
+typedef struct {
+  int32_t rot_dim, neighbours;
+  double magnitude;
+  const uint64_t* turns;
+} wd_rotation;
+
+/* The n frequencies (radians per position, at most 65536 in magnitude) as a
+ * rotation keeps them; both arrays in host memory. */
+moe_status wd_rope_turns(int32_t n, const double* freqs, uint64_t* turns);
+
+/*
+ * wd_rope -- turn the heads of x [T][heads][dim] (F32, BF16 or F16; dim a
+ * multiple of 8 up to 1024) by positions [T] int32 into out. Negative positions
+ * turn back. Elements behind rot_dim are copied. out may be x (with the same
+ * stride); token strides ldx and ldo a multiple of 16 bytes, as the addresses.
+ * Angles are exact to 2^-25 whatever the position; the rest is FP32, rounded once:
+ * off by 6 * 2^-24 (|a| + |b|) magnitude before that rounding.
+ */
+moe_status wd_rope(const wd_rotation* rotation, const void* x, int32_t type, int64_t ldx,
+                   int32_t T, int32_t heads, int32_t dim, const int32_t* positions, void* out,
+                   int64_t ldo, void* stream);
+
+/*
+ * wd_kv4_rope_append -- wd_kv4_append with the rotation on its way: k turned by
+ * its tokens' positions (seq_lens[s] + the token's number among the new ones) and
+ * quantised, v quantised, q [T][q_heads][dim] turned into q_out (which may be q
+ * with the same stride; type and strides as k's; q_heads 0: no queries).
+ * The cache holds the nearest MXFP4 to the exact turned key, not to one rounded to
+ * the input's type before (for blocks whose largest input is 2^-100 or more; FP32's
+ * infinity, which a turn of the largest finite BF16 can reach, makes a block NaN).
+ * What wd_kv4_append leaves out is left out here; a query without a place in the
+ * cache is turned all the same, one that is ignored or whose sequence has a
+ * negative length is not written.
+ */
+moe_status wd_kv4_rope_append(const wd_kv4_cache* cache, const wd_rotation* rotation,
+                              const void* q, int64_t ldq, int32_t q_heads, void* q_out,
+                              int64_t ldqo, const void* k, const void* v, int32_t type,
+                              int64_t ldk, int64_t ldv, int32_t T, const int32_t* block_table,
+                              int32_t max_blocks, const int32_t* seq_lens,
+                              const int32_t* cu_new, int32_t S, int32_t* err_flag, void* stream);
+
 /* --------------------------------------------------------- block norms -- */
 
 /*
@@ -200,7 +282,10 @@ enum {
   WD_CALL_KV4_APPEND = 1,
   WD_CALL_KV4_GATHER = 2,
   WD_CALL_KV4_ATTEND = 3,
-  WD_CALL_BLOCK_NORM = 4
+  WD_CALL_BLOCK_NORM = 4,
+  WD_CALL_ROPE = 8, /* (5 to 7 are none) */
+  WD_CALL_KV4_ROPE_APPEND = 9,
+  WD_CALL_KV4_ATTEND_CHUNK = 10
 };
 moe_status wd_call(int32_t which, const void* args);
 

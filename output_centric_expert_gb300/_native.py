@@ -59,7 +59,7 @@ def _stale(target: str, sources: list[str]) -> bool:
 def _cuda_sources() -> list[str]:
     names = ["warp_decode.cu", "wd_gate_up.cu", "wd_gate_up_fixed.cu", "wd_gate_up_grouped.cu",
              "wd_down.cu", "wd_down_grouped.cu", "wd_fp4.cu", "wd_fp4_tc.cu", "wd_kv4.cu", "wd_kv4_attend.cu",
-             "wd_norm.cu", "wd_call.cu", "pack.cpp"]
+             "wd_kv4_chunk.cu", "wd_norm.cu", "wd_rope.cu", "wd_call.cu", "pack.cpp"]
     return [os.path.join(CSRC, n) for n in names]
 
 

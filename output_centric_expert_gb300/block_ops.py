@@ -9,12 +9,15 @@ row stride the entry point takes; their last axis is dense.
 
 * ``Fp4Weights``, ``wd_fp4_matvec`` -- projections with MXFP4 weights
 * ``Kv4Cache``, ``wd_kv4_append``, ``wd_kv4_gather``, ``wd_kv4_attend`` -- a paged
-  KV cache held in MXFP4
+  KV cache held in MXFP4; ``wd_kv4_attend_chunk`` for several new tokens per sequence
+* ``rope_freqs``, ``Rope``, ``wd_rope``, ``wd_kv4_rope_append`` -- rotary positions,
+  by themselves and on the way into the cache
 * ``wd_block_norm`` -- the norms, gate and residual between two blocks
 """
 from __future__ import annotations
 
 import ctypes
+import math
 from struct import Struct
 
 import torch
@@ -23,7 +26,8 @@ from . import ops
 from .ops import WarpDecodeError
 
 __all__ = ["Fp4Weights", "Kv4Cache", "kv4_workspace", "wd_fp4_matvec", "wd_kv4_append", "wd_kv4_gather",
-           "wd_kv4_attend", "wd_block_norm", "exported_symbols"]
+           "wd_kv4_attend", "kv4_chunk_workspace", "wd_kv4_attend_chunk", "rope_freqs", "Rope", "wd_rope",
+           "wd_kv4_rope_append", "wd_block_norm", "exported_symbols"]
 
 _TYPES = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
 _raw_stream = torch._C._cuda_getCurrentRawStream  # torch.cuda.current_stream() without its Python object
@@ -39,14 +43,23 @@ class Kv4Struct(ctypes.Structure):
                 ("v_codes", ctypes.c_void_p), ("v_scales", ctypes.c_void_p)]
 
 
+class RotationStruct(ctypes.Structure):
+    _fields_ = [("rot_dim", ctypes.c_int32), ("neighbours", ctypes.c_int32), ("magnitude", ctypes.c_double),
+                ("turns", ctypes.c_void_p)]
+
+
 _lib_cache = None  # the entry points read it directly: a call's marshalling is a few us, as long as a small kernel
 
 # wd_call: number and arguments of the entry points of a decode step (q: integers and pointers, d: floats)
 _MATVEC, _APPEND, _GATHER, _ATTEND, _NORM = range(5)
+_ROPE, _ROPE_APPEND, _CHUNK = 8, 9, 10
 _matvec_args = Struct("11q").pack
 _token_args = Struct("14q").pack
 _attend_args = Struct("9qd8q").pack
 _norm_args = Struct("14q2d6q").pack
+_rope_args = Struct("11q").pack
+_rope_append_args = Struct("20q").pack
+_chunk_args = Struct("11qd8q").pack
 
 
 def lib() -> ctypes.CDLL:
@@ -56,7 +69,7 @@ def lib() -> ctypes.CDLL:
         L = ops.lib()
         vp, i32, i64, f32, sz = (ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_float,
                                  ctypes.c_size_t)
-        fp, kp = ctypes.POINTER(Fp4Shape), ctypes.POINTER(Kv4Struct)
+        fp, kp, rp = ctypes.POINTER(Fp4Shape), ctypes.POINTER(Kv4Struct), ctypes.POINTER(RotationStruct)
         L.wd_fp4_packed_bytes.restype = sz
         L.wd_fp4_packed_bytes.argtypes = [fp, ctypes.c_int]
         L.wd_kv4_cache_bytes.restype = sz
@@ -65,6 +78,8 @@ def lib() -> ctypes.CDLL:
         L.wd_kv4_attend_workspace.argtypes = [kp, i32, i32]
         L.wd_kv4_attend_ctas.restype = i32
         L.wd_kv4_attend_ctas.argtypes = [kp, i32, i32, i32, i32]
+        L.wd_kv4_attend_chunk_workspace.restype = sz
+        L.wd_kv4_attend_chunk_workspace.argtypes = [kp, i32, i32]
         tokens = [kp, vp, vp, i32, i64, i64, i32, vp, i32, vp, vp, i32, vp, vp]
         for name, args in (
                 ("wd_fp4_pack_codes", [fp, vp, vp, vp, vp, vp]),
@@ -72,6 +87,11 @@ def lib() -> ctypes.CDLL:
                 ("wd_fp4_matvec", [fp, vp, vp, vp, i32, i64, i32, vp, i32, i64, vp]),
                 ("wd_kv4_append", tokens), ("wd_kv4_gather", tokens),
                 ("wd_kv4_attend", [kp, vp, i32, i64, i32, i32, vp, i32, vp, f32, i32, vp, i64, vp, vp, sz, vp, vp]),
+                ("wd_kv4_attend_chunk", [kp, vp, i32, i64, i32, i32, vp, i32, vp, vp, i32, f32, i32, vp, i64, vp, vp, sz,
+                                         vp, vp]),
+                ("wd_rope_turns", [i32, vp, vp]),
+                ("wd_rope", [rp, vp, i32, i64, i32, i32, i32, vp, vp, i64, vp]),
+                ("wd_kv4_rope_append", [kp, rp, vp, i64, i32, vp, i64, *tokens[1:]]),
                 ("wd_block_norm", [i32, i32, vp, i32, i64, vp, i32, i64, vp, vp, vp, i32, i64, i32, f32, f32, vp,
                                    i64, vp, i32, i64, vp])):
             fn = getattr(L, name)
@@ -87,7 +107,8 @@ def exported_symbols() -> list[str]:
     """The entry points include/warp_decode_block.h declares."""
     return ["wd_fp4_packed_bytes", "wd_fp4_pack_codes", "wd_fp4_pack_weights", "wd_fp4_matvec",
             "wd_kv4_cache_bytes", "wd_kv4_append", "wd_kv4_gather", "wd_kv4_attend_workspace",
-            "wd_kv4_attend_ctas", "wd_kv4_attend", "wd_block_norm", "wd_call"]
+            "wd_kv4_attend_ctas", "wd_kv4_attend", "wd_kv4_attend_chunk_workspace", "wd_kv4_attend_chunk",
+            "wd_rope_turns", "wd_rope", "wd_kv4_rope_append", "wd_block_norm", "wd_call"]
 
 
 def _check(fn: str, status: int) -> None:
@@ -334,6 +355,149 @@ def wd_kv4_attend(cache: Kv4Cache, q: torch.Tensor, block_table: torch.Tensor, s
     if status:
         _check("wd_kv4_attend", status)
     return out
+
+
+def kv4_chunk_workspace(cache: Kv4Cache, T: int, q_heads: int) -> torch.Tensor:
+    """A workspace for wd_kv4_attend_chunk with this cache's sizes and up to T tokens: reusable, one per overlapping call."""
+    n = int(lib().wd_kv4_attend_chunk_workspace(cache._ref, T, q_heads))
+    if not n:
+        raise ValueError(f"kv4_chunk_workspace: T {T} or q_heads {q_heads} (a multiple of {cache.heads}) is unsupported")
+    return torch.empty(n, dtype=torch.uint8, device=cache.tensors[0].device)
+
+
+def wd_kv4_attend_chunk(cache: Kv4Cache, q: torch.Tensor, block_table: torch.Tensor, seq_lens: torch.Tensor,
+                        out: torch.Tensor, workspace: torch.Tensor, cu_new: torch.Tensor | None = None,
+                        lse: torch.Tensor | None = None, scale: float | None = None, window: int = 0,
+                        err_flag: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """out[T, q_heads, dim]: attention of the new tokens q over the cache, which holds them already. block_table, seq_lens
+    (without the new tokens) and cu_new are wd_kv4_append's. A token attends to itself and what is before it (to the last
+    `window` of these, 0 for all); lse [T, q_heads] float32. scale: 1 / sqrt(dim) by default."""
+    T, q_heads, S = q.shape[0], q.shape[1], seq_lens.shape[0]
+    if out.dtype != q.dtype:
+        raise TypeError(f"out: dtype {out.dtype} differs from q's {q.dtype}")
+    if lse is not None and (lse.dtype != torch.float32 or lse.shape != (T, q_heads) or not lse.is_contiguous()):
+        raise ValueError(f"lse: expected contiguous float32 {(T, q_heads)}, got {lse.dtype} {tuple(lse.shape)}")
+    if not (cache._on_gpu and out.is_cuda and workspace.is_cuda and (lse is None or lse.is_cuda)):
+        _elsewhere("cache, out, workspace or lse")
+    if not workspace.is_contiguous():
+        raise ValueError("workspace: must be contiguous")
+    D, blocks = cache.dim, block_table.shape[-1]
+    shape, row = (T, q_heads, D), q_heads * D
+    status = _lib_cache.wd_call(_CHUNK, _chunk_args(
+        cache._at, q.data_ptr(), _type(q, "q"), _rows(q, shape, row, "q"), T, q_heads,
+        _ints(block_table, (S, blocks), "block_table"), blocks, _ints(seq_lens, (S,), "seq_lens"),
+        0 if cu_new is None else _ints(cu_new, (S + 1,), "cu_new"), S,
+        D ** -0.5 if scale is None else scale, window, out.data_ptr(), _rows(out, shape, row, "out"),
+        0 if lse is None else lse.data_ptr(), workspace.data_ptr(), workspace.nbytes,
+        0 if err_flag is None else _flag(err_flag), _stream(stream, q)))
+    if status:
+        _check("wd_kv4_attend_chunk", status)
+    return out
+
+
+# ----------------------------------------------------------- rotary positions --
+
+def rope_freqs(rot_dim: int, base: float = 10000.0, scaling: str | None = None, factor: float = 1.0,
+               trained: int | None = None, slow: float = 1.0, fast: float = 32.0) -> torch.Tensor:
+    """Radians per position of the rot_dim / 2 pairs: base ** (-2 i / rot_dim), float64 on the CPU. For contexts `factor`
+    times as long as those trained on, `scaling` is
+
+    * "linear": every frequency divided by factor (positions interpolated);
+    * "base": a larger base, base * factor ** (rot_dim / (rot_dim - 2)): the slowest pair is divided by factor, the fastest stays;
+    * "parts": by a pair's turns over the `trained` positions: below `slow` divided by factor, above `fast` left, mixed between.
+      Queries and keys are then often multiplied by 0.1 ln(factor) + 1 each (`magnitude` of a Rope).
+    """
+    if rot_dim < 2 or rot_dim % 2 or not base > 0 or not factor > 0:
+        raise ValueError(f"rope_freqs: rot_dim {rot_dim}, base {base} or factor {factor} is unsupported")
+    i = torch.arange(0, rot_dim, 2, dtype=torch.float64) / rot_dim
+    if scaling == "base":
+        if rot_dim == 2:
+            raise ValueError("rope_freqs: a single pair has no other base")
+        base *= factor ** (rot_dim / (rot_dim - 2))
+    f = base ** -i
+    if scaling == "linear":
+        return f / factor
+    if scaling == "parts":
+        if not trained or trained < 1 or not fast > slow:
+            raise ValueError("rope_freqs: parts need the trained length, and fast above slow")
+        keep = ((trained * f / (2 * math.pi) - slow) / (fast - slow)).clamp(0, 1)
+        return f * (keep + (1 - keep) / factor)
+    if scaling not in (None, "base"):
+        raise ValueError(f"rope_freqs: scaling {scaling!r} is not 'linear', 'base' or 'parts'")
+    return f
+
+
+class Rope:
+    """A model's rotary positions: pair i of a head's first 2 * len(freqs) elements turns by freqs[i] radians per position
+    and is multiplied by magnitude. The pairs are elements i and i + len(freqs), or, `interleaved`, 2 i and 2 i + 1.
+    len(freqs) is a multiple of 8. Made once: it reads freqs (float32 or float64, as rope_freqs makes them) on the host."""
+
+    def __init__(self, freqs: torch.Tensor, interleaved: bool = False, magnitude: float = 1.0, device=None):
+        if freqs.dim() != 1 or freqs.dtype not in (torch.float32, torch.float64):
+            raise ValueError(f"freqs: expected float32 or float64 [pairs], got {freqs.dtype} {tuple(freqs.shape)}")
+        n = freqs.shape[0]
+        if n == 0 or n % 8:
+            raise ValueError(f"freqs: {n} pairs, not a multiple of 8")
+        host = freqs.detach().to(device="cpu", dtype=torch.float64).contiguous()
+        turns = torch.empty(n, dtype=torch.int64)
+        _check("wd_rope_turns", lib().wd_rope_turns(n, host.data_ptr(), turns.data_ptr()))
+        if device is None:
+            device = freqs.device if freqs.is_cuda else "cuda"
+        self.rot_dim, self.interleaved, self.magnitude = 2 * n, bool(interleaved), float(magnitude)
+        self._turns = turns.to(device)
+        self.struct = RotationStruct(2 * n, int(self.interleaved), self.magnitude, self._turns.data_ptr())
+        self._at = ctypes.addressof(self.struct)
+        self._on_gpu = self._turns.is_cuda
+
+    @property
+    def turns(self) -> torch.Tensor:
+        """The frequencies in turns per position times 2^64, as int64. Read-only: the kernels are given its address."""
+        return self._turns
+
+
+def wd_rope(rope: Rope, x: torch.Tensor, positions: torch.Tensor, out: torch.Tensor | None = None,
+            stream=None) -> torch.Tensor:
+    """x [T, heads, dim] (float32, bfloat16 or float16) turned by positions [T] int32 into out (by default x itself).
+    Negative positions turn back."""
+    out = x if out is None else out
+    if out.dtype != x.dtype:
+        raise TypeError(f"out: dtype {out.dtype} differs from x's {x.dtype}")
+    if not (rope._on_gpu and out.is_cuda):
+        _elsewhere("rope or out")
+    T, heads, dim = shape = x.shape
+    row = heads * dim
+    status = _lib_cache.wd_call(_ROPE, _rope_args(
+        rope._at, x.data_ptr(), _type(x, "x"), _rows(x, shape, row, "x"), T, heads, dim,
+        _ints(positions, (T,), "positions"), out.data_ptr(), _rows(out, shape, row, "out"), _stream(stream, x)))
+    if status:
+        _check("wd_rope", status)
+    return out
+
+
+def wd_kv4_rope_append(cache: Kv4Cache, rope: Rope, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
+                       block_table: torch.Tensor, seq_lens: torch.Tensor, q_out: torch.Tensor | None = None,
+                       cu_new: torch.Tensor | None = None, err_flag: torch.Tensor | None = None,
+                       stream=None) -> torch.Tensor:
+    """wd_kv4_append of k turned by its tokens' positions (seq_lens[s] and on) and of v, and q [T, q_heads, dim] turned
+    into q_out (by default q itself), which is returned."""
+    q_out = q if q_out is None else q_out
+    T, S, blocks, q_heads = k.shape[0], seq_lens.shape[0], block_table.shape[-1], q.shape[1]
+    if not v.dtype == q.dtype == q_out.dtype == k.dtype:
+        raise TypeError(f"q, q_out, k and v must have one dtype, got {q.dtype}, {q_out.dtype}, {k.dtype} and {v.dtype}")
+    if not (cache._on_gpu and rope._on_gpu and v.is_cuda and q.is_cuda and q_out.is_cuda):
+        _elsewhere("cache, rope, q, q_out or v")
+    D = cache.dim
+    row, q_row = cache.heads * D, q_heads * D
+    shape, q_shape = (T, cache.heads, D), (T, q_heads, D)
+    status = _lib_cache.wd_call(_ROPE_APPEND, _rope_append_args(
+        cache._at, rope._at, q.data_ptr(), _rows(q, q_shape, q_row, "q"), q_heads, q_out.data_ptr(),
+        _rows(q_out, q_shape, q_row, "q_out"), k.data_ptr(), v.data_ptr(), _type(k, "k"), _rows(k, shape, row, "k"),
+        _rows(v, shape, row, "v"), T, _ints(block_table, (S, blocks), "block_table"), blocks,
+        _ints(seq_lens, (S,), "seq_lens"), 0 if cu_new is None else _ints(cu_new, (S + 1,), "cu_new"), S,
+        0 if err_flag is None else _flag(err_flag), _stream(stream, k)))
+    if status:
+        _check("wd_kv4_rope_append", status)
+    return q_out
 
 
 # ---------------------------------------------------------------- block norms --

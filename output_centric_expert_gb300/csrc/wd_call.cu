@@ -118,6 +118,61 @@ extern "C" moe_status wd_call(int32_t which, const void* args) {
       return wd_block_norm(T, H, res, rt, ldr, y, yt, ldy, post, pre, gate, wt, gate_ld, gate_step, res_scale, eps,
                            res_out, ldro, out, ot, ldo, a.ptr<void>());
     }
+    case WD_CALL_ROPE: {
+      auto* r = a.ptr<const wd_rotation>();
+      auto* x = a.ptr<const void>();
+      const int32_t type = a.i32();
+      const int64_t ldx = a.word();
+      const int32_t T = a.i32(), heads = a.i32(), dim = a.i32();
+      auto* positions = a.ptr<const int32_t>();
+      auto* out = a.ptr<void>();
+      const int64_t ldo = a.word();
+      if (a.wide) return refused();
+      return wd_rope(r, x, type, ldx, T, heads, dim, positions, out, ldo, a.ptr<void>());
+    }
+    case WD_CALL_KV4_ROPE_APPEND: {
+      auto* c = a.ptr<const wd_kv4_cache>();
+      auto* r = a.ptr<const wd_rotation>();
+      auto* q = a.ptr<const void>();
+      const int64_t ldq = a.word();
+      const int32_t heads = a.i32();
+      auto* q_out = a.ptr<void>();
+      const int64_t ldqo = a.word();
+      auto *k = a.ptr<const void>(), *v = a.ptr<const void>();
+      const int32_t type = a.i32();
+      const int64_t ldk = a.word(), ldv = a.word();
+      const int32_t T = a.i32();
+      auto* table = a.ptr<const int32_t>();
+      const int32_t blocks = a.i32();
+      auto *lens = a.ptr<const int32_t>(), *cu = a.ptr<const int32_t>();
+      const int32_t S = a.i32();
+      auto* err = a.ptr<int32_t>();
+      if (a.wide) return refused();
+      return wd_kv4_rope_append(c, r, q, ldq, heads, q_out, ldqo, k, v, type, ldk, ldv, T, table, blocks, lens, cu, S, err,
+                                a.ptr<void>());
+    }
+    case WD_CALL_KV4_ATTEND_CHUNK: {
+      auto* c = a.ptr<const wd_kv4_cache>();
+      auto* q = a.ptr<const void>();
+      const int32_t type = a.i32();
+      const int64_t ldq = a.word();
+      const int32_t T = a.i32(), heads = a.i32();
+      auto* table = a.ptr<const int32_t>();
+      const int32_t blocks = a.i32();
+      auto *lens = a.ptr<const int32_t>(), *cu = a.ptr<const int32_t>();
+      const int32_t S = a.i32();
+      const float scale = a.f32();
+      const int32_t window = a.i32();
+      auto* out = a.ptr<void>();
+      const int64_t ldo = a.word();
+      auto* lse = a.ptr<float>();
+      auto* work = a.ptr<void>();
+      const size_t bytes = (size_t)a.word();
+      auto* err = a.ptr<int32_t>();
+      if (a.wide) return refused();
+      return wd_kv4_attend_chunk(c, q, type, ldq, T, heads, table, blocks, lens, cu, S, scale, window, out, ldo, lse, work,
+                                 bytes, err, a.ptr<void>());
+    }
   }
   return wd::refuse(MOE_ERR_UNSUPPORTED, "wd_call: no such entry point");
 }

@@ -1,6 +1,5 @@
 // The KV cache held in 4 bits (MXFP4): appending tokens and reading them back.
-#include "wd_block.cuh"
-#include "wd_kv4.cuh"
+#include "wd_kv4_tokens.cuh"
 
 namespace wd {
 namespace {
@@ -17,111 +16,6 @@ namespace {
 // the cache and back (100 MB): 23.5 us, 4.3 TB/s, half of it places, first loads and the
 // two launches; 262k tokens of 4 heads into it 98 us, DRAM 70 %, ALU 64 %. One token each
 // of 64 sequences: 3.6 us a launch.
-
-struct TokenArgs {
-  const int32_t *table, *lens, *cu;
-  int32_t* err;
-  int64_t ldk, ldv;
-  int32_t T, S, max_blocks;
-  int32_t pages, page_shift, heads;
-  int32_t per, chunk;  // tokens of a CTA, pieces of a token in a CTA
-};
-
-// The place of a new token; `before`, `behind`: the tokens next to it are new ones of
-// its sequence too. page -1: ignored (behind cu[S]) or left out (flagged).
-struct Place {
-  int32_t page, slot;
-  bool before, behind;
-};
-// A new token with an even slot and the next one where that is new too (`both`), or one
-// with an odd slot whose neighbour is none of its sequence's new ones: what shares bytes of V. j: the first's.
-struct Pair {
-  int32_t page, slot, j;
-  bool both;
-};
-constexpr int kMostPer = 64;
-constexpr int kResident = 5;  // CTAs of an SM: a pair's four loads in flight take 48 registers
-
-__device__ __forceinline__ Place place_of(const TokenArgs& a, int tok, bool here) {
-  Place p = {-1, 0, false, false};
-  int s = tok, first = tok, end = tok + 1;
-  if (!here || tok >= a.T) return p;
-  if (a.cu) {
-    if (tok >= __ldg(a.cu + a.S) || tok < __ldg(a.cu)) return p;
-    int lo = 0, hi = a.S - 1;  // the last s with cu[s] <= tok
-    while (lo < hi) {
-      const int mid = (lo + hi + 1) >> 1;
-      if (__ldg(a.cu + mid) <= tok)
-        lo = mid;
-      else
-        hi = mid - 1;
-    }
-    s = lo;
-    first = __ldg(a.cu + s);
-    end = min(__ldg(a.cu + s + 1), a.T);
-  }
-  p.before = tok > first;
-  p.behind = tok + 1 < end;
-  const int len = __ldg(a.lens + s);
-  const int64_t pos = (int64_t)len + (tok - first);
-  const int64_t block = pos >> a.page_shift;
-  if (len >= 0 && block < a.max_blocks) p.page = __ldg(a.table + (int64_t)s * a.max_blocks + block);
-  p.slot = (int)(pos & ((1 << a.page_shift) - 1));
-  if (p.page < 0 || p.page >= a.pages) {
-    p.page = -1;
-    flag_invalid(a.err);
-  }
-  return p;
-}
-
-// The pairs that begin in a CTA's tokens, in order; returns their number. All threads.
-__device__ __forceinline__ int find_pairs(const TokenArgs& a, int tok0, Pair* s_pair) {
-  __shared__ uint32_t s_first[kMostPer / 32];
-  const int tid = threadIdx.x;
-  Place p;
-  uint32_t first = 0;
-  if (tid < kMostPer) {  // whole warps
-    p = place_of(a, tok0 + tid, tid < a.per);
-    first = __ballot_sync(0xFFFFFFFFu, p.page >= 0 && !((p.slot & 1) && p.before));
-    if ((tid & 31) == 0) s_first[tid >> 5] = first;
-  }
-  __syncthreads();
-  int pairs = 0;
-#pragma unroll
-  for (int n = 0; n < kMostPer / 32; ++n) pairs += __popc(s_first[n]);
-  if (tid < kMostPer && (first >> (tid & 31)) & 1u) {
-    int at = __popc(first & ((1u << (tid & 31)) - 1u));
-#pragma unroll
-    for (int n = 0; n < kMostPer / 32; ++n) at += n < tid >> 5 ? __popc(s_first[n]) : 0;
-    s_pair[at] = {p.page, p.slot, tid, !(p.slot & 1) && p.behind};
-  }
-  __syncthreads();
-  return pairs;
-}
-
-// The (pair, piece) of a thread's i-th item, i = threadIdx.x, + kThreads, ...
-struct Walk {
-  int i, j, w;
-  const int chunk, dj, dw;
-  __device__ explicit Walk(int c)
-      : i(threadIdx.x), j(threadIdx.x / c), w(threadIdx.x - threadIdx.x / c * c), chunk(c), dj(kThreads / c),
-        dw(kThreads - kThreads / c * c) {}
-  __device__ void next() {
-    i += kThreads;
-    j += dj;
-    w += dw;
-    if (w >= chunk) {
-      w -= chunk;
-      ++j;
-    }
-  }
-};
-
-// Four E2M1 codes (the low 16 bits) to the low nibbles of four bytes.
-__device__ __forceinline__ uint32_t spread4(uint32_t x) {
-  const uint32_t t = __byte_perm(x, 0, 0x4140);  // byte 0 and byte 1 to the halves
-  return (t & 0x000F000Fu) | ((t << 4) & 0x0F000F00u);
-}
 
 template <int D, bool BF16>
 __global__ void __launch_bounds__(kThreads, kResident)
@@ -260,6 +154,43 @@ __global__ void __launch_bounds__(kThreads)
   }
 }
 
+// The grid: runs of tokens, and pieces of a token in chunks of whole heads.
+dim3 token_grid(const TokenArgs& a, int words) {
+  return dim3((unsigned)((a.T + a.per - 1) / a.per), (unsigned)(words / a.chunk));
+}
+
+template <int D>
+moe_status append(const wd_kv4_cache* c, const void* k, const void* v, int32_t type,
+                  const TokenArgs& a, cudaStream_t st) {
+  const dim3 grid = token_grid(a, a.heads * (D / 8));
+  const uint16_t *k16 = static_cast<const uint16_t*>(k), *v16 = static_cast<const uint16_t*>(v);
+  if (type == WD_BF16)
+    kv4_append_kernel<D, true><<<grid, kThreads, 0, st>>>(k16, v16, c->k_codes, c->k_scales,
+                                                             c->v_codes, c->v_scales, a);
+  else
+    kv4_append_kernel<D, false><<<grid, kThreads, 0, st>>>(k16, v16, c->k_codes, c->k_scales,
+                                                              c->v_codes, c->v_scales, a);
+  return launched("wd_kv4_append launch");
+}
+
+template <int D>
+moe_status gather(const wd_kv4_cache* c, void* k, void* v, int32_t type, const TokenArgs& a,
+                  cudaStream_t st) {
+  const dim3 grid = token_grid(a, a.heads * (D / 8));
+  auto run = [&](auto kernel) {
+    kernel<<<grid, kThreads, 0, st>>>(k, v, c->k_codes, c->k_scales, c->v_codes, c->v_scales, a);
+  };
+  if (type == WD_F32)
+    run(kv4_gather_kernel<D, WD_F32>);
+  else if (type == WD_BF16)
+    run(kv4_gather_kernel<D, WD_BF16>);
+  else
+    run(kv4_gather_kernel<D, WD_F16>);
+  return launched("wd_kv4_gather launch");
+}
+
+}  // namespace
+
 moe_status check_tokens(const wd_kv4_cache* c, const void* k, const void* v, int32_t type,
                         int64_t ldk, int64_t ldv, int32_t T, const int32_t* table,
                         int32_t max_blocks, const int32_t* lens, const int32_t* cu, int32_t S,
@@ -301,43 +232,6 @@ TokenArgs token_args(const wd_kv4_cache* c, int64_t ldk, int64_t ldv, int32_t T,
   return {table, lens, cu, err, ldk, ldv, T, S, max_blocks, c->pages, kv4_page_shift(c->page_size),
           c->heads, per, chunk};
 }
-
-// The grid: runs of tokens, and pieces of a token in chunks of whole heads.
-dim3 token_grid(const TokenArgs& a, int words) {
-  return dim3((unsigned)((a.T + a.per - 1) / a.per), (unsigned)(words / a.chunk));
-}
-
-template <int D>
-moe_status append(const wd_kv4_cache* c, const void* k, const void* v, int32_t type,
-                  const TokenArgs& a, cudaStream_t st) {
-  const dim3 grid = token_grid(a, a.heads * (D / 8));
-  const uint16_t *k16 = static_cast<const uint16_t*>(k), *v16 = static_cast<const uint16_t*>(v);
-  if (type == WD_BF16)
-    kv4_append_kernel<D, true><<<grid, kThreads, 0, st>>>(k16, v16, c->k_codes, c->k_scales,
-                                                             c->v_codes, c->v_scales, a);
-  else
-    kv4_append_kernel<D, false><<<grid, kThreads, 0, st>>>(k16, v16, c->k_codes, c->k_scales,
-                                                              c->v_codes, c->v_scales, a);
-  return launched("wd_kv4_append launch");
-}
-
-template <int D>
-moe_status gather(const wd_kv4_cache* c, void* k, void* v, int32_t type, const TokenArgs& a,
-                  cudaStream_t st) {
-  const dim3 grid = token_grid(a, a.heads * (D / 8));
-  auto run = [&](auto kernel) {
-    kernel<<<grid, kThreads, 0, st>>>(k, v, c->k_codes, c->k_scales, c->v_codes, c->v_scales, a);
-  };
-  if (type == WD_F32)
-    run(kv4_gather_kernel<D, WD_F32>);
-  else if (type == WD_BF16)
-    run(kv4_gather_kernel<D, WD_BF16>);
-  else
-    run(kv4_gather_kernel<D, WD_F16>);
-  return launched("wd_kv4_gather launch");
-}
-
-}  // namespace
 
 int kv4_page_shift(int page_size) {
   int s = 0;

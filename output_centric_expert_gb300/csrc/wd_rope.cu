@@ -1,0 +1,537 @@
+// Rotary positions: wd_rope turns the heads of a tensor, wd_kv4_rope_append turns the
+// queries and keys of new tokens and puts keys and values into the 4-bit cache.
+//
+// Mathematics. Pair i of a head is turned by the angle pos * f_i. A frequency is kept as
+// turns per position in units of 2^-64, so the product with a position in 64-bit
+// integers is the angle less its whole turns, exactly: no position is too far. What is
+// left after the nearest quarter turn, at most an eighth either way, becomes FP32 (off by
+// 2^-25) and goes through the Taylor series of sine and cosine.
+//
+// What the cache holds is the nearest MXFP4 to the exact turned key. FP32 gives it to
+// within kDoubt of the block's largest input: codes are taken at both ends of that
+// interval, and where they differ (one block of 2000) the element is computed again in
+// 64 bits. So the codes do not depend on the order of FP32 operations.
+//
+// Work. A CTA has a run of tokens and some of their heads. It computes the angles' sines
+// and cosines once for all its heads into shared memory (planes of 16 bytes, so that
+// neighbouring pieces are neighbouring words).
+#include <algorithm>
+#include <cmath>
+
+#include "wd_kv4_tokens.cuh"
+
+namespace wd {
+namespace {
+
+constexpr float kDoubt = 9.5367431640625e-7f;  // 2^-20: 12 of FP32's 2^-24 and some more (test_rope_gpu derives them)
+
+// cos and sin of pos * turns / 2^64 turns.
+__device__ __forceinline__ float2 cos_sin(uint64_t turns, int64_t pos) {
+  const uint64_t a = turns * (uint64_t)pos;
+  const uint32_t quarter = (uint32_t)((a + (1ull << 61)) >> 62);
+  const int64_t rest = (int64_t)(a - ((uint64_t)quarter << 62));  // within 2^61
+  const float x = (float)(int32_t)(rest >> 32) * 1.46291807926715968e-9f;  // 2 pi / 2^32
+  const float y = x * x;
+  const float s = fmaf(x * y, fmaf(y, fmaf(y, fmaf(y, 1.0f / 362880, -1.0f / 5040), 1.0f / 120), -1.0f / 6), x);
+  const float c = fmaf(y, fmaf(y, fmaf(y, fmaf(y, fmaf(y, -1.0f / 3628800, 1.0f / 40320), -1.0f / 720), 1.0f / 24), -0.5f), 1.0f);
+  const float u = quarter & 1 ? s : c, v = quarter & 1 ? c : s;
+  return make_float2((quarter + 1) & 2 ? -u : u, quarter & 2 ? -v : v);
+}
+
+// The table of a CTA's tokens, [token][4 planes][rot / 16 groups] of 16 bytes: planes 0, 1 hold the cosines of a group of
+// eight pairs, 2, 3 the sines. Positions of -1 are left out. All threads, a barrier behind it.
+struct RopeArgs {
+  const uint64_t* turns;
+  double magnitude;
+  int32_t rot, pairs;  // pairs: rot / 2
+  int32_t neighbours;
+};
+
+template <typename F>
+__device__ __forceinline__ void make_table(const RopeArgs& r, int tokens, float* table, F position) {
+  const float mag = (float)r.magnitude;
+  const int step_j = blockDim.x / r.pairs, step_i = blockDim.x - step_j * r.pairs;
+  int j = threadIdx.x / r.pairs, i = threadIdx.x - j * r.pairs;
+  while (j < tokens) {
+    int64_t pos;
+    if (position(j, pos)) {
+      const float2 cs = cos_sin(__ldg(r.turns + i), pos);
+      float* to = table + (size_t)j * r.rot + ((i & 7) >> 2) * (r.rot / 4) + (i >> 3) * 4 + (i & 3);
+      to[0] = cs.x * mag;
+      to[r.rot / 2] = cs.y * mag;
+    }
+    i += step_i;
+    j += step_j;
+    if (i >= r.pairs) i -= r.pairs, ++j;
+  }
+  __syncthreads();
+}
+
+// Eight cosines and sines of a group.
+__device__ __forceinline__ void group_of(const float* table, int rot, int g, float (&c)[8], float (&s)[8]) {
+  const float4* t = reinterpret_cast<const float4*>(table);
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const float4 a = t[h * (rot / 16) + g], b = t[(2 + h) * (rot / 16) + g];
+    c[4 * h] = a.x, c[4 * h + 1] = a.y, c[4 * h + 2] = a.z, c[4 * h + 3] = a.w;
+    s[4 * h] = b.x, s[4 * h + 1] = b.y, s[4 * h + 2] = b.z, s[4 * h + 3] = b.w;
+  }
+}
+
+// A piece of eight elements as it lies in memory.
+template <int TYPE>
+struct Piece {
+  uint4 w[TYPE == WD_F32 ? 2 : 1];
+};
+template <int TYPE>
+__device__ __forceinline__ Piece<TYPE> load_piece(const void* p) {  // (may be written by this kernel later)
+  Piece<TYPE> v;
+#pragma unroll
+  for (int i = 0; i < (TYPE == WD_F32 ? 2 : 1); ++i) v.w[i] = reinterpret_cast<const uint4*>(p)[i];
+  return v;
+}
+template <int TYPE>
+__device__ __forceinline__ void store_piece(void* p, const Piece<TYPE>& v) {
+#pragma unroll
+  for (int i = 0; i < (TYPE == WD_F32 ? 2 : 1); ++i) reinterpret_cast<uint4*>(p)[i] = v.w[i];
+}
+template <int TYPE>
+__device__ __forceinline__ void floats_of(const Piece<TYPE>& v, float (&f)[8]) {
+  if constexpr (TYPE == WD_F32) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      f[4 * i] = __uint_as_float(v.w[i].x), f[4 * i + 1] = __uint_as_float(v.w[i].y);
+      f[4 * i + 2] = __uint_as_float(v.w[i].z), f[4 * i + 3] = __uint_as_float(v.w[i].w);
+    }
+  } else {
+    unpack8<TYPE == WD_BF16>(v.w[0], f);
+  }
+}
+template <int TYPE>
+__device__ __forceinline__ Piece<TYPE> piece_of(const float (&f)[8]) {
+  Piece<TYPE> v;
+  if constexpr (TYPE == WD_F32) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+      v.w[i] = make_uint4(__float_as_uint(f[4 * i]), __float_as_uint(f[4 * i + 1]), __float_as_uint(f[4 * i + 2]),
+                          __float_as_uint(f[4 * i + 3]));
+  } else {
+    constexpr bool B = TYPE == WD_BF16;
+    v.w[0] = make_uint4(pack2<B>(f[0], f[1]), pack2<B>(f[2], f[3]), pack2<B>(f[4], f[5]), pack2<B>(f[6], f[7]));
+  }
+  return v;
+}
+
+// Item w of a head: two pieces, both read before either is written, so that out may be x.
+// The first rot / 16 turn (the pieces w and w + rot / 16, or 2w and 2w + 1), the rest are copied where `copies`.
+template <int TYPE>
+__device__ __forceinline__ void turn_item(const RopeArgs& r, const float* table, const void* head, void* out, int w, int pieces,
+                                          bool copies) {
+  constexpr int kPieceBytes = TYPE == WD_F32 ? 32 : 16;
+  const int groups = r.rot / 16;
+  const bool turns = w < groups;
+  if (!turns && !copies) return;
+  int p = 2 * w, q = 2 * w + 1;
+  if (turns && !r.neighbours) p = w, q = w + groups;
+  const char* from = static_cast<const char*>(head);
+  char* to = static_cast<char*>(out);
+  Piece<TYPE> a = load_piece<TYPE>(from + p * kPieceBytes), b = a;
+  if (q < pieces) b = load_piece<TYPE>(from + q * kPieceBytes);
+  if (turns) {
+    float x[8], y[8], c[8], s[8];
+    floats_of<TYPE>(a, x);
+    floats_of<TYPE>(b, y);
+    group_of(table, r.rot, w, c, s);
+    if (r.neighbours) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float e = x[2 * i], o = x[2 * i + 1], e2 = y[2 * i], o2 = y[2 * i + 1];
+        x[2 * i] = fmaf(e, c[i], -(o * s[i])), x[2 * i + 1] = fmaf(o, c[i], e * s[i]);
+        y[2 * i] = fmaf(e2, c[4 + i], -(o2 * s[4 + i])), y[2 * i + 1] = fmaf(o2, c[4 + i], e2 * s[4 + i]);
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const float u = x[i], v = y[i];
+        x[i] = fmaf(u, c[i], -(v * s[i])), y[i] = fmaf(v, c[i], u * s[i]);
+      }
+    }
+    a = piece_of<TYPE>(x);
+    b = piece_of<TYPE>(y);
+  }
+  store_piece<TYPE>(to + p * kPieceBytes, a);
+  if (q < pieces) store_piece<TYPE>(to + q * kPieceBytes, b);
+}
+
+// ------------------------------------------------------------------ wd_rope --
+
+struct TurnArgs {
+  RopeArgs r;
+  const char* x;
+  char* out;
+  const int32_t* positions;
+  int64_t ldx, ldo;  // bytes
+  int32_t T, head_bytes, pieces;
+  int32_t per, heads, items, chunk;  // tokens of a CTA, heads in all, items of a head, of a token in a CTA
+  bool copies;
+};
+
+template <int TYPE>
+__global__ void __launch_bounds__(kThreads) rope_kernel(const TurnArgs a) {
+  extern __shared__ float4 dyn4[];
+  float* table = reinterpret_cast<float*>(dyn4);
+  const int tok0 = blockIdx.x * a.per, tokens = min(a.per, a.T - tok0);
+  make_table(a.r, tokens, table, [&](int j, int64_t& pos) {
+    pos = __ldg(a.positions + tok0 + j);
+    return true;
+  });
+  const int w0 = blockIdx.y * a.chunk, end = min(a.chunk, a.heads * a.items - w0);
+  for (Walk walk(a.chunk); walk.j < tokens; walk.next()) {
+    if (walk.w >= end) continue;
+    const int head = (w0 + walk.w) / a.items, w = w0 + walk.w - head * a.items;
+    const int64_t tok = tok0 + walk.j;
+    turn_item<TYPE>(a.r, table + walk.j * a.r.rot, a.x + tok * a.ldx + (int64_t)head * a.head_bytes,
+                    a.out + tok * a.ldo + (int64_t)head * a.head_bytes, w, a.pieces, a.copies);
+  }
+}
+
+// ------------------------------------------------------- wd_kv4_rope_append --
+
+struct RopeAppendArgs {
+  RopeArgs r;
+  TokenArgs t;
+  const uint16_t *q, *k, *v;
+  uint16_t* q_out;
+  uint8_t *kc, *ks, *vc, *vs;
+  int64_t ldq, ldqo;
+  int32_t kv_slices;              // of the grid's y; the rest are the queries'
+  int32_t q_heads, q_chunk;       // items of a token in a CTA
+  bool copies;
+};
+
+// The exact turned element e of a head of k, in 64 bits.
+template <bool BF16>
+__device__ double exact_element(const RopeArgs& r, const uint16_t* head, int e, int64_t pos) {
+  const double x = load_elem(head, BF16 ? WD_BF16 : WD_F16, e);
+  if (e >= r.rot) return x;
+  const int half = r.rot / 2;
+  const int other = r.neighbours ? e ^ 1 : e < half ? e + half : e - half;
+  const bool second = r.neighbours ? e & 1 : e >= half;
+  const int i = r.neighbours ? e >> 1 : second ? other : e;
+  const double y = load_elem(head, BF16 ? WD_BF16 : WD_F16, other);
+  double s, c;
+  sincospi((double)(int64_t)(r.turns[i] * (uint64_t)pos) * 0x1p-63, &s, &c);
+  return r.magnitude * (second ? x * c + y * s : x * c - y * s);
+}
+
+__device__ __forceinline__ uint32_t nearest_e2m1(double v) {
+  const double m = fabs(v);
+  return (uint32_t)((m > 0.25) + (m >= 0.75) + (m > 1.25) + (m >= 1.75) + (m > 2.5) + (m >= 3.5) + (m > 5.0)) |
+         (signbit(v) ? 8u : 0u);
+}
+
+__device__ __forceinline__ double unscale64(uint32_t s) { return __longlong_as_double((long long)(1023 + 127 - (int)s) << 52); }
+
+// The codes of a piece again, for the nibbles that `unsure` has set.
+template <bool BF16>
+__device__ __noinline__ uint32_t settle_codes(const RopeArgs& r, const uint16_t* head, int w, int64_t pos, uint32_t scale,
+                                              uint32_t codes, uint32_t unsure) {
+#pragma unroll 1
+  for (int j = 0; j < 8; ++j)
+    if (unsure >> (4 * j) & 15u) {
+      const uint32_t c = nearest_e2m1(exact_element<BF16>(r, head, 8 * w + j, pos) * unscale64(scale));
+      codes = (codes & ~(15u << (4 * j))) | c << (4 * j);
+    }
+  return codes;
+}
+
+// The scale of a block again (the four threads of `quad`).
+template <bool BF16>
+__device__ __noinline__ uint32_t settle_scale(const RopeArgs& r, const uint16_t* head, int w, int64_t pos, unsigned quad) {
+  double m = 0.0;
+#pragma unroll 1
+  for (int j = 0; j < 8; ++j) m = fmax(m, fabs(exact_element<BF16>(r, head, 8 * w + j, pos)));
+  m = fmax(m, __shfl_xor_sync(quad, m, 1));
+  m = fmax(m, __shfl_xor_sync(quad, m, 2));
+  const int e = (int)(__double_as_longlong(m) >> 52) - 1023 - 2 + 127;
+  return (uint32_t)(m == 0.0 ? 0 : max(0, min(254, e)));
+}
+
+// The largest magnitude of a piece, as FP32 bits (NaN and infinities: infinity).
+template <bool BF16>
+__device__ __forceinline__ uint32_t piece_top(const uint4& raw) {
+  const uint32_t two = __vmaxu2(__vmaxu2(raw.x & 0x7FFF7FFFu, raw.y & 0x7FFF7FFFu),
+                                __vmaxu2(raw.z & 0x7FFF7FFFu, raw.w & 0x7FFF7FFFu));
+  const uint32_t m = max(two & 0xFFFFu, two >> 16);
+  return magnitude(BF16 ? __uint_as_float(m << 16) : half_lo(m));
+}
+
+template <int D, bool BF16>
+__global__ void __launch_bounds__(kThreads) kv4_rope_append_kernel(const RopeAppendArgs a) {
+  extern __shared__ float4 dyn4[];
+  float* table = reinterpret_cast<float*>(dyn4);
+  __shared__ Pair s_pair[kMostPer];
+  __shared__ int64_t s_pos[kMostPer];
+  const TokenArgs& t = a.t;
+  const RopeArgs& r = a.r;
+  const int tok0 = blockIdx.x * t.per, tid = threadIdx.x;
+  const int pairs = find_pairs(t, tok0, s_pair, s_pos);
+  const bool queries = (int)blockIdx.y >= a.kv_slices;
+  // one token more for the keys: a pair may end behind the run
+  make_table(r, t.per + (queries ? 0 : 1), table, [&](int j, int64_t& pos) {
+    pos = j < t.per ? s_pos[j] : s_pos[j - 1] + (s_pos[j - 1] >= 0);
+    return pos >= 0;
+  });
+  if (queries) {
+    constexpr int kItems = D / 16;
+    const int w0 = ((int)blockIdx.y - a.kv_slices) * a.q_chunk, end = min(a.q_chunk, a.q_heads * kItems - w0);
+    for (Walk walk(a.q_chunk); walk.j < t.per; walk.next()) {
+      if (walk.w >= end || s_pos[walk.j] < 0) continue;
+      const int w = w0 + walk.w;
+      const int64_t tok = tok0 + walk.j, head = (int64_t)(w / kItems) * D;
+      turn_item<BF16 ? WD_BF16 : WD_F16>(r, table + walk.j * r.rot, a.q + tok * a.ldq + head, a.q_out + tok * a.ldqo + head,
+                                         w % kItems, D / 8, a.copies);
+    }
+    return;
+  }
+  const unsigned quad = 0xFu << (tid & 28);
+  auto plain = [&](const uint4& raw, uint32_t& scale) {  // of V
+    uint32_t m = piece_top<BF16>(raw);
+    m = max(m, __shfl_xor_sync(quad, m, 1));
+    m = max(m, __shfl_xor_sync(quad, m, 2));
+    float f[8];
+    unpack8<BF16>(raw, f);
+    scale = fp4_scale_code(__uint_as_float(m));
+    const float u = fp4_unscale(scale);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) f[j] *= u;
+    return e2m1x8(f);
+  };
+  const int groups = r.rot / 16;
+  // w: the piece of the head; j: the token in the run
+  auto turned = [&](const uint4& raw, const uint4& raw2, int w, int j, int64_t tok, int head, uint32_t& scale) {
+    float f[8];
+    unpack8<BF16>(raw, f);
+    uint32_t in = 0;  // the largest of what is turned
+    if (w < 2 * groups) {
+      in = piece_top<BF16>(raw);
+      const float* row = table + j * r.rot;
+      if (r.neighbours) {
+        const float4 c = reinterpret_cast<const float4*>(row)[(w & 1) * groups + (w >> 1)];
+        const float4 s = reinterpret_cast<const float4*>(row)[(2 + (w & 1)) * groups + (w >> 1)];
+        const float cs[4] = {c.x, c.y, c.z, c.w}, sn[4] = {s.x, s.y, s.z, s.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float e = f[2 * i], o = f[2 * i + 1];
+          f[2 * i] = fmaf(e, cs[i], -(o * sn[i])), f[2 * i + 1] = fmaf(o, cs[i], e * sn[i]);
+        }
+      } else {
+        in = max(in, piece_top<BF16>(raw2));
+        float y[8], c[8], s[8];
+        unpack8<BF16>(raw2, y);
+        group_of(row, r.rot, w < groups ? w : w - groups, c, s);
+        const uint32_t flip = w < groups ? 0x80000000u : 0u;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) f[i] = fmaf(f[i], c[i], __uint_as_float(__float_as_uint(y[i] * s[i]) ^ flip));
+      }
+    }
+    uint32_t m = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) m = max(m, magnitude(f[i]));
+    m = max(m, __shfl_xor_sync(quad, m, 1));
+    m = max(m, __shfl_xor_sync(quad, m, 2));
+    in = max(in, __shfl_xor_sync(quad, in, 1));
+    in = max(in, __shfl_xor_sync(quad, in, 2));
+    scale = fp4_scale_code(__uint_as_float(m));
+    if (scale == 255u) return 0u;
+    const float doubt = __uint_as_float(in) * (kDoubt * fabsf((float)r.magnitude)), top = __uint_as_float(m);
+    const uint16_t* row = a.k + tok * t.ldk + (int64_t)head * D;
+    auto pos = [&]() { return j < t.per ? s_pos[j] : s_pos[j - 1] + 1; };
+    if (fp4_scale_code(fmaxf(top - doubt, 0.0f)) != fp4_scale_code(top + doubt))
+      scale = settle_scale<BF16>(r, row, w, pos(), quad);
+    const float u = fp4_unscale(scale), d = doubt * u;
+    float g[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) g[i] = fmaf(f[i], u, -d), f[i] = fmaf(f[i], u, d);
+    const uint32_t codes = e2m1x8(f), other = e2m1x8(g);
+    return codes == other ? codes : settle_codes<BF16>(r, row, w, pos(), scale, codes, codes ^ other);
+  };
+  const int kv0 = blockIdx.y * t.chunk;
+  for (Walk walk(t.chunk); walk.j < pairs; walk.next()) {
+    const int hw = kv0 + walk.w;
+    const Pair p = s_pair[walk.j];  // the four threads of a block have the same
+    const int head = hw / (D / 8), w = hw % (D / 8), b = w >> 2, q4 = w & 3;
+    const int64_t tok = tok0 + p.j;
+    const uint16_t *kp = a.k + tok * t.ldk + hw * 8, *vp = a.v + tok * t.ldv + hw * 8;
+    const int apart = r.neighbours || w >= 2 * groups ? 0 : w < groups ? 8 * groups : -8 * groups;  // to the partners' piece
+    const uint4 raw_v = ld_cached16(vp), raw_k = ld_cached16(kp), raw_k2 = ld_cached16(kp + apart);
+    uint4 next_v, next_k, next_k2;
+    if (p.both) next_v = ld_cached16(vp + t.ldv), next_k = ld_cached16(kp + t.ldk), next_k2 = ld_cached16(kp + t.ldk + apart);
+    const size_t at = ((size_t)p.page * t.heads + head) << t.page_shift;  // in tokens
+    uint32_t sv, sk, v0 = plain(raw_v, sv), v1 = 0, sv1 = 0;
+    uint8_t* kto = a.kc + at * (D / 2) + k_word<D>(p.slot, q4, b);
+    uint8_t* ksto = a.ks + at * (D / 32) + p.slot * (D / 32) + b;
+    *reinterpret_cast<uint32_t*>(kto) = turned(raw_k, raw_k2, w, p.j, tok, head, sk);
+    if (q4 == 0) *ksto = (uint8_t)sk;
+    if (p.both) {
+      v1 = plain(next_v, sv1);
+      *reinterpret_cast<uint32_t*>(kto + D / 2) = turned(next_k, next_k2, w, p.j + 1, tok + 1, head, sk);
+      if (q4 == 0) ksto[D / 32] = (uint8_t)sk;
+    }
+    // V as in wd_kv4_append: a key alone replaces its own nibbles
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      uint32_t* to = reinterpret_cast<uint32_t*>(a.vc + at * (D / 2) + v_word<D>(p.slot >> 1, 2 * q4 + h, b));
+      const uint32_t x = spread4(v0 >> (16 * h));
+      if (p.both) {
+        *to = x | spread4(v1 >> (16 * h)) << 4;
+      } else {
+        const int up = (p.slot & 1) * 4;
+        atomicAnd(to, ~(0x0F0F0F0Fu << up));
+        atomicOr(to, x << up);
+      }
+    }
+    if (q4 == 0) {
+      uint8_t* to = a.vs + at * (D / 32) + v_scale<D>(p.slot, b);
+      if (p.both)
+        *reinterpret_cast<uint16_t*>(to) = (uint16_t)(sv | sv1 << 8);
+      else
+        *to = (uint8_t)sv;
+    }
+  }
+}
+
+// ------------------------------------------------------------------ launches --
+
+moe_status check_rotation(const wd_rotation* r, int32_t dim) {
+  if (!r) return refuse(MOE_ERR_NULL, "wd_rope: a rotation is required");
+  if (r->rot_dim < 16 || r->rot_dim % 16 || r->rot_dim > dim)
+    return refuse(MOE_ERR_SHAPE, "wd_rope: rot_dim is a multiple of 16, from 16 to the head's elements");
+  if (!(std::fabs(r->magnitude) <= 65536.0))
+    return refuse(MOE_ERR_UNSUPPORTED, "wd_rope: the magnitude is at most 65536");
+  if (!r->turns) return refuse(MOE_ERR_NULL, "wd_rope: turns are required");
+  if (!aligned(r->turns, 8)) return refuse(MOE_ERR_ALIGN, "wd_rope: turns need 8 bytes");
+  return MOE_OK;
+}
+
+RopeArgs rope_args(const wd_rotation* r) {
+  return {r->turns, r->magnitude, r->rot_dim, r->rot_dim / 2, r->neighbours ? 1 : 0};
+}
+
+// Tokens of a CTA: T tokens in `slices` slices, each run's table at most kTable bytes, in whole waves.
+constexpr int kTable = 16 * 1024;
+int tokens_of_a_cta(int64_t T, int slices, int rot, int resident, int least) {
+  const int64_t slots = (int64_t)sm_count() * resident, most = std::max(least, std::min(kMostPer - 1, kTable / (rot * 4)));
+  const int64_t waves = (T * slices + slots * most - 1) / (slots * most);
+  const int64_t even = (T * slices + slots * waves - 1) / (slots * waves);
+  return (int)std::max((int64_t)least, std::min(most, even));
+}
+
+template <int TYPE>
+moe_status turn(const TurnArgs& a, cudaStream_t st) {
+  const dim3 grid((unsigned)((a.T + (int64_t)a.per - 1) / a.per), (unsigned)((a.heads * a.items + a.chunk - 1) / a.chunk));
+  rope_kernel<TYPE><<<grid, kThreads, (size_t)a.per * a.r.rot * 4, st>>>(a);
+  return launched("wd_rope launch");
+}
+
+template <int D>
+moe_status rope_append(const RopeAppendArgs& a, bool bf16, dim3 grid, cudaStream_t st) {
+  const size_t table = (size_t)(a.t.per + 1) * a.r.rot * 4;
+  if (bf16)
+    kv4_rope_append_kernel<D, true><<<grid, kThreads, table, st>>>(a);
+  else
+    kv4_rope_append_kernel<D, false><<<grid, kThreads, table, st>>>(a);
+  return launched("wd_kv4_rope_append launch");
+}
+
+}  // namespace
+}  // namespace wd
+
+extern "C" moe_status wd_rope_turns(int32_t n, const double* freqs, uint64_t* turns) {
+  using namespace wd;
+  if (n < 0) return refuse(MOE_ERR_SHAPE, "wd_rope_turns: need n >= 0");
+  if (n && (!freqs || !turns)) return refuse(MOE_ERR_NULL, "wd_rope_turns: freqs and turns are required");
+  for (int32_t i = 0; i < n; ++i)
+    if (!(std::fabs(freqs[i]) <= 65536.0))
+      return refuse(MOE_ERR_UNSUPPORTED, "wd_rope_turns: a frequency is at most 65536 radians per position");
+  // 1 / (2 pi) as a sum of two doubles; the product's whole turns do not matter
+  const double hi = 0x1.45f306dc9c883p-3, lo = -0x1.6b01ec5417056p-57;
+  for (int32_t i = 0; i < n; ++i) {
+    const double f = std::fabs(freqs[i]), p = f * hi, rest = std::fma(f, hi, -p) + f * lo;
+    const double part = p - std::floor(p);  // exact
+    const double first = std::floor(part * 0x1p32), second = (part * 0x1p32 - first) * 0x1p32 + rest * 0x1p64;
+    const uint64_t t = ((uint64_t)first << 32) + (uint64_t)(int64_t)std::nearbyint(second);
+    turns[i] = freqs[i] < 0 ? 0 - t : t;
+  }
+  return MOE_OK;
+}
+
+extern "C" moe_status wd_rope(const wd_rotation* r, const void* x, int32_t type, int64_t ldx, int32_t T, int32_t heads,
+                              int32_t dim, const int32_t* positions, void* out, int64_t ldo, void* stream) {
+  using namespace wd;
+  if (T < 0 || heads < 0 || dim < 16 || dim % 8 || dim > 1024)
+    return refuse(MOE_ERR_SHAPE, "wd_rope: need T, heads >= 0 and dim a multiple of 8 from 16 to 1024");
+  moe_status rc = check_rotation(r, dim);
+  if (rc != MOE_OK) return rc;
+  if (!valid_type(type)) return refuse(MOE_ERR_UNSUPPORTED, "wd_rope: x and out are F32, BF16 or F16");
+  const int64_t row = (int64_t)heads * dim;
+  if (row > 1 << 20) return refuse(MOE_ERR_SHAPE, "wd_rope: a token has at most 2^20 elements");
+  if (ldx < row || ldo < row || (x == out && ldx != ldo))
+    return refuse(MOE_ERR_SHAPE, "wd_rope: ldx or ldo is shorter than a token, or they differ in place");
+  if (T == 0 || heads == 0) return MOE_OK;
+  if (!x || !positions || !out) return refuse(MOE_ERR_NULL, "wd_rope: x, positions and out are required");
+  const int vec = type == WD_F32 ? 4 : 8;
+  if (!aligned(x, 16) || !aligned(out, 16) || ldx % vec || ldo % vec || !aligned(positions, 4))
+    return refuse(MOE_ERR_ALIGN, "wd_rope: x and out need 16 bytes, as do their strides, positions 4");
+  TurnArgs a = {};
+  a.r = rope_args(r);
+  a.x = static_cast<const char*>(x), a.out = static_cast<char*>(out), a.positions = positions;
+  a.ldx = ldx * type_bytes(type), a.ldo = ldo * type_bytes(type);
+  a.T = T, a.head_bytes = dim * type_bytes(type), a.pieces = dim / 8, a.heads = heads;
+  a.copies = x != out;
+  a.items = a.copies ? (a.pieces + 1) / 2 : a.r.rot / 16;
+  const int all = heads * a.items, slices = (all + kThreads - 1) / kThreads;
+  a.chunk = (all + slices - 1) / slices;
+  a.per = tokens_of_a_cta(T, slices, a.r.rot, 6, 1);
+  cudaStream_t st = (cudaStream_t)stream;
+  return type == WD_F32 ? turn<WD_F32>(a, st) : type == WD_BF16 ? turn<WD_BF16>(a, st) : turn<WD_F16>(a, st);
+}
+
+extern "C" moe_status wd_kv4_rope_append(const wd_kv4_cache* c, const wd_rotation* r, const void* q, int64_t ldq,
+                                         int32_t q_heads, void* q_out, int64_t ldqo, const void* k, const void* v, int32_t type,
+                                         int64_t ldk, int64_t ldv, int32_t T, const int32_t* table, int32_t max_blocks,
+                                         const int32_t* lens, const int32_t* cu, int32_t S, int32_t* err, void* stream) {
+  using namespace wd;
+  moe_status rc = check_tokens(c, k, v, type, ldk, ldv, T, table, max_blocks, lens, cu, S, err, false);
+  if (rc != MOE_OK) return rc;
+  rc = check_rotation(r, c->dim);
+  if (rc != MOE_OK) return rc;
+  const int64_t row = (int64_t)q_heads * c->dim;
+  if (q_heads < 0 || row > 1 << 20 || (q_heads && (ldq < row || ldqo < row || (q == q_out && ldq != ldqo))))
+    return refuse(MOE_ERR_SHAPE, "wd_kv4_rope_append: need q_heads >= 0, up to 2^20 elements, ldq and ldqo of a token "
+                                 "at least, and the same in place");
+  if (T == 0 || S == 0) return MOE_OK;
+  if (q_heads && (!q || !q_out)) return refuse(MOE_ERR_NULL, "wd_kv4_rope_append: q and q_out are required");
+  if (q_heads && (!aligned(q, 16) || !aligned(q_out, 16) || ldq % 8 || ldqo % 8))
+    return refuse(MOE_ERR_ALIGN, "wd_kv4_rope_append: q and q_out need 16 bytes and strides % 8 == 0");
+  RopeAppendArgs a = {};
+  a.r = rope_args(r);
+  a.t = token_args(c, ldk, ldv, T, table, max_blocks, lens, cu, S, err);
+  a.q = static_cast<const uint16_t*>(q), a.q_out = static_cast<uint16_t*>(q_out), a.ldq = ldq, a.ldqo = ldqo;
+  a.k = static_cast<const uint16_t*>(k), a.v = static_cast<const uint16_t*>(v);
+  a.kc = c->k_codes, a.ks = c->k_scales, a.vc = c->v_codes, a.vs = c->v_scales;
+  a.copies = q != q_out;
+  a.kv_slices = c->heads * (c->dim / 8) / a.t.chunk;
+  // A slice of the queries: up to 256 items of 16 elements.
+  const int items = q_heads * (c->dim / 16), q_slices = (items + kThreads - 1) / kThreads;
+  a.q_heads = q_heads;
+  a.q_chunk = q_slices ? (items + q_slices - 1) / q_slices : 1;
+  if (a.kv_slices + q_slices > 65535) return refuse(MOE_ERR_SHAPE, "wd_kv4_rope_append: too many heads");
+  a.t.per = tokens_of_a_cta(T, a.kv_slices + q_slices, a.r.rot, 4, 2);
+  const dim3 grid((unsigned)((T + (int64_t)a.t.per - 1) / a.t.per), (unsigned)(a.kv_slices + q_slices));
+  cudaStream_t st = (cudaStream_t)stream;
+  const bool bf16 = type == WD_BF16;
+  return c->dim == 64    ? rope_append<64>(a, bf16, grid, st)
+         : c->dim == 128 ? rope_append<128>(a, bf16, grid, st)
+                         : rope_append<256>(a, bf16, grid, st);
+}
