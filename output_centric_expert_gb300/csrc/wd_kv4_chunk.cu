@@ -37,7 +37,8 @@ constexpr int kItemUnits = 2;    // what an item costs beside its key tiles, in 
 constexpr int kMinUnits = 3;     // of a CTA, on average, unless it has an item to itself
 constexpr uint32_t kWaitLimit = 1u << 20;
 constexpr int kSeqChunk = 512;   // sequences whose units are in shared memory at a time
-constexpr int kMeta = 4;         // key tiles whose page masks are kept
+constexpr int kDecodeWarps = 8, kQueryWarps = 3;
+constexpr int kMeta = 4;         // key tiles whose page masks and bad blocks are kept
 
 // The split item that goes on from this CTA into the next, parts 0 where there is none: an item with parts in the
 // CTAs c .. c + parts - 1 is in all their entries but the last.
@@ -61,21 +62,28 @@ struct ChunkArgs {
   int32_t T, S, max_blocks, pages, page_shift, heads, group, window, room;  // room: keys of a row of the table
   int32_t part_rows;
   float scale_log2;  // positive
-  uint32_t flip;     // what a pair of queries is xored with: the scale's sign
+  uint32_t flip;     // what the factors of K are xored with: the scale's sign
   uint32_t keep;     // and then masked: 0 for a scale of 0
 };
 
-template <int D_, int KEYS, int Q, int TERMS, int NK_, int NV_, int CTAS>
+template <int D_, int KEYS, int Q, int TERMS>
 struct Config {
-  static constexpr int D = D_, kKeys = KEYS, kQ = Q, kTerms = TERMS, kNK = NK_, kNV = NV_, kCtas = CTAS;
+  static constexpr int D = D_, kKeys = KEYS, kQ = Q, kTerms = TERMS;
+  static constexpr int kSlots = TERMS == 2 && D_ >= 128 ? 1 : 2;  // of K, and of V
   static constexpr int kItemRows = Q * kRows;
-  static constexpr int kSoftWarps = 4 * Q, kThreadsAll = (4 * Q + 5) * 32;
-  static constexpr int kQBytes = kRows * D * 2;        // of a term of a row tile
-  static constexpr int kTile = KEYS * D * 2;           // of K or V
-  static constexpr int kSmem = 1024 + Q * TERMS * kQBytes + (NK_ + NV_) * kTile;
+  static constexpr int kSoftWarps = 4 * Q, kThreadsAll = (kSoftWarps + kDecodeWarps + 4) * 32;
+  static constexpr int kWarpKeys = KEYS / kDecodeWarps;  // keys of a decode warp in a tile: 8 or 16, inside a run of 16
+  static constexpr int kQBytes = kRows * D * 2;          // of a term of a row tile
+  static constexpr int kTile = KEYS * D * 2;             // of K or V
+  static constexpr int kCodes = kWarpKeys * D / 2, kScales = kWarpKeys * D / 32;  // bytes of a decode warp's keys, K or V
+  static constexpr int kRaw = 2 * (kCodes + kScales);    // codes of K, of V, scales of K, of V
+  static constexpr int kSmem = 1024 + Q * TERMS * kQBytes + 2 * kSlots * kTile + kDecodeWarps * kRaw;
   static constexpr int kCols = Q * (KEYS + D);
   static constexpr int kTmem = kCols <= 256 ? 256 : 512;
-  static_assert(kCols <= 512 && kTmem * CTAS <= 512 && kSmem * CTAS <= 226 * 1024, "fits an SM");
+  // registers of a thread: setmaxnreg shares out what the launch has
+  static constexpr int kSoftRegs = 160, kDecodeRegs = 56, kMmaRegs = 48;
+  static constexpr int kRegs = 32 * (kSoftWarps * kSoftRegs + kDecodeWarps * kDecodeRegs + 4 * kMmaRegs);
+  static_assert(kCols <= 512 && kSmem <= 221 * 1024, "fits an SM");
 };
 
 // ------------------------------------------------------------------ PTX --
@@ -112,26 +120,57 @@ __device__ __forceinline__ void tmem_store32(uint32_t at, const uint32_t (&r)[32
       "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
       : "memory");
 }
+// 16 columns, waited for.
+__device__ __forceinline__ void tmem_load16(uint32_t at, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];\n\t"
+      "tcgen05.wait::ld.sync.aligned;"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(at)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_store16(uint32_t at, const uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(at),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      : "memory");
+}
 __device__ __forceinline__ void tmem_stored() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 __device__ __forceinline__ void tc_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void tc_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
 
-// D (+)= A B: both by shared-memory descriptors, or A in tensor memory.
-__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool add) {
+// D (+)= A B: both by shared-memory descriptors (the low words; the high ones are constants), or A in tensor memory.
+template <uint32_t A_HI, uint32_t B_HI, uint32_t IDESC>
+__device__ __forceinline__ void mma_ss(uint32_t d, uint32_t a, uint32_t b, bool add) {
   asm volatile(
-      "{.reg .pred p;\n\t"
-      "setp.ne.u32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-      "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)add)
+      "{.reg .pred p;\n\t.reg .b64 x, y;\n\t"
+      "mov.b64 x, {%1, %4};\n\t"
+      "mov.b64 y, {%2, %5};\n\t"
+      "setp.ne.u32 p, %3, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %6, p;\n\t}" ::"r"(d),
+      "r"(a), "r"(b), "r"((uint32_t)add), "n"(A_HI), "n"(B_HI), "n"(IDESC)
       : "memory");
 }
-__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool add) {
+template <uint32_t B_HI, uint32_t IDESC>
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint32_t b, bool add) {
+  asm volatile(
+      "{.reg .pred p;\n\t.reg .b64 y;\n\t"
+      "mov.b64 y, {%2, %4};\n\t"
+      "setp.ne.u32 p, %3, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], y, %5, p;\n\t}" ::"r"(d),
+      "r"(a), "r"(b), "r"((uint32_t)add), "n"(B_HI), "n"(IDESC)
+      : "memory");
+}
+__device__ __forceinline__ bool elected() {
+  uint32_t r;
   asm volatile(
       "{.reg .pred p;\n\t"
-      "setp.ne.u32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
-      "r"(a), "l"(b), "r"(idesc), "r"((uint32_t)add)
-      : "memory");
+      "elect.sync _|p, 0xFFFFFFFF;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(r));
+  return r != 0;
 }
 // The barrier completes when every MMA issued so far by this thread has.
 __device__ __forceinline__ void tc_commit(uint32_t bar) {
@@ -145,8 +184,9 @@ __device__ __forceinline__ void bar_arrive(uint32_t bar) {
 }
 // Wait for the phase of an mbarrier, with a limit; false when it runs out.
 __device__ __forceinline__ bool bar_wait(uint32_t bar, uint32_t parity) {
-  uint32_t done = 0;
-  for (uint32_t i = 0; i < kWaitLimit && !done; ++i)
+#pragma unroll 1
+  for (uint32_t i = kWaitLimit; i; --i) {
+    uint32_t done;
     asm volatile(
         "{.reg .pred p;\n\t"
         "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
@@ -154,7 +194,42 @@ __device__ __forceinline__ bool bar_wait(uint32_t bar, uint32_t parity) {
         : "=r"(done)
         : "r"(bar), "r"(parity)
         : "memory");
-  return done != 0;
+    if (done) return true;
+  }
+  return false;
+}
+__device__ __forceinline__ void bar_expect(uint32_t bar, uint32_t bytes) {
+  asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void bulk_copy(uint32_t to, const void* from, uint32_t bytes, uint32_t bar) {
+  asm volatile("cp.async.bulk.shared::cta.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(to), "l"(from),
+               "r"(bytes), "r"(bar)
+               : "memory");
+}
+// All threads of the softmax warps.
+__device__ __forceinline__ void soft_sync(int id) { asm volatile("bar.sync %0, 256;" ::"r"(id) : "memory"); }
+
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+// Two FP32 operations in one instruction.
+__device__ __forceinline__ uint64_t pair_of(uint32_t a, uint32_t b) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "r"(a), "r"(b));
+  return r;
+}
+__device__ __forceinline__ void split_pair(uint64_t v, uint32_t& a, uint32_t& b) { asm("mov.b64 {%0, %1}, %2;" : "=r"(a), "=r"(b) : "l"(v)); }
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
 }
 __device__ __forceinline__ float exp2_fast(float v) {
   float r;
@@ -386,180 +461,157 @@ __device__ __forceinline__ uint32_t e2m1_pair(uint32_t up, uint32_t w, uint32_t 
 }
 
 template <int WORDS>
-__device__ __forceinline__ void load_words(const uint8_t* p, uint32_t (&w)[WORDS], int at = 0) {
-  if constexpr (WORDS == 2) {
-    const uint2 v = __ldg(reinterpret_cast<const uint2*>(p));
+__device__ __forceinline__ void read_words(const uint8_t* p, uint32_t (&w)[WORDS]) {  // shared memory
+  if constexpr (WORDS == 1) {
+    w[0] = *reinterpret_cast<const uint32_t*>(p);
+  } else if constexpr (WORDS == 2) {
+    const uint2 v = *reinterpret_cast<const uint2*>(p);
     w[0] = v.x, w[1] = v.y;
   } else {
 #pragma unroll
     for (int i = 0; i < WORDS; i += 4) {
-      const uint4 v = __ldg(reinterpret_cast<const uint4*>(p + 4 * i));
+      const uint4 v = *reinterpret_cast<const uint4*>(p + 4 * i);
       w[i] = v.x, w[i + 1] = v.y, w[i + 2] = v.z, w[i + 3] = v.w;
     }
   }
 }
 
-// A decode warp has a quarter of a tile's keys. K: lane (l & 7, t = l >> 3) has of 8 keys at a time the words (t, all
-// blocks); V: of 8 pairs of keys at a time those of g = 2u, 2u + 1, u = l >> 3. So the 8 lanes that store together
-// have 8 rows of 128 bytes, and the swizzle spreads them over all banks.
-template <typename C>
-struct KRegs {
-  static constexpr int NB = C::D / 32, kSteps = C::kKeys / 32;
-  uint32_t w[kSteps][NB], s[kSteps][(NB + 3) / 4];
-};
-template <typename C>
-struct VRegs {
-  static constexpr int NB = C::D / 32, kSteps = C::kKeys / 64;
-  uint32_t w[kSteps][2 * NB], s[kSteps][NB / 2];
-};
+// A decode warp has an eighth of a tile's keys, whose codes lie in `raw` as in the cache. Of 8 keys at a time a lane has
+// one key, l & 7, and the words t = l >> 3 ^ key >> 1 of all blocks; of 8 pairs of keys (4 where a warp has no more, and
+// half of the blocks) one pair and the words of g = 2u, 2u + 1. With that t the 8 lanes that read or write 16 bytes
+// together meet all banks, in the cache's order on one side and the 128-byte swizzle on the other.
 
-// run(i): the 16-key run i of this warp, -1 where it has no page.
-template <typename C, typename F>
-__device__ __forceinline__ void load_k(const ChunkArgs& a, KRegs<C>& r, F run) {
-  constexpr int D = C::D, NB = KRegs<C>::NB;
-  const int lane = threadIdx.x & 31;
+// K as it is in the tile: [D / 64][keys][128 bytes], 16-byte unit u of a row at u ^ (row & 7). here: the keys have a page.
+template <typename C>
+__device__ __forceinline__ void decode_k(uint8_t* tile, const uint8_t* raw, bool here, int warp, uint32_t flip, uint32_t keep) {
+  constexpr int D = C::D, NB = D / 32;
+  const int lane = threadIdx.x & 31, k = lane & 7, t = (lane >> 3) ^ (k >> 1);
+#pragma unroll 1
+  for (int i = 0; i < C::kWarpKeys / 8; ++i) {
+    const int key = 8 * i + k;
+    uint32_t w[NB], sc[(NB + 3) / 4];
+    read_words<NB>(raw + key * (D / 2) + t * (D / 8), w);
+    const uint8_t* scales = raw + 2 * C::kCodes + key * NB;
+    if constexpr (NB == 2)
+      sc[0] = *reinterpret_cast<const uint16_t*>(scales);
+    else
+      read_words<NB / 4>(scales, sc);
+    uint8_t* row = tile + (warp * C::kWarpKeys + key) * 128;
+    auto put = [&](int b, const uint32_t(&e)[4]) {
+      *reinterpret_cast<uint4*>(row + (b >> 1) * (C::kKeys * 128) + ((((b & 1) * 4 + t) ^ k) << 4)) = make_uint4(e[0], e[1], e[2], e[3]);
+    };
+    uint32_t big = 0;
 #pragma unroll
-  for (int i = 0; i < KRegs<C>::kSteps; ++i) {
-    const int id = run(i / 2);
+    for (int j = 0; j < (NB + 3) / 4; ++j) big |= __vmaxu4(sc[j], 0x80808080u) ^ 0x80808080u;
+    if (!here) keep = 0;
+    if (!big || !here) {
 #pragma unroll
-    for (int j = 0; j < NB; ++j) r.w[i][j] = 0;
+      for (int b = 0; b < NB; ++b) {
+        const uint32_t s = (sc[b / 4] >> (8 * (b & 3))) & 255u, up = w[b] << 4, f = (((s + 126u) * 0x800080u) ^ flip) & keep;
+        uint32_t e[4];
 #pragma unroll
-    for (int j = 0; j < (NB + 3) / 4; ++j) r.s[i][j] = 0;
-    if (id >= 0) {
-      const int64_t key = (int64_t)id * 16 + (i & 1) * 8 + (lane & 7);
-      load_words<NB>(a.kc + key * (D / 2) + (lane >> 3) * (D / 8), r.w[i]);
-      if constexpr (NB == 2)
-        r.s[i][0] = __ldg(reinterpret_cast<const uint16_t*>(a.ks + key * 2));
-      else if constexpr (NB == 4)
-        r.s[i][0] = __ldg(reinterpret_cast<const uint32_t*>(a.ks + key * 4));
-      else
-        load_words<2>(a.ks + key * 8, r.s[i]);
-    }
-  }
-}
-template <typename C, typename F>
-__device__ __forceinline__ void load_v(const ChunkArgs& a, VRegs<C>& r, F run) {
-  constexpr int D = C::D, NB = VRegs<C>::NB;
-  const int lane = threadIdx.x & 31;
+        for (int j = 0; j < 4; ++j) e[j] = mul2_bf16(e2m1_pair(up, w[b], 0xC480 + 0x1111 * j), f);
+        put(b, e);
+      }
+    } else {
+#pragma unroll 1
+      for (int b = 0; b < NB; ++b) {
+        const uint32_t s = scales[b], x = *reinterpret_cast<const uint32_t*>(raw + key * (D / 2) + t * (D / 8) + 4 * b), up = x << 4;
+        const uint32_t f = s == 255u ? 0x7FC07FC0u : (first_factor(s) ^ flip) & keep, g = second_factor(s);
+        uint32_t e[4];
 #pragma unroll
-  for (int i = 0; i < VRegs<C>::kSteps; ++i) {
-    const int id = run(i);
-#pragma unroll
-    for (int j = 0; j < 2 * NB; ++j) r.w[i][j] = 0;
-#pragma unroll
-    for (int j = 0; j < NB / 2; ++j) r.s[i][j] = 0;
-    if (id >= 0) {
-      const int64_t pair = (int64_t)id * 8 + (lane & 7);
-      load_words<2 * NB>(a.vc + pair * D + (lane >> 3) * (D / 4), r.w[i]);
-      if constexpr (NB == 2)
-        r.s[i][0] = __ldg(reinterpret_cast<const uint32_t*>(a.vs + pair * 4));
-      else
-        load_words<NB / 2>(a.vs + pair * (D / 16), r.s[i]);
+        for (int j = 0; j < 4; ++j) e[j] = mul2_bf16(mul2_bf16(e2m1_pair(up, x, 0xC480 + 0x1111 * j), f), g);
+        put(b, e);
+      }
     }
   }
 }
 
-// Decoded K into its tile: [D / 64][keys][128 bytes], 16-byte unit u of a row at u ^ (row & 7).
+// V as it is in the tile: [D / 64][keys][128 bytes] too. Blocks of NaN, or past BF16's range, become 0 and are noted in
+// `bad` (a byte per key, a bit per block); returns whether there are any.
 template <typename C>
-__device__ __forceinline__ void store_k(uint8_t* tile, const KRegs<C>& r) {
-  constexpr int NB = KRegs<C>::NB;
-  const int lane = threadIdx.x & 31, warp = (threadIdx.x >> 5) & 3, t = lane >> 3;
-  const int row0 = warp * (C::kKeys / 4) + (lane & 7);
+__device__ __forceinline__ bool decode_v(uint8_t* tile, const uint8_t* raw, bool here, uint8_t* bad, int warp) {
+  constexpr int D = C::D, NB = D / 32, PAIRS = C::kWarpKeys / 2, NBL = NB * PAIRS / 8;  // NBL: blocks of a lane
+  const int lane = threadIdx.x & 31, p = lane % PAIRS;
+  const int u = (lane / PAIRS & 3) ^ (PAIRS == 8 ? p >> 1 : p), half = PAIRS == 8 ? 0 : lane >> 4;
+  const uint8_t *codes = raw + C::kCodes + p * D + u * (D / 4) + half * 16;
+  const uint8_t* scales = raw + 2 * C::kCodes + C::kScales + p * (D / 16) + half * 8;
+  uint32_t w[2 * NBL], sc[NBL / 2];
+  uint32_t first[NBL], next[NBL];
+  read_words<NBL>(codes, first);
+  read_words<NBL>(codes + D / 8, next);
 #pragma unroll
-  for (int i = 0; i < KRegs<C>::kSteps; ++i) {
-    uint8_t* row = tile + (row0 + 8 * i) * 128;
+  for (int b = 0; b < NBL; ++b) w[b] = first[b], w[NBL + b] = next[b];
+  read_words<NBL / 2>(scales, sc);
+  const int row0 = warp * C::kWarpKeys + 2 * p;
+  uint32_t big = 0, mask = 0;
 #pragma unroll
-    for (int b = 0; b < NB; ++b) {
-      const uint32_t s = (r.s[i][b / 4] >> (8 * (b & 3))) & 255u, w = r.w[i][b], up = w << 4;
-      const uint32_t f = s == 255u ? 0x7FC07FC0u : first_factor(s);
+  for (int j = 0; j < NBL / 2; ++j) big |= __vmaxu4(sc[j], 0x80808080u) ^ 0x80808080u;
+  const bool plain = !big || !here;
+  if (!plain) {
+#pragma unroll
+    for (int b = 0; b < NBL; ++b)
+#pragma unroll
+      for (int k = 0; k < 2; ++k)
+        if (((sc[b / 2] >> (16 * (b & 1) + 8 * k)) & 255u) >= 253u) mask |= 1u << (8 * k + half * NBL + b);
+  }
+  if (PAIRS != 8) mask |= __shfl_xor_sync(kAll, mask, 16);
+  if (lane < PAIRS) *reinterpret_cast<uint16_t*>(bad + row0) = (uint16_t)mask;
+#pragma unroll 1
+  for (int n = 0; n < 2; ++n) {
+    const int key = PAIRS == 8 ? n ^ (p >> 2) : n, row = row0 + key;  // (8 pairs: half of the lanes store the odd key first)
+    const uint32_t sel = key ? 0xD5C4u : 0x9180u;                     // the bytes 0, 1 of w or of w << 4
+    uint8_t* at = tile + row * 128;
+#pragma unroll
+    for (int b = 0; b < NBL; ++b) {
+      const uint32_t s = (sc[b / 2] >> (16 * (b & 1) + 8 * key)) & 255u;
+      const uint32_t f = plain ? (here ? (s + 126u) * 0x800080u : 0u) : s >= 253u ? 0u : first_factor(s);
       uint32_t e[4];
 #pragma unroll
-      for (int j = 0; j < 4; ++j) e[j] = mul2_bf16(e2m1_pair(up, w, 0xC480 + 0x1111 * j), f);
-      if (s > 128u) {
-        const uint32_t g = second_factor(s);
+      for (int j = 0; j < 2; ++j) {
+        const uint32_t x = w[j * NBL + b], up = x << 4;
+        e[2 * j] = mul2_bf16(e2m1_pair(up, x, sel), f);
+        e[2 * j + 1] = mul2_bf16(e2m1_pair(up, x, sel + 0x2222u), f);
+      }
+      if (!plain) {
+        const uint32_t g = s >= 253u ? 0u : second_factor(s);
 #pragma unroll
         for (int j = 0; j < 4; ++j) e[j] = mul2_bf16(e[j], g);
       }
-      *reinterpret_cast<uint4*>(row + (b >> 1) * (C::kKeys * 128) + ((((b & 1) * 4 + t) ^ (lane & 7)) << 4)) =
+      const int block = half * NBL + b;
+      *reinterpret_cast<uint4*>(at + (block >> 1) * (C::kKeys * 128) + ((((block & 1) * 4 + u) ^ (row & 7)) << 4)) =
           make_uint4(e[0], e[1], e[2], e[3]);
     }
   }
-}
-
-// Decoded V into its tile: [D / 64][keys][128 bytes] too. Blocks of NaN, or past BF16's range, become 0 and are noted in
-// `bad` (a byte per key, a bit per block); returns whether there are any.
-template <typename C>
-__device__ __forceinline__ bool store_v(uint8_t* tile, const VRegs<C>& r, uint8_t* bad) {
-  constexpr int NB = VRegs<C>::NB;
-  const int lane = threadIdx.x & 31, warp = (threadIdx.x >> 5) & 3, u = lane >> 3;
-  const int odd = (lane >> 2) & 1;  // which key of the pair this lane stores first
-  bool any = false;
-#pragma unroll
-  for (int i = 0; i < VRegs<C>::kSteps; ++i) {
-    const int row0 = warp * (C::kKeys / 4) + 16 * i + 2 * (lane & 7);
-    uint32_t big = 0, mask[2] = {0, 0};
-#pragma unroll
-    for (int j = 0; j < NB / 2; ++j) big |= __vmaxu4(r.s[i][j], 0xFCFCFCFCu) ^ 0xFCFCFCFCu;
-    if (big) {
-      any = true;
-#pragma unroll
-      for (int b = 0; b < NB; ++b)
-#pragma unroll
-        for (int k = 0; k < 2; ++k)
-          if (((r.s[i][b / 2] >> (16 * (b & 1) + 8 * k)) & 255u) >= 253u) mask[k] |= 1u << b;
-    }
-    if (u == 0) *reinterpret_cast<uint16_t*>(bad + row0) = (uint16_t)(mask[0] | mask[1] << 8);
-#pragma unroll
-    for (int k = 0; k < 2; ++k) {
-      const int key = k ^ odd, row = row0 + key;
-      const uint32_t sel = key ? 0xD5C4u : 0x9180u;  // the bytes j, j + 1 of w or of w << 4
-#pragma unroll
-      for (int b = 0; b < NB; ++b) {
-        const uint32_t s = (r.s[i][b / 2] >> (16 * (b & 1) + 8 * key)) & 255u;
-        const uint32_t f = s >= 253u ? 0u : first_factor(s);
-        uint32_t e[4];
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          const uint32_t w = r.w[i][j * NB + b], up = w << 4;
-          e[2 * j] = mul2_bf16(e2m1_pair(up, w, sel), f);
-          e[2 * j + 1] = mul2_bf16(e2m1_pair(up, w, sel + 0x2222u), f);
-        }
-        if (s > 128u) {
-          const uint32_t g = s >= 253u ? 0u : second_factor(s);
-#pragma unroll
-          for (int j = 0; j < 4; ++j) e[j] = mul2_bf16(e[j], g);
-        }
-        *reinterpret_cast<uint4*>(tile + (b >> 1) * (C::kKeys * 128) + row * 128 + ((((b & 1) * 4 + u) ^ (row & 7)) << 4)) =
-            make_uint4(e[0], e[1], e[2], e[3]);
-      }
-    }
-  }
-  return any;
+  return mask != 0;
 }
 
 // ---------------------------------------------------------------- kernel --
 
 template <typename C>
 struct Shared {  // beside the operands
-  uint64_t q_full, q_free, k_full[C::kNK], k_free[C::kNK], v_full[C::kNV], v_free[C::kNV];
-  uint64_t s_full[C::kQ], p_full[C::kQ], o_done[C::kQ], drained;
+  uint64_t q_full, q_free, k_full[C::kSlots], k_free[C::kSlots], v_full[C::kSlots], v_free[C::kSlots];
+  uint64_t s_full[C::kQ], p_full[C::kQ][2], o_done[C::kQ], raw_full[2][kDecodeWarps], drained;  // (raw: K, V)
   int64_t units[kSeqChunk], warp[C::kThreadsAll / 32];
   Share share;
   uint32_t tmem, failed;
-  uint32_t bad_tile[C::kNV];                       // number + 1 of the last tile in the slot with bad blocks of V
-  __align__(4) uint8_t valid[kMeta][4];            // runs with a page, by decode warp
-  __align__(4) uint8_t bad[C::kNV][C::kKeys];      // blocks of V that are NaN
+  uint32_t bad_tile[kMeta];                        // number + 1 of the last tile in this place with bad blocks of V
+  __align__(8) uint8_t valid[kMeta][kDecodeWarps];  // whether a decode warp's keys have a page
+  __align__(4) uint8_t bad[kMeta][C::kKeys];       // blocks of V that are NaN
+  float twin_m[kRows], twin_l[kRows];              // a second row tile's, where both have the same rows
+  uint32_t twin_nan[kRows];
 };
 
 template <typename C, bool BF16>
-__global__ void __launch_bounds__(C::kThreadsAll, C::kCtas) kv4_chunk_kernel(const ChunkArgs a) {
-  constexpr int D = C::D, KEYS = C::kKeys;
+__global__ void __launch_bounds__(C::kThreadsAll, 1) kv4_chunk_kernel(const ChunkArgs a) {
+  constexpr int D = C::D, KEYS = C::kKeys, SLOTS = C::kSlots;
   extern __shared__ uint4 dyn4[];
   __shared__ Shared<C> sh;
   uint8_t* base = reinterpret_cast<uint8_t*>(dyn4) + (1024 - (smem_addr(dyn4) & 1023)) % 1024;
   uint8_t* const s_q = base;                                    // [row tile][term][D / 64][128][128 bytes]
   uint8_t* const s_k = s_q + C::kQ * C::kTerms * C::kQBytes;    // [slot][tile]
-  uint8_t* const s_v = s_k + C::kNK * C::kTile;
+  uint8_t* const s_v = s_k + SLOTS * C::kTile;
+  uint8_t* const s_raw = s_v + SLOTS * C::kTile;                // [decode warp]
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
   if (warp == 0) {
@@ -568,17 +620,18 @@ __global__ void __launch_bounds__(C::kThreadsAll, C::kCtas) kv4_chunk_kernel(con
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
   }
   if (tid == 32) {
-    bar_init(smem_addr(&sh.q_full), 128);
+    bar_init(smem_addr(&sh.q_full), kQueryWarps);
     bar_init(smem_addr(&sh.q_free), 1);
-    for (int i = 0; i < C::kNK; ++i) bar_init(smem_addr(&sh.k_full[i]), 128), bar_init(smem_addr(&sh.k_free[i]), 1);
-    for (int i = 0; i < C::kNV; ++i) {
-      bar_init(smem_addr(&sh.v_full[i]), 128), bar_init(smem_addr(&sh.v_free[i]), 1);
-      sh.bad_tile[i] = 0;
+    for (int i = 0; i < SLOTS; ++i) {
+      bar_init(smem_addr(&sh.k_full[i]), kDecodeWarps), bar_init(smem_addr(&sh.k_free[i]), 1);
+      bar_init(smem_addr(&sh.v_full[i]), kDecodeWarps), bar_init(smem_addr(&sh.v_free[i]), 1);
     }
+    for (int i = 0; i < kMeta; ++i) sh.bad_tile[i] = 0;
     for (int i = 0; i < C::kQ; ++i) {
-      bar_init(smem_addr(&sh.s_full[i]), 1), bar_init(smem_addr(&sh.p_full[i]), 128);
+      bar_init(smem_addr(&sh.s_full[i]), 1), bar_init(smem_addr(&sh.p_full[i][0]), 4), bar_init(smem_addr(&sh.p_full[i][1]), 4);
       bar_init(smem_addr(&sh.o_done[i]), 1);
     }
+    for (int i = 0; i < 2 * kDecodeWarps; ++i) bar_init(smem_addr(&sh.raw_full[0][0]) + 8 * i, 1);
     bar_init(smem_addr(&sh.drained), 1);
     sh.failed = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -595,81 +648,86 @@ __global__ void __launch_bounds__(C::kThreadsAll, C::kCtas) kv4_chunk_kernel(con
 
   if (warp < C::kSoftWarps) {
     // ---------------------------------------------------------- softmax --
+    if constexpr (C::kQ == 2) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::kSoftRegs));
     const int t = warp >> 2, r = tid & 127;
     const uint32_t lanes = (uint32_t)(warp & 3) << 21;
     const uint32_t s_at = tmem + lanes + t * KEYS, o_at = tmem + lanes + C::kQ * KEYS + t * D;
-    const uint32_t s_full = smem_addr(&sh.s_full[t]), p_full = smem_addr(&sh.p_full[t]), o_done = smem_addr(&sh.o_done[t]);
+    const uint32_t s_full = smem_addr(&sh.s_full[t]), p_full = smem_addr(&sh.p_full[t][0]), o_done = smem_addr(&sh.o_done[t]);
     uint32_t s_phase = 0, o_phase = 0;
     if (tid == 0) a.split[blockIdx.x] = Split{};
     while (items.next(it)) {
       if (tid == 0) {
-        if (!(it.begins && it.ends) && !it.ends) {  // goes on in the next CTA
+        if (!it.ends) {  // goes on in the next CTA
           const int c0 = it.begins ? (int)blockIdx.x : cta_of(share.total, share.ctas, it.unit0 + kItemUnits);
           const int c1 = cta_of(share.total, share.ctas, it.unit0 + it.all - 1);
           a.split[blockIdx.x] = {c1 - c0 + 1, (int)blockIdx.x - c0, it.seq, it.head, it.row0, it.rows, {0, 0}};
         }
         if (it.q.len < 0 || (int64_t)it.q.len + it.q.tokens > a.room) flag_invalid(a.err);
       }
-      const int rows = it.rows - t * kRows;  // of this row tile, and of the warp below
-      if (rows <= 0) {
-        tile += it.tiles;
-        continue;
-      }
+      // Few rows: both groups of warps have them, and every other key tile.
+      const bool twin = C::kQ == 2 && it.rows <= kRows;
+      const int above = twin ? 0 : t * kRows;  // rows of the item before this group's
+      const int rows = it.rows - above;
       const bool mine = r < rows, busy = (warp & 3) * 32 < rows;
-      const int flat = it.row0 + t * kRows + (mine ? r : 0), token = flat / a.group;
+      const int flat = it.row0 + above + (mine ? r : 0), token = flat / a.group;
       const int lo = keys_begin(a, it.q, token), hi = keys_end(a, it.q, token);
-      // keys that all rows of the tile see
-      const int all_lo = keys_begin(a, it.q, (it.row0 + t * kRows + min(rows, kRows) - 1) / a.group);
-      const int all_hi = keys_end(a, it.q, (it.row0 + t * kRows) / a.group);
+      // keys that all rows of the group see
+      const int all_lo = keys_begin(a, it.q, (it.row0 + above + min(rows, kRows) - 1) / a.group);
+      const int all_hi = keys_end(a, it.q, (it.row0 + above) / a.group);
       float m = -INFINITY, l = 0.0f, raw = 0.0f;  // m = raw * scale, rounded
       uint32_t nan = 0;
-      for (int i = 0; i < it.tiles; ++i, ++tile) {
+      const int step = twin ? 2 : 1, i0 = twin ? t : 0;
+      // Tile `at`, whose products have begun, so that its values are there: NaN blocks of keys that this row sees.
+      auto check = [&](uint32_t at, int k0, bool there) {
+        if (there && *reinterpret_cast<volatile uint32_t*>(&sh.bad_tile[at % kMeta]) == at + 1)
+          for (int key = max(0, lo - k0); key < min(KEYS, hi - k0); ++key) nan |= sh.bad[at % kMeta][key];
+      };
+      for (int i = i0; i < it.tiles; i += step) {
+        const uint32_t at = tile + i;
         ok = ok && bar_wait(s_full, s_phase);
         s_phase ^= 1;
         __syncwarp();
         tc_after();
         const int k0 = (it.tile + i) * KEYS;
+        check(at - step, k0 - step * KEYS, i > i0);
         if (busy) {
-          const uint32_t valid4 = *reinterpret_cast<const uint32_t*>(sh.valid[tile % kMeta]);
-          constexpr int kRuns = KEYS / 64;  // 16-key runs of a decode warp
-          uint32_t valid = 0;
+          constexpr int kC = KEYS / 32;
+          uint32_t x[kC][32];
 #pragma unroll
-          for (int w = 0; w < 4; ++w) valid |= ((valid4 >> (8 * w)) & ((1u << kRuns) - 1u)) << (w * kRuns);
-          const bool whole = k0 >= all_lo && k0 + KEYS <= all_hi && valid == (1u << (KEYS / 16)) - 1u;
-          // the row's keys among 32 from column c on
-          auto seen = [&](int c) {
-            const int b = max(0, min(32, lo - k0 - c)), e = max(0, min(32, hi - k0 - c));
-            uint32_t v = (e >= 32 ? kAll : (1u << e) - 1u) & ~(b >= 32 ? kAll : (1u << b) - 1u);
-            if (!(valid >> (c / 16) & 1u)) v &= 0xFFFF0000u;
-            if (!(valid >> (c / 16) & 2u)) v &= 0x0000FFFFu;
-            return v;
-          };
-          float top = -INFINITY;
-          uint32_t x[2][32];
+          for (int c = 0; c < kC / 2; ++c) tmem_load32(s_at + 32 * c, x[c]);
+          const uint2 valid8 = *reinterpret_cast<const uint2*>(sh.valid[at % kMeta]);
+          const bool whole = k0 >= all_lo && k0 + KEYS <= all_hi && (valid8.x & valid8.y) == 0x01010101u;
+          // a bit per run of 16 keys: bytes 0 .. 7, or (8 keys to a warp) every other one
+          uint32_t valid = ((valid8.x * 0x01020408u) >> 24 & 15u) | ((valid8.y * 0x01020408u) >> 20 & 0xF0u);
+          if (KEYS == 64) valid = (valid & 1u) | (valid >> 1 & 2u) | (valid >> 2 & 4u) | (valid >> 3 & 8u);
+          float tops[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-          for (int c = 0; c < KEYS; c += 64) {
-            tmem_load32(s_at + c, x[0]);
-            tmem_load32(s_at + c + 32, x[1]);
-            tmem_wait(x[0]);
-            asm volatile("" : WD_R32(x[1]));
+          for (int half = 0; half < 2; ++half) {
+            tmem_wait(x[half * kC / 2]);
+            if (kC == 4) asm volatile("" : WD_R32(x[(half * kC / 2 + 1) % kC]));
+            if (half == 0) {
 #pragma unroll
-            for (int half = 0; half < 2; ++half) {
-              if (!whole) {
-                const uint32_t v = seen(c + 32 * half);
+              for (int c = kC / 2; c < kC; ++c) tmem_load32(s_at + 32 * c, x[c]);
+            }
+#pragma unroll
+            for (int c = half * kC / 2; c < (half + 1) * kC / 2; ++c) {
+              if (!whole) {  // the row's keys among these 32
+                const int b = max(0, min(32, lo - k0 - 32 * c)), e = max(0, min(32, hi - k0 - 32 * c));
+                uint32_t v = (e >= 32 ? kAll : (1u << e) - 1u) & ~(b >= 32 ? kAll : (1u << b) - 1u);
+                if (!(valid >> (2 * c) & 1u)) v &= 0xFFFF0000u;
+                if (!(valid >> (2 * c) & 2u)) v &= 0x0000FFFFu;
 #pragma unroll
                 for (int j = 0; j < 32; ++j)
-                  if (!(v >> j & 1u)) x[half][j] = 0xFF800000u;
+                  if (!(v >> j & 1u)) x[c][j] = 0xFF800000u;
               }
-              float p0 = -INFINITY, p1 = -INFINITY;
 #pragma unroll
-              for (int j = 0; j < 32; j += 2) {
-                p0 = fmaxf(p0, __uint_as_float(x[half][j]));
-                p1 = fmaxf(p1, __uint_as_float(x[half][j + 1]));
-              }
-              top = fmaxf(top, fmaxf(p0, p1));
+              for (int j = 0; j < 32; j += 8)
+#pragma unroll
+                for (int n = 0; n < 4; ++n)
+                  tops[n] = max3(tops[n], __uint_as_float(x[c][j + 2 * n]), __uint_as_float(x[c][j + 2 * n + 1]));
             }
           }
-          const float to = top * a.scale_log2;
+          const float top = fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3])), to = top * a.scale_log2;
           bool moved = false;
           float f = 1.0f;
           if (m == -INFINITY) {
@@ -678,261 +736,350 @@ __global__ void __launch_bounds__(C::kThreadsAll, C::kCtas) kv4_chunk_kernel(con
             f = exp2_fast((raw - top) * a.scale_log2);
             m = to, raw = top;
             l *= f;
-            moved = i > 0 && mine;  // (rows that are not there hold anything)
+            moved = mine;  // (rows that are not there hold anything)
           }
-          if (__any_sync(kAll, moved)) {
+          if (__any_sync(kAll, moved)) {  // (not at the first tile: m is -inf)
 #pragma unroll 1
-            for (int c = 0; c < D; c += 32) {
-              tmem_load32(o_at + c, x[0]);
-              tmem_wait(x[0]);
+            for (int c = 0; c < D; c += 16) {
+              uint32_t o[16];
+              tmem_load16(o_at + c, o);
 #pragma unroll
-              for (int j = 0; j < 32; ++j) x[0][j] = __float_as_uint(__uint_as_float(x[0][j]) * f);
-              tmem_store32(o_at + c, x[0]);
+              for (int j = 0; j < 16; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * f);
+              tmem_store16(o_at + c, o);
             }
           }
           // s scale - m in one step is off by the rounding of m: too much for logits this loud
           const bool loud = __any_sync(kAll, mine && fabsf(m) > 1048576.0f && m != -INFINITY);
           const float less = m == -INFINITY || loud ? 0.0f : -m;
-          float sum0 = 0.0f, sum1 = 0.0f;
-          tmem_load32(s_at, x[0]);
+          if (loud) {
 #pragma unroll
-          for (int c = 0; c < KEYS; c += 32) {
-            uint32_t(&now)[32] = x[(c / 32) & 1];
-            tmem_wait(now);
-            if (c + 32 < KEYS) tmem_load32(s_at + c + 32, x[(c / 32 + 1) & 1]);
-            if (!whole) {
-              const uint32_t v = seen(c);
+            for (int c = 0; c < kC; ++c)
 #pragma unroll
-              for (int j = 0; j < 32; ++j)
-                if (!(v >> j & 1u)) now[j] = 0xFF800000u;
-            }
-            if (loud) {
+              for (int j = 0; j < 32; ++j) x[c][j] = __float_as_uint(__uint_as_float(x[c][j]) - raw);
+          }
+          const uint64_t scale2 = pair_of(__float_as_uint(a.scale_log2), __float_as_uint(a.scale_log2));
+          const uint64_t less2 = pair_of(__float_as_uint(less), __float_as_uint(less));
+          uint64_t sums[2] = {0, 0};
 #pragma unroll
-              for (int j = 0; j < 32; ++j) now[j] = __float_as_uint(__uint_as_float(now[j]) - raw);
-            }
+          for (int c = 0; c < kC; ++c) {
             uint32_t p[32];
 #pragma unroll
             for (int j = 0; j < 32; j += 2) {
-              const float p0 = exp2_fast(fmaf(__uint_as_float(now[j]), a.scale_log2, less));
-              const float p1 = exp2_fast(fmaf(__uint_as_float(now[j + 1]), a.scale_log2, less));
-              sum0 += p0;
-              sum1 += p1;
-              const uint32_t u0 = __float_as_uint(p0), u1 = __float_as_uint(p1);
+              uint32_t u0, u1;
+              float r0, r1;
+              split_pair(fma2(pair_of(x[c][j], x[c][j + 1]), scale2, less2), u0, u1);
+              u0 = __float_as_uint(exp2_fast(__uint_as_float(u0)));
+              u1 = __float_as_uint(exp2_fast(__uint_as_float(u1)));
+              sums[(j / 2) & 1] = add2(sums[(j / 2) & 1], pair_of(u0, u1));
               p[j / 2] = __byte_perm(u0, u1, 0x7632);
-              p[16 + j / 2] = pack2<true>(p0 - __uint_as_float(u0 & 0xFFFF0000u), p1 - __uint_as_float(u1 & 0xFFFF0000u));
+              // what the cut leaves: p - hi
+              asm("{.reg .b16 a, b, m;\n\t"
+                  "mov.b32 {a, b}, %2;\n\t"
+                  "mov.b16 m, 0xBF80;\n\t"
+                  "fma.rn.f32.bf16 %0, a, m, %3;\n\t"
+                  "fma.rn.f32.bf16 %1, b, m, %4;\n\t}"
+                  : "=f"(r0), "=f"(r1)
+                  : "r"(p[j / 2]), "f"(__uint_as_float(u0)), "f"(__uint_as_float(u1)));
+              p[16 + j / 2] = pack2<true>(r0, r1);
             }
-            tmem_store32(s_at + c, p);
+            tmem_store32(s_at + 32 * c, p);
+            if ((c + 1) % (kC / 2) == 0) {  // half of the tile's products may begin
+              tmem_stored();
+              tc_before();
+              __syncwarp();
+              if (lane == 0) bar_arrive(p_full + (c + 1 == kC ? 8 : 0));
+            }
           }
-          l += sum0 + sum1;
-          tmem_stored();
+          uint32_t a0, a1, b0, b1;
+          split_pair(sums[0], a0, a1);
+          split_pair(sums[1], b0, b1);
+          l += (__uint_as_float(a0) + __uint_as_float(a1)) + (__uint_as_float(b0) + __uint_as_float(b1));
+        } else {
+          tc_before();
+          __syncwarp();
+          if (lane == 0) bar_arrive(p_full), bar_arrive(p_full + 8);
         }
-        const uint32_t slot = tile % C::kNV;
-        ok = ok && bar_wait(smem_addr(&sh.v_full[slot]), (tile / C::kNV) & 1);
-        if (*reinterpret_cast<volatile uint32_t*>(&sh.bad_tile[slot]) == tile + 1)
-          for (int key = max(0, lo - k0); key < min(KEYS, hi - k0); ++key) nan |= sh.bad[slot][key];
-        tc_before();
-        bar_arrive(p_full);
       }
-      if (it.tiles) {
+      if (it.tiles > i0) {
         ok = ok && bar_wait(o_done, o_phase);
         o_phase ^= 1;
+        const int last = i0 + (it.tiles - 1 - i0) / step * step;
+        check(tile + last, (it.tile + last) * KEYS, true);
       }
+      tile += it.tiles;
       __syncwarp();
       tc_after();
       if (!ok) sh.failed = 1, l = NAN;
       const bool final = it.begins && it.ends;
+      float f0 = 1.0f, f1 = 0.0f;
+      const bool second = twin && it.tiles > 1;  // the other group has sums of these rows
+      if (twin) {
+        if (t == 1) {
+          sh.twin_m[r] = m, sh.twin_l[r] = l, sh.twin_nan[r] = nan;
+          tc_before();
+          soft_sync(1);
+          soft_sync(2);
+          continue;
+        }
+        soft_sync(1);
+        tc_after();
+        if (second) {
+          const float om = sh.twin_m[r], to = fmaxf(m, om), less = to == -INFINITY ? 0.0f : to;
+          f0 = exp2_fast(m - less), f1 = exp2_fast(om - less);
+          l = fmaf(sh.twin_l[r], f1, l * f0);
+          m = to;
+          nan |= sh.twin_nan[r];
+        }
+      }
       const float inv = l == 0.0f ? 0.0f : 1.0f / l;
       const int64_t row = it.q.first + token;
       const int q_head = it.head * a.group + flat % a.group;
       float* part = a.parts + ((size_t)blockIdx.x * 2 + (it.begins ? 1 : 0)) * a.part_rows * (D + 2);
       if (busy) {
+        const float w0 = final ? f0 * inv : f0, w1 = final ? f1 * inv : f1;
 #pragma unroll 1
-        for (int c = 0; c < D; c += 32) {
-          uint32_t x[32];
-          if (it.tiles) {
-            tmem_load32(o_at + c, x);
-            tmem_wait(x);
-          } else {
+        for (int c = 0; c < D; c += 16) {
+          uint32_t o[16], o2[16];
 #pragma unroll
-            for (int j = 0; j < 32; ++j) x[j] = 0;
-          }
+          for (int j = 0; j < 16; ++j) o[j] = o2[j] = 0;
+          if (it.tiles) tmem_load16(o_at + c, o);
+          if (second) tmem_load16(o_at + D + c, o2);
+#pragma unroll
+          for (int j = 0; j < 16; ++j) o[j] = __float_as_uint(fmaf(__uint_as_float(o2[j]), w1, __uint_as_float(o[j]) * w0));
           if (nan >> (c / 32) & 1u) {
 #pragma unroll
-            for (int j = 0; j < 32; ++j) x[j] = 0x7FC00000u;
+            for (int j = 0; j < 16; ++j) o[j] = 0x7FC00000u;
           }
           if (mine && final) {
             uint4* to = reinterpret_cast<uint4*>(a.out + row * a.ldo + (int64_t)q_head * D + c);
 #pragma unroll
-            for (int j = 0; j < 32; j += 8) {
-              uint32_t o[4];
+            for (int j = 0; j < 16; j += 8) {
+              uint32_t h[4];
 #pragma unroll
-              for (int k = 0; k < 4; ++k)
-                o[k] = pack2<BF16>(__uint_as_float(x[j + 2 * k]) * inv, __uint_as_float(x[j + 2 * k + 1]) * inv);
-              to[j / 8] = make_uint4(o[0], o[1], o[2], o[3]);
+              for (int k = 0; k < 4; ++k) h[k] = pack2<BF16>(__uint_as_float(o[j + 2 * k]), __uint_as_float(o[j + 2 * k + 1]));
+              to[j / 8] = make_uint4(h[0], h[1], h[2], h[3]);
             }
           } else if (mine) {
-            uint4* to = reinterpret_cast<uint4*>(part + (size_t)(t * kRows + r) * D + c);
+            uint4* to = reinterpret_cast<uint4*>(part + (size_t)(above + r) * D + c);
 #pragma unroll
-            for (int j = 0; j < 32; j += 4) to[j / 4] = make_uint4(x[j], x[j + 1], x[j + 2], x[j + 3]);
+            for (int j = 0; j < 16; j += 4) to[j / 4] = make_uint4(o[j], o[j + 1], o[j + 2], o[j + 3]);
           }
           __syncwarp();
         }
         if (mine && final && a.lse)
           a.lse[row * (a.heads * a.group) + q_head] = l == 0.0f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
         if (mine && !final) {
-          part[(size_t)a.part_rows * D + t * kRows + r] = m;
-          part[(size_t)a.part_rows * (D + 1) + t * kRows + r] = l;
+          part[(size_t)a.part_rows * D + above + r] = m;
+          part[(size_t)a.part_rows * (D + 1) + above + r] = l;
         }
-        tc_before();  // the next item's sums go where these were
       }
+      tc_before();  // the next item's sums go where these were
+      if (twin) soft_sync(2);
     }
-  } else if (warp < C::kSoftWarps + 4) {
+  } else if (warp < C::kSoftWarps + kDecodeWarps) {
     // ----------------------------------------------------------- decode --
-    const int w = warp - C::kSoftWarps, dt = tid - C::kSoftWarps * 32;
-    constexpr int kRuns = KEYS / 64, kAhead = 32 / kRuns;  // runs of this warp in a tile, tiles whose pages a warp holds
-    uint32_t number = 0;  // items with tiles
+    if constexpr (C::kQ == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kDecodeRegs));
+    const int w = warp - C::kSoftWarps;
+    const uint32_t raw_k = smem_addr(&sh.raw_full[0][w]), raw_v = smem_addr(&sh.raw_full[1][w]);
+    const uint8_t* raw = s_raw + w * C::kRaw;
     while (items.next(it)) {
       if (!it.tiles) continue;
       const int end = keys_end(a, it.q, (it.row0 + it.rows - 1) / a.group), begin = keys_begin(a, it.q, it.row0 / a.group);
       int held = -1;
-      auto pages = [&](int i) {  // lane: run lane % kRuns of tile i + lane / kRuns
-        const int j = i + lane / kRuns, key = (it.tile + j) * KEYS + w * (KEYS / 4) + (lane % kRuns) * 16;
+      // This warp's place in 32 tiles from tile i on: lane has tile i + lane. In units of a warp's keys, -1 without a page.
+      auto look_up = [&](int i) {
+        const int key = (it.tile + i + lane) * KEYS + w * C::kWarpKeys, run = key & ~15;
         held = -1;
-        if (j < it.tiles && key < end && key + 16 > begin) {
+        if (i + lane < it.tiles && run < end && run + 16 > begin) {
           const int page = __ldg(a.table + (int64_t)it.seq * a.max_blocks + (key >> a.page_shift));
           if (page < 0 || page >= a.pages)
             flag_invalid(a.err);
           else
-            held = ((page * a.heads + it.head) << (a.page_shift - 4)) + ((key & ((1 << a.page_shift) - 1)) >> 4);
+            held = page;
         }
       };
-      pages(0);
-      KRegs<C> kr;
-      VRegs<C> vr;
-      auto run_of = [&](int i) {
-        return [&, i](int n) { return __shfl_sync(kAll, held, (i % kAhead) * kRuns + n); };
-      };
-      load_k<C>(a, kr, run_of(0));
-      load_v<C>(a, vr, run_of(0));
-      uint32_t on = __ballot_sync(kAll, held >= 0);  // runs with a page, of the tiles in `held`
-      if (number) ok = ok && bar_wait(smem_addr(&sh.q_free), (number - 1) & 1);
-      ++number;
-      // the queries: as they are (BF16), or as two terms (F16), times the scale's sign
-      constexpr int kUnits = D / 8;
-#pragma unroll 4
-      for (int n = dt; n < it.rows * kUnits; n += 128) {
-        const int row = n / kUnits, u = n % kUnits, flat = it.row0 + row, token = flat / a.group;
-        uint4 v = ld_cached16(a.q + (int64_t)(it.q.first + token) * a.ldq + (int64_t)(it.head * a.group + flat - token * a.group) * D + u * 8);
-        v.x = (v.x ^ a.flip) & a.keep, v.y = (v.y ^ a.flip) & a.keep, v.z = (v.z ^ a.flip) & a.keep, v.w = (v.w ^ a.flip) & a.keep;
-        uint8_t* to = s_q + (row / kRows) * C::kTerms * C::kQBytes + (u >> 3) * (kRows * 128) + (row % kRows) * 128 + (((u & 7) ^ (row & 7)) << 4);
-        if constexpr (BF16) {
-          *reinterpret_cast<uint4*>(to) = v;
-        } else {
-          float f[8];
-          unpack8<false>(v, f);
-          uint32_t hi[4], lo[4];
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            hi[k] = pack2<true>(f[2 * k], f[2 * k + 1]);
-            lo[k] = pack2<true>(f[2 * k] - bf16_lo(hi[k]), f[2 * k + 1] - bf16_hi(hi[k]));
+      auto page_of = [&](int i) { return __shfl_sync(kAll, held, i & 31); };
+      // The codes and scales of tile i, in the page `page`, of K (part 0) or V.
+      auto send = [&](int i, int page, int part, const uint8_t* codes, const uint8_t* scales, uint32_t bar) {
+        if (lane == 0) {
+          bar_expect(bar, page < 0 ? 0 : C::kCodes + C::kScales);
+          if (page >= 0) {
+            const int key = (it.tile + i) * KEYS + w * C::kWarpKeys;
+            const int64_t id = ((((int64_t)page * a.heads + it.head) << a.page_shift) + (key & ((1 << a.page_shift) - 1))) / C::kWarpKeys;
+            bulk_copy(smem_addr(raw) + part * C::kCodes, codes + id * C::kCodes, C::kCodes, bar);
+            bulk_copy(smem_addr(raw) + 2 * C::kCodes + part * C::kScales, scales + id * C::kScales, C::kScales, bar);
           }
-          *reinterpret_cast<uint4*>(to) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-          *reinterpret_cast<uint4*>(to + C::kQBytes) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
         }
-      }
-      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-      bar_arrive(smem_addr(&sh.q_full));
+      };
+      look_up(0);
+      int page_k = page_of(0), page_v = page_k;
+      send(0, page_k, 0, a.kc, a.ks, raw_k);
+      send(0, page_v, 1, a.vc, a.vs, raw_v);
+      auto filled = [&](uint64_t* bar) {  // what this warp wrote is for the tensor cores
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        __syncwarp();
+        if (lane == 0) bar_arrive(smem_addr(bar));
+      };
       for (int i = 0; i < it.tiles; ++i, ++tile) {
-        const uint32_t ks = tile % C::kNK, kn = tile / C::kNK, vs = tile % C::kNV, vn = tile / C::kNV;
-        if (kn) ok = ok && bar_wait(smem_addr(&sh.k_free[ks]), (kn - 1) & 1);
-        store_k<C>(s_k + ks * C::kTile, kr);
-        if (lane == 0) sh.valid[tile % kMeta][w] = (uint8_t)((on >> ((i % kAhead) * kRuns)) & ((1u << kRuns) - 1u));
-        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-        bar_arrive(smem_addr(&sh.k_full[ks]));
+        const uint32_t slot = tile % SLOTS, uses = tile / SLOTS;
         const bool more = i + 1 < it.tiles;
-        if (more && (i + 1) % kAhead == 0) {
-          pages(i + 1);
-          on = __ballot_sync(kAll, held >= 0);
+        ok = bar_wait(raw_k, tile & 1) && ok;  // (whatever was before: the copies have to end)
+        if (uses) ok = ok && bar_wait(smem_addr(&sh.k_free[slot]), (uses - 1) & 1);
+        __syncwarp();
+        decode_k<C>(s_k + slot * C::kTile, raw, page_k >= 0, w, a.flip, a.keep);
+        if (lane == 0) sh.valid[tile % kMeta][w] = page_k >= 0;
+        filled(&sh.k_full[slot]);  // (every lane has read the codes)
+        if (more) {
+          if (((i + 1) & 31) == 0) look_up(i + 1);
+          page_k = page_of(i + 1);
+          send(i + 1, page_k, 0, a.kc, a.ks, raw_k);
         }
-        if (more) load_k<C>(a, kr, run_of(i + 1));
-        if (vn) ok = ok && bar_wait(smem_addr(&sh.v_free[vs]), (vn - 1) & 1);
-        if (store_v<C>(s_v + vs * C::kTile, vr, sh.bad[vs])) sh.bad_tile[vs] = tile + 1;
-        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-        bar_arrive(smem_addr(&sh.v_full[vs]));
-        if (more) load_v<C>(a, vr, run_of(i + 1));
+        ok = bar_wait(raw_v, tile & 1) && ok;
+        if (uses) ok = ok && bar_wait(smem_addr(&sh.v_free[slot]), (uses - 1) & 1);
+        __syncwarp();
+        if (decode_v<C>(s_v + slot * C::kTile, raw, page_v >= 0, sh.bad[tile % kMeta], w)) sh.bad_tile[tile % kMeta] = tile + 1;
+        filled(&sh.v_full[slot]);
+        page_v = page_k;
+        if (more) send(i + 1, page_v, 1, a.vc, a.vs, raw_v);
       }
     }
-  } else if (lane == 0) {  // (the others wait at the end)
+  } else {
     // -------------------------------------------------------------- MMA --
-    // BF16 operands, FP32 sums; N / 8 at bit 17, M / 16 at bit 24; bit 16: B is dim-major
-    constexpr uint32_t kIdesc = (1u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(kRows / 16) << 24);
-    constexpr uint32_t kIdescS = kIdesc | ((uint32_t)(KEYS / 8) << 17), kIdescO = kIdesc | (1u << 16) | ((uint32_t)(D / 8) << 17);
-    // K-major, 128-byte swizzle, 1024 bytes from 8 rows to the next
-    constexpr uint64_t kDesc = ((uint64_t)1 << 16) | ((uint64_t)64 << 32) | ((uint64_t)1 << 46) | ((uint64_t)2 << 61);
-    // dim-major: from 64 dims to the next a tile's keys, 1024 bytes from 8 keys to the next
-    constexpr uint64_t kDescV = ((uint64_t)(KEYS * 128 / 16) << 16) | ((uint64_t)64 << 32) | ((uint64_t)1 << 46) | ((uint64_t)2 << 61);
-    const uint32_t q_at = smem_addr(s_q) >> 4, k_at = smem_addr(s_k) >> 4, v_at = smem_addr(s_v) >> 4;
-    auto product = [&](int t, uint32_t slot) {  // S of row tile t
+    if constexpr (C::kQ == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kMmaRegs));
+    const int w = warp - C::kSoftWarps - kDecodeWarps;
+    uint32_t number = 0;  // items with tiles
+    if (w == 0) {
+      // BF16 operands, FP32 sums; N / 8 at bit 17, M / 16 at bit 24; bit 16: B is dim-major
+      constexpr uint32_t kIdesc = (1u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(kRows / 16) << 24);
+      constexpr uint32_t kIdescS = kIdesc | ((uint32_t)(KEYS / 8) << 17), kIdescO = kIdesc | (1u << 16) | ((uint32_t)(D / 8) << 17);
+      // Descriptors, high words: 128-byte swizzle, 1024 bytes from 8 rows (keys) to the next. Low words: the address; K-major
+      // 1, dim-major the bytes from 64 dims to the next, a tile's keys.
+      constexpr uint32_t kHigh = 64u | 1u << 14 | 2u << 29;
+      constexpr uint32_t kLow = 1u << 16, kLowV = (uint32_t)(KEYS * 128 / 16) << 16;
+      const uint32_t q_at = kLow + (smem_addr(s_q) >> 4), k_at = kLow + (smem_addr(s_k) >> 4), v_at = kLowV + (smem_addr(s_v) >> 4);
+      auto product = [&](int t, int row_tile, uint32_t slot) {  // S of group t
+        const uint32_t s = tmem + t * KEYS, q = q_at + row_tile * (C::kTerms * C::kQBytes / 16), k = k_at + slot * (C::kTile / 16);
+        if (elected()) {
 #pragma unroll
-      for (int term = 0; term < C::kTerms; ++term)
+          for (int term = 0; term < C::kTerms; ++term)
 #pragma unroll
-        for (int j = 0; j < D / 16; ++j) {
-          const uint32_t in = (j % 4) * 2;
-          mma_ss(tmem + t * KEYS,
-                 kDesc | (q_at + (uint32_t)((t * C::kTerms + term) * C::kQBytes + (j / 4) * kRows * 128) / 16 + in),
-                 kDesc | (k_at + (slot * C::kTile + (uint32_t)(j / 4) * KEYS * 128) / 16 + in), kIdescS, term + j > 0);
+            for (int j = 0; j < D / 16; ++j)
+              mma_ss<kHigh, kHigh, kIdescS>(s, q + (uint32_t)(term * C::kQBytes + (j / 4) * kRows * 128) / 16 + (j % 4) * 2,
+                                            k + (uint32_t)(j / 4) * (KEYS * 128 / 16) + (j % 4) * 2, term + j > 0);
         }
-    };
-    auto values = [&](int t, uint32_t slot, bool first) {  // its sums
+        __syncwarp();
+      };
+      auto values = [&](int t, uint32_t slot, int half, bool first) {  // its sums, of half of the tile's keys
+        const uint32_t o = tmem + C::kQ * KEYS + t * D, p = tmem + t * KEYS + half * (KEYS / 2),
+                       v = v_at + slot * (C::kTile / 16) + half * (KEYS / 32 * 128);
+        if (elected()) {
 #pragma unroll
-      for (int j = 0; j < KEYS / 16; ++j)
+          for (int j = 0; j < KEYS / 32; ++j)
 #pragma unroll
-        for (int term = 0; term < 2; ++term)
-          mma_ts(tmem + C::kQ * KEYS + t * D, tmem + t * KEYS + (j / 2) * 32 + term * 16 + (j % 2) * 8,
-                 kDescV | (v_at + (slot * C::kTile + (uint32_t)j * 2048) / 16), kIdescO, !first || j + term > 0);
-    };
-    uint32_t number = 0, p_phase[C::kQ] = {};
-    while (items.next(it)) {
-      if (!it.tiles) continue;
-      ok = ok && bar_wait(smem_addr(&sh.q_full), number & 1);
-      ++number;
-      ok = ok && bar_wait(smem_addr(&sh.k_full[tile % C::kNK]), (tile / C::kNK) & 1);
-      tc_after();
-#pragma unroll
-      for (int t = 0; t < C::kQ; ++t)
-        if (it.rows > t * kRows) {
-          product(t, tile % C::kNK);
-          tc_commit(smem_addr(&sh.s_full[t]));
+            for (int term = 0; term < 2; ++term)
+              mma_ts<kHigh, kIdescO>(o, p + (j / 2) * 32 + term * 16 + (j % 2) * 8, v + j * 128, !first || j + term > 0);
         }
-      tc_commit(smem_addr(&sh.k_free[tile % C::kNK]));
-      if (it.tiles == 1) tc_commit(smem_addr(&sh.q_free));
-      for (int i = 0; i < it.tiles; ++i, ++tile) {
-        const bool more = i + 1 < it.tiles;
-        const uint32_t vs = tile % C::kNV, ks = (tile + 1) % C::kNK;
-        ok = ok && bar_wait(smem_addr(&sh.v_full[vs]), (tile / C::kNV) & 1);
-        if (more) ok = ok && bar_wait(smem_addr(&sh.k_full[ks]), ((tile + 1) / C::kNK) & 1);
-#pragma unroll
-        for (int t = 0; t < C::kQ; ++t)
-          if (it.rows > t * kRows) {
-            ok = ok && bar_wait(smem_addr(&sh.p_full[t]), p_phase[t]);
-            p_phase[t] ^= 1;
-            tc_after();
-            values(t, vs, i == 0);
-            if (more) {
-              product(t, ks);
-              tc_commit(smem_addr(&sh.s_full[t]));
-            } else {
-              tc_commit(smem_addr(&sh.o_done[t]));
+        __syncwarp();
+      };
+      auto commit = [&](uint64_t* bar) {
+        if (elected()) tc_commit(smem_addr(bar));
+        __syncwarp();
+      };
+      uint32_t p_phase = 0;  // a bit per group
+      auto await_k = [&](uint32_t n) {
+        ok = ok && bar_wait(smem_addr(&sh.k_full[n % SLOTS]), (n / SLOTS) & 1);
+        __syncwarp();
+        tc_after();
+      };
+      auto await_v = [&](uint32_t n) { ok = ok && bar_wait(smem_addr(&sh.v_full[n % SLOTS]), (n / SLOTS) & 1); };
+      auto sums = [&](int t, uint32_t n, bool first) {  // group t's of tile n
+#pragma unroll 1
+        for (int half = 0; half < 2; ++half) {
+          ok = ok && bar_wait(smem_addr(&sh.p_full[t][half]), p_phase >> t & 1u);
+          __syncwarp();
+          tc_after();
+          values(t, n % SLOTS, half, first && half == 0);
+        }
+        p_phase ^= 1u << t;
+      };
+      while (items.next(it)) {
+        if (!it.tiles) continue;
+        ok = ok && bar_wait(smem_addr(&sh.q_full), number & 1);
+        ++number;
+        const int n = it.tiles;
+        const bool twin = C::kQ == 2 && it.rows <= kRows;
+        // Step i: for the pair of row tiles the products of key tile i behind the sums of i - 1; for the twins those of i behind
+        // the sums of i - 2, which have the same columns.
+        const int behind = twin ? 2 : 1;
+#pragma unroll 1
+        for (int i = 0; i < n + behind; ++i) {
+          const bool back = i >= behind, ahead = i < n;
+          const uint32_t old = tile + i - behind, now = tile + i;
+          if (!back && !ahead) continue;  // (one tile, twins: there is no second)
+          if (back) await_v(old);
+          if (ahead && !back) await_k(now);
+#pragma unroll 1
+          for (int t = twin ? i & 1 : 0; t < (twin ? (i & 1) + 1 : C::kQ); ++t) {
+            if (back) sums(t, old, i < 2 * behind);
+            // (before the wait for K: with one slot the values behind it wait for this)
+            if (back && (twin || t + 1 == C::kQ)) commit(&sh.v_free[old % SLOTS]);
+            if (ahead) {
+              if (back) await_k(now);
+              product(t, twin ? 0 : t, now % SLOTS);
             }
+            commit(ahead ? &sh.s_full[t] : &sh.o_done[t]);
           }
-        tc_commit(smem_addr(&sh.v_free[vs]));
-        if (more) tc_commit(smem_addr(&sh.k_free[ks]));
-        if (i + 2 == it.tiles) tc_commit(smem_addr(&sh.q_free));
+          if (ahead) commit(&sh.k_free[now % SLOTS]);
+          if (i + 1 == n) commit(&sh.q_free);
+        }
+        tile += n;
+      }
+      commit(&sh.drained);
+      ok = ok && bar_wait(smem_addr(&sh.drained), 0);
+      if (!ok) sh.failed = 1;
+    } else {
+      // --------------------------------------------------------- queries --
+      // As they are (BF16), or as two terms (F16). A warp has whole rows, D / 8 lanes each.
+      constexpr int kUnits = D / 8, kAtOnce = 32 / kUnits, kStep = kQueryWarps * kAtOnce;
+      const int u = lane % kUnits;
+      while (items.next(it)) {
+        if (!it.tiles) continue;
+        if (number) ok = ok && bar_wait(smem_addr(&sh.q_free), (number - 1) & 1);
+        ++number;
+        int row = (w - 1) * kAtOnce + lane / kUnits, token = (it.row0 + row) / a.group, head = it.row0 + row - token * a.group;
+        const uint16_t* q = a.q + (int64_t)it.q.first * a.ldq + (int64_t)it.head * a.group * D + u * 8;
+        uint8_t* const to0 = s_q + (u >> 3) * (kRows * 128);
+        auto place = [&](int r) {
+          return to0 + (r / kRows) * C::kTerms * C::kQBytes + (r % kRows) * 128 + (((u & 7) ^ (r & 7)) << 4);
+        };
+        const int first_row = row;
+        for (; row < it.rows; row += kStep) {
+          const uint32_t to = smem_addr(place(row));
+          asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(q + (int64_t)token * a.ldq + head * D) : "memory");
+          head += kStep;
+          while (head >= a.group) head -= a.group, ++token;
+        }
+        asm volatile("cp.async.wait_all;" ::: "memory");
+        if constexpr (!BF16) {
+          for (row = first_row; row < it.rows; row += kStep) {
+            uint8_t* to = place(row);
+            float f[8];
+            unpack8<false>(*reinterpret_cast<const uint4*>(to), f);
+            uint32_t hi[4], lo[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              hi[j] = pack2<true>(f[2 * j], f[2 * j + 1]);
+              lo[j] = pack2<true>(f[2 * j] - bf16_lo(hi[j]), f[2 * j + 1] - bf16_hi(hi[j]));
+            }
+            *reinterpret_cast<uint4*>(to) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+            *reinterpret_cast<uint4*>(to + C::kQBytes) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+          }
+        }
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        __syncwarp();
+        if (lane == 0) bar_arrive(smem_addr(&sh.q_full));
       }
     }
-    tc_commit(smem_addr(&sh.drained));
-    ok = ok && bar_wait(smem_addr(&sh.drained), 0);
-    if (!ok) sh.failed = 1;
   }
   __syncwarp();
   __syncthreads();
@@ -985,7 +1132,6 @@ __global__ void __launch_bounds__(kThreads) kv4_chunk_join_kernel(const ChunkArg
 
 // ---------------------------------------------------------------- launch --
 
-constexpr int kMostCtas = 2;      // per SM
 constexpr int kMostItemRows = 256;
 
 // Rows of a part, whose sums are 16-byte words.
@@ -997,11 +1143,18 @@ moe_status launch(ChunkArgs a, cudaStream_t st) {
   static SmemOnce once;
   moe_status rc = once.allow(k, C::kSmem);
   if (rc != MOE_OK) return rc;
+  if (C::kQ == 2) {  // what setmaxnreg shares out has to be there, or its increase would wait for ever
+    static const int regs = [&] {
+      cudaFuncAttributes attr = {};
+      return cudaFuncGetAttributes(&attr, k) == cudaSuccess ? attr.numRegs : 0;
+    }();
+    if (regs * C::kThreadsAll < C::kRegs) return refuse(MOE_ERR_UNSUPPORTED, "wd_kv4_attend_chunk: built with too few registers");
+  }
   // items at most, and units of one at most
   const int64_t items = ((int64_t)a.T * a.group / C::kItemRows + a.S) * a.heads;
   const int64_t seen = (int64_t)a.window + C::kItemRows + 2 * C::kKeys;
   const int64_t most = a.window > 0 && seen < a.room ? seen : a.room, units = (most + C::kKeys - 1) / C::kKeys;
-  const int64_t fill = (int64_t)sm_count() * C::kCtas;
+  const int64_t fill = (int64_t)sm_count();  // a CTA has an SM's shared memory
   const unsigned grid = (unsigned)(items < fill && items * (units + kItemUnits) < fill ? items * (units + kItemUnits) : fill);
   k<<<grid, C::kThreadsAll, C::kSmem, st>>>(a);
   rc = launched("wd_kv4_attend_chunk launch");
@@ -1029,7 +1182,7 @@ moe_status launch(ChunkArgs a, cudaStream_t st) {
 extern "C" size_t wd_kv4_attend_chunk_workspace(const wd_kv4_cache* c, int32_t T, int32_t q_heads) {
   using namespace wd;
   if (!c || wd_kv4_cache_bytes(c, WD_KV4_CODES) == 0 || T < 0 || q_heads < 1 || q_heads % c->heads) return 0;
-  const int64_t rows = part_rows_of(T, q_heads / c->heads), grid = (int64_t)sm_count() * kMostCtas;
+  const int64_t rows = part_rows_of(T, q_heads / c->heads), grid = (int64_t)sm_count();
   return (size_t)(grid * sizeof(Split) + grid * 2 * rows * (c->dim + 2) * 4);
 }
 
@@ -1070,21 +1223,14 @@ extern "C" moe_status wd_kv4_attend_chunk(const wd_kv4_cache* c, const void* q, 
   a.scale_log2 = z == 0.0f ? 1.0f : std::fabs(z);
   a.flip = std::signbit(z) ? 0x80008000u : 0u;
   a.keep = z == 0.0f ? 0u : ~0u;
-  const int64_t grid = (int64_t)sm_count() * kMostCtas;
+  const int64_t grid = (int64_t)sm_count();
   a.split = static_cast<Split*>(workspace);
   a.parts = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + grid * sizeof(Split));
   a.part_rows = (int32_t)part_rows_of(T, a.group);
   cudaStream_t st = (cudaStream_t)stream;
   const bool bf16 = type == WD_BF16;
-  // <dim, keys of a tile, row tiles, terms of a query, slots of K, of V, CTAs per SM>
-  const bool deep = (int64_t)T * a.group > (int64_t)S * kRows;  // more than one row tile per sequence
-  if (c->dim == 64) {
-    if (deep) return bf16 ? launch<Config<64, 128, 2, 1, 2, 2, 1>, true>(a, st) : launch<Config<64, 128, 2, 2, 2, 2, 1>, false>(a, st);
-    return bf16 ? launch<Config<64, 128, 1, 1, 2, 2, 2>, true>(a, st) : launch<Config<64, 128, 1, 2, 2, 2, 2>, false>(a, st);
-  }
-  if (c->dim == 128) {
-    if (deep) return bf16 ? launch<Config<128, 128, 2, 1, 2, 2, 1>, true>(a, st) : launch<Config<128, 128, 2, 2, 1, 1, 1>, false>(a, st);
-    return bf16 ? launch<Config<128, 128, 1, 1, 1, 1, 2>, true>(a, st) : launch<Config<128, 64, 1, 2, 1, 1, 2>, false>(a, st);
-  }
-  return bf16 ? launch<Config<256, 64, 1, 1, 2, 2, 1>, true>(a, st) : launch<Config<256, 64, 1, 2, 1, 1, 1>, false>(a, st);
+  // <dim, keys of a tile, row tiles, terms of a query>
+  if (c->dim == 64) return bf16 ? launch<Config<64, 128, 2, 1>, true>(a, st) : launch<Config<64, 128, 2, 2>, false>(a, st);
+  if (c->dim == 128) return bf16 ? launch<Config<128, 128, 2, 1>, true>(a, st) : launch<Config<128, 128, 2, 2>, false>(a, st);
+  return bf16 ? launch<Config<256, 64, 1, 1>, true>(a, st) : launch<Config<256, 64, 1, 2>, false>(a, st);
 }
