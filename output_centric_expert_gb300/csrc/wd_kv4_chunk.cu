@@ -6,10 +6,13 @@
 // 2^(z_j - m) v_j; partial results join as l = sum l_i 2^(m_i - m), acc likewise. m follows
 // the row's maximum only when that is more than 2^kSlack above it, so acc is hardly ever
 // rescaled.
-//   S = Q K^T and acc += P V: tcgen05.mma kind::f16 with BF16 operands, 128 rows. K and V are
-//   decoded to BF16, which holds every E2M1 code times every E8M0 scale up to 6 * 2^125
-//   exactly; so are queries (F16: as two BF16 terms). P is two BF16 terms, the second what
-//   the cut of the first left: 16 bits, and FP32's range of exponents, as in wd_kv4_attend.
+//   S = Q K^T: tcgen05.mma kind::f16, 128 rows, f16 operands. Queries are f16 times a power of
+//   two per row, as in wd_kv4_attend. Keys are E2M1 times 2^(s - 127 + 4), which f16 holds
+//   exactly for scale codes s from 109 to 136 (and zero blocks); keys with others get a power of
+//   two of their own, by which their column of S is multiplied.
+//   acc += P V: BF16 operands. V is decoded to BF16, which holds every E2M1 code times every E8M0
+//   scale up to 6 * 2^125 exactly. P is two BF16 terms, the second what the cut of the first
+//   left: 16 bits, and FP32's range of exponents, as in wd_kv4_attend.
 //
 // Work. A CTA has kQ tiles of 128 rows against tiles of kKeys keys. Its warps:
 //   4 per row tile   softmax: a thread has a row. S comes from tensor memory, P goes back in
@@ -25,6 +28,7 @@
 #include <cmath>
 
 #include "wd_block.cuh"
+#include "wd_fp4.h"
 #include "wd_kv4.cuh"
 
 namespace wd {
@@ -33,6 +37,7 @@ namespace {
 constexpr unsigned kAll = 0xFFFFFFFFu;
 constexpr float kSlack = 8.0f;
 constexpr int kRows = 128;       // of a row tile
+constexpr int kPiece = 64;       // keys that are in the softmax at a time
 constexpr int kItemUnits = 2;    // what an item costs beside its key tiles, in tiles
 constexpr int kMinUnits = 3;     // of a CTA, on average, unless it has an item to itself
 constexpr uint32_t kWaitLimit = 1u << 20;
@@ -61,27 +66,26 @@ struct ChunkArgs {
   int64_t ldq, ldo;
   int32_t T, S, max_blocks, pages, page_shift, heads, group, window, room;  // room: keys of a row of the table
   int32_t part_rows;
-  float scale_log2;  // positive
-  uint32_t flip;     // what the factors of K are xored with: the scale's sign
-  uint32_t keep;     // and then masked: 0 for a scale of 0
+  float scale_log2;
 };
 
-template <int D_, int KEYS, int Q, int TERMS>
+template <int D_, int KEYS, int Q>
 struct Config {
-  static constexpr int D = D_, kKeys = KEYS, kQ = Q, kTerms = TERMS;
-  static constexpr int kSlots = TERMS == 2 && D_ >= 128 ? 1 : 2;  // of K, and of V
+  static constexpr int D = D_, kKeys = KEYS, kQ = Q;
+  static constexpr int kSlots = 2;  // of K, and of V
   static constexpr int kItemRows = Q * kRows;
   static constexpr int kSoftWarps = 4 * Q, kThreadsAll = (kSoftWarps + kDecodeWarps + 4) * 32;
   static constexpr int kWarpKeys = KEYS / kDecodeWarps;  // keys of a decode warp in a tile: 8 or 16, inside a run of 16
-  static constexpr int kQBytes = kRows * D * 2;          // of a term of a row tile
+  static constexpr int kQBytes = kRows * D * 2;          // of a row tile
   static constexpr int kTile = KEYS * D * 2;             // of K or V
   static constexpr int kCodes = kWarpKeys * D / 2, kScales = kWarpKeys * D / 32;  // bytes of a decode warp's keys, K or V
   static constexpr int kRaw = 2 * (kCodes + kScales);    // codes of K, of V, scales of K, of V
-  static constexpr int kSmem = 1024 + Q * TERMS * kQBytes + 2 * kSlots * kTile + kDecodeWarps * kRaw;
-  static constexpr int kCols = Q * (KEYS + D);
+  static constexpr int kSmem = 1024 + Q * kQBytes + 2 * kSlots * kTile + kDecodeWarps * kRaw;
+  static constexpr int kPieces = KEYS / kPiece;          // of a tile
+  static constexpr int kCols = Q * (2 * kPiece + D);     // two pieces' S and the sums of each row tile
   static constexpr int kTmem = kCols <= 256 ? 256 : 512;
   // registers of a thread: setmaxnreg shares out what the launch has
-  static constexpr int kSoftRegs = 160, kDecodeRegs = 56, kMmaRegs = 48;
+  static constexpr int kSoftRegs = 112, kDecodeRegs = 80, kMmaRegs = 96;
   static constexpr int kRegs = 32 * (kSoftWarps * kSoftRegs + kDecodeWarps * kDecodeRegs + 4 * kMmaRegs);
   static_assert(kCols <= 512 && kSmem <= 221 * 1024, "fits an SM");
 };
@@ -313,7 +317,7 @@ __device__ __forceinline__ int cta_of(int64_t total, int ctas, int64_t unit) {
 struct Item {
   Seq q;
   int32_t seq, head, row0, rows;   // rows: of this block
-  int32_t tile, tiles;             // its key tiles
+  int32_t tile, tiles, pieces;     // its key tiles, and their pieces of 64 keys up to the last that is seen
   bool begins, ends;               // with the item's first tile, its last
   int64_t unit0;                   // the item's first unit of all
   int32_t all;                     // units of the whole item
@@ -350,6 +354,8 @@ struct Items {
       it.q = q, it.seq = s, it.head = h, it.row0 = b * C::kItemRows;
       it.rows = min(C::kItemRows, q.tokens * a.group - it.row0);
       it.tile = kt0 + first, it.tiles = last - first;
+      const int seen = keys_end(a, q, (it.row0 + it.rows - 1) / a.group) - it.tile * C::kKeys;
+      it.pieces = min(it.tiles * C::kPieces, (seen + kPiece - 1) / kPiece);
       it.begins = first == 0, it.ends = last == n;
       it.unit0 = unit - off, it.all = per;
       unit += take;
@@ -451,6 +457,9 @@ __device__ void find_share(const ChunkArgs& a, int64_t* s_units, int64_t* s_warp
 __device__ __forceinline__ uint32_t first_factor(uint32_t s) { return (min(s, 128u) + 126u) * 0x800080u; }
 __device__ __forceinline__ uint32_t second_factor(uint32_t s) { return s <= 128u ? 0x3F803F80u : (s - 1u) * 0x800080u; }
 
+constexpr int kLow = 108, kHigh = 136;  // scale codes of K in (kLow, kHigh] are the f16 exponents 1 .. 28
+constexpr float kUnit = 0.0625f;        // a key is its f16 values times this: 2^(kLow + 1 - 127) = 2^-14 * 2^-4
+
 // The codes in two bytes of (w << 4, w) that `sel` names (each byte, then it with its top bit repeated) as BF16
 // times 2^-126: E2M1's exponent and mantissa are the lowest bits of BF16's exponent and the highest of its
 // mantissa; its 0.5 becomes the subnormal 2^-127.
@@ -481,12 +490,38 @@ __device__ __forceinline__ void read_words(const uint8_t* p, uint32_t (&w)[WORDS
 // half of the blocks) one pair and the words of g = 2u, 2u + 1. With that t the 8 lanes that read or write 16 bytes
 // together meet all banks, in the cache's order on one side and the 128-byte swizzle on the other.
 
-// K as it is in the tile: [D / 64][keys][128 bytes], 16-byte unit u of a row at u ^ (row & 7). here: the keys have a page.
+__device__ __forceinline__ uint32_t mul2_f16(uint32_t a, uint32_t b) {
+  const __half2 r = __hmul2(*reinterpret_cast<const __half2*>(&a), *reinterpret_cast<const __half2*>(&b));
+  return *reinterpret_cast<const uint32_t*>(&r);
+}
+
+// A key whose scale codes f16 does not take as they are: its blocks relative to its largest scale, and the power of two
+// that its column of S is multiplied by. A block 2^-36 below that is 0.
 template <typename C>
-__device__ __forceinline__ void decode_k(uint8_t* tile, const uint8_t* raw, bool here, int warp, uint32_t flip, uint32_t keep) {
+__device__ __noinline__ float wide_key(uint8_t* row, const uint8_t* codes, const uint8_t* scales, int t, int k) {
+  constexpr int NB = C::D / 32;
+  int top = 0;
+#pragma unroll 1
+  for (int b = 0; b < NB; ++b) top = max(top, (int)scales[b]);
+#pragma unroll 1
+  for (int b = 0; b < NB; ++b) {
+    const uint32_t f = __half_as_ushort(__float2half_rn(exp2i(max(-126, (int)scales[b] - top + 12)))) * 0x10001u;
+    uint32_t e[4];
+    e2m1x8_to_f16(*reinterpret_cast<const uint32_t*>(codes + 4 * b), e);
+    *reinterpret_cast<uint4*>(row + (b >> 1) * (C::kKeys * 128) + ((((b & 1) * 4 + t) ^ k) << 4)) =
+        make_uint4(mul2_f16(e[0], f), mul2_f16(e[1], f), mul2_f16(e[2], f), mul2_f16(e[3], f));
+  }
+  return top == 255 ? NAN : ldexpf(1.0f, top - 127 - 12 + 4);
+}
+
+// K as it is in the tile: [D / 64][keys][128 bytes], 16-byte unit u of a row at u ^ (row & 7), f16. here: the keys have
+// a page. factors: of the tile's columns of S. Returns whether any of this warp's is not 1.
+template <typename C>
+__device__ __forceinline__ bool decode_k(uint8_t* tile, const uint8_t* raw, bool here, int warp, float* factors) {
   constexpr int D = C::D, NB = D / 32;
   const int lane = threadIdx.x & 31, k = lane & 7, t = (lane >> 3) ^ (k >> 1);
-#pragma unroll 1
+  bool wide = false;
+#pragma unroll
   for (int i = 0; i < C::kWarpKeys / 8; ++i) {
     const int key = 8 * i + k;
     uint32_t w[NB], sc[(NB + 3) / 4];
@@ -497,34 +532,32 @@ __device__ __forceinline__ void decode_k(uint8_t* tile, const uint8_t* raw, bool
     else
       read_words<NB / 4>(scales, sc);
     uint8_t* row = tile + (warp * C::kWarpKeys + key) * 128;
-    auto put = [&](int b, const uint32_t(&e)[4]) {
-      *reinterpret_cast<uint4*>(row + (b >> 1) * (C::kKeys * 128) + ((((b & 1) * 4 + t) ^ k) << 4)) = make_uint4(e[0], e[1], e[2], e[3]);
-    };
-    uint32_t big = 0;
+    uint32_t least = 0xFFFFFFFFu, most = 0;  // of codes less one (so that 0 is none), and of codes, in pairs
 #pragma unroll
-    for (int j = 0; j < (NB + 3) / 4; ++j) big |= __vmaxu4(sc[j], 0x80808080u) ^ 0x80808080u;
-    if (!here) keep = 0;
-    if (!big || !here) {
+    for (int j = 0; j < (NB + 3) / 4; ++j) {
+      // exponents of f16 in pairs of blocks (0, 2), (1, 3); 0 for what is below
+      const uint32_t even = sc[j] & 0x00FF00FFu, odd = sc[j] >> 8 & 0x00FF00FFu;
+      least = __viaddmin_u16x2(even, 0xFFFFFFFFu, least);
+      least = __viaddmin_u16x2(odd, 0xFFFFFFFFu, least);
+      most = __vmaxu2(__vmaxu2(even, odd), most);
+      constexpr uint32_t kLess = (uint32_t)(0x10000 - kLow) * 0x10001u;
+      const uint32_t e02 = here ? __viaddmax_s16x2(even, kLess, 0u) << 10 : 0u, e13 = here ? __viaddmax_s16x2(odd, kLess, 0u) << 10 : 0u;
 #pragma unroll
-      for (int b = 0; b < NB; ++b) {
-        const uint32_t s = (sc[b / 4] >> (8 * (b & 3))) & 255u, up = w[b] << 4, f = (((s + 126u) * 0x800080u) ^ flip) & keep;
+      for (int b = 0; b < 4 && 4 * j + b < NB; ++b) {
+        const uint32_t f = __byte_perm(b & 1 ? e13 : e02, 0, b & 2 ? 0x3232 : 0x1010);
         uint32_t e[4];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) e[j] = mul2_bf16(e2m1_pair(up, w[b], 0xC480 + 0x1111 * j), f);
-        put(b, e);
-      }
-    } else {
-#pragma unroll 1
-      for (int b = 0; b < NB; ++b) {
-        const uint32_t s = scales[b], x = *reinterpret_cast<const uint32_t*>(raw + key * (D / 2) + t * (D / 8) + 4 * b), up = x << 4;
-        const uint32_t f = s == 255u ? 0x7FC07FC0u : (first_factor(s) ^ flip) & keep, g = second_factor(s);
-        uint32_t e[4];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) e[j] = mul2_bf16(mul2_bf16(e2m1_pair(up, x, 0xC480 + 0x1111 * j), f), g);
-        put(b, e);
+        e2m1x8_to_f16(w[4 * j + b], e);
+        *reinterpret_cast<uint4*>(row + ((4 * j + b) >> 1) * (C::kKeys * 128) + ((((b & 1) * 4 + t) ^ k) << 4)) =
+            make_uint4(mul2_f16(e[0], f), mul2_f16(e[1], f), mul2_f16(e[2], f), mul2_f16(e[3], f));
       }
     }
+    const bool mine = here && (min(least & 0xFFFFu, least >> 16) < kLow || max(most & 0xFFFFu, most >> 16) > kHigh);
+    float f = 1.0f;
+    if (mine) f = wide_key<C>(row, raw + key * (D / 2) + t * (D / 8), scales, t, k);
+    if (lane < 8) factors[warp * C::kWarpKeys + 8 * i + k] = f;
+    wide |= mine;
   }
+  return __any_sync(kAll, wide);
 }
 
 // V as it is in the tile: [D / 64][keys][128 bytes] too. Blocks of NaN, or past BF16's range, become 0 and are noted in
@@ -591,12 +624,14 @@ __device__ __forceinline__ bool decode_v(uint8_t* tile, const uint8_t* raw, bool
 template <typename C>
 struct Shared {  // beside the operands
   uint64_t q_full, q_free, k_full[C::kSlots], k_free[C::kSlots], v_full[C::kSlots], v_free[C::kSlots];
-  uint64_t s_full[C::kQ], p_full[C::kQ][2], o_done[C::kQ], raw_full[2][kDecodeWarps], drained;  // (raw: K, V)
+  uint64_t s_full[C::kQ][2], p_full[C::kQ][2], o_done[C::kQ][2], raw_full[2][kDecodeWarps], drained;  // (raw: K, V)
   int64_t units[kSeqChunk], warp[C::kThreadsAll / 32];
   Share share;
   uint32_t tmem, failed;
   uint32_t bad_tile[kMeta];                        // number + 1 of the last tile in this place with bad blocks of V
-  __align__(8) uint8_t valid[kMeta][kDecodeWarps];  // whether a decode warp's keys have a page
+  __align__(8) uint8_t valid[kMeta][kDecodeWarps];  // a decode warp's keys: 1 with a page, 3 with factors besides
+  __align__(16) float factors[kMeta][C::kKeys];     // of the columns of S
+  float back[2][C::kItemRows];                      // 1 / the power of two of a row's queries, for two items in turn
   __align__(4) uint8_t bad[kMeta][C::kKeys];       // blocks of V that are NaN
   float twin_m[kRows], twin_l[kRows];              // a second row tile's, where both have the same rows
   uint32_t twin_nan[kRows];
@@ -608,8 +643,8 @@ __global__ void __launch_bounds__(C::kThreadsAll, 1) kv4_chunk_kernel(const Chun
   extern __shared__ uint4 dyn4[];
   __shared__ Shared<C> sh;
   uint8_t* base = reinterpret_cast<uint8_t*>(dyn4) + (1024 - (smem_addr(dyn4) & 1023)) % 1024;
-  uint8_t* const s_q = base;                                    // [row tile][term][D / 64][128][128 bytes]
-  uint8_t* const s_k = s_q + C::kQ * C::kTerms * C::kQBytes;    // [slot][tile]
+  uint8_t* const s_q = base;                                    // [row tile][D / 64][128][128 bytes]
+  uint8_t* const s_k = s_q + C::kQ * C::kQBytes;    // [slot][tile]
   uint8_t* const s_v = s_k + SLOTS * C::kTile;
   uint8_t* const s_raw = s_v + SLOTS * C::kTile;                // [decode warp]
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -628,8 +663,7 @@ __global__ void __launch_bounds__(C::kThreadsAll, 1) kv4_chunk_kernel(const Chun
     }
     for (int i = 0; i < kMeta; ++i) sh.bad_tile[i] = 0;
     for (int i = 0; i < C::kQ; ++i) {
-      bar_init(smem_addr(&sh.s_full[i]), 1), bar_init(smem_addr(&sh.p_full[i][0]), 4), bar_init(smem_addr(&sh.p_full[i][1]), 4);
-      bar_init(smem_addr(&sh.o_done[i]), 1);
+      for (int j = 0; j < 2; ++j) bar_init(smem_addr(&sh.s_full[i][j]), 1), bar_init(smem_addr(&sh.p_full[i][j]), 4), bar_init(smem_addr(&sh.o_done[i][j]), 1);
     }
     for (int i = 0; i < 2 * kDecodeWarps; ++i) bar_init(smem_addr(&sh.raw_full[0][0]) + 8 * i, 1);
     bar_init(smem_addr(&sh.drained), 1);
@@ -651,9 +685,13 @@ __global__ void __launch_bounds__(C::kThreadsAll, 1) kv4_chunk_kernel(const Chun
     if constexpr (C::kQ == 2) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::kSoftRegs));
     const int t = warp >> 2, r = tid & 127;
     const uint32_t lanes = (uint32_t)(warp & 3) << 21;
-    const uint32_t s_at = tmem + lanes + t * KEYS, o_at = tmem + lanes + C::kQ * KEYS + t * D;
-    const uint32_t s_full = smem_addr(&sh.s_full[t]), p_full = smem_addr(&sh.p_full[t][0]), o_done = smem_addr(&sh.o_done[t]);
-    uint32_t s_phase = 0, o_phase = 0;
+    const uint32_t s_at = tmem + lanes + t * 2 * kPiece, o_at = tmem + lanes + C::kQ * 2 * kPiece + t * D;
+    const uint32_t s_full = smem_addr(&sh.s_full[t][0]), p_full = smem_addr(&sh.p_full[t][0]), o_done = smem_addr(&sh.o_done[t][0]);
+    uint32_t s_phase = 0, number = 0;  // a bit per buffer; items with tiles
+    uint32_t taken = 0;                // a bit per buffer: whether its pieces so far are an odd number
+    // The sums of every piece given so far in a buffer. (s_full of a buffer's next piece says that the one before is done,
+    // so at most one phase is open.)
+    auto summed = [&](int buffer) { ok = ok && bar_wait(o_done + 8 * buffer, ~(taken >> buffer) & 1u); };
     if (tid == 0) a.split[blockIdx.x] = Split{};
     while (items.next(it)) {
       if (tid == 0) {
@@ -674,94 +712,122 @@ __global__ void __launch_bounds__(C::kThreadsAll, 1) kv4_chunk_kernel(const Chun
       // keys that all rows of the group see
       const int all_lo = keys_begin(a, it.q, (it.row0 + above + min(rows, kRows) - 1) / a.group);
       const int all_hi = keys_end(a, it.q, (it.row0 + above) / a.group);
-      float m = -INFINITY, l = 0.0f, raw = 0.0f;  // m = raw * scale, rounded
+      float m = -INFINITY, l = 0.0f, raw = 0.0f, scale = 0.0f;  // m = raw * scale, rounded
       uint32_t nan = 0;
-      const int step = twin ? 2 : 1, i0 = twin ? t : 0;
-      // Tile `at`, whose products have begun, so that its values are there: NaN blocks of keys that this row sees.
-      auto check = [&](uint32_t at, int k0, bool there) {
-        if (there && *reinterpret_cast<volatile uint32_t*>(&sh.bad_tile[at % kMeta]) == at + 1)
+      // Tile i of the item, whose sums have begun, so that its values are there: NaN blocks of keys that this row sees.
+      auto check = [&](int i) {
+        const uint32_t at = tile + i;
+        const int k0 = (it.tile + i) * KEYS;
+        if (*reinterpret_cast<volatile uint32_t*>(&sh.bad_tile[at % kMeta]) == at + 1)
           for (int key = max(0, lo - k0); key < min(KEYS, hi - k0); ++key) nan |= sh.bad[at % kMeta][key];
       };
-      for (int i = i0; i < it.tiles; i += step) {
-        const uint32_t at = tile + i;
-        ok = ok && bar_wait(s_full, s_phase);
-        s_phase ^= 1;
+      int before = -1;  // the tile before
+      for (int n = twin ? t * C::kPieces : 0; n < it.pieces;) {
+        const int i = n / C::kPieces, in = n % C::kPieces, buffer = n & 1;
+        const uint32_t at = (tile + i) % kMeta;
+        ok = ok && bar_wait(s_full + 8 * buffer, s_phase >> buffer & 1u);
+        s_phase ^= 1u << buffer;
         __syncwarp();
         tc_after();
-        const int k0 = (it.tile + i) * KEYS;
-        check(at - step, k0 - step * KEYS, i > i0);
+        const int k0 = (it.tile + i) * KEYS + in * kPiece;
+        if (in == 0) {
+          if (before >= 0) {
+            check(before);
+          } else {  // (the queries are there)
+            scale = fabsf(a.scale_log2) * sh.back[number & 1][above + r] * kUnit;
+            if (scale == 0.0f) scale = 1.17549435e-38f;  // masked: -inf times it stays -inf
+          }
+          before = i;
+        }
+        const uint32_t s_in = s_at + buffer * kPiece, p_bar = p_full + 8 * buffer;
         if (busy) {
-          constexpr int kC = KEYS / 32;
-          uint32_t x[kC][32];
-#pragma unroll
-          for (int c = 0; c < kC / 2; ++c) tmem_load32(s_at + 32 * c, x[c]);
-          const uint2 valid8 = *reinterpret_cast<const uint2*>(sh.valid[at % kMeta]);
-          const bool whole = k0 >= all_lo && k0 + KEYS <= all_hi && (valid8.x & valid8.y) == 0x01010101u;
-          // a bit per run of 16 keys: bytes 0 .. 7, or (8 keys to a warp) every other one
-          uint32_t valid = ((valid8.x * 0x01020408u) >> 24 & 15u) | ((valid8.y * 0x01020408u) >> 20 & 0xF0u);
-          if (KEYS == 64) valid = (valid & 1u) | (valid >> 1 & 2u) | (valid >> 2 & 4u) | (valid >> 3 & 8u);
-          float tops[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-          for (int half = 0; half < 2; ++half) {
-            tmem_wait(x[half * kC / 2]);
-            if (kC == 4) asm volatile("" : WD_R32(x[(half * kC / 2 + 1) % kC]));
-            if (half == 0) {
-#pragma unroll
-              for (int c = kC / 2; c < kC; ++c) tmem_load32(s_at + 32 * c, x[c]);
+          uint32_t x[2][32];
+          tmem_load32(s_in, x[0]);
+          tmem_load32(s_in + 32, x[1]);
+          // a decode warp's byte: a run of 16 keys (two warps to a run where they have 8 keys)
+          uint32_t valid4 = *reinterpret_cast<const uint32_t*>(&sh.valid[at][C::kPieces == 2 ? 4 * in : 0]), more = valid4;
+          if (C::kPieces == 1) more = *reinterpret_cast<const uint32_t*>(&sh.valid[at][4]);
+          const bool whole = k0 >= all_lo && k0 + kPiece <= all_hi && valid4 == 0x01010101u && more == 0x01010101u;
+          tmem_wait(x[0]);
+          asm volatile("" : WD_R32(x[1]));
+          if (!whole) {
+            const bool wide = ((valid4 | more) & 0x02020202u) != 0;
+            uint32_t valid = ((valid4 & 0x01010101u) * 0x01020408u) >> 24 & 15u;
+            if (C::kPieces == 1) {
+              valid |= ((more & 0x01010101u) * 0x01020408u) >> 20 & 0xF0u;
+              valid = (valid & 1u) | (valid >> 1 & 2u) | (valid >> 2 & 4u) | (valid >> 3 & 8u);
             }
 #pragma unroll
-            for (int c = half * kC / 2; c < (half + 1) * kC / 2; ++c) {
-              if (!whole) {  // the row's keys among these 32
-                const int b = max(0, min(32, lo - k0 - 32 * c)), e = max(0, min(32, hi - k0 - 32 * c));
-                uint32_t v = (e >= 32 ? kAll : (1u << e) - 1u) & ~(b >= 32 ? kAll : (1u << b) - 1u);
-                if (!(valid >> (2 * c) & 1u)) v &= 0xFFFF0000u;
-                if (!(valid >> (2 * c) & 2u)) v &= 0x0000FFFFu;
+            for (int c = 0; c < 2; ++c) {  // the row's keys among these 32
+              const int b = max(0, min(32, lo - k0 - 32 * c)), e = max(0, min(32, hi - k0 - 32 * c));
+              uint32_t v = (e >= 32 ? kAll : (1u << e) - 1u) & ~(b >= 32 ? kAll : (1u << b) - 1u);
+              if (!(valid >> (2 * c) & 1u)) v &= 0xFFFF0000u;
+              if (!(valid >> (2 * c) & 2u)) v &= 0x0000FFFFu;
+              if (wide) {
 #pragma unroll
-                for (int j = 0; j < 32; ++j)
-                  if (!(v >> j & 1u)) x[c][j] = 0xFF800000u;
+                for (int j = 0; j < 32; j += 4) {
+                  const float4 f4 = *reinterpret_cast<const float4*>(&sh.factors[at][in * kPiece + 32 * c + j]);
+                  x[c][j] = __float_as_uint(__uint_as_float(x[c][j]) * f4.x);
+                  x[c][j + 1] = __float_as_uint(__uint_as_float(x[c][j + 1]) * f4.y);
+                  x[c][j + 2] = __float_as_uint(__uint_as_float(x[c][j + 2]) * f4.z);
+                  x[c][j + 3] = __float_as_uint(__uint_as_float(x[c][j + 3]) * f4.w);
+                }
               }
 #pragma unroll
-              for (int j = 0; j < 32; j += 8)
-#pragma unroll
-                for (int n = 0; n < 4; ++n)
-                  tops[n] = max3(tops[n], __uint_as_float(x[c][j + 2 * n]), __uint_as_float(x[c][j + 2 * n + 1]));
+              for (int j = 0; j < 32; ++j)
+                if (!(v >> j & 1u)) x[c][j] = 0xFF800000u;
             }
           }
-          const float top = fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3])), to = top * a.scale_log2;
+          float tops[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+          for (int c = 0; c < 2; ++c)
+#pragma unroll
+            for (int j = 0; j < 32; j += 8)
+#pragma unroll
+              for (int k = 0; k < 4; ++k)
+                tops[k] = max3(tops[k], __uint_as_float(x[c][j + 2 * k]), __uint_as_float(x[c][j + 2 * k + 1]));
+          const float top = fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3])), to = top * scale;
           bool moved = false;
           float f = 1.0f;
           if (m == -INFINITY) {
             if (top != -INFINITY) m = to, raw = top;
           } else if (to > m + kSlack) {
-            f = exp2_fast((raw - top) * a.scale_log2);
+            f = exp2_fast((raw - top) * scale);
             m = to, raw = top;
             l *= f;
             moved = mine;  // (rows that are not there hold anything)
           }
-          if (__any_sync(kAll, moved)) {  // (not at the first tile: m is -inf)
+          // s scale - m in one step is off by the rounding of m: too much for logits this loud
+          const bool loud = mine && fabsf(m) > 1048576.0f && m != -INFINITY;
+          float less = m == -INFINITY ? 0.0f : -m;
+          if (__any_sync(kAll, moved || loud)) {
+            if (__any_sync(kAll, moved)) {  // (not at the item's first piece: m is -inf)
+              // the sums of the piece before have to be there
+              summed(buffer ^ 1);
+              __syncwarp();
+              tc_after();
 #pragma unroll 1
-            for (int c = 0; c < D; c += 16) {
-              uint32_t o[16];
-              tmem_load16(o_at + c, o);
+              for (int c = 0; c < D; c += 16) {
+                uint32_t o[16];
+                tmem_load16(o_at + c, o);
 #pragma unroll
-              for (int j = 0; j < 16; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * f);
-              tmem_store16(o_at + c, o);
+                for (int j = 0; j < 16; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * f);
+                tmem_store16(o_at + c, o);
+              }
+            }
+            if (__any_sync(kAll, loud)) {
+              less = 0.0f;
+#pragma unroll
+              for (int c = 0; c < 2; ++c)
+#pragma unroll
+                for (int j = 0; j < 32; ++j) x[c][j] = __float_as_uint(__uint_as_float(x[c][j]) - raw);
             }
           }
-          // s scale - m in one step is off by the rounding of m: too much for logits this loud
-          const bool loud = __any_sync(kAll, mine && fabsf(m) > 1048576.0f && m != -INFINITY);
-          const float less = m == -INFINITY || loud ? 0.0f : -m;
-          if (loud) {
-#pragma unroll
-            for (int c = 0; c < kC; ++c)
-#pragma unroll
-              for (int j = 0; j < 32; ++j) x[c][j] = __float_as_uint(__uint_as_float(x[c][j]) - raw);
-          }
-          const uint64_t scale2 = pair_of(__float_as_uint(a.scale_log2), __float_as_uint(a.scale_log2));
+          const uint64_t scale2 = pair_of(__float_as_uint(scale), __float_as_uint(scale));
           const uint64_t less2 = pair_of(__float_as_uint(less), __float_as_uint(less));
           uint64_t sums[2] = {0, 0};
 #pragma unroll
-          for (int c = 0; c < kC; ++c) {
+          for (int c = 0; c < 2; ++c) {
             uint32_t p[32];
 #pragma unroll
             for (int j = 0; j < 32; j += 2) {
@@ -782,37 +848,33 @@ __global__ void __launch_bounds__(C::kThreadsAll, 1) kv4_chunk_kernel(const Chun
                   : "r"(p[j / 2]), "f"(__uint_as_float(u0)), "f"(__uint_as_float(u1)));
               p[16 + j / 2] = pack2<true>(r0, r1);
             }
-            tmem_store32(s_at + 32 * c, p);
-            if ((c + 1) % (kC / 2) == 0) {  // half of the tile's products may begin
-              tmem_stored();
-              tc_before();
-              __syncwarp();
-              if (lane == 0) bar_arrive(p_full + (c + 1 == kC ? 8 : 0));
-            }
+            tmem_store32(s_in + 32 * c, p);
           }
           uint32_t a0, a1, b0, b1;
           split_pair(sums[0], a0, a1);
           split_pair(sums[1], b0, b1);
           l += (__uint_as_float(a0) + __uint_as_float(a1)) + (__uint_as_float(b0) + __uint_as_float(b1));
-        } else {
-          tc_before();
-          __syncwarp();
-          if (lane == 0) bar_arrive(p_full), bar_arrive(p_full + 8);
+          tmem_stored();
         }
+        tc_before();
+        __syncwarp();
+        if (lane == 0) bar_arrive(p_bar);
+        taken ^= 1u << buffer;
+        ++n;
+        if (twin && n % C::kPieces == 0) n += C::kPieces;
       }
-      if (it.tiles > i0) {
-        ok = ok && bar_wait(o_done, o_phase);
-        o_phase ^= 1;
-        const int last = i0 + (it.tiles - 1 - i0) / step * step;
-        check(tile + last, (it.tile + last) * KEYS, true);
+      if (before >= 0) {
+        summed(0), summed(1);
+        check(before);
       }
       tile += it.tiles;
+      if (it.tiles) ++number;
       __syncwarp();
       tc_after();
       if (!ok) sh.failed = 1, l = NAN;
       const bool final = it.begins && it.ends;
       float f0 = 1.0f, f1 = 0.0f;
-      const bool second = twin && it.tiles > 1;  // the other group has sums of these rows
+      const bool second = twin && it.pieces > C::kPieces;  // the other group has sums of these rows
       if (twin) {
         if (t == 1) {
           sh.twin_m[r] = m, sh.twin_l[r] = l, sh.twin_nan[r] = nan;
@@ -926,8 +988,8 @@ __global__ void __launch_bounds__(C::kThreadsAll, 1) kv4_chunk_kernel(const Chun
         ok = bar_wait(raw_k, tile & 1) && ok;  // (whatever was before: the copies have to end)
         if (uses) ok = ok && bar_wait(smem_addr(&sh.k_free[slot]), (uses - 1) & 1);
         __syncwarp();
-        decode_k<C>(s_k + slot * C::kTile, raw, page_k >= 0, w, a.flip, a.keep);
-        if (lane == 0) sh.valid[tile % kMeta][w] = page_k >= 0;
+        const bool wide = decode_k<C>(s_k + slot * C::kTile, raw, page_k >= 0, w, sh.factors[tile % kMeta]);
+        if (lane == 0) sh.valid[tile % kMeta][w] = (page_k >= 0 ? 1 : 0) | (wide ? 2 : 0);
         filled(&sh.k_full[slot]);  // (every lane has read the codes)
         if (more) {
           if (((i + 1) & 31) == 0) look_up(i + 1);
@@ -949,35 +1011,38 @@ __global__ void __launch_bounds__(C::kThreadsAll, 1) kv4_chunk_kernel(const Chun
     const int w = warp - C::kSoftWarps - kDecodeWarps;
     uint32_t number = 0;  // items with tiles
     if (w == 0) {
-      // BF16 operands, FP32 sums; N / 8 at bit 17, M / 16 at bit 24; bit 16: B is dim-major
-      constexpr uint32_t kIdesc = (1u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(kRows / 16) << 24);
-      constexpr uint32_t kIdescS = kIdesc | ((uint32_t)(KEYS / 8) << 17), kIdescO = kIdesc | (1u << 16) | ((uint32_t)(D / 8) << 17);
+      // FP32 sums, f16 operands (bits 7, 10: BF16); N / 8 at bit 17, M / 16 at bit 24; bit 16: B is dim-major
+      constexpr uint32_t kIdesc = (1u << 4) | ((uint32_t)(kRows / 16) << 24);
+      constexpr uint32_t kIdescS = kIdesc | ((uint32_t)(kPiece / 8) << 17);
+      constexpr uint32_t kIdescO = kIdesc | (1u << 7) | (1u << 10) | (1u << 16) | ((uint32_t)(D / 8) << 17);
       // Descriptors, high words: 128-byte swizzle, 1024 bytes from 8 rows (keys) to the next. Low words: the address; K-major
       // 1, dim-major the bytes from 64 dims to the next, a tile's keys.
-      constexpr uint32_t kHigh = 64u | 1u << 14 | 2u << 29;
-      constexpr uint32_t kLow = 1u << 16, kLowV = (uint32_t)(KEYS * 128 / 16) << 16;
-      const uint32_t q_at = kLow + (smem_addr(s_q) >> 4), k_at = kLow + (smem_addr(s_k) >> 4), v_at = kLowV + (smem_addr(s_v) >> 4);
-      auto product = [&](int t, int row_tile, uint32_t slot) {  // S of group t
-        const uint32_t s = tmem + t * KEYS, q = q_at + row_tile * (C::kTerms * C::kQBytes / 16), k = k_at + slot * (C::kTile / 16);
+      constexpr uint32_t kDescHigh = 64u | 1u << 14 | 2u << 29;
+      constexpr uint32_t kDescLow = 1u << 16, kLowV = (uint32_t)(KEYS * 128 / 16) << 16;
+      const uint32_t q_at = kDescLow + (smem_addr(s_q) >> 4), k_at = kDescLow + (smem_addr(s_k) >> 4), v_at = kLowV + (smem_addr(s_v) >> 4);
+      // Piece `in` of the tile in `slot`: S of group t, and its sums.
+      auto product = [&](int t, int row_tile, uint32_t slot, int in, int buffer) {
+        const uint32_t s = tmem + (t * 2 + buffer) * kPiece, q = q_at + row_tile * (C::kQBytes / 16),
+                       k = k_at + slot * (C::kTile / 16) + in * (kPiece * 128 / 16);
         if (elected()) {
 #pragma unroll
-          for (int term = 0; term < C::kTerms; ++term)
-#pragma unroll
-            for (int j = 0; j < D / 16; ++j)
-              mma_ss<kHigh, kHigh, kIdescS>(s, q + (uint32_t)(term * C::kQBytes + (j / 4) * kRows * 128) / 16 + (j % 4) * 2,
-                                            k + (uint32_t)(j / 4) * (KEYS * 128 / 16) + (j % 4) * 2, term + j > 0);
+          for (int j = 0; j < D / 16; ++j)
+            mma_ss<kDescHigh, kDescHigh, kIdescS>(s, q + (uint32_t)(j / 4) * (kRows * 128 / 16) + (j % 4) * 2,
+                                                  k + (uint32_t)(j / 4) * (KEYS * 128 / 16) + (j % 4) * 2, j > 0);
+          tc_commit(smem_addr(&sh.s_full[t][buffer]));
         }
         __syncwarp();
       };
-      auto values = [&](int t, uint32_t slot, int half, bool first) {  // its sums, of half of the tile's keys
-        const uint32_t o = tmem + C::kQ * KEYS + t * D, p = tmem + t * KEYS + half * (KEYS / 2),
-                       v = v_at + slot * (C::kTile / 16) + half * (KEYS / 32 * 128);
+      auto values = [&](int t, uint32_t slot, int in, int buffer, bool first) {
+        const uint32_t o = tmem + C::kQ * 2 * kPiece + t * D, p = tmem + (t * 2 + buffer) * kPiece,
+                       v = v_at + slot * (C::kTile / 16) + in * (kPiece * 128 / 16);
         if (elected()) {
 #pragma unroll
-          for (int j = 0; j < KEYS / 32; ++j)
+          for (int j = 0; j < kPiece / 16; ++j)
 #pragma unroll
             for (int term = 0; term < 2; ++term)
-              mma_ts<kHigh, kIdescO>(o, p + (j / 2) * 32 + term * 16 + (j % 2) * 8, v + j * 128, !first || j + term > 0);
+              mma_ts<kDescHigh, kIdescO>(o, p + (j / 2) * 32 + term * 16 + (j % 2) * 8, v + j * 128, !first || j + term > 0);
+          tc_commit(smem_addr(&sh.o_done[t][buffer]));
         }
         __syncwarp();
       };
@@ -985,94 +1050,93 @@ __global__ void __launch_bounds__(C::kThreadsAll, 1) kv4_chunk_kernel(const Chun
         if (elected()) tc_commit(smem_addr(bar));
         __syncwarp();
       };
-      uint32_t p_phase = 0;  // a bit per group
-      auto await_k = [&](uint32_t n) {
-        ok = ok && bar_wait(smem_addr(&sh.k_full[n % SLOTS]), (n / SLOTS) & 1);
-        __syncwarp();
-        tc_after();
-      };
-      auto await_v = [&](uint32_t n) { ok = ok && bar_wait(smem_addr(&sh.v_full[n % SLOTS]), (n / SLOTS) & 1); };
-      auto sums = [&](int t, uint32_t n, bool first) {  // group t's of tile n
-#pragma unroll 1
-        for (int half = 0; half < 2; ++half) {
-          ok = ok && bar_wait(smem_addr(&sh.p_full[t][half]), p_phase >> t & 1u);
-          __syncwarp();
-          tc_after();
-          values(t, n % SLOTS, half, first && half == 0);
-        }
-        p_phase ^= 1u << t;
-      };
+      uint32_t p_phase = 0;  // a bit per group and buffer
       while (items.next(it)) {
         if (!it.tiles) continue;
         ok = ok && bar_wait(smem_addr(&sh.q_full), number & 1);
         ++number;
-        const int n = it.tiles;
+        const int np = it.pieces;
         const bool twin = C::kQ == 2 && it.rows <= kRows;
-        // Step i: for the pair of row tiles the products of key tile i behind the sums of i - 1; for the twins those of i behind
-        // the sums of i - 2, which have the same columns.
-        const int behind = twin ? 2 : 1;
+        // Step i: the products of piece i behind the sums of the piece that had the same columns: 2 before, and 4 for the twins,
+        // who have every other tile.
+        const int behind = twin ? 2 * C::kPieces : 2;
 #pragma unroll 1
-        for (int i = 0; i < n + behind; ++i) {
-          const bool back = i >= behind, ahead = i < n;
-          const uint32_t old = tile + i - behind, now = tile + i;
-          if (!back && !ahead) continue;  // (one tile, twins: there is no second)
-          if (back) await_v(old);
-          if (ahead && !back) await_k(now);
+        for (int i = 0; i < np + behind; ++i) {
+          const int j = i - behind;
+          const bool back = j >= 0, ahead = i < np;
+          if (!back && !ahead) continue;
+          const int t0 = twin ? i / C::kPieces & 1 : 0, t1 = twin ? t0 + 1 : C::kQ, buffer = i & 1;
+          const uint32_t old = tile + j / C::kPieces, now = tile + i / C::kPieces;
+          if (back && j % C::kPieces == 0) ok = ok && bar_wait(smem_addr(&sh.v_full[old % SLOTS]), (old / SLOTS) & 1);
 #pragma unroll 1
-          for (int t = twin ? i & 1 : 0; t < (twin ? (i & 1) + 1 : C::kQ); ++t) {
-            if (back) sums(t, old, i < 2 * behind);
-            // (before the wait for K: with one slot the values behind it wait for this)
-            if (back && (twin || t + 1 == C::kQ)) commit(&sh.v_free[old % SLOTS]);
-            if (ahead) {
-              if (back) await_k(now);
-              product(t, twin ? 0 : t, now % SLOTS);
+          for (int t = t0; t < t1; ++t) {
+            if (back) {
+              const int bit = t * 2 + buffer;
+              ok = ok && bar_wait(smem_addr(&sh.p_full[t][buffer]), p_phase >> bit & 1u);
+              p_phase ^= 1u << bit;
+              __syncwarp();
+              tc_after();
+              values(t, old % SLOTS, j % C::kPieces, buffer, twin ? j < behind && j % C::kPieces == 0 : j == 0);
+              // (before the wait for K: the values behind it may wait for this)
+              if (t + 1 == t1 && (j % C::kPieces == C::kPieces - 1 || j == np - 1)) commit(&sh.v_free[old % SLOTS]);
             }
-            commit(ahead ? &sh.s_full[t] : &sh.o_done[t]);
+            if (ahead) {
+              if (t == t0 && i % C::kPieces == 0) {
+                ok = ok && bar_wait(smem_addr(&sh.k_full[now % SLOTS]), (now / SLOTS) & 1);
+                __syncwarp();
+                tc_after();
+              }
+              product(t, twin ? 0 : t, now % SLOTS, i % C::kPieces, buffer);
+            }
           }
-          if (ahead) commit(&sh.k_free[now % SLOTS]);
-          if (i + 1 == n) commit(&sh.q_free);
+          if (ahead && (i % C::kPieces == C::kPieces - 1 || i == np - 1)) commit(&sh.k_free[now % SLOTS]);
+          if (i == np - 1) commit(&sh.q_free);
         }
-        tile += n;
+        tile += it.tiles;
       }
       commit(&sh.drained);
       ok = ok && bar_wait(smem_addr(&sh.drained), 0);
       if (!ok) sh.failed = 1;
     } else {
       // --------------------------------------------------------- queries --
-      // As they are (BF16), or as two terms (F16). A warp has whole rows, D / 8 lanes each.
-      constexpr int kUnits = D / 8, kAtOnce = 32 / kUnits, kStep = kQueryWarps * kAtOnce;
+      // f16 times a power of two per row, the scale's sign among it: copied as they are, and converted in place. A warp has
+      // whole rows, D / 8 lanes each.
+      constexpr int kUnits = D / 8, kStep = kQueryWarps * (32 / kUnits);
       const int u = lane % kUnits;
+      auto place = [&](int row) {
+        return s_q + (row / kRows) * C::kQBytes + (u >> 3) * (kRows * 128) + (row % kRows) * 128 + (((u & 7) ^ (row & 7)) << 4);
+      };
       while (items.next(it)) {
         if (!it.tiles) continue;
         if (number) ok = ok && bar_wait(smem_addr(&sh.q_free), (number - 1) & 1);
         ++number;
-        int row = (w - 1) * kAtOnce + lane / kUnits, token = (it.row0 + row) / a.group, head = it.row0 + row - token * a.group;
+        const int row1 = (w - 1) * (32 / kUnits) + lane / kUnits;
+        int token = (it.row0 + row1) / a.group, head = it.row0 + row1 - token * a.group;
         const uint16_t* q = a.q + (int64_t)it.q.first * a.ldq + (int64_t)it.head * a.group * D + u * 8;
-        uint8_t* const to0 = s_q + (u >> 3) * (kRows * 128);
-        auto place = [&](int r) {
-          return to0 + (r / kRows) * C::kTerms * C::kQBytes + (r % kRows) * 128 + (((u & 7) ^ (r & 7)) << 4);
-        };
-        const int first_row = row;
-        for (; row < it.rows; row += kStep) {
-          const uint32_t to = smem_addr(place(row));
-          asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(q + (int64_t)token * a.ldq + head * D) : "memory");
+#pragma unroll 1
+        for (int row = row1; row < it.rows; row += kStep) {
+          asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_addr(place(row))), "l"(q + (int64_t)token * a.ldq + head * D)
+                       : "memory");
           head += kStep;
           while (head >= a.group) head -= a.group, ++token;
         }
         asm volatile("cp.async.wait_all;" ::: "memory");
-        if constexpr (!BF16) {
-          for (row = first_row; row < it.rows; row += kStep) {
-            uint8_t* to = place(row);
-            float f[8];
-            unpack8<false>(*reinterpret_cast<const uint4*>(to), f);
-            uint32_t hi[4], lo[4];
+        __syncwarp();
+#pragma unroll 2
+        for (int row0 = row1 - lane / kUnits; row0 < it.rows; row0 += kStep) {  // (the lanes of a warp together)
+          const int row = row0 + lane / kUnits;
+          uint4* at = reinterpret_cast<uint4*>(place(min(row, C::kItemRows - 1)));
+          const uint4 v = *at;
+          uint32_t pair = kPairs0<BF16>;
+          pair = largest_pairs<BF16>(v, pair);
+          uint32_t top = largest_of<BF16>(pair);
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              hi[j] = pack2<true>(f[2 * j], f[2 * j + 1]);
-              lo[j] = pack2<true>(f[2 * j] - bf16_lo(hi[j]), f[2 * j + 1] - bf16_hi(hi[j]));
-            }
-            *reinterpret_cast<uint4*>(to) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-            *reinterpret_cast<uint4*>(to + C::kQBytes) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+          for (int o = 1; o < kUnits; o <<= 1) top = max(top, __shfl_xor_sync(kAll, top, o));
+          const int sigma = shift_of_16<BF16>(top);
+          const float up = copysignf(exp2i(sigma), a.scale_log2);
+          if (row < it.rows) {
+            *at = scaled_f16<BF16>(v, up);
+            if (u == 0) sh.back[~number & 1][row] = exp2i(-sigma);  // (number counts this item)
           }
         }
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
@@ -1219,18 +1283,15 @@ extern "C" moe_status wd_kv4_attend_chunk(const wd_kv4_cache* c, const void* q, 
   a.ldq = ldq, a.ldo = ldo, a.T = T, a.S = S, a.max_blocks = max_blocks, a.pages = c->pages;
   a.page_shift = kv4_page_shift(c->page_size), a.heads = c->heads, a.group = q_heads / c->heads, a.window = window;
   a.room = max_blocks * c->page_size;
-  const float z = scale * 1.4426950408889634f;
-  a.scale_log2 = z == 0.0f ? 1.0f : std::fabs(z);
-  a.flip = std::signbit(z) ? 0x80008000u : 0u;
-  a.keep = z == 0.0f ? 0u : ~0u;
+  a.scale_log2 = scale * 1.4426950408889634f;
   const int64_t grid = (int64_t)sm_count();
   a.split = static_cast<Split*>(workspace);
   a.parts = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + grid * sizeof(Split));
   a.part_rows = (int32_t)part_rows_of(T, a.group);
   cudaStream_t st = (cudaStream_t)stream;
   const bool bf16 = type == WD_BF16;
-  // <dim, keys of a tile, row tiles, terms of a query>
-  if (c->dim == 64) return bf16 ? launch<Config<64, 128, 2, 1>, true>(a, st) : launch<Config<64, 128, 2, 2>, false>(a, st);
-  if (c->dim == 128) return bf16 ? launch<Config<128, 128, 2, 1>, true>(a, st) : launch<Config<128, 128, 2, 2>, false>(a, st);
-  return bf16 ? launch<Config<256, 64, 1, 1>, true>(a, st) : launch<Config<256, 64, 1, 2>, false>(a, st);
+  // <dim, keys of a tile, row tiles>
+  if (c->dim == 64) return bf16 ? launch<Config<64, 128, 2>, true>(a, st) : launch<Config<64, 128, 2>, false>(a, st);
+  if (c->dim == 128) return bf16 ? launch<Config<128, 128, 2>, true>(a, st) : launch<Config<128, 128, 2>, false>(a, st);
+  return bf16 ? launch<Config<256, 64, 1>, true>(a, st) : launch<Config<256, 64, 1>, false>(a, st);
 }
