@@ -187,7 +187,7 @@ moe_status wd_kv4_attend(const wd_kv4_cache* cache, const void* q, int32_t type,
  * do not overflow a sum on the way.
  * workspace: wd_kv4_attend_chunk_workspace bytes for T tokens or more, 16-byte aligned;
  * its contents do not matter before or after a call. Calls that may overlap need one
- * each. max_blocks * page_size < 2^31 - 2^16, T * q_heads < 2^31 - 2^16.
+ * each. max_blocks * page_size < 2^31 - 2^16, T * q_heads < 2^31 - 2^16, q_heads <= 65536.
  */
 size_t wd_kv4_attend_chunk_workspace(const wd_kv4_cache* cache, int32_t T, int32_t q_heads);
 moe_status wd_kv4_attend_chunk(const wd_kv4_cache* cache, const void* q, int32_t type,

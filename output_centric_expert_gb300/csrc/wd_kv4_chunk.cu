@@ -42,7 +42,7 @@ constexpr int kItemUnits = 2;    // what an item costs beside its key tiles, in 
 constexpr int kMinUnits = 3;     // of a CTA, on average, unless it has an item to itself
 constexpr uint32_t kWaitLimit = 1u << 20;
 constexpr int kSeqChunk = 512;   // sequences whose units are in shared memory at a time
-constexpr int kDecodeWarps = 8, kQueryWarps = 3;
+constexpr int kDecodeWarps = 8;
 constexpr int kMeta = 4;         // key tiles whose page masks and bad blocks are kept
 
 // The split item that goes on from this CTA into the next, parts 0 where there is none: an item with parts in the
@@ -67,6 +67,7 @@ struct ChunkArgs {
   int32_t T, S, max_blocks, pages, page_shift, heads, group, window, room;  // room: keys of a row of the table
   int32_t part_rows;
   float scale_log2;
+  uint32_t group_mul, group_shift;  // n / group = n * mul >> 32 >> shift for n below 2^31
 };
 
 template <int D_, int KEYS, int Q>
@@ -85,7 +86,7 @@ struct Config {
   static constexpr int kCols = Q * (2 * kPiece + D);     // two pieces' S and the sums of each row tile
   static constexpr int kTmem = kCols <= 256 ? 256 : 512;
   // registers of a thread: setmaxnreg shares out what the launch has
-  static constexpr int kSoftRegs = 112, kDecodeRegs = 80, kMmaRegs = 96;
+  static constexpr int kSoftRegs = 136, kDecodeRegs = 80, kMmaRegs = 48;
   static constexpr int kRegs = 32 * (kSoftWarps * kSoftRegs + kDecodeWarps * kDecodeRegs + 4 * kMmaRegs);
   static_assert(kCols <= 512 && kSmem <= 221 * 1024, "fits an SM");
 };
@@ -248,6 +249,11 @@ __device__ __forceinline__ uint32_t mul2_bf16(uint32_t a, uint32_t b) {
 
 // -------------------------------------------------------------- the items --
 
+// The token of a flat row.
+__device__ __forceinline__ int token_of(const ChunkArgs& a, int row) {
+  return a.group_mul ? (int)(__umulhi((uint32_t)row, a.group_mul) >> a.group_shift) : row >> a.group_shift;
+}
+
 // A sequence's new rows.
 struct Seq {
   int32_t first, tokens, len;  // first row of q, new tokens, keys before them
@@ -272,8 +278,8 @@ __device__ __forceinline__ int keys_begin(const ChunkArgs& a, const Seq& q, int 
 template <typename C>
 __device__ __forceinline__ int block_tiles(const ChunkArgs& a, const Seq& q, int b, int& kt0) {
   const int rows = q.tokens * a.group;
-  const int lo = keys_begin(a, q, b * C::kItemRows / a.group);
-  const int hi = keys_end(a, q, (min((b + 1) * C::kItemRows, rows) - 1) / a.group);
+  const int lo = keys_begin(a, q, token_of(a, b * C::kItemRows));
+  const int hi = keys_end(a, q, token_of(a, min((b + 1) * C::kItemRows, rows) - 1));
   kt0 = lo / C::kKeys;
   return hi > lo ? (hi + C::kKeys - 1) / C::kKeys - kt0 : 0;
 }
@@ -354,7 +360,7 @@ struct Items {
       it.q = q, it.seq = s, it.head = h, it.row0 = b * C::kItemRows;
       it.rows = min(C::kItemRows, q.tokens * a.group - it.row0);
       it.tile = kt0 + first, it.tiles = last - first;
-      const int seen = keys_end(a, q, (it.row0 + it.rows - 1) / a.group) - it.tile * C::kKeys;
+      const int seen = keys_end(a, q, token_of(a, it.row0 + it.rows - 1)) - it.tile * C::kKeys;
       it.pieces = min(it.tiles * C::kPieces, (seen + kPiece - 1) / kPiece);
       it.begins = first == 0, it.ends = last == n;
       it.unit0 = unit - off, it.all = per;
@@ -623,8 +629,9 @@ __device__ __forceinline__ bool decode_v(uint8_t* tile, const uint8_t* raw, bool
 
 template <typename C>
 struct Shared {  // beside the operands
-  uint64_t q_full, q_free, k_full[C::kSlots], k_free[C::kSlots], v_full[C::kSlots], v_free[C::kSlots];
-  uint64_t s_full[C::kQ][2], p_full[C::kQ][2], o_done[C::kQ][2], raw_full[2][kDecodeWarps], drained;  // (raw: K, V)
+  // (each of a single reader, who so sees every phase)
+  uint64_t q_full[C::kQ], q_twin, k_full[C::kSlots][C::kQ], v_full[C::kSlots][C::kQ], k_free[C::kSlots][C::kQ], v_free[C::kSlots][C::kQ];
+  uint64_t s_full[C::kQ][2], p_full[C::kQ][2], o_done[C::kQ][2], raw_full[2][kDecodeWarps], drained[C::kQ];  // (raw: K, V)
   int64_t units[kSeqChunk], warp[C::kThreadsAll / 32];
   Share share;
   uint32_t tmem, failed;
@@ -655,18 +662,19 @@ __global__ void __launch_bounds__(C::kThreadsAll, 1) kv4_chunk_kernel(const Chun
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
   }
   if (tid == 32) {
-    bar_init(smem_addr(&sh.q_full), kQueryWarps);
-    bar_init(smem_addr(&sh.q_free), 1);
     for (int i = 0; i < SLOTS; ++i) {
-      bar_init(smem_addr(&sh.k_full[i]), kDecodeWarps), bar_init(smem_addr(&sh.k_free[i]), 1);
-      bar_init(smem_addr(&sh.v_full[i]), kDecodeWarps), bar_init(smem_addr(&sh.v_free[i]), 1);
+      for (int j = 0; j < C::kQ; ++j) {
+        bar_init(smem_addr(&sh.k_full[i][j]), kDecodeWarps), bar_init(smem_addr(&sh.v_full[i][j]), kDecodeWarps);
+        bar_init(smem_addr(&sh.k_free[i][j]), 1), bar_init(smem_addr(&sh.v_free[i][j]), 1);
+      }
     }
     for (int i = 0; i < kMeta; ++i) sh.bad_tile[i] = 0;
+    bar_init(smem_addr(&sh.q_twin), 4);
     for (int i = 0; i < C::kQ; ++i) {
+      bar_init(smem_addr(&sh.q_full[i]), 4), bar_init(smem_addr(&sh.drained[i]), 1);
       for (int j = 0; j < 2; ++j) bar_init(smem_addr(&sh.s_full[i][j]), 1), bar_init(smem_addr(&sh.p_full[i][j]), 4), bar_init(smem_addr(&sh.o_done[i][j]), 1);
     }
     for (int i = 0; i < 2 * kDecodeWarps; ++i) bar_init(smem_addr(&sh.raw_full[0][0]) + 8 * i, 1);
-    bar_init(smem_addr(&sh.drained), 1);
     sh.failed = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
@@ -693,7 +701,50 @@ __global__ void __launch_bounds__(C::kThreadsAll, 1) kv4_chunk_kernel(const Chun
     // so at most one phase is open.)
     auto summed = [&](int buffer) { ok = ok && bar_wait(o_done + 8 * buffer, ~(taken >> buffer) & 1u); };
     if (tid == 0) a.split[blockIdx.x] = Split{};
-    while (items.next(it)) {
+    // The queries of an item, f16 times a power of two per row, the scale's sign among it: this warp's 32 rows, D / 8 lanes to
+    // a row, kBatch loads in flight.
+    constexpr int kUnits = D / 8, kRowsAtOnce = 32 / kUnits, kBatch = 8;
+    // The rows of a group: a twin's are the first group's; a second group of twins has none to bring.
+    auto has_twins = [&](const Item& n) { return C::kQ == 2 && n.rows <= kRows; };
+    auto bring = [&](const Item& n, uint32_t count) {
+      if (n.tiles == 0 || (t == 1 && has_twins(n))) return;
+      const int u = lane % kUnits, mine = (warp & 3) * 32 + lane / kUnits, first = has_twins(n) ? 0 : t * kRows;
+      float* back = sh.back[count & 1] + first;
+      uint8_t* const to = s_q + (first / kRows) * C::kQBytes + (u >> 3) * (kRows * 128);
+      const uint16_t* q = a.q + (int64_t)n.q.first * a.ldq + (int64_t)n.head * a.group * D + u * 8;
+      int token = token_of(a, n.row0 + first + mine), head = n.row0 + first + mine - token * a.group;
+#pragma unroll 1
+      for (int row0 = mine; row0 - mine < 32; row0 += kBatch * kRowsAtOnce) {
+        uint4 query[kBatch];
+#pragma unroll
+        for (int k = 0; k < kBatch; ++k) {
+          query[k] = make_uint4(0, 0, 0, 0);
+          if (first + row0 + k * kRowsAtOnce < n.rows) query[k] = ld_cached16(q + (int64_t)token * a.ldq + head * D);
+          head += kRowsAtOnce;
+          while (head >= a.group) head -= a.group, ++token;
+        }
+#pragma unroll
+        for (int k = 0; k < kBatch; ++k) {
+          const int row = row0 + k * kRowsAtOnce;
+          uint32_t top = largest_of<BF16>(largest_pairs<BF16>(query[k], kPairs0<BF16>));
+#pragma unroll
+          for (int o = 1; o < kUnits; o <<= 1) top = max(top, __shfl_xor_sync(kAll, top, o));
+          const int sigma = shift_of_16<BF16>(top);
+          *reinterpret_cast<uint4*>(to + row * 128 + (((u & 7) ^ (row & 7)) << 4)) =
+              scaled_f16<BF16>(query[k], copysignf(exp2i(sigma), a.scale_log2));
+          if (u == 0) back[row] = exp2i(-sigma);
+        }
+      }
+      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+      __syncwarp();
+      if (lane == 0) bar_arrive(smem_addr(&sh.q_full[t]));
+      if (lane == 0 && has_twins(n) && n.pieces > C::kPieces) bar_arrive(smem_addr(&sh.q_twin));
+    };
+    Item coming;
+    bool more_items = items.next(coming);
+    if (more_items) bring(coming, 0);
+    while (more_items) {
+      it = coming;
       if (tid == 0) {
         if (!it.ends) {  // goes on in the next CTA
           const int c0 = it.begins ? (int)blockIdx.x : cta_of(share.total, share.ctas, it.unit0 + kItemUnits);
@@ -703,21 +754,22 @@ __global__ void __launch_bounds__(C::kThreadsAll, 1) kv4_chunk_kernel(const Chun
         if (it.q.len < 0 || (int64_t)it.q.len + it.q.tokens > a.room) flag_invalid(a.err);
       }
       // Few rows: both groups of warps have them, and every other key tile.
-      const bool twin = C::kQ == 2 && it.rows <= kRows;
+      const bool twin = has_twins(it);
       const int above = twin ? 0 : t * kRows;  // rows of the item before this group's
       const int rows = it.rows - above;
       const bool mine = r < rows, busy = (warp & 3) * 32 < rows;
-      const int flat = it.row0 + above + (mine ? r : 0), token = flat / a.group;
+      const int flat = it.row0 + above + (mine ? r : 0), token = token_of(a, flat);
       const int lo = keys_begin(a, it.q, token), hi = keys_end(a, it.q, token);
       // keys that all rows of the group see
-      const int all_lo = keys_begin(a, it.q, (it.row0 + above + min(rows, kRows) - 1) / a.group);
-      const int all_hi = keys_end(a, it.q, (it.row0 + above) / a.group);
+      const int all_lo = keys_begin(a, it.q, token_of(a, it.row0 + above + min(rows, kRows) - 1));
+      const int all_hi = keys_end(a, it.q, token_of(a, it.row0 + above));
       float m = -INFINITY, l = 0.0f, raw = 0.0f, scale = 0.0f;  // m = raw * scale, rounded
       uint32_t nan = 0;
-      // Tile i of the item, whose sums have begun, so that its values are there: NaN blocks of keys that this row sees.
+      const uint32_t tile0 = tile;
+      // Tile i from `tile` on, whose sums have begun, so that its values are there: NaN blocks of keys that this row sees.
       auto check = [&](int i) {
         const uint32_t at = tile + i;
-        const int k0 = (it.tile + i) * KEYS;
+        const int k0 = (it.tile + i + (int)(tile - tile0)) * KEYS;
         if (*reinterpret_cast<volatile uint32_t*>(&sh.bad_tile[at % kMeta]) == at + 1)
           for (int key = max(0, lo - k0); key < min(KEYS, hi - k0); ++key) nan |= sh.bad[at % kMeta][key];
       };
@@ -863,59 +915,53 @@ __global__ void __launch_bounds__(C::kThreadsAll, 1) kv4_chunk_kernel(const Chun
         ++n;
         if (twin && n % C::kPieces == 0) n += C::kPieces;
       }
-      if (before >= 0) {
-        summed(0), summed(1);
-        check(before);
-      }
       tile += it.tiles;
       if (it.tiles) ++number;
+      more_items = items.next(coming);
+      if (before >= 0) {
+        summed(0), summed(1);
+        check(before - it.tiles);
+      }
       __syncwarp();
       tc_after();
       if (!ok) sh.failed = 1, l = NAN;
+      if (twin) {
+        if (t == 1) sh.twin_m[r] = m, sh.twin_l[r] = l, sh.twin_nan[r] = nan;
+        tc_before();
+        soft_sync(1);
+        tc_after();
+      }
+      // (every product with this item's queries is done)
+      if (more_items) bring(coming, number);
+      if (twin && t == 1) {
+        soft_sync(2);
+        continue;
+      }
       const bool final = it.begins && it.ends;
       float f0 = 1.0f, f1 = 0.0f;
       const bool second = twin && it.pieces > C::kPieces;  // the other group has sums of these rows
-      if (twin) {
-        if (t == 1) {
-          sh.twin_m[r] = m, sh.twin_l[r] = l, sh.twin_nan[r] = nan;
-          tc_before();
-          soft_sync(1);
-          soft_sync(2);
-          continue;
-        }
-        soft_sync(1);
-        tc_after();
-        if (second) {
-          const float om = sh.twin_m[r], to = fmaxf(m, om), less = to == -INFINITY ? 0.0f : to;
-          f0 = exp2_fast(m - less), f1 = exp2_fast(om - less);
-          l = fmaf(sh.twin_l[r], f1, l * f0);
-          m = to;
-          nan |= sh.twin_nan[r];
-        }
+      if (second) {
+        const float om = sh.twin_m[r], to = fmaxf(m, om), less = to == -INFINITY ? 0.0f : to;
+        f0 = exp2_fast(m - less), f1 = exp2_fast(om - less);
+        l = fmaf(sh.twin_l[r], f1, l * f0);
+        m = to;
+        nan |= sh.twin_nan[r];
       }
-      const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-      const int64_t row = it.q.first + token;
-      const int q_head = it.head * a.group + flat % a.group;
-      float* part = a.parts + ((size_t)blockIdx.x * 2 + (it.begins ? 1 : 0)) * a.part_rows * (D + 2);
       if (busy) {
+        const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+        const int64_t row = it.q.first + token;
+        const int q_head = it.head * a.group + flat - token * a.group;
+        float* part = a.parts + ((size_t)blockIdx.x * 2 + (it.begins ? 1 : 0)) * a.part_rows * (D + 2);
         const float w0 = final ? f0 * inv : f0, w1 = final ? f1 * inv : f1;
-#pragma unroll 1
-        for (int c = 0; c < D; c += 16) {
-          uint32_t o[16], o2[16];
-#pragma unroll
-          for (int j = 0; j < 16; ++j) o[j] = o2[j] = 0;
-          if (it.tiles) tmem_load16(o_at + c, o);
-          if (second) tmem_load16(o_at + D + c, o2);
-#pragma unroll
-          for (int j = 0; j < 16; ++j) o[j] = __float_as_uint(fmaf(__uint_as_float(o2[j]), w1, __uint_as_float(o[j]) * w0));
+        auto put = [&](int c, uint32_t(&o)[32]) {  // 32 columns
           if (nan >> (c / 32) & 1u) {
 #pragma unroll
-            for (int j = 0; j < 16; ++j) o[j] = 0x7FC00000u;
+            for (int j = 0; j < 32; ++j) o[j] = 0x7FC00000u;
           }
           if (mine && final) {
             uint4* to = reinterpret_cast<uint4*>(a.out + row * a.ldo + (int64_t)q_head * D + c);
 #pragma unroll
-            for (int j = 0; j < 16; j += 8) {
+            for (int j = 0; j < 32; j += 8) {
               uint32_t h[4];
 #pragma unroll
               for (int k = 0; k < 4; ++k) h[k] = pack2<BF16>(__uint_as_float(o[j + 2 * k]), __uint_as_float(o[j + 2 * k + 1]));
@@ -924,9 +970,35 @@ __global__ void __launch_bounds__(C::kThreadsAll, 1) kv4_chunk_kernel(const Chun
           } else if (mine) {
             uint4* to = reinterpret_cast<uint4*>(part + (size_t)(above + r) * D + c);
 #pragma unroll
-            for (int j = 0; j < 16; j += 4) to[j / 4] = make_uint4(o[j], o[j + 1], o[j + 2], o[j + 3]);
+            for (int j = 0; j < 32; j += 4) to[j / 4] = make_uint4(o[j], o[j + 1], o[j + 2], o[j + 3]);
           }
           __syncwarp();
+        };
+#pragma unroll 1
+        for (int c = 0; c < D; c += second ? 32 : 64) {
+          uint32_t o[2][32];
+          if (it.tiles) {
+            tmem_load32(o_at + c, o[0]);
+            tmem_load32(second ? o_at + D + c : o_at + c + 32, o[1]);
+            tmem_wait(o[0]);
+            asm volatile("" : WD_R32(o[1]));
+          } else {
+#pragma unroll
+            for (int j = 0; j < 32; ++j) o[0][j] = o[1][j] = 0;
+          }
+          if (second) {
+#pragma unroll
+            for (int j = 0; j < 32; ++j)
+              o[0][j] = __float_as_uint(fmaf(__uint_as_float(o[1][j]), w1, __uint_as_float(o[0][j]) * w0));
+            put(c, o[0]);
+          } else {
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+#pragma unroll
+              for (int j = 0; j < 32; ++j) o[k][j] = __float_as_uint(__uint_as_float(o[k][j]) * w0);
+              put(c + 32 * k, o[k]);
+            }
+          }
         }
         if (mine && final && a.lse)
           a.lse[row * (a.heads * a.group) + q_head] = l == 0.0f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
@@ -944,9 +1016,10 @@ __global__ void __launch_bounds__(C::kThreadsAll, 1) kv4_chunk_kernel(const Chun
     const int w = warp - C::kSoftWarps;
     const uint32_t raw_k = smem_addr(&sh.raw_full[0][w]), raw_v = smem_addr(&sh.raw_full[1][w]);
     const uint8_t* raw = s_raw + w * C::kRaw;
+    uint32_t pending_k = 0, phases_k = 0, pending_v = 0, phases_v = 0;
     while (items.next(it)) {
       if (!it.tiles) continue;
-      const int end = keys_end(a, it.q, (it.row0 + it.rows - 1) / a.group), begin = keys_begin(a, it.q, it.row0 / a.group);
+      const int end = keys_end(a, it.q, token_of(a, it.row0 + it.rows - 1)), begin = keys_begin(a, it.q, token_of(a, it.row0));
       int held = -1;
       // This warp's place in 32 tiles from tile i on: lane has tile i + lane. In units of a warp's keys, -1 without a page.
       auto look_up = [&](int i) {
@@ -977,30 +1050,43 @@ __global__ void __launch_bounds__(C::kThreadsAll, 1) kv4_chunk_kernel(const Chun
       int page_k = page_of(0), page_v = page_k;
       send(0, page_k, 0, a.kc, a.ks, raw_k);
       send(0, page_v, 1, a.vc, a.vs, raw_v);
-      auto filled = [&](uint64_t* bar) {  // what this warp wrote is for the tensor cores
+      auto filled = [&](uint64_t(&bars)[C::kQ], uint32_t users) {  // what this warp wrote is for the tensor cores
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
         __syncwarp();
-        if (lane == 0) bar_arrive(smem_addr(bar));
+        if (lane < C::kQ && users >> lane & 1u) bar_arrive(smem_addr(&bars[lane]));
       };
       for (int i = 0; i < it.tiles; ++i, ++tile) {
-        const uint32_t slot = tile % SLOTS, uses = tile / SLOTS;
+        const uint32_t slot = tile % SLOTS;
         const bool more = i + 1 < it.tiles;
+        // a bit per slot and group: who still reads what was there, and the phase of its barrier
+        const uint32_t users = C::kQ == 1 ? 1u : it.rows <= kRows ? 1u << (i & 1) : 3u;
+        auto await_free = [&](uint64_t(&bars)[SLOTS][C::kQ], uint32_t& pending, uint32_t& phases) {
+#pragma unroll
+          for (int t = 0; t < C::kQ; ++t) {
+            const uint32_t bit = 1u << (slot * 2 + t);
+            if (pending & bit) {
+              ok = ok && bar_wait(smem_addr(&bars[slot][t]), (phases & bit) != 0);
+              phases ^= bit;
+            }
+          }
+          pending = (pending & ~(3u << (slot * 2))) | users << (slot * 2);
+        };
         ok = bar_wait(raw_k, tile & 1) && ok;  // (whatever was before: the copies have to end)
-        if (uses) ok = ok && bar_wait(smem_addr(&sh.k_free[slot]), (uses - 1) & 1);
+        await_free(sh.k_free, pending_k, phases_k);
         __syncwarp();
         const bool wide = decode_k<C>(s_k + slot * C::kTile, raw, page_k >= 0, w, sh.factors[tile % kMeta]);
         if (lane == 0) sh.valid[tile % kMeta][w] = (page_k >= 0 ? 1 : 0) | (wide ? 2 : 0);
-        filled(&sh.k_full[slot]);  // (every lane has read the codes)
+        filled(sh.k_full[slot], users);  // (every lane has read the codes)
         if (more) {
           if (((i + 1) & 31) == 0) look_up(i + 1);
           page_k = page_of(i + 1);
           send(i + 1, page_k, 0, a.kc, a.ks, raw_k);
         }
         ok = bar_wait(raw_v, tile & 1) && ok;
-        if (uses) ok = ok && bar_wait(smem_addr(&sh.v_free[slot]), (uses - 1) & 1);
+        await_free(sh.v_free, pending_v, phases_v);
         __syncwarp();
         if (decode_v<C>(s_v + slot * C::kTile, raw, page_v >= 0, sh.bad[tile % kMeta], w)) sh.bad_tile[tile % kMeta] = tile + 1;
-        filled(&sh.v_full[slot]);
+        filled(sh.v_full[slot], users);
         page_v = page_k;
         if (more) send(i + 1, page_v, 1, a.vc, a.vs, raw_v);
       }
@@ -1008,9 +1094,9 @@ __global__ void __launch_bounds__(C::kThreadsAll, 1) kv4_chunk_kernel(const Chun
   } else {
     // -------------------------------------------------------------- MMA --
     if constexpr (C::kQ == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kMmaRegs));
-    const int w = warp - C::kSoftWarps - kDecodeWarps;
-    uint32_t number = 0;  // items with tiles
-    if (w == 0) {
+    // A warp per group of softmax warps: one alone spent longer on issuing than the tensor cores on computing.
+    const int t = warp - C::kSoftWarps - kDecodeWarps;
+    if (t < C::kQ) {
       // FP32 sums, f16 operands (bits 7, 10: BF16); N / 8 at bit 17, M / 16 at bit 24; bit 16: B is dim-major
       constexpr uint32_t kIdesc = (1u << 4) | ((uint32_t)(kRows / 16) << 24);
       constexpr uint32_t kIdescS = kIdesc | ((uint32_t)(kPiece / 8) << 17);
@@ -1020,10 +1106,11 @@ __global__ void __launch_bounds__(C::kThreadsAll, 1) kv4_chunk_kernel(const Chun
       constexpr uint32_t kDescHigh = 64u | 1u << 14 | 2u << 29;
       constexpr uint32_t kDescLow = 1u << 16, kLowV = (uint32_t)(KEYS * 128 / 16) << 16;
       const uint32_t q_at = kDescLow + (smem_addr(s_q) >> 4), k_at = kDescLow + (smem_addr(s_k) >> 4), v_at = kLowV + (smem_addr(s_v) >> 4);
-      // Piece `in` of the tile in `slot`: S of group t, and its sums.
-      auto product = [&](int t, int row_tile, uint32_t slot, int in, int buffer) {
-        const uint32_t s = tmem + (t * 2 + buffer) * kPiece, q = q_at + row_tile * (C::kQBytes / 16),
-                       k = k_at + slot * (C::kTile / 16) + in * (kPiece * 128 / 16);
+      const uint32_t s_at = tmem + t * 2 * kPiece, o_at = tmem + C::kQ * 2 * kPiece + t * D;
+      // Piece `in` of the tile in `slot`: S, and the sums.
+      auto product = [&](int row_tile, uint32_t slot, int in, int buffer) {
+        const uint32_t s = __shfl_sync(kAll, s_at + buffer * kPiece, 0), q = __shfl_sync(kAll, q_at + row_tile * (C::kQBytes / 16), 0),
+                       k = __shfl_sync(kAll, k_at + slot * (C::kTile / 16) + in * (kPiece * 128 / 16), 0);
         if (elected()) {
 #pragma unroll
           for (int j = 0; j < D / 16; ++j)
@@ -1033,15 +1120,15 @@ __global__ void __launch_bounds__(C::kThreadsAll, 1) kv4_chunk_kernel(const Chun
         }
         __syncwarp();
       };
-      auto values = [&](int t, uint32_t slot, int in, int buffer, bool first) {
-        const uint32_t o = tmem + C::kQ * 2 * kPiece + t * D, p = tmem + (t * 2 + buffer) * kPiece,
-                       v = v_at + slot * (C::kTile / 16) + in * (kPiece * 128 / 16);
+      auto values = [&](uint32_t slot, int in, int buffer, bool first) {
+        const uint32_t o = __shfl_sync(kAll, o_at, 0), p = __shfl_sync(kAll, s_at + buffer * kPiece, 0),
+                       v = __shfl_sync(kAll, v_at + slot * (C::kTile / 16) + in * (kPiece * 128 / 16), 0);
         if (elected()) {
 #pragma unroll
           for (int j = 0; j < kPiece / 16; ++j)
 #pragma unroll
             for (int term = 0; term < 2; ++term)
-              mma_ts<kDescHigh, kIdescO>(o, p + (j / 2) * 32 + term * 16 + (j % 2) * 8, v + j * 128, !first || j + term > 0);
+              mma_ts<kDescHigh, kIdescO>(o, p + (j / 2) * 32 + term * 16 + (j % 2) * 8, v + j * 128, j + term > 0 || !first);
           tc_commit(smem_addr(&sh.o_done[t][buffer]));
         }
         __syncwarp();
@@ -1050,99 +1137,60 @@ __global__ void __launch_bounds__(C::kThreadsAll, 1) kv4_chunk_kernel(const Chun
         if (elected()) tc_commit(smem_addr(bar));
         __syncwarp();
       };
-      uint32_t p_phase = 0;  // a bit per group and buffer
+      uint32_t p_phase = 0;               // a bit per buffer
+      uint32_t k_phase = 0, v_phase = 0;  // a bit per slot
+      uint32_t q_phase = 0;              // of q_full, and of q_twin
       while (items.next(it)) {
         if (!it.tiles) continue;
-        ok = ok && bar_wait(smem_addr(&sh.q_full), number & 1);
-        ++number;
         const int np = it.pieces;
         const bool twin = C::kQ == 2 && it.rows <= kRows;
-        // Step i: the products of piece i behind the sums of the piece that had the same columns: 2 before, and 4 for the twins,
-        // who have every other tile.
-        const int behind = twin ? 2 * C::kPieces : 2;
+        // This group's pieces: all, or those of every other tile.
+        const int full = np / (2 * C::kPieces) * C::kPieces, rest = np - 2 * full;
+        const int count = !twin ? np : full + (t == 0 ? min(rest, C::kPieces) : max(0, rest - C::kPieces));
+        auto piece = [&](int n) { return twin ? (n / C::kPieces * 2 + t) * C::kPieces + n % C::kPieces : n; };
+        if (count) {
+          const int which = twin && t == 1 ? 1 : 0;
+          ok = ok && bar_wait(smem_addr(which ? &sh.q_twin : &sh.q_full[t]), q_phase >> which & 1u);
+          q_phase ^= 1u << which;
+          __syncwarp();
+          tc_after();
+        }
+        // The product of a piece goes behind the sums of the piece two before, which had the same columns.
 #pragma unroll 1
-        for (int i = 0; i < np + behind; ++i) {
-          const int j = i - behind;
-          const bool back = j >= 0, ahead = i < np;
-          if (!back && !ahead) continue;
-          const int t0 = twin ? i / C::kPieces & 1 : 0, t1 = twin ? t0 + 1 : C::kQ, buffer = i & 1;
-          const uint32_t old = tile + j / C::kPieces, now = tile + i / C::kPieces;
-          if (back && j % C::kPieces == 0) ok = ok && bar_wait(smem_addr(&sh.v_full[old % SLOTS]), (old / SLOTS) & 1);
-#pragma unroll 1
-          for (int t = t0; t < t1; ++t) {
-            if (back) {
-              const int bit = t * 2 + buffer;
-              ok = ok && bar_wait(smem_addr(&sh.p_full[t][buffer]), p_phase >> bit & 1u);
-              p_phase ^= 1u << bit;
+        for (int n = 0; n < count + 2; ++n) {
+          const int buffer = n & 1;
+          if (n >= 2) {
+            const int i = piece(n - 2), in = i % C::kPieces;
+            const uint32_t old = tile + i / C::kPieces;
+            if (in == 0) {
+              ok = ok && bar_wait(smem_addr(&sh.v_full[old % SLOTS][t]), v_phase >> (old % SLOTS) & 1u);
+              v_phase ^= 1u << (old % SLOTS);
+            }
+            ok = ok && bar_wait(smem_addr(&sh.p_full[t][buffer]), p_phase >> buffer & 1u);
+            p_phase ^= 1u << buffer;
+            __syncwarp();
+            tc_after();
+            values(old % SLOTS, in, buffer, n == 2);
+            if (in == C::kPieces - 1 || i == np - 1) commit(&sh.v_free[old % SLOTS][t]);
+          }
+          if (n < count) {
+            const int i = piece(n), in = i % C::kPieces;
+            const uint32_t now = tile + i / C::kPieces;
+            if (in == 0) {
+              ok = ok && bar_wait(smem_addr(&sh.k_full[now % SLOTS][t]), k_phase >> (now % SLOTS) & 1u);
+              k_phase ^= 1u << (now % SLOTS);
               __syncwarp();
               tc_after();
-              values(t, old % SLOTS, j % C::kPieces, buffer, twin ? j < behind && j % C::kPieces == 0 : j == 0);
-              // (before the wait for K: the values behind it may wait for this)
-              if (t + 1 == t1 && (j % C::kPieces == C::kPieces - 1 || j == np - 1)) commit(&sh.v_free[old % SLOTS]);
             }
-            if (ahead) {
-              if (t == t0 && i % C::kPieces == 0) {
-                ok = ok && bar_wait(smem_addr(&sh.k_full[now % SLOTS]), (now / SLOTS) & 1);
-                __syncwarp();
-                tc_after();
-              }
-              product(t, twin ? 0 : t, now % SLOTS, i % C::kPieces, buffer);
-            }
+            product(twin ? 0 : t, now % SLOTS, in, buffer);
+            if (in == C::kPieces - 1 || i == np - 1) commit(&sh.k_free[now % SLOTS][t]);
           }
-          if (ahead && (i % C::kPieces == C::kPieces - 1 || i == np - 1)) commit(&sh.k_free[now % SLOTS]);
-          if (i == np - 1) commit(&sh.q_free);
         }
         tile += it.tiles;
       }
-      commit(&sh.drained);
-      ok = ok && bar_wait(smem_addr(&sh.drained), 0);
+      commit(&sh.drained[t]);
+      ok = ok && bar_wait(smem_addr(&sh.drained[t]), 0);
       if (!ok) sh.failed = 1;
-    } else {
-      // --------------------------------------------------------- queries --
-      // f16 times a power of two per row, the scale's sign among it: copied as they are, and converted in place. A warp has
-      // whole rows, D / 8 lanes each.
-      constexpr int kUnits = D / 8, kStep = kQueryWarps * (32 / kUnits);
-      const int u = lane % kUnits;
-      auto place = [&](int row) {
-        return s_q + (row / kRows) * C::kQBytes + (u >> 3) * (kRows * 128) + (row % kRows) * 128 + (((u & 7) ^ (row & 7)) << 4);
-      };
-      while (items.next(it)) {
-        if (!it.tiles) continue;
-        if (number) ok = ok && bar_wait(smem_addr(&sh.q_free), (number - 1) & 1);
-        ++number;
-        const int row1 = (w - 1) * (32 / kUnits) + lane / kUnits;
-        int token = (it.row0 + row1) / a.group, head = it.row0 + row1 - token * a.group;
-        const uint16_t* q = a.q + (int64_t)it.q.first * a.ldq + (int64_t)it.head * a.group * D + u * 8;
-#pragma unroll 1
-        for (int row = row1; row < it.rows; row += kStep) {
-          asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_addr(place(row))), "l"(q + (int64_t)token * a.ldq + head * D)
-                       : "memory");
-          head += kStep;
-          while (head >= a.group) head -= a.group, ++token;
-        }
-        asm volatile("cp.async.wait_all;" ::: "memory");
-        __syncwarp();
-#pragma unroll 2
-        for (int row0 = row1 - lane / kUnits; row0 < it.rows; row0 += kStep) {  // (the lanes of a warp together)
-          const int row = row0 + lane / kUnits;
-          uint4* at = reinterpret_cast<uint4*>(place(min(row, C::kItemRows - 1)));
-          const uint4 v = *at;
-          uint32_t pair = kPairs0<BF16>;
-          pair = largest_pairs<BF16>(v, pair);
-          uint32_t top = largest_of<BF16>(pair);
-#pragma unroll
-          for (int o = 1; o < kUnits; o <<= 1) top = max(top, __shfl_xor_sync(kAll, top, o));
-          const int sigma = shift_of_16<BF16>(top);
-          const float up = copysignf(exp2i(sigma), a.scale_log2);
-          if (row < it.rows) {
-            *at = scaled_f16<BF16>(v, up);
-            if (u == 0) sh.back[~number & 1][row] = exp2i(-sigma);  // (number counts this item)
-          }
-        }
-        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-        __syncwarp();
-        if (lane == 0) bar_arrive(smem_addr(&sh.q_full));
-      }
     }
   }
   __syncwarp();
@@ -1185,7 +1233,7 @@ __global__ void __launch_bounds__(kThreads) kv4_chunk_join_kernel(const ChunkArg
       for (int i = 0; i < V; ++i) acc[i] = fmaf(__ldcg(p + (size_t)r * D + lane + 32 * i), f, acc[i]);
     }
     const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-    const int flat = sp.row0 + r, token = flat / a.group, head = sp.head * a.group + flat - token * a.group;
+    const int flat = sp.row0 + r, token = token_of(a, flat), head = sp.head * a.group + flat - token * a.group;
     const int64_t row = q.first + token;
 #pragma unroll
     for (int i = 0; i < V; ++i)
@@ -1273,6 +1321,7 @@ extern "C" moe_status wd_kv4_attend_chunk(const wd_kv4_cache* c, const void* q, 
     return refuse(MOE_ERR_SHAPE, "wd_kv4_attend_chunk: workspace is smaller than wd_kv4_attend_chunk_workspace");
   if ((int64_t)c->pages * c->heads * (c->page_size / 16) > 0x7FFFFFFF)  // 1 TB of codes
     return refuse(MOE_ERR_SHAPE, "wd_kv4_attend_chunk: the cache has too many pages");
+  if (q_heads > 65536) return refuse(MOE_ERR_SHAPE, "wd_kv4_attend_chunk: a token has at most 65536 heads");
   constexpr int64_t kMost = 0x7FFFFFFF - 0xFFFF;
   if ((int64_t)max_blocks * c->page_size >= kMost || (int64_t)T * q_heads >= kMost)
     return refuse(MOE_ERR_SHAPE, "wd_kv4_attend_chunk: block_table's capacity, or T * q_heads, is too large");
@@ -1284,6 +1333,12 @@ extern "C" moe_status wd_kv4_attend_chunk(const wd_kv4_cache* c, const void* q, 
   a.page_shift = kv4_page_shift(c->page_size), a.heads = c->heads, a.group = q_heads / c->heads, a.window = window;
   a.room = max_blocks * c->page_size;
   a.scale_log2 = scale * 1.4426950408889634f;
+  // round up 2^(32 + shift) / group: exact for numerators below 2^31 (Granlund and Montgomery)
+  while ((1u << a.group_shift) < (unsigned)a.group) ++a.group_shift;
+  if ((1u << a.group_shift) != (unsigned)a.group) {
+    --a.group_shift;
+    a.group_mul = (uint32_t)(((1ull << (32 + a.group_shift)) + a.group - 1) / a.group);
+  }
   const int64_t grid = (int64_t)sm_count();
   a.split = static_cast<Split*>(workspace);
   a.parts = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + grid * sizeof(Split));
