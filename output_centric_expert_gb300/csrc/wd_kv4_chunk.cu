@@ -38,12 +38,12 @@ constexpr unsigned kAll = 0xFFFFFFFFu;
 constexpr float kSlack = 8.0f;
 constexpr int kRows = 128;       // of a row tile
 constexpr int kPiece = 64;       // keys that are in the softmax at a time
-constexpr int kItemUnits = 2;    // what an item costs beside its key tiles, in tiles
+constexpr int kItemUnits = 4;    // what an item costs beside its key tiles, in tiles
 constexpr int kMinUnits = 3;     // of a CTA, on average, unless it has an item to itself
 constexpr uint32_t kWaitLimit = 1u << 20;
 constexpr int kSeqChunk = 512;   // sequences whose units are in shared memory at a time
 constexpr int kDecodeWarps = 8;
-constexpr int kMeta = 4;         // key tiles whose page masks and bad blocks are kept
+constexpr int kMeta = 8;         // key tiles whose page masks and bad blocks are kept
 
 // The split item that goes on from this CTA into the next, parts 0 where there is none: an item with parts in the
 // CTAs c .. c + parts - 1 is in all their entries but the last.
@@ -75,7 +75,7 @@ struct Config {
   static constexpr int D = D_, kKeys = KEYS, kQ = Q;
   static constexpr int kSlots = 2;  // of K, and of V
   static constexpr int kItemRows = Q * kRows;
-  static constexpr int kSoftWarps = 4 * Q, kThreadsAll = (kSoftWarps + kDecodeWarps + 4) * 32;
+  static constexpr int kSoftWarps = 4 * Q, kDecoders = kDecodeWarps * Q, kThreadsAll = (kSoftWarps + kDecoders + 4) * 32;
   static constexpr int kWarpKeys = KEYS / kDecodeWarps;  // keys of a decode warp in a tile: 8 or 16, inside a run of 16
   static constexpr int kQBytes = kRows * D * 2;          // of a row tile
   static constexpr int kTile = KEYS * D * 2;             // of K or V
@@ -86,8 +86,8 @@ struct Config {
   static constexpr int kCols = Q * (2 * kPiece + D);     // two pieces' S and the sums of each row tile
   static constexpr int kTmem = kCols <= 256 ? 256 : 512;
   // registers of a thread: setmaxnreg shares out what the launch has
-  static constexpr int kSoftRegs = 136, kDecodeRegs = 80, kMmaRegs = 48;
-  static constexpr int kRegs = 32 * (kSoftWarps * kSoftRegs + kDecodeWarps * kDecodeRegs + 4 * kMmaRegs);
+  static constexpr int kSoftRegs = 136, kDecodeRegs = 48, kMmaRegs = 40;
+  static constexpr int kRegs = 32 * (kSoftWarps * kSoftRegs + kDecoders * kDecodeRegs + 4 * kMmaRegs);
   static_assert(kCols <= 512 && kSmem <= 221 * 1024, "fits an SM");
 };
 
@@ -329,30 +329,30 @@ struct Item {
   int32_t all;                     // units of the whole item
 };
 
-// A walk through a CTA's items. Every role has its own.
+// A walk through a CTA's items. Every warp has its own, between items in shared memory: it would take the registers of the
+// loops over tiles.
 template <typename C>
 struct Items {
-  const ChunkArgs& a;
   int64_t unit, end;
   int s, b, h, off, blocks, n, kt0;
   Seq q;
-  __device__ Items(const ChunkArgs& args, const Share& sh)
-      : a(args), unit(sh.begin), end(sh.end), s(sh.seq), b(sh.block), h(sh.head), off(sh.off) {
-    if (unit < end) open_seq(), open_block();
+  __device__ __forceinline__ void open(const ChunkArgs& a, const Share& sh) {
+    unit = sh.begin, end = sh.end, s = sh.seq, b = sh.block, h = sh.head, off = sh.off;
+    if (unit < end) open_seq(a), open_block(a);
   }
-  __device__ __forceinline__ void open_seq() {
+  __device__ __forceinline__ void open_seq(const ChunkArgs& a) {
     q = seq_of(a, s);
     blocks = blocks_of<C>(a, q);
   }
-  __device__ __forceinline__ void open_block() {
+  __device__ __forceinline__ void open_block(const ChunkArgs& a) {
     n = block_tiles<C>(a, q, b, kt0);
   }
-  __device__ __forceinline__ bool next(Item& it) {
+  __device__ __forceinline__ bool next(const ChunkArgs& a, Item& it) {
     while (unit < end) {
       while (b == blocks) {  // (units are left, so there is another sequence with rows)
         ++s, b = 0;
-        open_seq();
-        if (blocks) open_block();
+        open_seq(a);
+        if (blocks) open_block(a);
       }
       const int per = n + kItemUnits, take = (int)min((int64_t)(per - off), end - unit);
       const int first = max(0, off - kItemUnits), last = max(0, off + take - kItemUnits);
@@ -370,7 +370,7 @@ struct Items {
         off = 0;
         if (++h == a.heads) {
           h = 0, ++b;
-          if (b < blocks) open_block();
+          if (b < blocks) open_block(a);
         }
       }
       if (it.tiles > 0 || (head_of_it && it.begins && it.ends)) return true;
@@ -633,6 +633,7 @@ struct Shared {  // beside the operands
   uint64_t q_full[C::kQ], q_twin, k_full[C::kSlots][C::kQ], v_full[C::kSlots][C::kQ], k_free[C::kSlots][C::kQ], v_free[C::kSlots][C::kQ];
   uint64_t s_full[C::kQ][2], p_full[C::kQ][2], o_done[C::kQ][2], raw_full[2][kDecodeWarps], drained[C::kQ];  // (raw: K, V)
   int64_t units[kSeqChunk], warp[C::kThreadsAll / 32];
+  Items<C> items[C::kThreadsAll / 32];
   Share share;
   uint32_t tmem, failed;
   uint32_t bad_tile[kMeta];                        // number + 1 of the last tile in this place with bad blocks of V
@@ -683,7 +684,16 @@ __global__ void __launch_bounds__(C::kThreadsAll, 1) kv4_chunk_kernel(const Chun
   tc_after();
   const uint32_t tmem = sh.tmem;  // S of the row tiles, then their sums
   const Share share = sh.share;
-  Items<C> items(a, share);
+  if (lane == 0) sh.items[warp].open(a, share);
+  __syncwarp();
+  auto next_item = [&](Item& item) {
+    Items<C> items = sh.items[warp];
+    __syncwarp();
+    const bool more = items.next(a, item);
+    if (lane == 0) sh.items[warp] = items;
+    __syncwarp();
+    return more;
+  };
   Item it;
   bool ok = true;
   uint32_t tile = 0;  // key tiles so far
@@ -741,7 +751,7 @@ __global__ void __launch_bounds__(C::kThreadsAll, 1) kv4_chunk_kernel(const Chun
       if (lane == 0 && has_twins(n) && n.pieces > C::kPieces) bar_arrive(smem_addr(&sh.q_twin));
     };
     Item coming;
-    bool more_items = items.next(coming);
+    bool more_items = next_item(coming);
     if (more_items) bring(coming, 0);
     while (more_items) {
       it = coming;
@@ -917,7 +927,7 @@ __global__ void __launch_bounds__(C::kThreadsAll, 1) kv4_chunk_kernel(const Chun
       }
       tile += it.tiles;
       if (it.tiles) ++number;
-      more_items = items.next(coming);
+      more_items = next_item(coming);
       if (before >= 0) {
         summed(0), summed(1);
         check(before - it.tiles);
@@ -1010,14 +1020,16 @@ __global__ void __launch_bounds__(C::kThreadsAll, 1) kv4_chunk_kernel(const Chun
       tc_before();  // the next item's sums go where these were
       if (twin) soft_sync(2);
     }
-  } else if (warp < C::kSoftWarps + kDecodeWarps) {
+  } else if (warp < C::kSoftWarps + C::kDecoders) {
     // ----------------------------------------------------------- decode --
     if constexpr (C::kQ == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kDecodeRegs));
-    const int w = warp - C::kSoftWarps;
+    const int w = (warp - C::kSoftWarps) % kDecodeWarps;
+    const bool does_k = warp - C::kSoftWarps < kDecodeWarps, does_v = C::kQ == 1 || !does_k;
     const uint32_t raw_k = smem_addr(&sh.raw_full[0][w]), raw_v = smem_addr(&sh.raw_full[1][w]);
     const uint8_t* raw = s_raw + w * C::kRaw;
-    uint32_t pending_k = 0, phases_k = 0, pending_v = 0, phases_v = 0;
-    while (items.next(it)) {
+    uint32_t pending_k = 0, phases_k = 0, pending_own = 0, phases_own = 0;
+    uint32_t &pending_v = C::kQ == 2 ? pending_k : pending_own, &phases_v = C::kQ == 2 ? phases_k : phases_own;
+    while (next_item(it)) {
       if (!it.tiles) continue;
       const int end = keys_end(a, it.q, token_of(a, it.row0 + it.rows - 1)), begin = keys_begin(a, it.q, token_of(a, it.row0));
       int held = -1;
@@ -1048,8 +1060,8 @@ __global__ void __launch_bounds__(C::kThreadsAll, 1) kv4_chunk_kernel(const Chun
       };
       look_up(0);
       int page_k = page_of(0), page_v = page_k;
-      send(0, page_k, 0, a.kc, a.ks, raw_k);
-      send(0, page_v, 1, a.vc, a.vs, raw_v);
+      if (does_k) send(0, page_k, 0, a.kc, a.ks, raw_k);
+      if (does_v) send(0, page_v, 1, a.vc, a.vs, raw_v);
       auto filled = [&](uint64_t(&bars)[C::kQ], uint32_t users) {  // what this warp wrote is for the tensor cores
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
         __syncwarp();
@@ -1071,6 +1083,7 @@ __global__ void __launch_bounds__(C::kThreadsAll, 1) kv4_chunk_kernel(const Chun
           }
           pending = (pending & ~(3u << (slot * 2))) | users << (slot * 2);
         };
+        if (does_k) {
         ok = bar_wait(raw_k, tile & 1) && ok;  // (whatever was before: the copies have to end)
         await_free(sh.k_free, pending_k, phases_k);
         __syncwarp();
@@ -1082,6 +1095,9 @@ __global__ void __launch_bounds__(C::kThreadsAll, 1) kv4_chunk_kernel(const Chun
           page_k = page_of(i + 1);
           send(i + 1, page_k, 0, a.kc, a.ks, raw_k);
         }
+        }
+        if (does_v) {
+        if (!does_k && more && ((i + 1) & 31) == 0) { page_v = page_k; look_up(i + 1); } if (!does_k && more) page_k = page_of(i + 1);
         ok = bar_wait(raw_v, tile & 1) && ok;
         await_free(sh.v_free, pending_v, phases_v);
         __syncwarp();
@@ -1089,13 +1105,14 @@ __global__ void __launch_bounds__(C::kThreadsAll, 1) kv4_chunk_kernel(const Chun
         filled(sh.v_full[slot], users);
         page_v = page_k;
         if (more) send(i + 1, page_v, 1, a.vc, a.vs, raw_v);
+        }
       }
     }
   } else {
     // -------------------------------------------------------------- MMA --
     if constexpr (C::kQ == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kMmaRegs));
     // A warp per group of softmax warps: one alone spent longer on issuing than the tensor cores on computing.
-    const int t = warp - C::kSoftWarps - kDecodeWarps;
+    const int t = warp - C::kSoftWarps - C::kDecoders;
     if (t < C::kQ) {
       // FP32 sums, f16 operands (bits 7, 10: BF16); N / 8 at bit 17, M / 16 at bit 24; bit 16: B is dim-major
       constexpr uint32_t kIdesc = (1u << 4) | ((uint32_t)(kRows / 16) << 24);
@@ -1140,7 +1157,7 @@ __global__ void __launch_bounds__(C::kThreadsAll, 1) kv4_chunk_kernel(const Chun
       uint32_t p_phase = 0;               // a bit per buffer
       uint32_t k_phase = 0, v_phase = 0;  // a bit per slot
       uint32_t q_phase = 0;              // of q_full, and of q_twin
-      while (items.next(it)) {
+      while (next_item(it)) {
         if (!it.tiles) continue;
         const int np = it.pieces;
         const bool twin = C::kQ == 2 && it.rows <= kRows;
