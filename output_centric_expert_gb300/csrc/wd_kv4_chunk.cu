@@ -672,7 +672,7 @@ __global__ void __launch_bounds__(C::kThreadsAll, 1) kv4_chunk_kernel(const Chun
     for (int i = 0; i < kMeta; ++i) sh.bad_tile[i] = 0;
     bar_init(smem_addr(&sh.q_twin), 4);
     for (int i = 0; i < C::kQ; ++i) {
-      bar_init(smem_addr(&sh.q_full[i]), 4), bar_init(smem_addr(&sh.drained[i]), 1);
+      bar_init(smem_addr(&sh.q_full[i]), 4), bar_init(smem_addr(&sh.drained[i]), 2);
       for (int j = 0; j < 2; ++j) bar_init(smem_addr(&sh.s_full[i][j]), 1), bar_init(smem_addr(&sh.p_full[i][j]), 4), bar_init(smem_addr(&sh.o_done[i][j]), 1);
     }
     for (int i = 0; i < 2 * kDecodeWarps; ++i) bar_init(smem_addr(&sh.raw_full[0][0]) + 8 * i, 1);
@@ -1111,9 +1111,11 @@ __global__ void __launch_bounds__(C::kThreadsAll, 1) kv4_chunk_kernel(const Chun
   } else {
     // -------------------------------------------------------------- MMA --
     if constexpr (C::kQ == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kMmaRegs));
-    // A warp per group of softmax warps: one alone spent longer on issuing than the tensor cores on computing.
-    const int t = warp - C::kSoftWarps - C::kDecoders;
-    if (t < C::kQ) {
+    // For each group of softmax warps a warp issues the products with keys, and one those with values: fewer spent longer on
+    // issuing and on their barriers than the tensor cores on computing.
+    const int t = (warp & 3) % C::kQ;
+    const bool sums = (warp & 3) >= C::kQ;
+    if ((warp & 3) < 2 * C::kQ) {
       // FP32 sums, f16 operands (bits 7, 10: BF16); N / 8 at bit 17, M / 16 at bit 24; bit 16: B is dim-major
       constexpr uint32_t kIdesc = (1u << 4) | ((uint32_t)(kRows / 16) << 24);
       constexpr uint32_t kIdescS = kIdesc | ((uint32_t)(kPiece / 8) << 17);
@@ -1125,7 +1127,7 @@ __global__ void __launch_bounds__(C::kThreadsAll, 1) kv4_chunk_kernel(const Chun
       const uint32_t q_at = kDescLow + (smem_addr(s_q) >> 4), k_at = kDescLow + (smem_addr(s_k) >> 4), v_at = kLowV + (smem_addr(s_v) >> 4);
       const uint32_t s_at = tmem + t * 2 * kPiece, o_at = tmem + C::kQ * 2 * kPiece + t * D;
       // Piece `in` of the tile in `slot`: S, and the sums.
-      auto product = [&](int row_tile, uint32_t slot, int in, int buffer) {
+      auto product = [&](int row_tile, uint32_t slot, int in, int buffer, bool last) {
         const uint32_t s = __shfl_sync(kAll, s_at + buffer * kPiece, 0), q = __shfl_sync(kAll, q_at + row_tile * (C::kQBytes / 16), 0),
                        k = __shfl_sync(kAll, k_at + slot * (C::kTile / 16) + in * (kPiece * 128 / 16), 0);
         if (elected()) {
@@ -1134,10 +1136,11 @@ __global__ void __launch_bounds__(C::kThreadsAll, 1) kv4_chunk_kernel(const Chun
             mma_ss<kDescHigh, kDescHigh, kIdescS>(s, q + (uint32_t)(j / 4) * (kRows * 128 / 16) + (j % 4) * 2,
                                                   k + (uint32_t)(j / 4) * (KEYS * 128 / 16) + (j % 4) * 2, j > 0);
           tc_commit(smem_addr(&sh.s_full[t][buffer]));
+          if (last) tc_commit(smem_addr(&sh.k_free[slot][t]));
         }
         __syncwarp();
       };
-      auto values = [&](uint32_t slot, int in, int buffer, bool first) {
+      auto values = [&](uint32_t slot, int in, int buffer, bool first, bool last) {
         const uint32_t o = __shfl_sync(kAll, o_at, 0), p = __shfl_sync(kAll, s_at + buffer * kPiece, 0),
                        v = __shfl_sync(kAll, v_at + slot * (C::kTile / 16) + in * (kPiece * 128 / 16), 0);
         if (elected()) {
@@ -1147,16 +1150,13 @@ __global__ void __launch_bounds__(C::kThreadsAll, 1) kv4_chunk_kernel(const Chun
             for (int term = 0; term < 2; ++term)
               mma_ts<kDescHigh, kIdescO>(o, p + (j / 2) * 32 + term * 16 + (j % 2) * 8, v + j * 128, j + term > 0 || !first);
           tc_commit(smem_addr(&sh.o_done[t][buffer]));
+          if (last) tc_commit(smem_addr(&sh.v_free[slot][t]));
         }
         __syncwarp();
       };
-      auto commit = [&](uint64_t* bar) {
-        if (elected()) tc_commit(smem_addr(bar));
-        __syncwarp();
-      };
-      uint32_t p_phase = 0;               // a bit per buffer
-      uint32_t k_phase = 0, v_phase = 0;  // a bit per slot
-      uint32_t q_phase = 0;              // of q_full, and of q_twin
+      uint32_t phase = 0;                 // of p_full or o_done, a bit per buffer
+      uint32_t slot_phase = 0;            // of k_full or v_full, a bit per slot
+      uint32_t q_phase = 0;               // of q_full, and of q_twin
       while (next_item(it)) {
         if (!it.tiles) continue;
         const int np = it.pieces;
@@ -1164,48 +1164,38 @@ __global__ void __launch_bounds__(C::kThreadsAll, 1) kv4_chunk_kernel(const Chun
         // This group's pieces: all, or those of every other tile.
         const int full = np / (2 * C::kPieces) * C::kPieces, rest = np - 2 * full;
         const int count = !twin ? np : full + (t == 0 ? min(rest, C::kPieces) : max(0, rest - C::kPieces));
-        auto piece = [&](int n) { return twin ? (n / C::kPieces * 2 + t) * C::kPieces + n % C::kPieces : n; };
-        if (count) {
+        if (!sums && count) {
           const int which = twin && t == 1 ? 1 : 0;
           ok = ok && bar_wait(smem_addr(which ? &sh.q_twin : &sh.q_full[t]), q_phase >> which & 1u);
           q_phase ^= 1u << which;
+        }
+        // The product of a piece waits for the sums of the piece two before, which had the same columns (at the item's end for
+        // the last two, whose columns are the next item's).
+        const int steps = sums ? count : count + 2;
+#pragma unroll 1
+        for (int n = 0; n < steps; ++n) {
+          const int buffer = n & 1, i = twin ? (n / C::kPieces * 2 + t) * C::kPieces + n % C::kPieces : n, in = i % C::kPieces;
+          const uint32_t slot = (tile + i / C::kPieces) % SLOTS;
+          const bool last = in == C::kPieces - 1 || i == np - 1;
+          if (in == 0 && n < count) {
+            ok = ok && bar_wait(smem_addr(sums ? &sh.v_full[slot][t] : &sh.k_full[slot][t]), slot_phase >> slot & 1u);
+            slot_phase ^= 1u << slot;
+          }
+          if (sums || n >= 2) {
+            ok = ok && bar_wait(smem_addr(sums ? &sh.p_full[t][buffer] : &sh.o_done[t][buffer]), phase >> buffer & 1u);
+            phase ^= 1u << buffer;
+          }
           __syncwarp();
           tc_after();
-        }
-        // The product of a piece goes behind the sums of the piece two before, which had the same columns.
-#pragma unroll 1
-        for (int n = 0; n < count + 2; ++n) {
-          const int buffer = n & 1;
-          if (n >= 2) {
-            const int i = piece(n - 2), in = i % C::kPieces;
-            const uint32_t old = tile + i / C::kPieces;
-            if (in == 0) {
-              ok = ok && bar_wait(smem_addr(&sh.v_full[old % SLOTS][t]), v_phase >> (old % SLOTS) & 1u);
-              v_phase ^= 1u << (old % SLOTS);
-            }
-            ok = ok && bar_wait(smem_addr(&sh.p_full[t][buffer]), p_phase >> buffer & 1u);
-            p_phase ^= 1u << buffer;
-            __syncwarp();
-            tc_after();
-            values(old % SLOTS, in, buffer, n == 2);
-            if (in == C::kPieces - 1 || i == np - 1) commit(&sh.v_free[old % SLOTS][t]);
-          }
-          if (n < count) {
-            const int i = piece(n), in = i % C::kPieces;
-            const uint32_t now = tile + i / C::kPieces;
-            if (in == 0) {
-              ok = ok && bar_wait(smem_addr(&sh.k_full[now % SLOTS][t]), k_phase >> (now % SLOTS) & 1u);
-              k_phase ^= 1u << (now % SLOTS);
-              __syncwarp();
-              tc_after();
-            }
-            product(twin ? 0 : t, now % SLOTS, in, buffer);
-            if (in == C::kPieces - 1 || i == np - 1) commit(&sh.k_free[now % SLOTS][t]);
-          }
+          if (sums)
+            values(slot, in, buffer, n == 0, last);
+          else if (n < count)
+            product(twin ? 0 : t, slot, in, buffer, last);
         }
         tile += it.tiles;
       }
-      commit(&sh.drained[t]);
+      if (elected()) tc_commit(smem_addr(&sh.drained[t]));
+      __syncwarp();
       ok = ok && bar_wait(smem_addr(&sh.drained[t]), 0);
       if (!ok) sh.failed = 1;
     }
