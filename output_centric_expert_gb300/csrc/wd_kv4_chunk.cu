@@ -16,15 +16,31 @@
 //
 // Work. A CTA has kQ tiles of 128 rows against tiles of kKeys keys. Its warps:
 //   4 per row tile   softmax: a thread has a row. S comes from tensor memory, P goes back in
-//                    its place (16 columns of first terms, 16 of second for 32 keys)
-//   4                decode: K and V codes from global memory through registers into shared
-//                    memory (K-major and dim-major, 128-byte swizzle); the queries
-//   1                issues the MMAs
-// While one row tile is in its softmax the tensor cores have the other's products.
+//                    its place (16 columns of first terms, 16 of second for 32 keys); the
+//                    queries, copied into shared memory as f16
+//   8 per row tile   decode: codes and scales come by bulk copies, 8 or 16 keys to a warp, and
+//                    go to shared memory as operands (K-major and dim-major, 128-byte swizzle);
+//                    with two row tiles half of these warps have the keys, half the values
+//   4                issue the MMAs: for each row tile one the products with keys, one those
+//                    with values
+// The keys of a tile are in the softmax 64 at a time, in two buffers per row tile: while one is
+// exponentiated the other's scores are computed, and while one row tile is in its softmax the
+// tensor cores have the other's products. An item of up to 128 rows gives its even key tiles to
+// the first row tile and its odd ones to the second, which join at the end.
 // All (sequence, row block, KV head) items are cut into units of one key tile; CTA c of G
 // takes the c-th contiguous share of all units, found from the lengths on the device. An
 // item that several CTAs share leaves its parts in the workspace, and a dependent launch
-// joins them in CTA order.
+// joins them in CTA order. Each barrier has one reader, which sees all its phases; every wait
+// has a limit, after which the warp goes on and the results are NaN.
+//
+// Measured (GB300). 2048 tokens behind 30011 keys, 28 query heads of 128 on 4 KV heads: 1003
+// us, 911 TFLOP/s of the two products, or 1365 of the three that are issued, 74 % of a library
+// BF16 GEMM; 8192 tokens with 64 query heads, causal: 1319 us. What bounds it is the issue of
+// the decode and softmax warps: without the decoding the first takes 948, without the second
+// term of P 966, without exponentials, decoding and second terms 899. Tried: one warp per group
+// for all MMAs 1039; the same eight warps decoding K, then V 1171; an item counted as two
+// tiles 1620 for the second case, as six 1400; V as f16, K-major, 1290 (more code: the warps
+// of all roles share the instruction caches, which deliver half of what they can).
 #include <cmath>
 
 #include "wd_block.cuh"
@@ -334,25 +350,18 @@ struct Item {
 template <typename C>
 struct Items {
   int64_t unit, end;
-  int s, b, h, off, blocks, n, kt0;
+  int s, b, h, off, blocks, n, kt0;  // blocks: -1 before the sequence's are known
+  bool opened;                       // the block's tiles are known
   Seq q;
-  __device__ __forceinline__ void open(const ChunkArgs& a, const Share& sh) {
-    unit = sh.begin, end = sh.end, s = sh.seq, b = sh.block, h = sh.head, off = sh.off;
-    if (unit < end) open_seq(a), open_block(a);
-  }
-  __device__ __forceinline__ void open_seq(const ChunkArgs& a) {
-    q = seq_of(a, s);
-    blocks = blocks_of<C>(a, q);
-  }
-  __device__ __forceinline__ void open_block(const ChunkArgs& a) {
-    n = block_tiles<C>(a, q, b, kt0);
+  __device__ __forceinline__ void start(const Share& sh) {
+    unit = sh.begin, end = sh.end, s = sh.seq, b = sh.block, h = sh.head, off = sh.off, blocks = -1, opened = false;
   }
   __device__ __forceinline__ bool next(const ChunkArgs& a, Item& it) {
     while (unit < end) {
-      while (b == blocks) {  // (units are left, so there is another sequence with rows)
-        ++s, b = 0;
-        open_seq(a);
-        if (blocks) open_block(a);
+      while (!opened) {
+        if (b == blocks) ++s, b = 0, blocks = -1;  // (units are left, so there is another sequence with rows)
+        if (blocks < 0) q = seq_of(a, s), blocks = blocks_of<C>(a, q);
+        if (b < blocks) n = block_tiles<C>(a, q, b, kt0), opened = true;
       }
       const int per = n + kItemUnits, take = (int)min((int64_t)(per - off), end - unit);
       const int first = max(0, off - kItemUnits), last = max(0, off + take - kItemUnits);
@@ -369,8 +378,7 @@ struct Items {
       if (off == per) {
         off = 0;
         if (++h == a.heads) {
-          h = 0, ++b;
-          if (b < blocks) open_block(a);
+          h = 0, ++b, opened = false;
         }
       }
       if (it.tiles > 0 || (head_of_it && it.begins && it.ends)) return true;
@@ -684,7 +692,7 @@ __global__ void __launch_bounds__(C::kThreadsAll, 1) kv4_chunk_kernel(const Chun
   tc_after();
   const uint32_t tmem = sh.tmem;  // S of the row tiles, then their sums
   const Share share = sh.share;
-  if (lane == 0) sh.items[warp].open(a, share);
+  if (lane == 0) sh.items[warp].start(share);
   __syncwarp();
   auto next_item = [&](Item& item) {
     Items<C> items = sh.items[warp];
@@ -1023,6 +1031,7 @@ __global__ void __launch_bounds__(C::kThreadsAll, 1) kv4_chunk_kernel(const Chun
   } else if (warp < C::kSoftWarps + C::kDecoders) {
     // ----------------------------------------------------------- decode --
     if constexpr (C::kQ == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kDecodeRegs));
+    // Eight warps for K and eight for V; in one row tile's form (D 256) the same eight for both.
     const int w = (warp - C::kSoftWarps) % kDecodeWarps;
     const bool does_k = warp - C::kSoftWarps < kDecodeWarps, does_v = C::kQ == 1 || !does_k;
     const uint32_t raw_k = smem_addr(&sh.raw_full[0][w]), raw_v = smem_addr(&sh.raw_full[1][w]);
@@ -1033,7 +1042,7 @@ __global__ void __launch_bounds__(C::kThreadsAll, 1) kv4_chunk_kernel(const Chun
       if (!it.tiles) continue;
       const int end = keys_end(a, it.q, token_of(a, it.row0 + it.rows - 1)), begin = keys_begin(a, it.q, token_of(a, it.row0));
       int held = -1;
-      // This warp's place in 32 tiles from tile i on: lane has tile i + lane. In units of a warp's keys, -1 without a page.
+      // This warp's place in 32 tiles from tile i on: lane has tile i + lane. In runs of 16 keys, -1 without a page.
       auto look_up = [&](int i) {
         const int key = (it.tile + i + lane) * KEYS + w * C::kWarpKeys, run = key & ~15;
         held = -1;
@@ -1042,26 +1051,26 @@ __global__ void __launch_bounds__(C::kThreadsAll, 1) kv4_chunk_kernel(const Chun
           if (page < 0 || page >= a.pages)
             flag_invalid(a.err);
           else
-            held = page;
+            held = ((page * a.heads + it.head) << (a.page_shift - 4)) + ((key & ((1 << a.page_shift) - 1)) >> 4);
         }
       };
-      auto page_of = [&](int i) { return __shfl_sync(kAll, held, i & 31); };
-      // The codes and scales of tile i, in the page `page`, of K (part 0) or V.
-      auto send = [&](int i, int page, int part, const uint8_t* codes, const uint8_t* scales, uint32_t bar) {
+      auto run_of = [&](int i) { return __shfl_sync(kAll, held, i & 31); };
+      // The codes and scales of a run, of K (part 0) or V; run -1: nothing.
+      constexpr int kPerRun = 16 / C::kWarpKeys;
+      auto send = [&](int run, int part, const uint8_t* codes, const uint8_t* scales, uint32_t bar) {
         if (lane == 0) {
-          bar_expect(bar, page < 0 ? 0 : C::kCodes + C::kScales);
-          if (page >= 0) {
-            const int key = (it.tile + i) * KEYS + w * C::kWarpKeys;
-            const int64_t id = ((((int64_t)page * a.heads + it.head) << a.page_shift) + (key & ((1 << a.page_shift) - 1))) / C::kWarpKeys;
+          bar_expect(bar, run < 0 ? 0 : C::kCodes + C::kScales);
+          if (run >= 0) {
+            const int64_t id = (int64_t)run * kPerRun + w % kPerRun;
             bulk_copy(smem_addr(raw) + part * C::kCodes, codes + id * C::kCodes, C::kCodes, bar);
             bulk_copy(smem_addr(raw) + 2 * C::kCodes + part * C::kScales, scales + id * C::kScales, C::kScales, bar);
           }
         }
       };
       look_up(0);
-      int page_k = page_of(0), page_v = page_k;
-      if (does_k) send(0, page_k, 0, a.kc, a.ks, raw_k);
-      if (does_v) send(0, page_v, 1, a.vc, a.vs, raw_v);
+      int run_k = run_of(0), run_v = run_k;  // (without keys to decode, run_k is the next tile's)
+      if (does_k) send(run_k, 0, a.kc, a.ks, raw_k);
+      if (does_v) send(run_v, 1, a.vc, a.vs, raw_v);
       auto filled = [&](uint64_t(&bars)[C::kQ], uint32_t users) {  // what this warp wrote is for the tensor cores
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
         __syncwarp();
@@ -1084,27 +1093,30 @@ __global__ void __launch_bounds__(C::kThreadsAll, 1) kv4_chunk_kernel(const Chun
           pending = (pending & ~(3u << (slot * 2))) | users << (slot * 2);
         };
         if (does_k) {
-        ok = bar_wait(raw_k, tile & 1) && ok;  // (whatever was before: the copies have to end)
-        await_free(sh.k_free, pending_k, phases_k);
-        __syncwarp();
-        const bool wide = decode_k<C>(s_k + slot * C::kTile, raw, page_k >= 0, w, sh.factors[tile % kMeta]);
-        if (lane == 0) sh.valid[tile % kMeta][w] = (page_k >= 0 ? 1 : 0) | (wide ? 2 : 0);
-        filled(sh.k_full[slot], users);  // (every lane has read the codes)
-        if (more) {
-          if (((i + 1) & 31) == 0) look_up(i + 1);
-          page_k = page_of(i + 1);
-          send(i + 1, page_k, 0, a.kc, a.ks, raw_k);
-        }
+          ok = bar_wait(raw_k, tile & 1) && ok;  // (whatever was before: the copies have to end)
+          await_free(sh.k_free, pending_k, phases_k);
+          __syncwarp();
+          const bool wide = decode_k<C>(s_k + slot * C::kTile, raw, run_k >= 0, w, sh.factors[tile % kMeta]);
+          if (lane == 0) sh.valid[tile % kMeta][w] = (run_k >= 0 ? 1 : 0) | (wide ? 2 : 0);
+          filled(sh.k_full[slot], users);  // (every lane has read the codes)
+          if (more) {
+            if (((i + 1) & 31) == 0) look_up(i + 1);
+            run_k = run_of(i + 1);
+            send(run_k, 0, a.kc, a.ks, raw_k);
+          }
         }
         if (does_v) {
-        if (!does_k && more && ((i + 1) & 31) == 0) { page_v = page_k; look_up(i + 1); } if (!does_k && more) page_k = page_of(i + 1);
-        ok = bar_wait(raw_v, tile & 1) && ok;
-        await_free(sh.v_free, pending_v, phases_v);
-        __syncwarp();
-        if (decode_v<C>(s_v + slot * C::kTile, raw, page_v >= 0, sh.bad[tile % kMeta], w)) sh.bad_tile[tile % kMeta] = tile + 1;
-        filled(sh.v_full[slot], users);
-        page_v = page_k;
-        if (more) send(i + 1, page_v, 1, a.vc, a.vs, raw_v);
+          if (!does_k && more) {
+            if (((i + 1) & 31) == 0) look_up(i + 1);
+            run_k = run_of(i + 1);
+          }
+          ok = bar_wait(raw_v, tile & 1) && ok;
+          await_free(sh.v_free, pending_v, phases_v);
+          __syncwarp();
+          if (decode_v<C>(s_v + slot * C::kTile, raw, run_v >= 0, sh.bad[tile % kMeta], w)) sh.bad_tile[tile % kMeta] = tile + 1;
+          filled(sh.v_full[slot], users);
+          run_v = run_k;
+          if (more) send(run_v, 1, a.vc, a.vs, raw_v);
         }
       }
     }
