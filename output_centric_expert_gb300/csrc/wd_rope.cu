@@ -15,6 +15,17 @@
 // Work. A CTA has a run of tokens and some of their heads. It computes the angles' sines
 // and cosines once for all its heads into shared memory (planes of 16 bytes, so that
 // neighbouring pieces are neighbouring words).
+//
+// Measured (GB300). wd_rope, 7001 tokens with 20 heads of 256 in FP16, a quarter turned: 24 us
+// for 143 MB, 89 % of a copy's rate; with two items of a thread in flight, in 63 registers, 31. A few
+// tokens: 2.1 us, a launch. wd_kv4_rope_append, 10056 tokens with 32 query and 8 KV heads of
+// 128: 54 us for 216 MB; 64 tokens with 64 and 4: 4.6 us. The first is bound by the
+// instructions that a key takes (30 us with no queries, issue slots 63 % busy) and by the
+// queries' memory traffic, which overlap only in part. Left to the compiler the kernel took 83
+// registers, two CTAs of an SM, and 82 us; at 64 and four of them 59, and 56 with two items
+// of a thread's queries in flight. Three items, five CTAs (62), halves of the queries' slices
+// (62): slower. Runs short enough for three waves, with what a CTA reads asked into L2
+// while it finds its tokens' places: 54; for one wave 60.
 #include <algorithm>
 #include <cmath>
 
@@ -65,6 +76,11 @@ __device__ __forceinline__ void make_table(const RopeArgs& r, int tokens, float*
     if (i >= r.pairs) i -= r.pairs, ++j;
   }
   __syncthreads();
+}
+
+// Asks for bytes, a multiple of 16, to be in L2.
+__device__ __forceinline__ void prefetch_l2(const void* p, uint32_t bytes) {
+  asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(p), "r"(bytes) : "memory");
 }
 
 // Eight cosines and sines of a group.
@@ -125,43 +141,59 @@ __device__ __forceinline__ Piece<TYPE> piece_of(const float (&f)[8]) {
 // Item w of a head: two pieces, both read before either is written, so that out may be x.
 // The first rot / 16 turn (the pieces w and w + rot / 16, or 2w and 2w + 1), the rest are copied where `copies`.
 template <int TYPE>
-__device__ __forceinline__ void turn_item(const RopeArgs& r, const float* table, const void* head, void* out, int w, int pieces,
-                                          bool copies) {
-  constexpr int kPieceBytes = TYPE == WD_F32 ? 32 : 16;
-  const int groups = r.rot / 16;
-  const bool turns = w < groups;
-  if (!turns && !copies) return;
-  int p = 2 * w, q = 2 * w + 1;
-  if (turns && !r.neighbours) p = w, q = w + groups;
-  const char* from = static_cast<const char*>(head);
-  char* to = static_cast<char*>(out);
-  Piece<TYPE> a = load_piece<TYPE>(from + p * kPieceBytes), b = a;
-  if (q < pieces) b = load_piece<TYPE>(from + q * kPieceBytes);
-  if (turns) {
-    float x[8], y[8], c[8], s[8];
-    floats_of<TYPE>(a, x);
-    floats_of<TYPE>(b, y);
-    group_of(table, r.rot, w, c, s);
-    if (r.neighbours) {
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const float e = x[2 * i], o = x[2 * i + 1], e2 = y[2 * i], o2 = y[2 * i + 1];
-        x[2 * i] = fmaf(e, c[i], -(o * s[i])), x[2 * i + 1] = fmaf(o, c[i], e * s[i]);
-        y[2 * i] = fmaf(e2, c[4 + i], -(o2 * s[4 + i])), y[2 * i + 1] = fmaf(o2, c[4 + i], e2 * s[4 + i]);
-      }
-    } else {
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const float u = x[i], v = y[i];
-        x[i] = fmaf(u, c[i], -(v * s[i])), y[i] = fmaf(v, c[i], u * s[i]);
-      }
-    }
-    a = piece_of<TYPE>(x);
-    b = piece_of<TYPE>(y);
+struct TurnItem {
+  static constexpr int kPieceBytes = TYPE == WD_F32 ? 32 : 16;
+  Piece<TYPE> a, b;
+  const float* table;  // null: copied
+  char* to;            // null: nothing to do
+  int w, q;            // q: of the second piece, 0: none
+
+  __device__ __forceinline__ void none() { to = nullptr; }
+  __device__ __forceinline__ void load(const RopeArgs& r, const float* row, const void* head, void* out, int item, int pieces,
+                                       bool copies) {
+    const int groups = r.rot / 16;
+    const bool turns = item < groups;
+    to = nullptr;
+    if (!turns && !copies) return;
+    int p = 2 * item;
+    w = item, q = 2 * item + 1;
+    if (turns && !r.neighbours) p = item, q = item + groups;
+    const char* from = static_cast<const char*>(head);
+    table = turns ? row : nullptr;
+    to = static_cast<char*>(out) + p * kPieceBytes;
+    a = load_piece<TYPE>(from + p * kPieceBytes);
+    b = a;
+    if (q < pieces) b = load_piece<TYPE>(from + q * kPieceBytes);
+    q = q < pieces ? q - p : 0;
   }
-  store_piece<TYPE>(to + p * kPieceBytes, a);
-  if (q < pieces) store_piece<TYPE>(to + q * kPieceBytes, b);
-}
+  __device__ __forceinline__ void finish(const RopeArgs& r) {
+    if (!to) return;
+    if (table) {
+      float x[8], y[8], c[8], s[8];
+      floats_of<TYPE>(a, x);
+      floats_of<TYPE>(b, y);
+      group_of(table, r.rot, w, c, s);
+      if (r.neighbours) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float e = x[2 * i], o = x[2 * i + 1], e2 = y[2 * i], o2 = y[2 * i + 1];
+          x[2 * i] = fmaf(e, c[i], -(o * s[i])), x[2 * i + 1] = fmaf(o, c[i], e * s[i]);
+          y[2 * i] = fmaf(e2, c[4 + i], -(o2 * s[4 + i])), y[2 * i + 1] = fmaf(o2, c[4 + i], e2 * s[4 + i]);
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const float u = x[i], v = y[i];
+          x[i] = fmaf(u, c[i], -(v * s[i])), y[i] = fmaf(v, c[i], u * s[i]);
+        }
+      }
+      a = piece_of<TYPE>(x);
+      b = piece_of<TYPE>(y);
+    }
+    store_piece<TYPE>(to, a);
+    if (q) store_piece<TYPE>(to + q * kPieceBytes, b);
+  }
+};
 
 // ------------------------------------------------------------------ wd_rope --
 
@@ -190,8 +222,10 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const TurnArgs a) {
     if (walk.w >= end) continue;
     const int head = (w0 + walk.w) / a.items, w = w0 + walk.w - head * a.items;
     const int64_t tok = tok0 + walk.j;
-    turn_item<TYPE>(a.r, table + walk.j * a.r.rot, a.x + tok * a.ldx + (int64_t)head * a.head_bytes,
-                    a.out + tok * a.ldo + (int64_t)head * a.head_bytes, w, a.pieces, a.copies);
+    TurnItem<TYPE> item;
+    item.load(a.r, table + walk.j * a.r.rot, a.x + tok * a.ldx + (int64_t)head * a.head_bytes,
+              a.out + tok * a.ldo + (int64_t)head * a.head_bytes, w, a.pieces, a.copies);
+    item.finish(a.r);
   }
 }
 
@@ -204,7 +238,7 @@ struct RopeAppendArgs {
   uint16_t* q_out;
   uint8_t *kc, *ks, *vc, *vs;
   int64_t ldq, ldqo;
-  int32_t kv_slices;              // of the grid's y; the rest are the queries'
+  int32_t slices, kv_slices;      // of a run of tokens, one CTA each and next to each other; behind kv_slices the queries'
   int32_t q_heads, q_chunk;       // items of a token in a CTA
   bool copies;
 };
@@ -266,31 +300,52 @@ __device__ __forceinline__ uint32_t piece_top(const uint4& raw) {
   return magnitude(BF16 ? __uint_as_float(m << 16) : half_lo(m));
 }
 
+constexpr int kAppendResident = 4;  // CTAs of an SM, in 64 registers
+
 template <int D, bool BF16>
-__global__ void __launch_bounds__(kThreads) kv4_rope_append_kernel(const RopeAppendArgs a) {
+__global__ void __launch_bounds__(kThreads, kAppendResident) kv4_rope_append_kernel(const RopeAppendArgs a) {
   extern __shared__ float4 dyn4[];
   float* table = reinterpret_cast<float*>(dyn4);
   __shared__ Pair s_pair[kMostPer];
   __shared__ int64_t s_pos[kMostPer];
   const TokenArgs& t = a.t;
   const RopeArgs& r = a.r;
-  const int tok0 = blockIdx.x * t.per, tid = threadIdx.x;
+  const int run = blockIdx.x / a.slices, slice = blockIdx.x - run * a.slices;
+  const int tok0 = run * t.per, tid = threadIdx.x;
+  const bool queries = slice >= a.kv_slices;
+  // What this CTA reads comes to L2 while it finds its tokens' places.
+  if (t.per > 4 && tid < t.per && tok0 + tid < t.T) {
+    const int64_t tok = tok0 + tid;
+    if (queries) {
+      const int w0 = (slice - a.kv_slices) * a.q_chunk, end = min(a.q_chunk, a.q_heads * (D / 16) - w0);
+      prefetch_l2(a.q + tok * a.ldq + w0 * 16, end * 32);
+    } else {
+      prefetch_l2(a.k + tok * t.ldk + slice * t.chunk * 8, t.chunk * 16);
+      prefetch_l2(a.v + tok * t.ldv + slice * t.chunk * 8, t.chunk * 16);
+    }
+  }
   const int pairs = find_pairs(t, tok0, s_pair, s_pos);
-  const bool queries = (int)blockIdx.y >= a.kv_slices;
   // one token more for the keys: a pair may end behind the run
   make_table(r, t.per + (queries ? 0 : 1), table, [&](int j, int64_t& pos) {
     pos = j < t.per ? s_pos[j] : s_pos[j - 1] + (s_pos[j - 1] >= 0);
     return pos >= 0;
   });
   if (queries) {
-    constexpr int kItems = D / 16;
-    const int w0 = ((int)blockIdx.y - a.kv_slices) * a.q_chunk, end = min(a.q_chunk, a.q_heads * kItems - w0);
-    for (Walk walk(a.q_chunk); walk.j < t.per; walk.next()) {
-      if (walk.w >= end || s_pos[walk.j] < 0) continue;
-      const int w = w0 + walk.w;
-      const int64_t tok = tok0 + walk.j, head = (int64_t)(w / kItems) * D;
-      turn_item<BF16 ? WD_BF16 : WD_F16>(r, table + walk.j * r.rot, a.q + tok * a.ldq + head, a.q_out + tok * a.ldqo + head,
-                                         w % kItems, D / 8, a.copies);
+    constexpr int kPerHead = D / 16, kItems = 2;  // kItems: of a thread, in flight
+    const int w0 = (slice - a.kv_slices) * a.q_chunk, end = min(a.q_chunk, a.q_heads * kPerHead - w0);
+    for (Walk walk(a.q_chunk); walk.j < t.per;) {
+      TurnItem<BF16 ? WD_BF16 : WD_F16> item[kItems];
+#pragma unroll
+      for (int n = 0; n < kItems; ++n, walk.next()) {
+        item[n].none();
+        if (walk.j >= t.per || walk.w >= end || s_pos[walk.j] < 0) continue;
+        const int w = w0 + walk.w;
+        const int64_t tok = tok0 + walk.j, head = (int64_t)(w / kPerHead) * D;
+        item[n].load(r, table + walk.j * r.rot, a.q + tok * a.ldq + head, a.q_out + tok * a.ldqo + head, w % kPerHead, D / 8,
+                     a.copies);
+      }
+#pragma unroll
+      for (int n = 0; n < kItems; ++n) item[n].finish(r);
     }
     return;
   }
@@ -356,7 +411,7 @@ __global__ void __launch_bounds__(kThreads) kv4_rope_append_kernel(const RopeApp
     const uint32_t codes = e2m1x8(f), other = e2m1x8(g);
     return codes == other ? codes : settle_codes<BF16>(r, row, w, pos(), scale, codes, codes ^ other);
   };
-  const int kv0 = blockIdx.y * t.chunk;
+  const int kv0 = slice * t.chunk;
   for (Walk walk(t.chunk); walk.j < pairs; walk.next()) {
     const int hw = kv0 + walk.w;
     const Pair p = s_pair[walk.j];  // the four threads of a block have the same
@@ -418,11 +473,11 @@ RopeArgs rope_args(const wd_rotation* r) {
   return {r->turns, r->magnitude, r->rot_dim, r->rot_dim / 2, r->neighbours ? 1 : 0};
 }
 
-// Tokens of a CTA: T tokens in `slices` slices, each run's table at most kTable bytes, in whole waves.
+// Tokens of a CTA: T tokens in `slices` slices, each run's table at most kTable bytes, in a multiple of `waves_of` waves.
 constexpr int kTable = 16 * 1024;
-int tokens_of_a_cta(int64_t T, int slices, int rot, int resident, int least) {
+int tokens_of_a_cta(int64_t T, int slices, int rot, int resident, int least, int waves_of) {
   const int64_t slots = (int64_t)sm_count() * resident, most = std::max(least, std::min(kMostPer - 1, kTable / (rot * 4)));
-  const int64_t waves = (T * slices + slots * most - 1) / (slots * most);
+  const int64_t waves = (T * slices + slots * most * waves_of - 1) / (slots * most * waves_of) * waves_of;
   const int64_t even = (T * slices + slots * waves - 1) / (slots * waves);
   return (int)std::max((int64_t)least, std::min(most, even));
 }
@@ -435,7 +490,7 @@ moe_status turn(const TurnArgs& a, cudaStream_t st) {
 }
 
 template <int D>
-moe_status rope_append(const RopeAppendArgs& a, bool bf16, dim3 grid, cudaStream_t st) {
+moe_status rope_append(const RopeAppendArgs& a, bool bf16, unsigned grid, cudaStream_t st) {
   const size_t table = (size_t)(a.t.per + 1) * a.r.rot * 4;
   if (bf16)
     kv4_rope_append_kernel<D, true><<<grid, kThreads, table, st>>>(a);
@@ -492,7 +547,7 @@ extern "C" moe_status wd_rope(const wd_rotation* r, const void* x, int32_t type,
   a.items = a.copies ? (a.pieces + 1) / 2 : a.r.rot / 16;
   const int all = heads * a.items, slices = (all + kThreads - 1) / kThreads;
   a.chunk = (all + slices - 1) / slices;
-  a.per = tokens_of_a_cta(T, slices, a.r.rot, 6, 1);
+  a.per = tokens_of_a_cta(T, slices, a.r.rot, 6, 1, 1);
   cudaStream_t st = (cudaStream_t)stream;
   return type == WD_F32 ? turn<WD_F32>(a, st) : type == WD_BF16 ? turn<WD_BF16>(a, st) : turn<WD_F16>(a, st);
 }
@@ -526,9 +581,11 @@ extern "C" moe_status wd_kv4_rope_append(const wd_kv4_cache* c, const wd_rotatio
   const int items = q_heads * (c->dim / 16), q_slices = (items + kThreads - 1) / kThreads;
   a.q_heads = q_heads;
   a.q_chunk = q_slices ? (items + q_slices - 1) / q_slices : 1;
-  if (a.kv_slices + q_slices > 65535) return refuse(MOE_ERR_SHAPE, "wd_kv4_rope_append: too many heads");
-  a.t.per = tokens_of_a_cta(T, a.kv_slices + q_slices, a.r.rot, 4, 2);
-  const dim3 grid((unsigned)((T + (int64_t)a.t.per - 1) / a.t.per), (unsigned)(a.kv_slices + q_slices));
+  a.slices = a.kv_slices + q_slices;
+  a.t.per = tokens_of_a_cta(T, a.slices, a.r.rot, kAppendResident, 2, 3);
+  const int64_t ctas = (T + (int64_t)a.t.per - 1) / a.t.per * a.slices;
+  if (ctas > INT32_MAX) return refuse(MOE_ERR_SHAPE, "wd_kv4_rope_append: too many tokens times heads");
+  const unsigned grid = (unsigned)ctas;
   cudaStream_t st = (cudaStream_t)stream;
   const bool bf16 = type == WD_BF16;
   return c->dim == 64    ? rope_append<64>(a, bf16, grid, st)
