@@ -182,9 +182,10 @@ moe_status wd_kv4_attend(const wd_kv4_cache* cache, const void* q, int32_t type,
  * length, none of its pages valid) gets out = 0 and lse = -inf. A key that a row does
  * not see has no influence on it, NaN and infinities included. Results are the same on
  * every call with the same inputs.
- * Logits, softmax statistics and sums are FP32, q is used exactly; a probability has
- * 16 bits and FP32's range of exponents. Keys and values of up to 2^100 in magnitude
- * do not overflow a sum on the way.
+ * Logits, softmax statistics and sums are FP32; q is used as in wd_kv4_attend. Keys are used
+ * exactly, but for a key with scale codes outside 109 .. 136: its blocks 2^-36 below its
+ * largest count as 0. A probability has 16 bits and FP32's range of exponents. Keys and
+ * values of up to 2^100 in magnitude do not overflow a sum on the way.
  * workspace: wd_kv4_attend_chunk_workspace bytes for T tokens or more, 16-byte aligned;
  * its contents do not matter before or after a call. Calls that may overlap need one
  * each. max_blocks * page_size < 2^31 - 2^16, T * q_heads < 2^31 - 2^16, q_heads <= 65536.

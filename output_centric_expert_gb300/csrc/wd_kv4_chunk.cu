@@ -942,7 +942,8 @@ __global__ void __launch_bounds__(C::kThreadsAll, 1) kv4_chunk_kernel(const Chun
       }
       __syncwarp();
       tc_after();
-      if (!ok) sh.failed = 1, l = NAN;
+      if (!ok) sh.failed = 1;
+      if (*(volatile uint32_t*)&sh.failed) l = NAN;  // a wait that ran out, of any role: no sums to trust
       if (twin) {
         if (t == 1) sh.twin_m[r] = m, sh.twin_l[r] = l, sh.twin_nan[r] = nan;
         tc_before();
@@ -1091,6 +1092,7 @@ __global__ void __launch_bounds__(C::kThreadsAll, 1) kv4_chunk_kernel(const Chun
             }
           }
           pending = (pending & ~(3u << (slot * 2))) | users << (slot * 2);
+          if (!ok) sh.failed = 1;
         };
         if (does_k) {
           ok = bar_wait(raw_k, tile & 1) && ok;  // (whatever was before: the copies have to end)
@@ -1197,6 +1199,7 @@ __global__ void __launch_bounds__(C::kThreadsAll, 1) kv4_chunk_kernel(const Chun
             ok = ok && bar_wait(smem_addr(sums ? &sh.p_full[t][buffer] : &sh.o_done[t][buffer]), phase >> buffer & 1u);
             phase ^= 1u << buffer;
           }
+          if (!ok) sh.failed = 1;
           __syncwarp();
           tc_after();
           if (sums)
