@@ -1224,49 +1224,99 @@ __global__ void __launch_bounds__(C::kThreadsAll, 1) kv4_chunk_kernel(const Chun
 }
 
 // Joins the parts of the items that several CTAs share: an item with P parts has P - 1 CTAs here (each attending CTA's
-// entry names at most one item), which share out its rows; a warp takes a row. A dependent launch.
+// entry names at most one item), which share out its rows. A dependent launch. What it takes is its chain of trips to
+// memory, so a CTA asks for all maxima at once, then every thread for four words of sums per part, and where its rows are few
+// its threads share out the parts too. (A warp per row, one after the other: 54 us where the rows are 256, now 18.)
+constexpr int kMostItemRows = 256;
+constexpr int kMostWeights = 1024;  // parts of an item times a CTA's rows of it: P (256 / (P - 1) + 1), at most 514
+
 template <int D, bool BF16>
 __global__ void __launch_bounds__(kThreads) kv4_chunk_join_kernel(const ChunkArgs a) {
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  __shared__ float s_m[kMostWeights], s_l[kMostWeights], s_inv[kMostItemRows];
+  __shared__ float4 s_sum[kThreads];
+  constexpr int kWords = D / 4, kAtOnce = 4;
+  const int tid = threadIdx.x;
   wait_prerequisite();
   const Split sp = a.split[blockIdx.x];
   if (sp.parts == 0) return;
-  const int c0 = (int)blockIdx.x - sp.index, shares = sp.parts - 1;
+  const int c0 = (int)blockIdx.x - sp.index, shares = sp.parts - 1, parts = sp.parts;
+  const int r0 = (int)((int64_t)sp.rows * sp.index / shares), n = (int)((int64_t)sp.rows * (sp.index + 1) / shares) - r0;
+  if (n == 0) return;
   const size_t size = (size_t)a.part_rows * (D + 2);
-  const Seq q = seq_of(a, sp.seq);
   auto part_of = [&](int k) { return a.parts + ((size_t)(c0 + k) * 2 + (k == 0 ? 1 : 0)) * size; };
-  constexpr int V = D / 32;
-  for (int r = (int)((int64_t)sp.rows * sp.index / shares) + warp; r < (int)((int64_t)sp.rows * (sp.index + 1) / shares);
-       r += kWarpsPerCta) {
-    float top = -INFINITY;
-    for (int k = lane; k < sp.parts; k += 32) top = fmaxf(top, __ldcg(part_of(k) + (size_t)a.part_rows * D + r));
-#pragma unroll
-    for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(kAll, top, o));
+  for (int i = tid; i < parts * n; i += kThreads) {
+    const int k = i / n, r = i - k * n;
+    const float* p = part_of(k) + (size_t)a.part_rows * D + r0 + r;
+    s_m[i] = __ldcg(p);
+    s_l[i] = __ldcg(p + a.part_rows);
+  }
+  const Seq q = seq_of(a, sp.seq);
+  __syncthreads();
+  // What each part weighs.
+  if (tid < n) {
+    float top = -INFINITY, l = 0.0f;
+#pragma unroll 8
+    for (int k = 0; k < parts; ++k) top = fmaxf(top, s_m[k * n + tid]);
     const float less = top == -INFINITY ? 0.0f : top;
-    float l = 0.0f, acc[V];
-#pragma unroll
-    for (int i = 0; i < V; ++i) acc[i] = 0.0f;
-#pragma unroll 4
-    for (int k = 0; k < sp.parts; ++k) {
-      const float* p = part_of(k);
-      const float f = exp2_fast(__ldcg(p + (size_t)a.part_rows * D + r) - less);
-      l = fmaf(__ldcg(p + (size_t)a.part_rows * (D + 1) + r), f, l);
-#pragma unroll
-      for (int i = 0; i < V; ++i) acc[i] = fmaf(__ldcg(p + (size_t)r * D + lane + 32 * i), f, acc[i]);
+#pragma unroll 8
+    for (int k = 0; k < parts; ++k) {
+      const float f = exp2_fast(s_m[k * n + tid] - less);
+      l = fmaf(s_l[k * n + tid], f, l);
+      s_m[k * n + tid] = f;
     }
-    const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-    const int flat = sp.row0 + r, token = token_of(a, flat), head = sp.head * a.group + flat - token * a.group;
-    const int64_t row = q.first + token;
+    s_inv[tid] = l == 0.0f ? 0.0f : 1.0f / l;
+    const int flat = sp.row0 + r0 + tid, token = token_of(a, flat), head = sp.head * a.group + flat - token * a.group;
+    if (a.lse)
+      a.lse[((int64_t)q.first + token) * (a.heads * a.group) + head] = l == 0.0f ? -INFINITY : (less + log2f(l)) * 0.6931471805599453f;
+  }
+  __syncthreads();
+  auto put = [&](int word, const float4& v) {
+    const int r = word / kWords, flat = sp.row0 + r0 + r, token = token_of(a, flat), head = sp.head * a.group + flat - token * a.group;
+    const float inv = s_inv[r];
+    *reinterpret_cast<uint2*>(a.out + ((int64_t)q.first + token) * a.ldo + (int64_t)head * D + word % kWords * 4) =
+        make_uint2(pack2<BF16>(v.x * inv, v.y * inv), pack2<BF16>(v.z * inv, v.w * inv));
+  };
+  auto add = [&](float4& v, const float4& x, float f) {
+    v.x = fmaf(x.x, f, v.x), v.y = fmaf(x.y, f, v.y), v.z = fmaf(x.z, f, v.z), v.w = fmaf(x.w, f, v.w);
+  };
+  const int words = n * kWords;
+  auto word_of = [&](int k, int word) { return __ldcg(reinterpret_cast<const float4*>(part_of(k) + (size_t)r0 * D) + word); };
+  if (words * 2 <= kThreads) {
+    const int teams = kThreads / words, team = tid / words, word = tid - team * words;
+    float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    if (team < teams) {
+#pragma unroll 4
+      for (int k = team; k < parts; k += teams) add(v, word_of(k, word), s_m[k * n + word / kWords]);
+    }
+    s_sum[tid] = v;
+    __syncthreads();
+    if (team == 0) {
+      for (int i = 1; i < teams; ++i) add(v, s_sum[i * words + word], 1.0f);
+      put(word, v);
+    }
+    return;
+  }
+  for (int base = tid; base < words; base += kThreads * kAtOnce) {
+    float4 v[kAtOnce];
 #pragma unroll
-    for (int i = 0; i < V; ++i)
-      store_elem(a.out, BF16 ? WD_BF16 : WD_F16, row * a.ldo + (int64_t)head * D + lane + 32 * i, acc[i] * inv);
-    if (a.lse && lane == 0) a.lse[row * (a.heads * a.group) + head] = l == 0.0f ? -INFINITY : (less + log2f(l)) * 0.6931471805599453f;
+    for (int i = 0; i < kAtOnce; ++i) v[i] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 2
+    for (int k = 0; k < parts; ++k) {
+      float4 x[kAtOnce];
+#pragma unroll
+      for (int i = 0; i < kAtOnce; ++i)
+        if (base + i * kThreads < words) x[i] = word_of(k, base + i * kThreads);
+#pragma unroll
+      for (int i = 0; i < kAtOnce; ++i)
+        if (base + i * kThreads < words) add(v[i], x[i], s_m[k * n + (base + i * kThreads) / kWords]);
+    }
+#pragma unroll
+    for (int i = 0; i < kAtOnce; ++i)
+      if (base + i * kThreads < words) put(base + i * kThreads, v[i]);
   }
 }
 
 // ---------------------------------------------------------------- launch --
-
-constexpr int kMostItemRows = 256;
 
 // Rows of a part, whose sums are 16-byte words.
 int64_t part_rows_of(int64_t T, int group) { return T * group < kMostItemRows ? (T * group + 3) / 4 * 4 : kMostItemRows; }
