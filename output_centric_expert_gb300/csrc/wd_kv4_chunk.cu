@@ -1069,6 +1069,15 @@ __global__ void __launch_bounds__(C::kThreadsAll, 1) kv4_chunk_kernel(const Chun
         }
       };
       look_up(0);
+      if constexpr (C::kQ == 1) {  // the queries, which the softmax warps will want soon, to L2 (two row tiles' form lost 1 % by it)
+        const int row = w * 32 + lane;
+        if (row < it.rows) {
+          const int token = token_of(a, it.row0 + row), head = it.head * a.group + it.row0 + row - token * a.group;
+          asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(a.q + ((int64_t)it.q.first + token) * a.ldq + (int64_t)head * D),
+                       "n"(D * 2)
+                       : "memory");
+        }
+      }
       int run_k = run_of(0), run_v = run_k;  // (without keys to decode, run_k is the next tile's)
       if (does_k) send(run_k, 0, a.kc, a.ks, raw_k);
       if (does_v) send(run_v, 1, a.vc, a.vs, raw_v);
@@ -1226,14 +1235,16 @@ __global__ void __launch_bounds__(C::kThreadsAll, 1) kv4_chunk_kernel(const Chun
 // Joins the parts of the items that several CTAs share: an item with P parts has P - 1 CTAs here (each attending CTA's
 // entry names at most one item), which share out its rows. A dependent launch. What it takes is its chain of trips to
 // memory, so a CTA asks for all maxima at once, then every thread for four words of sums per part, and where its rows are few
-// its threads share out the parts too. (A warp per row, one after the other: 54 us where the rows are 256, now 18.)
+// its threads share out the parts too. (A warp per row, one after the other: 54 us where the rows are 256; this 18, and 11 with
+// 1024 threads.)
 constexpr int kMostItemRows = 256;
+constexpr int kJoinThreads = 1024;
 constexpr int kMostWeights = 1024;  // parts of an item times a CTA's rows of it: P (256 / (P - 1) + 1), at most 514
 
 template <int D, bool BF16>
-__global__ void __launch_bounds__(kThreads) kv4_chunk_join_kernel(const ChunkArgs a) {
+__global__ void __launch_bounds__(kJoinThreads) kv4_chunk_join_kernel(const ChunkArgs a) {
   __shared__ float s_m[kMostWeights], s_l[kMostWeights], s_inv[kMostItemRows];
-  __shared__ float4 s_sum[kThreads];
+  __shared__ float4 s_sum[kJoinThreads];
   constexpr int kWords = D / 4, kAtOnce = 4;
   const int tid = threadIdx.x;
   wait_prerequisite();
@@ -1244,7 +1255,7 @@ __global__ void __launch_bounds__(kThreads) kv4_chunk_join_kernel(const ChunkArg
   if (n == 0) return;
   const size_t size = (size_t)a.part_rows * (D + 2);
   auto part_of = [&](int k) { return a.parts + ((size_t)(c0 + k) * 2 + (k == 0 ? 1 : 0)) * size; };
-  for (int i = tid; i < parts * n; i += kThreads) {
+  for (int i = tid; i < parts * n; i += kJoinThreads) {
     const int k = i / n, r = i - k * n;
     const float* p = part_of(k) + (size_t)a.part_rows * D + r0 + r;
     s_m[i] = __ldcg(p);
@@ -1281,8 +1292,8 @@ __global__ void __launch_bounds__(kThreads) kv4_chunk_join_kernel(const ChunkArg
   };
   const int words = n * kWords;
   auto word_of = [&](int k, int word) { return __ldcg(reinterpret_cast<const float4*>(part_of(k) + (size_t)r0 * D) + word); };
-  if (words * 2 <= kThreads) {
-    const int teams = kThreads / words, team = tid / words, word = tid - team * words;
+  if (words * 2 <= kJoinThreads) {
+    const int teams = kJoinThreads / words, team = tid / words, word = tid - team * words;
     float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
     if (team < teams) {
 #pragma unroll 4
@@ -1296,7 +1307,7 @@ __global__ void __launch_bounds__(kThreads) kv4_chunk_join_kernel(const ChunkArg
     }
     return;
   }
-  for (int base = tid; base < words; base += kThreads * kAtOnce) {
+  for (int base = tid; base < words; base += kJoinThreads * kAtOnce) {
     float4 v[kAtOnce];
 #pragma unroll
     for (int i = 0; i < kAtOnce; ++i) v[i] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
@@ -1305,14 +1316,14 @@ __global__ void __launch_bounds__(kThreads) kv4_chunk_join_kernel(const ChunkArg
       float4 x[kAtOnce];
 #pragma unroll
       for (int i = 0; i < kAtOnce; ++i)
-        if (base + i * kThreads < words) x[i] = word_of(k, base + i * kThreads);
+        if (base + i * kJoinThreads < words) x[i] = word_of(k, base + i * kJoinThreads);
 #pragma unroll
       for (int i = 0; i < kAtOnce; ++i)
-        if (base + i * kThreads < words) add(v[i], x[i], s_m[k * n + (base + i * kThreads) / kWords]);
+        if (base + i * kJoinThreads < words) add(v[i], x[i], s_m[k * n + (base + i * kJoinThreads) / kWords]);
     }
 #pragma unroll
     for (int i = 0; i < kAtOnce; ++i)
-      if (base + i * kThreads < words) put(base + i * kThreads, v[i]);
+      if (base + i * kJoinThreads < words) put(base + i * kJoinThreads, v[i]);
   }
 }
 
@@ -1348,7 +1359,7 @@ moe_status launch(ChunkArgs a, cudaStream_t st) {
   dependent.val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(grid);
-  cfg.blockDim = dim3(kThreads);
+  cfg.blockDim = dim3(kJoinThreads);
   cfg.stream = st;
   cfg.attrs = &dependent;
   cfg.numAttrs = 1;
