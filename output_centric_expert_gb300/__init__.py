@@ -12,7 +12,8 @@ The layer is two hand-written CUDA kernels for sm_103a behind a C ABI
 
 Around the layer, ``include/warp_decode_block.h`` has the rest of a decoder
 block: projections with MXFP4 weights, a paged KV cache in MXFP4 with its
-attention, and the norms between blocks (``block_ops``).
+attention (one token per sequence, or prompts and drafts), rotary positions, and
+the norms between blocks (``block_ops``).
 
 ``ops`` is the thin Python binding (argument marshalling only); ``workload``
 is the seeded synthetic input generator. Importing this package loads nothing

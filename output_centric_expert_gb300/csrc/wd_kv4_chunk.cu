@@ -33,14 +33,15 @@
 // joins them in CTA order. Each barrier has one reader, which sees all its phases; every wait
 // has a limit, after which the warp goes on and the results are NaN.
 //
-// Measured (GB300). 2048 tokens behind 30011 keys, 28 query heads of 128 on 4 KV heads: 1003
-// us, 911 TFLOP/s of the two products, or 1365 of the three that are issued, 74 % of a library
-// BF16 GEMM; 8192 tokens with 64 query heads, causal: 1319 us. What bounds it is the issue of
-// the decode and softmax warps: without the decoding the first takes 948, without the second
-// term of P 966, without exponentials, decoding and second terms 899. Tried: one warp per group
-// for all MMAs 1039; the same eight warps decoding K, then V 1171; an item counted as two
-// tiles 1620 for the second case, as six 1400; V as f16, K-major, 1290 (more code: the warps
-// of all roles share the instruction caches, which deliver half of what they can).
+// Measured (GB300). 2048 tokens behind 30011 keys, 28 query heads of 128 on 4 KV heads: 938
+// us, 971 TFLOP/s of the two products, or 1457 of the three that are issued, 79 % of a library
+// BF16 GEMM; 8192 tokens with 64 query heads, causal: 1251 us; heads of 256, 24 prompts of up
+// to 1500 with a window of 1000: 210 us. What bounds it is the issue of the decode and softmax
+// warps: when the first took 1044 it took 948 without decoding, 966 without the second term
+// of P, 899 without these and exponentials. Tried: one warp per group for all MMAs, 2 % slower;
+// the same eight warps decoding K, then V, 12 %; an item counted as two tiles 18 % for the second
+// case, as six 2 %; V as f16, K-major, 24 % (more code: the warps of all roles share the
+// instruction caches, which miss in 13 % of their requests).
 #include <cmath>
 
 #include "wd_block.cuh"

@@ -16,8 +16,9 @@
 // and cosines once for all its heads into shared memory (planes of 16 bytes, so that
 // neighbouring pieces are neighbouring words).
 //
-// Measured (GB300). wd_rope, 7001 tokens with 20 heads of 256 in FP16, a quarter turned: 24 us
-// for 143 MB, 89 % of a copy's rate; with two items of a thread in flight, in 63 registers, 31. A few
+// Measured (GB300). wd_rope, 7001 tokens with 20 heads of 256 in FP16, a quarter turned: 28.9 us
+// for 143 MB, 73 % of a copy's rate (in a graph on one set of inputs, which L2 holds in part, 24.8; with
+// two items of a thread in flight, in 63 registers, 31). A few
 // tokens: 2.1 us, a launch. wd_kv4_rope_append, 10056 tokens with 32 query and 8 KV heads of
 // 128: 54 us for 216 MB; 64 tokens with 64 and 4: 4.6 us. The first is bound by the
 // instructions that a key takes (30 us with no queries, issue slots 63 % busy) and by the
