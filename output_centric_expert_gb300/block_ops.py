@@ -157,6 +157,9 @@ def _rows(t: torch.Tensor, shape: tuple, row: int, name: str) -> int:
         raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
     if t.is_contiguous():
         return row
+    strides = t.stride()
+    if len(strides) == 3 and strides[2] == 1 and strides[1] == shape[2]:
+        return strides[0]  # (the loop below takes 1 us)
     want = 1
     for size, stride in zip(reversed(t.shape[1:]), reversed(t.stride()[1:])):
         if size != 1 and stride != want:

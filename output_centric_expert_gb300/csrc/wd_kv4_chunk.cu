@@ -1355,6 +1355,7 @@ moe_status launch(ChunkArgs a, cudaStream_t st) {
   k<<<grid, C::kThreadsAll, C::kSmem, st>>>(a);
   rc = launched("wd_kv4_attend_chunk launch");
   if (rc != MOE_OK) return rc;
+  if (a.room <= C::kKeys) return MOE_OK;  // items of one key tile, which are in one CTA: nothing to join (12.0 us to 10.9)
   cudaLaunchAttribute dependent = {};
   dependent.id = cudaLaunchAttributeProgrammaticStreamSerialization;
   dependent.val.programmaticStreamSerializationAllowed = 1;
