@@ -78,7 +78,6 @@ class DecoderLayer:
         self.workspace = block_ops.kv4_workspace(cache, max_batch, q_heads)
         if rope is not None:
             self.chunk_workspace = block_ops.kv4_chunk_workspace(cache, max_batch, q_heads)
-            self.attn.zero_()  # what padding rows start from
             return
         freq = rope_base ** (-torch.arange(0, dim, 2, device=device, dtype=torch.float32) / dim)
         angle = torch.arange(max_positions, device=device, dtype=torch.float32)[:, None] * freq
@@ -118,7 +117,7 @@ class DecoderLayer:
                err_flag: torch.Tensor | None = None) -> torch.Tensor:
         """Several new tokens of each sequence through the layer: res [T, H] (bfloat16 or float32), rows cu_new[s] to
         cu_new[s + 1] - 1 of sequence s, is updated in place and returned. seq_lens [S]: tokens that the cache holds
-        before the call. Rows behind cu_new[S] (padding) come out undefined and touch nothing else. The layer needs a
+        before the call. Rows behind cu_new[S] (padding; finite) come out undefined, but finite, and touch nothing else. The layer needs a
         rope. err_flag as for a step."""
         if self.rope is None:
             raise ValueError("extend: the layer has no rope")
@@ -127,7 +126,8 @@ class DecoderLayer:
             raise ValueError(f"extend: {T} tokens, the layer's buffers hold {self.a.shape[0]}")
         q, k, v, _ = self._project(res)
         block_ops.wd_kv4_rope_append(self.cache, self.rope, q, k, v, block_table, seq_lens, cu_new=cu_new, err_flag=err_flag)
-        block_ops.wd_kv4_attend_chunk(self.cache, q, block_table, seq_lens, self.attn[:T], self.chunk_workspace, cu_new,
+        attn = self.attn[:T].zero_()  # padding rows are not written: what an earlier call left there could be NaN
+        block_ops.wd_kv4_attend_chunk(self.cache, q, block_table, seq_lens, attn, self.chunk_workspace, cu_new,
                                       err_flag=err_flag)
         return self._behind_attention(res, err_flag)
 

@@ -8,6 +8,8 @@ import torch
 from output_centric_expert_gb300 import block_ops
 
 from .test_chunk_gpu import Chunk
+from .test_decoder_layer_extend_gpu import layer  # noqa: F401
+from .test_decoder_layer_gpu import layer as plain_layer  # noqa: F401
 from .test_rope_gpu import _fill
 
 pytestmark = pytest.mark.gpu
@@ -78,3 +80,19 @@ def test_a_long_turned_append_is_many_short_ones(q_heads, heads, dim, rot, inter
         step = lens + torch.tensor([first, 0, at], dtype=torch.int32, device="cuda")
         short[rows] = block_ops.wd_kv4_rope_append(cache, rope, q[rows], k[rows], v[rows], table, step, cu_new=c)
     assert all(torch.equal(a, b) for a, b in zip(whole, cache.tensors)) and torch.equal(short[:T], out[:T])
+
+
+def test_padding_after_rows_of_nan(layer):  # noqa: F811
+    """What an earlier call left in the layer's buffers reaches no padding row of a later one."""
+    table = torch.tensor([[0, 1], [2, 3]], dtype=torch.int32, device="cuda")
+    start, err = (torch.tensor(t, dtype=torch.int32, device="cuda") for t in ([3, 0], [0]))
+    x = torch.randn(12, layer.w.moe.shape.H, device="cuda").to(torch.bfloat16)
+    for t in layer.cache.tensors:
+        t.zero_()
+    bad = x.clone()
+    bad[5:] = float("nan")
+    layer.extend(bad, table, start, torch.tensor([0, 5, 12], dtype=torch.int32, device="cuda"))
+    for t in layer.cache.tensors:
+        t.zero_()
+    out = layer.extend(x.clone(), table, start, torch.tensor([0, 3, 5], dtype=torch.int32, device="cuda"), err)
+    assert int(err) == 0 and torch.isfinite(out.float()).all()
