@@ -16,9 +16,9 @@
 // and cosines once for all its heads into shared memory (planes of 16 bytes, so that
 // neighbouring pieces are neighbouring words).
 //
-// Measured (GB300). wd_rope, 7001 tokens with 20 heads of 256 in FP16, a quarter turned: 28.9 us
-// for 143 MB, 73 % of a copy's rate (in a graph on one set of inputs, which L2 holds in part, 24.8; with
-// two items of a thread in flight, in 63 registers, 31). A few
+// Measured (GB300). wd_rope, 7001 tokens with 20 heads of 256 in FP16, a quarter turned: 22.4 us
+// for 143 MB in a graph on one set of inputs, which L2 holds in part; 24.4 in one wave of CTAs that wait for their
+// tables before they read, 31 with two items of a thread in flight, in 63 registers. A few
 // tokens: 2.1 us, a launch. wd_kv4_rope_append, 10056 tokens with 32 query and 8 KV heads of
 // 128: 54 us for 216 MB; 64 tokens with 64 and 4: 4.6 us. The first is bound by the
 // instructions that a key takes (30 us with no queries, issue slots 63 % busy) and by the
@@ -214,11 +214,15 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const TurnArgs a) {
   extern __shared__ float4 dyn4[];
   float* table = reinterpret_cast<float*>(dyn4);
   const int tok0 = blockIdx.x * a.per, tokens = min(a.per, a.T - tok0);
+  const int w0 = blockIdx.y * a.chunk, end = min(a.chunk, a.heads * a.items - w0);
+  if (a.per > 1 && threadIdx.x < tokens) {  // what this CTA reads comes to L2 while it computes its table
+    const int h0 = w0 / a.items, h1 = (w0 + end - 1) / a.items;
+    prefetch_l2(a.x + (int64_t)(tok0 + threadIdx.x) * a.ldx + (int64_t)h0 * a.head_bytes, (h1 - h0 + 1) * a.head_bytes);
+  }
   make_table(a.r, tokens, table, [&](int j, int64_t& pos) {
     pos = __ldg(a.positions + tok0 + j);
     return true;
   });
-  const int w0 = blockIdx.y * a.chunk, end = min(a.chunk, a.heads * a.items - w0);
   for (Walk walk(a.chunk); walk.j < tokens; walk.next()) {
     if (walk.w >= end) continue;
     const int head = (w0 + walk.w) / a.items, w = w0 + walk.w - head * a.items;
@@ -548,7 +552,7 @@ extern "C" moe_status wd_rope(const wd_rotation* r, const void* x, int32_t type,
   a.items = a.copies ? (a.pieces + 1) / 2 : a.r.rot / 16;
   const int all = heads * a.items, slices = (all + kThreads - 1) / kThreads;
   a.chunk = (all + slices - 1) / slices;
-  a.per = tokens_of_a_cta(T, slices, a.r.rot, 6, 1, 1);
+  a.per = tokens_of_a_cta(T, slices, a.r.rot, 6, 1, 4);
   cudaStream_t st = (cudaStream_t)stream;
   return type == WD_F32 ? turn<WD_F32>(a, st) : type == WD_BF16 ? turn<WD_BF16>(a, st) : turn<WD_F16>(a, st);
 }
