@@ -10,7 +10,8 @@
 // What the cache holds is the nearest MXFP4 to the exact turned key. FP32 gives it to
 // within kDoubt of the block's largest input: codes are taken at both ends of that
 // interval, and where they differ (one block of 2000) the element is computed again in
-// 64 bits. So the codes do not depend on the order of FP32 operations.
+// 64 bits. So the codes do not depend on the order of FP32 operations. A turn by nothing is exact and leaves
+// no doubt: its results are the inputs, which in BF16 often lie on a border.
 //
 // Work. A CTA has a run of tokens and some of their heads. It computes the angles' sines
 // and cosines once for all its heads into shared memory (planes of 16 bytes, so that
@@ -44,7 +45,8 @@ __device__ __forceinline__ float2 cos_sin(uint64_t turns, int64_t pos) {
   const int64_t rest = (int64_t)(a - ((uint64_t)quarter << 62));  // within 2^61
   const float x = (float)(int32_t)(rest >> 32) * 1.46291807926715968e-9f;  // 2 pi / 2^32
   const float y = x * x;
-  const float s = fmaf(x * y, fmaf(y, fmaf(y, fmaf(y, 1.0f / 362880, -1.0f / 5040), 1.0f / 120), -1.0f / 6), x);
+  float s = fmaf(x * y, fmaf(y, fmaf(y, fmaf(y, 1.0f / 362880, -1.0f / 5040), 1.0f / 120), -1.0f / 6), x);
+  if (x == 0.0f && rest != 0) s = 1.17549435e-38f;  // so that 0 says that the angle is whole quarter turns
   const float c = fmaf(y, fmaf(y, fmaf(y, fmaf(y, fmaf(y, -1.0f / 3628800, 1.0f / 40320), -1.0f / 720), 1.0f / 24), -0.5f), 1.0f);
   const float u = quarter & 1 ? s : c, v = quarter & 1 ? c : s;
   return make_float2((quarter + 1) & 2 ? -u : u, quarter & 2 ? -v : v);
@@ -373,6 +375,7 @@ __global__ void __launch_bounds__(kThreads, kAppendResident) kv4_rope_append_ker
     float f[8];
     unpack8<BF16>(raw, f);
     uint32_t in = 0;  // the largest of what is turned
+    uint32_t sines = 0;  // 0 where the turn changes signs at most
     if (w < 2 * groups) {
       in = piece_top<BF16>(raw);
       const float* row = table + j * r.rot;
@@ -380,6 +383,8 @@ __global__ void __launch_bounds__(kThreads, kAppendResident) kv4_rope_append_ker
         const float4 c = reinterpret_cast<const float4*>(row)[(w & 1) * groups + (w >> 1)];
         const float4 s = reinterpret_cast<const float4*>(row)[(2 + (w & 1)) * groups + (w >> 1)];
         const float cs[4] = {c.x, c.y, c.z, c.w}, sn[4] = {s.x, s.y, s.z, s.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) sines |= __float_as_uint(sn[i]) << 1;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           const float e = f[2 * i], o = f[2 * i + 1];
@@ -390,11 +395,14 @@ __global__ void __launch_bounds__(kThreads, kAppendResident) kv4_rope_append_ker
         float y[8], c[8], s[8];
         unpack8<BF16>(raw2, y);
         group_of(row, r.rot, w < groups ? w : w - groups, c, s);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) sines |= __float_as_uint(s[i]) << 1;
         const uint32_t flip = w < groups ? 0x80000000u : 0u;
 #pragma unroll
         for (int i = 0; i < 8; ++i) f[i] = fmaf(f[i], c[i], __uint_as_float(__float_as_uint(y[i] * s[i]) ^ flip));
       }
     }
+    if (sines == 0 && fabsf((float)r.magnitude) == 1.0f) in = 0;  // f is exact
     uint32_t m = 0;
 #pragma unroll
     for (int i = 0; i < 8; ++i) m = max(m, magnitude(f[i]));

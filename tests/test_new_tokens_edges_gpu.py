@@ -7,10 +7,11 @@ import torch
 
 from output_centric_expert_gb300 import block_ops
 
+from . import _block_ref as ref
 from .test_chunk_gpu import Chunk
 from .test_decoder_layer_extend_gpu import layer  # noqa: F401
 from .test_decoder_layer_gpu import layer as plain_layer  # noqa: F401
-from .test_rope_gpu import _fill
+from .test_rope_gpu import _fill, turned
 
 pytestmark = pytest.mark.gpu
 
@@ -80,6 +81,21 @@ def test_a_long_turned_append_is_many_short_ones(q_heads, heads, dim, rot, inter
         step = lens + torch.tensor([first, 0, at], dtype=torch.int32, device="cuda")
         short[rows] = block_ops.wd_kv4_rope_append(cache, rope, q[rows], k[rows], v[rows], table, step, cu_new=c)
     assert all(torch.equal(a, b) for a, b in zip(whole, cache.tensors)) and torch.equal(short[:T], out[:T])
+
+
+@pytest.mark.parametrize("interleaved,magnitude", [(False, 1.0), (True, 1.0), (False, -1.0), (False, 1.25)])
+def test_pairs_that_do_not_turn(interleaved, magnitude):
+    """Frequencies of 0, and some so low that the first angles vanish in FP32 but not in 64 bits, where BF16 inputs often lie on a
+    border between codes."""
+    cache, table, lens, cu, q, k, v, pos = _fill([2000, 300], [0, 5], 3, 3, 128, 32, "bf16", seed=11)
+    freqs = block_ops.rope_freqs(128)
+    freqs[16:40] = 0.0
+    freqs[40:] = torch.tensor([5e-11, -3e-11, 1e-12]).double().repeat(8)
+    block_ops.wd_kv4_rope_append(cache, block_ops.Rope(freqs, interleaved, magnitude), q, k, v, table, lens, cu_new=cu)
+    got = torch.empty(k.shape, device="cuda")
+    block_ops.wd_kv4_gather(cache, table, lens, got, torch.empty_like(got), cu)
+    want = turned(k.double().cpu().numpy(), pos, freqs.numpy(), interleaved, magnitude)[0]
+    assert np.array_equal(got.double().cpu().numpy(), ref.rounded(want))
 
 
 def test_padding_after_rows_of_nan(layer):  # noqa: F811
