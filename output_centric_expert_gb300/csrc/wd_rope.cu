@@ -59,6 +59,7 @@ struct RopeArgs {
   double magnitude;
   int32_t rot, pairs;  // pairs: rot / 2
   int32_t neighbours;
+  int32_t unit;  // the magnitude is 1 or -1, not merely in FP32
 };
 
 template <typename F>
@@ -402,7 +403,7 @@ __global__ void __launch_bounds__(kThreads, kAppendResident) kv4_rope_append_ker
         for (int i = 0; i < 8; ++i) f[i] = fmaf(f[i], c[i], __uint_as_float(__float_as_uint(y[i] * s[i]) ^ flip));
       }
     }
-    if (sines == 0 && fabsf((float)r.magnitude) == 1.0f) in = 0;  // f is exact
+    if (sines == 0 && r.unit) in = 0;  // f is exact
     uint32_t m = 0;
 #pragma unroll
     for (int i = 0; i < 8; ++i) m = max(m, magnitude(f[i]));
@@ -483,7 +484,7 @@ moe_status check_rotation(const wd_rotation* r, int32_t dim) {
 }
 
 RopeArgs rope_args(const wd_rotation* r) {
-  return {r->turns, r->magnitude, r->rot_dim, r->rot_dim / 2, r->neighbours ? 1 : 0};
+  return {r->turns, r->magnitude, r->rot_dim, r->rot_dim / 2, r->neighbours ? 1 : 0, std::fabs(r->magnitude) == 1.0};
 }
 
 // Tokens of a CTA: T tokens in `slices` slices, each run's table at most kTable bytes, in a multiple of `waves_of` waves.
