@@ -36,3 +36,19 @@ def test_magnitudes_that_are_one_in_fp32_only(magnitude, interleaved, kind):
     want = np.concatenate([k[..., :64] * magnitude, k[..., 64:]], -1)
     assert np.array_equal(got_k, ref.rounded(want)) and np.array_equal(got_v, ref.rounded(_n(case[6])))
     assert not np.array_equal(got_k, ref.rounded(k * np.sign(magnitude)))  # (the magnitude does decide some)
+
+
+@pytest.mark.parametrize("interleaved", [False, True])
+@pytest.mark.parametrize("dim,rot", [(64, 16), (64, 48), (128, 80), (128, 16), (256, 112), (256, 240)])
+def test_elements_that_do_not_turn_in_blocks_that_do(dim, rot, interleaved):
+    """Half of a block turns: its scale may be a turned element's, and the other half's codes are of what was given, zeros and
+    values on borders among them."""
+    def edit(k, v):
+        k[::2, 0, rot:] = 0
+        k[1::2, 0, rot:] = np.float32([2.5, -0.25, 0.75, -5, 1.25, 0, 3.5, -1.75]).repeat(2)[np.arange(dim - rot) % 16]
+        k[::3, 0, :rot] = np.float32([3, -1, 2, 0.5]).repeat(4)[np.arange(rot) % 16]
+    case = _fill([500, 63], [0, 9], 2, 3, dim, 64, "bf16", seed=rot, edit=edit)
+    freqs = block_ops.rope_freqs(rot)
+    got_k, got_v = _held(block_ops.Rope(freqs, interleaved), case)
+    want = turned(_n(case[5]), case[7], freqs.numpy(), interleaved)[0]
+    assert np.array_equal(got_k, ref.rounded(want)) and np.array_equal(got_v, ref.rounded(_n(case[6])))
