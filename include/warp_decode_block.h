@@ -204,7 +204,8 @@ moe_status wd_kv4_attend_chunk(const wd_kv4_cache* cache, const void* q, int32_t
 /* How heads turn with their tokens' positions. rot_dim elements of a head (its
  * first; a multiple of 16) form rot_dim / 2 pairs: pair i is elements i and
  * i + rot_dim / 2, or, where neighbours is not 0, 2i and 2i + 1. At position p it
- * turns by the angle p * f_i and is multiplied by magnitude (at most 65536):
+ * turns by the angle p * f_i and is multiplied by magnitude (0, or from 2^-100 to 65536 in
+ * size):
  *   a' = magnitude (a cos - b sin),   b' = magnitude (b cos + a sin)
  * turns [rot_dim/2] (device memory, 8 bytes aligned): f_i as turns per position
  * times 2^64, modulo whole turns, written on the host by wd_rope_turns. */

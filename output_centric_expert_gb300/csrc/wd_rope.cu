@@ -480,8 +480,9 @@ moe_status check_rotation(const wd_rotation* r, int32_t dim) {
   if (!r) return refuse(MOE_ERR_NULL, "wd_rope: a rotation is required");
   if (r->rot_dim < 16 || r->rot_dim % 16 || r->rot_dim > dim)
     return refuse(MOE_ERR_SHAPE, "wd_rope: rot_dim is a multiple of 16, from 16 to the head's elements");
-  if (!(std::fabs(r->magnitude) <= 65536.0))
-    return refuse(MOE_ERR_UNSUPPORTED, "wd_rope: the magnitude is at most 65536");
+  const double m = std::fabs(r->magnitude);
+  if (!(m <= 65536.0 && (m == 0.0 || m >= 0x1p-100)))  // (below, FP32 has it with fewer bits, or as 0)
+    return refuse(MOE_ERR_UNSUPPORTED, "wd_rope: the magnitude is 0, or from 2^-100 to 65536");
   if (!r->turns) return refuse(MOE_ERR_NULL, "wd_rope: turns are required");
   if (!aligned(r->turns, 8)) return refuse(MOE_ERR_ALIGN, "wd_rope: turns need 8 bytes");
   return MOE_OK;
