@@ -101,8 +101,10 @@ class DecoderLayer:
              err_flag: torch.Tensor | None = None) -> torch.Tensor:
         """One token of each sequence through the layer: res [B, H] (bfloat16 or float32) is updated in
         place and returned. seq_lens [B]: tokens that the cache holds before the step. What has no place in the
-        cache or no rotation sets bit 0 of err_flag, and its output does not count."""
+        cache or no rotation sets bit 0 of err_flag, and its output does not count. Without rows nothing is done."""
         B = res.shape[0]
+        if B == 0:
+            return res
         q, k, v, turned = self._project(res)
         if self.rope is None:
             self._rotate(turned, self._positions(seq_lens, err_flag))
@@ -118,12 +120,14 @@ class DecoderLayer:
         """Several new tokens of each sequence through the layer: res [T, H] (bfloat16 or float32), rows cu_new[s] to
         cu_new[s + 1] - 1 of sequence s, is updated in place and returned. seq_lens [S]: tokens that the cache holds
         before the call. Rows behind cu_new[S] (padding; finite) come out undefined, but finite, and touch nothing else. The layer needs a
-        rope. err_flag as for a step."""
+        rope. err_flag as for a step. Without rows nothing is done."""
         if self.rope is None:
             raise ValueError("extend: the layer has no rope")
         T = res.shape[0]
         if T > self.a.shape[0]:
             raise ValueError(f"extend: {T} tokens, the layer's buffers hold {self.a.shape[0]}")
+        if T == 0:
+            return res
         q, k, v, _ = self._project(res)
         block_ops.wd_kv4_rope_append(self.cache, self.rope, q, k, v, block_table, seq_lens, cu_new=cu_new, err_flag=err_flag)
         attn = self.attn[:T].zero_()  # padding rows are not written: what an earlier call left there could be NaN
