@@ -119,7 +119,7 @@ size_t wd_kv4_cache_bytes(const wd_kv4_cache* cache, int which);
  * cu_new[s] ... cu_new[s+1]-1 of k and v (cu_new [S+1] int32, not decreasing).
  * Rows from cu_new[S] on are ignored. cu_new NULL: one new token each (T == S).
  * Two sequences must not append to the same slot; neighbouring slots of a page
- * are independent, although their V shares bytes.
+ * are independent, although their V shares bytes. T and S are below 2^31 - 2^16.
  *
  * wd_kv4_gather -- the reverse with the same arguments: the values of positions
  * seq_lens[s] ... of each sequence as k_out and v_out. Every MXFP4 value is
@@ -188,7 +188,8 @@ moe_status wd_kv4_attend(const wd_kv4_cache* cache, const void* q, int32_t type,
  * values of up to 2^100 in magnitude do not overflow a sum on the way.
  * workspace: wd_kv4_attend_chunk_workspace bytes for T tokens or more, 16-byte aligned;
  * its contents do not matter before or after a call. Calls that may overlap need one
- * each. max_blocks * page_size < 2^31 - 2^16, T * q_heads < 2^31 - 2^16, q_heads <= 65536.
+ * each. max_blocks * page_size < 2^31 - 2^16, T * q_heads and S < 2^31 - 2^16,
+ * q_heads <= 65536.
  */
 size_t wd_kv4_attend_chunk_workspace(const wd_kv4_cache* cache, int32_t T, int32_t q_heads);
 moe_status wd_kv4_attend_chunk(const wd_kv4_cache* cache, const void* q, int32_t type,

@@ -209,8 +209,8 @@ moe_status check_tokens(const wd_kv4_cache* c, const void* k, const void* v, int
   if (!aligned(k, 16) || !aligned(v, 16) || ldk % 8 || ldv % 8 || !aligned(table, 4) ||
       !aligned(lens, 4) || !aligned(cu, 4) || !aligned(err, 4))
     return refuse(MOE_ERR_ALIGN, "wd_kv4: k and v need 16 bytes and strides % 8 == 0, the int32 arrays 4");
-  if ((int64_t)T * row / 8 > 0x7FFFFFFFll * kThreads)
-    return refuse(MOE_ERR_SHAPE, "wd_kv4: too many tokens for one call");
+  if (T >= kMostTokens || S >= kMostTokens || (int64_t)T * row / 8 > 0x7FFFFFFFll * kThreads)
+    return refuse(MOE_ERR_SHAPE, "wd_kv4: too many tokens or sequences for one call");
   return MOE_OK;
 }
 

@@ -1408,8 +1408,8 @@ extern "C" moe_status wd_kv4_attend_chunk(const wd_kv4_cache* c, const void* q, 
     return refuse(MOE_ERR_SHAPE, "wd_kv4_attend_chunk: the cache has too many pages");
   if (q_heads > 65536) return refuse(MOE_ERR_SHAPE, "wd_kv4_attend_chunk: a token has at most 65536 heads");
   constexpr int64_t kMost = 0x7FFFFFFF - 0xFFFF;
-  if ((int64_t)max_blocks * c->page_size >= kMost || (int64_t)T * q_heads >= kMost)
-    return refuse(MOE_ERR_SHAPE, "wd_kv4_attend_chunk: block_table's capacity, or T * q_heads, is too large");
+  if ((int64_t)max_blocks * c->page_size >= kMost || (int64_t)T * q_heads >= kMost || S >= kMost)
+    return refuse(MOE_ERR_SHAPE, "wd_kv4_attend_chunk: block_table's capacity, T * q_heads, or S is too large");
   ChunkArgs a = {};
   a.kc = c->k_codes, a.ks = c->k_scales, a.vc = c->v_codes, a.vs = c->v_scales;
   a.q = static_cast<const uint16_t*>(q), a.out = static_cast<uint16_t*>(out), a.lse = lse, a.err = err;

@@ -16,6 +16,7 @@ struct TokenArgs {
   int32_t per, chunk;  // tokens of a CTA, pieces of a token in a CTA
 };
 
+constexpr int32_t kMostTokens = 0x7FFFFFFF - 0xFFFF;  // tokens, or sequences, of a call are fewer: a run behind the last fits 32 bits
 // The arguments' checks, and the work of a CTA.
 moe_status check_tokens(const wd_kv4_cache* c, const void* k, const void* v, int32_t type, int64_t ldk, int64_t ldv,
                         int32_t T, const int32_t* table, int32_t max_blocks, const int32_t* lens, const int32_t* cu,
