@@ -51,7 +51,7 @@ __device__ __forceinline__ Place place_of(const TokenArgs& a, int tok, bool here
     if (tok >= __ldg(a.cu + a.S) || tok < __ldg(a.cu)) return p;
     int lo = 0, hi = a.S - 1;  // the last s with cu[s] <= tok
     while (lo < hi) {
-      const int mid = (lo + hi + 1) >> 1;
+      const int mid = lo + ((hi - lo + 1) >> 1);
       if (__ldg(a.cu + mid) <= tok)
         lo = mid;
       else
