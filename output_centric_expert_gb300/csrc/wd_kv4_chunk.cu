@@ -806,7 +806,7 @@ __global__ void __launch_bounds__(C::kThreadsAll, 1) kv4_chunk_kernel(const Chun
             check(before);
           } else {  // (the queries are there)
             scale = fabsf(a.scale_log2) * sh.back[number & 1][above + r] * kUnit;
-            if (scale == 0.0f) scale = 1.17549435e-38f;  // masked: -inf times it stays -inf
+            if (scale == 0.0f) scale = 1.40129846e-45f;  // masked: -inf times it stays -inf; 2^127 times it is nothing
           }
           before = i;
         }

@@ -1,0 +1,22 @@
+"""Bits and range of the attention of several new tokens: what its logits, probabilities and keys have to hold at the ends of what
+its description allows. Tolerances as in test_chunk_gpu, but for what a test says itself."""
+import numpy as np
+import pytest
+import torch
+
+from .test_chunk_gpu import Chunk
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.mark.parametrize("dim,group,new", [(64, 2, 30), (128, 4, 90), (256, 1, 40)])
+@pytest.mark.parametrize("scale", [0.0, -0.0])
+def test_no_scale_with_large_keys(scale, dim, group, new):
+    """Logits of 0 whatever the keys, up to 2^100: every key weighs the same."""
+    def edit(k, v):
+        k[:] = 2.0 ** 99
+        k[::2] *= -1
+        v[::2] = np.abs(v[::2])
+    c = Chunk([70], [new], 2, group, dim, 16, edit=edit)
+    c.q.fill_(1.0)
+    c.check(*c.run(scale=scale), scale=scale)
