@@ -566,7 +566,15 @@ __device__ __forceinline__ bool decode_k(uint8_t* tile, const uint8_t* raw, bool
             make_uint4(mul2_f16(e[0], f), mul2_f16(e[1], f), mul2_f16(e[2], f), mul2_f16(e[3], f));
       }
     }
-    const bool mine = here && (min(least & 0xFFFFu, least >> 16) < kLow || max(most & 0xFFFFu, most >> 16) > kHigh);
+    bool mine = here && (min(least & 0xFFFFu, least >> 16) < kLow || max(most & 0xFFFFu, most >> 16) > kHigh);
+    if (here && __any_sync(kAll, most == 0)) {  // keys of zeros, as a rule; or of 2^-127 times what is not
+      uint32_t codes = 0;
+#pragma unroll
+      for (int b = 0; b < NB; ++b) codes |= w[b];
+      codes |= __shfl_xor_sync(kAll, codes, 8);  // (the key's four lanes)
+      codes |= __shfl_xor_sync(kAll, codes, 16);
+      mine |= most == 0 && (codes & 0x77777777u);
+    }
     float f = 1.0f;
     if (mine) f = wide_key<C>(row, raw + key * (D / 2) + t * (D / 8), scales, t, k);
     if (lane < 8) factors[warp * C::kWarpKeys + 8 * i + k] = f;
