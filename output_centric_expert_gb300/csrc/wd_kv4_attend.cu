@@ -680,7 +680,7 @@ __global__ void __launch_bounds__(W * 32, CTAS) kv4_attend_kernel(const AttendAr
                        pack2<false>(f[4] * up, f[5] * up), pack2<false>(f[6] * up, f[7] * up));
       }
       const float back = exp2i(-sigma) * fabsf(a.scale_log2);
-      if (t == 0) s_qs[n * 8 + g] = back == 0.0f ? 1.17549435e-38f : back;  // masked: -inf times it stays -inf
+      if (t == 0) s_qs[n * 8 + g] = back == 0.0f ? 1.40129846e-45f : back;  // masked: -inf times it stays -inf
     }
     __syncthreads();
     float qs[NT][2];
