@@ -511,13 +511,20 @@ __device__ __forceinline__ uint32_t mul2_f16(uint32_t a, uint32_t b) {
 }
 
 // A key whose scale codes f16 does not take as they are: its blocks relative to its largest scale, and the power of two
-// that its column of S is multiplied by. A block 2^-36 below that is 0.
+// that its column of S is multiplied by. A block 2^-36 below that is 0. Where all scale codes are 0, which is a key of zeros as a
+// rule, the result is negative if this lane's codes are zeros.
 template <typename C>
 __device__ __noinline__ float wide_key(uint8_t* row, const uint8_t* codes, const uint8_t* scales, int t, int k) {
   constexpr int NB = C::D / 32;
   int top = 0;
 #pragma unroll 1
   for (int b = 0; b < NB; ++b) top = max(top, (int)scales[b]);
+  if (top == 0) {
+    uint32_t any = 0;
+#pragma unroll 1
+    for (int b = 0; b < NB; ++b) any |= *reinterpret_cast<const uint32_t*>(codes + 4 * b);
+    if (!(any & 0x77777777u)) return -ldexpf(1.0f, -127 - 12 + 4);
+  }
 #pragma unroll 1
   for (int b = 0; b < NB; ++b) {
     const uint32_t f = __half_as_ushort(__float2half_rn(exp2i(max(-126, (int)scales[b] - top + 12)))) * 0x10001u;
@@ -566,19 +573,11 @@ __device__ __forceinline__ bool decode_k(uint8_t* tile, const uint8_t* raw, bool
             make_uint4(mul2_f16(e[0], f), mul2_f16(e[1], f), mul2_f16(e[2], f), mul2_f16(e[3], f));
       }
     }
-    bool mine = here && (min(least & 0xFFFFu, least >> 16) < kLow || max(most & 0xFFFFu, most >> 16) > kHigh);
-    if (here && __any_sync(kAll, most == 0)) {  // keys of zeros, as a rule; or of 2^-127 times what is not
-      uint32_t codes = 0;
-#pragma unroll
-      for (int b = 0; b < NB; ++b) codes |= w[b];
-      codes |= __shfl_xor_sync(kAll, codes, 8);  // (the key's four lanes)
-      codes |= __shfl_xor_sync(kAll, codes, 16);
-      mine |= most == 0 && (codes & 0x77777777u);
-    }
+    const bool mine = here && (min(least & 0xFFFFu, least >> 16) < kLow || max(most & 0xFFFFu, most >> 16) > kHigh || most == 0);
     float f = 1.0f;
     if (mine) f = wide_key<C>(row, raw + key * (D / 2) + t * (D / 8), scales, t, k);
-    if (lane < 8) factors[warp * C::kWarpKeys + 8 * i + k] = f;
-    wide |= mine;
+    if (lane < 8) factors[warp * C::kWarpKeys + 8 * i + k] = fabsf(f);
+    wide |= mine && !(f < 0.0f);
   }
   return __any_sync(kAll, wide);
 }
