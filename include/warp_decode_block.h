@@ -184,11 +184,12 @@ moe_status wd_kv4_attend(const wd_kv4_cache* cache, const void* q, int32_t type,
  * every call with the same inputs.
  * Logits, softmax statistics and sums are FP32; q is used as in wd_kv4_attend. Keys are used
  * exactly, but for a key with scale codes outside 109 .. 136: its blocks 2^-36 below its
- * largest count as 0. A probability has 16 bits and FP32's range of exponents. Keys and
+ * largest are rounded to that, and lower ones count as 0. A probability has 16 bits and FP32's range of exponents. Keys and
  * values of up to 2^100 in magnitude do not overflow a sum on the way.
  * workspace: wd_kv4_attend_chunk_workspace bytes for T tokens or more, 16-byte aligned;
  * its contents do not matter before or after a call. Calls that may overlap need one
- * each. max_blocks * page_size < 2^31 - 2^16, T * q_heads and S < 2^31 - 2^16,
+ * each. Every wait between the kernel's warps has a limit; were one to run out, results would be NaN
+ * (err_flag only tells of lengths and pages). max_blocks * page_size < 2^31 - 2^16, T * q_heads and S < 2^31 - 2^16,
  * q_heads <= 65536.
  */
 size_t wd_kv4_attend_chunk_workspace(const wd_kv4_cache* cache, int32_t T, int32_t q_heads);
@@ -225,8 +226,8 @@ moe_status wd_rope_turns(int32_t n, const double* freqs, uint64_t* turns);
  * multiple of 8 up to 1024) by positions [T] int32 into out. Negative positions
  * turn back. Elements behind rot_dim are copied. out may be x (with the same
  * stride); token strides ldx and ldo a multiple of 16 bytes, as the addresses.
- * Angles are exact to 2^-25 whatever the position; the rest is FP32, rounded once:
- * off by 6 * 2^-24 (|a| + |b|) magnitude before that rounding.
+ * Angles are exact to 2^-23 whatever the position; with these and FP32 results are
+ * off by 6 * 2^-24 (|a| + |b|) magnitude before their one rounding.
  */
 moe_status wd_rope(const wd_rotation* rotation, const void* x, int32_t type, int64_t ldx,
                    int32_t T, int32_t heads, int32_t dim, const int32_t* positions, void* out,
@@ -286,7 +287,7 @@ enum {
   WD_CALL_KV4_GATHER = 2,
   WD_CALL_KV4_ATTEND = 3,
   WD_CALL_BLOCK_NORM = 4,
-  WD_CALL_ROPE = 8, /* (5 to 7 are none) */
+  WD_CALL_ROPE = 8, /* a number once given stays its entry point's; 5 to 7 never were one */
   WD_CALL_KV4_ROPE_APPEND = 9,
   WD_CALL_KV4_ATTEND_CHUNK = 10
 };

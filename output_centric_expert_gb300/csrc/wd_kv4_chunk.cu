@@ -30,15 +30,25 @@
 // All (sequence, row block, KV head) items are cut into units of one key tile; CTA c of G
 // takes the c-th contiguous share of all units, found from the lengths on the device. An
 // item that several CTAs share leaves its parts in the workspace, and a dependent launch
-// joins them in CTA order. Each barrier has one reader, which sees all its phases; every wait
-// has a limit, after which the warp goes on and the results are NaN.
+// joins them in CTA order.
+//
+// Barriers. A wait names a phase by its parity, so a reader must not fall two phases behind. All readers but one kind wait
+// for every phase: one warp for queries, filled slots, probabilities and raw codes, the four softmax warps of a row tile
+// for scores, eight decode warps for freed slots. o_done, the sums of a buffer, is read by the warp that issues the
+// products with keys, at every phase, and by the row tile's four softmax warps, which skip some. They are safe
+// because a buffer's next sums need its next probabilities, which these same warps give: one phase at most
+// is open when they wait. Every wait for an mbarrier has a limit, after which the warp goes on and the results are NaN;
+// the two named barriers of the softmax warps have none, and all of these warps always reach them.
 //
 // Measured (GB300). 2048 tokens behind 30011 keys, 28 query heads of 128 on 4 KV heads: 938
 // us, 971 TFLOP/s of the two products, or 1457 of the three that are issued, 79 % of a library
 // BF16 GEMM; 8192 tokens with 64 query heads, causal: 1251 us; heads of 256, 24 prompts of up
-// to 1500 with a window of 1000: 210 us. What bounds it is the issue of the decode and softmax
-// warps: when the first took 1044 it took 948 without decoding, 966 without the second term
-// of P, 899 without these and exponentials. Tried: one warp per group for all MMAs, 2 % slower;
+// to 1500 with a window of 1000: 210 us. Of the first's 942 (as a call) it takes 817 without the arithmetic of decoding, 888
+// without the second term of P, 950 without exponentials, 734 without all three; 7 tokens behind 131000 keys 123, 92,
+// 119, 126 and 88; heads of 256 213, 175, 203, 215 and 154. So exponentials cost nothing, decoding an eighth to a
+// quarter, and what is left is presumably the chain of a piece (scores out of tensor memory, their
+// largest, probabilities back in, sums), which a row tile's pieces go through one after the other. 72 registers at launch spill
+// 64 to 84 bytes of a thread, 128 with heads of 256 72. Tried: one warp per group for all MMAs, 2 % slower;
 // the same eight warps decoding K, then V, 12 %; an item counted as two tiles 18 % for the second
 // case, as six 2 %; V as f16, K-major, 24 % (more code: the warps of all roles share the
 // instruction caches, which miss in 13 % of their requests).
@@ -57,7 +67,7 @@ constexpr int kRows = 128;       // of a row tile
 constexpr int kPiece = 64;       // keys that are in the softmax at a time
 constexpr int kItemUnits = 4;    // what an item costs beside its key tiles, in tiles
 constexpr int kMinUnits = 3;     // of a CTA, on average, unless it has an item to itself
-constexpr uint32_t kWaitLimit = 1u << 20;
+constexpr uint32_t kWaitLimit = 1u << 20;  // tries of a wait for an mbarrier
 constexpr int kSeqChunk = 512;   // sequences whose units are in shared memory at a time
 constexpr int kDecodeWarps = 8;
 constexpr int kMeta = 8;         // key tiles whose page masks and bad blocks are kept
@@ -228,7 +238,7 @@ __device__ __forceinline__ void bulk_copy(uint32_t to, const void* from, uint32_
                "r"(bytes), "r"(bar)
                : "memory");
 }
-// All threads of the softmax warps.
+// All threads of the softmax warps (no limit: none of them leaves its loop before the others).
 __device__ __forceinline__ void soft_sync(int id) { asm volatile("bar.sync %0, 256;" ::"r"(id) : "memory"); }
 
 __device__ __forceinline__ float max3(float a, float b, float c) {
@@ -645,7 +655,7 @@ __device__ __forceinline__ bool decode_v(uint8_t* tile, const uint8_t* raw, bool
 
 template <typename C>
 struct Shared {  // beside the operands
-  // (each of a single reader, who so sees every phase)
+  // (their readers, and why none falls behind: in the file's first comment)
   uint64_t q_full[C::kQ], q_twin, k_full[C::kSlots][C::kQ], v_full[C::kSlots][C::kQ], k_free[C::kSlots][C::kQ], v_free[C::kSlots][C::kQ];
   uint64_t s_full[C::kQ][2], p_full[C::kQ][2], o_done[C::kQ][2], raw_full[2][kDecodeWarps], drained[C::kQ];  // (raw: K, V)
   int64_t units[kSeqChunk], warp[C::kThreadsAll / 32];

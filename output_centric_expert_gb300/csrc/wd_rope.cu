@@ -4,8 +4,8 @@
 // Mathematics. Pair i of a head is turned by the angle pos * f_i. A frequency is kept as
 // turns per position in units of 2^-64, so the product with a position in 64-bit
 // integers is the angle less its whole turns, exactly: no position is too far. What is
-// left after the nearest quarter turn, at most an eighth either way, becomes FP32 (off by
-// 2^-25) and goes through the Taylor series of sine and cosine.
+// left after the nearest quarter turn, at most an eighth either way, becomes FP32 (off by 1.3 * 2^-24 at
+// most: conversion, product with 2 pi, its rounding) and goes through the Taylor series of sine and cosine.
 //
 // What the cache holds is the nearest MXFP4 to the exact turned key. FP32 gives it to
 // within kDoubt of the largest input of a piece of eight elements and of their partners: codes are
@@ -23,10 +23,10 @@
 // for 143 MB in a graph on one set of inputs, which L2 holds in part; 24.4 in one wave of CTAs that wait for their
 // tables before they read, 31 with two items of a thread in flight, in 63 registers. A few
 // tokens: 2.1 us, a launch. wd_kv4_rope_append, 10056 tokens with 32 query and 8 KV heads of
-// 128: 54 us for 216 MB; 64 tokens with 64 and 4: 4.6 us. The first is bound by the
+// 128: 53 us for 216 MB; 64 tokens with 64 and 4: 4.6 us. The first is bound by the
 // instructions that a key takes (30 us with no queries, issue slots 63 % busy) and by the
 // queries' memory traffic, which overlap only in part. Left to the compiler the kernel took 83
-// registers, two CTAs of an SM, and 82 us; at 64 and four of them 59, and 56 with two items
+// registers, two CTAs of an SM, and 82 us; at 64 and four of them, with 72 bytes of a thread spilled and 100 to 108 read back, 59, and 56 with two items
 // of a thread's queries in flight. Three items, five CTAs (62), halves of the queries' slices
 // (62): slower. Runs short enough for three waves, with what a CTA reads asked into L2
 // while it finds its tokens' places: 54; for one wave 60.
@@ -323,7 +323,9 @@ __global__ void __launch_bounds__(kThreads, kAppendResident) kv4_rope_append_ker
   const int run = blockIdx.x / a.slices, slice = blockIdx.x - run * a.slices;
   const int tok0 = run * t.per, tid = threadIdx.x;
   const bool queries = slice >= a.kv_slices;
-  // What this CTA reads comes to L2 while it finds its tokens' places.
+  // What this CTA reads comes to L2 while it finds its tokens' places, unless its run is short, as in a step: then a projection has
+  // just written it, and it is there. 64 tokens with 64 + 4 heads 4.6 us so and 4.8 with it (5.5 and 5.0 from DRAM), 256 with 32 + 8 heads
+  // 5.6 and 5.8 (6.2 and 5.8); 4800 tokens 31.4 without and 29.7 with it (32.5 and 31.1).
   if (t.per > 4 && tid < t.per && tok0 + tid < t.T) {
     const int64_t tok = tok0 + tid;
     if (queries) {
