@@ -184,13 +184,14 @@ moe_status wd_kv4_attend(const wd_kv4_cache* cache, const void* q, int32_t type,
  * every call with the same inputs.
  * Logits, softmax statistics and sums are FP32; q is used as in wd_kv4_attend. Keys are used
  * exactly, but for a key with scale codes outside 109 .. 136: its blocks 2^-36 below its
- * largest are rounded to that, and lower ones count as 0. A probability has 16 bits and FP32's range of exponents. Keys and
+ * largest are rounded to that, and lower ones count as 0. A probability has 16 bits, fewer
+ * below 2^-118 of its row's largest; below 2^-126 of that it counts as 0. Keys and
  * values of up to 2^100 in magnitude do not overflow a sum on the way.
  * workspace: wd_kv4_attend_chunk_workspace bytes for T tokens or more, 16-byte aligned;
  * its contents do not matter before or after a call. Calls that may overlap need one
- * each. Every wait between the kernel's warps has a limit; were one to run out, results would be NaN
- * (err_flag only tells of lengths and pages). max_blocks * page_size < 2^31 - 2^16, T * q_heads and S < 2^31 - 2^16,
- * q_heads <= 65536.
+ * each. The kernel's waits for copies and products have a limit; were one to run out, results
+ * would be NaN (err_flag only tells of lengths and pages). max_blocks * page_size < 2^31 - 2^16,
+ * T * q_heads and S < 2^31 - 2^16, q_heads <= 65536.
  */
 size_t wd_kv4_attend_chunk_workspace(const wd_kv4_cache* cache, int32_t T, int32_t q_heads);
 moe_status wd_kv4_attend_chunk(const wd_kv4_cache* cache, const void* q, int32_t type,
@@ -206,8 +207,7 @@ moe_status wd_kv4_attend_chunk(const wd_kv4_cache* cache, const void* q, int32_t
 /* How heads turn with their tokens' positions. rot_dim elements of a head (its
  * first; a multiple of 16) form rot_dim / 2 pairs: pair i is elements i and
  * i + rot_dim / 2, or, where neighbours is not 0, 2i and 2i + 1. At position p it
- * turns by the angle p * f_i and is multiplied by magnitude (0, or from 2^-100 to 65536 in
- * size):
+ * turns by the angle p * f_i and is multiplied by magnitude (0, or 2^-100 to 65536 in size):
  *   a' = magnitude (a cos - b sin),   b' = magnitude (b cos + a sin)
  * turns [rot_dim/2] (device memory, 8 bytes aligned): f_i as turns per position
  * times 2^64, modulo whole turns, written on the host by wd_rope_turns. */

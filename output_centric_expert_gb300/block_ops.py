@@ -433,7 +433,8 @@ def rope_freqs(rot_dim: int, base: float = 10000.0, scaling: str | None = None, 
 class Rope:
     """A model's rotary positions: pair i of a head's first 2 * len(freqs) elements turns by freqs[i] radians per position
     and is multiplied by magnitude. The pairs are elements i and i + len(freqs), or, `interleaved`, 2 i and 2 i + 1.
-    len(freqs) is a multiple of 8. Made once: it reads freqs (float32 or float64, as rope_freqs makes them) on the host."""
+    len(freqs) is a multiple of 8, magnitude 0 or from 2^-100 to 65536 in size. Made once: it reads freqs (float32 or float64,
+    as rope_freqs makes them) on the host."""
 
     def __init__(self, freqs: torch.Tensor, interleaved: bool = False, magnitude: float = 1.0, device=None):
         if freqs.dim() != 1 or freqs.dtype not in (torch.float32, torch.float64):

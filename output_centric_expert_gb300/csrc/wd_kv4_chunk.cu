@@ -12,7 +12,7 @@
 //   two of their own, by which their column of S is multiplied.
 //   acc += P V: BF16 operands. V is decoded to BF16, which holds every E2M1 code times every E8M0
 //   scale up to 6 * 2^125 exactly. P is two BF16 terms, the second what the cut of the first
-//   left: 16 bits, and FP32's range of exponents, as in wd_kv4_attend.
+//   left: 16 bits down to 2^-118, where BF16 begins to lack the second term's, and none below 2^-126.
 //
 // Work. A CTA has kQ tiles of 128 rows against tiles of kKeys keys. Its warps:
 //   4 per row tile   softmax: a thread has a row. S comes from tensor memory, P goes back in
